@@ -61,8 +61,10 @@ extern "C" {
 #endif
 
 /* 2: the workspace must be 16-byte aligned; the forward with checkpoints and
- * the backward from them were added. */
-#define SSM_ABI_VERSION 2
+ * the backward from them were added.
+ * 3: the gated delta rule (forward, backward, single-token update) and the RMS
+ * norm (forward, backward) were added. */
+#define SSM_ABI_VERSION 3
 
 /* Status codes. */
 #define SSM_OK 0
@@ -75,10 +77,12 @@ extern "C" {
 #define SSM_E_UNSUPPORTED 7 /* a size or an option outside the supported range */
 #define SSM_E_HIP 8         /* the HIP runtime reported an error at launch       */
 
-/* Bits of the `flags` argument of the scan and decode entry points. Any other
- * bit set returns SSM_E_UNSUPPORTED. */
-#define SSM_FLAG_SOFTPLUS 1 /* dt = softplus(delta + delta_bias), else delta + delta_bias */
-#define SSM_FLAG_ZOH 2      /* input coefficient k = (exp(dt A) - 1) / A, else k = dt   */
+/* Bits of the `flags` argument. Each entry point names those it takes; any
+ * other bit set returns SSM_E_UNSUPPORTED. */
+#define SSM_FLAG_SOFTPLUS 1     /* dt = softplus(delta + delta_bias), else delta + delta_bias */
+#define SSM_FLAG_ZOH 2          /* input coefficient k = (exp(dt A) - 1) / A, else k = dt   */
+#define SSM_FLAG_BETA_SIGMOID 4 /* write strength sigmoid(beta), else beta (gated delta rule) */
+#define SSM_FLAG_QK_L2NORM 8    /* q and k divided by sqrt(|.|^2 + 1e-6) (gated delta rule) */
 
 /* Version of this ABI (SSM_ABI_VERSION of the header the library was built from). */
 int ssm_abi_version(void);
@@ -403,6 +407,187 @@ int ssm_ssd_fwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, 
                 const void* x, const void* dt, const float* A, const void* B, const void* C,
                 const float* D, const void* z, const float* dt_bias, const float* h0,
                 void* y, float* h_final, void* stream);
+
+/*
+ * Gated delta rule: a layer with a matrix state that forgets by a scalar gate
+ * and writes by the delta rule (what the state already answers for a key is
+ * taken off the value before it is written). It stands next to the SSD layer
+ * above: the same state [N, P] a head and the same step sizes and decays, with
+ * a correcting write in place of an adding one. Per batch row b, value head h
+ * (its query/key head is g = h / (H / G)), step t, with the state S [N, P]:
+ *
+ *   dt   = softplus(dt_raw[b,t,h] + dt_bias[h])         (or without softplus)
+ *   beta = sigmoid(beta_raw[b,t,h])                     (or beta_raw itself)
+ *   q, k = q_raw / sqrt(|q_raw|^2 + 1e-6), k alike      (or as they are)
+ *   S    = exp(dt * A[h]) * S
+ *   S    = S + k (beta (v[b,t,h,:] - k^T S))
+ *   y[b,t,h,:] = scale * q^T S
+ *
+ *   batch, seqlen              : B >= 0, 0 <= L < 2^30.
+ *   nkheads, nheads            : G and H; H a multiple of G (else
+ *                                SSM_E_SHAPE), H = 0 only with G = 0.
+ *   headdim, dstate            : 1 <= P <= 256, 1 <= N <= 128 (else
+ *                                SSM_E_UNSUPPORTED); B * H * P < 2^31.
+ *   in_dtype, out_dtype        : 0 float32, 1 bfloat16.
+ *   flags                      : SSM_FLAG_SOFTPLUS, SSM_FLAG_BETA_SIGMOID,
+ *                                SSM_FLAG_QK_L2NORM, in any combination.
+ *   scale                      : factor on y (1/sqrt(N) is usual).
+ *   q_step, k_step, v_step     : elements between consecutive steps of q, k
+ *                                and v (at least G N, G N, H P, else
+ *                                SSM_E_SHAPE; below 2^23, else
+ *                                SSM_E_UNSUPPORTED); batch rows are
+ *                                L times as far apart. The three may thus be
+ *                                column ranges of one [B, L, G N + G N + H P]
+ *                                array, as the convolution leaves them.
+ *   q, k      [B, L, G, N]  in_dtype
+ *   v         [B, L, H, P]  in_dtype
+ *   dt, beta  [B, L, H]     in_dtype   raw step size, raw write strength
+ *   A         [H]           float32    decay rate (expected <= 0). A log
+ *                                      decay dt A below -200 (minus infinity
+ *                                      too) is taken as -200, whose
+ *                                      exponential is 0 in float32.
+ *   dt_bias   [H]           float32    (optional, 0)
+ *   h0        [B, H, P, N]  float32    initial state (optional, 0)
+ *   seqlens   [B]           int32      steps that each batch row has
+ *                                      (optional, L for all; taken as 0 below
+ *                                      0 and as L above L). Steps behind a
+ *                                      row's last are not read; their y is 0.
+ *   y         [B, L, H, P]  out_dtype  must not overlap any input
+ *   h_final   [B, H, P, N]  float32    state behind each row's last step
+ *                                      (optional); may equal h0
+ *   workspace, workspace_bytes         at least
+ *                                      ssm_gated_delta_workspace_bytes() bytes
+ *                                      on a 16-byte boundary (NULL when 0)
+ *
+ * q, k, v, dt, beta and y need the alignment of their element type only; rows
+ * that start on 16-byte boundaries with N and P multiples of 8 are read
+ * fastest. Products are taken in 22 bits or more of every float32 operand and
+ * added in float32; results are bitwise deterministic. A value of a step that
+ * is not finite may make every y and state element of its head NaN from the
+ * start of its block of 64 steps on.
+ */
+size_t ssm_gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
+                                       int64_t headdim, int64_t dstate, int in_dtype);
+int ssm_gated_delta_fwd(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
+                        int64_t headdim, int64_t dstate, int in_dtype, int out_dtype, int flags, float scale,
+                        int64_t q_step, int64_t k_step, int64_t v_step,
+                        const void* q, const void* k, const void* v, const void* dt, const float* A,
+                        const void* beta, const float* dt_bias, const float* h0, const int32_t* seqlens,
+                        void* y, float* h_final, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gated delta rule, one token: the step above for L = 1 with h0 = h_final =
+ * state, in place. Sizes, types, flags, scale and alignment as for the
+ * forward; q, k [B, G, N], v, y [B, H, P], dt, beta [B, H]; q_step, k_step
+ * and v_step are the elements between batch rows.
+ *   state     [B, H, P, N]  float32    read, then overwritten; 16-byte aligned
+ *   y         [B, H, P]     out_dtype  must not overlap state or inputs
+ */
+int ssm_gated_delta_update(int64_t batch, int64_t nkheads, int64_t nheads, int64_t headdim, int64_t dstate,
+                           int in_dtype, int out_dtype, int flags, float scale,
+                           int64_t q_step, int64_t k_step, int64_t v_step,
+                           float* state, const void* q, const void* k, const void* v, const void* dt,
+                           const float* A, const void* beta, const float* dt_bias, void* y, void* stream);
+
+/*
+ * Gated delta rule backward: gradients of a loss through ssm_gated_delta_fwd
+ * with the same inputs, given dy = dL/dy and optionally dh_final. In reverse
+ * over the steps, with the states S' = exp(dt A) S_{t-1} and S_t of the
+ * forward, e = v - k^T S', and the gradient X [N, P] of S_t:
+ *
+ *   X    = X + scale q dy^T            dq = scale S_t dy
+ *   de   = beta k^T X                  dbeta = (k^T X) . e
+ *   dv   = de                          dk = X beta e - S' de
+ *   X'   = X - k de^T                  d(dt A) = <X', S'>,  X_{t-1} = exp(dt A) X'
+ *
+ * carried on through the norms, the sigmoid and the softplus to the raw
+ * inputs. Gradients of q and k are summed over the H / G heads that share
+ * them. Steps behind a row's length have gradient 0.
+ *
+ *   inputs, sizes, flags, scale, steps as for the forward.
+ *   dy        [B, L, H, P]  float32    gradient w.r.t. y
+ *   dh_final  [B, H, P, N]  float32    (optional, 0)
+ *   dq, dk    [B, L, G, N]  float32    outputs, dense
+ *   dv        [B, L, H, P]  float32    output
+ *   ddt, dbeta [B, L, H]    float32    outputs (w.r.t. the raw values)
+ *   dA        [H]           float32    output
+ *   ddt_bias  [H]           float32    output (optional; written only when
+ *                                      dt_bias is given)
+ *   dh0       [B, H, P, N]  float32    output (optional)
+ *   workspace, workspace_bytes         at least
+ *                                      ssm_gated_delta_bwd_workspace_bytes(),
+ *                                      on a 16-byte boundary
+ * No output may overlap an input, another output or the workspace. Bitwise
+ * deterministic (sums over steps, batch rows and shared heads in a fixed
+ * order).
+ */
+size_t ssm_gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
+                                           int64_t headdim, int64_t dstate, int in_dtype);
+int ssm_gated_delta_bwd(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
+                        int64_t headdim, int64_t dstate, int in_dtype, int flags, float scale,
+                        int64_t q_step, int64_t k_step, int64_t v_step,
+                        const void* q, const void* k, const void* v, const void* dt, const float* A,
+                        const void* beta, const float* dt_bias, const float* h0, const int32_t* seqlens,
+                        const float* dy, const float* dh_final,
+                        float* dq, float* dk, float* dv, float* ddt, float* dA, float* dbeta,
+                        float* ddt_bias, float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual stream's addition in front
+ * (the block's entry in "从 Transformer 到 Mamba", ybb.press, section 5) and,
+ * on request, an output in 8 bits:
+ *
+ *   s = x + residual  (s = x when residual is NULL), rounded to res_dtype
+ *   n = s / sqrt(mean(s^2) + eps) * weight            (weight NULL: 1)
+ *   y = n, or with out_dtype 2: scales[r] = max|n| / 448 over the row (1 when
+ *       that is 0) and y = n / scales[r] in the 8-bit format e4m3 (OCP: 448 is
+ *       its largest value), rounded to nearest even
+ *
+ *   rows, dim                  : R >= 0, 1 <= d <= 16384 (else
+ *                                SSM_E_UNSUPPORTED), R < 2^31.
+ *   in_dtype                   : of x, 0 float32, 1 bfloat16
+ *   res_dtype                  : of residual and residual_out, 0 or 1 (not
+ *                                used when residual is NULL)
+ *   out_dtype                  : of y, 0, 1, or 2 (e4m3 with scales)
+ *   eps                        : >= 0 (else SSM_E_UNSUPPORTED)
+ *   x         [R, d]  in_dtype
+ *   residual  [R, d]  res_dtype (optional)
+ *   weight    [d]     float32   (optional)
+ *   y         [R, d]  out_dtype; must not overlap any input
+ *   residual_out [R, d] res_dtype: s; required with residual, NULL without;
+ *                                may equal residual
+ *   scales    [R]     float32: required with out_dtype 2, NULL otherwise
+ * Alignment: that of the element types; 16-byte aligned arrays with d a
+ * multiple of 8 are read fastest. Sums are in float32; deterministic.
+ */
+int ssm_rms_norm_fwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, int out_dtype, float eps,
+                     const void* x, const void* residual, const float* weight,
+                     void* y, void* residual_out, float* scales, void* stream);
+
+/*
+ * Gradients of the norm. s is what the forward normalised (residual_out, or x
+ * when there was no residual), dy the gradient w.r.t. n (with the 8-bit output:
+ * w.r.t. the value y scales[r] stands for, the rounding passed straight
+ * through), dresidual the gradient that reaches residual_out from elsewhere.
+ *
+ *   r = 1 / sqrt(mean(s^2) + eps),  w = dy * weight
+ *   ds = r (w - s r mean(w s r)) + dresidual     (the gradient w.r.t. x and
+ *                                                 w.r.t. residual)
+ *   dweight = sum over rows of dy s r
+ *
+ *   s         [R, d]  s_dtype (0 float32, 1 bfloat16)
+ *   weight    [d]     float32   (optional, 1)
+ *   dy        [R, d]  float32
+ *   dresidual [R, d]  float32   (optional, 0)
+ *   ds        [R, d]  float32   output; may equal dresidual or dy
+ *   dweight   [d]     float32   output (optional)
+ *   workspace, workspace_bytes  at least ssm_rms_norm_bwd_workspace_bytes(),
+ *                               on a 16-byte boundary (NULL when dweight is)
+ */
+size_t ssm_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+int ssm_rms_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps,
+                     const void* s, const float* weight, const float* dy, const float* dresidual,
+                     float* ds, float* dweight, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

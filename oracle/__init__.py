@@ -30,3 +30,5 @@ from .ssm_oracle import (  # noqa: F401
     selective_state_update,
     scaled_error,
 )
+from .gated_delta_oracle import gated_delta, gated_delta_bwd  # noqa: F401
+from .rms_norm_oracle import e4m3_nearest, rms_norm, rms_norm_bwd  # noqa: F401

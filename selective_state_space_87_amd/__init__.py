@@ -10,6 +10,14 @@ from .binding import (  # noqa: F401
     ssm_abi_version,
     ssm_causal_conv1d_fwd,
     ssm_causal_conv1d_update,
+    ssm_gated_delta_bwd,
+    ssm_gated_delta_bwd_workspace_bytes,
+    ssm_gated_delta_fwd,
+    ssm_gated_delta_update,
+    ssm_gated_delta_workspace_bytes,
+    ssm_rms_norm_bwd,
+    ssm_rms_norm_bwd_workspace_bytes,
+    ssm_rms_norm_fwd,
     ssm_scan_bwd_workspace_bytes,
     ssm_scan_chunks,
     ssm_scan_workspace_bytes,

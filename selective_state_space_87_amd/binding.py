@@ -87,6 +87,23 @@ def _load():
                                                  vp, vp, vp, vp, vp, vp]
         lib.ssm_ssd_fwd.restype = i32
         lib.ssm_ssd_fwd.argtypes = [i64, i64, i64, i64, i64, i32, i32, i32] + [vp] * 11 + [vp]
+        f32 = ctypes.c_float
+        lib.ssm_gated_delta_workspace_bytes.restype = sz
+        lib.ssm_gated_delta_workspace_bytes.argtypes = [i64] * 6 + [i32]
+        lib.ssm_gated_delta_fwd.restype = i32
+        lib.ssm_gated_delta_fwd.argtypes = [i64] * 6 + [i32] * 3 + [f32] + [i64] * 3 + [vp] * 12 + [sz, vp]
+        lib.ssm_gated_delta_update.restype = i32
+        lib.ssm_gated_delta_update.argtypes = [i64] * 5 + [i32] * 3 + [f32] + [i64] * 3 + [vp] * 10
+        lib.ssm_gated_delta_bwd_workspace_bytes.restype = sz
+        lib.ssm_gated_delta_bwd_workspace_bytes.argtypes = [i64] * 6 + [i32]
+        lib.ssm_gated_delta_bwd.restype = i32
+        lib.ssm_gated_delta_bwd.argtypes = [i64] * 6 + [i32] * 2 + [f32] + [i64] * 3 + [vp] * 20 + [sz, vp]
+        lib.ssm_rms_norm_fwd.restype = i32
+        lib.ssm_rms_norm_fwd.argtypes = [i64] * 2 + [i32] * 3 + [f32] + [vp] * 7
+        lib.ssm_rms_norm_bwd_workspace_bytes.restype = sz
+        lib.ssm_rms_norm_bwd_workspace_bytes.argtypes = [i64] * 2
+        lib.ssm_rms_norm_bwd.restype = i32
+        lib.ssm_rms_norm_bwd.argtypes = [i64] * 2 + [i32, f32] + [vp] * 7 + [sz, vp]
         _lib = lib
         return lib
 
@@ -518,3 +535,286 @@ def ssm_ssd_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=False,
     if return_final_state or h_final is not None:
         return y, h_final
     return y
+
+
+FLAG_BETA_SIGMOID = 4   # SSM_FLAG_BETA_SIGMOID
+FLAG_QK_L2NORM = 8      # SSM_FLAG_QK_L2NORM
+
+
+def _step_of(name, t, lead, dense):
+    """Elements between consecutive steps of t, whose last two dimensions are
+    dense and whose first ``lead`` are rows at one distance (a column range of
+    a wider dense array, or a dense array)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.numel() == 0:
+        return dense
+    heads, width = t.shape[lead:]
+    step, rows = None, 1
+    for i in reversed(range(lead)):
+        if t.shape[i] > 1:
+            if step is None:
+                if t.stride(i) % rows:
+                    raise ValueError(f"{name}: rows must be at one distance")
+                step = t.stride(i) // rows
+            elif t.stride(i) != step * rows:
+                raise ValueError(f"{name}: batch rows must follow each other (seqlen steps apart)")
+        rows *= t.shape[i]
+    if (width > 1 and t.stride(lead + 1) != 1) or (heads > 1 and t.stride(lead) != width):
+        raise ValueError(f"{name}: heads and their channels must be dense")
+    return dense if step is None else step
+
+
+def _strided_tensor(name, t, shape, dtype, device):
+    """Checks of a tensor that may be a column range; contiguity is _step_of's matter."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor (got {t.device}); there is no CPU path")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+
+
+def _gdr_inputs(q, k, v, dt, A, beta, dt_bias, lead):
+    """Checked sizes (lead sizes, G, H, P, N), device and steps of the gated delta rule's inputs."""
+    for name, t in (("q", q), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != lead + 2:
+            raise ValueError(f"{name} must be a {lead + 2}-d tensor")
+    if q.dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported input dtype {q.dtype}")
+    dev, ind = q.device, q.dtype
+    rows, (G, N), (H, P) = tuple(q.shape[:lead]), q.shape[lead:], v.shape[lead:]
+    _strided_tensor("q", q, rows + (G, N), ind, dev)
+    _strided_tensor("k", k, rows + (G, N), ind, dev)
+    _strided_tensor("v", v, rows + (H, P), ind, dev)
+    _dev_tensor("dt", dt, rows + (H,), (ind,), dev)
+    _dev_tensor("beta", beta, rows + (H,), (ind,), dev)
+    _dev_tensor("A", A, (H,), (torch.float32,), dev)
+    _dev_tensor("dt_bias", dt_bias, (H,), (torch.float32,), dev)
+    if dt is None or beta is None or A is None:
+        raise ValueError("dt, A and beta are required")
+    steps = (_step_of("q", q, lead, G * N), _step_of("k", k, lead, G * N), _step_of("v", v, lead, H * P))
+    return rows, G, H, P, N, dev, steps
+
+
+def _gdr_flags(dt_softplus, beta_sigmoid, qk_l2norm):
+    return ((FLAG_SOFTPLUS if dt_softplus else 0) | (FLAG_BETA_SIGMOID if beta_sigmoid else 0)
+            | (FLAG_QK_L2NORM if qk_l2norm else 0))
+
+
+def ssm_gated_delta_workspace_bytes(batch, seqlen, nkheads, nheads, headdim, dstate, in_dtype) -> int:
+    return int(_load().ssm_gated_delta_workspace_bytes(batch, seqlen, nkheads, nheads, headdim, dstate,
+                                                       _DTYPE_CODE[in_dtype]))
+
+
+def ssm_gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=False, beta_sigmoid=False,
+                        qk_l2norm=False, scale=None, h0=None, seqlens=None, out_dtype=None,
+                        return_final_state=False, y=None, h_final=None, workspace=None, stream=None):
+    """Gated delta rule forward; see ssm_gated_delta_fwd in include/ssm_scan.h.
+
+    q, k: [B, L, G, N]; v: [B, L, H, P]; dt, beta: [B, L, H] (all float32 or
+    all bfloat16); A, dt_bias: [H], h0: [B, H, P, N] float32; seqlens: [B]
+    int32. q, k and v may be column ranges of one wider dense array. ``scale``
+    defaults to N**-0.5. Returns y ([B, L, H, P]) or (y, h_final).
+    """
+    lib = _load()
+    (Bt, L), G, H, P, N, dev, steps = _gdr_inputs(q, k, v, dt, A, beta, dt_bias, 2)
+    _dev_tensor("h0", h0, (Bt, H, P, N), (torch.float32,), dev)
+    _dev_tensor("seqlens", seqlens, (Bt,), (torch.int32,), dev)
+    out_dtype = q.dtype if out_dtype is None else out_dtype
+    if out_dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported output dtype {out_dtype}")
+    scale = N ** -0.5 if scale is None else float(scale)
+    with _launch_context(dev, stream):
+        if y is None:
+            y = torch.empty((Bt, L, H, P), dtype=out_dtype, device=dev)
+        _dev_tensor("y", y, (Bt, L, H, P), (out_dtype,), dev)
+        if return_final_state and h_final is None:
+            h_final = torch.empty((Bt, H, P, N), dtype=torch.float32, device=dev)
+        _dev_tensor("h_final", h_final, (Bt, H, P, N), (torch.float32,), dev)
+        code = _DTYPE_CODE[q.dtype]
+        ws_bytes = int(lib.ssm_gated_delta_workspace_bytes(Bt, L, G, H, P, N, code))
+        if workspace is None and ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        ws_size = _check_workspace(workspace, dev)
+        st = lib.ssm_gated_delta_fwd(Bt, L, G, H, P, N, code, _DTYPE_CODE[out_dtype],
+                                     _gdr_flags(dt_softplus, beta_sigmoid, qk_l2norm), scale, *steps,
+                                     _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(beta), _ptr(dt_bias),
+                                     _ptr(h0), _ptr(seqlens), _ptr(y), _ptr(h_final), _ptr(workspace), ws_size,
+                                     _stream_handle(stream, dev))
+    _check("ssm_gated_delta_fwd", st)
+    if return_final_state or h_final is not None:
+        return y, h_final
+    return y
+
+
+def ssm_gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, dt_softplus=False, beta_sigmoid=False,
+                           qk_l2norm=False, scale=None, out_dtype=None, y=None, stream=None):
+    """One token of the gated delta rule, in place on ``state``; see
+    ssm_gated_delta_update in include/ssm_scan.h.
+
+    state: [B, H, P, N] float32 (updated in place); q, k: [B, G, N]; v:
+    [B, H, P]; dt, beta: [B, H]. Returns y [B, H, P].
+    """
+    lib = _load()
+    (Bt,), G, H, P, N, dev, steps = _gdr_inputs(q, k, v, dt, A, beta, dt_bias, 1)
+    _dev_tensor("state", state, (Bt, H, P, N), (torch.float32,), dev)
+    if state is None:
+        raise ValueError("state is required")
+    out_dtype = q.dtype if out_dtype is None else out_dtype
+    if out_dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported output dtype {out_dtype}")
+    scale = N ** -0.5 if scale is None else float(scale)
+    with _launch_context(dev, stream):
+        if y is None:
+            y = torch.empty((Bt, H, P), dtype=out_dtype, device=dev)
+        _dev_tensor("y", y, (Bt, H, P), (out_dtype,), dev)
+        st = lib.ssm_gated_delta_update(Bt, G, H, P, N, _DTYPE_CODE[q.dtype], _DTYPE_CODE[out_dtype],
+                                        _gdr_flags(dt_softplus, beta_sigmoid, qk_l2norm), scale, *steps,
+                                        _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(beta),
+                                        _ptr(dt_bias), _ptr(y), _stream_handle(stream, dev))
+    _check("ssm_gated_delta_update", st)
+    return y
+
+
+def ssm_gated_delta_bwd_workspace_bytes(batch, seqlen, nkheads, nheads, headdim, dstate, in_dtype) -> int:
+    return int(_load().ssm_gated_delta_bwd_workspace_bytes(batch, seqlen, nkheads, nheads, headdim, dstate,
+                                                           _DTYPE_CODE[in_dtype]))
+
+
+def ssm_gated_delta_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, dt_softplus=False, beta_sigmoid=False,
+                        qk_l2norm=False, scale=None, h0=None, dh_final=None, seqlens=None, workspace=None,
+                        stream=None):
+    """Gradients of the gated delta rule; see ssm_gated_delta_bwd in include/ssm_scan.h.
+
+    Inputs as ssm_gated_delta_fwd, plus dy [B, L, H, P] and dh_final
+    [B, H, P, N] (float32). Returns a dict of float32 tensors: dq, dk, dv, ddt,
+    dA, dbeta, dh0, and ddt_bias when dt_bias is given.
+    """
+    lib = _load()
+    (Bt, L), G, H, P, N, dev, steps = _gdr_inputs(q, k, v, dt, A, beta, dt_bias, 2)
+    f32 = (torch.float32,)
+    _dev_tensor("h0", h0, (Bt, H, P, N), f32, dev)
+    _dev_tensor("seqlens", seqlens, (Bt,), (torch.int32,), dev)
+    _dev_tensor("dy", dy, (Bt, L, H, P), f32, dev)
+    _dev_tensor("dh_final", dh_final, (Bt, H, P, N), f32, dev)
+    scale = N ** -0.5 if scale is None else float(scale)
+    new = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)  # noqa: E731
+    with _launch_context(dev, stream):
+        g = dict(dq=new(Bt, L, G, N), dk=new(Bt, L, G, N), dv=new(Bt, L, H, P), ddt=new(Bt, L, H), dA=new(H),
+                 dbeta=new(Bt, L, H), dh0=new(Bt, H, P, N))
+        if dt_bias is not None:
+            g["ddt_bias"] = new(H)
+        code = _DTYPE_CODE[q.dtype]
+        ws_bytes = int(lib.ssm_gated_delta_bwd_workspace_bytes(Bt, L, G, H, P, N, code))
+        if workspace is None and ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        ws_size = _check_workspace(workspace, dev)
+        st = lib.ssm_gated_delta_bwd(Bt, L, G, H, P, N, code, _gdr_flags(dt_softplus, beta_sigmoid, qk_l2norm),
+                                     scale, *steps, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(beta),
+                                     _ptr(dt_bias), _ptr(h0), _ptr(seqlens), _ptr(dy), _ptr(dh_final),
+                                     _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["ddt"]), _ptr(g["dA"]),
+                                     _ptr(g["dbeta"]), _ptr(g.get("ddt_bias")), _ptr(g["dh0"]), _ptr(workspace),
+                                     ws_size, _stream_handle(stream, dev))
+    _check("ssm_gated_delta_bwd", st)
+    return g
+
+
+_E4M3 = 2  # out_dtype code of the norm's 8-bit output
+
+
+def ssm_rms_norm_fwd(x, weight=None, residual=None, eps=1e-5, out_dtype=None, y=None, residual_out=None,
+                     scales=None, stream=None):
+    """RMS norm of rows with the residual's addition; see ssm_rms_norm_fwd in include/ssm_scan.h.
+
+    x: [..., d] float32 or bfloat16, contiguous; residual: the same shape,
+    float32 or bfloat16; weight: [d] float32. ``out_dtype``: float32, bfloat16
+    or float8_e4m3fn (with a float32 scale a row). Returns a dict: y, and
+    residual_out (with a residual; may be the residual itself) and scales [...]
+    (with the 8-bit output).
+    """
+    lib = _load()
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.dtype not in _DTYPE_CODE:
+        raise ValueError("x must be a float32 or bfloat16 tensor [..., d]")
+    dev, d = x.device, x.shape[-1]
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    _dev_tensor("x", x, x.shape, (x.dtype,), dev)
+    _dev_tensor("weight", weight, (d,), (torch.float32,), dev)
+    _dev_tensor("residual", residual, x.shape, (torch.float32, torch.bfloat16), dev)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    eight = out_dtype == torch.float8_e4m3fn
+    if not eight and out_dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported output dtype {out_dtype}")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if scales is not None and not eight:
+        raise ValueError("scales are written for the 8-bit output only")
+    with _launch_context(dev, stream):
+        if y is None:
+            y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        _dev_tensor("y", y, x.shape, (out_dtype,), dev)
+        if residual is not None:
+            if residual_out is None:
+                residual_out = torch.empty_like(residual)
+            _dev_tensor("residual_out", residual_out, x.shape, (residual.dtype,), dev)
+        if eight and scales is None:
+            scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        _dev_tensor("scales", scales, x.shape[:-1], (torch.float32,), dev)
+        st = lib.ssm_rms_norm_fwd(rows, d, _DTYPE_CODE[x.dtype], 0 if residual is None else _DTYPE_CODE[residual.dtype],
+                                  _E4M3 if eight else _DTYPE_CODE[out_dtype], float(eps), _ptr(x), _ptr(residual),
+                                  _ptr(weight), _ptr(y), _ptr(residual_out), _ptr(scales),
+                                  _stream_handle(stream, dev))
+    _check("ssm_rms_norm_fwd", st)
+    out = {"y": y}
+    if residual is not None:
+        out["residual_out"] = residual_out
+    if eight:
+        out["scales"] = scales
+    return out
+
+
+def ssm_rms_norm_bwd_workspace_bytes(rows, dim) -> int:
+    return int(_load().ssm_rms_norm_bwd_workspace_bytes(rows, dim))
+
+
+def ssm_rms_norm_bwd(s, weight, dy, dresidual=None, eps=1e-5, ds=None, workspace=None, stream=None):
+    """Gradients of the RMS norm; see ssm_rms_norm_bwd in include/ssm_scan.h.
+
+    s: what the forward normalised (residual_out, or x without a residual)
+    [..., d]; weight: [d] float32 or None; dy, dresidual: [..., d] float32.
+    Returns (ds, dweight), float32; ds is the gradient of x and of the residual.
+    """
+    lib = _load()
+    if not isinstance(s, torch.Tensor) or s.dim() < 1 or s.dtype not in _DTYPE_CODE:
+        raise ValueError("s must be a float32 or bfloat16 tensor [..., d]")
+    dev, d = s.device, s.shape[-1]
+    rows = 1
+    for n in s.shape[:-1]:
+        rows *= n
+    f32 = (torch.float32,)
+    _dev_tensor("s", s, s.shape, (s.dtype,), dev)
+    _dev_tensor("weight", weight, (d,), f32, dev)
+    if dy is None:
+        raise ValueError("dy is required")
+    _dev_tensor("dy", dy, s.shape, f32, dev)
+    _dev_tensor("dresidual", dresidual, s.shape, f32, dev)
+    with _launch_context(dev, stream):
+        if ds is None:
+            ds = torch.empty(s.shape, dtype=torch.float32, device=dev)
+        _dev_tensor("ds", ds, s.shape, f32, dev)
+        dweight = torch.empty((d,), dtype=torch.float32, device=dev)
+        ws_bytes = int(lib.ssm_rms_norm_bwd_workspace_bytes(rows, d))
+        if workspace is None and ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        ws_size = _check_workspace(workspace, dev)
+        st = lib.ssm_rms_norm_bwd(rows, d, _DTYPE_CODE[s.dtype], float(eps), _ptr(s), _ptr(weight), _ptr(dy),
+                                  _ptr(dresidual), _ptr(ds), _ptr(dweight), _ptr(workspace), ws_size,
+                                  _stream_handle(stream, dev))
+    _check("ssm_rms_norm_bwd", st)
+    return ds, dweight

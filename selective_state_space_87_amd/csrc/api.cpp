@@ -593,3 +593,370 @@ int ssm_ssd_fwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, 
 }
 
 }  // extern "C"
+
+namespace {
+
+struct GdrSizes {
+  int64_t batch, seqlen, nkheads, nheads, headdim, dstate;
+  int64_t bl, blh, blhp, blgn, bh, bhpn;  // products of the sizes
+};
+
+int gdr_sizes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, int64_t headdim, int64_t dstate,
+              int in_dtype, GdrSizes* z) {
+  if (batch < 0 || seqlen < 0 || nkheads < 0 || nheads < 0 || headdim < 1 || dstate < 1) return SSM_E_SHAPE;
+  if (nkheads == 0 ? nheads != 0 : nheads % nkheads != 0) return SSM_E_SHAPE;
+  if (headdim > ssm::kGdrMaxHeadDim || dstate > ssm::kGdrMaxState) return SSM_E_UNSUPPORTED;
+  if (in_dtype != 0 && in_dtype != 1) return SSM_E_DTYPE;
+  *z = GdrSizes{batch, seqlen, nkheads, nheads, headdim, dstate, 0, 0, 0, 0, 0, 0};
+  int64_t t;
+  if (!safe_mul(batch, seqlen, &z->bl) || !safe_mul(z->bl, nheads, &z->blh) ||
+      !safe_mul(z->blh, headdim, &z->blhp) || !safe_mul(z->bl, nkheads, &t) || !safe_mul(t, dstate, &z->blgn) ||
+      !safe_mul(batch, nheads, &z->bh) || !safe_mul(z->bh, headdim, &t) || !safe_mul(t, dstate, &z->bhpn)) {
+    return SSM_E_SHAPE;
+  }
+  if (seqlen >= (int64_t(1) << 30) || z->bh * headdim > 0x7fffffff) return SSM_E_UNSUPPORTED;
+  // one (batch row, head, 64 steps) item a block
+  if (z->bh * ((seqlen + 63) / 64) > 0x7fffffff) return SSM_E_UNSUPPORTED;
+  return SSM_OK;
+}
+
+int gdr_options(const GdrSizes& z, int flags, int64_t q_step, int64_t k_step, int64_t v_step) {
+  if ((flags & ~(SSM_FLAG_SOFTPLUS | SSM_FLAG_BETA_SIGMOID | SSM_FLAG_QK_L2NORM)) != 0) return SSM_E_UNSUPPORTED;
+  if (q_step < z.nkheads * z.dstate || k_step < z.nkheads * z.dstate || v_step < z.nheads * z.headdim) {
+    return SSM_E_SHAPE;
+  }
+  // the rows of 64 steps are addressed with 32-bit offsets
+  constexpr int64_t most = int64_t(1) << 23;
+  if (q_step >= most || k_step >= most || v_step >= most) return SSM_E_UNSUPPORTED;
+  int64_t t;
+  if (!safe_mul(z.bl, q_step, &t) || !safe_mul(z.bl, k_step, &t) || !safe_mul(z.bl, v_step, &t)) return SSM_E_SHAPE;
+  return SSM_OK;
+}
+
+// Elements from the first to the last of a [B L, step] array whose rows hold `width`.
+int64_t strided(int64_t rows, int64_t step, int64_t width) { return rows > 0 ? (rows - 1) * step + width : 0; }
+
+// in[0..8]: q, k, v, dt, A, beta, dt_bias, h0, seqlens.
+void gdr_inputs(const GdrSizes& z, int64_t isz, int64_t q_step, int64_t k_step, int64_t v_step, const void* q,
+                const void* k, const void* v, const void* dt, const float* A, const void* beta,
+                const float* dt_bias, const float* h0, const int32_t* seqlens, Range* in) {
+  in[0] = span(q, strided(z.bl, q_step, z.nkheads * z.dstate), isz);
+  in[1] = span(k, strided(z.bl, k_step, z.nkheads * z.dstate), isz);
+  in[2] = span(v, strided(z.bl, v_step, z.nheads * z.headdim), isz);
+  in[3] = span(dt, z.blh, isz);
+  in[4] = span(A, z.nheads, 4);
+  in[5] = span(beta, z.blh, isz);
+  in[6] = span(dt_bias, z.nheads, 4);
+  in[7] = span(h0, z.bhpn, 4);
+  in[8] = span(seqlens, z.batch, 4);
+}
+
+ssm::GatedDeltaArgs gdr_args(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, int64_t headdim,
+                             int64_t dstate, int in_dtype, int flags, float scale, int64_t q_step, int64_t k_step,
+                             int64_t v_step, const void* q, const void* k, const void* v, const void* dt,
+                             const float* A, const void* beta, const float* dt_bias, const float* h0,
+                             const int32_t* seqlens) {
+  ssm::GatedDeltaArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.dt = dt;
+  a.A = A;
+  a.beta = beta;
+  a.dt_bias = dt_bias;
+  a.h0 = h0;
+  a.seqlens = seqlens;
+  a.batch = batch;
+  a.seqlen = seqlen;
+  a.nkheads = nkheads;
+  a.nheads = nheads;
+  a.headdim = headdim;
+  a.dstate = dstate;
+  a.q_step = q_step;
+  a.k_step = k_step;
+  a.v_step = v_step;
+  a.scale = scale;
+  a.in_bf16 = in_dtype;
+  a.dt_softplus = (flags & SSM_FLAG_SOFTPLUS) != 0;
+  a.beta_sigmoid = (flags & SSM_FLAG_BETA_SIGMOID) != 0;
+  a.qk_l2norm = (flags & SSM_FLAG_QK_L2NORM) != 0;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssm_gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
+                                       int64_t headdim, int64_t dstate, int in_dtype) {
+  GdrSizes z;
+  if (gdr_sizes(batch, seqlen, nkheads, nheads, headdim, dstate, in_dtype, &z) != SSM_OK) return 0;
+  return ssm::gated_delta_workspace_bytes(batch, seqlen, nkheads, nheads, headdim, dstate, in_dtype);
+}
+
+int ssm_gated_delta_fwd(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
+                        int64_t headdim, int64_t dstate, int in_dtype, int out_dtype, int flags, float scale,
+                        int64_t q_step, int64_t k_step, int64_t v_step,
+                        const void* q, const void* k, const void* v, const void* dt, const float* A,
+                        const void* beta, const float* dt_bias, const float* h0, const int32_t* seqlens,
+                        void* y, float* h_final, void* workspace, size_t workspace_bytes, void* stream) {
+  GdrSizes z;
+  if (const int st = gdr_sizes(batch, seqlen, nkheads, nheads, headdim, dstate, in_dtype, &z)) return st;
+  if (out_dtype != 0 && out_dtype != 1) return SSM_E_DTYPE;
+  if (const int st = gdr_options(z, flags, q_step, k_step, v_step)) return st;
+  if (z.bh == 0) return SSM_OK;  // no head: nothing to compute or write
+  if (A == nullptr) return SSM_E_NULLPTR;
+  if (seqlen > 0 && (q == nullptr || k == nullptr || v == nullptr || dt == nullptr || beta == nullptr ||
+                     y == nullptr)) {
+    return SSM_E_NULLPTR;
+  }
+  const int64_t isz = in_dtype == 1 ? 2 : 4, osz = out_dtype == 1 ? 2 : 4;
+  const void* in_ptrs[] = {q, k, v, dt, beta};
+  for (const void* p : in_ptrs) {
+    if (p && !aligned(p, static_cast<uintptr_t>(isz))) return SSM_E_ALIGN;
+  }
+  const void* f32_ptrs[] = {A, dt_bias, h0, h_final, seqlens};
+  for (const void* p : f32_ptrs) {
+    if (p && !aligned(p, 4)) return SSM_E_ALIGN;
+  }
+  if (y && !aligned(y, static_cast<uintptr_t>(osz))) return SSM_E_ALIGN;
+  const size_t need =
+      ssm::gated_delta_workspace_bytes(batch, seqlen, nkheads, nheads, headdim, dstate, in_dtype);
+  if (need > 0 && workspace != nullptr && !aligned(workspace, 16)) return SSM_E_ALIGN;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_E_WORKSPACE;
+
+  Range in[9];
+  gdr_inputs(z, isz, q_step, k_step, v_step, q, k, v, dt, A, beta, dt_bias, h0, seqlens, in);
+  const Range ry = span(y, z.blhp, osz), rhf = span(h_final, z.bhpn, 4);
+  const Range rws = span(need > 0 ? workspace : nullptr, static_cast<int64_t>(need), 1);
+  for (const Range& r : in) {
+    if (overlaps(ry, r) || overlaps(rws, r)) return SSM_E_ALIAS;
+    const bool same_h0 = &r == &in[7] && rhf.lo == r.lo && rhf.hi == r.hi;
+    if (!same_h0 && overlaps(rhf, r)) return SSM_E_ALIAS;
+  }
+  if (overlaps(ry, rhf) || overlaps(ry, rws) || overlaps(rhf, rws)) return SSM_E_ALIAS;
+
+  ssm::GatedDeltaArgs a = gdr_args(batch, seqlen, nkheads, nheads, headdim, dstate, in_dtype, flags, scale,
+                                   q_step, k_step, v_step, q, k, v, dt, A, beta, dt_bias, h0, seqlens);
+  a.y = y;
+  a.h_final = h_final;
+  a.out_bf16 = out_dtype;
+  a.workspace = workspace;
+  return ssm::launch_gated_delta ? map_hip(ssm::launch_gated_delta(a, stream)) : SSM_E_HIP;
+}
+
+int ssm_gated_delta_update(int64_t batch, int64_t nkheads, int64_t nheads, int64_t headdim, int64_t dstate,
+                           int in_dtype, int out_dtype, int flags, float scale,
+                           int64_t q_step, int64_t k_step, int64_t v_step,
+                           float* state, const void* q, const void* k, const void* v, const void* dt,
+                           const float* A, const void* beta, const float* dt_bias, void* y, void* stream) {
+  GdrSizes z;
+  if (const int st = gdr_sizes(batch, 1, nkheads, nheads, headdim, dstate, in_dtype, &z)) return st;
+  if (out_dtype != 0 && out_dtype != 1) return SSM_E_DTYPE;
+  if (const int st = gdr_options(z, flags, q_step, k_step, v_step)) return st;
+  if (z.bh == 0) return SSM_OK;
+  if (state == nullptr || q == nullptr || k == nullptr || v == nullptr || dt == nullptr || A == nullptr ||
+      beta == nullptr || y == nullptr) {
+    return SSM_E_NULLPTR;
+  }
+  const int64_t isz = in_dtype == 1 ? 2 : 4, osz = out_dtype == 1 ? 2 : 4;
+  const void* in_ptrs[] = {q, k, v, dt, beta};
+  for (const void* p : in_ptrs) {
+    if (!aligned(p, static_cast<uintptr_t>(isz))) return SSM_E_ALIGN;
+  }
+  if (!aligned(state, 16) || !aligned(A, 4) || (dt_bias && !aligned(dt_bias, 4)) ||
+      !aligned(y, static_cast<uintptr_t>(osz))) {
+    return SSM_E_ALIGN;
+  }
+  Range in[9];
+  gdr_inputs(z, isz, q_step, k_step, v_step, q, k, v, dt, A, beta, dt_bias, nullptr, nullptr, in);
+  const Range ry = span(y, z.blhp, osz), rs = span(state, z.bhpn, 4);
+  for (const Range& r : in) {
+    if (overlaps(ry, r) || overlaps(rs, r)) return SSM_E_ALIAS;
+  }
+  if (overlaps(ry, rs)) return SSM_E_ALIAS;
+
+  ssm::GatedDeltaArgs a = gdr_args(batch, 1, nkheads, nheads, headdim, dstate, in_dtype, flags, scale, q_step,
+                                   k_step, v_step, q, k, v, dt, A, beta, dt_bias, state, nullptr);
+  a.y = y;
+  a.h_final = state;
+  a.out_bf16 = out_dtype;
+  return ssm::launch_gated_delta_update ? map_hip(ssm::launch_gated_delta_update(a, stream)) : SSM_E_HIP;
+}
+
+size_t ssm_gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
+                                           int64_t headdim, int64_t dstate, int in_dtype) {
+  GdrSizes z;
+  if (gdr_sizes(batch, seqlen, nkheads, nheads, headdim, dstate, in_dtype, &z) != SSM_OK) return 0;
+  return ssm::gated_delta_bwd_workspace_bytes(batch, seqlen, nkheads, nheads, headdim, dstate, in_dtype);
+}
+
+int ssm_gated_delta_bwd(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
+                        int64_t headdim, int64_t dstate, int in_dtype, int flags, float scale,
+                        int64_t q_step, int64_t k_step, int64_t v_step,
+                        const void* q, const void* k, const void* v, const void* dt, const float* A,
+                        const void* beta, const float* dt_bias, const float* h0, const int32_t* seqlens,
+                        const float* dy, const float* dh_final,
+                        float* dq, float* dk, float* dv, float* ddt, float* dA, float* dbeta,
+                        float* ddt_bias, float* dh0, void* workspace, size_t workspace_bytes, void* stream) {
+  GdrSizes z;
+  if (const int st = gdr_sizes(batch, seqlen, nkheads, nheads, headdim, dstate, in_dtype, &z)) return st;
+  if (const int st = gdr_options(z, flags, q_step, k_step, v_step)) return st;
+  if (nheads == 0) return SSM_OK;
+  if (A == nullptr || dA == nullptr) return SSM_E_NULLPTR;
+  if (z.blh > 0 && (q == nullptr || k == nullptr || v == nullptr || dt == nullptr || beta == nullptr ||
+                    dy == nullptr || dq == nullptr || dk == nullptr || dv == nullptr || ddt == nullptr ||
+                    dbeta == nullptr)) {
+    return SSM_E_NULLPTR;
+  }
+  const int64_t isz = in_dtype == 1 ? 2 : 4;
+  const void* in_ptrs[] = {q, k, v, dt, beta};
+  for (const void* p : in_ptrs) {
+    if (p && !aligned(p, static_cast<uintptr_t>(isz))) return SSM_E_ALIGN;
+  }
+  const void* f32_ptrs[] = {A, dt_bias, h0, seqlens, dy, dh_final, dq, dk, dv, ddt, dA, dbeta, ddt_bias, dh0};
+  for (const void* p : f32_ptrs) {
+    if (p && !aligned(p, 4)) return SSM_E_ALIGN;
+  }
+  const size_t need =
+      ssm::gated_delta_bwd_workspace_bytes(batch, seqlen, nkheads, nheads, headdim, dstate, in_dtype);
+  if (need > 0 && workspace != nullptr && !aligned(workspace, 16)) return SSM_E_ALIGN;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_E_WORKSPACE;
+
+  Range in[11];
+  gdr_inputs(z, isz, q_step, k_step, v_step, q, k, v, dt, A, beta, dt_bias, h0, seqlens, in);
+  in[9] = span(dy, z.blhp, 4);
+  in[10] = span(dh_final, z.bhpn, 4);
+  const int64_t gn = z.blgn;
+  const Range out[] = {span(dq, gn, 4),      span(dk, gn, 4),    span(dv, z.blhp, 4),
+                       span(ddt, z.blh, 4),  span(dA, nheads, 4), span(dbeta, z.blh, 4),
+                       span(dt_bias ? ddt_bias : nullptr, nheads, 4), span(dh0, z.bhpn, 4),
+                       span(need > 0 ? workspace : nullptr, static_cast<int64_t>(need), 1)};
+  constexpr int kOut = sizeof(out) / sizeof(out[0]);
+  for (int i = 0; i < kOut; ++i) {
+    for (const Range& r : in) {
+      if (overlaps(out[i], r)) return SSM_E_ALIAS;
+    }
+    for (int j = 0; j < i; ++j) {
+      if (overlaps(out[i], out[j])) return SSM_E_ALIAS;
+    }
+  }
+
+  ssm::GatedDeltaBwdArgs a;
+  a.f = gdr_args(batch, seqlen, nkheads, nheads, headdim, dstate, in_dtype, flags, scale, q_step, k_step, v_step,
+                 q, k, v, dt, A, beta, dt_bias, h0, seqlens);
+  a.f.workspace = workspace;
+  a.dy = dy;
+  a.dh_final = dh_final;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.ddt = ddt;
+  a.dA = dA;
+  a.dbeta = dbeta;
+  a.ddt_bias = dt_bias ? ddt_bias : nullptr;
+  a.dh0 = dh0;
+  return ssm::launch_gated_delta_bwd ? map_hip(ssm::launch_gated_delta_bwd(a, stream)) : SSM_E_HIP;
+}
+
+int ssm_rms_norm_fwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, int out_dtype, float eps,
+                     const void* x, const void* residual, const float* weight,
+                     void* y, void* residual_out, float* scales, void* stream) {
+  int64_t n;
+  if (rows < 0 || dim < 1 || !safe_mul(rows, dim, &n)) return SSM_E_SHAPE;
+  if (dim > ssm::kRmsMaxDim || rows > 0x7fffffff || !(eps >= 0.0f)) return SSM_E_UNSUPPORTED;
+  if ((in_dtype != 0 && in_dtype != 1) || (residual && res_dtype != 0 && res_dtype != 1) || out_dtype < 0 ||
+      out_dtype > 2) {
+    return SSM_E_DTYPE;
+  }
+  if (rows == 0) return SSM_OK;
+  if (x == nullptr || y == nullptr || (residual == nullptr) != (residual_out == nullptr) ||
+      (out_dtype == 2) != (scales != nullptr)) {
+    return SSM_E_NULLPTR;
+  }
+  const int64_t isz = in_dtype == 1 ? 2 : 4, rsz = res_dtype == 1 ? 2 : 4;
+  const int64_t osz = out_dtype == 0 ? 4 : (out_dtype == 1 ? 2 : 1);
+  if (!aligned(x, static_cast<uintptr_t>(isz)) || !aligned(residual, static_cast<uintptr_t>(rsz)) ||
+      !aligned(residual_out, static_cast<uintptr_t>(rsz)) || !aligned(weight, 4) || !aligned(scales, 4) ||
+      !aligned(y, static_cast<uintptr_t>(osz))) {
+    return SSM_E_ALIGN;
+  }
+  const Range rx = span(x, n, isz), rr = span(residual, n, rsz), rw = span(weight, dim, 4);
+  const Range ry = span(y, n, osz), ro = span(residual_out, n, rsz), rs = span(scales, rows, 4);
+  if (overlaps(ry, rx) || overlaps(ry, rr) || overlaps(ry, rw) || overlaps(ry, ro) || overlaps(ry, rs) ||
+      overlaps(ro, rx) || overlaps(ro, rw) || overlaps(ro, rs) || overlaps(rs, rx) || overlaps(rs, rr) ||
+      overlaps(rs, rw)) {
+    return SSM_E_ALIAS;
+  }
+  if (overlaps(ro, rr) && ro.lo != rr.lo) return SSM_E_ALIAS;
+
+  ssm::RmsNormArgs a;
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.y = y;
+  a.residual_out = residual_out;
+  a.scales = scales;
+  a.rows = rows;
+  a.dim = dim;
+  a.in_bf16 = in_dtype;
+  a.res_bf16 = residual ? res_dtype : 0;
+  a.out_type = out_dtype;
+  a.eps = eps;
+  return ssm::launch_rms_norm ? map_hip(ssm::launch_rms_norm(a, stream)) : SSM_E_HIP;
+}
+
+size_t ssm_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t dim) {
+  int64_t n;
+  if (rows < 1 || dim < 1 || dim > ssm::kRmsMaxDim || rows > 0x7fffffff || !safe_mul(rows, dim, &n)) return 0;
+  return static_cast<size_t>(ssm::rms_norm_bwd_blocks(rows, dim)) * static_cast<size_t>(dim) * 4;
+}
+
+int ssm_rms_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps,
+                     const void* s, const float* weight, const float* dy, const float* dresidual,
+                     float* ds, float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+  int64_t n;
+  if (rows < 0 || dim < 1 || !safe_mul(rows, dim, &n)) return SSM_E_SHAPE;
+  if (dim > ssm::kRmsMaxDim || rows > 0x7fffffff || !(eps >= 0.0f)) return SSM_E_UNSUPPORTED;
+  if (s_dtype != 0 && s_dtype != 1) return SSM_E_DTYPE;
+  if (rows == 0 && dweight == nullptr) return SSM_OK;
+  if (rows > 0 && (s == nullptr || dy == nullptr || ds == nullptr)) return SSM_E_NULLPTR;
+  const int64_t ssz = s_dtype == 1 ? 2 : 4;
+  const void* f32_ptrs[] = {weight, dy, dresidual, ds, dweight};
+  for (const void* p : f32_ptrs) {
+    if (!aligned(p, 4)) return SSM_E_ALIGN;
+  }
+  if (!aligned(s, static_cast<uintptr_t>(ssz))) return SSM_E_ALIGN;
+  const size_t need = dweight ? ssm_rms_norm_bwd_workspace_bytes(rows, dim) : 0;
+  if (need > 0 && workspace != nullptr && !aligned(workspace, 16)) return SSM_E_ALIGN;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_E_WORKSPACE;
+  const Range rs = span(s, n, ssz), rw = span(weight, dim, 4), ry = span(dy, n, 4), rr = span(dresidual, n, 4);
+  const Range rds = span(ds, n, 4), rdw = span(dweight, dim, 4);
+  const Range rws = span(need > 0 ? workspace : nullptr, static_cast<int64_t>(need), 1);
+  const Range fixed[] = {rs, rw, rdw, rws};
+  for (const Range& r : fixed) {
+    if (overlaps(rds, r)) return SSM_E_ALIAS;
+  }
+  if ((overlaps(rds, ry) && rds.lo != ry.lo) || (overlaps(rds, rr) && rds.lo != rr.lo)) return SSM_E_ALIAS;
+  const Range in[] = {rs, rw, ry, rr};
+  for (const Range& r : in) {
+    if (overlaps(rdw, r) || overlaps(rws, r)) return SSM_E_ALIAS;
+  }
+  if (overlaps(rdw, rws)) return SSM_E_ALIAS;
+
+  ssm::RmsNormBwdArgs a;
+  a.s = s;
+  a.weight = weight;
+  a.dy = dy;
+  a.dresidual = dresidual;
+  a.ds = ds;
+  a.dweight = dweight;
+  a.workspace = workspace;
+  a.rows = rows;
+  a.dim = dim;
+  a.s_bf16 = s_dtype;
+  a.eps = eps;
+  return ssm::launch_rms_norm_bwd ? map_hip(ssm::launch_rms_norm_bwd(a, stream)) : SSM_E_HIP;
+}
+
+}  // extern "C"

@@ -137,4 +137,10 @@ size_t scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t 
   return p.ok ? p.bytes : 0;
 }
 
+size_t gated_delta_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int) { return 0; }
+
+size_t gated_delta_bwd_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int) { return 0; }
+
+int64_t rms_norm_bwd_blocks(int64_t rows, int64_t) { return rows < 512 ? rows : 512; }
+
 }  // namespace ssm
