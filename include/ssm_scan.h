@@ -461,8 +461,9 @@ int ssm_ssd_fwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, 
  *
  * q, k, v, dt, beta and y need the alignment of their element type only; rows
  * that start on 16-byte boundaries with N and P multiples of 8 are read
- * fastest. Products are taken in 22 bits or more of every float32 operand and
- * added in float32; results are bitwise deterministic. A value of a step that
+ * fastest. Products are taken in 22 bits or more of every float32 operand (11
+ * bits in those that only a bfloat16 y sees) and added in float32; results are
+ * bitwise deterministic. A value of a step that
  * is not finite may make every y and state element of its head NaN from the
  * start of its block of 64 steps on.
  */

@@ -18,6 +18,7 @@
 
 #include "device_math.h"
 #include "gated_delta.h"
+#include "gdr_mma.h"
 #include "kernels.h"
 
 namespace ssm {
@@ -193,7 +194,19 @@ int launch_gated_delta_update(const GatedDeltaArgs& a, void* stream) {
 }
 
 int launch_gated_delta(const GatedDeltaArgs& a, void* stream) {
-  return launch_gated_delta_recurrent(a, stream);
+  const GdrPlan pl = plan_gated_delta(a.batch, a.seqlen, a.nkheads, a.nheads, a.headdim, a.dstate);
+  if (pl.recurrent) return launch_gated_delta_recurrent(a, stream);
+  char* base = static_cast<char*>(a.workspace);
+  GdrWork ws;
+  ws.T = reinterpret_cast<_Float16*>(base + pl.off_t);
+  ws.Pm = reinterpret_cast<_Float16*>(base + pl.off_p);
+  ws.fac = reinterpret_cast<float*>(base + pl.off_fac);
+  const int64_t per16 = a.in_bf16 ? 8 : 4;  // elements in 16 bytes
+  const bool vec = a.dstate % 8 == 0 && a.q_step % per16 == 0 && a.k_step % per16 == 0 && on_boundary(a.q, 16) &&
+                   on_boundary(a.k, 16);
+  if (const int e = launch_gdr_prep(a, ws, pl.chunks, !a.out_bf16, vec, stream)) return e;
+  return a.in_bf16 ? launch_gdr_chunk_b(a, ws, pl.chunks, vec, stream)
+                   : launch_gdr_chunk_f(a, ws, pl.chunks, vec, stream);
 }
 
 }  // namespace ssm

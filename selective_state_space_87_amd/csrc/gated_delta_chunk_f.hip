@@ -1,0 +1,10 @@
+// Gated delta rule, the walk over a head's chunks: float32 inputs.
+#include "gated_delta_chunk.h"
+
+namespace ssm {
+
+int launch_gdr_chunk_f(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool vec, void* stream) {
+  return gdr_launch_chunk<false>(a, ws, static_cast<int>(chunks), vec, static_cast<hipStream_t>(stream));
+}
+
+}  // namespace ssm

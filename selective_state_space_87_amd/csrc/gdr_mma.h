@@ -1,0 +1,204 @@
+// The chunked form of the gated delta rule: operand precision, layouts and
+// workspace shared by its kernels (gfx950).
+//
+// A sequence is cut into chunks of 64 steps. With c_t the sum of the log decays
+// of a chunk's steps up to t, S the state entering the chunk, and row t of K, Q,
+// V the step's k, q, v:
+//   E  = T (V - diag(e^c) K S),      T = (1 + L diag(beta))^-1,
+//        L[t,s] = e^(c_t - c_s) k_t . k_s   for s < t
+//   Y  = scale diag(e^c) Q S + Pm E, Pm[t,s] = scale e^(c_t - c_s) q_t . k_s beta_s  for s <= t
+//   S' = e^(c_end) S + K^T diag(beta e^(c_end - c)) E
+// where row s of E is the error e_s of step s. T and Pm do not depend on the
+// state: one kernel makes them for all chunks at once, another walks a head's
+// chunks in order.
+//
+// Operands of the matrix cores. The state has to come out to float32's
+// precision whatever the inputs' type, and v_mfma_f32_16x16x4_f32 runs at a
+// sixteenth of the 16-bit rate. So every float32 operand x is split into two
+// halves hi + lo (float16, 11 bits each), after scaling its row or column by
+// the power of two that brings its largest element to [2^13, 2^14): an
+// element is then held to 22 bits, or to 2^-38 of the largest, and hi.hi +
+// hi.lo + lo.hi leaves out 2^-22 of a product. A bfloat16 input is one half
+// exactly (to 2^-37 of its row's largest element), so its products with split
+// operands take two instructions instead of three. The scales are powers of
+// two and leave again in the float32 factor that the result is multiplied with
+// anyway. (Two bfloat16 halves would hold 16 bits: 2^-17 of an element.)
+//
+// Layouts of v_mfma_f32_16x16x32_f16, lane l = 16 g + m: A[m][8 g + j],
+// B[8 g + j][m] (j = 0..7), D[4 g + i][m] (i = 0..3). The order of the 32
+// contraction indices is free as long as A and B agree, so the D of two tiles
+// is a B without moving anything between lanes: slot (g, j) stands for row
+// 4 g + j of the first tile (j < 4) or 4 g + j - 4 of the second. A wave keeps 16 columns of
+// the state for the whole sequence and forms everything that depends on it
+// in registers; only K, Q, T and Pm, which all waves share, come through LDS.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "gated_delta.h"
+
+namespace ssm {
+
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef short short4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kGdrC = 64;       // steps a chunk
+constexpr int kGdrFrags = 6;    // 16 x 32 pieces of a lower triangle of 64: (0,0) (1,0) (2,0) (2,1) (3,0) (3,1)
+constexpr int kGdrFragHalves = 64 * 8;
+
+// Index of the piece (row tile tt, half p) among the six.
+__device__ __forceinline__ constexpr int gdr_frag(int tt, int p) { return tt < 2 ? tt : 2 * tt - 2 + p; }
+
+__device__ __forceinline__ f32x4_t mfma16(half8_t a, half8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// The power of two that brings m >= 0 into [2^13, 2^14), and its inverse.
+// m below 2^-100 counts as 2^-100, infinity as 2^127.
+struct Pow2 {
+  float up, down;
+};
+__device__ __forceinline__ Pow2 pow2_to_top(float m) {
+  int e = static_cast<int>(__float_as_uint(m) >> 23);
+  e = e < 27 ? 27 : (e > 254 ? 254 : e);
+  return Pow2{__uint_as_float(static_cast<uint32_t>(267 - e) << 23), __uint_as_float(static_cast<uint32_t>(e - 13) << 23)};
+}
+
+// Largest value over the lanes l, l ^ 16, l ^ 32, l ^ 48 (those that share a column of D).
+__device__ __forceinline__ float col_max(float v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  const float w = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(w), __float_as_uint(w), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// Eight scaled values as halves, rounded to nearest even; and what is left of them.
+__device__ __forceinline__ half8_t halves(const float (&x)[8]) {
+  half8_t h;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const half2_t t = __builtin_convertvector((f32x2_t{x[2 * i], x[2 * i + 1]}), half2_t);
+    h[2 * i] = t[0];
+    h[2 * i + 1] = t[1];
+  }
+  return h;
+}
+__device__ __forceinline__ half8_t rest(const float (&x)[8], half8_t h) {
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = x[i] - static_cast<float>(h[i]);
+  return halves(r);
+}
+
+// Two D tiles times f as a B operand: its halves and, with LO, what is left.
+template <bool LO>
+__device__ __forceinline__ void tiles_to_operand(f32x4_t a, f32x4_t b, float f, half8_t& hi, half8_t& lo) {
+  const float x[8] = {a[0] * f, a[1] * f, a[2] * f, a[3] * f, b[0] * f, b[1] * f, b[2] * f, b[3] * f};
+  hi = halves(x);
+  if constexpr (LO) lo = rest(x, hi);
+}
+
+template <int T>
+__device__ __forceinline__ float tiles_absmax(const f32x4_t (&x)[T]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(x[j][i]));
+  }
+  return col_max(m);
+}
+
+// Four rows of a column out of a row-major array of halves in LDS: lane m of
+// a group of 16 passes the address of row m / 4, columns 4 (m % 4) .. + 3 of a
+// 4 x 16 piece, and gets column m.
+__device__ __forceinline__ half4_t lds_column4(const _Float16* at) {
+  typedef __attribute__((address_space(3))) short4_t* lds_ptr;
+  return __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at)));
+}
+
+// Eight elements n .. n+7 of row t (rows `step` elements apart from the
+// buffer's start), zero past the buffer's end and past `count`. VEC: rows and
+// the start on 16-byte boundaries, count a multiple of 8.
+template <bool BF16, bool VEC>
+struct Raw8 {
+  u32x4_t w[BF16 ? 1 : 2];
+};
+template <bool BF16, bool VEC>
+__device__ __forceinline__ Raw8<BF16, VEC> load_raw8(rsrc_t r, int t, int n, uint32_t step, int count) {
+  constexpr int EB = BF16 ? 2 : 4;
+  Raw8<BF16, VEC> o;
+  const uint32_t off = (static_cast<uint32_t>(t) * step + static_cast<uint32_t>(n)) * EB;
+  if constexpr (VEC) {
+    const uint32_t at = n < count ? off : kOutOfRange;
+    o.w[0] = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+    if constexpr (!BF16) o.w[1] = __builtin_amdgcn_raw_buffer_load_b128(r, n < count ? off + 16 : kOutOfRange, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t at = n + i < count ? off + static_cast<uint32_t>(i * EB) : kOutOfRange;
+      if constexpr (BF16) {
+        const uint32_t b = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0));
+        o.w[0][i / 2] = (i & 1) ? (o.w[0][i / 2] | (b << 16)) : b;
+      } else {
+        o.w[i / 4][i % 4] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+      }
+    }
+  }
+  return o;
+}
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void raw8_values(const Raw8<BF16, VEC>& o, float (&x)[8]) {
+  if constexpr (BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(o.w[0][i] << 16);
+      x[2 * i + 1] = __uint_as_float(o.w[0][i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o.w[i / 4][i % 4]);
+  }
+}
+
+// A buffer over `rows` rows of `width` elements, `step` apart.
+template <int EB>
+__device__ __forceinline__ rsrc_t rows_buffer(const void* base, int64_t at, int rows, uint32_t step, int width) {
+  const uint32_t bytes =
+      rows > 0 ? (static_cast<uint32_t>(rows - 1) * step + static_cast<uint32_t>(width)) * EB : 0u;
+  return raw_buffer(static_cast<const char*>(base) + at * EB, bytes);
+}
+
+// What the chunk kernels share of a chunk (an item: (batch row, head, chunk)).
+// Per-step factors, 64 floats each:
+enum GdrFactor {
+  kFacKup = 0,  // power of two that the raw k row is scaled with
+  kFacQup,      // the same for q
+  kFacK,        // e^(c_t) |1/k| / kup: row factor of K S
+  kFacQ,        // scale e^(c_t) |1/q| / qup: row factor of Q S
+  kFacW,        // beta_t e^(c_end - c_t) |1/k| / kup: row factor of E in the state's update
+  kFacT,        // 1 / row scale of T's halves
+  kFacP,        // 1 / row scale of Pm's halves
+  kFacEnd,      // [0]: e^(c_end)
+  kGdrFactors
+};
+constexpr int kGdrPieceHalves = kGdrFrags * 2 * kGdrFragHalves;  // T or Pm, hi and lo of every piece
+
+struct GdrWork {  // device pointers into the workspace
+  _Float16* T;    // [items][6][2][64 lanes][8]
+  _Float16* Pm;   // the same
+  float* fac;     // [items][kGdrFactors][64]
+};
+
+// Launchers (0 or a HIP error code). vec: every row of q and k starts on a
+// 16-byte boundary and N is a multiple of 8.
+int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, int out_lo, bool vec, void* stream);
+int launch_gdr_chunk_b(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool vec, void* stream);
+int launch_gdr_chunk_f(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool vec, void* stream);
+
+}  // namespace ssm

@@ -277,7 +277,19 @@ __attribute__((weak)) int launch_gated_delta_bwd(const GatedDeltaBwdArgs& a, voi
 __attribute__((weak)) int launch_rms_norm(const RmsNormArgs& a, void* stream);
 __attribute__((weak)) int launch_rms_norm_bwd(const RmsNormBwdArgs& a, void* stream);
 
-// Workspace layouts (pure functions of the sizes; 0 bytes: none needed).
+// How a gated delta rule of given sizes runs forward: as a plain recurrence
+// (one launch, no workspace) or in chunks of 64 steps, with the workspace
+// holding the chunks' triangular inverses and output weights (halves) and
+// per-step factors. A pure function of the sizes.
+struct GdrPlan {
+  bool recurrent;
+  int64_t chunks;  // per batch row
+  size_t off_t, off_p, off_fac, bytes;
+};
+// Up to this length the recurrence is taken.
+constexpr int64_t kGdrRecurrentSteps = 16;
+GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, int64_t headdim,
+                         int64_t dstate);
 size_t gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
                                    int64_t headdim, int64_t dstate, int in_bf16);
 size_t gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,

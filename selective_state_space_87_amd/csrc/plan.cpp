@@ -137,7 +137,24 @@ size_t scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t 
   return p.ok ? p.bytes : 0;
 }
 
-size_t gated_delta_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int) { return 0; }
+GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t, int64_t nheads, int64_t, int64_t) {
+  GdrPlan p{};
+  p.recurrent = seqlen <= kGdrRecurrentSteps || batch == 0 || nheads == 0;
+  if (p.recurrent) return p;
+  p.chunks = ceil_div(seqlen, 64);
+  const size_t items = static_cast<size_t>(batch * nheads * p.chunks);
+  constexpr size_t kPieces = 6 * 2 * 64 * 8 * 2;  // bytes of T's (or the weights') halves a chunk
+  p.off_t = 0;
+  p.off_p = items * kPieces;
+  p.off_fac = 2 * items * kPieces;
+  p.bytes = p.off_fac + items * (8 * 64 * 4);
+  return p;
+}
+
+size_t gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
+                                   int64_t headdim, int64_t dstate, int) {
+  return plan_gated_delta(batch, seqlen, nkheads, nheads, headdim, dstate).bytes;
+}
 
 size_t gated_delta_bwd_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int) { return 0; }
 

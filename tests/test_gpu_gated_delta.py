@@ -7,7 +7,12 @@ y or of the state is a sum of a few hundred such products (128 states, 64 steps
 of a chunk) that each carry what earlier sums were off by. Errors of random
 sign add as a root, (3 * 192)^(1/2) 2^-21 = 1.1e-5; four times that is allowed,
 on the scale of the tensor's largest element: 5e-5. A bfloat16 output adds half
-a step of its own value, 2^-8.
+a step of its own value, 2^-8, and the operands' rounding in the two products
+that only y sees (q^T S and the sum over the chunk), which are taken in one
+float16 half for it: an operand is off by at most 2^-12 of itself, a product of
+two by 2^-11, and a sum of products with random signs by at most 2^-11 of the
+root of the sum of their squares, which is the size of y itself: 2^-11 of the
+largest element, an eighth of the output's own half step.
 """
 
 import numpy as np
@@ -71,7 +76,8 @@ def close(name, got, ref, tol=TOL):
     g = got.double().cpu().numpy()
     if not ref.size:
         return
-    room = tol * max(np.abs(ref).max(), 1e-30) + (2.0 ** -8 * np.abs(ref) if got.dtype == torch.bfloat16 else 0.0)
+    top = max(np.abs(ref).max(), 1e-30)
+    room = tol * top + (2.0 ** -8 * np.abs(ref) + 2.0 ** -11 * top if got.dtype == torch.bfloat16 else 0.0)
     worst = float((np.abs(g - ref) / room).max())
     print(f"[parity] {name}: {worst:.3f} of the tolerance", flush=True)
     assert worst <= 1.0, f"{name}: {worst} of the tolerance"
