@@ -79,7 +79,8 @@ def gated_delta_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, softplus=False, sigm
                     h0=None, dh_final=None, seqlens=None):
     """Gradients of sum(dy y) + sum(dh_final h_final) by the reversed recurrence:
     a dict of dq, dk, dv, ddt, dA, dbeta, ddt_bias, dh0, and under "mag" the
-    sums of absolute values behind dA and ddt_bias."""
+    sums of absolute values behind dA and ddt_bias, and of the two terms that
+    the norms' gradients subtract behind dq and dk."""
     s = _Steps(q, k, v, dt, A, beta, dt_bias, softplus, sigmoid, l2norm, seqlens)
     dy = _f64(dy)
     S = np.zeros((s.B, s.H, s.P, s.N)) if h0 is None else _f64(h0).copy()
@@ -111,18 +112,20 @@ def gated_delta_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, softplus=False, sigm
     on = s.on[:, :, None]
     dg, db = dg * on, db * on
     out = {"dv": dv * on[..., None], "dh0": X}
+    mag = {}
     for name, d, raw, nr in (("dq", dq, s.qr, s.nq), ("dk", dk, s.kr, s.nk)):
         d = (d * on[..., None]).reshape(s.B, s.L, s.G, s.r, s.N).sum(3)
         if l2norm:
             unit = raw * nr
+            mag[name] = nr * (np.abs(d) + np.abs(unit * (unit * d).sum(-1, keepdims=True)))
             d = nr * (d - unit * (unit * d).sum(-1, keepdims=True))
         out[name] = d
     with np.errstate(invalid="ignore"):
         dg = np.where(s.dt * s.A < -200.0, 0.0, dg)            # the clamp's own gradient
         dx = dg * s.A * (_sigmoid(s.x) if softplus else 1.0)
-        along = np.where(on, dg * s.dt, 0.0)
+        along = np.where(on & (dg != 0.0), dg * s.dt, 0.0)     # a cut-off step: 0, whatever dt
     out["dA"] = along.sum((0, 1))
     out["ddt"], out["ddt_bias"] = dx, dx.sum((0, 1))
     out["dbeta"] = db * s.beta * (1.0 - s.beta) if sigmoid else db
-    out["mag"] = {"dA": np.abs(along).sum((0, 1)), "ddt_bias": np.abs(dx).sum((0, 1))}
+    out["mag"] = dict(mag, dA=np.abs(along).sum((0, 1)), ddt_bias=np.abs(dx).sum((0, 1)))
     return out

@@ -193,20 +193,56 @@ int launch_gated_delta_update(const GatedDeltaArgs& a, void* stream) {
   return launch_gated_delta_recurrent(a, stream);
 }
 
-int launch_gated_delta(const GatedDeltaArgs& a, void* stream) {
-  const GdrPlan pl = plan_gated_delta(a.batch, a.seqlen, a.nkheads, a.nheads, a.headdim, a.dstate);
-  if (pl.recurrent) return launch_gated_delta_recurrent(a, stream);
-  char* base = static_cast<char*>(a.workspace);
-  GdrWork ws;
+namespace {
+
+GdrWork gdr_work(void* workspace, const GdrPlan& pl) {
+  char* base = static_cast<char*>(workspace);
+  GdrWork ws{};
   ws.T = reinterpret_cast<_Float16*>(base + pl.off_t);
   ws.Pm = reinterpret_cast<_Float16*>(base + pl.off_p);
   ws.fac = reinterpret_cast<float*>(base + pl.off_fac);
+  ws.Tt = reinterpret_cast<_Float16*>(base + pl.off_tt);
+  ws.Pt = ws.Pm;
+  ws.S = reinterpret_cast<float*>(base + pl.off_s);
+  ws.X = reinterpret_cast<float*>(base + pl.off_x);
+  ws.E = reinterpret_cast<float*>(base + pl.off_e);
+  ws.top = reinterpret_cast<float*>(base + pl.off_top);
+  ws.part = reinterpret_cast<float*>(base + pl.off_part);
+  return ws;
+}
+
+bool rows_on_16(const GatedDeltaArgs& a) {
   const int64_t per16 = a.in_bf16 ? 8 : 4;  // elements in 16 bytes
-  const bool vec = a.dstate % 8 == 0 && a.q_step % per16 == 0 && a.k_step % per16 == 0 && on_boundary(a.q, 16) &&
-                   on_boundary(a.k, 16);
-  if (const int e = launch_gdr_prep(a, ws, pl.chunks, !a.out_bf16, vec, stream)) return e;
-  return a.in_bf16 ? launch_gdr_chunk_b(a, ws, pl.chunks, vec, stream)
-                   : launch_gdr_chunk_f(a, ws, pl.chunks, vec, stream);
+  return a.dstate % 8 == 0 && a.q_step % per16 == 0 && a.k_step % per16 == 0 && on_boundary(a.q, 16) &&
+         on_boundary(a.k, 16);
+}
+
+int launch_chunks(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, void* stream) {
+  const bool vec = rows_on_16(a);
+  if (const int e = launch_gdr_prep(a, ws, chunks, !a.out_bf16, backward, vec, stream)) return e;
+  return a.in_bf16 ? launch_gdr_chunk_b(a, ws, chunks, backward, vec, stream)
+                   : launch_gdr_chunk_f(a, ws, chunks, backward, vec, stream);
+}
+
+}  // namespace
+
+int launch_gated_delta(const GatedDeltaArgs& a, void* stream) {
+  const GdrPlan pl = plan_gated_delta(a.batch, a.seqlen, a.nkheads, a.nheads, a.headdim, a.dstate, false);
+  if (pl.recurrent) return launch_gated_delta_recurrent(a, stream);
+  return launch_chunks(a, gdr_work(a.workspace, pl), pl.chunks, false, stream);
+}
+
+int launch_gated_delta_bwd(const GatedDeltaBwdArgs& a, void* stream) {
+  const GatedDeltaArgs& f = a.f;
+  const GdrPlan pl = plan_gated_delta(f.batch, f.seqlen, f.nkheads, f.nheads, f.headdim, f.dstate, true);
+  const GdrWork ws = gdr_work(f.workspace, pl);
+  if (pl.chunks > 0 && f.batch > 0) {
+    if (const int e = launch_chunks(f, ws, pl.chunks, true, stream)) return e;
+  }
+  if (f.batch > 0) {
+    if (const int e = launch_gdr_reverse(a, ws, pl.chunks, rows_on_16(f), stream)) return e;
+  }
+  return launch_gdr_grads(a, ws, f.batch > 0 ? pl.chunks : 0, rows_on_16(f), stream);
 }
 
 }  // namespace ssm

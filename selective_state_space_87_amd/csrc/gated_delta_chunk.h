@@ -16,7 +16,9 @@
 
 namespace ssm {
 
-template <int NP, bool BF16, bool OB16, bool VEC, int NW>
+// KEEP: the backward's pass over the chunks, which leaves the entering states
+// and E in the workspace and no y (neither Q nor Pm is touched).
+template <int NP, bool BF16, bool OB16, bool VEC, int NW, bool KEEP>
 struct GdrWalk {
   static constexpr int NT = 64 * NW;
   static constexpr int RAW = BF16 ? 1 : 2;
@@ -24,9 +26,9 @@ struct GdrWalk {
   static constexpr int RS = NP + 8;                     // row stride of K and Q in LDS (halves)
   static constexpr int kMat = RAW * kGdrC * RS;         // halves of K (or Q)
   static constexpr int kT = kGdrFrags * 2 * kGdrFragHalves;
-  static constexpr int kP = kGdrFrags * OP * kGdrFragHalves;
+  static constexpr int kP = KEEP ? 0 : kGdrFrags * OP * kGdrFragHalves;
   static constexpr int kFac = 5 * kGdrC + 4;            // K, Q, W, T, P factors and the end's
-  static constexpr int kBufBytes = (2 * kMat + kT + kP) * 2 + kFac * 4;
+  static constexpr int kBufBytes = ((KEEP ? 1 : 2) * kMat + kT + kP) * 2 + kFac * 4;
   static constexpr int NBUF = 2 * kBufBytes <= 160 * 1024 ? 2 : 1;
   static constexpr int NKQ = kGdrC * NP / 8 / NT;       // 8-element pieces of K (and Q) a thread
   static constexpr int NTL = (kT / 8 + NT - 1) / NT;    // 16-byte pieces of T a thread
@@ -34,9 +36,9 @@ struct GdrWalk {
   static constexpr int NFL = (5 * kGdrC + NT - 1) / NT;
 };
 
-template <int NP, bool BF16, bool OB16, bool VEC, int NW>
+template <int NP, bool BF16, bool OB16, bool VEC, int NW, bool KEEP>
 __global__ __launch_bounds__(64 * NW) void gdr_chunk_kernel(const GatedDeltaArgs p, const GdrWork ws, int chunks) {
-  using W = GdrWalk<NP, BF16, OB16, VEC, NW>;
+  using W = GdrWalk<NP, BF16, OB16, VEC, NW, KEEP>;
   constexpr int NT = W::NT, RAW = W::RAW, OP = W::OP, RS = W::RS, NJ = NP / 16, NK = NP / 32;
   constexpr int EB = BF16 ? 2 : 4;
   __shared__ __align__(16) char lds[W::NBUF][W::kBufBytes];
@@ -72,7 +74,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_chunk_kernel(const GatedDeltaArgs
 
   Raw8<BF16, VEC> kr[W::NKQ], qr[W::NKQ];
   float ku[W::NKQ], qu[W::NKQ], fr[W::NFL], fend = 0.0f;
-  u32x4_t tr[W::NTL], pr[W::NPL];
+  u32x4_t tr[W::NTL], pr[W::NPL > 0 ? W::NPL : 1];
   storage_t<BF16> vr[16];
 
   auto fetch = [&](int c) __attribute__((always_inline)) {
@@ -89,9 +91,9 @@ __global__ __launch_bounds__(64 * NW) void gdr_chunk_kernel(const GatedDeltaArgs
     for (int i = 0; i < W::NKQ; ++i) {
       const int e = (i * NT + tid) * 8, t = e / NP, n = e % NP;
       kr[i] = load_raw8<BF16, VEC>(rk, t, n, ks, N);
-      qr[i] = load_raw8<BF16, VEC>(rq, t, n, qs, N);
+      if constexpr (!KEEP) qr[i] = load_raw8<BF16, VEC>(rq, t, n, qs, N);
       ku[i] = fac[kFacKup * kGdrC + t];
-      qu[i] = fac[kFacQup * kGdrC + t];
+      if constexpr (!KEEP) qu[i] = fac[kFacQup * kGdrC + t];
     }
     const u32x4_t* T = reinterpret_cast<const u32x4_t*>(ws.T + (item0 + c) * kGdrPieceHalves);
     const u32x4_t* Pm = reinterpret_cast<const u32x4_t*>(ws.Pm + (item0 + c) * kGdrPieceHalves);
@@ -125,7 +127,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_chunk_kernel(const GatedDeltaArgs
   auto stage = [&](int buf) __attribute__((always_inline)) {
     _Float16* sK = reinterpret_cast<_Float16*>(lds[buf]);
     _Float16* sQ = sK + W::kMat;
-    u32x4_t* sT = reinterpret_cast<u32x4_t*>(sQ + W::kMat);
+    u32x4_t* sT = reinterpret_cast<u32x4_t*>(KEEP ? sQ : sQ + W::kMat);
     u32x4_t* sP = sT + W::kT / 8;
     float* sF = reinterpret_cast<float*>(sP + W::kP / 8);
 #pragma unroll
@@ -138,6 +140,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_chunk_kernel(const GatedDeltaArgs
       half8_t hi = halves(x);
       *reinterpret_cast<half8_t*>(sK + t * RS + n) = hi;
       if constexpr (RAW == 2) *reinterpret_cast<half8_t*>(sK + kGdrC * RS + t * RS + n) = rest(x, hi);
+      if constexpr (KEEP) continue;
       raw8_values<BF16, VEC>(qr[i], x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] *= qu[i];
@@ -177,13 +180,33 @@ __global__ __launch_bounds__(64 * NW) void gdr_chunk_kernel(const GatedDeltaArgs
     const int buf = W::NBUF == 2 ? (c & 1) : 0;
     const _Float16* sK = reinterpret_cast<const _Float16*>(lds[buf]);
     const _Float16* sQ = sK + W::kMat;
-    const _Float16* sT = sQ + W::kMat;
+    const _Float16* sT = KEEP ? sQ : sQ + W::kMat;
     const _Float16* sP = sT + W::kT;
     const float* sF = reinterpret_cast<const float*>(sP + W::kP);
     float v[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = bits_to_f32<BF16>(vr[i]);
     if (c + 1 < n_chunks) fetch(c + 1);
+    if constexpr (KEEP) {
+      const int64_t item = item0 + c;
+      if (col_ok) {
+        float* dst = ws.S + (item * P + col) * N;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int n = 32 * (j / 2) + 8 * g + 4 * (j & 1);
+          if (N % 4 == 0) {
+            if (n < N) *reinterpret_cast<f32x4_t*>(dst + n) = S[j];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (n + i < N) dst[n + i] = S[j][i];
+            }
+          }
+        }
+      }
+      const float top = lanes16_max(tiles_absmax<NJ>(S));
+      if (lane == 0 && col < P) ws.top[(item * kGdrMaxima + kMaxS) * kGdrMaxSlices + col / 16] = top;
+    }
 
     // K S and Q S
     f32x4_t ks[4], qs[4];
@@ -200,6 +223,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_chunk_kernel(const GatedDeltaArgs
         if constexpr (RAW == 2) {
           ks[tt] = mfma16(*reinterpret_cast<const half8_t*>(sK + kGdrC * RS + at), Sh[q], ks[tt]);
         }
+        if constexpr (KEEP) continue;
         const half8_t aq = *reinterpret_cast<const half8_t*>(sQ + at);
         qs[tt] = mfma16(aq, Sh[q], qs[tt]);
         if constexpr (OP == 2) {
@@ -275,8 +299,21 @@ __global__ __launch_bounds__(64 * NW) void gdr_chunk_kernel(const GatedDeltaArgs
         for (int i = 0; i < 4; ++i) S[j][i] = fmaf(acc[i], sd.down, end * S[j][i]);
       }
     }
+    if constexpr (KEEP) {
+      const int64_t item = item0 + c;
+      float* dst = ws.E + item * kGdrC * P;
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (col_ok) dst[(16 * tt + 4 * g + i) * P + col] = E[tt][i];
+        }
+      }
+      const float top = lanes16_max(tiles_absmax<4>(E));
+      if (lane == 0 && col < P) ws.top[(item * kGdrMaxima + kMaxE) * kGdrMaxSlices + col / 16] = top;
+    }
     // Y = diag(scale e^c) Q S + Pm E (S: the state before)
-    {
+    if constexpr (!KEEP) {
       const Pow2 se = pow2_to_top(tiles_absmax<4>(E));
       half8_t Eh[2], El[2];
 #pragma unroll
@@ -319,6 +356,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_chunk_kernel(const GatedDeltaArgs
     __syncthreads();
   }
 
+  if constexpr (KEEP) return;
   // Steps behind the row's last: zeros from the first chunk that was not walked.
   for (int64_t t = static_cast<int64_t>(n_chunks) * kGdrC + g; t < L; t += 4) {
     if (col_ok) store_elem<OB16>(p.y, (row_b + t) * yrow + static_cast<int64_t>(h) * P + col, 0.0f);
@@ -335,27 +373,32 @@ __global__ __launch_bounds__(64 * NW) void gdr_chunk_kernel(const GatedDeltaArgs
   }
 }
 
-template <int NP, bool BF16, bool OB16, bool VEC>
+template <int NP, bool BF16, bool OB16, bool VEC, bool KEEP>
 void gdr_launch_chunk_nw(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, hipStream_t st) {
   const int64_t bh = a.batch * a.nheads;
   const int64_t slices = (a.headdim + 15) / 16;
   if (slices <= 2) {
-    gdr_chunk_kernel<NP, BF16, OB16, VEC, 2><<<static_cast<unsigned>(bh * ((slices + 1) / 2)), 128, 0, st>>>(a, ws, chunks);
+    gdr_chunk_kernel<NP, BF16, OB16, VEC, 2, KEEP>
+        <<<static_cast<unsigned>(bh * ((slices + 1) / 2)), 128, 0, st>>>(a, ws, chunks);
   } else {
-    gdr_chunk_kernel<NP, BF16, OB16, VEC, 4><<<static_cast<unsigned>(bh * ((slices + 3) / 4)), 256, 0, st>>>(a, ws, chunks);
+    gdr_chunk_kernel<NP, BF16, OB16, VEC, 4, KEEP>
+        <<<static_cast<unsigned>(bh * ((slices + 3) / 4)), 256, 0, st>>>(a, ws, chunks);
   }
 }
 
 template <bool BF16>
-int gdr_launch_chunk(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, bool vec, hipStream_t st) {
+int gdr_launch_chunk(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, bool backward, bool vec, hipStream_t st) {
   const auto types = [&](auto np) {
     constexpr int NP = decltype(np)::value;
-    if (a.out_bf16) {
-      vec ? gdr_launch_chunk_nw<NP, BF16, true, true>(a, ws, chunks, st)
-          : gdr_launch_chunk_nw<NP, BF16, true, false>(a, ws, chunks, st);
+    if (backward) {
+      vec ? gdr_launch_chunk_nw<NP, BF16, true, true, true>(a, ws, chunks, st)
+          : gdr_launch_chunk_nw<NP, BF16, true, false, true>(a, ws, chunks, st);
+    } else if (a.out_bf16) {
+      vec ? gdr_launch_chunk_nw<NP, BF16, true, true, false>(a, ws, chunks, st)
+          : gdr_launch_chunk_nw<NP, BF16, true, false, false>(a, ws, chunks, st);
     } else {
-      vec ? gdr_launch_chunk_nw<NP, BF16, false, true>(a, ws, chunks, st)
-          : gdr_launch_chunk_nw<NP, BF16, false, false>(a, ws, chunks, st);
+      vec ? gdr_launch_chunk_nw<NP, BF16, false, true, false>(a, ws, chunks, st)
+          : gdr_launch_chunk_nw<NP, BF16, false, false, false>(a, ws, chunks, st);
     }
   };
   if (a.dstate <= 64) {

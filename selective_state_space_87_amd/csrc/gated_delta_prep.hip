@@ -35,7 +35,8 @@ __device__ __forceinline__ f32x4_t tile_product(const float* A, f32x4_t X, f32x4
   return acc;
 }
 
-template <int NP, bool BF16, bool VEC>
+// BWD: also the pieces of T^T and, in place of Pm's, those of Pm^T.
+template <int NP, bool BF16, bool VEC, bool BWD>
 __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs p, const GdrWork ws, int chunks,
                                                             int out_lo) {
   constexpr int RAW = BF16 ? 1 : 2;
@@ -52,7 +53,7 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
   float* sP = sT + kGdrC * kMS;
 
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, m = lane & 15, g = lane >> 4;
-  const int H = static_cast<int>(p.nheads), G = static_cast<int>(p.nkheads), N = static_cast<int>(p.dstate);
+  const int H = static_cast<int>(p.nheads), G = static_cast<int>(p.nkheads);
   const int64_t item = blockIdx.x;
   const int c = static_cast<int>(item % chunks);
   const int bh = static_cast<int>(item / chunks);
@@ -71,65 +72,13 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
       ld = gdr_log_decay(p, load_elem<BF16>(p.dt, at), p.dt_bias ? p.dt_bias[h] : 0.0f, p.A[h]);
       beta = gdr_beta(p, load_elem<BF16>(p.beta, at));
     }
-    double cs = ld;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double o = __shfl_up(cs, d);
-      if (lane >= d) cs += o;
-    }
+    const double cs = wave_prefix(ld, lane);
     sC[lane] = cs;
     sBeta[lane] = beta;
   }
 
-  // (2) Rows of K and Q as halves: four lanes a row, 8 elements a piece.
-  {
-    const int t = tid >> 2, part = tid & 3;
-    const rsrc_t rk = rows_buffer<BF16 ? 2 : 4>(p.k, row0 * p.k_step + static_cast<int64_t>(kh) * N, rows,
-                                                static_cast<uint32_t>(p.k_step), N);
-    const rsrc_t rq = rows_buffer<BF16 ? 2 : 4>(p.q, row0 * p.q_step + static_cast<int64_t>(kh) * N, rows,
-                                                static_cast<uint32_t>(p.q_step), N);
-    Raw8<BF16, VEC> raw[2][NP / 32];
-#pragma unroll
-    for (int i = 0; i < NP / 32; ++i) {
-      raw[0][i] = load_raw8<BF16, VEC>(rk, t, 32 * i + 8 * part, static_cast<uint32_t>(p.k_step), N);
-      raw[1][i] = load_raw8<BF16, VEC>(rq, t, 32 * i + 8 * part, static_cast<uint32_t>(p.q_step), N);
-    }
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      float sum = 0.0f, top = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NP / 32; ++i) {
-        float x[8];
-        raw8_values<BF16, VEC>(raw[a][i], x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sum = fmaf(x[e], x[e], sum);
-          top = fmaxf(top, fabsf(x[e]));
-        }
-      }
-      sum += quad_xor<1>(sum);
-      sum += quad_xor<2>(sum);
-      top = fmaxf(top, quad_xor<1>(top));
-      top = fmaxf(top, quad_xor<2>(top));
-      const Pow2 s = pow2_to_top(top);
-      _Float16* dst = (a == 0 ? sK : sQ) + t * RS + 8 * part;
-#pragma unroll
-      for (int i = 0; i < NP / 32; ++i) {
-        float x[8];
-        raw8_values<BF16, VEC>(raw[a][i], x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= s.up;
-        const half8_t hi = halves(x);
-        *reinterpret_cast<half8_t*>(dst + 32 * i) = hi;
-        if constexpr (RAW == 2) *reinterpret_cast<half8_t*>(dst + kGdrC * RS + 32 * i) = rest(x, hi);
-      }
-      if (part == 0) {
-        const float n = p.qk_l2norm ? rsqrtf(sum + kL2NormEps) : 1.0f;
-        (a == 0 ? sKn : sQn)[t] = n * s.down;
-        (a == 0 ? sKup : sQup)[t] = s.up;
-      }
-    }
-  }
+  // (2) Rows of K and Q as halves.
+  gdr_stage_kq<NP, BF16, VEC>(p, row0, rows, kh, tid, sK, sQ, sKn, sQn, sKup, sQup);
   __syncthreads();
 
   // (3) The ten lower tiles of K K^T and Q K^T, q = w, w + 4, w + 8.
@@ -228,9 +177,8 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
   // (6) Rows 16 w .. + 15 of T and Pm as halves, in the order a lane feeds them.
   float* fac = ws.fac + item * (kGdrFactors * kGdrC);
   const int t = 16 * w + m;
-#pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    const float* src = (a == 0 ? sT : sP) + t * kMS;
+  // Row tile w of a matrix (or of its transpose) as halves, scaled by rows.
+  const auto pieces = [&](const float* src, bool up, _Float16* out, float* down, bool lo) __attribute__((always_inline)) {
     float x[2][8];
     float top = 0.0f;
 #pragma unroll
@@ -239,23 +187,30 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
       for (int e = 0; e < 8; ++e) {
         const int s = 32 * q + (e < 4 ? 4 * g + e : 12 + 4 * g + e);
         // (a block above the diagonal was never written)
-        x[q][e] = s <= t ? src[s <= t ? s : 0] : 0.0f;
+        const bool in = up ? s >= t : s <= t;
+        x[q][e] = in ? src[up ? s * kMS + t : t * kMS + s] : 0.0f;
         top = fmaxf(top, fabsf(x[q][e]));
       }
     }
     const Pow2 s = pow2_to_top(col_max(top));
-    if (g == 0) fac[(a == 0 ? kFacT : kFacP) * kGdrC + t] = s.down;
-    _Float16* out = (a == 0 ? ws.T : ws.Pm) + item * kGdrPieceHalves;
+    if (g == 0) down[t] = s.down;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      if (q == 1 && w < 2) continue;
+      if (up ? (q == 0 && w >= 2) : (q == 1 && w < 2)) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[q][e] *= s.up;
       const half8_t hi = halves(x[q]);
-      _Float16* at = out + gdr_frag(w, q) * 2 * kGdrFragHalves + lane * 8;
+      _Float16* at = out + (up ? gdr_frag_up(w, q) : gdr_frag(w, q)) * 2 * kGdrFragHalves + lane * 8;
       *reinterpret_cast<half8_t*>(at) = hi;
-      if (a == 0 || out_lo) *reinterpret_cast<half8_t*>(at + kGdrFragHalves) = rest(x[q], hi);
+      if (lo) *reinterpret_cast<half8_t*>(at + kGdrFragHalves) = rest(x[q], hi);
     }
+  };
+  pieces(sT, false, ws.T + item * kGdrPieceHalves, fac + kFacT * kGdrC, true);
+  if constexpr (BWD) {
+    pieces(sT, true, ws.Tt + item * kGdrPieceHalves, fac + kFacTt * kGdrC, true);
+    pieces(sP, true, ws.Pt + item * kGdrPieceHalves, fac + kFacP * kGdrC, true);
+  } else {
+    pieces(sP, false, ws.Pm + item * kGdrPieceHalves, fac + kFacP * kGdrC, out_lo);
   }
   if (w == 0) {
     const double ct = sC[lane];
@@ -270,28 +225,36 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
   }
 }
 
-template <int NP, bool BF16>
-void launch_np(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, unsigned blocks, int out_lo, bool vec,
+template <int NP, bool BF16, bool VEC>
+void launch_np(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, unsigned blocks, int out_lo, bool backward,
                hipStream_t st) {
-  if (vec) {
-    gdr_prep_kernel<NP, BF16, true><<<blocks, kThreads, 0, st>>>(a, ws, chunks, out_lo);
+  if (backward) {
+    gdr_prep_kernel<NP, BF16, VEC, true><<<blocks, kThreads, 0, st>>>(a, ws, chunks, out_lo);
   } else {
-    gdr_prep_kernel<NP, BF16, false><<<blocks, kThreads, 0, st>>>(a, ws, chunks, out_lo);
+    gdr_prep_kernel<NP, BF16, VEC, false><<<blocks, kThreads, 0, st>>>(a, ws, chunks, out_lo);
   }
+}
+
+template <int NP, bool BF16>
+void launch_vec(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, unsigned blocks, int out_lo, bool backward,
+                bool vec, hipStream_t st) {
+  vec ? launch_np<NP, BF16, true>(a, ws, chunks, blocks, out_lo, backward, st)
+      : launch_np<NP, BF16, false>(a, ws, chunks, blocks, out_lo, backward, st);
 }
 
 }  // namespace
 
-int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, int out_lo, bool vec, void* stream) {
+int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, int out_lo, bool backward, bool vec,
+                    void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   const unsigned blocks = static_cast<unsigned>(a.batch * a.nheads * chunks);
   const int n = static_cast<int>(chunks);
   if (a.dstate <= 64) {
-    a.in_bf16 ? launch_np<64, true>(a, ws, n, blocks, out_lo, vec, st)
-              : launch_np<64, false>(a, ws, n, blocks, out_lo, vec, st);
+    a.in_bf16 ? launch_vec<64, true>(a, ws, n, blocks, out_lo, backward, vec, st)
+              : launch_vec<64, false>(a, ws, n, blocks, out_lo, backward, vec, st);
   } else {
-    a.in_bf16 ? launch_np<128, true>(a, ws, n, blocks, out_lo, vec, st)
-              : launch_np<128, false>(a, ws, n, blocks, out_lo, vec, st);
+    a.in_bf16 ? launch_vec<128, true>(a, ws, n, blocks, out_lo, backward, vec, st)
+              : launch_vec<128, false>(a, ws, n, blocks, out_lo, backward, vec, st);
   }
   return static_cast<int>(hipGetLastError());
 }

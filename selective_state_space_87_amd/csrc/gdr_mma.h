@@ -183,22 +183,123 @@ enum GdrFactor {
   kFacQ,        // scale e^(c_t) |1/q| / qup: row factor of Q S
   kFacW,        // beta_t e^(c_end - c_t) |1/k| / kup: row factor of E in the state's update
   kFacT,        // 1 / row scale of T's halves
-  kFacP,        // 1 / row scale of Pm's halves
+  kFacP,        // 1 / row scale of Pm's halves (backward: Pm^T's)
   kFacEnd,      // [0]: e^(c_end)
+  kFacTt,       // 1 / row scale of T^T's halves (backward)
   kGdrFactors
 };
 constexpr int kGdrPieceHalves = kGdrFrags * 2 * kGdrFragHalves;  // T or Pm, hi and lo of every piece
 
+constexpr int kGdrMaxSlices = 16;  // 16-column slices of a head (P <= 256)
+// Largest magnitudes of an item's arrays, one a slice of 16 columns: the
+// scales of the backward's last kernel, which contracts over the columns.
+enum GdrMaximum { kMaxS = 0, kMaxE, kMaxX, kMaxDE, kMaxDY, kGdrMaxima };
+
 struct GdrWork {  // device pointers into the workspace
   _Float16* T;    // [items][6][2][64 lanes][8]
-  _Float16* Pm;   // the same
+  _Float16* Pm;   // the same (forward)
+  _Float16* Tt;   // pieces of T^T (backward), order gdr_frag_up
+  _Float16* Pt;   // pieces of Pm^T (backward)
   float* fac;     // [items][kGdrFactors][64]
+  float* S;       // [items][P][N] state entering the chunk (backward)
+  float* X;       // [items][P][N] gradient of the state leaving it
+  float* E;       // [items][64][P]
+  float* top;     // [items][kGdrMaxima][kGdrMaxSlices]
+  float* part;    // [2][items]: an item's part of dA and of ddt_bias
 };
+
+// Pieces of an upper triangle: (0,0) (0,1) (1,0) (1,1) (2,1) (3,1).
+__device__ __forceinline__ constexpr int gdr_frag_up(int tt, int p) { return tt < 2 ? 2 * tt + p : tt + 2; }
+
+// Largest |x| over a wave's D tiles, in every lane.
+__device__ __forceinline__ float lanes16_max(float v) {
+  v = fmaxf(v, quad_xor<1>(v));
+  v = fmaxf(v, quad_xor<2>(v));
+  v = fmaxf(v, dpp_f<0x141>(v));  // row_half_mirror
+  return fmaxf(v, dpp_f<0x140>(v));  // row_mirror
+}
+__device__ __forceinline__ float lanes16_sum(float v) {
+  v += quad_xor<1>(v);
+  v += quad_xor<2>(v);
+  v += dpp_f<0x141>(v);
+  return v + dpp_f<0x140>(v);
+}
+
+// The rows of K and Q of a chunk as halves in LDS ([RAW][64][RS] each; lo
+// halves behind the hi ones), by a block of 256 threads: four lanes a row, 8
+// elements a piece. kn, qn: a row's norm factor (1 without the norm) times the
+// inverse of its power of two; kup, qup: that power. Rows past `rows` are 0.
+template <int NP, bool BF16, bool VEC>
+__device__ __forceinline__ void gdr_stage_kq(const GatedDeltaArgs& p, int64_t row0, int rows, int kh, int tid,
+                                             _Float16* sK, _Float16* sQ, float* kn, float* qn, float* kup,
+                                             float* qup) {
+  constexpr int RS = NP + 8, RAW = BF16 ? 1 : 2;
+  const int N = static_cast<int>(p.dstate);
+  const int t = tid >> 2, part = tid & 3;
+  const rsrc_t rk = rows_buffer<BF16 ? 2 : 4>(p.k, row0 * p.k_step + static_cast<int64_t>(kh) * N, rows,
+                                              static_cast<uint32_t>(p.k_step), N);
+  const rsrc_t rq = rows_buffer<BF16 ? 2 : 4>(p.q, row0 * p.q_step + static_cast<int64_t>(kh) * N, rows,
+                                              static_cast<uint32_t>(p.q_step), N);
+  Raw8<BF16, VEC> raw[2][NP / 32];
+#pragma unroll
+  for (int i = 0; i < NP / 32; ++i) {
+    raw[0][i] = load_raw8<BF16, VEC>(rk, t, 32 * i + 8 * part, static_cast<uint32_t>(p.k_step), N);
+    raw[1][i] = load_raw8<BF16, VEC>(rq, t, 32 * i + 8 * part, static_cast<uint32_t>(p.q_step), N);
+  }
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    float sum = 0.0f, top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NP / 32; ++i) {
+      float x[8];
+      raw8_values<BF16, VEC>(raw[a][i], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum = fmaf(x[e], x[e], sum);
+        top = fmaxf(top, fabsf(x[e]));
+      }
+    }
+    sum += quad_xor<1>(sum);
+    sum += quad_xor<2>(sum);
+    top = fmaxf(top, quad_xor<1>(top));
+    top = fmaxf(top, quad_xor<2>(top));
+    const Pow2 s = pow2_to_top(top);
+    _Float16* dst = (a == 0 ? sK : sQ) + t * RS + 8 * part;
+#pragma unroll
+    for (int i = 0; i < NP / 32; ++i) {
+      float x[8];
+      raw8_values<BF16, VEC>(raw[a][i], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= s.up;
+      const half8_t hi = halves(x);
+      *reinterpret_cast<half8_t*>(dst + 32 * i) = hi;
+      if constexpr (RAW == 2) *reinterpret_cast<half8_t*>(dst + kGdrC * RS + 32 * i) = rest(x, hi);
+    }
+    if (part == 0) {
+      const float n = p.qk_l2norm ? rsqrtf(sum + kL2NormEps) : 1.0f;
+      (a == 0 ? kn : qn)[t] = n * s.down;
+      (a == 0 ? kup : qup)[t] = s.up;
+    }
+  }
+}
+
+// Inclusive prefix sum over the 64 lanes in double: a chunk's log decays.
+__device__ __forceinline__ double wave_prefix(double v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
 
 // Launchers (0 or a HIP error code). vec: every row of q and k starts on a
 // 16-byte boundary and N is a multiple of 8.
-int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, int out_lo, bool vec, void* stream);
-int launch_gdr_chunk_b(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool vec, void* stream);
-int launch_gdr_chunk_f(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool vec, void* stream);
+int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, int out_lo, bool backward, bool vec,
+                    void* stream);
+int launch_gdr_chunk_b(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, bool vec, void* stream);
+int launch_gdr_chunk_f(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, bool vec, void* stream);
+int launch_gdr_reverse(const GatedDeltaBwdArgs& a, const GdrWork& ws, int64_t chunks, bool vec, void* stream);
+int launch_gdr_grads(const GatedDeltaBwdArgs& a, const GdrWork& ws, int64_t chunks, bool vec, void* stream);
 
 }  // namespace ssm

@@ -284,12 +284,14 @@ __attribute__((weak)) int launch_rms_norm_bwd(const RmsNormBwdArgs& a, void* str
 struct GdrPlan {
   bool recurrent;
   int64_t chunks;  // per batch row
-  size_t off_t, off_p, off_fac, bytes;
+  size_t off_t, off_p, off_fac;
+  size_t off_tt, off_s, off_x, off_e, off_top, off_part;  // backward only
+  size_t bytes;
 };
 // Up to this length the recurrence is taken.
 constexpr int64_t kGdrRecurrentSteps = 16;
 GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, int64_t headdim,
-                         int64_t dstate);
+                         int64_t dstate, bool backward);
 size_t gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
                                    int64_t headdim, int64_t dstate, int in_bf16);
 size_t gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,

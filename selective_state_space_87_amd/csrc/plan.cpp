@@ -137,26 +137,45 @@ size_t scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t 
   return p.ok ? p.bytes : 0;
 }
 
-GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t, int64_t nheads, int64_t, int64_t) {
+GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t, int64_t nheads, int64_t headdim, int64_t dstate,
+                         bool backward) {
   GdrPlan p{};
-  p.recurrent = seqlen <= kGdrRecurrentSteps || batch == 0 || nheads == 0;
+  p.recurrent = !backward && (seqlen <= kGdrRecurrentSteps || batch == 0 || nheads == 0);
   if (p.recurrent) return p;
   p.chunks = ceil_div(seqlen, 64);
   const size_t items = static_cast<size_t>(batch * nheads * p.chunks);
   constexpr size_t kPieces = 6 * 2 * 64 * 8 * 2;  // bytes of T's (or the weights') halves a chunk
-  p.off_t = 0;
-  p.off_p = items * kPieces;
-  p.off_fac = 2 * items * kPieces;
-  p.bytes = p.off_fac + items * (8 * 64 * 4);
+  size_t at = 0;
+  const auto take = [&](size_t item_bytes) {
+    const size_t here = at;
+    at = align256(at + items * item_bytes);
+    return here;
+  };
+  p.off_t = take(kPieces);
+  p.off_p = take(kPieces);
+  p.off_fac = take(9 * 64 * 4);
+  if (backward) {
+    const size_t state = static_cast<size_t>(headdim * dstate) * 4;
+    p.off_tt = take(kPieces);
+    p.off_s = take(state);
+    p.off_x = take(state);
+    p.off_e = take(static_cast<size_t>(64 * headdim) * 4);
+    p.off_top = take(5 * 16 * 4);
+    p.off_part = take(2 * 4);
+  }
+  p.bytes = at;
   return p;
 }
 
 size_t gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
                                    int64_t headdim, int64_t dstate, int) {
-  return plan_gated_delta(batch, seqlen, nkheads, nheads, headdim, dstate).bytes;
+  return plan_gated_delta(batch, seqlen, nkheads, nheads, headdim, dstate, false).bytes;
 }
 
-size_t gated_delta_bwd_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int) { return 0; }
+size_t gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
+                                       int64_t headdim, int64_t dstate, int) {
+  return plan_gated_delta(batch, seqlen, nkheads, nheads, headdim, dstate, true).bytes;
+}
 
 int64_t rms_norm_bwd_blocks(int64_t rows, int64_t) { return rows < 512 ? rows : 512; }
 
