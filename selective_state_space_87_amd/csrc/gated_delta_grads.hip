@@ -139,12 +139,12 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     }
     Pow2 top[kGdrMaxima];
     {
-      const float* t = ws.top + item * kGdrMaxima * kGdrMaxSlices;
-      const int slices = (P + 15) / 16;
+      const float* t = ws.top + item * kGdrMaxima * kGdrMaxSlots;
+      const int slots = (P + 15) / 16 * 2;
 #pragma unroll
       for (int k = 0; k < kGdrMaxima; ++k) {
         float v = 0.0f;
-        for (int i = 0; i < slices; ++i) v = fmaxf(v, t[k * kGdrMaxSlices + i]);
+        for (int i = 0; i < slots; ++i) v = fmaxf(v, t[k * kGdrMaxSlots + i]);
         top[k] = pow2_to_top(v);
       }
     }

@@ -46,6 +46,7 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
   __shared__ __align__(16) char pool[kKQ > kTP ? kKQ : kTP];  // K and Q, then T and Pm
   __shared__ __align__(16) float sM[kGdrC * kMS];
   __shared__ double sC[kGdrC];
+  __shared__ float sTop[4];
   __shared__ float sBeta[kGdrC], sKn[kGdrC], sQn[kGdrC], sKup[kGdrC], sQup[kGdrC];
   _Float16* sK = reinterpret_cast<_Float16*>(pool);   // [RAW][64][RS]
   _Float16* sQ = sK + RAW * kGdrC * RS;
@@ -177,8 +178,11 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
   // (6) Rows 16 w .. + 15 of T and Pm as halves, in the order a lane feeds them.
   float* fac = ws.fac + item * (kGdrFactors * kGdrC);
   const int t = 16 * w + m;
-  // Row tile w of a matrix (or of its transpose) as halves, scaled by rows.
-  const auto pieces = [&](const float* src, bool up, _Float16* out, float* down, bool lo) __attribute__((always_inline)) {
+  // Row tile w of a matrix (or of its transpose) as halves, scaled by rows, or
+  // by one power of two for the whole triangle (T: its rows all have a 1, and
+  // halves reach down to 2^-38 of the largest element).
+  const auto pieces = [&](const float* src, bool up, _Float16* out, float* down, bool whole, bool lo)
+                          __attribute__((always_inline)) {
     float x[2][8];
     float top = 0.0f;
 #pragma unroll
@@ -192,8 +196,19 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
         top = fmaxf(top, fabsf(x[q][e]));
       }
     }
-    const Pow2 s = pow2_to_top(col_max(top));
-    if (g == 0) down[t] = s.down;
+    top = col_max(top);
+    if (whole) {
+      top = lanes16_max(top);
+      if (lane == 0) sTop[w] = top;
+      __syncthreads();
+      top = fmaxf(fmaxf(sTop[0], sTop[1]), fmaxf(sTop[2], sTop[3]));
+    }
+    const Pow2 s = pow2_to_top(top);
+    if (whole) {
+      if (tid == 0) *down = s.down;
+    } else if (g == 0) {
+      down[t] = s.down;
+    }
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (up ? (q == 0 && w >= 2) : (q == 1 && w < 2)) continue;
@@ -205,12 +220,12 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
       if (lo) *reinterpret_cast<half8_t*>(at + kGdrFragHalves) = rest(x[q], hi);
     }
   };
-  pieces(sT, false, ws.T + item * kGdrPieceHalves, fac + kFacT * kGdrC, true);
+  pieces(sT, false, ws.T + item * kGdrPieceHalves, fac + kFacEnd * kGdrC + 1, true, true);
   if constexpr (BWD) {
-    pieces(sT, true, ws.Tt + item * kGdrPieceHalves, fac + kFacTt * kGdrC, true);
-    pieces(sP, true, ws.Pt + item * kGdrPieceHalves, fac + kFacP * kGdrC, true);
+    pieces(sT, true, ws.Tt + item * kGdrPieceHalves, fac + kFacTt * kGdrC, false, true);
+    pieces(sP, true, ws.Pt + item * kGdrPieceHalves, fac + kFacP * kGdrC, false, true);
   } else {
-    pieces(sP, false, ws.Pm + item * kGdrPieceHalves, fac + kFacP * kGdrC, out_lo);
+    pieces(sP, false, ws.Pm + item * kGdrPieceHalves, fac + kFacP * kGdrC, false, out_lo);
   }
   if (w == 0) {
     const double ct = sC[lane];

@@ -94,7 +94,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_reverse_kernel(const GatedDeltaBw
 #pragma unroll
     for (int i = 0; i < W::NFL; ++i) {
       const int e = i * NT + tid;
-      if (e < 5 * kGdrC) fr[i] = fac[factor(e / kGdrC) * kGdrC + e % kGdrC];
+      fr[i] = fac[factor(e / kGdrC % 5) * kGdrC + e % kGdrC];
     }
     fend = fac[kFacEnd * kGdrC];
 #pragma unroll
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_reverse_kernel(const GatedDeltaBw
     f32x4_t Y[4];
 #pragma unroll
     for (int i = 0; i < 16; ++i) Y[i / 4][i % 4] = yr[i];
-    if (step + 1 < n_chunks) fetch(c - 1);
+    fetch(c > 0 ? c - 1 : 0);  // (in no branch: a conditional load is waited for where the branches join)
 
     const int64_t item = item0 + c;
     {
@@ -255,10 +255,10 @@ __global__ __launch_bounds__(64 * NW) void gdr_reverse_kernel(const GatedDeltaBw
     {
       const float mx = lanes16_max(xtop), my = lanes16_max(ytop), me = lanes16_max(etop);
       if (lane == 0 && col < P) {
-        float* top = ws.top + item * kGdrMaxima * kGdrMaxSlices + col / 16;
-        top[kMaxX * kGdrMaxSlices] = mx;
-        top[kMaxDY * kGdrMaxSlices] = my;
-        top[kMaxDE * kGdrMaxSlices] = me;
+        float* top = ws.top + item * kGdrMaxima * kGdrMaxSlots + col / 16 * 2;
+        top[kMaxX * kGdrMaxSlots] = top[kMaxX * kGdrMaxSlots + 1] = mx;
+        top[kMaxDY * kGdrMaxSlots] = top[kMaxDY * kGdrMaxSlots + 1] = my;
+        top[kMaxDE * kGdrMaxSlots] = top[kMaxDE * kGdrMaxSlots + 1] = me;
       }
     }
     // X' = e^(c_end) X + Q^T (qf dY) - K^T (kf dE)

@@ -182,16 +182,15 @@ enum GdrFactor {
   kFacK,        // e^(c_t) |1/k| / kup: row factor of K S
   kFacQ,        // scale e^(c_t) |1/q| / qup: row factor of Q S
   kFacW,        // beta_t e^(c_end - c_t) |1/k| / kup: row factor of E in the state's update
-  kFacT,        // 1 / row scale of T's halves
   kFacP,        // 1 / row scale of Pm's halves (backward: Pm^T's)
-  kFacEnd,      // [0]: e^(c_end)
+  kFacEnd,      // [0]: e^(c_end), [1]: 1 / scale of T's halves (one for the whole triangle)
   kFacTt,       // 1 / row scale of T^T's halves (backward)
   kGdrFactors
 };
 constexpr int kGdrPieceHalves = kGdrFrags * 2 * kGdrFragHalves;  // T or Pm, hi and lo of every piece
 
-constexpr int kGdrMaxSlices = 16;  // 16-column slices of a head (P <= 256)
-// Largest magnitudes of an item's arrays, one a slice of 16 columns: the
+constexpr int kGdrMaxSlots = 32;  // two waves a 16-column slice of a head (P <= 256)
+// Largest magnitudes of an item's arrays, one a wave that made a part: the
 // scales of the backward's last kernel, which contracts over the columns.
 enum GdrMaximum { kMaxS = 0, kMaxE, kMaxX, kMaxDE, kMaxDY, kGdrMaxima };
 
@@ -204,7 +203,7 @@ struct GdrWork {  // device pointers into the workspace
   float* S;       // [items][P][N] state entering the chunk (backward)
   float* X;       // [items][P][N] gradient of the state leaving it
   float* E;       // [items][64][P]
-  float* top;     // [items][kGdrMaxima][kGdrMaxSlices]
+  float* top;     // [items][kGdrMaxima][kGdrMaxSlots]
   float* part;    // [2][items]: an item's part of dA and of ddt_bias
 };
 
@@ -291,6 +290,14 @@ __device__ __forceinline__ double wave_prefix(double v, int lane) {
     if (lane >= d) v += o;
   }
   return v;
+}
+
+// Pairs of waves (16 columns each) a block of the walks over the chunks: as
+// many as leave a block for every one of the 256 CUs.
+inline int gdr_block_pairs(int64_t heads, int64_t slices) {
+  if (slices >= 4 && heads * ((slices + 3) / 4) >= 256) return 4;
+  if (slices >= 2 && heads * ((slices + 1) / 2) >= 256) return 2;
+  return 1;
 }
 
 // Launchers (0 or a HIP error code). vec: every row of q and k starts on a

@@ -153,14 +153,14 @@ GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t, int64_t nheads,
   };
   p.off_t = take(kPieces);
   p.off_p = take(kPieces);
-  p.off_fac = take(9 * 64 * 4);
+  p.off_fac = take(8 * 64 * 4);
   if (backward) {
     const size_t state = static_cast<size_t>(headdim * dstate) * 4;
     p.off_tt = take(kPieces);
     p.off_s = take(state);
     p.off_x = take(state);
     p.off_e = take(static_cast<size_t>(64 * headdim) * 4);
-    p.off_top = take(5 * 16 * 4);
+    p.off_top = take(5 * 32 * 4);
     p.off_part = take(2 * 4);
   }
   p.bytes = at;
