@@ -200,6 +200,8 @@ GdrWork gdr_work(void* workspace, const GdrPlan& pl) {
   GdrWork ws{};
   ws.T = reinterpret_cast<_Float16*>(base + pl.off_t);
   ws.Pm = reinterpret_cast<_Float16*>(base + pl.off_p);
+  ws.K = reinterpret_cast<_Float16*>(base + pl.off_k);
+  ws.Q = reinterpret_cast<_Float16*>(base + pl.off_q);
   ws.fac = reinterpret_cast<float*>(base + pl.off_fac);
   ws.Tt = reinterpret_cast<_Float16*>(base + pl.off_tt);
   ws.Pt = ws.Pm;
@@ -218,31 +220,30 @@ bool rows_on_16(const GatedDeltaArgs& a) {
 }
 
 int launch_chunks(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, void* stream) {
-  const bool vec = rows_on_16(a);
-  if (const int e = launch_gdr_prep(a, ws, chunks, !a.out_bf16, backward, vec, stream)) return e;
-  return a.in_bf16 ? launch_gdr_chunk_b(a, ws, chunks, backward, vec, stream)
-                   : launch_gdr_chunk_f(a, ws, chunks, backward, vec, stream);
+  if (const int e = launch_gdr_prep(a, ws, chunks, !a.out_bf16, backward, rows_on_16(a), stream)) return e;
+  return a.in_bf16 ? launch_gdr_chunk_b(a, ws, chunks, backward, stream)
+                   : launch_gdr_chunk_f(a, ws, chunks, backward, stream);
 }
 
 }  // namespace
 
 int launch_gated_delta(const GatedDeltaArgs& a, void* stream) {
-  const GdrPlan pl = plan_gated_delta(a.batch, a.seqlen, a.nkheads, a.nheads, a.headdim, a.dstate, false);
+  const GdrPlan pl = plan_gated_delta(a.batch, a.seqlen, a.nkheads, a.nheads, a.headdim, a.dstate, a.in_bf16, false);
   if (pl.recurrent) return launch_gated_delta_recurrent(a, stream);
   return launch_chunks(a, gdr_work(a.workspace, pl), pl.chunks, false, stream);
 }
 
 int launch_gated_delta_bwd(const GatedDeltaBwdArgs& a, void* stream) {
   const GatedDeltaArgs& f = a.f;
-  const GdrPlan pl = plan_gated_delta(f.batch, f.seqlen, f.nkheads, f.nheads, f.headdim, f.dstate, true);
+  const GdrPlan pl = plan_gated_delta(f.batch, f.seqlen, f.nkheads, f.nheads, f.headdim, f.dstate, f.in_bf16, true);
   const GdrWork ws = gdr_work(f.workspace, pl);
   if (pl.chunks > 0 && f.batch > 0) {
     if (const int e = launch_chunks(f, ws, pl.chunks, true, stream)) return e;
   }
   if (f.batch > 0) {
-    if (const int e = launch_gdr_reverse(a, ws, pl.chunks, rows_on_16(f), stream)) return e;
+    if (const int e = launch_gdr_reverse(a, ws, pl.chunks, stream)) return e;
   }
-  return launch_gdr_grads(a, ws, f.batch > 0 ? pl.chunks : 0, rows_on_16(f), stream);
+  return launch_gdr_grads(a, ws, f.batch > 0 ? pl.chunks : 0, stream);
 }
 
 }  // namespace ssm

@@ -14,8 +14,8 @@
 // (4, 8192, 32 heads of 128 x 128) took 13 000 clocks, of which the vector ALU
 // worked 4 100 and the matrix unit 1 660.
 //
-// A block of NPAIR pairs (16 NPAIR columns) shares K, Q (halves made while
-// staging) and the factors through LDS; the next chunk's are in flight in
+// A block of NPAIR pairs (16 NPAIR columns) shares the halves of K and Q and
+// the factors through LDS; the next chunk's are in flight in
 // registers meanwhile, and go into the other LDS buffer where two fit. T and
 // Pm are read by a wave straight into the registers it feeds them from.
 #pragma once
@@ -26,13 +26,12 @@ namespace ssm {
 
 // KEEP: the backward's pass over the chunks, which leaves the entering states
 // and E in the workspace and no y (neither Q nor Pm is touched).
-template <int NP, bool BF16, bool OB16, bool VEC, int NPAIR, bool KEEP>
+template <int NP, bool BF16, bool OB16, int NPAIR, bool KEEP>
 struct GdrWalk {
   static constexpr int NT = 128 * NPAIR;
   static constexpr int RAW = BF16 ? 1 : 2;
   static constexpr int OP = OB16 ? 1 : 2;               // halves in the products that only y sees
-  static constexpr int RS = NP + 8;                     // row stride of K and Q in LDS (halves)
-  static constexpr int kMat = RAW * kGdrC * RS;         // halves of K (or Q)
+  static constexpr int kMat = RAW * kGdrC * NP;         // halves of K (or Q)
   static constexpr int kFac = 4 * kGdrC + 4;            // K, Q, W, P factors and the end's
   static constexpr int kBufBytes = (KEEP ? 1 : 2) * kMat * 2 + kFac * 4;
   // a pair's exchange, in halves: S (NP / 32 pieces), R, w E (2), E; then scales (floats, a lane each)
@@ -40,15 +39,16 @@ struct GdrWalk {
   static constexpr int kXE = kXD + 4 * kGdrFragHalves, kXF = kXE + OP * kGdrFragHalves;
   static constexpr int kPairBytes = kXF * 2 + 6 * 64 * 4;
   static constexpr int NBUF = 2 * kBufBytes + NPAIR * kPairBytes <= 160 * 1024 ? 2 : 1;
-  static constexpr int NKQ = kGdrC * NP / 8 / NT;       // 8-element pieces of K (and Q) a thread
+  static constexpr int NKQ = kMat / 8 / NT;             // 16-byte pieces of K (and Q) a thread
   static constexpr int NFL = (4 * kGdrC + NT - 1) / NT;
 };
 
-template <int NP, bool BF16, bool OB16, bool VEC, int NPAIR, bool KEEP>
+template <int NP, bool BF16, bool OB16, int NPAIR, bool KEEP>
 __global__ __launch_bounds__(128 * NPAIR, NPAIR == 4 ? 2 : 1) void gdr_chunk_kernel(const GatedDeltaArgs p,
                                                                                     const GdrWork ws, int chunks) {
-  using W = GdrWalk<NP, BF16, OB16, VEC, NPAIR, KEEP>;
-  constexpr int NT = W::NT, RAW = W::RAW, OP = W::OP, RS = W::RS;
+  using W = GdrWalk<NP, BF16, OB16, NPAIR, KEEP>;
+  constexpr int NT = W::NT, RAW = W::RAW, OP = W::OP;
+  constexpr int kLo = kGdrC * NP;                       // from an element's hi half to its lo half
   constexpr int NJ = NP / 32, NK = NP / 64;             // state tiles and operand pieces of a wave
   constexpr int EB = BF16 ? 2 : 4;
   __shared__ __align__(16) char lds[W::NBUF][W::kBufBytes];
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(128 * NPAIR, NPAIR == 4 ? 2 : 1) void gdr_chunk_ker
   const int64_t len = gdr_row_steps(p.seqlens, b, L);
   const int n_chunks = static_cast<int>((len + kGdrC - 1) / kGdrC);
   const int64_t row_b = static_cast<int64_t>(b) * L;
-  const int64_t item0 = static_cast<int64_t>(bh) * chunks;
+  const int64_t item0 = static_cast<int64_t>(bh) * chunks, kv0 = (static_cast<int64_t>(b) * G + kh) * chunks;
   const int64_t sb = (static_cast<int64_t>(bh) * P + (col_ok ? col : 0)) * N;
   const uint32_t yrow = static_cast<uint32_t>(H * P);
 
@@ -94,8 +94,8 @@ __global__ __launch_bounds__(128 * NPAIR, NPAIR == 4 ? 2 : 1) void gdr_chunk_ker
     }
   }
 
-  Raw8<BF16, VEC> kr[W::NKQ], qr[W::NKQ];
-  float ku[W::NKQ], qu[W::NKQ], fr[W::NFL];
+  u32x4_t kr[W::NKQ], qr[W::NKQ];
+  float fr[W::NFL];
   float fend = 0.0f, ftri = 0.0f, fend_next = 0.0f, ftri_next = 0.0f;
   half8_t Td[2][2], To[2][2], Pd[2][OP], Po[2][OP];  // pieces on the diagonal, and left of it (wave 1)
   uint32_t vr[8];
@@ -105,21 +105,15 @@ __global__ __launch_bounds__(128 * NPAIR, NPAIR == 4 ? 2 : 1) void gdr_chunk_ker
     const int64_t t0 = static_cast<int64_t>(c) * kGdrC;
     const int rows = static_cast<int>(len - t0 < kGdrC ? len - t0 : kGdrC);
     const int64_t row0 = row_b + t0;
-    const uint32_t ks = static_cast<uint32_t>(p.k_step), qs = static_cast<uint32_t>(p.q_step);
     const uint32_t vs = static_cast<uint32_t>(p.v_step);
-    const rsrc_t rk = rows_buffer<EB>(p.k, row0 * p.k_step + static_cast<int64_t>(kh) * N, rows, ks, N);
-    const rsrc_t rq = rows_buffer<EB>(p.q, row0 * p.q_step + static_cast<int64_t>(kh) * N, rows, qs, N);
     const rsrc_t rv = rows_buffer<EB>(p.v, row0 * p.v_step + static_cast<int64_t>(h) * P, rows, vs, P);
     const float* fac = ws.fac + (item0 + c) * (kGdrFactors * kGdrC);
+    const u32x4_t* K = reinterpret_cast<const u32x4_t*>(ws.K + (kv0 + c) * W::kMat) + tid;
+    const u32x4_t* Q = reinterpret_cast<const u32x4_t*>(ws.Q + (kv0 + c) * W::kMat) + tid;
 #pragma unroll
     for (int i = 0; i < W::NKQ; ++i) {
-      const int e = (i * NT + tid) * 8, t = e / NP, n = e % NP;
-      kr[i] = load_raw8<BF16, VEC>(rk, t, n, ks, N);
-      ku[i] = fac[kFacKup * kGdrC + t];
-      if constexpr (!KEEP) {
-        qr[i] = load_raw8<BF16, VEC>(rq, t, n, qs, N);
-        qu[i] = fac[kFacQup * kGdrC + t];
-      }
+      kr[i] = K[i * NT];
+      if constexpr (!KEEP) qr[i] = Q[i * NT];
     }
 #pragma unroll
     for (int i = 0; i < W::NFL; ++i) {
@@ -167,21 +161,8 @@ __global__ __launch_bounds__(128 * NPAIR, NPAIR == 4 ? 2 : 1) void gdr_chunk_ker
     float* sF = reinterpret_cast<float*>(KEEP ? sQ : sQ + W::kMat);
 #pragma unroll
     for (int i = 0; i < W::NKQ; ++i) {
-      const int e = (i * NT + tid) * 8, t = e / NP, n = e % NP;
-      float x[8];
-      raw8_values<BF16, VEC>(kr[i], x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= ku[i];
-      half8_t hi = halves(x);
-      *reinterpret_cast<half8_t*>(sK + t * RS + n) = hi;
-      if constexpr (RAW == 2) *reinterpret_cast<half8_t*>(sK + kGdrC * RS + t * RS + n) = rest(x, hi);
-      if constexpr (KEEP) continue;
-      raw8_values<BF16, VEC>(qr[i], x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= qu[i];
-      hi = halves(x);
-      *reinterpret_cast<half8_t*>(sQ + t * RS + n) = hi;
-      if constexpr (RAW == 2) *reinterpret_cast<half8_t*>(sQ + kGdrC * RS + t * RS + n) = rest(x, hi);
+      reinterpret_cast<u32x4_t*>(sK)[i * NT + tid] = kr[i];
+      if constexpr (!KEEP) reinterpret_cast<u32x4_t*>(sQ)[i * NT + tid] = qr[i];
     }
 #pragma unroll
     for (int i = 0; i < W::NFL; ++i) {
@@ -269,12 +250,12 @@ __global__ __launch_bounds__(128 * NPAIR, NPAIR == 4 ? 2 : 1) void gdr_chunk_ker
         const half8_t sl = o == 0 ? Sl[q] : *piece(W::kXS, f, 1, 2);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int at = (32 * r + 16 * u + m) * RS + 32 * f + 8 * g;
+          const int at = kq_at<NP>(32 * r + 16 * u + m, 32 * f + 8 * g);
           const half8_t a = *reinterpret_cast<const half8_t*>(sK + at);
           ks[o][u] = mfma16(a, sh, ks[o][u]);
           ks[o][u] = mfma16(a, sl, ks[o][u]);
           if constexpr (RAW == 2) {
-            ks[o][u] = mfma16(*reinterpret_cast<const half8_t*>(sK + kGdrC * RS + at), sh, ks[o][u]);
+            ks[o][u] = mfma16(*reinterpret_cast<const half8_t*>(sK + kLo + at), sh, ks[o][u]);
           }
           if constexpr (KEEP) continue;
           const half8_t aq = *reinterpret_cast<const half8_t*>(sQ + at);
@@ -282,7 +263,7 @@ __global__ __launch_bounds__(128 * NPAIR, NPAIR == 4 ? 2 : 1) void gdr_chunk_ker
           if constexpr (OP == 2) {
             qs[o][u] = mfma16(aq, sl, qs[o][u]);
             if constexpr (RAW == 2) {
-              qs[o][u] = mfma16(*reinterpret_cast<const half8_t*>(sQ + kGdrC * RS + at), sh, qs[o][u]);
+              qs[o][u] = mfma16(*reinterpret_cast<const half8_t*>(sQ + kLo + at), sh, qs[o][u]);
             }
           }
         }
@@ -389,13 +370,13 @@ __global__ __launch_bounds__(128 * NPAIR, NPAIR == 4 ? 2 : 1) void gdr_chunk_ker
           acc[o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
           const half8_t dh = o == 0 ? Dh : oh, dl = o == 0 ? Dl : ol;
           // rows 32 q + 4 g + m / 4 (and + 16), columns of tile j in its order
-          const int at = (32 * (o == 0 ? r : 1 - r) + 4 * g + (m >> 2)) * RS + n0 + 32 * (j / 2) + 8 * (m & 3) + 4 * (j & 1);
-          const half4_t a0 = lds_column4(sK + at), a1 = lds_column4(sK + at + 16 * RS);
+          const int at = kq_at<NP>(32 * (o == 0 ? r : 1 - r) + 4 * g + (m >> 2), n0 + 32 * (j / 2) + 8 * (m & 3)) + 4 * (j & 1);
+          const half4_t a0 = lds_column4(sK + at), a1 = lds_column4(sK + at + 16 * NP);
           const half8_t a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
           acc[o] = mfma16(a, dh, acc[o]);
           acc[o] = mfma16(a, dl, acc[o]);
           if constexpr (RAW == 2) {
-            const half4_t b0 = lds_column4(sK + kGdrC * RS + at), b1 = lds_column4(sK + kGdrC * RS + at + 16 * RS);
+            const half4_t b0 = lds_column4(sK + kLo + at), b1 = lds_column4(sK + kLo + at + 16 * NP);
             acc[o] = mfma16(__builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7), dh, acc[o]);
           }
         }
@@ -473,34 +454,31 @@ __global__ __launch_bounds__(128 * NPAIR, NPAIR == 4 ? 2 : 1) void gdr_chunk_ker
   }
 }
 
-template <int NP, bool BF16, bool OB16, bool VEC, bool KEEP>
+template <int NP, bool BF16, bool OB16, bool KEEP>
 void gdr_launch_chunk_pairs(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, hipStream_t st) {
   const int64_t bh = a.batch * a.nheads;
   const int64_t slices = (a.headdim + 15) / 16;
   const int pairs = gdr_block_pairs(bh, slices);
   const auto blocks = [&](int n) { return static_cast<unsigned>(bh * ((slices + n - 1) / n)); };
   if (pairs == 1) {
-    gdr_chunk_kernel<NP, BF16, OB16, VEC, 1, KEEP><<<blocks(1), 128, 0, st>>>(a, ws, chunks);
+    gdr_chunk_kernel<NP, BF16, OB16, 1, KEEP><<<blocks(1), 128, 0, st>>>(a, ws, chunks);
   } else if (pairs == 2) {
-    gdr_chunk_kernel<NP, BF16, OB16, VEC, 2, KEEP><<<blocks(2), 256, 0, st>>>(a, ws, chunks);
+    gdr_chunk_kernel<NP, BF16, OB16, 2, KEEP><<<blocks(2), 256, 0, st>>>(a, ws, chunks);
   } else {
-    gdr_chunk_kernel<NP, BF16, OB16, VEC, 4, KEEP><<<blocks(4), 512, 0, st>>>(a, ws, chunks);
+    gdr_chunk_kernel<NP, BF16, OB16, 4, KEEP><<<blocks(4), 512, 0, st>>>(a, ws, chunks);
   }
 }
 
 template <bool BF16>
-int gdr_launch_chunk(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, bool backward, bool vec, hipStream_t st) {
+int gdr_launch_chunk(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, bool backward, hipStream_t st) {
   const auto types = [&](auto np) {
     constexpr int NP = decltype(np)::value;
     if (backward) {
-      vec ? gdr_launch_chunk_pairs<NP, BF16, true, true, true>(a, ws, chunks, st)
-          : gdr_launch_chunk_pairs<NP, BF16, true, false, true>(a, ws, chunks, st);
+      gdr_launch_chunk_pairs<NP, BF16, true, true>(a, ws, chunks, st);
     } else if (a.out_bf16) {
-      vec ? gdr_launch_chunk_pairs<NP, BF16, true, true, false>(a, ws, chunks, st)
-          : gdr_launch_chunk_pairs<NP, BF16, true, false, false>(a, ws, chunks, st);
+      gdr_launch_chunk_pairs<NP, BF16, true, false>(a, ws, chunks, st);
     } else {
-      vec ? gdr_launch_chunk_pairs<NP, BF16, false, true, false>(a, ws, chunks, st)
-          : gdr_launch_chunk_pairs<NP, BF16, false, false, false>(a, ws, chunks, st);
+      gdr_launch_chunk_pairs<NP, BF16, false, false>(a, ws, chunks, st);
     }
   };
   if (a.dstate <= 64) {

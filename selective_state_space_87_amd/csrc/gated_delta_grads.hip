@@ -56,17 +56,26 @@ __device__ __forceinline__ half8_t column8(const _Float16* mat, int stride, int 
   return __builtin_shufflevector(lds_column4(at), lds_column4(at + 4 * stride), 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// The same of K or Q (kq_at's order).
+template <int NP>
+__device__ __forceinline__ half8_t kq_column8(const _Float16* mat, int r0, int c0, int m, int g) {
+  const int t = r0 + 8 * g + (m >> 2), n = c0 + 4 * (m & 3);
+  return __builtin_shufflevector(lds_column4(mat + kq_at<NP>(t, n)), lds_column4(mat + kq_at<NP>(t + 4, n)), 0, 1, 2, 3, 4,
+                                 5, 6, 7);
+}
+
 __device__ __forceinline__ float wave_sum64(float v) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
   return v;
 }
 
-template <int NP, bool BF16, bool VEC>
+template <int NP, bool BF16>
 __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwdArgs a, const GdrWork ws, int chunks,
                                                              int yvec, int nvec) {
   constexpr int RAW = BF16 ? 1 : 2, RS = NP + 8, NJ = NP / 16;
-  constexpr int kMat = RAW * kGdrC * RS;
+  constexpr int kMat = RAW * kGdrC * NP;
+  constexpr int kLo = kGdrC * NP;
   constexpr int kSX = 32 * RS;                            // halves of a staged 32 x NP piece
   constexpr int kTP = kGdrC * kPS;                        // halves of a staged 64 x 32 piece
   constexpr int kStage = (4 * kSX + 6 * kTP) * 2;         // S, X and dY, E, dE, hi and lo
@@ -108,7 +117,21 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
 #pragma unroll
   for (int j = 0; j < NJ; ++j) dq[j] = dk[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  if (rows > 0) gdr_stage_kq<NP, BF16, VEC>(p, row0, rows, kh, tid, sK, sQ, sKn, sQn, sKup, sQup);
+  if (rows > 0) {
+    const u32x4_t* K = reinterpret_cast<const u32x4_t*>(ws.K + static_cast<int64_t>(blockIdx.x) * kMat);
+    const u32x4_t* Q = reinterpret_cast<const u32x4_t*>(ws.Q + static_cast<int64_t>(blockIdx.x) * kMat);
+    for (int i = tid; i < kMat / 8; i += kThreads) {
+      reinterpret_cast<u32x4_t*>(sK)[i] = K[i];
+      reinterpret_cast<u32x4_t*>(sQ)[i] = Q[i];
+    }
+    const float* fac = ws.fac + ((static_cast<int64_t>(b) * H + kh * r) * chunks + c) * (kGdrFactors * kGdrC);
+    if (tid < kGdrC) {
+      sKn[tid] = fac[kFacKn * kGdrC + tid];
+      sQn[tid] = fac[kFacQn * kGdrC + tid];
+      sKup[tid] = fac[kFacKup * kGdrC + tid];
+      sQup[tid] = fac[kFacQup * kGdrC + tid];
+    }
+  }
 
   for (int hh = 0; hh < r; ++hh) {
     const int h = kh * r + hh;
@@ -236,18 +259,18 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
         f32x4_t kk = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, qk = kk;
 #pragma unroll
         for (int n = 0; n < NP; n += 32) {
-          const int at = (16 * w + m) * RS + n + 8 * g, bt = (16 * si + m) * RS + n + 8 * g;
+          const int at = kq_at<NP>(16 * w + m, n + 8 * g), bt = kq_at<NP>(16 * si + m, n + 8 * g);
           const half8_t bk = *reinterpret_cast<const half8_t*>(sK + bt);
           const half8_t ak = *reinterpret_cast<const half8_t*>(sK + at);
           const half8_t aq = *reinterpret_cast<const half8_t*>(sQ + at);
           kk = mfma16(ak, bk, kk);
           qk = mfma16(aq, bk, qk);
           if constexpr (RAW == 2) {
-            const half8_t bl = *reinterpret_cast<const half8_t*>(sK + kGdrC * RS + bt);
+            const half8_t bl = *reinterpret_cast<const half8_t*>(sK + kLo + bt);
             kk = mfma16(ak, bl, kk);
             qk = mfma16(aq, bl, qk);
-            kk = mfma16(*reinterpret_cast<const half8_t*>(sK + kGdrC * RS + at), bk, kk);
-            qk = mfma16(*reinterpret_cast<const half8_t*>(sQ + kGdrC * RS + at), bk, qk);
+            kk = mfma16(*reinterpret_cast<const half8_t*>(sK + kLo + at), bk, kk);
+            qk = mfma16(*reinterpret_cast<const half8_t*>(sQ + kLo + at), bk, qk);
           }
         }
         const float bs = sBeta[s], kns = sKn[s];
@@ -281,11 +304,11 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
       for (int j = 0; j < NJ; ++j) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int at = (16 * w + 4 * g + i) * RS + 16 * j + m;
+          const int at = kq_at<NP>(16 * w + 4 * g + i, 16 * j + m);
           float kv = static_cast<float>(sK[at]), qv = static_cast<float>(sQ[at]);
           if constexpr (RAW == 2) {
-            kv += static_cast<float>(sK[kGdrC * RS + at]);
-            qv += static_cast<float>(sQ[kGdrC * RS + at]);
+            kv += static_cast<float>(sK[kLo + at]);
+            qv += static_cast<float>(sQ[kLo + at]);
           }
           const float v1 = n1[j][i] * f1, v2 = n2[j][i] * f2, v3 = n3[j][i] * f3;
           r1[i] = fmaf(qv, v1, r1[i]);
@@ -341,10 +364,10 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           if (up ? (q == 0 && w >= 2) : (q == 1 && w < 2)) continue;
-          const half8_t bv = column8(mat, RS, 32 * q, 16 * j, m, g);
+          const half8_t bv = kq_column8<NP>(mat, 32 * q, 16 * j, m, g);
           acc = mfma16(hi[q], bv, acc);
           acc = mfma16(lo[q], bv, acc);
-          if constexpr (RAW == 2) acc = mfma16(hi[q], column8(mat + kGdrC * RS, RS, 32 * q, 16 * j, m, g), acc);
+          if constexpr (RAW == 2) acc = mfma16(hi[q], kq_column8<NP>(mat + kLo, 32 * q, 16 * j, m, g), acc);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) out[j][i] = fmaf(acc[i], sc.down, out[j][i]);
@@ -404,14 +427,14 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     const bool on = t < rows;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int at = t * RS + 16 * j + m;
+      const int at = kq_at<NP>(t, 16 * j + m);
       qv[j] = kv[j] = 0.0f;
       if (rows > 0 && p.qk_l2norm) {
         qv[j] = static_cast<float>(sQ[at]);
         kv[j] = static_cast<float>(sK[at]);
         if constexpr (RAW == 2) {
-          qv[j] += static_cast<float>(sQ[kGdrC * RS + at]);
-          kv[j] += static_cast<float>(sK[kGdrC * RS + at]);
+          qv[j] += static_cast<float>(sQ[kLo + at]);
+          kv[j] += static_cast<float>(sK[kLo + at]);
         }
         qv[j] *= sQn[t];
         kv[j] *= sKn[t];
@@ -470,7 +493,7 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
 
-int launch_gdr_grads(const GatedDeltaBwdArgs& a, const GdrWork& ws, int64_t chunks, bool vec, void* stream) {
+int launch_gdr_grads(const GatedDeltaBwdArgs& a, const GdrWork& ws, int64_t chunks, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int n = static_cast<int>(chunks);
   if (n > 0) {
@@ -479,8 +502,7 @@ int launch_gdr_grads(const GatedDeltaBwdArgs& a, const GdrWork& ws, int64_t chun
     const auto types = [&](auto np, auto bf16) {
       constexpr int NP = decltype(np)::value;
       constexpr bool BF16 = decltype(bf16)::value;
-      vec ? gdr_grads_kernel<NP, BF16, true><<<blocks, kThreads, 0, st>>>(a, ws, n, yvec, nvec)
-          : gdr_grads_kernel<NP, BF16, false><<<blocks, kThreads, 0, st>>>(a, ws, n, yvec, nvec);
+      gdr_grads_kernel<NP, BF16><<<blocks, kThreads, 0, st>>>(a, ws, n, yvec, nvec);
     };
     const auto width = [&](auto np) { a.f.in_bf16 ? types(np, std::true_type{}) : types(np, std::false_type{}); };
     if (a.f.dstate <= 64) {

@@ -47,6 +47,7 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef short short4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
+constexpr double kLog2eD = 1.4426950408889634;
 constexpr int kGdrC = 64;       // steps a chunk
 constexpr int kGdrFrags = 6;    // 16 x 32 pieces of a lower triangle of 64: (0,0) (1,0) (2,0) (2,1) (3,0) (3,1)
 constexpr int kGdrFragHalves = 64 * 8;
@@ -177,14 +178,15 @@ __device__ __forceinline__ rsrc_t rows_buffer(const void* base, int64_t at, int 
 // What the chunk kernels share of a chunk (an item: (batch row, head, chunk)).
 // Per-step factors, 64 floats each:
 enum GdrFactor {
-  kFacKup = 0,  // power of two that the raw k row is scaled with
+  kFacKup = 0,  // power of two that the raw k row is scaled with (backward)
   kFacQup,      // the same for q
   kFacK,        // e^(c_t) |1/k| / kup: row factor of K S
   kFacQ,        // scale e^(c_t) |1/q| / qup: row factor of Q S
   kFacW,        // beta_t e^(c_end - c_t) |1/k| / kup: row factor of E in the state's update
   kFacP,        // 1 / row scale of Pm's halves (backward: Pm^T's)
   kFacEnd,      // [0]: e^(c_end), [1]: 1 / scale of T's halves (one for the whole triangle)
-  kFacTt,       // 1 / row scale of T^T's halves (backward)
+  kFacKn,       // |1/k| / kup (backward)
+  kFacQn,       // |1/q| / qup (backward)
   kGdrFactors
 };
 constexpr int kGdrPieceHalves = kGdrFrags * 2 * kGdrFragHalves;  // T or Pm, hi and lo of every piece
@@ -199,6 +201,8 @@ struct GdrWork {  // device pointers into the workspace
   _Float16* Pm;   // the same (forward)
   _Float16* Tt;   // pieces of T^T (backward), order gdr_frag_up
   _Float16* Pt;   // pieces of Pm^T (backward)
+  _Float16* K;    // [batch, query/key heads, chunks][1 or 2 halves][64][64 or 128], order kq_at
+  _Float16* Q;    // the same
   float* fac;     // [items][kGdrFactors][64]
   float* S;       // [items][P][N] state entering the chunk (backward)
   float* X;       // [items][P][N] gradient of the state leaving it
@@ -224,15 +228,27 @@ __device__ __forceinline__ float lanes16_sum(float v) {
   return v + dpp_f<0x140>(v);
 }
 
-// The rows of K and Q of a chunk as halves in LDS ([RAW][64][RS] each; lo
-// halves behind the hi ones), by a block of 256 threads: four lanes a row, 8
-// elements a piece. kn, qn: a row's norm factor (1 without the norm) times the
-// inverse of its power of two; kup, qup: that power. Rows past `rows` are 0.
+// Where element n (a multiple of 8, or of 4 for half a slot) of row t of K or
+// Q stands among its halves, in LDS and in the workspace alike: rows of NP
+// halves without padding, their 16-byte slots exchanged by an exclusive or
+// with a number of the row. Both reads of a wave are then free of bank
+// conflicts: 16 rows of one slot (an A operand), and four rows of four slots (lds_column4).
+template <int NP>
+__device__ __forceinline__ int kq_at(int t, int n) {
+  const int f = NP == 128 ? ((t & 3) << 2) | ((t >> 2) & 3) : ((t >> 1) & 1) << 2 | ((t >> 2) & 3);
+  return t * NP + (((n >> 3) ^ f) << 3) + (n & 7);
+}
+
+// The rows of K and Q of a chunk as halves, by a block of 256 threads: four
+// lanes a row, 8 elements a piece; into LDS and into the workspace ([RAW][64]
+// [NP] each, lo halves behind the hi ones). kn, qn: a row's norm factor (1
+// without the norm) times the inverse of its power of two; kup, qup: that
+// power. Rows past `rows` are 0.
 template <int NP, bool BF16, bool VEC>
 __device__ __forceinline__ void gdr_stage_kq(const GatedDeltaArgs& p, int64_t row0, int rows, int kh, int tid,
-                                             _Float16* sK, _Float16* sQ, float* kn, float* qn, float* kup,
-                                             float* qup) {
-  constexpr int RS = NP + 8, RAW = BF16 ? 1 : 2;
+                                             _Float16* sK, _Float16* sQ, _Float16* gK, _Float16* gQ, float* kn,
+                                             float* qn, float* kup, float* qup) {
+  constexpr int RAW = BF16 ? 1 : 2;
   const int N = static_cast<int>(p.dstate);
   const int t = tid >> 2, part = tid & 3;
   const rsrc_t rk = rows_buffer<BF16 ? 2 : 4>(p.k, row0 * p.k_step + static_cast<int64_t>(kh) * N, rows,
@@ -248,14 +264,14 @@ __device__ __forceinline__ void gdr_stage_kq(const GatedDeltaArgs& p, int64_t ro
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
     float sum = 0.0f, top = 0.0f;
+    float x[NP / 32][8];
 #pragma unroll
     for (int i = 0; i < NP / 32; ++i) {
-      float x[8];
-      raw8_values<BF16, VEC>(raw[a][i], x);
+      raw8_values<BF16, VEC>(raw[a][i], x[i]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        sum = fmaf(x[e], x[e], sum);
-        top = fmaxf(top, fabsf(x[e]));
+        sum = fmaf(x[i][e], x[i][e], sum);
+        top = fmaxf(top, fabsf(x[i][e]));
       }
     }
     sum += quad_xor<1>(sum);
@@ -263,16 +279,20 @@ __device__ __forceinline__ void gdr_stage_kq(const GatedDeltaArgs& p, int64_t ro
     top = fmaxf(top, quad_xor<1>(top));
     top = fmaxf(top, quad_xor<2>(top));
     const Pow2 s = pow2_to_top(top);
-    _Float16* dst = (a == 0 ? sK : sQ) + t * RS + 8 * part;
+    _Float16 *dst = a == 0 ? sK : sQ, *out = a == 0 ? gK : gQ;
 #pragma unroll
     for (int i = 0; i < NP / 32; ++i) {
-      float x[8];
-      raw8_values<BF16, VEC>(raw[a][i], x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= s.up;
-      const half8_t hi = halves(x);
-      *reinterpret_cast<half8_t*>(dst + 32 * i) = hi;
-      if constexpr (RAW == 2) *reinterpret_cast<half8_t*>(dst + kGdrC * RS + 32 * i) = rest(x, hi);
+      for (int e = 0; e < 8; ++e) x[i][e] *= s.up;
+      const int at = kq_at<NP>(t, 32 * i + 8 * part);
+      const half8_t hi = halves(x[i]);
+      *reinterpret_cast<half8_t*>(dst + at) = hi;
+      *reinterpret_cast<half8_t*>(out + at) = hi;
+      if constexpr (RAW == 2) {
+        const half8_t lo = rest(x[i], hi);
+        *reinterpret_cast<half8_t*>(dst + kGdrC * NP + at) = lo;
+        *reinterpret_cast<half8_t*>(out + kGdrC * NP + at) = lo;
+      }
     }
     if (part == 0) {
       const float n = p.qk_l2norm ? rsqrtf(sum + kL2NormEps) : 1.0f;
@@ -304,9 +324,9 @@ inline int gdr_block_pairs(int64_t heads, int64_t slices) {
 // 16-byte boundary and N is a multiple of 8.
 int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, int out_lo, bool backward, bool vec,
                     void* stream);
-int launch_gdr_chunk_b(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, bool vec, void* stream);
-int launch_gdr_chunk_f(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, bool vec, void* stream);
-int launch_gdr_reverse(const GatedDeltaBwdArgs& a, const GdrWork& ws, int64_t chunks, bool vec, void* stream);
-int launch_gdr_grads(const GatedDeltaBwdArgs& a, const GdrWork& ws, int64_t chunks, bool vec, void* stream);
+int launch_gdr_chunk_b(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, void* stream);
+int launch_gdr_chunk_f(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, void* stream);
+int launch_gdr_reverse(const GatedDeltaBwdArgs& a, const GdrWork& ws, int64_t chunks, void* stream);
+int launch_gdr_grads(const GatedDeltaBwdArgs& a, const GdrWork& ws, int64_t chunks, void* stream);
 
 }  // namespace ssm

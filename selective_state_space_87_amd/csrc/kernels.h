@@ -279,19 +279,19 @@ __attribute__((weak)) int launch_rms_norm_bwd(const RmsNormBwdArgs& a, void* str
 
 // How a gated delta rule of given sizes runs forward: as a plain recurrence
 // (one launch, no workspace) or in chunks of 64 steps, with the workspace
-// holding the chunks' triangular inverses and output weights (halves) and
-// per-step factors. A pure function of the sizes.
+// holding the chunks' triangular inverses, output weights, keys and queries
+// (halves) and per-step factors. A pure function of the sizes.
 struct GdrPlan {
   bool recurrent;
   int64_t chunks;  // per batch row
-  size_t off_t, off_p, off_fac;
+  size_t off_t, off_p, off_k, off_q, off_fac;
   size_t off_tt, off_s, off_x, off_e, off_top, off_part;  // backward only
   size_t bytes;
 };
 // Up to this length the recurrence is taken.
 constexpr int64_t kGdrRecurrentSteps = 16;
 GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, int64_t headdim,
-                         int64_t dstate, bool backward);
+                         int64_t dstate, int in_bf16, bool backward);
 size_t gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
                                    int64_t headdim, int64_t dstate, int in_bf16);
 size_t gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,

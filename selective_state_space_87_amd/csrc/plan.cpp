@@ -137,8 +137,8 @@ size_t scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t 
   return p.ok ? p.bytes : 0;
 }
 
-GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t, int64_t nheads, int64_t headdim, int64_t dstate,
-                         bool backward) {
+GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, int64_t headdim,
+                         int64_t dstate, int in_bf16, bool backward) {
   GdrPlan p{};
   p.recurrent = !backward && (seqlen <= kGdrRecurrentSteps || batch == 0 || nheads == 0);
   if (p.recurrent) return p;
@@ -146,14 +146,19 @@ GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t, int64_t nheads,
   const size_t items = static_cast<size_t>(batch * nheads * p.chunks);
   constexpr size_t kPieces = 6 * 2 * 64 * 8 * 2;  // bytes of T's (or the weights') halves a chunk
   size_t at = 0;
-  const auto take = [&](size_t item_bytes) {
+  const auto take_n = [&](size_t n, size_t bytes) {
     const size_t here = at;
-    at = align256(at + items * item_bytes);
+    at = align256(at + n * bytes);
     return here;
   };
+  const auto take = [&](size_t item_bytes) { return take_n(items, item_bytes); };
   p.off_t = take(kPieces);
   p.off_p = take(kPieces);
-  p.off_fac = take(8 * 64 * 4);
+  const size_t kv_items = static_cast<size_t>(batch * nkheads * p.chunks);
+  const size_t kv = (in_bf16 ? 1 : 2) * 64 * (dstate <= 64 ? 64 : 128) * 2;
+  p.off_k = take_n(kv_items, kv);
+  p.off_q = take_n(kv_items, kv);
+  p.off_fac = take(9 * 64 * 4);
   if (backward) {
     const size_t state = static_cast<size_t>(headdim * dstate) * 4;
     p.off_tt = take(kPieces);
@@ -168,13 +173,13 @@ GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t, int64_t nheads,
 }
 
 size_t gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
-                                   int64_t headdim, int64_t dstate, int) {
-  return plan_gated_delta(batch, seqlen, nkheads, nheads, headdim, dstate, false).bytes;
+                                   int64_t headdim, int64_t dstate, int in_bf16) {
+  return plan_gated_delta(batch, seqlen, nkheads, nheads, headdim, dstate, in_bf16, false).bytes;
 }
 
 size_t gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
-                                       int64_t headdim, int64_t dstate, int) {
-  return plan_gated_delta(batch, seqlen, nkheads, nheads, headdim, dstate, true).bytes;
+                                       int64_t headdim, int64_t dstate, int in_bf16) {
+  return plan_gated_delta(batch, seqlen, nkheads, nheads, headdim, dstate, in_bf16, true).bytes;
 }
 
 int64_t rms_norm_bwd_blocks(int64_t rows, int64_t) { return rows < 512 ? rows : 512; }
