@@ -46,6 +46,8 @@ struct GdrWalk {
   // Four pairs (twelve waves) have 168 registers a wave: enough with one half in
   // K, Q and in what only y sees. Elsewhere two pairs.
   static constexpr bool kFits = NBUF * kBufBytes + kFixed <= 160 * 1024 && (KEEP || (RAW == 1 && OP == 1));
+  // With two buffers, half the pairs run one phase behind the others.
+  static constexpr bool kLag = NBUF == 2 && NPAIR >= 2;
   static constexpr int NKQ = kMat / 8 / NL;             // 16-byte pieces of K (and Q) a loading thread
   static constexpr int NTL = kT / 8 / NL;
   static constexpr int NPL = (kP / 8 + NL - 1) / NL;
@@ -81,9 +83,14 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
   const int64_t item0 = static_cast<int64_t>(bh) * chunks, kv0 = (static_cast<int64_t>(b) * G + kh) * chunks;
   const uint32_t yrow = static_cast<uint32_t>(H * P);
 
-  // Barriers a chunk: R is there; w E and E are there; S' and the next chunk's
-  // K, Q, T are there (with one buffer for K and Q: S' is there and K is done
-  // with; the next chunk's are there).
+  // A phase ends with a barrier, three a chunk: R is there; w E and E are
+  // there; S' is there. Pairs that lag take part in one barrier before their
+  // first phase, the others in one behind their last. Into LDS go, counted in
+  // phases of the pairs that do not lag: T of chunk c in phase 3 c (read from
+  // 3 c + 1, last by the lagging pairs in 3 c + 2), Pm in 3 c + 1 (read in 3 c + 2
+  // and 3 c + 3), K, Q and the factors of chunk c + 1 in 3 c + 1 and 3 c + 2, into
+  // the buffer that was last read in 3 c. With one buffer nobody lags, and K, Q and
+  // the factors come in between two barriers more, when the old ones are done with.
   if (w < 2 * NPAIR) {
     // ---------------------------------------------------------------- state
     const int pr = w >> 1, r = w & 1;
@@ -113,26 +120,25 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
     }
     // The wave's rows of V, a chunk ahead. (No load of a next chunk stands in a
     // branch, here or below: it would be waited for where the branches join.)
-    uint32_t vr[8], voff[8];
+    uint32_t vr[8];
     const uint32_t vs = static_cast<uint32_t>(p.v_step);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = 32 * r + 16 * (i / 4) + 4 * g + (i % 4);
-      voff[i] = col_ok ? (static_cast<uint32_t>(t) * vs + static_cast<uint32_t>(col)) * EB : kOutOfRange;
-    }
+    const uint32_t vbase = col_ok ? (static_cast<uint32_t>(32 * r + 4 * g) * vs + static_cast<uint32_t>(col)) * EB : 0x80000000u;
     auto fetch_v = [&](int c) __attribute__((always_inline)) {
       const int64_t t0 = static_cast<int64_t>(c) * kGdrC;
       const int rows = static_cast<int>(len - t0 < kGdrC ? len - t0 : kGdrC);
       const rsrc_t rv = rows_buffer<EB>(p.v, (row_b + t0) * p.v_step + static_cast<int64_t>(h) * P, rows, vs, P);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) vr[i] = buffer_load_bits<BF16>(rv, voff[i]);
+      for (int i = 0; i < 8; ++i) {
+        vr[i] = buffer_load_bits<BF16>(rv, vbase + static_cast<uint32_t>(16 * (i / 4) + (i % 4)) * vs * EB);
+      }
     };
 
     half8_t Sh[NK], Sl[NK];
-    float s_down = 0.0f;
+    float s_down = 0.0f, s_top = 0.0f;
     // The wave's half of S as an operand, for itself and for the others.
     auto split_S = [&]() __attribute__((always_inline)) {
-      const Pow2 s = pow2_to_top(tiles_absmax<NJ>(S));
+      s_top = tiles_absmax<NJ>(S);
+      const Pow2 s = pow2_to_top(s_top);
       s_down = s.down;
 #pragma unroll
       for (int q = 0; q < NK; ++q) {
@@ -144,7 +150,9 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
     };
     if (n_chunks > 0) fetch_v(0);
     split_S();
+    const bool lag = W::kLag && pr >= NPAIR / 2;
     __syncthreads();
+    if (lag) __syncthreads();
 
     for (int c = 0; c < n_chunks; ++c) {
       const int buf = W::NBUF == 2 ? (c & 1) : 0;
@@ -175,7 +183,7 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
             }
           }
         }
-        const float top = lanes16_max(tiles_absmax<NJ>(S));
+        const float top = lanes16_max(s_top);
         if (lane == 0 && col < P) ws.top[(item * kGdrMaxima + kMaxS) * kGdrMaxSlots + col / 16 * 2 + r] = top;
       }
 
@@ -327,6 +335,7 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
         if (lane == 0 && col < P) ws.top[(item * kGdrMaxima + kMaxE) * kGdrMaxSlots + col / 16 * 2 + r] = top;
       }
     }
+    if (W::kLag && !lag) __syncthreads();
     if constexpr (!KEEP) {
       if (p.h_final != nullptr && col_ok) {
 #pragma unroll
@@ -356,29 +365,32 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
   u32x4_t kr[W::NKQ], qr[KEEP ? 1 : W::NKQ], tr[W::NTL], pm[KEEP ? 1 : W::NPL];
   float fr[W::NFL];
   f32x2_t fe;
-  auto fetch = [&](int c) __attribute__((always_inline)) {
+  auto fetch_kq = [&](int c) __attribute__((always_inline)) {
     const float* fac = ws.fac + (item0 + c) * (kGdrFactors * kGdrC);
     const u32x4_t* K = reinterpret_cast<const u32x4_t*>(ws.K + (kv0 + c) * W::kMat) + ltid;
     const u32x4_t* Q = reinterpret_cast<const u32x4_t*>(ws.Q + (kv0 + c) * W::kMat) + ltid;
-    const u32x4_t* T = reinterpret_cast<const u32x4_t*>(ws.T + (item0 + c) * kGdrPieceHalves) + ltid;
-    const u32x4_t* Pm = reinterpret_cast<const u32x4_t*>(ws.Pm + (item0 + c) * kGdrPieceHalves);
 #pragma unroll
     for (int i = 0; i < W::NKQ; ++i) {
       kr[i] = K[i * W::NL];
       if constexpr (!KEEP) qr[i] = Q[i * W::NL];
     }
 #pragma unroll
-    for (int i = 0; i < W::NTL; ++i) tr[i] = T[i * W::NL];
-    if constexpr (!KEEP) {
-#pragma unroll
-      for (int i = 0; i < W::NPL; ++i) {
-        const int e = (i * W::NL + ltid) % (W::kP / 8);  // (past the end: any)
-        pm[i] = Pm[OP == 2 ? e : 2 * e - (e & 63)];      // with one half a piece, every other 64 of the workspace's
-      }
-    }
-#pragma unroll
     for (int i = 0; i < W::NFL; ++i) fr[i] = fac[kFacK * kGdrC + (i * W::NL + ltid) % (4 * kGdrC)];
     fe = *reinterpret_cast<const f32x2_t*>(fac + kFacEnd * kGdrC);
+  };
+  auto fetch_T = [&](int c) __attribute__((always_inline)) {
+    const u32x4_t* T = reinterpret_cast<const u32x4_t*>(ws.T + (item0 + c) * kGdrPieceHalves) + ltid;
+#pragma unroll
+    for (int i = 0; i < W::NTL; ++i) tr[i] = T[i * W::NL];
+  };
+  auto fetch_P = [&](int c) __attribute__((always_inline)) {
+    if constexpr (KEEP) return;
+    const u32x4_t* Pm = reinterpret_cast<const u32x4_t*>(ws.Pm + (item0 + c) * kGdrPieceHalves);
+#pragma unroll
+    for (int i = 0; i < W::NPL; ++i) {
+      const int e = (i * W::NL + ltid) % (W::kP / 8);  // (past the end: any)
+      pm[i] = Pm[OP == 2 ? e : 2 * e - (e & 63)];      // with one half a piece, every other 64 of the workspace's
+    }
   };
   // K, Q and the factors into a buffer.
   auto stage_kq = [&](int buf) __attribute__((always_inline)) {
@@ -408,32 +420,15 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
       if (W::kP / 8 % W::NL == 0 || e < W::kP / 8) reinterpret_cast<u32x4_t*>(sP)[e] = pm[i];
     }
   };
-  uint32_t yoff[W::kHalvesOut][8];
-#pragma unroll
-  for (int hf = 0; hf < W::kHalvesOut; ++hf) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = 32 * (W::kHalvesOut == 2 ? hf : (ow & 1)) + 16 * (i / 4) + 4 * g + (i % 4);
-      yoff[hf][i] = col_ok ? (static_cast<uint32_t>(t) * yrow + static_cast<uint32_t>(col)) * (OB16 ? 2 : 4) : kOutOfRange;
-    }
-  }
-  if (n_chunks > 0) {
-    fetch(0);
-    stage_kq(0);
-    stage_T();
-  }
-  __syncthreads();
-
-  for (int c = 0; c < n_chunks; ++c) {
-    const int buf = W::NBUF == 2 ? (c & 1) : 0;
-    const _Float16* sQ = reinterpret_cast<const _Float16*>(lds[buf]) + W::kMat;
+  // Byte offset of the wave's element (4 g, col) of a chunk of y; past any
+  // buffer (and staying there with a chunk's rows added) where there is no column.
+  constexpr uint32_t YB = OB16 ? 2 : 4;
+  const uint32_t ybase = col_ok ? (static_cast<uint32_t>(4 * g) * yrow + static_cast<uint32_t>(col)) * YB : 0x80000000u;
+  // Q S of a chunk, in its first phase.
+  f32x4_t qs[KEEP ? 1 : W::kHalvesOut][2][2];
+  auto readout = [&](int c) __attribute__((always_inline)) {
+    const _Float16* sQ = reinterpret_cast<const _Float16*>(lds[W::NBUF == 2 ? (c & 1) : 0]) + W::kMat;
     const float* sF = reinterpret_cast<const float*>(sQ + W::kMat);
-    const bool more = c + 1 < n_chunks;
-    // The weights of this chunk (nobody reads them before the next barrier),
-    // then all loads of the next.
-    stage_P();
-    fetch(more ? c + 1 : c);
-    f32x4_t qs[KEEP ? 1 : W::kHalvesOut][2][2];
     if constexpr (!KEEP) {
 #pragma unroll
       for (int hf = 0; hf < W::kHalvesOut; ++hf) {
@@ -471,8 +466,11 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
         }
       }
     }
-    __syncthreads();
-    __syncthreads();
+  };
+  // Its y, in its third.
+  auto output = [&](int c) __attribute__((always_inline)) {
+    const float* sF = reinterpret_cast<const float*>(reinterpret_cast<const _Float16*>(lds[W::NBUF == 2 ? (c & 1) : 0]) +
+                                                     2 * W::kMat);
     if constexpr (!KEEP) {
       const int64_t t0 = static_cast<int64_t>(c) * kGdrC;
       const int rows = static_cast<int>(len - t0 < kGdrC ? len - t0 : kGdrC);
@@ -530,18 +528,75 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
           }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) buffer_store_f32<OB16>(pe[i / 4][i % 4], ry, yoff[hf][i]);
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t t = static_cast<uint32_t>(32 * r + 16 * (i / 4) + (i % 4));
+          buffer_store_f32<OB16>(pe[i / 4][i % 4], ry, ybase + t * yrow * YB);
+        }
       }
     }
-    if (more) {
-      stage_T();
-      if constexpr (W::NBUF == 2) stage_kq((c + 1) & 1);
+  };
+  // A wave forms y in two phases of a chunk and moves data in the third. (A
+  // fetch behind the last chunk fetches that again.)
+  const bool lag = W::kLag && pr >= NPAIR / 2;
+  const auto at_most = [&](int c) { return c < n_chunks ? c : n_chunks - 1; };
+  const auto walk = [&](auto lags) __attribute__((always_inline)) {  // (a loop for either, its loads in no branch)
+    constexpr bool LAG = decltype(lags)::value;
+    if (n_chunks > 0) {
+      fetch_kq(0);
+      stage_kq(0);
+      fetch_kq(at_most(1));
+      fetch_T(0);
+      fetch_P(0);
     }
     __syncthreads();
-    if constexpr (W::NBUF == 1) {
-      if (more) stage_kq(0);
+    for (int c = 0; c < n_chunks; ++c) {
+      const auto move = [&]() __attribute__((always_inline)) {
+        if constexpr (W::NBUF == 2) {
+          stage_kq((c + 1) & 1);
+          fetch_kq(at_most(c + 2));
+        }
+        fetch_T(at_most(c + 1));
+        fetch_P(at_most(c + 1));
+      };
+      stage_T();
+      if constexpr (!LAG) {
+        readout(c);
+      } else {
+        if (c > 0) output(c - 1);
+      }
       __syncthreads();
+      stage_P();
+      if constexpr (LAG) {
+        readout(c);
+      } else {
+        move();
+      }
+      __syncthreads();
+      if constexpr (LAG) {
+        move();
+      } else {
+        output(c);
+      }
+      __syncthreads();
+      if constexpr (W::NBUF == 1) {
+        stage_kq(0);
+        fetch_kq(at_most(c + 2));
+        __syncthreads();
+      }
     }
+    if constexpr (LAG) {
+      if (n_chunks > 0) output(n_chunks - 1);
+    }
+    if constexpr (W::kLag) __syncthreads();
+  };
+  if constexpr (W::kLag) {
+    if (lag) {
+      walk(std::true_type{});
+    } else {
+      walk(std::false_type{});
+    }
+  } else {
+    walk(std::false_type{});
   }
 
   if constexpr (KEEP) return;
