@@ -13,9 +13,13 @@
 //   dc_t = scale e^c_t q_t . N1_t - e^c_t k_t . N2_t - w_t k_t . N3_t + sum_s beta_s Z[t,s] - beta_t sum_u Z[u,t]
 //          (+ sum_s w_s k_s . N3_s + e^c_end <X, S> at the chunk's end)
 //   d(dt A)_t = sum_{u >= t} dc_u
-// One block of four waves per (batch row, query/key head, chunk); wave w has
-// row tile w. The heads that share q and k are taken one after another, their
-// dq and dk added in registers: no partial sums in memory, no atomics.
+// One block of eight waves per (batch row, query/key head, chunk); wave w has
+// row tile w % 4 and half w / 4 of the N columns (and of dP and M: the one or
+// the other). The heads that share q and k are taken one after another, their
+// dq and dk added in registers: no partial sums in memory, no atomics. (With
+// four waves a block the accumulators of a wave, 192 registers, and their
+// operands spilled: 600 us where the layer (2, 4096, 16 heads of 128 x 128) needs
+// less now.)
 #include <hip/hip_runtime.h>
 
 #include "gdr_mma.h"
@@ -24,21 +28,28 @@ namespace ssm {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kGS = kGdrC + 4;   // row stride of Gq and Gk in LDS (floats)
 constexpr int kPS = 32 + 8;      // row stride of the staged 64 x 32 pieces (halves)
 
-// Eight float32 of a row, zero past `count` and where !ok. vec: 16-byte loads.
-__device__ __forceinline__ void load8_f32(const float* row, int e, int count, bool ok, bool vec, float (&x)[8]) {
-  if (vec) {
-    f32x4_t u = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, v = u;
-    if (ok && e < count) u = *reinterpret_cast<const f32x4_t*>(row + e);
-    if (ok && e + 4 < count) v = *reinterpret_cast<const f32x4_t*>(row + e + 4);
+// Elements e .. e+7 of a float32 row that starts `row` elements into the
+// buffer; zero past `count` and where !ok. FAST: rows on 16-byte boundaries,
+// count a multiple of 4. (No branch: a conditional load is waited for where
+// the branches join.)
+template <bool FAST>
+__device__ __forceinline__ void load8_f32(rsrc_t r, uint32_t row, int e, int count, bool ok, float (&x)[8]) {
+  const uint32_t at = (row + static_cast<uint32_t>(e)) * 4;
+  if constexpr (FAST) {
+    const u32x4_t u = __builtin_amdgcn_raw_buffer_load_b128(r, ok && e < count ? at : kOutOfRange, 0, 0);
+    const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, ok && e + 4 < count ? at + 16 : kOutOfRange, 0, 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = u[i], x[4 + i] = v[i];
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]), x[4 + i] = __uint_as_float(v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = ok && e + i < count ? row[e + i] : 0.0f;
+    for (int i = 0; i < 8; ++i) {
+      x[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          r, ok && e + i < count ? at + static_cast<uint32_t>(4 * i) : kOutOfRange, 0, 0));
+    }
   }
 }
 
@@ -70,10 +81,9 @@ __device__ __forceinline__ float wave_sum64(float v) {
   return v;
 }
 
-template <int NP, bool BF16>
-__global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwdArgs a, const GdrWork ws, int chunks,
-                                                             int yvec, int nvec) {
-  constexpr int RAW = BF16 ? 1 : 2, RS = NP + 8, NJ = NP / 16;
+template <int NP, bool BF16, bool FAST>
+__global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwdArgs a, const GdrWork ws, int chunks) {
+  constexpr int RAW = BF16 ? 1 : 2, RS = NP + 8, NJ = NP / 32;  // NJ: column tiles of a wave
   constexpr int kMat = RAW * kGdrC * NP;
   constexpr int kLo = kGdrC * NP;
   constexpr int kSX = 32 * RS;                            // halves of a staged 32 x NP piece
@@ -84,9 +94,9 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
   __shared__ __align__(16) char pool[kStage > kG ? kStage : kG];
   __shared__ double sC[kGdrC];
   __shared__ float sBeta[kGdrC], sKn[kGdrC], sQn[kGdrC], sKup[kGdrC], sQup[kGdrC];
-  __shared__ float sRow[4][kGdrC];                        // q.N1, k.N2, k.N3, sum_s beta_s Z
-  __shared__ float sCol[4][kGdrC];                        // a wave's sums of Z down the columns
-  __shared__ float sDot[4];
+  __shared__ float sRow[4][2][kGdrC];                     // q.N1, k.N2, k.N3 (half the columns each), sum_s beta_s Z
+  __shared__ float sCol[8][kGdrC];                        // a wave's sums of Z down the columns
+  __shared__ float sDot[8];
   const GatedDeltaArgs& p = a.f;
   _Float16* sS = reinterpret_cast<_Float16*>(pool);       // [2][32][RS]
   _Float16* sX = sS + 2 * kSX;
@@ -96,7 +106,10 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
   float* sGq = reinterpret_cast<float*>(pool);            // [64][kGS]
   float* sGk = sGq + kGdrC * kGS;
 
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, m = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w8 = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int w = w8 & 3, hf = w8 >> 2;                     // row tile, half
+  const int c0 = hf * (NP / 2);                           // the wave's first column
   const int H = static_cast<int>(p.nheads), G = static_cast<int>(p.nkheads), r = H / G;
   const int N = static_cast<int>(p.dstate), P = static_cast<int>(p.headdim);
   const int c = static_cast<int>(blockIdx.x) % chunks;
@@ -134,10 +147,14 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
   }
 
   for (int hh = 0; hh < r; ++hh) {
+    // The lane's place, made anew for every head as far as the compiler can
+    // tell: it would else keep every LDS address and mask of the body in
+    // registers across the heads (125 of them spilled).
+    const int place = anew(lane), m = place & 15, g = place >> 4;
     const int h = kh * r + hh;
     const int64_t item = (static_cast<int64_t>(b) * H + h) * chunks + c;
     if (rows == 0) {  // behind the row's last step
-      if (w == 0) {
+      if (w8 == 0) {
         if (lane < out_rows) {
           a.ddt[(row0 + lane) * H + h] = 0.0f;
           a.dbeta[(row0 + lane) * H + h] = 0.0f;
@@ -148,7 +165,7 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     }
     // Gates (wave 0; its lane t keeps the step's values for the end).
     float x = 0.0f, beta_raw = 0.0f;
-    if (w == 0) {
+    if (w8 == 0) {
       float ld = 0.0f, beta = 0.0f;
       if (lane < rows) {
         const int64_t at = (row0 + lane) * H + h;
@@ -157,7 +174,7 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
         beta_raw = load_elem<BF16>(p.beta, at);
         beta = gdr_beta(p, beta_raw);
       }
-      sC[lane] = wave_prefix(ld, lane);
+      sC[lane] = wave_prefix(static_cast<double>(ld) * kLog2eD, lane);
       sBeta[lane] = beta;
     }
     Pow2 top[kGdrMaxima];
@@ -166,53 +183,70 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
       const int slots = (P + 15) / 16 * 2;
 #pragma unroll
       for (int k = 0; k < kGdrMaxima; ++k) {
-        float v = 0.0f;
-        for (int i = 0; i < slots; ++i) v = fmaxf(v, t[k * kGdrMaxSlots + i]);
-        top[k] = pow2_to_top(v);
+        const float v = (lane & 31) < slots ? t[k * kGdrMaxSlots + (lane & 31)] : 0.0f;
+        top[k] = pow2_to_top(lanes16_max(col_max(v)));
       }
     }
 
-    f32x4_t n1[NJ], n2[NJ], n3[NJ], dp[4], mm[4];
+    f32x4_t n1[NJ], n2[NJ], n3[NJ], tri[4];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) n1[j] = n2[j] = n3[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dp[j] = mm[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < 4; ++j) tri[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     float dot = 0.0f;  // this thread's part of <X, S>
 
+    // 32 columns of S, X, dY, E, dE at a time, the next ones in flight in
+    // registers: a piece of S and X a thread, a piece of dY or dE, half a piece of E.
+    constexpr int kSXT = 32 * NP / 8 < kThreads ? 1 : 32 * NP / 8 / kThreads;
+    float fs[kSXT][8], fx[kSXT][8], fy[8], fe[8];
+    const int trow = (tid >> 2) & 63, tcol = 8 * (tid & 3);
+    const uint32_t yrow = static_cast<uint32_t>(H * P);
+    const rsrc_t rs = raw_buffer(ws.S + item * P * N, static_cast<uint32_t>(P * N * 4));
+    const rsrc_t rx = raw_buffer(ws.X + item * P * N, static_cast<uint32_t>(P * N * 4));
+    const rsrc_t re = raw_buffer(ws.E + item * kGdrC * P, static_cast<uint32_t>(kGdrC * P * 4));
+    const rsrc_t ry = rows_buffer<4>(hf == 0 ? a.dy : a.dv, row0 * yrow + static_cast<int64_t>(h) * P, rows, yrow, P);
+    const auto fetch = [&](int p0) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < kSXT; ++i) {
+        const int e = (i * kThreads + tid) * 8 % (32 * NP), pr = e / NP, n = e % NP;
+        const bool ok = p0 + pr < P;
+        load8_f32<FAST>(rs, static_cast<uint32_t>((p0 + pr) * N), n, N, ok, fs[i]);
+        load8_f32<FAST>(rx, static_cast<uint32_t>((p0 + pr) * N), n, N, ok, fx[i]);
+      }
+      load8_f32<FAST>(ry, static_cast<uint32_t>(trow) * yrow + static_cast<uint32_t>(p0), tcol, P - p0, trow < rows, fy);
+      load8_f32<FAST>(re, static_cast<uint32_t>(trow * P + p0), tcol, P - p0, true, fe);
+    };
+    fetch(0);
     for (int p0 = 0; p0 < P; p0 += 32) {
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 32 * NP / 8 / kThreads; ++i) {
-        const int e = (i * kThreads + tid) * 8, pr = e / NP, n = e % NP;
-        const bool ok = p0 + pr < P;
-        float s[8], xx[8];
-        load8_f32(ws.S + (item * P + p0 + pr) * N, n, N, ok, nvec, s);
-        load8_f32(ws.X + (item * P + p0 + pr) * N, n, N, ok, nvec, xx);
+      for (int i = 0; i < kSXT; ++i) {
+        const int e = (i * kThreads + tid) * 8 % (32 * NP), pr = e / NP, n = e % NP;
+        if (32 * NP / 8 >= kThreads || tid < 32 * NP / 8) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) dot = fmaf(s[k], xx[k], dot);
-        store_split(sS + pr * RS + n, kSX, s, top[kMaxS].up);
-        store_split(sX + pr * RS + n, kSX, xx, top[kMaxX].up);
+          for (int k = 0; k < 8; ++k) dot = fmaf(fs[i][k], fx[i][k], dot);
+        }
+        // (with 64 states two threads have, and write, the same piece)
+        store_split(sS + pr * RS + n, kSX, fs[i], top[kMaxS].up);
+        store_split(sX + pr * RS + n, kSX, fx[i], top[kMaxX].up);
       }
-      {
-        const int t = tid >> 2, e = 8 * (tid & 3);
-        const bool ok = t < rows;
-        float v[8];
-        load8_f32(a.dy + (row0 + t) * H * P + h * P + p0, e, P - p0, ok, yvec, v);
-        store_split(sY + t * kPS + e, kTP, v, top[kMaxDY].up);
-        load8_f32(a.dv + (row0 + t) * H * P + h * P + p0, e, P - p0, ok, yvec, v);
-        store_split(sD + t * kPS + e, kTP, v, top[kMaxDE].up);
-        load8_f32(ws.E + (item * kGdrC + t) * P + p0, e, P - p0, true, P % 4 == 0, v);
-        store_split(sE + t * kPS + e, kTP, v, top[kMaxE].up);
-      }
+      store_split((hf == 0 ? sY : sD) + trow * kPS + tcol, kTP, fy, top[hf == 0 ? kMaxDY : kMaxDE].up);
+      if (hf == 0) store_split(sE + trow * kPS + tcol, kTP, fe, top[kMaxE].up);
       __syncthreads();
+      fetch(p0 + 32);  // (past the last columns: zeros)
       const int at = (16 * w + m) * kPS + 8 * g;
-      const half8_t yh = *reinterpret_cast<const half8_t*>(sY + at), yl = *reinterpret_cast<const half8_t*>(sY + kTP + at);
-      const half8_t eh = *reinterpret_cast<const half8_t*>(sE + at), el = *reinterpret_cast<const half8_t*>(sE + kTP + at);
-      const half8_t dh = *reinterpret_cast<const half8_t*>(sD + at), dl = *reinterpret_cast<const half8_t*>(sD + kTP + at);
+      const auto two = [&](const _Float16* q, half8_t& hi, half8_t& lo) __attribute__((always_inline)) {
+        hi = *reinterpret_cast<const half8_t*>(q);
+        lo = *reinterpret_cast<const half8_t*>(q + kTP);
+      };
+      half8_t yh, yl, eh, el, dh, dl;
+      two(sY + at, yh, yl);
+      two(sE + at, eh, el);
+      two(sD + at, dh, dl);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const half8_t sh = column8(sS, RS, 0, 16 * j, m, g), sl = column8(sS + kSX, RS, 0, 16 * j, m, g);
-        const half8_t xh = column8(sX, RS, 0, 16 * j, m, g), xl = column8(sX + kSX, RS, 0, 16 * j, m, g);
+        const half8_t sh = column8(sS, RS, 0, c0 + 16 * j, m, g), sl = column8(sS + kSX, RS, 0, c0 + 16 * j, m, g);
+        const half8_t xh = column8(sX, RS, 0, c0 + 16 * j, m, g), xl = column8(sX + kSX, RS, 0, c0 + 16 * j, m, g);
         n1[j] = mfma16(yh, sh, n1[j]);
         n2[j] = mfma16(dh, sh, n2[j]);
         n3[j] = mfma16(eh, xh, n3[j]);
@@ -223,77 +257,73 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
         n2[j] = mfma16(dl, sh, n2[j]);
         n3[j] = mfma16(el, xh, n3[j]);
       }
+      const half8_t lh = hf == 0 ? yh : dh, ll = hf == 0 ? yl : dl;
 #pragma unroll
       for (int si = 0; si < 4; ++si) {
         if (si > w) continue;
-        const int bt = (16 * si + m) * kPS + 8 * g;
-        const half8_t bh = *reinterpret_cast<const half8_t*>(sE + bt), bl = *reinterpret_cast<const half8_t*>(sE + kTP + bt);
-        dp[si] = mfma16(yh, bh, dp[si]);
-        mm[si] = mfma16(dh, bh, mm[si]);
-        dp[si] = mfma16(yh, bl, dp[si]);
-        mm[si] = mfma16(dh, bl, mm[si]);
-        dp[si] = mfma16(yl, bh, dp[si]);
-        mm[si] = mfma16(dl, bh, mm[si]);
+        half8_t bh, bl;
+        two(sE + (16 * si + m) * kPS + 8 * g, bh, bl);
+        tri[si] = mfma16(lh, bh, tri[si]);
+        tri[si] = mfma16(lh, bl, tri[si]);
+        tri[si] = mfma16(ll, bh, tri[si]);
       }
     }
     dot = wave_sum64(dot);
-    if (lane == 0) sDot[w] = dot;
+    if (lane == 0) sDot[w8] = dot;
     __syncthreads();  // the staged pieces are done with; Gq and Gk take their place
 
     const double cend = sC[kGdrC - 1];
-    float ct[4], into[4], wt[4], row_z[4];
+    float into[4], wt[4], row_z[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = 16 * w + 4 * g + i;
-      ct[i] = 0.0f;
-      into[i] = exp2_hw(static_cast<float>(sC[t]) * kLog2e);
-      wt[i] = sBeta[t] * exp2_hw(static_cast<float>(cend - sC[t]) * kLog2e);
+      into[i] = exp2_hw(static_cast<float>(sC[t]));
+      wt[i] = sBeta[t] * exp2_hw(static_cast<float>(cend - sC[t]));
       row_z[i] = 0.0f;
     }
-    (void)ct;
+    // Gq and the first term of Z (half 0), Gk and the second (half 1).
+    {
+      const _Float16* left = hf == 0 ? sQ : sK;
+      const float* ln = hf == 0 ? sQn : sKn;
+      float* out = hf == 0 ? sGq : sGk;
+      const float unit = hf == 0 ? top[kMaxDY].down * top[kMaxE].down * p.scale : -(top[kMaxDE].down * top[kMaxE].down);
 #pragma unroll
-    for (int si = 0; si < 4; ++si) {
-      float col_z = 0.0f;
-      const int s = 16 * si + m;
-      if (si <= w) {
-        f32x4_t kk = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, qk = kk;
+      for (int si = 0; si < 4; ++si) {
+        float col_z = 0.0f;
+        const int s = 16 * si + m;
+        if (si <= w) {
+          f32x4_t xk = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};  // q_t . k_s or k_t . k_s
 #pragma unroll
-        for (int n = 0; n < NP; n += 32) {
-          const int at = kq_at<NP>(16 * w + m, n + 8 * g), bt = kq_at<NP>(16 * si + m, n + 8 * g);
-          const half8_t bk = *reinterpret_cast<const half8_t*>(sK + bt);
-          const half8_t ak = *reinterpret_cast<const half8_t*>(sK + at);
-          const half8_t aq = *reinterpret_cast<const half8_t*>(sQ + at);
-          kk = mfma16(ak, bk, kk);
-          qk = mfma16(aq, bk, qk);
-          if constexpr (RAW == 2) {
-            const half8_t bl = *reinterpret_cast<const half8_t*>(sK + kLo + bt);
-            kk = mfma16(ak, bl, kk);
-            qk = mfma16(aq, bl, qk);
-            kk = mfma16(*reinterpret_cast<const half8_t*>(sK + kLo + at), bk, kk);
-            qk = mfma16(*reinterpret_cast<const half8_t*>(sQ + kLo + at), bk, qk);
+          for (int n = 0; n < NP; n += 32) {
+            const int at = kq_at<NP>(16 * w + m, n + 8 * g), bt = kq_at<NP>(16 * si + m, n + 8 * g);
+            const half8_t bk = *reinterpret_cast<const half8_t*>(sK + bt);
+            const half8_t al = *reinterpret_cast<const half8_t*>(left + at);
+            xk = mfma16(al, bk, xk);
+            if constexpr (RAW == 2) {
+              xk = mfma16(al, *reinterpret_cast<const half8_t*>(sK + kLo + bt), xk);
+              xk = mfma16(*reinterpret_cast<const half8_t*>(left + kLo + at), bk, xk);
+            }
+          }
+          const float bs = sBeta[s], kns = sKn[s];
+          const double cs = sC[s];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = 16 * w + 4 * g + i;
+            const bool in = hf == 0 ? s <= t : s < t;
+            const float dec = exp2_hw(static_cast<float>(sC[t] - cs));
+            const float u = in ? tri[si][i] * unit * dec : 0.0f;
+            const float z = in ? u * (xk[i] * ln[t] * kns) : 0.0f;  // (no product of a masked infinity)
+            row_z[i] = fmaf(bs, z, row_z[i]);
+            col_z += z;
+            out[t * kGS + s] = u * bs;
           }
         }
-        const float bs = sBeta[s], kns = sKn[s];
-        const double cs = sC[s];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = 16 * w + 4 * g + i;
-          const float dec = exp2_hw(static_cast<float>(sC[t] - cs) * kLog2e);
-          const float u = s <= t ? dp[si][i] * (top[kMaxDY].down * top[kMaxE].down) * (p.scale * dec) : 0.0f;
-          const float v = s < t ? mm[si][i] * (top[kMaxDE].down * top[kMaxE].down) * dec : 0.0f;
-          const float z = u * (qk[i] * sQn[t] * kns) - v * (kk[i] * sKn[t] * kns);
-          const float zz = s <= t ? z : 0.0f;  // (no product of a masked infinity)
-          row_z[i] = fmaf(bs, zz, row_z[i]);
-          col_z += zz;
-          sGq[t * kGS + s] = u * bs;
-          sGk[t * kGS + s] = -v * bs;
-        }
+        const auto x32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(col_z), __float_as_uint(col_z), false, false);
+        col_z = __uint_as_float(x32[0]) + __uint_as_float(x32[1]);
+        const auto x16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(col_z), __float_as_uint(col_z), false, false);
+        col_z = __uint_as_float(x16[0]) + __uint_as_float(x16[1]);
+        if (g == 0) sCol[w8][s] = col_z;
       }
-      const auto x32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(col_z), __float_as_uint(col_z), false, false);
-      col_z = __uint_as_float(x32[0]) + __uint_as_float(x32[1]);
-      const auto x16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(col_z), __float_as_uint(col_z), false, false);
-      col_z = __uint_as_float(x16[0]) + __uint_as_float(x16[1]);
-      if (g == 0) sCol[w][s] = col_z;
     }
     // Row products with N1, N2, N3, and their parts of dq and dk.
     {
@@ -304,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
       for (int j = 0; j < NJ; ++j) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int at = kq_at<NP>(16 * w + 4 * g + i, 16 * j + m);
+          const int at = kq_at<NP>(16 * w + 4 * g + i, c0 + 16 * j + m);
           float kv = static_cast<float>(sK[at]), qv = static_cast<float>(sQ[at]);
           if constexpr (RAW == 2) {
             kv += static_cast<float>(sK[kLo + at]);
@@ -324,10 +354,10 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
         const float q1 = lanes16_sum(r1[i]), q2 = lanes16_sum(r2[i]), q3 = lanes16_sum(r3[i]);
         const float qz = lanes16_sum(row_z[i]);
         if (m == 0) {
-          sRow[0][t] = q1 * sQn[t];
-          sRow[1][t] = q2 * sKn[t];
-          sRow[2][t] = q3 * sKn[t];
-          sRow[3][t] = qz;
+          sRow[0][hf][t] = q1 * sQn[t];
+          sRow[1][hf][t] = q2 * sKn[t];
+          sRow[2][hf][t] = q3 * sKn[t];
+          sRow[3][hf][t] = qz;
         }
       }
     }
@@ -335,8 +365,9 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
 
     // dq += Gq K;  dk += Gk K + Gk^T K + Gq^T Q. The row factors of K and Q go
     // into the triangles' columns; a triangle's rows 16 w .. are halves of one scale.
-    const auto product = [&](const float* G, bool up, const float* cn, const _Float16* mat, f32x4_t* out)
+    const auto product = [&](const float* T, bool up, const float* cn, const _Float16* mat, f32x4_t* out)
                              __attribute__((always_inline)) {
+      const int place = anew(lane), m = place & 15, g = place >> 4;
       const int t = 16 * w + m;
       float x8[2][8];
       float mx = 0.0f;
@@ -345,7 +376,7 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int s = 32 * q + 8 * g + e;
-          x8[q][e] = (up ? s >= t : s <= t) ? G[up ? s * kGS + t : t * kGS + s] * cn[s] : 0.0f;
+          x8[q][e] = (up ? s >= t : s <= t) ? T[up ? s * kGS + t : t * kGS + s] * cn[s] : 0.0f;
           mx = fmaxf(mx, fabsf(x8[q][e]));
         }
       }
@@ -364,10 +395,10 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           if (up ? (q == 0 && w >= 2) : (q == 1 && w < 2)) continue;
-          const half8_t bv = kq_column8<NP>(mat, 32 * q, 16 * j, m, g);
+          const half8_t bv = kq_column8<NP>(mat, 32 * q, c0 + 16 * j, m, g);
           acc = mfma16(hi[q], bv, acc);
           acc = mfma16(lo[q], bv, acc);
-          if constexpr (RAW == 2) acc = mfma16(hi[q], kq_column8<NP>(mat + kLo, 32 * q, 16 * j, m, g), acc);
+          if constexpr (RAW == 2) acc = mfma16(hi[q], kq_column8<NP>(mat + kLo, 32 * q, c0 + 16 * j, m, g), acc);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) out[j][i] = fmaf(acc[i], sc.down, out[j][i]);
@@ -379,18 +410,21 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     product(sGq, true, sQn, sQ, dk);
 
     // The gates: lane t of wave 0.
-    if (w == 0) {
+    if (w8 == 0) {
       const double cl = sC[lane];
-      const float in = exp2_hw(static_cast<float>(cl) * kLog2e);
-      const float last = exp2_hw(static_cast<float>(cend - cl) * kLog2e);
-      const float beta = sBeta[lane], colz = (sCol[0][lane] + sCol[1][lane]) + (sCol[2][lane] + sCol[3][lane]);
-      const float r3 = sRow[2][lane];
+      const float in = exp2_hw(static_cast<float>(cl));
+      const float last = exp2_hw(static_cast<float>(cend - cl));
+      const float beta = sBeta[lane];
+      float colz = 0.0f, dots = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) colz += sCol[k][lane], dots += sDot[k];
+      const auto row = [&](int k) { return sRow[k][0][lane] + sRow[k][1][lane]; };
+      const float r3 = row(2);
       const float w3 = beta * last * r3;
-      float dc = p.scale * in * sRow[0][lane] - in * sRow[1][lane] - w3 + sRow[3][lane] - beta * colz;
+      const float dc = p.scale * in * row(0) - in * row(1) - w3 + row(3) - beta * colz;
       const float dbeta = fmaf(last, r3, colz);
       // sum over the steps from t on, the end's own part with the last one
-      const float at_end = wave_sum64(w3) + exp2_hw(static_cast<float>(cend) * kLog2e) *
-                                                ((sDot[0] + sDot[1]) + (sDot[2] + sDot[3]));
+      const float at_end = wave_sum64(w3) + exp2_hw(static_cast<float>(cend)) * dots;
       double suffix = dc;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
@@ -419,42 +453,62 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     __syncthreads();
   }
 
+  const int m = lane & 15, g = lane >> 4;
   // Through the norms: d = n (dhat - hat (hat . dhat)), hat = raw n.
+  const bool norm = rows > 0 && p.qk_l2norm;
+  if (norm) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 16 * w + 4 * g + i;
+      float sq = 0.0f, sk = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int at = kq_at<NP>(t, c0 + 16 * j + m);
+        float qv = static_cast<float>(sQ[at]), kv = static_cast<float>(sK[at]);
+        if constexpr (RAW == 2) {
+          qv += static_cast<float>(sQ[kLo + at]);
+          kv += static_cast<float>(sK[kLo + at]);
+        }
+        sq = fmaf(qv, dq[j][i], sq);
+        sk = fmaf(kv, dk[j][i], sk);
+      }
+      sq = lanes16_sum(sq);
+      sk = lanes16_sum(sk);
+      if (m == 0) {
+        sRow[0][hf][t] = sq * sQn[t];
+        sRow[1][hf][t] = sk * sKn[t];
+      }
+    }
+  }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = 16 * w + 4 * g + i;
-    float sq = 0.0f, sk = 0.0f, qv[NJ], kv[NJ];
     const bool on = t < rows;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int at = kq_at<NP>(t, 16 * j + m);
-      qv[j] = kv[j] = 0.0f;
-      if (rows > 0 && p.qk_l2norm) {
-        qv[j] = static_cast<float>(sQ[at]);
-        kv[j] = static_cast<float>(sK[at]);
-        if constexpr (RAW == 2) {
-          qv[j] += static_cast<float>(sQ[kLo + at]);
-          kv[j] += static_cast<float>(sK[kLo + at]);
-        }
-        qv[j] *= sQn[t];
-        kv[j] *= sKn[t];
-        sq = fmaf(qv[j], dq[j][i], sq);
-        sk = fmaf(kv[j], dk[j][i], sk);
-      }
-    }
-    float nq = 1.0f, nk = 1.0f;
-    if (rows > 0 && p.qk_l2norm) {
-      sq = lanes16_sum(sq);
-      sk = lanes16_sum(sk);
+    float fq = 0.0f, fk = 0.0f, nq = 1.0f, nk = 1.0f;
+    if (norm) {
+      fq = (sRow[0][0][t] + sRow[0][1][t]) * sQn[t];
+      fk = (sRow[1][0][t] + sRow[1][1][t]) * sKn[t];
       nq = sQn[t] * sQup[t];
       nk = sKn[t] * sKup[t];
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int n = 16 * j + m;
+      const int n = c0 + 16 * j + m;
+      float vq = dq[j][i], vk = dk[j][i];
+      if (norm) {
+        const int at = kq_at<NP>(t, n);
+        float qv = static_cast<float>(sQ[at]), kv = static_cast<float>(sK[at]);
+        if constexpr (RAW == 2) {
+          qv += static_cast<float>(sQ[kLo + at]);
+          kv += static_cast<float>(sK[kLo + at]);
+        }
+        vq = nq * fmaf(-qv, fq, vq);
+        vk = nk * fmaf(-kv, fk, vk);
+      }
       const uint32_t off = n < N ? (static_cast<uint32_t>(t) * grow + static_cast<uint32_t>(n)) * 4 : kOutOfRange;
-      buffer_store_f32<false>(on ? nq * (dq[j][i] - qv[j] * sq) : 0.0f, rdq, off);
-      buffer_store_f32<false>(on ? nk * (dk[j][i] - kv[j] * sk) : 0.0f, rdk, off);
+      buffer_store_f32<false>(on ? vq : 0.0f, rdq, off);
+      buffer_store_f32<false>(on ? vk : 0.0f, rdk, off);
     }
   }
 }
@@ -498,11 +552,12 @@ int launch_gdr_grads(const GatedDeltaBwdArgs& a, const GdrWork& ws, int64_t chun
   const int n = static_cast<int>(chunks);
   if (n > 0) {
     const unsigned blocks = static_cast<unsigned>(a.f.batch * a.f.nkheads * chunks);
-    const int yvec = a.f.headdim % 4 == 0 && on16(a.dy) && on16(a.dv), nvec = a.f.dstate % 4 == 0;
+    const bool fast = a.f.headdim % 4 == 0 && a.f.dstate % 4 == 0 && on16(a.dy) && on16(a.dv);
     const auto types = [&](auto np, auto bf16) {
       constexpr int NP = decltype(np)::value;
       constexpr bool BF16 = decltype(bf16)::value;
-      gdr_grads_kernel<NP, BF16><<<blocks, kThreads, 0, st>>>(a, ws, n, yvec, nvec);
+      fast ? gdr_grads_kernel<NP, BF16, true><<<blocks, kThreads, 0, st>>>(a, ws, n)
+           : gdr_grads_kernel<NP, BF16, false><<<blocks, kThreads, 0, st>>>(a, ws, n);
     };
     const auto width = [&](auto np) { a.f.in_bf16 ? types(np, std::true_type{}) : types(np, std::false_type{}); };
     if (a.f.dstate <= 64) {

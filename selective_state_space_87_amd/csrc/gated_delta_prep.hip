@@ -55,7 +55,7 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
   float* sT = reinterpret_cast<float*>(pool);         // [64][kMS]
   float* sP = sT + kGdrC * kMS;
 
-  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int H = static_cast<int>(p.nheads), G = static_cast<int>(p.nkheads), heads = H / G;
   const int c = static_cast<int>(blockIdx.x) % chunks;
@@ -80,6 +80,8 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
     si = q - ti * (ti + 1) / 2;
     return q < 10;
   };
+  {
+  const int m = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int j = 0; j < 3; ++j) {
     int ti, si;
@@ -110,8 +112,10 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
       qk[j][i] *= qt[i] * (ks * p.scale);
     }
   }
+  }
 
   for (int hh = 0; hh < heads; ++hh) {
+    const int place = anew(lane), m = place & 15, g = place >> 4;
     const int h = kh * heads + hh;
     const int64_t item = (static_cast<int64_t>(b) * H + h) * chunks + c;
     // Gates: lane t of wave 0. (Sums in units of log 2, for the base-2 exponential.)
@@ -149,6 +153,7 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
     // lane feeds them, scaled by rows, or by a given power of two.
     const auto pieces = [&](const float* src, int tt, bool up, _Float16* out, float* down, bool lo, bool whole,
                             Pow2 given) __attribute__((always_inline)) {
+      const int place = anew(lane), m = place & 15, g = place >> 4;
       const int t = 16 * tt + m;
       float x[2][8];
       float top = 0.0f;

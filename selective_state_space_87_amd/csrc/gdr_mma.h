@@ -59,6 +59,13 @@ __device__ __forceinline__ f32x4_t mfma16(half8_t a, half8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// x, as a value that the compiler cannot trace back: what is computed from it
+// inside a loop is not kept in registers across the loop.
+__device__ __forceinline__ int anew(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // The power of two that brings m >= 0 into [2^13, 2^14), and its inverse.
 // m below 2^-100 counts as 2^-100, infinity as 2^127.
 struct Pow2 {
