@@ -120,12 +120,16 @@ def _check(fn, status):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()  # (0, an empty tensor's, is NULL too)
 
 
 def _dev_tensor(name, t, shape, dtypes, device):
     if t is None:
         return None
+    # all is as it should be: one expression, since small calls are bound by these checks
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.shape == shape and t.dtype in dtypes
+            and t.is_contiguous() and (device is None or t.device == device)):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -143,8 +147,11 @@ def _dev_tensor(name, t, shape, dtypes, device):
 
 def _stream_handle(stream, device):
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(device.index)  # current_stream(device) without the object
+    return stream.cuda_stream
+
+
+_NOTHING_TO_ENTER = contextlib.nullcontext()
 
 
 def _launch_context(device, stream):
@@ -152,6 +159,8 @@ def _launch_context(device, stream):
     too: what the binding allocates here (outputs, workspace) is then owned by
     that stream in torch's caching allocator, so a workspace dropped after the
     call is not handed to work on another stream while the kernels still use it."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return _NOTHING_TO_ENTER
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(device))
     if stream is not None:
@@ -545,9 +554,7 @@ def _step_of(name, t, lead, dense):
     """Elements between consecutive steps of t, whose last two dimensions are
     dense and whose first ``lead`` are rows at one distance (a column range of
     a wider dense array, or a dense array)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return dense
     heads, width = t.shape[lead:]
     step, rows = None, 1
@@ -567,6 +574,8 @@ def _step_of(name, t, lead, dense):
 
 def _strided_tensor(name, t, shape, dtype, device):
     """Checks of a tensor that may be a column range; contiguity is _step_of's matter."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.shape == shape and t.dtype == dtype and t.device == device:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":

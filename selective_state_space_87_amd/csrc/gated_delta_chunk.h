@@ -27,8 +27,10 @@ template <int NP, bool BF16, bool OB16, int NPAIR, bool KEEP>
 struct GdrWalk {
   static constexpr int RAW = BF16 ? 1 : 2;
   static constexpr int OP = OB16 ? 1 : 2;               // halves in the products that only y sees
-  // Waves for y: one for every 32 steps of a slice, or (4 pairs) one a slice.
-  static constexpr int NOUT = NPAIR == 4 ? 4 : 2 * NPAIR;
+  // Waves for y and the loads: one for every 32 steps of a slice. (KEEP with
+  // four pairs: half as many, which have less to load; with sixteen waves a
+  // wave's 128 registers would not do.)
+  static constexpr int NOUT = KEEP && NPAIR == 4 ? 4 : 2 * NPAIR;
   static constexpr int kHalvesOut = 2 * NPAIR / NOUT;
   static constexpr int NT = 64 * (2 * NPAIR + NOUT);
   static constexpr int NL = 64 * NOUT;                  // threads that load
@@ -43,13 +45,13 @@ struct GdrWalk {
   static constexpr int kPairBytes = kXF * 2 + 7 * 64 * 4;
   static constexpr int kFixed = (kT + kP) * 2 + NPAIR * kPairBytes;
   static constexpr int NBUF = 2 * kBufBytes + kFixed <= 160 * 1024 ? 2 : 1;
-  // Four pairs (twelve waves) have 168 registers a wave: enough with one half in
+  // Four pairs (sixteen waves) have 128 registers a wave: enough with one half in
   // K, Q and in what only y sees. Elsewhere two pairs.
   static constexpr bool kFits = NBUF * kBufBytes + kFixed <= 160 * 1024 && (KEEP || (RAW == 1 && OP == 1));
   // With two buffers, half the pairs run one phase behind the others.
   static constexpr bool kLag = NBUF == 2 && NPAIR >= 2;
   static constexpr int NKQ = kMat / 8 / NL;             // 16-byte pieces of K (and Q) a loading thread
-  static constexpr int NTL = kT / 8 / NL;
+  static constexpr int NTL = (kT / 8 + NL - 1) / NL;
   static constexpr int NPL = (kP / 8 + NL - 1) / NL;
   static constexpr int NFL = (4 * kGdrC + NL - 1) / NL;
 };
@@ -379,9 +381,9 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
     fe = *reinterpret_cast<const f32x2_t*>(fac + kFacEnd * kGdrC);
   };
   auto fetch_T = [&](int c) __attribute__((always_inline)) {
-    const u32x4_t* T = reinterpret_cast<const u32x4_t*>(ws.T + (item0 + c) * kGdrPieceHalves) + ltid;
+    const u32x4_t* T = reinterpret_cast<const u32x4_t*>(ws.T + (item0 + c) * kGdrPieceHalves);
 #pragma unroll
-    for (int i = 0; i < W::NTL; ++i) tr[i] = T[i * W::NL];
+    for (int i = 0; i < W::NTL; ++i) tr[i] = T[(i * W::NL + ltid) % (W::kT / 8)];
   };
   auto fetch_P = [&](int c) __attribute__((always_inline)) {
     if constexpr (KEEP) return;
@@ -410,7 +412,10 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
   };
   auto stage_T = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < W::NTL; ++i) reinterpret_cast<u32x4_t*>(sT)[i * W::NL + ltid] = tr[i];
+    for (int i = 0; i < W::NTL; ++i) {
+      const int e = i * W::NL + ltid;
+      if (W::kT / 8 % W::NL == 0 || e < W::kT / 8) reinterpret_cast<u32x4_t*>(sT)[e] = tr[i];
+    }
   };
   auto stage_P = [&]() __attribute__((always_inline)) {
     if constexpr (KEEP) return;

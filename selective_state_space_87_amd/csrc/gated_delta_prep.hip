@@ -1,18 +1,23 @@
 // Gated delta rule, the part of a chunk that does not depend on the state: the
-// halves of K and Q, the triangular inverse T, the output's weights Pm and the per-step factors, for
-// every chunk at once.
+// halves of K and Q, the triangular inverse T, the output's weights Pm and the
+// per-step factors, for every chunk at once.
 //
 // One block of four waves per (batch row, query/key head, chunk); the value
-// heads that share q and k are taken one after another. K K^T and Q K^T (the
-// ten lower 16 x 16 tiles each) run on the matrix cores and stay in registers.
+// heads that share q and k are taken one after another. K K^T and K Q^T (the
+// ten 16 x 16 tiles of a triangle each) run on the matrix cores and stay in
+// registers: K Q^T, not Q K^T, since the D of its tiles is then, two tiles
+// together, the operand that Pm is fed as (lane m has row m of Pm, its elements
+// are 4 consecutive columns of either tile), with no way through LDS.
 // M = L diag(beta) is strictly lower, and T = (1 + M)^-1 is found by
 // substitution, never by powers of M (with equal keys and no decay the powers
 // reach 10^18 and cancel): one wave inverts the four diagonal blocks, a column
-// a lane, while the others write out Pm; then wave w takes block column w of T
-// down the rows, T_iw = -T_ii sum_k M_ik T_kw, in float32 matrix instructions,
-// without leaving its registers.
-// Sums of log decays and their differences are in double: behind a step that
-// forgets nearly everything the sums are large and the differences small.
+// a lane; then wave w takes block row w of T leftwards,
+//   T_wj = -(sum_(k > j) T_wk M_kj) T_jj,
+// transposed, in float32 matrix instructions, without leaving its registers,
+// and has again in D what T is fed as. (The backward's T^T: the same by block columns.)
+// Sums of log decays are in double, and kept as two floats whose differences
+// are taken apart: behind a step that forgets nearly everything the sums are
+// large and the differences small.
 #include <hip/hip_runtime.h>
 
 #include "gdr_mma.h"
@@ -22,19 +27,35 @@ namespace ssm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMS = kGdrC + 4;  // row stride of the float32 matrices in LDS
+constexpr int kMS = kGdrC + 4;  // row stride of M in LDS (floats)
+constexpr int kDS = 16 + 4;     // row stride of a diagonal block's inverse
 
 __device__ __forceinline__ f32x4_t mfma4(float a, float b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-// acc += A X for 16 x 16 tiles: A from LDS (row-major), X a D tile. Step s of
-// the four contracts rows 4 g + s, which is where X's element s lives.
-__device__ __forceinline__ f32x4_t tile_product(const float* A, f32x4_t X, f32x4_t acc, int m, int g) {
-  const f32x4_t a = *reinterpret_cast<const f32x4_t*>(A + m * kMS + 4 * g);
+// acc += A X for 16 x 16 tiles: A from LDS (row-major, or TR its transpose), X
+// a D tile. Step s of the four contracts rows 4 g + s, which is where X's element s lives.
+template <bool TR>
+__device__ __forceinline__ f32x4_t tile_product(const float* A, int stride, f32x4_t X, f32x4_t acc, int m, int g) {
+  f32x4_t a;
+  if constexpr (TR) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) a[s] = A[(4 * g + s) * stride + m];
+  } else {
+    a = *reinterpret_cast<const f32x4_t*>(A + m * stride + 4 * g);
+  }
 #pragma unroll
   for (int s = 0; s < 4; ++s) acc = mfma4(a[s], X[s], acc);
   return acc;
+}
+
+// The two D tiles 2 q, 2 q + 1 as a piece: its halves times `up` (lo: if asked for).
+__device__ __forceinline__ void store_piece(_Float16* at, f32x4_t a, f32x4_t b, float up, bool lo) {
+  const float x[8] = {a[0] * up, a[1] * up, a[2] * up, a[3] * up, b[0] * up, b[1] * up, b[2] * up, b[3] * up};
+  const half8_t hi = halves(x);
+  *reinterpret_cast<half8_t*>(at) = hi;
+  if (lo) *reinterpret_cast<half8_t*>(at + kGdrFragHalves) = rest(x, hi);
 }
 
 // BWD: also the pieces of T^T and, in place of Pm's, those of Pm^T.
@@ -44,16 +65,15 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
   constexpr int RAW = BF16 ? 1 : 2;
   constexpr int kMat = RAW * kGdrC * NP;              // halves of K (or Q)
   constexpr int kKQ = 2 * kMat * 2;                   // bytes
-  constexpr int kTP = 2 * kGdrC * kMS * 4;
-  __shared__ __align__(16) char pool[kKQ > kTP ? kKQ : kTP];  // K and Q, then T and Pm
-  __shared__ __align__(16) float sM[kGdrC * kMS];
-  __shared__ double sC[kGdrC];
+  constexpr int kMD = (kGdrC * kMS + 4 * 16 * kDS) * 4;
+  __shared__ __align__(16) char pool[kKQ > kMD ? kKQ : kMD];  // K and Q, then M and the diagonal inverses
+  __shared__ float sCh[kGdrC], sCl[kGdrC];            // sums of log decays in units of log 2, hi + lo
   __shared__ float sTop[4];
   __shared__ __align__(16) float sBeta[kGdrC], sKn[kGdrC], sQn[kGdrC], sKup[kGdrC], sQup[kGdrC];
   _Float16* sK = reinterpret_cast<_Float16*>(pool);   // [RAW][64][NP]
   _Float16* sQ = sK + kMat;
-  float* sT = reinterpret_cast<float*>(pool);         // [64][kMS]
-  float* sP = sT + kGdrC * kMS;
+  float* sM = reinterpret_cast<float*>(pool);         // [64][kMS]
+  float* sD = sM + kGdrC * kMS;                       // [4][16][kDS]
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -71,53 +91,62 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
                               ws.Q + static_cast<int64_t>(blockIdx.x) * kMat, sKn, sQn, sKup, sQup);
   __syncthreads();
 
-  // The ten lower tiles of K K^T and Q K^T, q = w, w + 4, w + 8, times the
-  // rows' factors.
-  f32x4_t kk[3], qk[3];
+  // K K^T: the ten lower tiles, tile q = w, w + 4, w + 8. For Pm: K Q^T, its
+  // tiles (s-tile j, t-tile w), j <= w (D: lane m step t, elements steps s);
+  // for Pm^T: Q K^T, tiles (t-tile j, s-tile w), j >= w. Times the rows' factors.
+  f32x4_t kk[3], pq[4];
   const auto tile = [&](int j, int& ti, int& si) __attribute__((always_inline)) {
     const int q = w + 4 * j;
     ti = q == 0 ? 0 : (q < 3 ? 1 : (q < 6 ? 2 : 3));
     si = q - ti * (ti + 1) / 2;
     return q < 10;
   };
+  const auto in_row = [&](int j) __attribute__((always_inline)) { return BWD ? j >= w : j <= w; };
   {
-  const int m = lane & 15, g = lane >> 4;
+    const int m = lane & 15, g = lane >> 4;
+    // A B^T for 16-row tiles of two matrices of halves.
+    const auto product = [&](const _Float16* A, int ta, const _Float16* B, int tb) __attribute__((always_inline)) {
+      f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    int ti, si;
-    kk[j] = qk[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    if (!tile(j, ti, si)) continue;
-#pragma unroll
-    for (int n = 0; n < NP; n += 32) {
-      const int at = kq_at<NP>(16 * ti + m, n + 8 * g), bt = kq_at<NP>(16 * si + m, n + 8 * g);
-      const half8_t bk = *reinterpret_cast<const half8_t*>(sK + bt);
-      const half8_t ak = *reinterpret_cast<const half8_t*>(sK + at);
-      const half8_t aq = *reinterpret_cast<const half8_t*>(sQ + at);
-      kk[j] = mfma16(ak, bk, kk[j]);
-      qk[j] = mfma16(aq, bk, qk[j]);
-      if constexpr (RAW == 2) {
-        const half8_t bl = *reinterpret_cast<const half8_t*>(sK + kGdrC * NP + bt);
-        kk[j] = mfma16(ak, bl, kk[j]);
-        qk[j] = mfma16(aq, bl, qk[j]);
-        kk[j] = mfma16(*reinterpret_cast<const half8_t*>(sK + kGdrC * NP + at), bk, kk[j]);
-        qk[j] = mfma16(*reinterpret_cast<const half8_t*>(sQ + kGdrC * NP + at), bk, qk[j]);
+      for (int n = 0; n < NP; n += 32) {
+        const int at = kq_at<NP>(16 * ta + m, n + 8 * g), bt = kq_at<NP>(16 * tb + m, n + 8 * g);
+        const half8_t x = *reinterpret_cast<const half8_t*>(A + at), y = *reinterpret_cast<const half8_t*>(B + bt);
+        acc = mfma16(x, y, acc);
+        if constexpr (RAW == 2) {
+          acc = mfma16(x, *reinterpret_cast<const half8_t*>(B + kGdrC * NP + bt), acc);
+          acc = mfma16(*reinterpret_cast<const half8_t*>(A + kGdrC * NP + at), y, acc);
+        }
       }
-    }
-    const f32x4_t kt = *reinterpret_cast<const f32x4_t*>(sKn + 16 * ti + 4 * g);
-    const f32x4_t qt = *reinterpret_cast<const f32x4_t*>(sQn + 16 * ti + 4 * g);
-    const float ks = sKn[16 * si + m];
+      return acc;
+    };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      kk[j][i] *= kt[i] * ks;
-      qk[j][i] *= qt[i] * (ks * p.scale);
+    for (int j = 0; j < 3; ++j) {
+      int ti, si;
+      kk[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      if (!tile(j, ti, si)) continue;
+      kk[j] = product(sK, ti, sK, si);
+      const f32x4_t kt = *reinterpret_cast<const f32x4_t*>(sKn + 16 * ti + 4 * g);
+      const float ks = sKn[16 * si + m];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kk[j][i] *= kt[i] * ks;
     }
-  }
+    const float own = (BWD ? sKn : sQn)[16 * w + m] * p.scale;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      pq[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      if (!in_row(j)) continue;
+      pq[j] = product(BWD ? sQ : sK, j, BWD ? sK : sQ, w);
+      const f32x4_t f = *reinterpret_cast<const f32x4_t*>((BWD ? sQn : sKn) + 16 * j + 4 * g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pq[j][i] *= f[i] * own;
+    }
   }
 
   for (int hh = 0; hh < heads; ++hh) {
     const int place = anew(lane), m = place & 15, g = place >> 4;
     const int h = kh * heads + hh;
     const int64_t item = (static_cast<int64_t>(b) * H + h) * chunks + c;
+    float* fac = ws.fac + item * (kGdrFactors * kGdrC);
     // Gates: lane t of wave 0. (Sums in units of log 2, for the base-2 exponential.)
     if (w == 0) {
       float ld = 0.0f, beta = 0.0f;
@@ -126,71 +155,32 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
         ld = gdr_log_decay(p, load_elem<BF16>(p.dt, at), p.dt_bias ? p.dt_bias[h] : 0.0f, p.A[h]);
         beta = gdr_beta(p, load_elem<BF16>(p.beta, at));
       }
-      sC[lane] = wave_prefix(static_cast<double>(ld) * kLog2eD, lane);
+      const double cs = wave_prefix(static_cast<double>(ld) * kLog2eD, lane);
+      sCh[lane] = static_cast<float>(cs);
+      sCl[lane] = static_cast<float>(cs - static_cast<double>(static_cast<float>(cs)));
       sBeta[lane] = beta;
     }
-    __syncthreads();  // gates; K and Q (or the last head's T and Pm) are done with
+    __syncthreads();  // gates; K and Q (or the last head's M) are done with
+    const auto decay = [&](float hi, float lo, float hi0, float lo0) __attribute__((always_inline)) {
+      return exp2_hw((hi - hi0) + (lo - lo0));
+    };
 
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
       int ti, si;
       if (!tile(j, ti, si)) continue;
       const int s = 16 * si + m;
-      const double cs = sC[s];
-      const float bs = sBeta[s];
+      const float hs = sCh[s], ls = sCl[s], bs = sBeta[s];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = 16 * ti + 4 * g + i;
-        const float dec = exp2_hw(static_cast<float>(sC[t] - cs)) * bs;
-        sM[t * kMS + s] = t > s ? dec * kk[j][i] : 0.0f;
-        sP[t * kMS + s] = t >= s ? dec * qk[j][i] : 0.0f;
+        const float v = decay(sCh[t], sCl[t], hs, ls) * (bs * kk[j][i]);
+        sM[t * kMS + s] = ti != si || t > s ? v : 0.0f;
       }
     }
     __syncthreads();
 
-    float* fac = ws.fac + item * (kGdrFactors * kGdrC);
-    // Row tile `tt` of a matrix (or of its transpose) as halves in the order a
-    // lane feeds them, scaled by rows, or by a given power of two.
-    const auto pieces = [&](const float* src, int tt, bool up, _Float16* out, float* down, bool lo, bool whole,
-                            Pow2 given) __attribute__((always_inline)) {
-      const int place = anew(lane), m = place & 15, g = place >> 4;
-      const int t = 16 * tt + m;
-      float x[2][8];
-      float top = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (up ? (q == 0 && tt >= 2) : (q == 1 && tt < 2)) continue;
-        if (!up) {
-          const f32x4_t a = *reinterpret_cast<const f32x4_t*>(src + t * kMS + 32 * q + 4 * g);
-          const f32x4_t d = *reinterpret_cast<const f32x4_t*>(src + t * kMS + 32 * q + 16 + 4 * g);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[q][e] = a[e], x[q][4 + e] = d[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int s = 32 * q + (e < 4 ? 4 * g + e : 12 + 4 * g + e);
-          // (a block above the diagonal was never written)
-          if (up) x[q][e] = src[s * kMS + t];
-          if (up ? s < t : s > t) x[q][e] = 0.0f;
-          top = fmaxf(top, fabsf(x[q][e]));
-        }
-      }
-      const Pow2 s = whole ? given : pow2_to_top(col_max(top));
-      if (!whole && g == 0) down[t] = s.down;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (up ? (q == 0 && tt >= 2) : (q == 1 && tt < 2)) continue;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[q][e] *= s.up;
-        const half8_t hi = halves(x[q]);
-        _Float16* at = out + (up ? gdr_frag_up(tt, q) : gdr_frag(tt, q)) * 2 * kGdrFragHalves + lane * 8;
-        *reinterpret_cast<half8_t*>(at) = hi;
-        if (lo) *reinterpret_cast<half8_t*>(at + kGdrFragHalves) = rest(x[q], hi);
-      }
-    };
-
     // Wave 0: the diagonal blocks' inverses, lane (g, m) column m of block g.
-    // The others: Pm, and the factors.
     if (w == 0) {
       float x[16];
       const float* D = sM + 16 * g * kMS + 16 * g;
@@ -200,57 +190,101 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
 #pragma unroll
         for (int k = 0; k < i; ++k) acc = fmaf(-D[i * kMS + k], x[k], acc);
         x[i] = acc;
-        sT[(16 * g + i) * kMS + 16 * g + m] = acc;
+        sD[(16 * g + i) * kDS + m] = acc;
       }
-    } else {
-      const Pow2 none = Pow2{1.0f, 1.0f};
-      _Float16* out = (BWD ? ws.Pt : ws.Pm) + item * kGdrPieceHalves;
-      pieces(sP, w, BWD, out, fac + kFacP * kGdrC, BWD || out_lo, false, none);
-      if (w == 1) pieces(sP, 0, BWD, out, fac + kFacP * kGdrC, BWD || out_lo, false, none);
-      if (w == 2) {
-        const double ct = sC[lane], cend = sC[kGdrC - 1];
-        const float into = exp2_hw(static_cast<float>(ct));
-        const float last = exp2_hw(static_cast<float>(cend - ct));
-        fac[kFacK * kGdrC + lane] = into * sKn[lane];
-        fac[kFacQ * kGdrC + lane] = p.scale * into * sQn[lane];
-        fac[kFacW * kGdrC + lane] = sBeta[lane] * last * sKn[lane];
-        if constexpr (BWD) {
-          fac[kFacKup * kGdrC + lane] = sKup[lane];
-          fac[kFacQup * kGdrC + lane] = sQup[lane];
-          fac[kFacKn * kGdrC + lane] = sKn[lane];
-          fac[kFacQn * kGdrC + lane] = sQn[lane];
+    }
+    // Row tile w of Pm (or of Pm^T), scaled by rows.
+    {
+      f32x4_t x[4];
+      float top = 0.0f;
+      const int own = 16 * w + m;
+      const float ho = sCh[own], lo = sCl[own], bo = BWD ? sBeta[own] : 1.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        if (!in_row(j)) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int o = 16 * j + 4 * g + i;  // s (or t)
+          const float d = BWD ? decay(sCh[o], sCl[o], ho, lo) * bo : decay(ho, lo, sCh[o], sCl[o]) * sBeta[o];
+          const float v = d * pq[j][i];
+          x[j][i] = j != w || (BWD ? o >= own : o <= own) ? v : 0.0f;
+          top = fmaxf(top, fabsf(x[j][i]));
         }
-        if (lane == 0) fac[kFacEnd * kGdrC] = exp2_hw(static_cast<float>(cend));
       }
+      const Pow2 s = pow2_to_top(col_max(top));
+      if (g == 0) fac[kFacP * kGdrC + own] = s.down;
+      _Float16* out = (BWD ? ws.Pt : ws.Pm) + item * kGdrPieceHalves + lane * 8;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (BWD ? (q == 0 && w >= 2) : (q == 1 && w < 2)) continue;
+        store_piece(out + (BWD ? gdr_frag_up(w, q) : gdr_frag(w, q)) * 2 * kGdrFragHalves, x[2 * q], x[2 * q + 1], s.up,
+                    BWD || out_lo);
+      }
+    }
+    if (w == 1) {
+      const float ht = sCh[lane], lt = sCl[lane];
+      const float into = exp2_hw(ht + lt);
+      const float last = decay(sCh[kGdrC - 1], sCl[kGdrC - 1], ht, lt);
+      fac[kFacK * kGdrC + lane] = into * sKn[lane];
+      fac[kFacQ * kGdrC + lane] = p.scale * into * sQn[lane];
+      fac[kFacW * kGdrC + lane] = sBeta[lane] * last * sKn[lane];
+      if constexpr (BWD) {
+        fac[kFacKup * kGdrC + lane] = sKup[lane];
+        fac[kFacQup * kGdrC + lane] = sQup[lane];
+        fac[kFacKn * kGdrC + lane] = sKn[lane];
+        fac[kFacQn * kGdrC + lane] = sQn[lane];
+      }
+      if (lane == kGdrC - 1) fac[kFacEnd * kGdrC] = into;
     }
     __syncthreads();
 
-    // Block column w of T.
+    // Block row w of T, transposed: R[j] is T_wj^T (lane m row t of T, elements
+    // its columns s). R_j = -T_jj^T sum_(k > j) M_kj^T R_k.
+    f32x4_t R[4], C[4];
     float top = 0.0f;
-    {
-      f32x4_t T[4];
+#pragma unroll
+    for (int j = 3; j >= 0; --j) {
+      R[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      if (j == w) {
+        R[j] = *reinterpret_cast<const f32x4_t*>(sD + (16 * j + m) * kDS + 4 * g);  // (T_jj^T)[4 g + i][m]
+      }
+      if (j < w) {
+        f32x4_t X = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 3; k > j; --k) {
+          if (k <= w) X = tile_product<true>(sM + 16 * k * kMS + 16 * j, kMS, R[k], X, m, g);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) X[e] = -X[e];
+        R[j] = tile_product<true>(sD + 16 * j * kDS, kDS, X, R[j], m, g);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(R[j][e]));
+    }
+    if constexpr (BWD) {  // block column w: C[i] = T_iw
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        T[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        C[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         if (i == w) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) T[i][e] = sT[(16 * i + 4 * g + e) * kMS + 16 * i + m];
+          for (int e = 0; e < 4; ++e) C[i][e] = sD[(16 * i + 4 * g + e) * kDS + m];
         }
         if (i > w) {
           f32x4_t X = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int k = 0; k < i; ++k) {
-            if (k >= w) X = tile_product(sM + 16 * i * kMS + 16 * k, T[k], X, m, g);
+            if (k >= w) X = tile_product<false>(sM + 16 * i * kMS + 16 * k, kMS, C[k], X, m, g);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) X[e] = -X[e];
-          T[i] = tile_product(sT + 16 * i * kMS + 16 * i, X, T[i], m, g);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sT[(16 * i + 4 * g + e) * kMS + 16 * w + m] = T[i][e];
+          C[i] = tile_product<false>(sD + 16 * i * kDS, kDS, X, C[i], m, g);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(C[i][e]));
       }
-      top = lanes16_max(tiles_absmax<4>(T));
     }
+    top = lanes16_max(col_max(top));
     if (lane == 0) sTop[w] = top;
     __syncthreads();
 
@@ -258,8 +292,20 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
     // halves reach down to 2^-38 of the largest element.
     const Pow2 st = pow2_to_top(fmaxf(fmaxf(sTop[0], sTop[1]), fmaxf(sTop[2], sTop[3])));
     if (tid == 0) fac[kFacEnd * kGdrC + 1] = st.down;
-    pieces(sT, w, false, ws.T + item * kGdrPieceHalves, nullptr, true, true, st);
-    if constexpr (BWD) pieces(sT, w, true, ws.Tt + item * kGdrPieceHalves, nullptr, true, true, st);
+    _Float16* out = ws.T + item * kGdrPieceHalves + lane * 8;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (q == 1 && w < 2) continue;
+      store_piece(out + gdr_frag(w, q) * 2 * kGdrFragHalves, R[2 * q], R[2 * q + 1], st.up, true);
+    }
+    if constexpr (BWD) {
+      out = ws.Tt + item * kGdrPieceHalves + lane * 8;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (q == 0 && w >= 2) continue;
+        store_piece(out + gdr_frag_up(w, q) * 2 * kGdrFragHalves, C[2 * q], C[2 * q + 1], st.up, true);
+      }
+    }
   }
 }
 
