@@ -182,6 +182,9 @@ size_t gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nk
   return plan_gated_delta(batch, seqlen, nkheads, nheads, headdim, dstate, in_bf16, true).bytes;
 }
 
-int64_t rms_norm_bwd_blocks(int64_t rows, int64_t) { return rows < 512 ? rows : 512; }
+int64_t rms_norm_bwd_blocks(int64_t rows, int64_t dim) {
+  const int64_t groups = ceil_div(rows, dim <= 1024 ? 4 : 1);  // rows a block takes at a time
+  return groups < 512 ? groups : 512;
+}
 
 }  // namespace ssm

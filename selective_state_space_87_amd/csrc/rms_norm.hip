@@ -11,7 +11,8 @@
 // elements, four rows a block; above, a block of four waves per row with one
 // LDS exchange per sum. A thread holds 8 elements a piece, NPK pieces; pieces
 // are 16 bytes of bfloat16 or 32 of float32, consecutive threads read
-// consecutive pieces.
+// consecutive pieces. (Rows that are not whole 16-byte pieces: one element a
+// load, consecutive threads consecutive elements.)
 #include <hip/hip_runtime.h>
 
 #include "device_math.h"
@@ -23,8 +24,9 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Eight elements e .. e+7 of a row that starts at `at`; zeros past `dim`.
-template <bool BF16, bool VEC>
+// Eight elements of a row that starts at `at`: e, e + step .. e + 7 step (VEC:
+// step 1); zeros past `dim`.
+template <bool BF16, bool VEC, int STEP>
 __device__ __forceinline__ void load8(const void* base, int64_t at, int e, int dim, float (&o)[8]) {
   if constexpr (VEC) {
     if (e < dim) {  // dim is a multiple of 8
@@ -48,11 +50,11 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int e, int d
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = e + i < dim ? load_elem<BF16>(base, at + e + i) : 0.0f;
+    for (int i = 0; i < 8; ++i) o[i] = e + i * STEP < dim ? load_elem<BF16>(base, at + e + i * STEP) : 0.0f;
   }
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16, bool VEC, int STEP>
 __device__ __forceinline__ void store8(void* base, int64_t at, int e, int dim, const float (&v)[8]) {
   if constexpr (VEC) {
     if (e < dim) {
@@ -73,14 +75,14 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int e, int dim, c
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (e + i < dim) store_elem<BF16>(base, at + e + i, v[i]);
+      if (e + i * STEP < dim) store_elem<BF16>(base, at + e + i * STEP, v[i]);
     }
   }
 }
 
 // Eight values in e4m3 (already divided by the row's scale; what rounding took
 // past 448 is brought back, NaN stays).
-template <bool VEC>
+template <bool VEC, int STEP>
 __device__ __forceinline__ void store8_e4m3(void* base, int64_t at, int e, int dim, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = v[i] > 448.0f ? 448.0f : (v[i] < -448.0f ? -448.0f : v[i]);
@@ -95,7 +97,7 @@ __device__ __forceinline__ void store8_e4m3(void* base, int64_t at, int e, int d
     const uint64_t w = static_cast<uint32_t>(lo) | (static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (e + i < dim) dst[i] = static_cast<uint8_t>(w >> (8 * i));
+      if (e + i * STEP < dim) dst[i * STEP] = static_cast<uint8_t>(w >> (8 * i));
     }
   }
 }
@@ -138,6 +140,7 @@ __device__ __forceinline__ float row_max(float v, float* slot) {
 // OUT: 0 float32, 1 bfloat16, 2 e4m3. RES: 0 none, 1 float32, 2 bfloat16.
 template <int TPR, int NPK, bool BF16_IN, int RES, int OUT, bool VEC>
 __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const RmsNormArgs p) {
+  constexpr int STEP = VEC ? 1 : TPR;
   __shared__ float slots[2][4];
   const int dim = static_cast<int>(p.dim);
   const int t = threadIdx.x % TPR;
@@ -148,18 +151,18 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const RmsNormArgs p)
   float sq = 0.0f;
 #pragma unroll
   for (int i = 0; i < NPK; ++i) {
-    const int e = (i * TPR + t) * 8;
-    load8<BF16_IN, VEC>(p.x, at, e, dim, s[i]);
+    const int e = VEC ? (i * TPR + t) * 8 : i * TPR * 8 + t;
+    load8<BF16_IN, VEC, STEP>(p.x, at, e, dim, s[i]);
     if constexpr (RES != 0) {
       float r[8];
-      load8<RES == 2, VEC>(p.residual, at, e, dim, r);
+      load8<RES == 2, VEC, STEP>(p.residual, at, e, dim, r);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         s[i][k] += r[k];
         // the norm is taken of what the stream holds
         if constexpr (RES == 2) s[i][k] = bf16_bits_to_f32(f32_to_bf16_bits(s[i][k]));
       }
-      store8<RES == 2, VEC>(p.residual_out, at, e, dim, s[i]);
+      store8<RES == 2, VEC, STEP>(p.residual_out, at, e, dim, s[i]);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) sq = fmaf(s[i][k], s[i][k], sq);
@@ -168,10 +171,10 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const RmsNormArgs p)
   float top = 0.0f;
 #pragma unroll
   for (int i = 0; i < NPK; ++i) {
-    const int e = (i * TPR + t) * 8;
+    const int e = VEC ? (i * TPR + t) * 8 : i * TPR * 8 + t;
     float w[8];
     if (p.weight != nullptr) {
-      load8<false, VEC>(p.weight, 0, e, dim, w);
+      load8<false, VEC, STEP>(p.weight, 0, e, dim, w);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) w[k] = 1.0f;
@@ -181,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const RmsNormArgs p)
       s[i][k] = s[i][k] * r * w[k];
       if constexpr (OUT == 2) top = fmaxf(top, fabsf(s[i][k]));
     }
-    if constexpr (OUT != 2) store8<OUT == 1, VEC>(p.y, at, e, dim, s[i]);
+    if constexpr (OUT != 2) store8<OUT == 1, VEC, STEP>(p.y, at, e, dim, s[i]);
   }
   if constexpr (OUT == 2) {
     top = row_max<TPR>(top, slots[1]);
@@ -191,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const RmsNormArgs p)
     for (int i = 0; i < NPK; ++i) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) s[i][k] *= inv;
-      store8_e4m3<VEC>(p.y, at, (i * TPR + t) * 8, dim, s[i]);
+      store8_e4m3<VEC, STEP>(p.y, at, VEC ? (i * TPR + t) * 8 : i * TPR * 8 + t, dim, s[i]);
     }
     if (t == 0) p.scales[row] = scale;
   }
@@ -202,17 +205,17 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const RmsNormArgs p)
 // rms_norm_dweight_kernel in block order.
 template <int TPR, int NPK, bool BF16, bool VEC>
 __global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(const RmsNormBwdArgs p) {
-  constexpr int kRows = kThreads / TPR;
+  constexpr int kRows = kThreads / TPR, STEP = VEC ? 1 : TPR;
   __shared__ float slots[4][4];
   const int dim = static_cast<int>(p.dim);
   const int t = threadIdx.x % TPR, part = threadIdx.x / TPR;
   float dw[NPK][8], w[NPK][8];
 #pragma unroll
   for (int i = 0; i < NPK; ++i) {
-    const int e = (i * TPR + t) * 8;
+    const int e = VEC ? (i * TPR + t) * 8 : i * TPR * 8 + t;
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[i][k] = 0.0f, w[i][k] = 1.0f;
-    if (p.weight != nullptr) load8<false, VEC>(p.weight, 0, e, dim, w[i]);
+    if (p.weight != nullptr) load8<false, VEC, STEP>(p.weight, 0, e, dim, w[i]);
   }
   int pass = 0;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + part; row < p.rows;
@@ -222,9 +225,9 @@ __global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(const RmsNormBwd
     float sq = 0.0f, su = 0.0f;
 #pragma unroll
     for (int i = 0; i < NPK; ++i) {
-      const int e = (i * TPR + t) * 8;
-      load8<BF16, VEC>(p.s, at, e, dim, s[i]);
-      load8<false, VEC>(p.dy, at, e, dim, g[i]);
+      const int e = VEC ? (i * TPR + t) * 8 : i * TPR * 8 + t;
+      load8<BF16, VEC, STEP>(p.s, at, e, dim, s[i]);
+      load8<false, VEC, STEP>(p.dy, at, e, dim, g[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         sq = fmaf(s[i][k], s[i][k], sq);
@@ -239,10 +242,10 @@ __global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(const RmsNormBwd
     const float c = su / static_cast<float>(dim) * r * r;
 #pragma unroll
     for (int i = 0; i < NPK; ++i) {
-      const int e = (i * TPR + t) * 8;
+      const int e = VEC ? (i * TPR + t) * 8 : i * TPR * 8 + t;
       float o[8];
       if (p.dresidual != nullptr) {
-        load8<false, VEC>(p.dresidual, at, e, dim, o);
+        load8<false, VEC, STEP>(p.dresidual, at, e, dim, o);
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] = 0.0f;
@@ -252,7 +255,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(const RmsNormBwd
         dw[i][k] = fmaf(g[i][k], s[i][k] * r, dw[i][k]);
         o[k] = fmaf(r, fmaf(-s[i][k], c, g[i][k] * w[i][k]), o[k]);
       }
-      store8<false, VEC>(p.ds, at, e, dim, o);
+      store8<false, VEC, STEP>(p.ds, at, e, dim, o);
     }
   }
   if (p.dweight == nullptr) return;
@@ -260,7 +263,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(const RmsNormBwd
   if constexpr (kRows == 1) {
 #pragma unroll
     for (int i = 0; i < NPK; ++i) {
-      store8<false, VEC>(out, static_cast<int64_t>(blockIdx.x) * dim, (i * TPR + t) * 8, dim, dw[i]);
+      store8<false, VEC, STEP>(out, static_cast<int64_t>(blockIdx.x) * dim, VEC ? (i * TPR + t) * 8 : i * TPR * 8 + t, dim, dw[i]);
     }
   } else {
     __shared__ float sums[kRows][NPK * 8 * TPR];
@@ -278,34 +281,41 @@ __global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(const RmsNormBwd
           const int at = (i * 8 + k) * TPR + t;
           dw[i][k] = (sums[0][at] + sums[1][at]) + (sums[2][at] + sums[3][at]);
         }
-        store8<false, VEC>(out, static_cast<int64_t>(blockIdx.x) * dim, (i * TPR + t) * 8, dim, dw[i]);
+        store8<false, VEC, STEP>(out, static_cast<int64_t>(blockIdx.x) * dim, VEC ? (i * TPR + t) * 8 : i * TPR * 8 + t, dim, dw[i]);
       }
     }
   }
 }
 
-// dweight[c] = sum over the blocks' parts: 64 columns a block, four waves each
-// adding every fourth part, then the four sums.
-__global__ __launch_bounds__(kThreads) void rms_norm_dweight_kernel(const float* __restrict__ parts, int nparts,
-                                                                    int dim, float* __restrict__ dweight) {
-  __shared__ float sums[4][64];
+// dweight[c] = sum over the blocks' parts: 64 columns a block, sixteen waves
+// each adding every sixteenth part, then the sixteen sums in order. (Four waves
+// took 7.4 us for 500 parts of 1537: too few loads in flight.)
+constexpr int kDwWaves = 16;
+__global__ __launch_bounds__(64 * kDwWaves) void rms_norm_dweight_kernel(const float* __restrict__ parts, int nparts,
+                                                                         int dim, float* __restrict__ dweight) {
+  __shared__ float sums[kDwWaves][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int c = static_cast<int>(blockIdx.x) * 64 + lane;
   float acc = 0.0f;
   if (c < dim) {
     int i = w;
-    for (; i + 28 < nparts; i += 32) {
+    for (; i + 7 * kDwWaves < nparts; i += 8 * kDwWaves) {
       float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = parts[static_cast<int64_t>(i + 4 * k) * dim + c];
+      for (int k = 0; k < 8; ++k) v[k] = parts[static_cast<int64_t>(i + k * kDwWaves) * dim + c];
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc += v[k];
     }
-    for (; i < nparts; i += 4) acc += parts[static_cast<int64_t>(i) * dim + c];
+    for (; i < nparts; i += kDwWaves) acc += parts[static_cast<int64_t>(i) * dim + c];
   }
   sums[w][lane] = acc;
   __syncthreads();
-  if (w == 0 && c < dim) dweight[c] = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
+  if (w == 0 && c < dim) {
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kDwWaves; ++k) v += sums[k][lane];
+    dweight[c] = v;
+  }
 }
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -395,7 +405,7 @@ int launch_rms_norm_bwd(const RmsNormBwdArgs& a, void* stream) {
   }
   if (a.dweight != nullptr) {
     const unsigned blocks = static_cast<unsigned>((a.dim + 63) / 64);
-    rms_norm_dweight_kernel<<<blocks, kThreads, 0, st>>>(static_cast<const float*>(a.workspace), nparts,
+    rms_norm_dweight_kernel<<<blocks, 64 * kDwWaves, 0, st>>>(static_cast<const float*>(a.workspace), nparts,
                                                          static_cast<int>(a.dim), a.dweight);
   }
   return static_cast<int>(hipGetLastError());
