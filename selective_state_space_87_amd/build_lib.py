@@ -35,7 +35,7 @@ CXX = os.environ.get("CXX_HOST", "g++")
 DEVICE_SOURCES = ["scan_fwd.hip", "scan_fwd_bb.hip", "scan_fwd_bf.hip", "scan_fwd_fb.hip", "scan_fwd_ff.hip",
                   "scan_ckpt_b.hip", "scan_ckpt_f.hip", "scan_bwd.hip", "state_update.hip", "conv1d.hip", "ssd.hip",
                   "scan_noalloc.hip", "gated_delta.hip", "gated_delta_prep.hip",
-                  "gated_delta_chunk_b.hip", "gated_delta_chunk_f.hip", "gated_delta_reverse.hip", "gated_delta_grads.hip",
+                  "gated_delta_chunk_b.hip", "gated_delta_chunk_f.hip", "gdr_segments.hip", "gated_delta_reverse.hip", "gated_delta_grads.hip",
                   "rms_norm.hip"]
 HOST_SOURCES = ["api.cpp", "plan.cpp"]
 PROBE_SOURCES = ["probe.hip"]

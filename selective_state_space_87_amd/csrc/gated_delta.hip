@@ -195,7 +195,7 @@ int launch_gated_delta_update(const GatedDeltaArgs& a, void* stream) {
 
 namespace {
 
-GdrWork gdr_work(void* workspace, const GdrPlan& pl) {
+GdrWork gdr_work(void* workspace, const GdrPlan& pl, const GatedDeltaArgs& a) {
   char* base = static_cast<char*>(workspace);
   GdrWork ws{};
   ws.T = reinterpret_cast<_Float16*>(base + pl.off_t);
@@ -210,6 +210,9 @@ GdrWork gdr_work(void* workspace, const GdrPlan& pl) {
   ws.E = reinterpret_cast<float*>(base + pl.off_e);
   ws.top = reinterpret_cast<float*>(base + pl.off_top);
   ws.part = reinterpret_cast<float*>(base + pl.off_part);
+  ws.map = reinterpret_cast<float*>(base + pl.off_map);
+  ws.seg = reinterpret_cast<float*>(base + pl.off_seg);
+  ws.seg_stride = a.batch * a.nheads * a.headdim * a.dstate;
   return ws;
 }
 
@@ -219,10 +222,10 @@ bool rows_on_16(const GatedDeltaArgs& a) {
          on_boundary(a.k, 16);
 }
 
-int launch_chunks(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, void* stream) {
-  if (const int e = launch_gdr_prep(a, ws, chunks, !a.out_bf16, backward, rows_on_16(a), stream)) return e;
-  return a.in_bf16 ? launch_gdr_chunk_b(a, ws, chunks, backward, stream)
-                   : launch_gdr_chunk_f(a, ws, chunks, backward, stream);
+int launch_chunks(const GatedDeltaArgs& a, const GdrWork& ws, const GdrPlan& pl, bool backward, void* stream) {
+  if (const int e = launch_gdr_prep(a, ws, pl.chunks, !a.out_bf16, backward, rows_on_16(a), stream)) return e;
+  return a.in_bf16 ? launch_gdr_chunk_b(a, ws, pl, backward, stream)
+                   : launch_gdr_chunk_f(a, ws, pl, backward, stream);
 }
 
 }  // namespace
@@ -230,15 +233,15 @@ int launch_chunks(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bo
 int launch_gated_delta(const GatedDeltaArgs& a, void* stream) {
   const GdrPlan pl = plan_gated_delta(a.batch, a.seqlen, a.nkheads, a.nheads, a.headdim, a.dstate, a.in_bf16, false);
   if (pl.recurrent) return launch_gated_delta_recurrent(a, stream);
-  return launch_chunks(a, gdr_work(a.workspace, pl), pl.chunks, false, stream);
+  return launch_chunks(a, gdr_work(a.workspace, pl, a), pl, false, stream);
 }
 
 int launch_gated_delta_bwd(const GatedDeltaBwdArgs& a, void* stream) {
   const GatedDeltaArgs& f = a.f;
   const GdrPlan pl = plan_gated_delta(f.batch, f.seqlen, f.nkheads, f.nheads, f.headdim, f.dstate, f.in_bf16, true);
-  const GdrWork ws = gdr_work(f.workspace, pl);
+  const GdrWork ws = gdr_work(f.workspace, pl, f);
   if (pl.chunks > 0 && f.batch > 0) {
-    if (const int e = launch_chunks(f, ws, pl.chunks, true, stream)) return e;
+    if (const int e = launch_chunks(f, ws, pl, true, stream)) return e;
   }
   if (f.batch > 0) {
     if (const int e = launch_gdr_reverse(a, ws, pl.chunks, stream)) return e;

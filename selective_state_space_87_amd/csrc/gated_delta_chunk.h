@@ -21,10 +21,14 @@
 
 namespace ssm {
 
-// KEEP: the backward's pass over the chunks, which leaves the entering states
-// and E in the workspace and no y (neither Q nor Pm is touched).
-template <int NP, bool BF16, bool OB16, int NPAIR, bool KEEP>
+// What a walk is for: y; the backward's entering states and E, left in the
+// workspace; or a segment's map (see gdr_segments.hip). The last two touch
+// neither Q nor Pm.
+enum GdrMode { kGdrForward, kGdrKeep, kGdrMap };
+
+template <int NP, bool BF16, bool OB16, int NPAIR, int MODE>
 struct GdrWalk {
+  static constexpr bool KEEP = MODE != kGdrForward;
   static constexpr int RAW = BF16 ? 1 : 2;
   static constexpr int OP = OB16 ? 1 : 2;               // halves in the products that only y sees
   // Waves for y and the loads: one for every 32 steps of a slice. (KEEP with
@@ -56,11 +60,13 @@ struct GdrWalk {
   static constexpr int NFL = (4 * kGdrC + NL - 1) / NL;
 };
 
-template <int NP, bool BF16, bool OB16, int NPAIR, bool KEEP>
-__global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gdr_chunk_kernel(const GatedDeltaArgs p,
+template <int NP, bool BF16, bool OB16, int NPAIR, int MODE>
+__global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, MODE>::NT)) void gdr_chunk_kernel(const GatedDeltaArgs p,
                                                                                              const GdrWork ws,
-                                                                                             int chunks) {
-  using W = GdrWalk<NP, BF16, OB16, NPAIR, KEEP>;
+                                                                                             int chunks, int segs,
+                                                                                             int seg_chunks) {
+  using W = GdrWalk<NP, BF16, OB16, NPAIR, MODE>;
+  constexpr bool KEEP = W::KEEP;
   constexpr int RAW = W::RAW, OP = W::OP;
   constexpr int kLo = kGdrC * NP;                       // from an element's hi half to its lo half
   constexpr int NJ = NP / 32, NK = NP / 64;             // state tiles and operand pieces of a wave
@@ -74,15 +80,23 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int H = static_cast<int>(p.nheads), G = static_cast<int>(p.nkheads);
   const int N = static_cast<int>(p.dstate), P = static_cast<int>(p.headdim);
-  const int pblocks = (P + 16 * NPAIR - 1) / (16 * NPAIR);
-  const int bh = static_cast<int>(blockIdx.x) / pblocks;
+  const int cols = MODE == kGdrMap ? P + N : P;  // a map's columns: a state from zero, then the unit vectors
+  const int pblocks = (cols + 16 * NPAIR - 1) / (16 * NPAIR);
+  const int walk_id = static_cast<int>(blockIdx.x) / pblocks;
+  const int bh = walk_id / segs, z = walk_id % segs;
   const int b = bh / H, h = bh % H, kh = h / (H / G);
   const int col0 = (static_cast<int>(blockIdx.x) % pblocks) * 16 * NPAIR;
-  const int64_t L = p.seqlen;
-  const int64_t len = gdr_row_steps(p.seqlens, b, L);
+  // The segment: steps from `first` on, at most seg_chunks chunks.
+  const int64_t first = static_cast<int64_t>(z) * seg_chunks * kGdrC, most = static_cast<int64_t>(seg_chunks) * kGdrC;
+  const int64_t row_len = gdr_row_steps(p.seqlens, b, p.seqlen);
+  const bool last_seg = row_len <= first + most && (row_len > first || z == 0);
+  if (MODE == kGdrMap && (row_len <= first + most || (z == 0 && col0 >= P))) return;  // nothing follows; a known state
+  const int64_t len = row_len <= first ? 0 : (row_len - first < most ? row_len - first : most);
+  const int64_t L = p.seqlen - first < most ? p.seqlen - first : most;
   const int n_chunks = static_cast<int>((len + kGdrC - 1) / kGdrC);
-  const int64_t row_b = static_cast<int64_t>(b) * L;
-  const int64_t item0 = static_cast<int64_t>(bh) * chunks, kv0 = (static_cast<int64_t>(b) * G + kh) * chunks;
+  const int64_t row_b = static_cast<int64_t>(b) * p.seqlen + first;
+  const int64_t item0 = static_cast<int64_t>(bh) * chunks + z * seg_chunks;
+  const int64_t kv0 = (static_cast<int64_t>(b) * G + kh) * chunks + z * seg_chunks;
   const uint32_t yrow = static_cast<uint32_t>(H * P);
 
   // A phase ends with a barrier, three a chunk: R is there; w E and E are
@@ -99,6 +113,7 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
     const int col = col0 + 16 * pr + m;
     const bool col_ok = col < P;
     const int64_t sb = (static_cast<int64_t>(bh) * P + (col_ok ? col : 0)) * N;
+    const float* enters = z == 0 ? p.h0 : (MODE == kGdrMap ? nullptr : ws.seg + static_cast<int64_t>(z - 1) * ws.seg_stride);
     _Float16* const xh = reinterpret_cast<_Float16*>(xch[pr]);
     float* const xf = reinterpret_cast<float*>(xh + W::kXF);
     float *const xs_f = xf, *const xd_f = xf + 128, *const xe_f = xf + 256, *const xr_f = xf + 384;
@@ -117,7 +132,8 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int n = n0 + 32 * (j / 2) + 8 * g + 4 * (j & 1) + i;
-        S[j][i] = (p.h0 != nullptr && col_ok && n < N) ? p.h0[sb + n] : 0.0f;
+        S[j][i] = (enters != nullptr && col_ok && n < N) ? enters[sb + n] : 0.0f;
+        if (MODE == kGdrMap && col == P + n) S[j][i] = 1.0f;
       }
     }
     // The wave's rows of V, a chunk ahead. (No load of a next chunk stands in a
@@ -168,7 +184,7 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
       for (int i = 0; i < 8; ++i) v[i] = bits_to_f32<BF16>(vr[i]);
       const bool more = c + 1 < n_chunks;
       fetch_v(more ? c + 1 : c);
-      if constexpr (KEEP) {
+      if constexpr (MODE == kGdrKeep) {
         const int64_t item = item0 + c;
         if (col_ok) {
           float* dst = ws.S + (item * P + col) * N;
@@ -326,7 +342,7 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
       if (more) split_S();
       __syncthreads();
       if constexpr (W::NBUF == 1) __syncthreads();
-      if constexpr (KEEP) {
+      if constexpr (MODE == kGdrKeep) {
         const int64_t item = item0 + c;
         float* dst = ws.E + item * kGdrC * P;
 #pragma unroll
@@ -338,14 +354,16 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
       }
     }
     if (W::kLag && !lag) __syncthreads();
-    if constexpr (!KEEP) {
-      if (p.h_final != nullptr && col_ok) {
+    if constexpr (MODE != kGdrKeep) {
+      float* out = MODE == kGdrMap ? ws.map + (static_cast<int64_t>(walk_id) * cols + (col < cols ? col : 0)) * N
+                                   : (p.h_final != nullptr && last_seg ? p.h_final + sb : nullptr);
+      if (out != nullptr && col < cols) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int n = n0 + 32 * (j / 2) + 8 * g + 4 * (j & 1) + i;
-            if (n < N) p.h_final[sb + n] = S[j][i];
+            if (n < N) out[n] = S[j][i];
           }
         }
       }
@@ -612,36 +630,47 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, KEEP>::NT)) void gd
   }
 }
 
-template <int NP, bool BF16, bool OB16, bool KEEP>
-void gdr_launch_chunk_pairs(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, hipStream_t st) {
-  const int64_t bh = a.batch * a.nheads;
-  const int64_t slices = (a.headdim + 15) / 16;
-  const int pairs = gdr_block_pairs(bh, slices);
-  const auto blocks = [&](int n) { return static_cast<unsigned>(bh * ((slices + n - 1) / n)); };
-  using W4 = GdrWalk<NP, BF16, OB16, 4, KEEP>;
+template <int NP, bool BF16, bool OB16, int MODE>
+void gdr_launch_chunk_pairs(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, int segs, int seg_chunks,
+                            hipStream_t st) {
+  const int64_t walks = a.batch * a.nheads * segs;
+  const int64_t slices = (a.headdim + (MODE == kGdrMap ? a.dstate : 0) + 15) / 16;
+  const int pairs = gdr_block_pairs(walks, slices);
+  const auto blocks = [&](int n) { return static_cast<unsigned>(walks * ((slices + n - 1) / n)); };
+  using W4 = GdrWalk<NP, BF16, OB16, 4, MODE>;
   if constexpr (W4::kFits) {
     if (pairs == 4) {
-      gdr_chunk_kernel<NP, BF16, OB16, 4, KEEP><<<blocks(4), W4::NT, 0, st>>>(a, ws, chunks);
+      gdr_chunk_kernel<NP, BF16, OB16, 4, MODE><<<blocks(4), W4::NT, 0, st>>>(a, ws, chunks, segs, seg_chunks);
       return;
     }
   }
   if (pairs == 1) {
-    gdr_chunk_kernel<NP, BF16, OB16, 1, KEEP><<<blocks(1), GdrWalk<NP, BF16, OB16, 1, KEEP>::NT, 0, st>>>(a, ws, chunks);
+    gdr_chunk_kernel<NP, BF16, OB16, 1, MODE>
+        <<<blocks(1), GdrWalk<NP, BF16, OB16, 1, MODE>::NT, 0, st>>>(a, ws, chunks, segs, seg_chunks);
   } else {
-    gdr_chunk_kernel<NP, BF16, OB16, 2, KEEP><<<blocks(2), GdrWalk<NP, BF16, OB16, 2, KEEP>::NT, 0, st>>>(a, ws, chunks);
+    gdr_chunk_kernel<NP, BF16, OB16, 2, MODE>
+        <<<blocks(2), GdrWalk<NP, BF16, OB16, 2, MODE>::NT, 0, st>>>(a, ws, chunks, segs, seg_chunks);
   }
 }
 
 template <bool BF16>
-int gdr_launch_chunk(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, bool backward, hipStream_t st) {
+int gdr_launch_chunk(const GatedDeltaArgs& a, const GdrWork& ws, const GdrPlan& pl, bool backward, hipStream_t st) {
+  const int chunks = static_cast<int>(pl.chunks), segs = static_cast<int>(pl.segs);
+  const int seg_chunks = static_cast<int>(pl.seg_chunks);
   const auto types = [&](auto np) {
     constexpr int NP = decltype(np)::value;
     if (backward) {
-      gdr_launch_chunk_pairs<NP, BF16, true, true>(a, ws, chunks, st);
-    } else if (a.out_bf16) {
-      gdr_launch_chunk_pairs<NP, BF16, true, false>(a, ws, chunks, st);
+      gdr_launch_chunk_pairs<NP, BF16, true, kGdrKeep>(a, ws, chunks, 1, chunks, st);
+      return;
+    }
+    if (segs > 1) {
+      gdr_launch_chunk_pairs<NP, BF16, true, kGdrMap>(a, ws, chunks, segs, seg_chunks, st);
+      launch_gdr_join(a, ws, segs, seg_chunks, st);
+    }
+    if (a.out_bf16) {
+      gdr_launch_chunk_pairs<NP, BF16, true, kGdrForward>(a, ws, chunks, segs, seg_chunks, st);
     } else {
-      gdr_launch_chunk_pairs<NP, BF16, false, false>(a, ws, chunks, st);
+      gdr_launch_chunk_pairs<NP, BF16, false, kGdrForward>(a, ws, chunks, segs, seg_chunks, st);
     }
   };
   if (a.dstate <= 64) {

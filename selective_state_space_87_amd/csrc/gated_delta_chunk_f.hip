@@ -3,8 +3,8 @@
 
 namespace ssm {
 
-int launch_gdr_chunk_f(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, void* stream) {
-  return gdr_launch_chunk<false>(a, ws, static_cast<int>(chunks), backward, static_cast<hipStream_t>(stream));
+int launch_gdr_chunk_f(const GatedDeltaArgs& a, const GdrWork& ws, const GdrPlan& pl, bool backward, void* stream) {
+  return gdr_launch_chunk<false>(a, ws, pl, backward, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace ssm

@@ -216,6 +216,9 @@ struct GdrWork {  // device pointers into the workspace
   float* E;       // [items][64][P]
   float* top;     // [items][kGdrMaxima][kGdrMaxSlots]
   float* part;    // [2][items]: an item's part of dA and of ddt_bias
+  float* map;     // [heads][segments][P + N][N]: a segment's map (forward in segments)
+  float* seg;     // [segments - 1][heads][P][N]: state entering segment z + 1
+  int64_t seg_stride;  // elements from one segment's states to the next's
 };
 
 // Pieces of an upper triangle: (0,0) (0,1) (1,0) (1,1) (2,1) (3,1).
@@ -331,8 +334,9 @@ inline int gdr_block_pairs(int64_t heads, int64_t slices) {
 // 16-byte boundary and N is a multiple of 8.
 int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, int out_lo, bool backward, bool vec,
                     void* stream);
-int launch_gdr_chunk_b(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, void* stream);
-int launch_gdr_chunk_f(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, void* stream);
+int launch_gdr_chunk_b(const GatedDeltaArgs& a, const GdrWork& ws, const GdrPlan& pl, bool backward, void* stream);
+int launch_gdr_chunk_f(const GatedDeltaArgs& a, const GdrWork& ws, const GdrPlan& pl, bool backward, void* stream);
+void launch_gdr_join(const GatedDeltaArgs& a, const GdrWork& ws, int segs, int seg_chunks, hipStream_t st);
 int launch_gdr_reverse(const GatedDeltaBwdArgs& a, const GdrWork& ws, int64_t chunks, void* stream);
 int launch_gdr_grads(const GatedDeltaBwdArgs& a, const GdrWork& ws, int64_t chunks, void* stream);
 

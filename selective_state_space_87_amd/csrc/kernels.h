@@ -284,12 +284,25 @@ __attribute__((weak)) int launch_rms_norm_bwd(const RmsNormBwdArgs& a, void* str
 struct GdrPlan {
   bool recurrent;
   int64_t chunks;  // per batch row
+  // Forward of few heads and many chunks: `segs` segments of seg_chunks chunks,
+  // walked at the same time from states that a pass before has found.
+  int64_t segs, seg_chunks;
+  size_t off_map, off_seg;
   size_t off_t, off_p, off_k, off_q, off_fac;
   size_t off_tt, off_s, off_x, off_e, off_top, off_part;  // backward only
   size_t bytes;
 };
 // Up to this length the recurrence is taken.
 constexpr int64_t kGdrRecurrentSteps = 16;
+// Segments: with at most kGdrFewSlices slices of 16 columns (batch, heads and
+// head size together) the walks of whole sequences leave most of the device
+// idle, and finding the segments' states first (a pass over P + N columns in
+// place of P) costs less than it gives. As many segments as make
+// kGdrManySlices slices, 4 to 32, of at least kGdrSegChunks chunks. Measured
+// (bf16, N = P = 128, whole -> in segments): 1 head of 65536 steps 1761 -> 281
+// us, 8 heads 2109 -> 830, 16 heads (128 slices) 2273 -> 1345; 4 heads of 4096
+// steps 129 -> 88, 2 of 2048 74 -> 63 (in two segments 80).
+constexpr int64_t kGdrFewSlices = 128, kGdrManySlices = 1024, kGdrSegChunks = 8, kGdrMinSegs = 4, kGdrMaxSegs = 32;
 GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, int64_t headdim,
                          int64_t dstate, int in_bf16, bool backward);
 size_t gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,

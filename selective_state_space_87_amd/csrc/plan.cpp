@@ -143,6 +143,10 @@ GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t
   p.recurrent = !backward && (seqlen <= kGdrRecurrentSteps || batch == 0 || nheads == 0);
   if (p.recurrent) return p;
   p.chunks = ceil_div(seqlen, 64);
+  if (p.chunks == 0 || batch == 0 || nheads == 0) {  // (backward of nothing)
+    p.segs = p.seg_chunks = 1;
+    return p;
+  }
   const size_t items = static_cast<size_t>(batch * nheads * p.chunks);
   constexpr size_t kPieces = 6 * 2 * 64 * 8 * 2;  // bytes of T's (or the weights') halves a chunk
   size_t at = 0;
@@ -159,6 +163,21 @@ GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t
   p.off_k = take_n(kv_items, kv);
   p.off_q = take_n(kv_items, kv);
   p.off_fac = take(9 * 64 * 4);
+  p.segs = 1;
+  const int64_t slices = batch * nheads * ceil_div(headdim, 16);
+  if (!backward && slices <= kGdrFewSlices) {
+    int64_t n = kGdrManySlices / slices;
+    if (n > kGdrMaxSegs) n = kGdrMaxSegs;
+    if (n > p.chunks / kGdrSegChunks) n = p.chunks / kGdrSegChunks;
+    if (n >= kGdrMinSegs) p.segs = n;
+  }
+  p.seg_chunks = ceil_div(p.chunks, p.segs);
+  p.segs = ceil_div(p.chunks, p.seg_chunks);
+  if (p.segs > 1) {
+    const size_t heads = static_cast<size_t>(batch * nheads);
+    p.off_map = take_n(heads * static_cast<size_t>(p.segs), static_cast<size_t>((headdim + dstate) * dstate) * 4);
+    p.off_seg = take_n(heads * static_cast<size_t>(p.segs - 1), static_cast<size_t>(headdim * dstate) * 4);
+  }
   if (backward) {
     const size_t state = static_cast<size_t>(headdim * dstate) * 4;
     p.off_tt = take(kPieces);

@@ -281,6 +281,23 @@ def test_side_stream_and_captured_forward():
     close("captured h", h, href)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L,G,H,N,P,lens", [(2048, 1, 1, 32, 16, None), (2100, 1, 2, 64, 40, None),
+                                            (4200, 1, 1, 100, 16, None), (4096, 1, 1, 16, 33, [4096, 2049, 0]),
+                                            (3300, 1, 1, 16, 16, [1, 2048, 2112, 3299])])
+def test_long_sequences_of_few_heads(L, G, H, N, P, lens, dtype):
+    """Walked in segments whose entering states are found first. Slow decays, so
+    that what enters a segment matters to its end."""
+    B = 1 if lens is None else len(lens)
+    p = problem(B, L, G, H, N, P, dtype, 17)
+    p["dt_bias"] = torch.full((H,), -7.0, device="cuda")
+    seq = None if lens is None else torch.tensor(lens, dtype=torch.int32)
+    ref, href = oracle_fwd(p, seqlens=None if seq is None else seq.numpy())
+    y, h = run(p, out_dtype=torch.float32, seqlens=None if seq is None else seq.cuda())
+    close(f"segments {(L, G, H, N, P)} {dtype} y", y, ref, tol=2 * TOL)   # the map's products and the walk's
+    close(f"segments {(L, G, H, N, P)} {dtype} h", h, href, tol=2 * TOL)
+
+
 def test_refusals():
     p = problem(1, 8, 2, 4, 16, 8, "f32", 16)
     with pytest.raises(ValueError):
