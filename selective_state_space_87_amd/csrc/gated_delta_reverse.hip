@@ -5,10 +5,12 @@
 //   X' = e^(c_end) X + Q^T (qf dY) - K^T (kf dE)
 // the mirror image of the forward's walk, and split the same way: a pair of
 // waves owns 16 columns of X in registers; wave r takes steps 32 r .. + 31 of
-// the first two lines and half r of the N rows of the third. Through LDS go X
-// (both ways), dY and U of the last 32 steps (to the wave of the first), and
-// the third line's operands. X is left in the workspace for every chunk (the
-// gradient of its leaving state), dE in dv.
+// K X and of the second line, and half r of the N rows of the third. Through
+// LDS go X (both ways), U of the last 32 steps (to the wave of the first) and
+// kf dE (both ways). What does not depend on X is made by two more waves a
+// pair, a chunk ahead: Pm^T dY and Q^T (qf dY), which the state's waves add from
+// LDS, and all loads. X is left in the workspace for every chunk (the gradient
+// of its leaving state), dE in dv.
 #include <hip/hip_runtime.h>
 
 #include "gdr_mma.h"
@@ -19,33 +21,40 @@ namespace {
 
 template <int NP, bool BF16, int NPAIR>
 struct GdrBack {
-  static constexpr int NT = 128 * NPAIR;
+  static constexpr int NT = 256 * NPAIR;
+  static constexpr int NL = 128 * NPAIR;                // threads that load
   static constexpr int RAW = BF16 ? 1 : 2;
   static constexpr int kMat = RAW * kGdrC * NP;
-  static constexpr int kFac = 4 * kGdrC;                // K, Q, W, P factors
-  static constexpr int kBufBytes = 2 * kMat * 2 + kFac * 4;
-  // a pair's exchange, in halves: X (NP / 32 pieces), dY, U, (qf dY and kf dE of either wave); then scales
-  static constexpr int kXX = 0, kXY = kXX + NP / 32 * 2 * kGdrFragHalves, kXU = kXY + 2 * kGdrFragHalves;
-  static constexpr int kXD = kXU + 2 * kGdrFragHalves, kXF = kXD + 8 * kGdrFragHalves;
-  static constexpr int kPairBytes = kXF * 2 + 6 * 64 * 4;
-  static constexpr int NBUF = 2 * kBufBytes + NPAIR * kPairBytes <= 160 * 1024 ? 2 : 1;
-  static constexpr int NKQ = kMat / 8 / NT;
-  static constexpr int NFL = (4 * kGdrC + NT - 1) / NT;
+  static constexpr int kTri = kGdrPieceHalves;
+  static constexpr int kFac = 4 * kGdrC + 4;            // K, Q, W, P factors; the end's and T's
+  static constexpr int kBufBytes = 2 * kMat * 2;
+  // a pair's exchange, in halves: X (NP / 32 pieces), U, kf dE of either wave;
+  // then floats: Pm^T dY (4 tiles), Q^T (qf dY) (NP / 16 tiles), scales
+  static constexpr int kXX = 0, kXU = kXX + NP / 32 * 2 * kGdrFragHalves, kXB = kXU + 2 * kGdrFragHalves;
+  static constexpr int kXH = kXB + 4 * kGdrFragHalves;
+  static constexpr int kFY = 0, kFQ = kFY + 4 * 256, kFS = kFQ + NP / 16 * 256;
+  static constexpr int kPairBytes = kXH * 2 + (kFS + 5 * 64) * 4;
+  static constexpr int kFixed = kTri * 2 + 2 * kFac * 4 + NPAIR * kPairBytes;
+  static constexpr int NBUF = 2 * kBufBytes + kFixed <= 160 * 1024 ? 2 : 1;
+  static constexpr int NKQ = kMat / 8 / NL;
+  static constexpr int NTL = kTri / 8 / NL;
+  static constexpr int NFL = (4 * kGdrC + NL - 1) / NL;
 };
 
 template <int NP, bool BF16, int NPAIR>
-__global__ __launch_bounds__(128 * NPAIR, NPAIR == 4 ? 2 : 1) void gdr_reverse_kernel(const GatedDeltaBwdArgs a,
-                                                                                      const GdrWork ws, int chunks) {
+__global__ __launch_bounds__(256 * NPAIR) void gdr_reverse_kernel(const GatedDeltaBwdArgs a, const GdrWork ws, int chunks) {
   using W = GdrBack<NP, BF16, NPAIR>;
-  constexpr int NT = W::NT, RAW = W::RAW, NJ = NP / 32, NK = NP / 64;
+  constexpr int RAW = W::RAW, NJ = NP / 32, NK = NP / 64;
   constexpr int kLo = kGdrC * NP;
   __shared__ __align__(16) char lds[W::NBUF][W::kBufBytes];
+  __shared__ __align__(16) _Float16 sT[W::kTri];
+  __shared__ __align__(16) float sFac[2][W::kFac];
   __shared__ __align__(16) char xch[NPAIR][W::kPairBytes];
   const GatedDeltaArgs& p = a.f;
 
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int pr = w >> 1, r = w & 1;
+  const int pr = (w >> 1) % NPAIR, r = w & 1;
   const int H = static_cast<int>(p.nheads), G = static_cast<int>(p.nkheads);
   const int N = static_cast<int>(p.dstate), P = static_cast<int>(p.headdim);
   const int pblocks = (P + 16 * NPAIR - 1) / (16 * NPAIR);
@@ -60,343 +69,400 @@ __global__ __launch_bounds__(128 * NPAIR, NPAIR == 4 ? 2 : 1) void gdr_reverse_k
   const int64_t item0 = static_cast<int64_t>(bh) * chunks, kv0 = (static_cast<int64_t>(b) * G + kh) * chunks;
   const int64_t sb = (static_cast<int64_t>(bh) * P + (col_ok ? col : 0)) * N;
   const uint32_t yrow = static_cast<uint32_t>(H * P);
+  // Byte offset of element (4 g, col) of a chunk of dY or dV; past any buffer where there is no column.
+  const uint32_t ybase = col_ok ? (static_cast<uint32_t>(4 * g) * yrow + static_cast<uint32_t>(col)) * 4 : 0x80000000u;
 
   _Float16* const xh = reinterpret_cast<_Float16*>(xch[pr]);
-  float* const xf = reinterpret_cast<float*>(xh + W::kXF);
-  float *const xx_f = xf, *const xy_f = xf + 128, *const xu_f = xf + 192, *const xd_f = xf + 256;
+  float* const xf = reinterpret_cast<float*>(xh + W::kXH);
+  float *const xx_f = xf + W::kFS, *const xu_f = xx_f + 128, *const xb_f = xx_f + 192;
   const auto piece = [&](int at, int q, int half) __attribute__((always_inline)) {
     return reinterpret_cast<half8_t*>(xh + at + (2 * q + half) * kGdrFragHalves + lane * 8);
   };
-
-  const int n0 = r * (NP / 2);
-  f32x4_t X[NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + 32 * (j / 2) + 8 * g + 4 * (j & 1) + i;
-      X[j][i] = (a.dh_final != nullptr && col_ok && n < N) ? a.dh_final[sb + n] : 0.0f;
-    }
-  }
-
-  u32x4_t kr[W::NKQ], qr[W::NKQ];
-  float fr[W::NFL], yr[8];
-  float fend = 0.0f, ftri = 0.0f, fend_next = 0.0f, ftri_next = 0.0f;
-  half8_t Td[2][2], To[2][2], Pd[2][2], Po[2][2];  // pieces on the diagonal, and right of it (wave 0)
-
-  // (No load of the next chunk stands in a branch: it would be waited for
-  // where the branches join.)
-  auto fetch = [&](int c) __attribute__((always_inline)) {
-    const int64_t t0 = static_cast<int64_t>(c) * kGdrC;
-    const int rows = static_cast<int>(len - t0 < kGdrC ? len - t0 : kGdrC);
-    const rsrc_t ry = rows_buffer<4>(a.dy, (row_b + t0) * yrow + static_cast<int64_t>(h) * P, rows, yrow, P);
-    const float* fac = ws.fac + (item0 + c) * (kGdrFactors * kGdrC);
-    const u32x4_t* K = reinterpret_cast<const u32x4_t*>(ws.K + (kv0 + c) * W::kMat) + tid;
-    const u32x4_t* Q = reinterpret_cast<const u32x4_t*>(ws.Q + (kv0 + c) * W::kMat) + tid;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = 32 * r + 16 * (i / 4) + 4 * g + (i % 4);
-      const uint32_t off = (static_cast<uint32_t>(t) * yrow + static_cast<uint32_t>(col)) * 4;
-      yr[i] = __uint_as_float(buffer_load_bits<false>(ry, col_ok ? off : kOutOfRange));
-    }
-#pragma unroll
-    for (int i = 0; i < W::NKQ; ++i) {
-      kr[i] = K[i * NT];
-      qr[i] = Q[i * NT];
-    }
-#pragma unroll
-    for (int i = 0; i < W::NFL; ++i) {
-      const int e = i * NT + tid;
-      fr[i] = fac[kFacK * kGdrC + (4 * kGdrC % NT == 0 ? e : e % (4 * kGdrC))];
-    }
-    fend_next = fac[kFacEnd * kGdrC];
-    ftri_next = fac[kFacEnd * kGdrC + 1];
-  };
-  auto fetch_tri = [&](const _Float16* base, int c, half8_t (&d)[2][2], half8_t (&o)[2][2])
-                       __attribute__((always_inline)) {
-    const half8_t* src = reinterpret_cast<const half8_t*>(base + (item0 + c) * kGdrPieceHalves) + lane;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int fd = r == 0 ? 2 * u : 4 + u, fo = r == 0 ? 2 * u + 1 : fd;  // (wave 1 has no other: its own again)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        d[u][k] = src[(2 * fd + k) * 64];
-        o[u][k] = src[(2 * fo + k) * 64];
-      }
-    }
-  };
-  auto stage = [&](int buf) __attribute__((always_inline)) {
-    _Float16* sK = reinterpret_cast<_Float16*>(lds[buf]);
-    _Float16* sQ = sK + W::kMat;
-    float* sF = reinterpret_cast<float*>(sQ + W::kMat);
-#pragma unroll
-    for (int i = 0; i < W::NKQ; ++i) {
-      reinterpret_cast<u32x4_t*>(sK)[i * NT + tid] = kr[i];
-      reinterpret_cast<u32x4_t*>(sQ)[i * NT + tid] = qr[i];
-    }
-#pragma unroll
-    for (int i = 0; i < W::NFL; ++i) {
-      const int e = i * NT + tid;
-      if (4 * kGdrC % NT == 0 || e < 4 * kGdrC) sF[e] = fr[i];
-    }
-    fend = fend_next;
-    ftri = ftri_next;
+  const auto ftile = [&](int at, int t) __attribute__((always_inline)) {
+    return reinterpret_cast<f32x4_t*>(xf + at + t * 256 + lane * 4);
   };
 
-  half8_t Xh[NK], Xl[NK], Yh, Yl;
-  f32x4_t Y[2];
-  float x_down = 0.0f, y_down = 0.0f, xtop = 0.0f, ytop = 0.0f;
-  // X and the next chunk's dY as operands, for this wave and for the other.
-  auto split = [&]() __attribute__((always_inline)) {
-    xtop = tiles_absmax<NJ>(X);
-    const Pow2 s = pow2_to_top(xtop);
-    x_down = s.down;
-#pragma unroll
-    for (int q = 0; q < NK; ++q) {
-      tiles_to_operand<true>(X[2 * q], X[2 * q + 1], s.up, Xh[q], Xl[q]);
-      *piece(W::kXX, r * NK + q, 0) = Xh[q];
-      *piece(W::kXX, r * NK + q, 1) = Xl[q];
-    }
-    xx_f[64 * r + lane] = s.down;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) Y[i / 4][i % 4] = yr[i];
-    ytop = tiles_absmax<2>(Y);
-    const Pow2 sy = pow2_to_top(ytop);
-    y_down = sy.down;
-    tiles_to_operand<true>(Y[0], Y[1], sy.up, Yh, Yl);
-    if (r == 1) {
-      *piece(W::kXY, 0, 0) = Yh;
-      *piece(W::kXY, 0, 1) = Yl;
-      xy_f[lane] = sy.down;
-    }
-  };
-
-  if (n_chunks > 0) {
-    fetch(n_chunks - 1);
-    fetch_tri(ws.Tt, n_chunks - 1, Td, To);
-    fetch_tri(ws.Pt, n_chunks - 1, Pd, Po);
-    stage(0);
-    split();
-  }
-  __syncthreads();
-
-  for (int step = 0; step < n_chunks; ++step) {
-    const int c = n_chunks - 1 - step;
-    const int buf = W::NBUF == 2 ? (step & 1) : 0;
-    const _Float16* sK = reinterpret_cast<const _Float16*>(lds[buf]);
-    const _Float16* sQ = sK + W::kMat;
-    const float* sF = reinterpret_cast<const float*>(sQ + W::kMat);
-    const auto factor = [&](int which, int u) __attribute__((always_inline)) {
-      return *reinterpret_cast<const f32x4_t*>(sF + which * kGdrC + 32 * r + 16 * u + 4 * g);
-    };
-    const bool more = c > 0;
-    const int next = more ? c - 1 : 0;
-    fetch(next);
-
-    const int64_t item = item0 + c;
-    if (col_ok) {
-      float* dst = ws.X + (item * P + col) * N;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int n = n0 + 32 * (j / 2) + 8 * g + 4 * (j & 1);
-        if (N % 4 == 0) {
-          if (n < N) *reinterpret_cast<f32x4_t*>(dst + n) = X[j];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (n + i < N) dst[n + i] = X[j][i];
-          }
-        }
-      }
-    }
-
-    // U = Pm^T dY + diag(w) K X on the wave's 32 steps
-    half8_t Uh, Ul;
-    Pow2 su;
-    {
-      f32x4_t kx[2][2], py[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) kx[0][u] = kx[1][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int o = 0; o < 2; ++o) {
-#pragma unroll
-        for (int q = 0; q < NK; ++q) {
-          const int f = (o == 0 ? r : 1 - r) * NK + q;
-          const half8_t vh = o == 0 ? Xh[q] : *piece(W::kXX, f, 0);
-          const half8_t vl = o == 0 ? Xl[q] : *piece(W::kXX, f, 1);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int at = kq_at<NP>(32 * r + 16 * u + m, 32 * f + 8 * g);
-            const half8_t k = *reinterpret_cast<const half8_t*>(sK + at);
-            kx[o][u] = mfma16(k, vh, kx[o][u]);
-            kx[o][u] = mfma16(k, vl, kx[o][u]);
-            if constexpr (RAW == 2) kx[o][u] = mfma16(*reinterpret_cast<const half8_t*>(sK + kLo + at), vh, kx[o][u]);
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        acc = mfma16(Pd[u][0], Yh, acc);
-        acc = mfma16(Pd[u][0], Yl, acc);
-        acc = mfma16(Pd[u][1], Yh, acc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) py[u][i] = acc[i] * y_down;
-      }
-      if (r == 0) {
-        const half8_t oh = *piece(W::kXY, 0, 0), ol = *piece(W::kXY, 0, 1);
-        const float other = xy_f[lane];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-          acc = mfma16(Po[u][0], oh, acc);
-          acc = mfma16(Po[u][0], ol, acc);
-          acc = mfma16(Po[u][1], oh, acc);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) py[u][i] = fmaf(acc[i], other, py[u][i]);
-        }
-      }
-      fetch_tri(ws.Pt, next, Pd, Po);
-      const float xo_down = xx_f[64 * (1 - r) + lane];
-      f32x4_t U[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const f32x4_t fw = factor(2, u), fp = factor(3, u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          U[u][i] = fmaf(fw[i], fmaf(kx[1][u][i], xo_down, kx[0][u][i] * x_down), fp[i] * py[u][i]);
-        }
-      }
-      su = pow2_to_top(tiles_absmax<2>(U));
-      tiles_to_operand<true>(U[0], U[1], su.up, Uh, Ul);
-      if (r == 1) {
-        *piece(W::kXU, 0, 0) = Uh;
-        *piece(W::kXU, 0, 1) = Ul;
-        xu_f[lane] = su.down;
-      }
-    }
-    __syncthreads();
-
-    // dE = T^T U
-    f32x4_t E[2];
-    {
-      const float down = su.down * ftri;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        acc = mfma16(Td[u][0], Uh, acc);
-        acc = mfma16(Td[u][0], Ul, acc);
-        acc = mfma16(Td[u][1], Uh, acc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) E[u][i] = acc[i] * down;
-      }
-      if (r == 0) {
-        const half8_t oh = *piece(W::kXU, 0, 0), ol = *piece(W::kXU, 0, 1);
-        const float other = xu_f[lane] * ftri;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-          acc = mfma16(To[u][0], oh, acc);
-          acc = mfma16(To[u][0], ol, acc);
-          acc = mfma16(To[u][1], oh, acc);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) E[u][i] = fmaf(acc[i], other, E[u][i]);
-        }
-      }
-    }
-    fetch_tri(ws.Tt, next, Td, To);
-    // qf dY and -kf dE as operands for both waves, one scale for the two so that one accumulator takes them
-    half8_t Ah, Al, Bh, Bl;
-    Pow2 sd;
-    {
-      f32x4_t A[2], B[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const f32x4_t fk = factor(0, u), fq = factor(1, u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          A[u][i] = Y[u][i] * fq[i];
-          B[u][i] = E[u][i] * -fk[i];
-        }
-      }
-      sd = pow2_to_top(fmaxf(tiles_absmax<2>(A), tiles_absmax<2>(B)));
-      tiles_to_operand<true>(A[0], A[1], sd.up, Ah, Al);
-      tiles_to_operand<true>(B[0], B[1], sd.up, Bh, Bl);
-      *piece(W::kXD, 2 * r, 0) = Ah;
-      *piece(W::kXD, 2 * r, 1) = Al;
-      *piece(W::kXD, 2 * r + 1, 0) = Bh;
-      *piece(W::kXD, 2 * r + 1, 1) = Bl;
-      xd_f[64 * r + lane] = sd.down;
-    }
-    __syncthreads();
-
-    // X' = e^(c_end) X + Q^T (qf dY) - K^T (kf dE) on the wave's half of the rows
-    {
-      const half8_t oah = *piece(W::kXD, 2 * (1 - r), 0), oal = *piece(W::kXD, 2 * (1 - r), 1);
-      const half8_t obh = *piece(W::kXD, 2 * (1 - r) + 1, 0), obl = *piece(W::kXD, 2 * (1 - r) + 1, 1);
-      const float d_own = sd.down, d_oth = xd_f[64 * (1 - r) + lane];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        f32x4_t acc[2];
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          acc[o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-          const half8_t vah = o == 0 ? Ah : oah, val = o == 0 ? Al : oal, vbh = o == 0 ? Bh : obh, vbl = o == 0 ? Bl : obl;
-          const int at = kq_at<NP>(32 * (o == 0 ? r : 1 - r) + 4 * g + (m >> 2), n0 + 32 * (j / 2) + 8 * (m & 3)) + 4 * (j & 1);
-          const auto column = [&](const _Float16* mat) __attribute__((always_inline)) {
-            return __builtin_shufflevector(lds_column4(mat + at), lds_column4(mat + at + 16 * NP), 0, 1, 2, 3, 4, 5, 6, 7);
-          };
-          const half8_t kc = column(sK), qc = column(sQ);
-          acc[o] = mfma16(qc, vah, acc[o]);
-          acc[o] = mfma16(qc, val, acc[o]);
-          acc[o] = mfma16(kc, vbh, acc[o]);
-          acc[o] = mfma16(kc, vbl, acc[o]);
-          if constexpr (RAW == 2) {
-            acc[o] = mfma16(column(sQ + kLo), vah, acc[o]);
-            acc[o] = mfma16(column(sK + kLo), vbh, acc[o]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) X[j][i] = fmaf(acc[1][i], d_oth, fmaf(acc[0][i], d_own, fend * X[j][i]));
-      }
-    }
-    {
-      const int64_t t0 = static_cast<int64_t>(c) * kGdrC;
-      const int rows = static_cast<int>(len - t0 < kGdrC ? len - t0 : kGdrC);
-      const int out_rows = static_cast<int>(L - t0 < kGdrC ? L - t0 : kGdrC);
-      const rsrc_t rv = rows_buffer<4>(a.dv, (row_b + t0) * yrow + static_cast<int64_t>(h) * P, out_rows, yrow, P);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int t = 32 * r + 16 * (i / 4) + 4 * g + (i % 4);
-        const uint32_t off = (static_cast<uint32_t>(t) * yrow + static_cast<uint32_t>(col)) * 4;
-        buffer_store_f32<false>(t < rows ? E[i / 4][i % 4] : 0.0f, rv, col_ok ? off : kOutOfRange);
-      }
-      const float mx = lanes16_max(xtop), my = lanes16_max(ytop), me = lanes16_max(tiles_absmax<2>(E));
-      if (lane == 0 && col < P) {
-        float* top = ws.top + item * kGdrMaxima * kGdrMaxSlots + col / 16 * 2 + r;
-        top[kMaxX * kGdrMaxSlots] = mx;
-        top[kMaxDY * kGdrMaxSlots] = my;
-        top[kMaxDE * kGdrMaxSlots] = me;
-      }
-    }
-    if (more) split();
-    if constexpr (W::NBUF == 1) __syncthreads();
-    if (more) stage(W::NBUF == 2 ? ((step + 1) & 1) : 0);
-    __syncthreads();
-  }
-
-  for (int64_t t = static_cast<int64_t>(n_chunks) * kGdrC + 4 * r + g; t < L; t += 8) {
-    if (col_ok) a.dv[(row_b + t) * yrow + static_cast<int64_t>(h) * P + col] = 0.0f;
-  }
-  if (a.dh0 != nullptr && col_ok) {
+  // Step `step` walks chunk n_chunks - 1 - step. Its phases end with barriers:
+  // U is there (and T); kf dE and Q^T (qf dY) are there (and the next chunk's
+  // factors); X' and the next Pm^T dY are there. With one buffer for K and Q
+  // they come in behind the third, before a fourth.
+  if (w < 2 * NPAIR) {
+    // ---------------------------------------------------------------- X
+    const int n0 = r * (NP / 2);
+    f32x4_t X[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int n = n0 + 32 * (j / 2) + 8 * g + 4 * (j & 1) + i;
-        if (n < N) a.dh0[sb + n] = X[j][i];
+        X[j][i] = (a.dh_final != nullptr && col_ok && n < N) ? a.dh_final[sb + n] : 0.0f;
       }
     }
+    half8_t Xh[NK], Xl[NK];
+    float x_down = 0.0f, xtop = 0.0f;
+    auto split = [&]() __attribute__((always_inline)) {
+      xtop = tiles_absmax<NJ>(X);
+      const Pow2 s = pow2_to_top(xtop);
+      x_down = s.down;
+#pragma unroll
+      for (int q = 0; q < NK; ++q) {
+        tiles_to_operand<true>(X[2 * q], X[2 * q + 1], s.up, Xh[q], Xl[q]);
+        *piece(W::kXX, r * NK + q, 0) = Xh[q];
+        *piece(W::kXX, r * NK + q, 1) = Xl[q];
+      }
+      xx_f[64 * r + lane] = s.down;
+    };
+    split();
+    __syncthreads();
+    __syncthreads();
+
+    for (int step = 0; step < n_chunks; ++step) {
+      const int c = n_chunks - 1 - step;
+      const _Float16* sK = reinterpret_cast<const _Float16*>(lds[W::NBUF == 2 ? (step & 1) : 0]);
+      const float* sF = sFac[step & 1];
+      const auto factor = [&](int which, int u) __attribute__((always_inline)) {
+        return *reinterpret_cast<const f32x4_t*>(sF + which * kGdrC + 32 * r + 16 * u + 4 * g);
+      };
+      const int64_t item = item0 + c;
+      float* const tops = ws.top + item * kGdrMaxima * kGdrMaxSlots + col / 16 * 2 + r;
+      // U = Pm^T dY + diag(w) K X on the wave's 32 steps
+      half8_t Uh, Ul;
+      Pow2 su;
+      {
+        f32x4_t kx[2][2];
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) kx[o][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int q = 0; q < NK; ++q) {
+            const int f = (o == 0 ? r : 1 - r) * NK + q;
+            const half8_t vh = o == 0 ? Xh[q] : *piece(W::kXX, f, 0);
+            const half8_t vl = o == 0 ? Xl[q] : *piece(W::kXX, f, 1);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int at = kq_at<NP>(32 * r + 16 * u + m, 32 * f + 8 * g);
+              const half8_t k = *reinterpret_cast<const half8_t*>(sK + at);
+              kx[o][u] = mfma16(k, vh, kx[o][u]);
+              kx[o][u] = mfma16(k, vl, kx[o][u]);
+              if constexpr (RAW == 2) kx[o][u] = mfma16(*reinterpret_cast<const half8_t*>(sK + kLo + at), vh, kx[o][u]);
+            }
+          }
+        }
+        const float xo_down = xx_f[64 * (1 - r) + lane];
+        f32x4_t U[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const f32x4_t fw = factor(2, u), py = *ftile(W::kFY, 2 * r + u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) U[u][i] = fmaf(fw[i], fmaf(kx[1][u][i], xo_down, kx[0][u][i] * x_down), py[i]);
+        }
+        su = pow2_to_top(tiles_absmax<2>(U));
+        tiles_to_operand<true>(U[0], U[1], su.up, Uh, Ul);
+        if (r == 1) {
+          *piece(W::kXU, 0, 0) = Uh;
+          *piece(W::kXU, 0, 1) = Ul;
+          xu_f[lane] = su.down;
+        }
+      }
+      if (col_ok) {
+        float* dst = ws.X + (item * P + col) * N;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int n = n0 + 32 * (j / 2) + 8 * g + 4 * (j & 1);
+          if (N % 4 == 0) {
+            if (n < N) *reinterpret_cast<f32x4_t*>(dst + n) = X[j];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (n + i < N) dst[n + i] = X[j][i];
+            }
+          }
+        }
+      }
+      const float mx = lanes16_max(xtop);
+      if (lane == 0 && col < P) tops[kMaxX * kGdrMaxSlots] = mx;
+      __syncthreads();
+
+      // dE = T^T U
+      f32x4_t E[2];
+      {
+        const float tri = sF[4 * kGdrC + 1], down = su.down * tri;
+        const auto T = [&](int f, int half) __attribute__((always_inline)) {
+          return *reinterpret_cast<const half8_t*>(sT + (2 * f + half) * kGdrFragHalves + lane * 8);
+        };
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int f = r == 0 ? 2 * u : 4 + u;
+          const half8_t th = T(f, 0), tl = T(f, 1);
+          f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+          acc = mfma16(th, Uh, acc);
+          acc = mfma16(th, Ul, acc);
+          acc = mfma16(tl, Uh, acc);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) E[u][i] = acc[i] * down;
+        }
+        if (r == 0) {
+          const half8_t oh = *piece(W::kXU, 0, 0), ol = *piece(W::kXU, 0, 1);
+          const float other = xu_f[lane] * tri;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const half8_t th = T(2 * u + 1, 0), tl = T(2 * u + 1, 1);
+            f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            acc = mfma16(th, oh, acc);
+            acc = mfma16(th, ol, acc);
+            acc = mfma16(tl, oh, acc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) E[u][i] = fmaf(acc[i], other, E[u][i]);
+          }
+        }
+      }
+      // kf dE as an operand for both waves
+      half8_t Bh, Bl;
+      Pow2 sd;
+      {
+        f32x4_t B[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const f32x4_t fk = factor(0, u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) B[u][i] = E[u][i] * -fk[i];
+        }
+        sd = pow2_to_top(tiles_absmax<2>(B));
+        tiles_to_operand<true>(B[0], B[1], sd.up, Bh, Bl);
+        *piece(W::kXB, r, 0) = Bh;
+        *piece(W::kXB, r, 1) = Bl;
+        xb_f[64 * r + lane] = sd.down;
+      }
+      const float end = sF[4 * kGdrC];
+      __syncthreads();
+
+      // X' = e^(c_end) X + Q^T (qf dY) - K^T (kf dE) on the wave's half of the rows
+      {
+        const half8_t oh = *piece(W::kXB, 1 - r, 0), ol = *piece(W::kXB, 1 - r, 1);
+        const float d_own = sd.down, d_oth = xb_f[64 * (1 - r) + lane];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          f32x4_t acc[2];
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            acc[o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            const half8_t bh = o == 0 ? Bh : oh, bl = o == 0 ? Bl : ol;
+            const int at = kq_at<NP>(32 * (o == 0 ? r : 1 - r) + 4 * g + (m >> 2), n0 + 32 * (j / 2) + 8 * (m & 3)) + 4 * (j & 1);
+            const auto column = [&](const _Float16* mat) __attribute__((always_inline)) {
+              return __builtin_shufflevector(lds_column4(mat + at), lds_column4(mat + at + 16 * NP), 0, 1, 2, 3, 4, 5, 6, 7);
+            };
+            const half8_t kc = column(sK);
+            acc[o] = mfma16(kc, bh, acc[o]);
+            acc[o] = mfma16(kc, bl, acc[o]);
+            if constexpr (RAW == 2) acc[o] = mfma16(column(sK + kLo), bh, acc[o]);
+          }
+          const f32x4_t qa = *ftile(W::kFQ, r * NJ + j);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) X[j][i] = fmaf(acc[1][i], d_oth, fmaf(acc[0][i], d_own, fmaf(end, X[j][i], qa[i])));
+        }
+      }
+      if (step + 1 < n_chunks) split();
+      {
+        const int64_t t0 = static_cast<int64_t>(c) * kGdrC;
+        const int rows = static_cast<int>(len - t0 < kGdrC ? len - t0 : kGdrC);
+        const int out_rows = static_cast<int>(L - t0 < kGdrC ? L - t0 : kGdrC);
+        const rsrc_t rv = rows_buffer<4>(a.dv, (row_b + t0) * yrow + static_cast<int64_t>(h) * P, out_rows, yrow, P);
+        const float me = lanes16_max(tiles_absmax<2>(E));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int t = 32 * r + 16 * (i / 4) + (i % 4);
+          buffer_store_f32<false>(t + 4 * g < rows ? E[i / 4][i % 4] : 0.0f, rv, ybase + static_cast<uint32_t>(t) * yrow * 4);
+        }
+        if (lane == 0 && col < P) tops[kMaxDE * kGdrMaxSlots] = me;
+      }
+      __syncthreads();
+      if constexpr (W::NBUF == 1) __syncthreads();
+    }
+    if (a.dh0 != nullptr && col_ok) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = n0 + 32 * (j / 2) + 8 * g + 4 * (j & 1) + i;
+          if (n < N) a.dh0[sb + n] = X[j][i];
+        }
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------- loads, Pm^T dY and Q^T (qf dY)
+  const int ltid = tid - 128 * NPAIR;
+  const int n0 = r * (NP / 2);
+  u32x4_t kr[W::NKQ], qr[W::NKQ], tr[W::NTL];
+  float fr[W::NFL], yr[16];
+  f32x2_t fe;
+  half8_t Pd[2][2], Po[2][2], Ah[2], Al[2];
+  float a_down = 0.0f;
+  // (A load in no branch: it would be waited for where the branches join.)
+  auto fetch_kq = [&](int c) __attribute__((always_inline)) {
+    const u32x4_t* K = reinterpret_cast<const u32x4_t*>(ws.K + (kv0 + c) * W::kMat) + ltid;
+    const u32x4_t* Q = reinterpret_cast<const u32x4_t*>(ws.Q + (kv0 + c) * W::kMat) + ltid;
+#pragma unroll
+    for (int i = 0; i < W::NKQ; ++i) {
+      kr[i] = K[i * W::NL];
+      qr[i] = Q[i * W::NL];
+    }
+  };
+  auto fetch_T = [&](int c) __attribute__((always_inline)) {
+    const u32x4_t* T = reinterpret_cast<const u32x4_t*>(ws.Tt + (item0 + c) * kGdrPieceHalves) + ltid;
+#pragma unroll
+    for (int i = 0; i < W::NTL; ++i) tr[i] = T[i * W::NL];
+  };
+  auto fetch_fac = [&](int c) __attribute__((always_inline)) {
+    const float* fac = ws.fac + (item0 + c) * (kGdrFactors * kGdrC);
+#pragma unroll
+    for (int i = 0; i < W::NFL; ++i) fr[i] = fac[kFacK * kGdrC + (i * W::NL + ltid) % (4 * kGdrC)];
+    fe = *reinterpret_cast<const f32x2_t*>(fac + kFacEnd * kGdrC);
+  };
+  // dY's rows, and the pieces of Pm^T for row tiles 2 r, 2 r + 1.
+  auto fetch_y = [&](int c) __attribute__((always_inline)) {
+    const int64_t t0 = static_cast<int64_t>(c) * kGdrC;
+    const int rows = static_cast<int>(len - t0 < kGdrC ? len - t0 : kGdrC);
+    const rsrc_t ry = rows_buffer<4>(a.dy, (row_b + t0) * yrow + static_cast<int64_t>(h) * P, rows, yrow, P);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      yr[i] = __uint_as_float(buffer_load_bits<false>(ry, ybase + static_cast<uint32_t>(16 * (i / 4) + (i % 4)) * yrow * 4));
+    }
+    const half8_t* src = reinterpret_cast<const half8_t*>(ws.Pt + (item0 + c) * kGdrPieceHalves) + lane;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int fd = r == 0 ? 2 * u : 4 + u, fo = r == 0 ? 2 * u + 1 : fd;  // (wave 1 has no other: its own again)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        Pd[u][k] = src[(2 * fd + k) * 64];
+        Po[u][k] = src[(2 * fo + k) * 64];
+      }
+    }
+  };
+  auto stage_kq = [&](int buf) __attribute__((always_inline)) {
+    u32x4_t* sK = reinterpret_cast<u32x4_t*>(lds[buf]);
+#pragma unroll
+    for (int i = 0; i < W::NKQ; ++i) {
+      sK[i * W::NL + ltid] = kr[i];
+      sK[W::kMat / 8 + i * W::NL + ltid] = qr[i];
+    }
+  };
+  auto stage_T = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < W::NTL; ++i) reinterpret_cast<u32x4_t*>(sT)[i * W::NL + ltid] = tr[i];
+  };
+  auto stage_fac = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < W::NFL; ++i) {
+      const int e = i * W::NL + ltid;
+      if (4 * kGdrC % W::NL == 0 || e < 4 * kGdrC) sFac[buf][e] = fr[i];
+    }
+    if (ltid == 0) *reinterpret_cast<f32x2_t*>(&sFac[buf][4 * kGdrC]) = fe;
+  };
+  // Pm^T dY of chunk c into LDS, qf dY as an operand into registers.
+  auto from_y = [&](int c, int buf) __attribute__((always_inline)) {
+    const float* sF = sFac[buf];
+    f32x4_t Y[4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) Y[i / 4][i % 4] = yr[i];
+    const float ytop = tiles_absmax<4>(Y);
+    const Pow2 sy = pow2_to_top(ytop);
+    half8_t Yh[2], Yl[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) tiles_to_operand<true>(Y[2 * q], Y[2 * q + 1], sy.up, Yh[q], Yl[q]);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      const half8_t oh = r == 0 ? Yh[0] : Yh[1], ol = r == 0 ? Yl[0] : Yl[1];
+      acc = mfma16(Pd[u][0], oh, acc);
+      acc = mfma16(Pd[u][0], ol, acc);
+      acc = mfma16(Pd[u][1], oh, acc);
+      if (r == 0) {
+        acc = mfma16(Po[u][0], Yh[1], acc);
+        acc = mfma16(Po[u][0], Yl[1], acc);
+        acc = mfma16(Po[u][1], Yh[1], acc);
+      }
+      const f32x4_t fp = *reinterpret_cast<const f32x4_t*>(sF + 3 * kGdrC + 32 * r + 16 * u + 4 * g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] *= fp[i] * sy.down;
+      *ftile(W::kFY, 2 * r + u) = acc;
+    }
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+      const f32x4_t fq = *reinterpret_cast<const f32x4_t*>(sF + 1 * kGdrC + 16 * tt + 4 * g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) Y[tt][i] *= fq[i];
+    }
+    const Pow2 sa = pow2_to_top(tiles_absmax<4>(Y));
+    a_down = sa.down;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) tiles_to_operand<true>(Y[2 * q], Y[2 * q + 1], sa.up, Ah[q], Al[q]);
+    const float my = lanes16_max(ytop);
+    if (lane == 0 && col < P) {
+      ws.top[((item0 + c) * kGdrMaxima + kMaxDY) * kGdrMaxSlots + col / 16 * 2 + r] = my;
+    }
+  };
+  const auto chunk_at = [&](int step) { return step < n_chunks ? n_chunks - 1 - step : 0; };
+  if (n_chunks > 0) {
+    fetch_fac(chunk_at(0));
+    fetch_kq(chunk_at(0));
+    fetch_y(chunk_at(0));
+    fetch_T(chunk_at(0));
+    stage_fac(0);
+    stage_kq(0);
+    fetch_fac(chunk_at(1));
+    fetch_kq(chunk_at(1));
+  }
+  __syncthreads();  // (the factors, for the first Pm^T dY)
+  if (n_chunks > 0) {
+    from_y(chunk_at(0), 0);
+    fetch_y(chunk_at(1));
+  }
+  __syncthreads();
+  for (int step = 0; step < n_chunks; ++step) {
+    const _Float16* sQ = reinterpret_cast<const _Float16*>(lds[W::NBUF == 2 ? (step & 1) : 0]) + W::kMat;
+    stage_T();
+    // Q^T (qf dY) on half r of the rows of X
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int at = kq_at<NP>(32 * q + 4 * g + (m >> 2), n0 + 32 * (j / 2) + 8 * (m & 3)) + 4 * (j & 1);
+        const auto column = [&](const _Float16* mat) __attribute__((always_inline)) {
+          return __builtin_shufflevector(lds_column4(mat + at), lds_column4(mat + at + 16 * NP), 0, 1, 2, 3, 4, 5, 6, 7);
+        };
+        const half8_t qc = column(sQ);
+        acc = mfma16(qc, Ah[q], acc);
+        acc = mfma16(qc, Al[q], acc);
+        if constexpr (RAW == 2) acc = mfma16(column(sQ + kLo), Ah[q], acc);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] *= a_down;
+      *ftile(W::kFQ, r * NJ + j) = acc;
+    }
+    __syncthreads();
+    stage_fac((step + 1) & 1);
+    fetch_fac(chunk_at(step + 2));
+    if constexpr (W::NBUF == 2) {
+      stage_kq((step + 1) & 1);
+      fetch_kq(chunk_at(step + 2));
+    }
+    fetch_T(chunk_at(step + 1));
+    __syncthreads();
+    if (step + 1 < n_chunks) from_y(chunk_at(step + 1), (step + 1) & 1);
+    fetch_y(chunk_at(step + 2));
+    __syncthreads();
+    if constexpr (W::NBUF == 1) {
+      stage_kq(0);
+      fetch_kq(chunk_at(step + 2));
+      __syncthreads();
+    }
+  }
+  for (int64_t t = static_cast<int64_t>(n_chunks) * kGdrC + 4 * r + g; t < L; t += 8) {
+    if (col_ok) a.dv[(row_b + t) * yrow + static_cast<int64_t>(h) * P + col] = 0.0f;
   }
 }
 
@@ -404,14 +470,10 @@ template <int NP, bool BF16>
 void launch_pairs(const GatedDeltaBwdArgs& a, const GdrWork& ws, int chunks, hipStream_t st) {
   const int64_t bh = a.f.batch * a.f.nheads;
   const int64_t slices = (a.f.headdim + 15) / 16;
-  const int pairs = gdr_block_pairs(bh, slices);
-  const auto blocks = [&](int n) { return static_cast<unsigned>(bh * ((slices + n - 1) / n)); };
-  if (pairs == 1) {
-    gdr_reverse_kernel<NP, BF16, 1><<<blocks(1), 128, 0, st>>>(a, ws, chunks);
-  } else if (pairs == 2) {
-    gdr_reverse_kernel<NP, BF16, 2><<<blocks(2), 256, 0, st>>>(a, ws, chunks);
+  if (gdr_block_pairs(bh, slices) == 1) {
+    gdr_reverse_kernel<NP, BF16, 1><<<static_cast<unsigned>(bh * slices), 256, 0, st>>>(a, ws, chunks);
   } else {
-    gdr_reverse_kernel<NP, BF16, 4><<<blocks(4), 512, 0, st>>>(a, ws, chunks);
+    gdr_reverse_kernel<NP, BF16, 2><<<static_cast<unsigned>(bh * ((slices + 1) / 2)), 512, 0, st>>>(a, ws, chunks);
   }
 }
 
