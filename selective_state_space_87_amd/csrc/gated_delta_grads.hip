@@ -13,13 +13,19 @@
 //   dc_t = scale e^c_t q_t . N1_t - e^c_t k_t . N2_t - w_t k_t . N3_t + sum_s beta_s Z[t,s] - beta_t sum_u Z[u,t]
 //          (+ sum_s w_s k_s . N3_s + e^c_end <X, S> at the chunk's end)
 //   d(dt A)_t = sum_{u >= t} dc_u
+// Gq and Gk are kept with the row factors of both their sides (those of k on
+// the columns, of q or k on the rows) and taken out of the products' rows again:
+// one set of halves, read by rows and, transposed by the LDS, by columns, serves
+// Gq K and Gq^T Q, and one Gk K and Gk^T K.
 // One block of eight waves per (batch row, query/key head, chunk); wave w has
 // row tile w % 4 and half w / 4 of the N columns (and of dP and M: the one or
 // the other). The heads that share q and k are taken one after another, their
-// dq and dk added in registers: no partial sums in memory, no atomics. (With
-// four waves a block the accumulators of a wave, 192 registers, and their
-// operands spilled: 600 us where the layer (2, 4096, 16 heads of 128 x 128) needs
-// less now.)
+// dq and dk added in registers: no partial sums in memory, no atomics.
+// Measured at (2, 4096, 16 heads of 128 x 128), bfloat16 inputs, 0.54 GB in: 251
+// us, one block a CU. (Four waves a block: 600 us, for the 192 registers of a
+// wave's accumulators left none for operands. Gq and Gk in float32, made into
+// halves once for each of the four products: 281 us.) The staged pieces of S and
+// X, split into halves by all waves between two barriers, take the most.
 #include <hip/hip_runtime.h>
 
 #include "gdr_mma.h"
@@ -29,7 +35,7 @@ namespace ssm {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kGS = kGdrC + 4;   // row stride of Gq and Gk in LDS (floats)
+constexpr int kGS = kGdrC + 8;   // row stride of Gq and Gk in LDS (halves)
 constexpr int kPS = 32 + 8;      // row stride of the staged 64 x 32 pieces (halves)
 
 // Elements e .. e+7 of a float32 row that starts `row` elements into the
@@ -81,6 +87,23 @@ __device__ __forceinline__ float wave_sum64(float v) {
   return v;
 }
 
+// The factors of a chunk's 64 rows of K or Q, a lane each. unit: the power of
+// two of the largest (down: that power, up: its inverse). Rows whose factor is
+// under 2^-8 of it (a key of nothing has one of 2^-113) are lifted by a power of
+// two there, and their halves lowered: Gq and Gk, kept with the factors of
+// their rows and columns, then hold every row of the products to 2^-38 2^16 of
+// the largest. The halves themselves stay as exact as they were for rows down
+// to 2^-24 of the largest.
+__device__ __forceinline__ Pow2 row_lift(float f, Pow2& unit) {
+  const int e = static_cast<int>(__float_as_uint(f) >> 23) & 255;
+  const int top = static_cast<int>(__float_as_uint(lanes16_max(col_max(f))) >> 23) & 255;
+  const int u = top < 8 ? 8 : (top > 246 ? 246 : top);
+  unit = Pow2{__uint_as_float(static_cast<uint32_t>(254 - u) << 23), __uint_as_float(static_cast<uint32_t>(u) << 23)};
+  int j = top - 8 - e;
+  j = j < 0 ? 0 : (j > 126 ? 126 : j);
+  return Pow2{__uint_as_float(static_cast<uint32_t>(127 + j) << 23), __uint_as_float(static_cast<uint32_t>(127 - j) << 23)};
+}
+
 template <int NP, bool BF16, bool FAST>
 __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwdArgs a, const GdrWork ws, int chunks) {
   constexpr int RAW = BF16 ? 1 : 2, RS = NP + 8, NJ = NP / 32;  // NJ: column tiles of a wave
@@ -89,22 +112,23 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
   constexpr int kSX = 32 * RS;                            // halves of a staged 32 x NP piece
   constexpr int kTP = kGdrC * kPS;                        // halves of a staged 64 x 32 piece
   constexpr int kStage = (4 * kSX + 6 * kTP) * 2;         // S, X and dY, E, dE, hi and lo
-  constexpr int kG = 2 * kGdrC * kGS * 4;
+  constexpr int kGP = kGdrC * kGS;                        // halves of a plane of Gq or Gk
+  constexpr int kG = 4 * kGP * 2;                         // Gq and Gk, hi and lo
   __shared__ __align__(16) _Float16 sK[kMat], sQ[kMat];
   __shared__ __align__(16) char pool[kStage > kG ? kStage : kG];
   __shared__ double sC[kGdrC];
   __shared__ float sBeta[kGdrC], sKn[kGdrC], sQn[kGdrC], sKup[kGdrC], sQup[kGdrC];
   __shared__ float sRow[4][2][kGdrC];                     // q.N1, k.N2, k.N3 (half the columns each), sum_s beta_s Z
   __shared__ float sCol[8][kGdrC];                        // a wave's sums of Z down the columns
-  __shared__ float sDot[8];
+  __shared__ float sDot[8], sTop[8];
   const GatedDeltaArgs& p = a.f;
   _Float16* sS = reinterpret_cast<_Float16*>(pool);       // [2][32][RS]
   _Float16* sX = sS + 2 * kSX;
   _Float16* sY = sX + 2 * kSX;                            // [2][64][kPS]
   _Float16* sE = sY + 2 * kTP;
   _Float16* sD = sE + 2 * kTP;
-  float* sGq = reinterpret_cast<float*>(pool);            // [64][kGS]
-  float* sGk = sGq + kGdrC * kGS;
+  _Float16* sGq = reinterpret_cast<_Float16*>(pool);      // [2][64][kGS]
+  _Float16* sGk = sGq + 2 * kGP;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w8 = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -130,19 +154,24 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
 #pragma unroll
   for (int j = 0; j < NJ; ++j) dq[j] = dk[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
+  Pow2 kunit, qunit;
   if (rows > 0) {
-    const u32x4_t* K = reinterpret_cast<const u32x4_t*>(ws.K + static_cast<int64_t>(blockIdx.x) * kMat);
-    const u32x4_t* Q = reinterpret_cast<const u32x4_t*>(ws.Q + static_cast<int64_t>(blockIdx.x) * kMat);
-    for (int i = tid; i < kMat / 8; i += kThreads) {
-      reinterpret_cast<u32x4_t*>(sK)[i] = K[i];
-      reinterpret_cast<u32x4_t*>(sQ)[i] = Q[i];
-    }
+    const half8_t* K = reinterpret_cast<const half8_t*>(ws.K + static_cast<int64_t>(blockIdx.x) * kMat);
+    const half8_t* Q = reinterpret_cast<const half8_t*>(ws.Q + static_cast<int64_t>(blockIdx.x) * kMat);
     const float* fac = ws.fac + ((static_cast<int64_t>(b) * H + kh * r) * chunks + c) * (kGdrFactors * kGdrC);
+    const float kn = fac[kFacKn * kGdrC + lane], qn = fac[kFacQn * kGdrC + lane];
+    const float kup = fac[kFacKup * kGdrC + lane], qup = fac[kFacQup * kGdrC + lane];
+    const Pow2 kf = row_lift(kn, kunit), qf = row_lift(qn, qunit);
+    for (int i = tid; i < kMat / 8; i += kThreads) {
+      const int t = i * 8 % (kGdrC * NP) / NP;
+      reinterpret_cast<half8_t*>(sK)[i] = K[i] * static_cast<_Float16>(__shfl(kf.down, t));
+      reinterpret_cast<half8_t*>(sQ)[i] = Q[i] * static_cast<_Float16>(__shfl(qf.down, t));
+    }
     if (tid < kGdrC) {
-      sKn[tid] = fac[kFacKn * kGdrC + tid];
-      sQn[tid] = fac[kFacQn * kGdrC + tid];
-      sKup[tid] = fac[kFacKup * kGdrC + tid];
-      sQup[tid] = fac[kFacQup * kGdrC + tid];
+      sKn[tid] = kn * kf.up;
+      sQn[tid] = qn * qf.up;
+      sKup[tid] = kup * kf.down;
+      sQup[tid] = qup * qf.down;
     }
   }
 
@@ -163,6 +192,28 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
       }
       continue;
     }
+    // 32 columns of S, X, dY, E, dE at a time, the next ones in flight in
+    // registers: a piece of S and X a thread, a piece of dY or dE, half a piece of E.
+    constexpr int kSXT = 32 * NP / 8 < kThreads ? 1 : 32 * NP / 8 / kThreads;
+    float fs[kSXT][8], fx[kSXT][8], fy[8], fe[8];
+    const int trow = (tid >> 2) & 63, tcol = 8 * (tid & 3);
+    const uint32_t yrow = static_cast<uint32_t>(H * P);
+    const rsrc_t rs = raw_buffer(ws.S + item * P * N, static_cast<uint32_t>(P * N * 4));
+    const rsrc_t rx = raw_buffer(ws.X + item * P * N, static_cast<uint32_t>(P * N * 4));
+    const rsrc_t re = raw_buffer(ws.E + item * kGdrC * P, static_cast<uint32_t>(kGdrC * P * 4));
+    const rsrc_t ry = rows_buffer<4>(hf == 0 ? a.dy : a.dv, row0 * yrow + static_cast<int64_t>(h) * P, rows, yrow, P);
+    const auto fetch = [&](int p0) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < kSXT; ++i) {
+        const int e = (i * kThreads + tid) * 8 % (32 * NP), pr = e / NP, n = e % NP;
+        const bool ok = p0 + pr < P;
+        load8_f32<FAST>(rs, static_cast<uint32_t>((p0 + pr) * N), n, N, ok, fs[i]);
+        load8_f32<FAST>(rx, static_cast<uint32_t>((p0 + pr) * N), n, N, ok, fx[i]);
+      }
+      load8_f32<FAST>(ry, static_cast<uint32_t>(trow) * yrow + static_cast<uint32_t>(p0), tcol, P - p0, trow < rows, fy);
+      load8_f32<FAST>(re, static_cast<uint32_t>(trow * P + p0), tcol, P - p0, true, fe);
+    };
+    fetch(0);
     // Gates (wave 0; its lane t keeps the step's values for the end).
     float x = 0.0f, beta_raw = 0.0f;
     if (w8 == 0) {
@@ -195,28 +246,6 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     for (int j = 0; j < 4; ++j) tri[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     float dot = 0.0f;  // this thread's part of <X, S>
 
-    // 32 columns of S, X, dY, E, dE at a time, the next ones in flight in
-    // registers: a piece of S and X a thread, a piece of dY or dE, half a piece of E.
-    constexpr int kSXT = 32 * NP / 8 < kThreads ? 1 : 32 * NP / 8 / kThreads;
-    float fs[kSXT][8], fx[kSXT][8], fy[8], fe[8];
-    const int trow = (tid >> 2) & 63, tcol = 8 * (tid & 3);
-    const uint32_t yrow = static_cast<uint32_t>(H * P);
-    const rsrc_t rs = raw_buffer(ws.S + item * P * N, static_cast<uint32_t>(P * N * 4));
-    const rsrc_t rx = raw_buffer(ws.X + item * P * N, static_cast<uint32_t>(P * N * 4));
-    const rsrc_t re = raw_buffer(ws.E + item * kGdrC * P, static_cast<uint32_t>(kGdrC * P * 4));
-    const rsrc_t ry = rows_buffer<4>(hf == 0 ? a.dy : a.dv, row0 * yrow + static_cast<int64_t>(h) * P, rows, yrow, P);
-    const auto fetch = [&](int p0) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < kSXT; ++i) {
-        const int e = (i * kThreads + tid) * 8 % (32 * NP), pr = e / NP, n = e % NP;
-        const bool ok = p0 + pr < P;
-        load8_f32<FAST>(rs, static_cast<uint32_t>((p0 + pr) * N), n, N, ok, fs[i]);
-        load8_f32<FAST>(rx, static_cast<uint32_t>((p0 + pr) * N), n, N, ok, fx[i]);
-      }
-      load8_f32<FAST>(ry, static_cast<uint32_t>(trow) * yrow + static_cast<uint32_t>(p0), tcol, P - p0, trow < rows, fy);
-      load8_f32<FAST>(re, static_cast<uint32_t>(trow * P + p0), tcol, P - p0, true, fe);
-    };
-    fetch(0);
     for (int p0 = 0; p0 < P; p0 += 32) {
       __syncthreads();
 #pragma unroll
@@ -285,8 +314,11 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     {
       const _Float16* left = hf == 0 ? sQ : sK;
       const float* ln = hf == 0 ? sQn : sKn;
-      float* out = hf == 0 ? sGq : sGk;
+      const float lup = hf == 0 ? qunit.up : kunit.up, whole = (hf == 0 ? qunit.down : kunit.down) * kunit.down;
       const float unit = hf == 0 ? top[kMaxDY].down * top[kMaxE].down * p.scale : -(top[kMaxDE].down * top[kMaxE].down);
+      float mx = 0.0f, lnt[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lnt[i] = ln[16 * w + 4 * g + i] * lup;
 #pragma unroll
       for (int si = 0; si < 4; ++si) {
         float col_z = 0.0f;
@@ -304,19 +336,22 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
               xk = mfma16(*reinterpret_cast<const half8_t*>(left + kLo + at), bk, xk);
             }
           }
-          const float bs = sBeta[s], kns = sKn[s];
+          const float bs = sBeta[s], kns = sKn[s] * kunit.up;
           const double cs = sC[s];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int t = 16 * w + 4 * g + i;
-            const bool in = hf == 0 ? s <= t : s < t;
-            const float dec = exp2_hw(static_cast<float>(sC[t] - cs));
+            const bool in = si < w || (hf == 0 ? s <= t : s < t);
+            const float dec = exp2_hw(static_cast<float>(sC[t] - cs)) * (lnt[i] * kns);
             const float u = in ? tri[si][i] * unit * dec : 0.0f;
-            const float z = in ? u * (xk[i] * ln[t] * kns) : 0.0f;  // (no product of a masked infinity)
+            const float z = in ? u * (xk[i] * whole) : 0.0f;  // (no product of a masked infinity)
             row_z[i] = fmaf(bs, z, row_z[i]);
             col_z += z;
-            out[t * kGS + s] = u * bs;
+            tri[si][i] = u * bs;
+            mx = fmaxf(mx, fabsf(tri[si][i]));
           }
+        } else {
+          tri[si] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         }
         const auto x32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(col_z), __float_as_uint(col_z), false, false);
         col_z = __uint_as_float(x32[0]) + __uint_as_float(x32[1]);
@@ -324,6 +359,8 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
         col_z = __uint_as_float(x16[0]) + __uint_as_float(x16[1]);
         if (g == 0) sCol[w8][s] = col_z;
       }
+      mx = lanes16_max(col_max(mx));
+      if (lane == 0) sTop[w8] = mx;
     }
     // Row products with N1, N2, N3, and their parts of dq and dk.
     {
@@ -363,51 +400,77 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     }
     __syncthreads();
 
-    // dq += Gq K;  dk += Gk K + Gk^T K + Gq^T Q. The row factors of K and Q go
-    // into the triangles' columns; a triangle's rows 16 w .. are halves of one scale.
-    const auto product = [&](const float* T, bool up, const float* cn, const _Float16* mat, f32x4_t* out)
-                             __attribute__((always_inline)) {
-      const int place = anew(lane), m = place & 15, g = place >> 4;
-      const int t = 16 * w + m;
-      float x8[2][8];
-      float mx = 0.0f;
+    // dq += Gq K;  dk += Gk K + Gk^T K + Gq^T Q.
+    Pow2 sg[2];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+    for (int k = 0; k < 2; ++k) {
+      sg[k] = pow2_to_top(fmaxf(fmaxf(sTop[4 * k], sTop[4 * k + 1]), fmaxf(sTop[4 * k + 2], sTop[4 * k + 3])));
+    }
+    {
+      // the wave's tiles of its triangle, and the zeros right of an even
+      // diagonal tile (pieces are two tiles wide)
+      _Float16* out = hf == 0 ? sGq : sGk;
+      const float up = hf == 0 ? sg[0].up : sg[1].up;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int s = 32 * q + 8 * g + e;
-          x8[q][e] = (up ? s >= t : s <= t) ? T[up ? s * kGS + t : t * kGS + s] * cn[s] : 0.0f;
-          mx = fmaxf(mx, fabsf(x8[q][e]));
+      for (int si = 0; si < 4; ++si) {
+        if (si > (w | 1)) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v = tri[si][i] * up;
+          const _Float16 hi = static_cast<_Float16>(v);
+          const int at = (16 * w + 4 * g + i) * kGS + 16 * si + m;
+          out[at] = hi;
+          out[kGP + at] = static_cast<_Float16>(v - static_cast<float>(hi));
         }
       }
-      const Pow2 sc = pow2_to_top(lanes16_max(col_max(mx)));
-      half8_t hi[2], lo[2];
+    }
+    __syncthreads();
+    {
+      f32x4_t aq[NJ], ak[NJ], ag[NJ];  // Gq K; Gk K + Gk^T K; Gq^T Q
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) aq[j] = ak[j] = ag[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
+        const bool low = 2 * q <= w, upp = 2 * q + 1 >= w;  // (of the wave)
+        const int at = (16 * w + m) * kGS + 32 * q + 8 * g;
+        half8_t bk[NJ];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x8[q][e] *= sc.up;
-        hi[q] = halves(x8[q]);
-        lo[q] = rest(x8[q], hi[q]);
-      }
+        for (int j = 0; j < NJ; ++j) bk[j] = kq_column8<NP>(sK, 32 * q, c0 + 16 * j, m, g);
+        const auto times_k = [&](half8_t hi, half8_t lo, f32x4_t* acc) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (up ? (q == 0 && w >= 2) : (q == 1 && w < 2)) continue;
-          const half8_t bv = kq_column8<NP>(mat, 32 * q, c0 + 16 * j, m, g);
-          acc = mfma16(hi[q], bv, acc);
-          acc = mfma16(lo[q], bv, acc);
-          if constexpr (RAW == 2) acc = mfma16(hi[q], kq_column8<NP>(mat + kLo, 32 * q, c0 + 16 * j, m, g), acc);
+          for (int j = 0; j < NJ; ++j) {
+            acc[j] = mfma16(hi, bk[j], acc[j]);
+            acc[j] = mfma16(lo, bk[j], acc[j]);
+            if constexpr (RAW == 2) acc[j] = mfma16(hi, kq_column8<NP>(sK + kLo, 32 * q, c0 + 16 * j, m, g), acc[j]);
+          }
+        };
+        if (low) {
+          times_k(*reinterpret_cast<const half8_t*>(sGq + at), *reinterpret_cast<const half8_t*>(sGq + kGP + at), aq);
+          times_k(*reinterpret_cast<const half8_t*>(sGk + at), *reinterpret_cast<const half8_t*>(sGk + kGP + at), ak);
         }
+        if (upp) {
+          times_k(column8(sGk, kGS, 32 * q, 16 * w, m, g), column8(sGk + kGP, kGS, 32 * q, 16 * w, m, g), ak);
+          const half8_t hi = column8(sGq, kGS, 32 * q, 16 * w, m, g), lo = column8(sGq + kGP, kGS, 32 * q, 16 * w, m, g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[j][i] = fmaf(acc[i], sc.down, out[j][i]);
+          for (int j = 0; j < NJ; ++j) {
+            const half8_t bq = kq_column8<NP>(sQ, 32 * q, c0 + 16 * j, m, g);
+            ag[j] = mfma16(hi, bq, ag[j]);
+            ag[j] = mfma16(lo, bq, ag[j]);
+            if constexpr (RAW == 2) ag[j] = mfma16(hi, kq_column8<NP>(sQ + kLo, 32 * q, c0 + 16 * j, m, g), ag[j]);
+          }
+        }
       }
-    };
-    product(sGq, false, sKn, sK, dq);
-    product(sGk, false, sKn, sK, dk);
-    product(sGk, true, sKn, sK, dk);
-    product(sGq, true, sQn, sQ, dk);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * w + 4 * g + i;
+        const float iq = kunit.down * sg[0].down / (sQn[t] * qunit.up), ik = 1.0f / (sKn[t] * kunit.up);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          dq[j][i] = fmaf(aq[j][i], iq, dq[j][i]);
+          dk[j][i] = fmaf(ik, fmaf(ag[j][i], qunit.down * sg[0].down, ak[j][i] * (kunit.down * sg[1].down)), dk[j][i]);
+        }
+      }
+    }
 
     // The gates: lane t of wave 0.
     if (w8 == 0) {

@@ -147,6 +147,28 @@ def test_repeated_and_zero_keys():
     compare("repeated keys, ordinary steps", {"dk": sub(got["dk"])}, {"dk": sub(ref["dk"]), "mag": {}})
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("l2norm", [False, True])
+def test_rows_of_unequal_size(l2norm, dtype):
+    # a chunk of ordinary, small and minute rows; one of zero keys; one of zero queries
+    p = problem(1, 250, 1, 2, 64, 64, dtype, 19, l2norm)
+    p["k"][0, 10:20] *= 2.0**-9
+    p["k"][0, 20:25] *= 2.0**-30
+    p["q"][0, 15:30] *= 2.0**-11
+    p["q"][0, 40:44] *= 2.0**-40
+    p["k"][0, 64:128] = 0.0
+    p["q"][0, 128:192] = 0.0
+    p["k"][0, 192:] *= 2.0**-20
+    dy, dh = seeds(p, 23)
+    got, ref = run(p, dy, dh, l2norm), reference(p, dy, dh, l2norm)
+    compare(f"unequal rows {dtype} {l2norm}", got, ref)
+    # with the norm a small key's gradient is the largest by far: the ordinary rows with their own scale too
+    keep = [*range(0, 10), *range(30, 40), *range(44, 64)]
+    sub = lambda a: a[:, keep]  # noqa: E731
+    compare("ordinary rows", {x: sub(got[x]) for x in ("dq", "dk")},
+            {"dq": sub(ref["dq"]), "dk": sub(ref["dk"]), "mag": {}})
+
+
 @pytest.mark.parametrize("size", [1e-4, 1e4])
 def test_large_and_small_values(size):
     p = problem(1, 140, 1, 2, 64, 64, "bf16", 11)
