@@ -113,7 +113,10 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, MODE>::NT)) void gd
     const int col = col0 + 16 * pr + m;
     const bool col_ok = col < P;
     const int64_t sb = (static_cast<int64_t>(bh) * P + (col_ok ? col : 0)) * N;
-    const float* enters = z == 0 ? p.h0 : (MODE == kGdrMap ? nullptr : ws.seg + static_cast<int64_t>(z - 1) * ws.seg_stride);
+    // (In segments, not from h0: another segment's block may write it as h_final.)
+    const float* enters = p.h0;
+    if (MODE == kGdrMap && z > 0) enters = nullptr;
+    if (MODE == kGdrForward && segs > 1) enters = ws.seg + z * ws.seg_stride;
     _Float16* const xh = reinterpret_cast<_Float16*>(xch[pr]);
     float* const xf = reinterpret_cast<float*>(xh + W::kXF);
     float *const xs_f = xf, *const xd_f = xf + 128, *const xe_f = xf + 256, *const xr_f = xf + 384;

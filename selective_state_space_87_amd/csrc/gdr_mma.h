@@ -217,7 +217,7 @@ struct GdrWork {  // device pointers into the workspace
   float* top;     // [items][kGdrMaxima][kGdrMaxSlots]
   float* part;    // [2][items]: an item's part of dA and of ddt_bias
   float* map;     // [heads][segments][P + N][N]: a segment's map (forward in segments)
-  float* seg;     // [segments - 1][heads][P][N]: state entering segment z + 1
+  float* seg;     // [segments][heads][P][N]: state entering a segment
   int64_t seg_stride;  // elements from one segment's states to the next's
 };
 

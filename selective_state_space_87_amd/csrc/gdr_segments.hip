@@ -8,7 +8,8 @@
 //   s_(z+1) = u_z + s_z F_z,
 // in order, in float32 matrix instructions (16x16x4): one block of four waves
 // per 16 rows of a head's state, a wave a quarter of the N columns; the rows of F
-// come straight from memory in the operand's order.
+// come straight from memory in the operand's order. The first segment's state is
+// copied: h_final may be h0 itself, and the walks of all segments run at once.
 #include <hip/hip_runtime.h>
 
 #include "gdr_mma.h"
@@ -32,6 +33,9 @@ __global__ __launch_bounds__(kThreads) void gdr_join_kernel(const GatedDeltaArgs
   const int64_t most = static_cast<int64_t>(seg_chunks) * kGdrC;
   const float* maps = ws.map + static_cast<int64_t>(bh) * segs * (P + N) * N;
   for (int i = tid; i < 16 * kSS; i += kThreads) sS[i] = 0.0f;
+  const int64_t at0 = (static_cast<int64_t>(bh) * P + p0) * N;
+  const int mine = (P - p0 < 16 ? P - p0 : 16) * N;
+  for (int i = tid; i < mine; i += kThreads) ws.seg[at0 + i] = p.h0 != nullptr ? p.h0[at0 + i] : 0.0f;
   __syncthreads();
   // Tile u of the wave: column m is n = 32 w + 16 u + m; element i is row p0 + 4 g + i.
   for (int z = 0; z + 1 < segs && len > (z + 1) * most; ++z) {
@@ -66,7 +70,7 @@ __global__ __launch_bounds__(kThreads) void gdr_join_kernel(const GatedDeltaArgs
       }
     }
     __syncthreads();
-    float* out = ws.seg + z * ws.seg_stride + (static_cast<int64_t>(bh) * P + p0) * N;
+    float* out = ws.seg + (z + 1) * ws.seg_stride + at0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int n = 32 * w + 16 * t + m;

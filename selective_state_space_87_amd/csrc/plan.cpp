@@ -176,7 +176,7 @@ GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t
   if (p.segs > 1) {
     const size_t heads = static_cast<size_t>(batch * nheads);
     p.off_map = take_n(heads * static_cast<size_t>(p.segs), static_cast<size_t>((headdim + dstate) * dstate) * 4);
-    p.off_seg = take_n(heads * static_cast<size_t>(p.segs - 1), static_cast<size_t>(headdim * dstate) * 4);
+    p.off_seg = take_n(heads * static_cast<size_t>(p.segs), static_cast<size_t>(headdim * dstate) * 4);
   }
   if (backward) {
     const size_t state = static_cast<size_t>(headdim * dstate) * 4;

@@ -298,6 +298,16 @@ def test_long_sequences_of_few_heads(L, G, H, N, P, lens, dtype):
     close(f"segments {(L, G, H, N, P)} {dtype} h", h, href, tol=2 * TOL)
 
 
+def test_long_sequence_with_its_state_in_place():
+    p = problem(2, 4096, 1, 1, 32, 32, "f32", 18)
+    p["dt_bias"] = torch.full((1,), -7.0, device="cuda")
+    lens = torch.tensor([4096, 600], dtype=torch.int32, device="cuda")
+    y, h = run(p, seqlens=lens)
+    state = p["h0"].clone()
+    y2, h2 = run(dict(p, h0=state), h_final=state, seqlens=lens)
+    assert h2 is state and torch.equal(y, y2) and torch.equal(h, state)
+
+
 def test_refusals():
     p = problem(1, 8, 2, 4, 16, 8, "f32", 16)
     with pytest.raises(ValueError):
