@@ -427,7 +427,9 @@ int ssm_ssd_fwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, 
  *   nkheads, nheads            : G and H; H a multiple of G (else
  *                                SSM_E_SHAPE), H = 0 only with G = 0.
  *   headdim, dstate            : 1 <= P <= 256, 1 <= N <= 128 (else
- *                                SSM_E_UNSUPPORTED); B * H * P < 2^31.
+ *                                SSM_E_UNSUPPORTED). B H times the 16-column
+ *                                slices of P, and times the 64-step blocks of
+ *                                L: at most 2^22 each (else SSM_E_UNSUPPORTED).
  *   in_dtype, out_dtype        : 0 float32, 1 bfloat16.
  *   flags                      : SSM_FLAG_SOFTPLUS, SSM_FLAG_BETA_SIGMOID,
  *                                SSM_FLAG_QK_L2NORM, in any combination.

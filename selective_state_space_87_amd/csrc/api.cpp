@@ -614,9 +614,14 @@ int gdr_sizes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, in
       !safe_mul(batch, nheads, &z->bh) || !safe_mul(z->bh, headdim, &t) || !safe_mul(t, dstate, &z->bhpn)) {
     return SSM_E_SHAPE;
   }
-  if (seqlen >= (int64_t(1) << 30) || z->bh * headdim > 0x7fffffff) return SSM_E_UNSUPPORTED;
-  // one (batch row, head, 64 steps) item a block
-  if (z->bh * ((seqlen + 63) / 64) > 0x7fffffff) return SSM_E_UNSUPPORTED;
+  if (!safe_mul(nkheads, dstate, &t) || !safe_mul(nheads, headdim, &t)) return SSM_E_SHAPE;
+  if (seqlen >= (int64_t(1) << 30)) return SSM_E_UNSUPPORTED;
+  // a block for every 64 steps, or 16 columns, of a head at most, of up to 512
+  // threads (1024 for 64 columns): launches stay below 2^32 threads
+  constexpr int64_t most = int64_t(1) << 22;
+  if (z->bh > most || z->bh * ((headdim + 15) / 16) > most || z->bh * ((seqlen + 63) / 64) > most) {
+    return SSM_E_UNSUPPORTED;
+  }
   return SSM_OK;
 }
 

@@ -65,6 +65,19 @@ def test_sizes_types_and_options(lib, call):
     assert call(lib, B=1 << 28) == E_UNSUPPORTED
 
 
+def test_size_limits(lib):
+    # at most 2^22 head slices of 16 columns, and as many blocks of 64 steps
+    assert fwd(lib, B=1 << 20, L=17, Pd=17, vs=68) == E_UNSUPPORTED
+    assert upd(lib, B=(1 << 20) + 1) == E_UNSUPPORTED
+    assert bwd(lib, B=1 << 13, L=64 * 128 + 1) == E_UNSUPPORTED
+    assert fwd(lib, B=1 << 20, L=17, wsb=0) == E_WORKSPACE  # 2^22 slices: taken
+    # products of sizes past 64 bits, though nothing is there
+    for call in (fwd, bwd):
+        assert call(lib, B=0, G=1 << 61, H=1 << 61, qs=1, ks=1, vs=1) == E_SHAPE
+    assert upd(lib, B=0, G=1 << 61, H=1 << 61, qs=1, ks=1, vs=1) == E_SHAPE
+    assert lib.ssm_gated_delta_workspace_bytes(0, 8, 1 << 61, 1 << 61, 8, 8, 0) == 0
+
+
 def test_fwd_pointers(lib):
     for name in ("q", "k", "v", "dt", "A", "beta", "y"):
         assert fwd(lib, **{name: None}) == E_NULLPTR, name
