@@ -543,7 +543,7 @@ int ssm_gated_delta_bwd(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t 
  *   s = x + residual  (s = x when residual is NULL), rounded to res_dtype
  *   n = s / sqrt(mean(s^2) + eps) * weight            (weight NULL: 1)
  *   y = n, or with out_dtype 2: scales[r] = max|n| / 448 over the row (1 when
- *       that is 0) and y = n / scales[r] in the 8-bit format e4m3 (OCP: 448 is
+ *       that is 0, and at least 2^-126) and y = n / scales[r] in the 8-bit format e4m3 (OCP: 448 is
  *       its largest value), rounded to nearest even
  *
  *   rows, dim                  : R >= 0, 1 <= d <= 16384 (else

@@ -188,7 +188,8 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const RmsNormArgs p)
   }
   if constexpr (OUT == 2) {
     top = row_max<TPR>(top, slots[1]);
-    const float scale = top > 0.0f ? top / 448.0f : 1.0f;
+    // (not below 2^-126: under 2^-128 a scale has no finite inverse)
+    const float scale = top > 0.0f ? fmaxf(top / 448.0f, 0x1p-126f) : 1.0f;
     const float inv = 1.0f / scale;
 #pragma unroll
     for (int i = 0; i < NPK; ++i) {

@@ -99,6 +99,17 @@ def test_zero_rows_of_zeros_and_in_place():
     assert torch.equal(got[0], want[0])
 
 
+def test_minute_rows_in_eight_bits():
+    # largest values 2^-118 (scale below 2^-126 if it were max / 448) and 2^-100, and zeros between
+    s = torch.zeros(3, 64, device="cuda")
+    s[0, ::3], s[1, ::3], s[2, 5] = 2.0**-118, -(2.0**-100), 2.0**-126
+    out = binding.ssm_rms_norm_fwd(s, None, eps=1.0, out_dtype=torch.float8_e4m3fn)
+    sc, y = out["scales"], out["y"].float()
+    assert float(sc[0]) == 2.0**-126 == float(sc[2]) and abs(float(sc[1]) * 448 / 2.0**-100 - 1) < 3e-6
+    assert not y[:, 1].any() and torch.equal(y[0, ::3], torch.full((22,), 256.0, device="cuda"))
+    assert torch.equal(y[1, ::3], torch.full((22,), -448.0, device="cuda")) and float(y[2, 5]) == 1.0
+
+
 def test_not_finite_rows_stay_their_own():
     x = data(4, 96, 5, torch.float32)[0]
     want = binding.ssm_rms_norm_fwd(x, out_dtype=T["e4m3"])
