@@ -377,12 +377,28 @@ void launch_norm_res(const RmsNormArgs& a, bool vec, hipStream_t st) {
 
 }  // namespace
 
-int launch_rms_norm(const RmsNormArgs& a, void* stream) {
+int launch_rms_norm(const RmsNormArgs& all, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const bool vec = a.dim % 8 == 0 && on16(a.x) && on16(a.residual) && on16(a.weight) && on16(a.y) &&
-                   on16(a.residual_out);
-  a.in_bf16 ? launch_norm_res<true>(a, vec, st) : launch_norm_res<false>(a, vec, st);
-  return static_cast<int>(hipGetLastError());
+  // 2^23 rows a launch: up to as many blocks, which stay below 2^32 threads.
+  constexpr int64_t kRowsALaunch = int64_t(1) << 23;
+  const auto behind = [](const void* p, int64_t bytes) {
+    return p != nullptr ? const_cast<char*>(static_cast<const char*>(p)) + bytes : nullptr;
+  };
+  for (int64_t row = 0; row < all.rows; row += kRowsALaunch) {
+    RmsNormArgs a = all;
+    const int64_t n = row * a.dim, res = n * (a.res_bf16 ? 2 : 4);
+    a.rows = all.rows - row < kRowsALaunch ? all.rows - row : kRowsALaunch;
+    a.x = behind(a.x, n * (a.in_bf16 ? 2 : 4));
+    a.residual = behind(a.residual, res);
+    a.residual_out = behind(a.residual_out, res);
+    a.y = behind(a.y, n * (a.out_type == 0 ? 4 : (a.out_type == 1 ? 2 : 1)));
+    a.scales = reinterpret_cast<float*>(behind(a.scales, row * 4));
+    const bool vec = a.dim % 8 == 0 && on16(a.x) && on16(a.residual) && on16(a.weight) && on16(a.y) &&
+                     on16(a.residual_out);
+    a.in_bf16 ? launch_norm_res<true>(a, vec, st) : launch_norm_res<false>(a, vec, st);
+    if (const hipError_t e = hipGetLastError()) return static_cast<int>(e);
+  }
+  return 0;
 }
 
 int launch_rms_norm_bwd(const RmsNormBwdArgs& a, void* stream) {

@@ -110,6 +110,19 @@ def test_minute_rows_in_eight_bits():
     assert torch.equal(y[1, ::3], torch.full((22,), -448.0, device="cuda")) and float(y[2, 5]) == 1.0
 
 
+def test_more_rows_than_a_launch_takes():
+    rows, dim = (1 << 24) + 5, 5
+    x = torch.randn(rows, dim, device="cuda", dtype=torch.bfloat16)
+    res = torch.randn(rows, dim, device="cuda", dtype=torch.bfloat16)
+    out = binding.ssm_rms_norm_fwd(x, None, residual=res, out_dtype=torch.float8_e4m3fn)
+    for a in (0, (1 << 23) - 3, (1 << 23), rows - 3):
+        part = binding.ssm_rms_norm_fwd(x[a:a + 3].clone(), None, residual=res[a:a + 3].clone(),
+                                        out_dtype=torch.float8_e4m3fn)
+        assert torch.equal(out["y"][a:a + 3].view(torch.uint8), part["y"].view(torch.uint8))
+        assert torch.equal(out["scales"][a:a + 3], part["scales"])
+        assert torch.equal(out["residual_out"][a:a + 3], part["residual_out"])
+
+
 def test_not_finite_rows_stay_their_own():
     x = data(4, 96, 5, torch.float32)[0]
     want = binding.ssm_rms_norm_fwd(x, out_dtype=T["e4m3"])
