@@ -465,9 +465,11 @@ int ssm_ssd_fwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, 
  * that start on 16-byte boundaries with N and P multiples of 8 are read
  * fastest. Products are taken in 22 bits or more of every float32 operand (11
  * bits in those that only a bfloat16 y sees) and added in float32; results are
- * bitwise deterministic. A value of a step that
- * is not finite may make every y and state element of its head NaN from the
- * start of its block of 64 steps on.
+ * bitwise deterministic. Errors grow as the products of the steps' maps
+ * exp(dt A) (1 - beta k k^T) do: not at all where 0 <= beta |k|^2 <= 2, as with
+ * both the sigmoid and the norm. A value of a step that is not finite may make
+ * every y and state element of its head NaN from the start of its block of 64
+ * steps on.
  */
 size_t ssm_gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
                                        int64_t headdim, int64_t dstate, int in_dtype);
@@ -522,7 +524,8 @@ int ssm_gated_delta_update(int64_t batch, int64_t nkheads, int64_t nheads, int64
  *                                      on a 16-byte boundary
  * No output may overlap an input, another output or the workspace. Bitwise
  * deterministic (sums over steps, batch rows and shared heads in a fixed
- * order).
+ * order). A value that is not finite may make every gradient of its head and of
+ * the q and k that it shares NaN.
  */
 size_t ssm_gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
                                            int64_t headdim, int64_t dstate, int in_dtype);

@@ -1,6 +1,6 @@
 // Gated delta rule backward, what is left once the states S, E and the
 // gradients X, dE of every chunk are there (see gdr_mma.h and
-// gated_delta_reverse.h): the gradients of q, k and the gates, for every chunk
+// gated_delta_reverse.hip): the gradients of q, k and the gates, for every chunk
 // at once. Per head, with hats for the (normalised) rows and
 //   L[t,s] = e^(c_t - c_s) k_t . k_s (s < t),  Pm[t,s] = scale e^(c_t - c_s) q_t . k_s beta_s
 //   N1 = dY S, N2 = dE S, N3 = E X              (64 x N, contracted over the columns)
@@ -215,15 +215,14 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     };
     fetch(0);
     // Gates (wave 0; its lane t keeps the step's values for the end).
-    float x = 0.0f, beta_raw = 0.0f;
+    float x = 0.0f;
     if (w8 == 0) {
       float ld = 0.0f, beta = 0.0f;
       if (lane < rows) {
         const int64_t at = (row0 + lane) * H + h;
         x = load_elem<BF16>(p.dt, at) + (p.dt_bias ? p.dt_bias[h] : 0.0f);
         ld = gdr_log_decay(p, load_elem<BF16>(p.dt, at), p.dt_bias ? p.dt_bias[h] : 0.0f, p.A[h]);
-        beta_raw = load_elem<BF16>(p.beta, at);
-        beta = gdr_beta(p, beta_raw);
+        beta = gdr_beta(p, load_elem<BF16>(p.beta, at));
       }
       sC[lane] = wave_prefix(static_cast<double>(ld) * kLog2eD, lane);
       sBeta[lane] = beta;

@@ -292,8 +292,11 @@ struct GdrPlan {
   size_t off_tt, off_s, off_x, off_e, off_top, off_part;  // backward only
   size_t bytes;
 };
-// Up to this length the recurrence is taken.
-constexpr int64_t kGdrRecurrentSteps = 16;
+// Up to this length the recurrence is taken: its time grows with the steps, a
+// chunk's does not. Measured (bf16, N = P = 128, chunks against recurrence) at 4, 8
+// and 16 steps: 2 heads 19 us against 18, 20, 32; 256 heads 51 against 20, 27, 45;
+// 2048 heads 242 against 109, 175, 315.
+constexpr int64_t kGdrRecurrentSteps = 8;
 // Segments: with at most kGdrFewSlices slices of 16 columns (batch, heads and
 // head size together) the walks of whole sequences leave most of the device
 // idle, and finding the segments' states first (a pass over P + N columns in
