@@ -37,31 +37,41 @@ __global__ __launch_bounds__(kThreads) void gdr_join_kernel(const GatedDeltaArgs
   const int mine = (P - p0 < 16 ? P - p0 : 16) * N;
   for (int i = tid; i < mine; i += kThreads) ws.seg[at0 + i] = p.h0 != nullptr ? p.h0[at0 + i] : 0.0f;
   __syncthreads();
-  // Tile u of the wave: column m is n = 32 w + 16 u + m; element i is row p0 + 4 g + i.
-  for (int z = 0; z + 1 < segs && len > (z + 1) * most; ++z) {
-    const float* u = maps + static_cast<int64_t>(z) * (P + N) * N;
-    const float* F = u + static_cast<int64_t>(P) * N;
-    f32x4_t acc[2];
+  // Tile t of the wave: column m is n = 32 w + 16 t + m; element i is row p0 + 4 g
+  // + i. Rows and columns past P and N are read as the last ones (no load in a
+  // branch): what they give is not kept, and the state's columns past N are 0.
+  const int64_t map = static_cast<int64_t>(P + N) * N;
+  const int n0 = 32 * w + m < N ? 32 * w + m : N - 1, n1 = 32 * w + 16 + m < N ? 32 * w + 16 + m : N - 1;
+  float f0[NP / 4], f1[NP / 4], u[2][4];
+  const auto fetch = [&](int z) __attribute__((always_inline)) {
+    const float* at = maps + z * map;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int n = 32 * w + 16 * t + m;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = p0 + 4 * g + i;
-        acc[t][i] = row < P && n < N ? u[static_cast<int64_t>(row) * N + n] : 0.0f;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int row = p0 + 4 * g + i < P ? p0 + 4 * g + i : P - 1;
+      u[0][i] = at[static_cast<int64_t>(row) * N + n0];
+      u[1][i] = at[static_cast<int64_t>(row) * N + n1];
     }
-    if (z > 0) {  // (the first segment's walk started from the state itself)
-      // past N the state's columns in LDS are 0: rows and columns of F past it
-      // may be any, the last ones here (no load in a branch)
-      const int n0 = 32 * w + m < N ? 32 * w + m : N - 1, n1 = 32 * w + 16 + m < N ? 32 * w + 16 + m : N - 1;
-      float b0[NP / 4], b1[NP / 4];  // all of them in flight at once
+    at += static_cast<int64_t>(P) * N;
 #pragma unroll
-      for (int k = 0; k < NP; k += 4) {
-        const float* row = F + (k + g < N ? k + g : N - 1) * N;
-        b0[k / 4] = row[n0];
-        b1[k / 4] = row[n1];
-      }
+    for (int k = 0; k < NP; k += 4) {
+      const float* row = at + (k + g < N ? k + g : N - 1) * N;
+      f0[k / 4] = row[n0];
+      f1[k / 4] = row[n1];
+    }
+  };
+  int last = 0;  // maps of segments 0 .. last - 1 are there
+  for (int z = 0; z + 1 < segs && len > (z + 1) * most; ++z) last = z + 1;
+  if (last == 0) return;
+  fetch(0);
+  for (int z = 0; z < last; ++z) {
+    f32x4_t acc[2];
+    float b0[NP / 4], b1[NP / 4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[0][i] = u[0][i], acc[1][i] = u[1][i];
+#pragma unroll
+    for (int k = 0; k < NP / 4; ++k) b0[k] = f0[k], b1[k] = f1[k];
+    fetch(z + 1 < last ? z + 1 : z);  // the next segment's, while this one's is worked on
+    if (z > 0) {  // (the first segment's walk started from the state itself)
 #pragma unroll
       for (int k = 0; k < NP; k += 4) {
         const float a = sS[m * kSS + k + g];
