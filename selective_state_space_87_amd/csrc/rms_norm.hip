@@ -167,7 +167,20 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const RmsNormArgs p)
 #pragma unroll
     for (int k = 0; k < 8; ++k) sq = fmaf(s[i][k], s[i][k], sq);
   }
-  const float r = rsqrtf(row_sum<TPR>(sq, slots[0]) / static_cast<float>(dim) + p.eps);
+  float r = rsqrtf(row_sum<TPR>(sq, slots[0]) / static_cast<float>(dim) + p.eps);
+  // 8 bits: the rows are first taken with the power of two in r alone, so that
+  // y = n / scale is one rounding of s w and one of a factor, and what r was
+  // rounded by stands in the scale only. (With n, the scale's inverse and their
+  // product, two roundings more, more elements came out as the other neighbour.)
+  float rest = 1.0f;
+  if constexpr (OUT == 2) {
+    const uint32_t bits = __float_as_uint(r);
+    const bool normal = (bits >> 23) > 0 && (bits >> 23) < 255;
+    if (normal) {
+      rest = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+      r = __uint_as_float(bits & 0x7f800000u);
+    }
+  }
   float top = 0.0f;
 #pragma unroll
   for (int i = 0; i < NPK; ++i) {
@@ -188,9 +201,11 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const RmsNormArgs p)
   }
   if constexpr (OUT == 2) {
     top = row_max<TPR>(top, slots[1]);
-    // (not below 2^-126: under 2^-128 a scale has no finite inverse)
-    const float scale = top > 0.0f ? fmaxf(top / 448.0f, 0x1p-126f) : 1.0f;
-    const float inv = 1.0f / scale;
+    float scale = top * rest / 448.0f, inv = 448.0f / top;
+    if (!(scale >= 0x1p-126f)) {  // (under 2^-128 a scale has no finite inverse; 1 for a row of zeros)
+      scale = top > 0.0f ? 0x1p-126f : 1.0f;
+      inv = rest / scale;
+    }
 #pragma unroll
     for (int i = 0; i < NPK; ++i) {
 #pragma unroll
