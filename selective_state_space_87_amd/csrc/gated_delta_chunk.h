@@ -60,32 +60,43 @@ struct GdrWalk {
   static constexpr int NFL = (4 * kGdrC + NL - 1) / NL;
 };
 
+// A walk's LDS.
+template <class W, int NPAIR>
+struct GdrWalkLds {
+  __align__(16) char kq[W::NBUF][W::kBufBytes];
+  __align__(16) _Float16 T[W::kT];
+  __align__(16) _Float16 P[W::kP > 0 ? W::kP : 8];
+  __align__(16) char xch[NPAIR][W::kPairBytes];
+};
+
+// The walk of block `block`, by threads 0 .. W::NT - 1 (tid). Its barriers: one,
+// three a chunk (four with one buffer), and one more where pairs lag.
 template <int NP, bool BF16, bool OB16, int NPAIR, int MODE>
-__global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, MODE>::NT)) void gdr_chunk_kernel(const GatedDeltaArgs p,
-                                                                                             const GdrWork ws,
-                                                                                             int chunks, int segs,
-                                                                                             int seg_chunks) {
+__device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork& ws, int chunks, int segs,
+                                         int seg_chunks, int block, int tid,
+                                         GdrWalkLds<GdrWalk<NP, BF16, OB16, NPAIR, MODE>, NPAIR>& sh) {
   using W = GdrWalk<NP, BF16, OB16, NPAIR, MODE>;
   constexpr bool KEEP = W::KEEP;
   constexpr int RAW = W::RAW, OP = W::OP;
   constexpr int kLo = kGdrC * NP;                       // from an element's hi half to its lo half
   constexpr int NJ = NP / 32, NK = NP / 64;             // state tiles and operand pieces of a wave
   constexpr int EB = BF16 ? 2 : 4;
-  __shared__ __align__(16) char lds[W::NBUF][W::kBufBytes];
-  __shared__ __align__(16) _Float16 sT[W::kT];
-  __shared__ __align__(16) _Float16 sP[W::kP > 0 ? W::kP : 8];
-  __shared__ __align__(16) char xch[NPAIR][W::kPairBytes];
+  auto& lds = sh.kq;
+  auto& xch = sh.xch;
+  _Float16 *const sT = sh.T, *const sP = sh.P;
 
-  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
+  const int lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int H = static_cast<int>(p.nheads), G = static_cast<int>(p.nkheads);
   const int N = static_cast<int>(p.dstate), P = static_cast<int>(p.headdim);
   const int cols = MODE == kGdrMap ? P + N : P;  // a map's columns: a state from zero, then the unit vectors
   const int pblocks = (cols + 16 * NPAIR - 1) / (16 * NPAIR);
-  const int walk_id = static_cast<int>(blockIdx.x) / pblocks;
+  // K and Q are read by every slice of the heads that share them, T and Pm by every slice of a head.
+  const int place = gdr_xcd_place(block, static_cast<int>(gridDim.x), segs == 1 ? H / G * pblocks : pblocks);
+  const int walk_id = place / pblocks;
   const int bh = walk_id / segs, z = walk_id % segs;
   const int b = bh / H, h = bh % H, kh = h / (H / G);
-  const int col0 = (static_cast<int>(blockIdx.x) % pblocks) * 16 * NPAIR;
+  const int col0 = (place % pblocks) * 16 * NPAIR;
   // The segment: steps from `first` on, at most seg_chunks chunks.
   const int64_t first = static_cast<int64_t>(z) * seg_chunks * kGdrC, most = static_cast<int64_t>(seg_chunks) * kGdrC;
   const int64_t row_len = gdr_row_steps(p.seqlens, b, p.seqlen);
@@ -633,6 +644,16 @@ __global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, MODE>::NT)) void gd
   }
 }
 
+template <int NP, bool BF16, bool OB16, int NPAIR, int MODE>
+__global__ __launch_bounds__((GdrWalk<NP, BF16, OB16, NPAIR, MODE>::NT)) void gdr_chunk_kernel(const GatedDeltaArgs p,
+                                                                                             const GdrWork ws,
+                                                                                             int chunks, int segs,
+                                                                                             int seg_chunks) {
+  __shared__ GdrWalkLds<GdrWalk<NP, BF16, OB16, NPAIR, MODE>, NPAIR> lds;
+  gdr_walk<NP, BF16, OB16, NPAIR, MODE>(p, ws, chunks, segs, seg_chunks, static_cast<int>(blockIdx.x),
+                                        static_cast<int>(threadIdx.x), lds);
+}
+
 template <int NP, bool BF16, bool OB16, int MODE>
 void gdr_launch_chunk_pairs(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, int segs, int seg_chunks,
                             hipStream_t st) {
@@ -648,8 +669,10 @@ void gdr_launch_chunk_pairs(const GatedDeltaArgs& a, const GdrWork& ws, int chun
     }
   }
   if (pairs == 1) {
-    gdr_chunk_kernel<NP, BF16, OB16, 1, MODE>
-        <<<blocks(1), GdrWalk<NP, BF16, OB16, 1, MODE>::NT, 0, st>>>(a, ws, chunks, segs, seg_chunks);
+    if constexpr (MODE != kGdrKeep || !gdr_both_fit(NP, BF16)) {
+      gdr_chunk_kernel<NP, BF16, OB16, 1, MODE>
+          <<<blocks(1), GdrWalk<NP, BF16, OB16, 1, MODE>::NT, 0, st>>>(a, ws, chunks, segs, seg_chunks);
+    }
   } else {
     gdr_chunk_kernel<NP, BF16, OB16, 2, MODE>
         <<<blocks(2), GdrWalk<NP, BF16, OB16, 2, MODE>::NT, 0, st>>>(a, ws, chunks, segs, seg_chunks);

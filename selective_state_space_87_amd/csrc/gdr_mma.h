@@ -322,6 +322,18 @@ __device__ __forceinline__ double wave_prefix(double v, int lane) {
   return v;
 }
 
+// The place of block `block` of a launch among the work's items, so that the
+// `group` consecutive items that read the same arrays run on one XCD, whose L2
+// then fetches them once: blocks go to the eight XCDs in turn. (Groups are dealt
+// one by one, so that rows of different lengths spread; the last groups, where
+// there are no eight more, stay in order.)
+__device__ __forceinline__ int gdr_xcd_place(int block, int blocks, int group) {
+  const int set = 8 * group;
+  if (block >= blocks / set * set) return block;
+  const int k = block % set;
+  return block - k + k % 8 * group + k / 8;
+}
+
 // Pairs of waves (16 columns each) a block of the walks over the chunks: as
 // many as leave a block for every one of the 256 CUs. Measured (forward of 4096
 // steps, bf16, 128 x 128, with 1, 2 and 4 pairs a block): 32 heads 145, 148, 184
@@ -330,6 +342,15 @@ inline int gdr_block_pairs(int64_t heads, int64_t slices) {
   if (slices >= 4 && heads * ((slices + 3) / 4) >= 256) return 4;
   if (slices >= 2 && heads * ((slices + 1) / 2) >= 256) return 2;
   return 1;
+}
+
+// The backward's two walks, forth and back, by one kernel: where a block has one
+// pair (few heads: a walk is bound by its own latency, and the two together
+// take the time of the longer) and both fit the LDS.
+constexpr bool gdr_both_fit(int np, bool bf16) { return np == 64 || bf16; }
+inline bool gdr_both_at_once(const GatedDeltaArgs& a) {
+  return gdr_both_fit(a.dstate <= 64 ? 64 : 128, a.in_bf16) &&
+         gdr_block_pairs(a.batch * a.nheads, (a.headdim + 15) / 16) == 1;
 }
 
 // Launchers (0 or a HIP error code). vec: every row of q and k starts on a

@@ -28,7 +28,8 @@ __global__ __launch_bounds__(kThreads) void gdr_join_kernel(const GatedDeltaArgs
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, m = lane & 15, g = lane >> 4;
   const int N = static_cast<int>(p.dstate), P = static_cast<int>(p.headdim), H = static_cast<int>(p.nheads);
   const int groups = (P + 15) / 16;
-  const int bh = static_cast<int>(blockIdx.x) / groups, p0 = (static_cast<int>(blockIdx.x) % groups) * 16;
+  const int place = gdr_xcd_place(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), groups);
+  const int bh = place / groups, p0 = place % groups * 16;
   const int64_t len = gdr_row_steps(p.seqlens, bh / H, p.seqlen);
   const int64_t most = static_cast<int64_t>(seg_chunks) * kGdrC;
   const float* maps = ws.map + static_cast<int64_t>(bh) * segs * (P + N) * N;
