@@ -4,7 +4,9 @@
 // side effects (and without a HIP device being present at all).
 #include <cstdint>
 
+#include "gated_delta_args.h"
 #include "kernels.h"
+#include "rms_norm.h"
 #include "ssm_scan.h"
 
 namespace {

@@ -4,7 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include "device_math.h"
-#include "kernels.h"
+#include "gated_delta_args.h"
 
 namespace ssm {
 

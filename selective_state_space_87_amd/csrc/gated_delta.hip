@@ -22,7 +22,6 @@
 #include "device_math.h"
 #include "gated_delta.h"
 #include "gdr_mma.h"
-#include "kernels.h"
 
 namespace ssm {
 

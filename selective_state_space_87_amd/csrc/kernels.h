@@ -108,70 +108,6 @@ struct SsdArgs {
 constexpr int64_t kSsdMaxHeadDim = 64;
 constexpr int64_t kSsdMaxState = 128;
 
-struct GatedDeltaArgs {
-  const void* q;          // [B, L, G, N], steps q_step elements apart
-  const void* k;          // [B, L, G, N]
-  const void* v;          // [B, L, H, P]
-  const void* dt;         // [B, L, H]
-  const float* A;         // [H]
-  const void* beta;       // [B, L, H]
-  const float* dt_bias;   // [H] or null
-  const float* h0;        // [B, H, P, N] or null
-  const int32_t* seqlens; // [B] or null
-  void* y;                // [B, L, H, P]
-  float* h_final;         // [B, H, P, N] or null
-  void* workspace;
-  int64_t batch, seqlen, nkheads, nheads, headdim, dstate;
-  int64_t q_step, k_step, v_step;
-  float scale;
-  int in_bf16, out_bf16, dt_softplus, beta_sigmoid, qk_l2norm;
-};
-
-struct GatedDeltaBwdArgs {
-  GatedDeltaArgs f;       // the forward's inputs (y and h_final unused)
-  const float* dy;
-  const float* dh_final;
-  float* dq;
-  float* dk;
-  float* dv;
-  float* ddt;
-  float* dA;
-  float* dbeta;
-  float* ddt_bias;
-  float* dh0;
-};
-
-struct RmsNormArgs {
-  const void* x;
-  const void* residual;   // or null
-  const float* weight;    // or null
-  void* y;
-  void* residual_out;     // or null
-  float* scales;          // or null
-  int64_t rows, dim;
-  int in_bf16, res_bf16, out_type;  // out_type: 0 float32, 1 bfloat16, 2 e4m3
-  float eps;
-};
-
-struct RmsNormBwdArgs {
-  const void* s;
-  const float* weight;    // or null
-  const float* dy;
-  const float* dresidual; // or null
-  float* ds;
-  float* dweight;         // or null
-  void* workspace;
-  int64_t rows, dim;
-  int s_bf16;
-  float eps;
-};
-
-constexpr int64_t kGdrMaxHeadDim = 256;
-constexpr int64_t kGdrMaxState = 128;
-constexpr float kGdrMinLogDecay = -200.0f;  // exp of it is 0 in float32
-constexpr float kL2NormEps = 1e-6f;
-constexpr int64_t kRmsMaxDim = 16384;
-
 // How a scan of a given shape is run. The sequence is split into `chunks`
 // pieces of `chunk` steps (the last may be shorter) when there are too few
 // channel blocks to fill the device, or when one batch row's [L, d] plane is
@@ -267,52 +203,5 @@ int scan_tile_steps(int NS);
 int launch_conv1d_fwd(const ConvArgs& a, void* stream);
 int launch_conv1d_update(const ConvUpdateArgs& a, void* stream);
 int launch_ssd(const SsdArgs& a, void* stream);
-
-// Weak: the validation front end also links without these kernels (a host-only
-// build with stand-ins for the scan's launchers); a call that passes
-// validation there reports a launch failure.
-__attribute__((weak)) int launch_gated_delta(const GatedDeltaArgs& a, void* stream);
-__attribute__((weak)) int launch_gated_delta_update(const GatedDeltaArgs& a, void* stream);  // h_final: the state
-__attribute__((weak)) int launch_gated_delta_bwd(const GatedDeltaBwdArgs& a, void* stream);
-__attribute__((weak)) int launch_rms_norm(const RmsNormArgs& a, void* stream);
-__attribute__((weak)) int launch_rms_norm_bwd(const RmsNormBwdArgs& a, void* stream);
-
-// How a gated delta rule of given sizes runs forward: as a plain recurrence
-// (one launch, no workspace) or in chunks of 64 steps, with the workspace
-// holding the chunks' triangular inverses, output weights, keys and queries
-// (halves) and per-step factors. A pure function of the sizes.
-struct GdrPlan {
-  bool recurrent;
-  int64_t chunks;  // per batch row
-  // Forward of few heads and many chunks: `segs` segments of seg_chunks chunks,
-  // walked at the same time from states that a pass before has found.
-  int64_t segs, seg_chunks;
-  size_t off_map, off_seg;
-  size_t off_t, off_p, off_k, off_q, off_fac;
-  size_t off_tt, off_s, off_x, off_e, off_top, off_part;  // backward only
-  size_t bytes;
-};
-// Up to this length the recurrence is taken: its time grows with the steps, a
-// chunk's does not. Measured (bf16, N = P = 128, chunks against recurrence) at 4, 8
-// and 16 steps: 2 heads 19 us against 18, 20, 32; 256 heads 51 against 20, 27, 45;
-// 2048 heads 242 against 109, 175, 315.
-constexpr int64_t kGdrRecurrentSteps = 8;
-// Segments: with at most kGdrFewSlices slices of 16 columns (batch, heads and
-// head size together) the walks of whole sequences leave most of the device
-// idle, and finding the segments' states first (a pass over P + N columns in
-// place of P) costs less than it gives. As many segments as make
-// kGdrManySlices slices, 4 to 32, of at least kGdrSegChunks chunks. Measured
-// (bf16, N = P = 128, whole -> in segments): 1 head of 65536 steps 1761 -> 281
-// us, 8 heads 2109 -> 830, 16 heads (128 slices) 2273 -> 1345; 4 heads of 4096
-// steps 129 -> 88, 2 of 2048 74 -> 63 (in two segments 80).
-constexpr int64_t kGdrFewSlices = 128, kGdrManySlices = 1024, kGdrSegChunks = 8, kGdrMinSegs = 4, kGdrMaxSegs = 32;
-GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, int64_t headdim,
-                         int64_t dstate, int in_bf16, bool backward);
-size_t gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
-                                   int64_t headdim, int64_t dstate, int in_bf16);
-size_t gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
-                                       int64_t headdim, int64_t dstate, int in_bf16);
-// Blocks of the norm's backward, each with one partial row of dweight.
-int64_t rms_norm_bwd_blocks(int64_t rows, int64_t dim);
 
 }  // namespace ssm

@@ -137,73 +137,4 @@ size_t scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t 
   return p.ok ? p.bytes : 0;
 }
 
-GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, int64_t headdim,
-                         int64_t dstate, int in_bf16, bool backward) {
-  GdrPlan p{};
-  p.recurrent = !backward && (seqlen <= kGdrRecurrentSteps || batch == 0 || nheads == 0);
-  if (p.recurrent) return p;
-  p.chunks = ceil_div(seqlen, 64);
-  if (p.chunks == 0 || batch == 0 || nheads == 0) {  // (backward of nothing)
-    p.segs = p.seg_chunks = 1;
-    return p;
-  }
-  const size_t items = static_cast<size_t>(batch * nheads * p.chunks);
-  constexpr size_t kPieces = 6 * 2 * 64 * 8 * 2;  // bytes of T's (or the weights') halves a chunk
-  size_t at = 0;
-  const auto take_n = [&](size_t n, size_t bytes) {
-    const size_t here = at;
-    at = align256(at + n * bytes);
-    return here;
-  };
-  const auto take = [&](size_t item_bytes) { return take_n(items, item_bytes); };
-  p.off_t = take(kPieces);
-  p.off_p = take(kPieces);
-  const size_t kv_items = static_cast<size_t>(batch * nkheads * p.chunks);
-  const size_t kv = (in_bf16 ? 1 : 2) * 64 * (dstate <= 64 ? 64 : 128) * 2;
-  p.off_k = take_n(kv_items, kv);
-  p.off_q = take_n(kv_items, kv);
-  p.off_fac = take(9 * 64 * 4);
-  p.segs = 1;
-  const int64_t slices = batch * nheads * ceil_div(headdim, 16);
-  if (!backward && slices <= kGdrFewSlices) {
-    int64_t n = kGdrManySlices / slices;
-    if (n > kGdrMaxSegs) n = kGdrMaxSegs;
-    if (n > p.chunks / kGdrSegChunks) n = p.chunks / kGdrSegChunks;
-    if (n >= kGdrMinSegs) p.segs = n;
-  }
-  p.seg_chunks = ceil_div(p.chunks, p.segs);
-  p.segs = ceil_div(p.chunks, p.seg_chunks);
-  if (p.segs > 1) {
-    const size_t heads = static_cast<size_t>(batch * nheads);
-    p.off_map = take_n(heads * static_cast<size_t>(p.segs), static_cast<size_t>((headdim + dstate) * dstate) * 4);
-    p.off_seg = take_n(heads * static_cast<size_t>(p.segs), static_cast<size_t>(headdim * dstate) * 4);
-  }
-  if (backward) {
-    const size_t state = static_cast<size_t>(headdim * dstate) * 4;
-    p.off_tt = take(kPieces);
-    p.off_s = take(state);
-    p.off_x = take(state);
-    p.off_e = take(static_cast<size_t>(64 * headdim) * 4);
-    p.off_top = take(5 * 32 * 4);
-    p.off_part = take(2 * 4);
-  }
-  p.bytes = at;
-  return p;
-}
-
-size_t gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
-                                   int64_t headdim, int64_t dstate, int in_bf16) {
-  return plan_gated_delta(batch, seqlen, nkheads, nheads, headdim, dstate, in_bf16, false).bytes;
-}
-
-size_t gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
-                                       int64_t headdim, int64_t dstate, int in_bf16) {
-  return plan_gated_delta(batch, seqlen, nkheads, nheads, headdim, dstate, in_bf16, true).bytes;
-}
-
-int64_t rms_norm_bwd_blocks(int64_t rows, int64_t dim) {
-  const int64_t groups = ceil_div(rows, dim <= 1024 ? 4 : 1);  // rows a block takes at a time
-  return groups < 512 ? groups : 512;
-}
-
 }  // namespace ssm

@@ -16,7 +16,7 @@
 #include <hip/hip_runtime.h>
 
 #include "device_math.h"
-#include "kernels.h"
+#include "rms_norm.h"
 
 namespace ssm {
 
