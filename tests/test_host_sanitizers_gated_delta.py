@@ -12,13 +12,22 @@ import sys
 
 import pytest
 
-from tests.test_host_sanitizers import CSRC, OUT, ROOT, _runtime
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "selective_state_space_87_amd", "csrc")
+OUT = os.path.join(ROOT, "_build", "sanitize")
+
+
+def _runtime(name):
+    p = subprocess.run(["g++", f"-print-file-name={name}"], capture_output=True, text=True).stdout.strip()
+    return p if os.path.isabs(p) and os.path.exists(p) else None
 
 
 def test_validation_under_asan_and_ubsan():
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not available")
     asan, ubsan = _runtime("libasan.so"), _runtime("libubsan.so")
-    if shutil.which("g++") is None or asan is None or ubsan is None:
-        pytest.skip("g++ or its sanitizer runtimes not available")
+    if asan is None or ubsan is None:
+        pytest.skip("sanitizer runtimes not available")
     os.makedirs(OUT, exist_ok=True)
     lib = os.path.join(OUT, "libssm_scan_gated_delta_sanitized.so")
     srcs = [os.path.join(CSRC, "api.cpp"), os.path.join(CSRC, "plan.cpp"),
