@@ -198,25 +198,27 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
       for (int i = 0; i < 8; ++i) v[i] = bits_to_f32<BF16>(vr[i]);
       const bool more = c + 1 < n_chunks;
       fetch_v(more ? c + 1 : c);
+      // (Stores in no branch either, here and for E: V's loads are counted from the
+      // last access backwards, and behind a store that may have been skipped they
+      // would be waited for with all stores.)
       if constexpr (MODE == kGdrKeep) {
         const int64_t item = item0 + c;
-        if (col_ok) {
-          float* dst = ws.S + (item * P + col) * N;
+        const rsrc_t rs = raw_buffer(ws.S + item * P * N, static_cast<uint32_t>(P * N * 4));
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const int n = n0 + 32 * (j / 2) + 8 * g + 4 * (j & 1);
-            if (N % 4 == 0) {
-              if (n < N) *reinterpret_cast<f32x4_t*>(dst + n) = S[j];
-            } else {
+        for (int j = 0; j < NJ; ++j) {
+          const int n = n0 + 32 * (j / 2) + 8 * g + 4 * (j & 1);
+          const uint32_t at = static_cast<uint32_t>(col * N + n) * 4;
+          if (N % 4 == 0) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, S[j]), rs, col_ok && n < N ? at : kOutOfRange, 0, 0);
+          } else {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (n + i < N) dst[n + i] = S[j][i];
-              }
+            for (int i = 0; i < 4; ++i) {
+              buffer_store_f32<false>(S[j][i], rs, col_ok && n + i < N ? at + static_cast<uint32_t>(4 * i) : kOutOfRange);
             }
           }
         }
-        const float top = lanes16_max(s_top);
-        if (lane == 0 && col < P) ws.top[(item * kGdrMaxima + kMaxS) * kGdrMaxSlots + col / 16 * 2 + r] = top;
+        buffer_store_f32<false>(lanes16_max(s_top), raw_buffer(ws.top + item * kGdrMaxima * kGdrMaxSlots, kGdrMaxima * kGdrMaxSlots * 4),
+                                lane == 0 && col < P ? static_cast<uint32_t>(kMaxS * kGdrMaxSlots + col / 16 * 2 + r) * 4 : kOutOfRange);
       }
 
       // K S on the wave's 32 steps: its own half of S, and the other's.
@@ -358,13 +360,14 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
       if constexpr (W::NBUF == 1) __syncthreads();
       if constexpr (MODE == kGdrKeep) {
         const int64_t item = item0 + c;
-        float* dst = ws.E + item * kGdrC * P;
+        const rsrc_t re = raw_buffer(ws.E + item * kGdrC * P, static_cast<uint32_t>(kGdrC * P * 4));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (col_ok) dst[(32 * r + 16 * (i / 4) + 4 * g + (i % 4)) * P + col] = E[i / 4][i % 4];
+          const uint32_t at = static_cast<uint32_t>((32 * r + 16 * (i / 4) + 4 * g + (i % 4)) * P + col) * 4;
+          buffer_store_f32<false>(E[i / 4][i % 4], re, col_ok ? at : kOutOfRange);
         }
-        const float top = lanes16_max(tiles_absmax<2>(E));
-        if (lane == 0 && col < P) ws.top[(item * kGdrMaxima + kMaxE) * kGdrMaxSlots + col / 16 * 2 + r] = top;
+        buffer_store_f32<false>(lanes16_max(tiles_absmax<2>(E)), raw_buffer(ws.top + item * kGdrMaxima * kGdrMaxSlots, kGdrMaxima * kGdrMaxSlots * 4),
+                                lane == 0 && col < P ? static_cast<uint32_t>(kMaxE * kGdrMaxSlots + col / 16 * 2 + r) * 4 : kOutOfRange);
       }
     }
     if (W::kLag && !lag) __syncthreads();

@@ -314,7 +314,8 @@ __device__ __forceinline__ void gdr_walk_back(const GatedDeltaBwdArgs& a, const 
   f32x2_t fe;
   half8_t Pd[2][2], Po[2][2], Ah[2], Al[2];
   float a_down = 0.0f;
-  // (A load in no branch: it would be waited for where the branches join.)
+  // (A load in no branch: it would be waited for where the branches join. No store
+  // either: loads are counted from the last access backwards.)
   auto fetch_kq = [&](int c) __attribute__((always_inline)) {
     const u32x4_t* K = reinterpret_cast<const u32x4_t*>(ws.K + (kv0 + c) * W::kMat) + ltid;
     const u32x4_t* Q = reinterpret_cast<const u32x4_t*>(ws.Q + (kv0 + c) * W::kMat) + ltid;
@@ -414,9 +415,8 @@ __device__ __forceinline__ void gdr_walk_back(const GatedDeltaBwdArgs& a, const 
 #pragma unroll
     for (int q = 0; q < 2; ++q) tiles_to_operand<true>(Y[2 * q], Y[2 * q + 1], sa.up, Ah[q], Al[q]);
     const float my = lanes16_max(ytop);
-    if (lane == 0 && col < P) {
-      ws.top[((item0 + c) * kGdrMaxima + kMaxDY) * kGdrMaxSlots + col / 16 * 2 + r] = my;
-    }
+    buffer_store_f32<false>(my, raw_buffer(ws.top + (item0 + c) * kGdrMaxima * kGdrMaxSlots, kGdrMaxima * kGdrMaxSlots * 4),
+                            lane == 0 && col < P ? static_cast<uint32_t>(kMaxDY * kGdrMaxSlots + col / 16 * 2 + r) * 4 : kOutOfRange);
   };
   const auto chunk_at = [&](int step) { return step < n_chunks ? n_chunks - 1 - step : 0; };
   if (n_chunks > 0) {
