@@ -161,11 +161,15 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     const float* fac = ws.fac + ((static_cast<int64_t>(b) * H + kh * r) * chunks + c) * (kGdrFactors * kGdrC);
     const float kn = fac[kFacKn * kGdrC + lane], qn = fac[kFacQn * kGdrC + lane];
     const float kup = fac[kFacKup * kGdrC + lane], qup = fac[kFacQup * kGdrC + lane];
+    half8_t kv[kMat / 8 / kThreads], qv[kMat / 8 / kThreads];
+#pragma unroll
+    for (int i = 0; i < kMat / 8 / kThreads; ++i) kv[i] = K[i * kThreads + tid], qv[i] = Q[i * kThreads + tid];
     const Pow2 kf = row_lift(kn, kunit), qf = row_lift(qn, qunit);
-    for (int i = tid; i < kMat / 8; i += kThreads) {
-      const int t = i * 8 % (kGdrC * NP) / NP;
-      reinterpret_cast<half8_t*>(sK)[i] = K[i] * static_cast<_Float16>(__shfl(kf.down, t));
-      reinterpret_cast<half8_t*>(sQ)[i] = Q[i] * static_cast<_Float16>(__shfl(qf.down, t));
+#pragma unroll
+    for (int i = 0; i < kMat / 8 / kThreads; ++i) {
+      const int at = i * kThreads + tid, t = at * 8 % (kGdrC * NP) / NP;
+      reinterpret_cast<half8_t*>(sK)[at] = kv[i] * static_cast<_Float16>(__shfl(kf.down, t));
+      reinterpret_cast<half8_t*>(sQ)[at] = qv[i] * static_cast<_Float16>(__shfl(qf.down, t));
     }
     if (tid < kGdrC) {
       sKn[tid] = kn * kf.up;
@@ -213,30 +217,28 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
       load8_f32<FAST>(ry, static_cast<uint32_t>(trow) * yrow + static_cast<uint32_t>(p0), tcol, P - p0, trow < rows, fy);
       load8_f32<FAST>(re, static_cast<uint32_t>(trow * P + p0), tcol, P - p0, true, fe);
     };
-    fetch(0);
-    // Gates (wave 0; its lane t keeps the step's values for the end).
-    float x = 0.0f;
-    if (w8 == 0) {
-      float ld = 0.0f, beta = 0.0f;
-      if (lane < rows) {
-        const int64_t at = (row0 + lane) * H + h;
-        x = load_elem<BF16>(p.dt, at) + (p.dt_bias ? p.dt_bias[h] : 0.0f);
-        ld = gdr_log_decay(p, load_elem<BF16>(p.dt, at), p.dt_bias ? p.dt_bias[h] : 0.0f, p.A[h]);
-        beta = gdr_beta(p, load_elem<BF16>(p.beta, at));
-      }
-      sC[lane] = wave_prefix(static_cast<double>(ld) * kLog2eD, lane);
-      sBeta[lane] = beta;
-    }
-    Pow2 top[kGdrMaxima];
+    // What the gates and the scales need, then the first pieces: loads in no branch.
+    const int64_t gate_at = (row0 + (lane < rows ? lane : rows - 1)) * H + h;
+    const float dt_raw = load_elem<BF16>(p.dt, gate_at), beta_raw = load_elem<BF16>(p.beta, gate_at);
+    const float dt_bias = p.dt_bias ? p.dt_bias[h] : 0.0f, A = p.A[h];
+    float tops[kGdrMaxima];
     {
       const float* t = ws.top + item * kGdrMaxima * kGdrMaxSlots;
-      const int slots = (P + 15) / 16 * 2;
+      const int slots = (P + 15) / 16 * 2, slot = (lane & 31) < slots ? lane & 31 : slots - 1;
 #pragma unroll
-      for (int k = 0; k < kGdrMaxima; ++k) {
-        const float v = (lane & 31) < slots ? t[k * kGdrMaxSlots + (lane & 31)] : 0.0f;
-        top[k] = pow2_to_top(lanes16_max(col_max(v)));
-      }
+      for (int k = 0; k < kGdrMaxima; ++k) tops[k] = t[k * kGdrMaxSlots + slot];
     }
+    fetch(0);
+    // Gates (wave 0; its lane t keeps the step's values for the end).
+    const float x = dt_raw + dt_bias;
+    if (w8 == 0) {
+      const float ld = lane < rows ? gdr_log_decay(p, dt_raw, dt_bias, A) : 0.0f;
+      sC[lane] = wave_prefix(static_cast<double>(ld) * kLog2eD, lane);
+      sBeta[lane] = lane < rows ? gdr_beta(p, beta_raw) : 0.0f;
+    }
+    Pow2 top[kGdrMaxima];
+#pragma unroll
+    for (int k = 0; k < kGdrMaxima; ++k) top[k] = pow2_to_top(lanes16_max(col_max(tops[k])));
 
     f32x4_t n1[NJ], n2[NJ], n3[NJ], tri[4];
 #pragma unroll
@@ -493,7 +495,6 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
         const double o = __shfl_down(suffix, d);
         if (lane + d < 64) suffix += o;
       }
-      const float A = p.A[h];
       const float dt = p.dt_softplus ? softplus_f(x) : x;
       float dg = static_cast<float>(suffix + static_cast<double>(at_end));
       if (lane >= rows || dt * A < kGdrMinLogDecay) dg = 0.0f;  // behind the end; where the decay was cut off
