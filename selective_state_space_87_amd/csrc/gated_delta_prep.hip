@@ -87,6 +87,18 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
   const int rows = static_cast<int>(len - t0 < kGdrC ? len - t0 : kGdrC);
   const int64_t row0 = static_cast<int64_t>(b) * p.seqlen + t0;
 
+  // The gates of a head, read before the work in front of their use (lane t has
+  // step t; loads in no branch).
+  const int64_t gate_row = (row0 + (lane < rows ? lane : rows - 1)) * H + kh * heads;
+  float dt_raw, beta_raw, dt_bias, A;
+  const auto fetch_gates = [&](int hh) __attribute__((always_inline)) {
+    dt_raw = load_elem<BF16>(p.dt, gate_row + hh);
+    beta_raw = load_elem<BF16>(p.beta, gate_row + hh);
+    dt_bias = p.dt_bias ? p.dt_bias[kh * heads + hh] : 0.0f;
+    A = p.A[kh * heads + hh];
+  };
+  fetch_gates(0);
+
   gdr_stage_kq<NP, BF16, VEC>(p, row0, rows, kh, tid, sK, sQ, ws.K + static_cast<int64_t>(blockIdx.x) * kMat,
                               ws.Q + static_cast<int64_t>(blockIdx.x) * kMat, sKn, sQn, sKup, sQup);
   __syncthreads();
@@ -149,17 +161,13 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
     float* fac = ws.fac + item * (kGdrFactors * kGdrC);
     // Gates: lane t of wave 0. (Sums in units of log 2, for the base-2 exponential.)
     if (w == 0) {
-      float ld = 0.0f, beta = 0.0f;
-      if (lane < rows) {
-        const int64_t at = (row0 + lane) * H + h;
-        ld = gdr_log_decay(p, load_elem<BF16>(p.dt, at), p.dt_bias ? p.dt_bias[h] : 0.0f, p.A[h]);
-        beta = gdr_beta(p, load_elem<BF16>(p.beta, at));
-      }
+      const float ld = lane < rows ? gdr_log_decay(p, dt_raw, dt_bias, A) : 0.0f;
       const double cs = wave_prefix(static_cast<double>(ld) * kLog2eD, lane);
       sCh[lane] = static_cast<float>(cs);
       sCl[lane] = static_cast<float>(cs - static_cast<double>(static_cast<float>(cs)));
-      sBeta[lane] = beta;
+      sBeta[lane] = lane < rows ? gdr_beta(p, beta_raw) : 0.0f;
     }
+    fetch_gates(hh + 1 < heads ? hh + 1 : hh);
     __syncthreads();  // gates; K and Q (or the last head's M) are done with
     const auto decay = [&](float hi, float lo, float hi0, float lo0) __attribute__((always_inline)) {
       return exp2_hw((hi - hi0) + (lo - lo0));
