@@ -250,14 +250,14 @@ __device__ __forceinline__ int kq_at(int t, int n) {
 }
 
 // The rows of K and Q of a chunk as halves, by a block of 256 threads: four
-// lanes a row, 8 elements a piece; into LDS and into the workspace ([RAW][64]
+// lanes a row, 8 elements a piece; into LDS and (keep) into the workspace ([RAW][64]
 // [NP] each, lo halves behind the hi ones). kn, qn: a row's norm factor (1
 // without the norm) times the inverse of its power of two; kup, qup: that
 // power. Rows past `rows` are 0.
 template <int NP, bool BF16, bool VEC>
 __device__ __forceinline__ void gdr_stage_kq(const GatedDeltaArgs& p, int64_t row0, int rows, int kh, int tid,
-                                             _Float16* sK, _Float16* sQ, _Float16* gK, _Float16* gQ, float* kn,
-                                             float* qn, float* kup, float* qup) {
+                                             _Float16* sK, _Float16* sQ, bool keep, _Float16* gK, _Float16* gQ,
+                                             float* kn, float* qn, float* kup, float* qup) {
   constexpr int RAW = BF16 ? 1 : 2;
   const int N = static_cast<int>(p.dstate);
   const int t = tid >> 2, part = tid & 3;
@@ -297,11 +297,11 @@ __device__ __forceinline__ void gdr_stage_kq(const GatedDeltaArgs& p, int64_t ro
       const int at = kq_at<NP>(t, 32 * i + 8 * part);
       const half8_t hi = halves(x[i]);
       *reinterpret_cast<half8_t*>(dst + at) = hi;
-      *reinterpret_cast<half8_t*>(out + at) = hi;
+      if (keep) *reinterpret_cast<half8_t*>(out + at) = hi;
       if constexpr (RAW == 2) {
         const half8_t lo = rest(x[i], hi);
         *reinterpret_cast<half8_t*>(dst + kGdrC * NP + at) = lo;
-        *reinterpret_cast<half8_t*>(out + kGdrC * NP + at) = lo;
+        if (keep) *reinterpret_cast<half8_t*>(out + kGdrC * NP + at) = lo;
       }
     }
     if (part == 0) {
