@@ -588,6 +588,15 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
       fetch_T(0);
       fetch_P(0);
     }
+    // As many stores behind these loads as y's are behind a later chunk's: the loads
+    // are counted from the last access backwards, for the first chunk and the later
+    // ones alike, and T would else be waited for with all of y's stores. (A buffer
+    // of no bytes: nothing is written.)
+    if constexpr (!LAG && !KEEP) {
+      const rsrc_t none = raw_buffer(p.y, 0);
+#pragma unroll
+      for (int i = 0; i < 8 * W::kHalvesOut; ++i) buffer_store_f32<OB16>(0.0f, none, static_cast<uint32_t>(16 * i));
+    }
     __syncthreads();
     for (int c = 0; c < n_chunks; ++c) {
       const auto move = [&]() __attribute__((always_inline)) {
