@@ -21,11 +21,13 @@
 // row tile w % 4 and half w / 4 of the N columns (and of dP and M: the one or
 // the other). The heads that share q and k are taken one after another, their
 // dq and dk added in registers: no partial sums in memory, no atomics.
-// Measured at (2, 4096, 16 heads of 128 x 128), bfloat16 inputs, 0.54 GB in: 251
-// us, one block a CU. (Four waves a block: 600 us, for the 192 registers of a
-// wave's accumulators left none for operands. Gq and Gk in float32, made into
-// halves once for each of the four products: 281 us.) The staged pieces of S and
-// X, split into halves by all waves between two barriers, take the most.
+// Measured at (2, 4096, 16 heads of 128 x 128), bfloat16 inputs, 0.55 GB in and
+// 0.13 GB out: 235 us, one block a CU. (Four waves a block: 600 us, for the 192
+// registers of a wave's accumulators left none for operands. Gq and Gk in
+// float32, made into halves once for each of the four products: 30 us more. Gates
+// and scales read where they are used: 17 us more. Addresses kept over the heads,
+// which spilled: 10 us more.) While the pieces of S and X are read, a quarter of
+// the time, HBM gives 4.3 TB/s; between, it waits for the products.
 #include <hip/hip_runtime.h>
 
 #include "gdr_mma.h"
@@ -81,6 +83,11 @@ __device__ __forceinline__ half8_t kq_column8(const _Float16* mat, int r0, int c
                                  5, 6, 7);
 }
 
+// A value that all lanes share, in a scalar register.
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+
 __device__ __forceinline__ float wave_sum64(float v) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
@@ -96,7 +103,7 @@ __device__ __forceinline__ float wave_sum64(float v) {
 // to 2^-24 of the largest.
 __device__ __forceinline__ Pow2 row_lift(float f, Pow2& unit) {
   const int e = static_cast<int>(__float_as_uint(f) >> 23) & 255;
-  const int top = static_cast<int>(__float_as_uint(lanes16_max(col_max(f))) >> 23) & 255;
+  const int top = static_cast<int>(__float_as_uint(uniform(lanes16_max(col_max(f)))) >> 23) & 255;
   const int u = top < 8 ? 8 : (top > 246 ? 246 : top);
   unit = Pow2{__uint_as_float(static_cast<uint32_t>(254 - u) << 23), __uint_as_float(static_cast<uint32_t>(u) << 23)};
   int j = top - 8 - e;
@@ -218,13 +225,13 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
       load8_f32<FAST>(re, static_cast<uint32_t>(trow * P + p0), tcol, P - p0, true, fe);
     };
     // What the gates and the scales need, then the first pieces: loads in no branch.
-    const int64_t gate_at = (row0 + (lane < rows ? lane : rows - 1)) * H + h;
+    const int64_t gate_at = (row0 + (place < rows ? place : rows - 1)) * H + h;
     const float dt_raw = load_elem<BF16>(p.dt, gate_at), beta_raw = load_elem<BF16>(p.beta, gate_at);
     const float dt_bias = p.dt_bias ? p.dt_bias[h] : 0.0f, A = p.A[h];
     float tops[kGdrMaxima];
     {
       const float* t = ws.top + item * kGdrMaxima * kGdrMaxSlots;
-      const int slots = (P + 15) / 16 * 2, slot = (lane & 31) < slots ? lane & 31 : slots - 1;
+      const int slots = (P + 15) / 16 * 2, slot = (place & 31) < slots ? place & 31 : slots - 1;
 #pragma unroll
       for (int k = 0; k < kGdrMaxima; ++k) tops[k] = t[k * kGdrMaxSlots + slot];
     }
@@ -232,13 +239,13 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     // Gates (wave 0; its lane t keeps the step's values for the end).
     const float x = dt_raw + dt_bias;
     if (w8 == 0) {
-      const float ld = lane < rows ? gdr_log_decay(p, dt_raw, dt_bias, A) : 0.0f;
-      sC[lane] = wave_prefix(static_cast<double>(ld) * kLog2eD, lane);
-      sBeta[lane] = lane < rows ? gdr_beta(p, beta_raw) : 0.0f;
+      const float ld = place < rows ? gdr_log_decay(p, dt_raw, dt_bias, A) : 0.0f;
+      sC[place] = wave_prefix(static_cast<double>(ld) * kLog2eD, place);
+      sBeta[place] = place < rows ? gdr_beta(p, beta_raw) : 0.0f;
     }
     Pow2 top[kGdrMaxima];
 #pragma unroll
-    for (int k = 0; k < kGdrMaxima; ++k) top[k] = pow2_to_top(lanes16_max(col_max(tops[k])));
+    for (int k = 0; k < kGdrMaxima; ++k) top[k] = pow2_to_top(uniform(lanes16_max(col_max(tops[k]))));
 
     f32x4_t n1[NJ], n2[NJ], n3[NJ], tri[4];
 #pragma unroll
@@ -299,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
       }
     }
     dot = wave_sum64(dot);
-    if (lane == 0) sDot[w8] = dot;
+    if (place == 0) sDot[w8] = dot;
     __syncthreads();  // the staged pieces are done with; Gq and Gk take their place
 
     const double cend = sC[kGdrC - 1];
@@ -361,7 +368,7 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
         if (g == 0) sCol[w8][s] = col_z;
       }
       mx = lanes16_max(col_max(mx));
-      if (lane == 0) sTop[w8] = mx;
+      if (place == 0) sTop[w8] = mx;
     }
     // Row products with N1, N2, N3, and their parts of dq and dk.
     {
@@ -475,14 +482,15 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
 
     // The gates: lane t of wave 0.
     if (w8 == 0) {
-      const double cl = sC[lane];
+      const int t = anew(lane);  // (its addresses are not kept from one head to the next)
+      const double cl = sC[t];
       const float in = exp2_hw(static_cast<float>(cl));
       const float last = exp2_hw(static_cast<float>(cend - cl));
-      const float beta = sBeta[lane];
+      const float beta = sBeta[t];
       float colz = 0.0f, dots = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) colz += sCol[k][lane], dots += sDot[k];
-      const auto row = [&](int k) { return sRow[k][0][lane] + sRow[k][1][lane]; };
+      for (int k = 0; k < 8; ++k) colz += sCol[k][t], dots += sDot[k];
+      const auto row = [&](int k) { return sRow[k][0][t] + sRow[k][1][t]; };
       const float r3 = row(2);
       const float w3 = beta * last * r3;
       const float dc = p.scale * in * row(0) - in * row(1) - w3 + row(3) - beta * colz;
@@ -493,22 +501,23 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
         const double o = __shfl_down(suffix, d);
-        if (lane + d < 64) suffix += o;
+        if (t + d < 64) suffix += o;
       }
       const float dt = p.dt_softplus ? softplus_f(x) : x;
       float dg = static_cast<float>(suffix + static_cast<double>(at_end));
-      if (lane >= rows || dt * A < kGdrMinLogDecay) dg = 0.0f;  // behind the end; where the decay was cut off
+      if (t >= rows || dt * A < kGdrMinLogDecay) dg = 0.0f;  // behind the end; where the decay was cut off
       float ddt = dg * A;
       if (p.dt_softplus) ddt *= sigmoid_f(x);
       float db = dbeta;
       if (p.beta_sigmoid) db *= beta * (1.0f - beta);
-      if (lane < out_rows) {
-        a.ddt[(row0 + lane) * H + h] = lane < rows ? ddt : 0.0f;
-        a.dbeta[(row0 + lane) * H + h] = lane < rows ? db : 0.0f;
+      if (t < out_rows) {
+        const int64_t at = (row0 + t) * H + h;
+        a.ddt[at] = t < rows ? ddt : 0.0f;
+        a.dbeta[at] = t < rows ? db : 0.0f;
       }
-      const float da = wave_sum64(lane < rows && dg != 0.0f ? dg * dt : 0.0f);
-      const float dbias = wave_sum64(lane < rows ? ddt : 0.0f);
-      if (lane == 0) {
+      const float da = wave_sum64(t < rows && dg != 0.0f ? dg * dt : 0.0f);
+      const float dbias = wave_sum64(t < rows ? ddt : 0.0f);
+      if (t == 0) {
         ws.part[item] = da;
         ws.part[items + item] = dbias;
       }
