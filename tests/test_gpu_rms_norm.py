@@ -123,6 +123,18 @@ def test_more_rows_than_a_launch_takes():
         assert torch.equal(out["residual_out"][a:a + 3], part["residual_out"])
 
 
+def test_more_elements_than_32_bits_count():
+    rows, dim = (1 << 20) + 9, 4096 + 8
+    x = torch.empty(rows, dim, device="cuda", dtype=torch.bfloat16)
+    w = 1.0 + 0.1 * torch.randn(dim, device="cuda")
+    ends = (0, (1 << 20) - 2, rows - 4)
+    for a in ends:
+        x[a:a + 4] = torch.randn(4, dim, device="cuda")
+    y = binding.ssm_rms_norm_fwd(x, w)["y"]
+    for a in ends:
+        assert torch.equal(y[a:a + 4], binding.ssm_rms_norm_fwd(x[a:a + 4].clone(), w)["y"])
+
+
 def test_not_finite_rows_stay_their_own():
     x = data(4, 96, 5, torch.float32)[0]
     want = binding.ssm_rms_norm_fwd(x, out_dtype=T["e4m3"])
