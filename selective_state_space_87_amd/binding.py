@@ -595,17 +595,28 @@ def _gdr_inputs(q, k, v, dt, A, beta, dt_bias, lead):
             raise ValueError(f"{name} must be a {lead + 2}-d tensor")
     if q.dtype not in _DTYPE_CODE:
         raise ValueError(f"unsupported input dtype {q.dtype}")
-    dev, ind = q.device, q.dtype
-    rows, (G, N), (H, P) = tuple(q.shape[:lead]), q.shape[lead:], v.shape[lead:]
-    _strided_tensor("q", q, rows + (G, N), ind, dev)
-    _strided_tensor("k", k, rows + (G, N), ind, dev)
-    _strided_tensor("v", v, rows + (H, P), ind, dev)
-    _dev_tensor("dt", dt, rows + (H,), (ind,), dev)
-    _dev_tensor("beta", beta, rows + (H,), (ind,), dev)
-    _dev_tensor("A", A, (H,), (torch.float32,), dev)
+    dev, ind, qs, vs = q.device, q.dtype, q.shape, v.shape
+    rows, G, N, H, P = tuple(qs[:lead]), qs[lead], qs[lead + 1], vs[lead], vs[lead + 1]
+    heads = rows + (H,)
+    # all is as it should be: one expression, as in _dev_tensor
+    try:
+        fits = (q.is_cuda and k.shape == qs and vs == rows + (H, P) and dt.shape == heads and beta.shape == heads
+                and A.shape == (H,) and k.dtype == ind and v.dtype == ind and dt.dtype == ind and beta.dtype == ind
+                and A.dtype == torch.float32 and k.device == dev and v.device == dev and dt.device == dev
+                and beta.device == dev and A.device == dev and dt.is_contiguous() and beta.is_contiguous()
+                and A.is_contiguous())
+    except AttributeError:  # not a tensor
+        fits = False
+    if not fits:
+        _strided_tensor("q", q, rows + (G, N), ind, dev)
+        _strided_tensor("k", k, rows + (G, N), ind, dev)
+        _strided_tensor("v", v, rows + (H, P), ind, dev)
+        if dt is None or beta is None or A is None:
+            raise ValueError("dt, A and beta are required")
+        _dev_tensor("dt", dt, heads, (ind,), dev)
+        _dev_tensor("beta", beta, heads, (ind,), dev)
+        _dev_tensor("A", A, (H,), (torch.float32,), dev)
     _dev_tensor("dt_bias", dt_bias, (H,), (torch.float32,), dev)
-    if dt is None or beta is None or A is None:
-        raise ValueError("dt, A and beta are required")
     steps = (_step_of("q", q, lead, G * N), _step_of("k", k, lead, G * N), _step_of("v", v, lead, H * P))
     return rows, G, H, P, N, dev, steps
 
