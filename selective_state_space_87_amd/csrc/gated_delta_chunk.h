@@ -152,7 +152,8 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
     }
     // The wave's rows of V, a chunk ahead. (No load of a next chunk stands in a
     // branch, here or below: it would be waited for where the branches join.)
-    uint32_t vr[8];
+    // (bfloat16 as 16 bits until it is used: carried in 32 it is masked every time.)
+    std::conditional_t<BF16, uint16_t, uint32_t> vr[8];
     const uint32_t vs = static_cast<uint32_t>(p.v_step);
     const uint32_t vbase = col_ok ? (static_cast<uint32_t>(32 * r + 4 * g) * vs + static_cast<uint32_t>(col)) * EB : 0x80000000u;
     auto fetch_v = [&](int c) __attribute__((always_inline)) {
@@ -161,7 +162,8 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
       const rsrc_t rv = rows_buffer<EB>(p.v, (row_b + t0) * p.v_step + static_cast<int64_t>(h) * P, rows, vs, P);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        vr[i] = buffer_load_bits<BF16>(rv, vbase + static_cast<uint32_t>(16 * (i / 4) + (i % 4)) * vs * EB);
+        vr[i] = static_cast<std::remove_reference_t<decltype(vr[i])>>(
+            buffer_load_bits<BF16>(rv, vbase + static_cast<uint32_t>(16 * (i / 4) + (i % 4)) * vs * EB));
       }
     };
 
@@ -195,7 +197,13 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
       };
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = bits_to_f32<BF16>(vr[i]);
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (BF16) {
+          v[i] = static_cast<float>(__builtin_bit_cast(__bf16, vr[i]));
+        } else {
+          v[i] = __uint_as_float(vr[i]);
+        }
+      }
       const bool more = c + 1 < n_chunks;
       fetch_v(more ? c + 1 : c);
       // (Stores in no branch either, here and for E: V's loads are counted from the
