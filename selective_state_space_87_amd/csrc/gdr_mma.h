@@ -72,9 +72,10 @@ struct Pow2 {
   float up, down;
 };
 __device__ __forceinline__ Pow2 pow2_to_top(float m) {
-  int e = static_cast<int>(__float_as_uint(m) >> 23);
-  e = e < 27 ? 27 : (e > 254 ? 254 : e);
-  return Pow2{__uint_as_float(static_cast<uint32_t>(267 - e) << 23), __uint_as_float(static_cast<uint32_t>(e - 13) << 23)};
+  uint32_t e = __float_as_uint(m) & 0x7f800000u;  // the exponent where it stands
+  e = e > 27u << 23 ? e : 27u << 23;
+  e = e < 254u << 23 ? e : 254u << 23;
+  return Pow2{__uint_as_float((267u << 23) - e), __uint_as_float(e - (13u << 23))};
 }
 
 // Largest value over the lanes l, l ^ 16, l ^ 32, l ^ 48 (those that share a column of D).
