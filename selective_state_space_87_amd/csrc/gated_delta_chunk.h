@@ -14,7 +14,10 @@
 //   Y = diag(scale e^c) Q S + Pm E
 // one phase behind, and move K, Q, T, Pm and the factors of the next chunk from
 // memory through their registers into LDS. A chain as long as this is bound by
-// what a single wave can issue, not by the units.
+// what a single wave can issue, not by the units. Measured at (4, 8192, 16 key and
+// 32 value heads of 128 x 128), bfloat16: 500 us (one wave for all of a slice's
+// work 790, a pair without waves for y and the loads 590), 3.9 us a chunk with four
+// pairs a CU; vector instructions 54 % of a SIMD's cycles, LDS 53 %, matrix cores 24 %.
 #pragma once
 
 #include "gdr_mma.h"

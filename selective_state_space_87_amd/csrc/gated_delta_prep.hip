@@ -19,6 +19,8 @@
 // Sums of log decays are in double, and kept as two floats whose differences
 // are taken apart: behind a step that forgets nearly everything the sums are
 // large and the differences small.
+// Measured at (4, 8192, 16 key and 32 value heads of 128 x 128), bfloat16: 194 us
+// for 0.28 GB in and 0.59 GB out, 4.5 TB/s. (T through LDS and stored from there: 216.)
 #include <hip/hip_runtime.h>
 
 #include "gdr_mma.h"

