@@ -463,8 +463,8 @@ int ssm_ssd_fwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, 
  *
  * q, k, v, dt, beta and y need the alignment of their element type only; rows
  * that start on 16-byte boundaries with N and P multiples of 8 are read
- * fastest. Products are taken in 22 bits or more of every float32 operand (11
- * bits in those that only a bfloat16 y sees) and added in float32; results are
+ * fastest. Products are taken in 22 bits or more of every float32 operand and
+ * added in float32; a bfloat16 y is the float32 y rounded once. Results are
  * bitwise deterministic. Errors grow as the products of the steps' maps
  * exp(dt A) (1 - beta k k^T) do: not at all where 0 <= beta |k|^2 <= 2, as with
  * both the sigmoid and the norm. A value of a step that is not finite may make

@@ -225,7 +225,7 @@ bool rows_on_16(const GatedDeltaArgs& a) {
 }
 
 int launch_chunks(const GatedDeltaArgs& a, const GdrWork& ws, const GdrPlan& pl, bool backward, void* stream) {
-  if (const int e = launch_gdr_prep(a, ws, pl.chunks, !a.out_bf16, backward, rows_on_16(a), stream)) return e;
+  if (const int e = launch_gdr_prep(a, ws, pl.chunks, backward, rows_on_16(a), stream)) return e;
   if (backward && gdr_both_at_once(a)) return 0;  // (walked by launch_gdr_reverse)
   return a.in_bf16 ? launch_gdr_chunk_b(a, ws, pl, backward, stream)
                    : launch_gdr_chunk_f(a, ws, pl, backward, stream);

@@ -13,7 +13,9 @@
 // waves: waves of their own read S and E from the exchange and form
 //   Y = diag(scale e^c) Q S + Pm E
 // one phase behind, and move K, Q, T, Pm and the factors of the next chunk from
-// memory through their registers into LDS. A chain as long as this is bound by
+// memory through their registers into LDS. Every product is of two halves, for a
+// bfloat16 y too: with one in those of y, y is off by 2^-11 of its terms, which
+// cancel, and the layer below took 568 us in place of 654. A chain as long as this is bound by
 // what a single wave can issue, not by the units. Measured at (4, 8192, 16 key and
 // 32 value heads of 128 x 128), bfloat16: 500 us (one wave for all of a slice's
 // work 790, a pair without waves for y and the loads 590), 3.9 us a chunk with four
@@ -33,7 +35,6 @@ template <int NP, bool BF16, bool OB16, int NPAIR, int MODE>
 struct GdrWalk {
   static constexpr bool KEEP = MODE != kGdrForward;
   static constexpr int RAW = BF16 ? 1 : 2;
-  static constexpr int OP = OB16 ? 1 : 2;               // halves in the products that only y sees
   // Waves for y and the loads: one for every 32 steps of a slice. (KEEP with
   // four pairs: half as many, which have less to load; with sixteen waves a
   // wave's 128 registers would not do.)
@@ -43,18 +44,21 @@ struct GdrWalk {
   static constexpr int NL = 64 * NOUT;                  // threads that load
   static constexpr int kMat = RAW * kGdrC * NP;         // halves of K (or Q)
   static constexpr int kT = kGdrFrags * 2 * kGdrFragHalves;
-  static constexpr int kP = KEEP ? 0 : kGdrFrags * OP * kGdrFragHalves;
+  static constexpr int kP = KEEP ? 0 : kT;
   static constexpr int kFac = 4 * kGdrC + 4;            // K, Q, W, P factors; the end's and T's
   static constexpr int kBufBytes = (KEEP ? 1 : 2) * kMat * 2 + kFac * 4;
-  // a pair's exchange, in halves: S (NP / 32 pieces), R, w E (2), E (2); then scales (floats, a lane each)
+  // a pair's exchange, in halves: S (NP / 32 pieces), R of wave 0, w E (2), E of wave
+  // 0; then scales (floats, a column each). E of wave 1 takes the place of R, which
+  // that wave has read by then, and wave 0 writes again a barrier after E's last use.
   static constexpr int kXS = 0, kXR = kXS + NP / 32 * 2 * kGdrFragHalves, kXD = kXR + 2 * kGdrFragHalves;
-  static constexpr int kXE = kXD + 4 * kGdrFragHalves, kXF = kXE + (KEEP ? 0 : 2 * OP * kGdrFragHalves);
-  static constexpr int kPairBytes = kXF * 2 + 7 * 64 * 4;
+  static constexpr int kXE = kXD + 4 * kGdrFragHalves, kXF = kXE + (KEEP ? 0 : 2 * kGdrFragHalves);
+  static constexpr int kSS = 0, kSD = 32, kSE = 64, kSR = 96, kScales = 112;
+  static constexpr int kPairBytes = kXF * 2 + kScales * 4;
   static constexpr int kFixed = (kT + kP) * 2 + NPAIR * kPairBytes;
   static constexpr int NBUF = 2 * kBufBytes + kFixed <= 160 * 1024 ? 2 : 1;
   // Four pairs (sixteen waves) have 128 registers a wave: enough with one half in
-  // K, Q and in what only y sees. Elsewhere two pairs.
-  static constexpr bool kFits = NBUF * kBufBytes + kFixed <= 160 * 1024 && (KEEP || (RAW == 1 && OP == 1));
+  // K and Q. Elsewhere two pairs.
+  static constexpr bool kFits = NBUF * kBufBytes + kFixed <= 160 * 1024 && (KEEP || RAW == 1);
   // With two buffers, half the pairs run one phase behind the others.
   static constexpr bool kLag = NBUF == 2 && NPAIR >= 2;
   static constexpr int NKQ = kMat / 8 / NL;             // 16-byte pieces of K (and Q) a loading thread
@@ -80,7 +84,7 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
                                          GdrWalkLds<GdrWalk<NP, BF16, OB16, NPAIR, MODE>, NPAIR>& sh) {
   using W = GdrWalk<NP, BF16, OB16, NPAIR, MODE>;
   constexpr bool KEEP = W::KEEP;
-  constexpr int RAW = W::RAW, OP = W::OP;
+  constexpr int RAW = W::RAW;
   constexpr int kLo = kGdrC * NP;                       // from an element's hi half to its lo half
   constexpr int NJ = NP / 32, NK = NP / 64;             // state tiles and operand pieces of a wave
   constexpr int EB = BF16 ? 2 : 4;
@@ -133,9 +137,9 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
     if (MODE == kGdrForward && segs > 1) enters = ws.seg + z * ws.seg_stride;
     _Float16* const xh = reinterpret_cast<_Float16*>(xch[pr]);
     float* const xf = reinterpret_cast<float*>(xh + W::kXF);
-    float *const xs_f = xf, *const xd_f = xf + 128, *const xe_f = xf + 256, *const xr_f = xf + 384;
-    const auto piece = [&](int at, int q, int half, int halves_a_piece) __attribute__((always_inline)) {
-      return reinterpret_cast<half8_t*>(xh + at + (q * halves_a_piece + half) * kGdrFragHalves + lane * 8);
+    float *const xs_f = xf + W::kSS + m, *const xd_f = xf + W::kSD + m, *const xe_f = xf + W::kSE + m, *const xr_f = xf + W::kSR + m;
+    const auto piece = [&](int at, int q, int half) __attribute__((always_inline)) {
+      return reinterpret_cast<half8_t*>(xh + at + (2 * q + half) * kGdrFragHalves + lane * 8);
     };
 
     // The state: tile j = 2 q + u of the wave's half, element i is n = n0 + 32 q
@@ -180,10 +184,10 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
 #pragma unroll
       for (int q = 0; q < NK; ++q) {
         tiles_to_operand<true>(S[2 * q], S[2 * q + 1], s.up, Sh[q], Sl[q]);
-        *piece(W::kXS, r * NK + q, 0, 2) = Sh[q];
-        *piece(W::kXS, r * NK + q, 1, 2) = Sl[q];
+        *piece(W::kXS, r * NK + q, 0) = Sh[q];
+        *piece(W::kXS, r * NK + q, 1) = Sl[q];
       }
-      xs_f[64 * r + lane] = s.down;
+      xs_f[16 * r] = s.down;
     };
     if (n_chunks > 0) fetch_v(0);
     split_S();
@@ -241,8 +245,8 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
 #pragma unroll
         for (int q = 0; q < NK; ++q) {
           const int f = (o == 0 ? r : 1 - r) * NK + q;
-          const half8_t sh = o == 0 ? Sh[q] : *piece(W::kXS, f, 0, 2);
-          const half8_t sl = o == 0 ? Sl[q] : *piece(W::kXS, f, 1, 2);
+          const half8_t sh = o == 0 ? Sh[q] : *piece(W::kXS, f, 0);
+          const half8_t sl = o == 0 ? Sl[q] : *piece(W::kXS, f, 1);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int at = kq_at<NP>(32 * r + 16 * u + m, 32 * f + 8 * g);
@@ -255,7 +259,7 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
           }
         }
       }
-      const float so_down = xs_f[64 * (1 - r) + lane];
+      const float so_down = xs_f[16 * (1 - r)];
       // R = V - diag(e^c) K S; the first 32 steps' also for the other wave.
       half8_t Rh, Rl;
       Pow2 sr;
@@ -272,9 +276,9 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
         sr = pow2_to_top(tiles_absmax<2>(R));
         tiles_to_operand<true>(R[0], R[1], sr.up, Rh, Rl);
         if (r == 0) {
-          *piece(W::kXR, 0, 0, 2) = Rh;
-          *piece(W::kXR, 0, 1, 2) = Rl;
-          xr_f[lane] = sr.down;
+          *piece(W::kXR, 0, 0) = Rh;
+          *piece(W::kXR, 0, 1) = Rl;
+          *xr_f = sr.down;
         }
       }
       __syncthreads();
@@ -298,8 +302,8 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
           for (int i = 0; i < 4; ++i) E[u][i] = acc[i] * down;
         }
         if (r == 1) {
-          const half8_t oh = *piece(W::kXR, 0, 0, 2), ol = *piece(W::kXR, 0, 1, 2);
-          const float other = xr_f[lane] * tri;
+          const half8_t oh = *piece(W::kXR, 0, 0), ol = *piece(W::kXR, 0, 1);
+          const float other = *xr_f * tri;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const half8_t th = T(2 + 2 * u, 0), tl = T(2 + 2 * u, 1);
@@ -325,16 +329,17 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
         }
         sd = pow2_to_top(tiles_absmax<2>(D));
         tiles_to_operand<true>(D[0], D[1], sd.up, Dh, Dl);
-        *piece(W::kXD, r, 0, 2) = Dh;
-        *piece(W::kXD, r, 1, 2) = Dl;
-        xd_f[64 * r + lane] = sd.down;
+        *piece(W::kXD, r, 0) = Dh;
+        *piece(W::kXD, r, 1) = Dl;
+        xd_f[16 * r] = sd.down;
         if constexpr (!KEEP) {
           half8_t Eh, El;
           const Pow2 se = pow2_to_top(tiles_absmax<2>(E));
-          tiles_to_operand<OP == 2>(E[0], E[1], se.up, Eh, El);
-          *piece(W::kXE, r, 0, OP) = Eh;
-          if constexpr (OP == 2) *piece(W::kXE, r, OP - 1, OP) = El;
-          xe_f[64 * r + lane] = se.down;
+          tiles_to_operand<true>(E[0], E[1], se.up, Eh, El);
+          const int at = r == 0 ? W::kXE : W::kXR;
+          *piece(at, 0, 0) = Eh;
+          *piece(at, 0, 1) = El;
+          xe_f[16 * r] = se.down;
         }
       }
       const float end = sF[4 * kGdrC];
@@ -342,8 +347,8 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
 
       // S' = e^(c_end) S + K^T (w E) on the wave's half of the rows
       {
-        const half8_t oh = *piece(W::kXD, 1 - r, 0, 2), ol = *piece(W::kXD, 1 - r, 1, 2);
-        const float d_own = sd.down, d_oth = xd_f[64 * (1 - r) + lane];
+        const half8_t oh = *piece(W::kXD, 1 - r, 0), ol = *piece(W::kXD, 1 - r, 1);
+        const float d_own = sd.down, d_oth = xd_f[16 * (1 - r)];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           f32x4_t acc[2];
@@ -406,9 +411,9 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
   const bool col_ok = col < P;
   const _Float16* const xh = reinterpret_cast<const _Float16*>(xch[pr]);
   const float* const xf = reinterpret_cast<const float*>(xh + W::kXF);
-  const float *const xs_f = xf, *const xe_f = xf + 256;
-  const auto piece = [&](int at, int q, int half, int halves_a_piece) __attribute__((always_inline)) {
-    return *reinterpret_cast<const half8_t*>(xh + at + (q * halves_a_piece + half) * kGdrFragHalves + lane * 8);
+  const float *const xs_f = xf + W::kSS + m, *const xe_f = xf + W::kSE + m;
+  const auto piece = [&](int at, int q, int half) __attribute__((always_inline)) {
+    return *reinterpret_cast<const half8_t*>(xh + at + (2 * q + half) * kGdrFragHalves + lane * 8);
   };
   u32x4_t kr[W::NKQ], qr[KEEP ? 1 : W::NKQ], tr[W::NTL], pm[KEEP ? 1 : W::NPL];
   float fr[W::NFL];
@@ -435,10 +440,7 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
     if constexpr (KEEP) return;
     const u32x4_t* Pm = reinterpret_cast<const u32x4_t*>(ws.Pm + (item0 + c) * kGdrPieceHalves);
 #pragma unroll
-    for (int i = 0; i < W::NPL; ++i) {
-      const int e = (i * W::NL + ltid) % (W::kP / 8);  // (past the end: any)
-      pm[i] = Pm[OP == 2 ? e : 2 * e - (e & 63)];      // with one half a piece, every other 64 of the workspace's
-    }
+    for (int i = 0; i < W::NPL; ++i) pm[i] = Pm[(i * W::NL + ltid) % (W::kP / 8)];  // (past the end: any)
   };
   // K, Q and the factors into a buffer.
   auto stage_kq = [&](int buf) __attribute__((always_inline)) {
@@ -491,22 +493,20 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
 #pragma unroll
           for (int q = 0; q < NK; ++q) {
             const int f = o * NK + q;
-            const half8_t sh = piece(W::kXS, f, 0, 2);
+            const half8_t sh = piece(W::kXS, f, 0), sl = piece(W::kXS, f, 1);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const int at = kq_at<NP>(32 * r + 16 * u + m, 32 * f + 8 * g);
               const half8_t a = *reinterpret_cast<const half8_t*>(sQ + at);
               qs[hf][o][u] = mfma16(a, sh, qs[hf][o][u]);
-              if constexpr (OP == 2) {
-                qs[hf][o][u] = mfma16(a, piece(W::kXS, f, 1, 2), qs[hf][o][u]);
-                if constexpr (RAW == 2) {
-                  qs[hf][o][u] = mfma16(*reinterpret_cast<const half8_t*>(sQ + kLo + at), sh, qs[hf][o][u]);
-                }
+              qs[hf][o][u] = mfma16(a, sl, qs[hf][o][u]);
+              if constexpr (RAW == 2) {
+                qs[hf][o][u] = mfma16(*reinterpret_cast<const half8_t*>(sQ + kLo + at), sh, qs[hf][o][u]);
               }
             }
           }
         }
-        const float d0 = xs_f[lane], d1 = xs_f[64 + lane];
+        const float d0 = xs_f[0], d1 = xs_f[16];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const f32x4_t fq = *reinterpret_cast<const f32x4_t*>(sF + 1 * kGdrC + 32 * r + 16 * u + 4 * g);
@@ -529,39 +529,34 @@ __device__ __forceinline__ void gdr_walk(const GatedDeltaArgs& p, const GdrWork&
       const rsrc_t ry = rows_buffer<OB16 ? 2 : 4>(p.y, (row_b + t0) * yrow + static_cast<int64_t>(h) * P, out_rows,
                                                   yrow, P);
       const auto Pm = [&](int f, int half) __attribute__((always_inline)) {
-        return *reinterpret_cast<const half8_t*>(sP + (OP * f + half) * kGdrFragHalves + lane * 8);
+        return *reinterpret_cast<const half8_t*>(sP + (2 * f + half) * kGdrFragHalves + lane * 8);
       };
 #pragma unroll
       for (int hf = 0; hf < W::kHalvesOut; ++hf) {
         const int r = W::kHalvesOut == 2 ? hf : (ow & 1);
-        const half8_t eh = piece(W::kXE, r, 0, OP);
-        half8_t el;
-        if constexpr (OP == 2) el = piece(W::kXE, r, OP - 1, OP);
-        const float e_own = xe_f[64 * r + lane];
+        const int own = r == 0 ? W::kXE : W::kXR;
+        const half8_t eh = piece(own, 0, 0), el = piece(own, 0, 1);
+        const float e_own = xe_f[16 * r];
         f32x4_t pe[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int f = r == 0 ? u : 3 + 2 * u;
           f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
           acc = mfma16(Pm(f, 0), eh, acc);
-          if constexpr (OP == 2) {
-            acc = mfma16(Pm(f, 0), el, acc);
-            acc = mfma16(Pm(f, 1), eh, acc);
-          }
+          acc = mfma16(Pm(f, 0), el, acc);
+          acc = mfma16(Pm(f, 1), eh, acc);
 #pragma unroll
           for (int i = 0; i < 4; ++i) pe[u][i] = acc[i] * e_own;
         }
         if (r == 1) {
-          const half8_t oh = piece(W::kXE, 0, 0, OP);
-          const float e_oth = xe_f[lane];
+          const half8_t oh = piece(W::kXE, 0, 0), ol = piece(W::kXE, 0, 1);
+          const float e_oth = xe_f[0];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
             acc = mfma16(Pm(2 + 2 * u, 0), oh, acc);
-            if constexpr (OP == 2) {
-              acc = mfma16(Pm(2 + 2 * u, 0), piece(W::kXE, 0, OP - 1, OP), acc);
-              acc = mfma16(Pm(2 + 2 * u, 1), oh, acc);
-            }
+            acc = mfma16(Pm(2 + 2 * u, 0), ol, acc);
+            acc = mfma16(Pm(2 + 2 * u, 1), oh, acc);
 #pragma unroll
             for (int i = 0; i < 4; ++i) pe[u][i] = fmaf(acc[i], e_oth, pe[u][i]);
           }

@@ -53,18 +53,18 @@ __device__ __forceinline__ f32x4_t tile_product(const float* A, int stride, f32x
   return acc;
 }
 
-// The two D tiles 2 q, 2 q + 1 as a piece: its halves times `up` (lo: if asked for).
-__device__ __forceinline__ void store_piece(_Float16* at, f32x4_t a, f32x4_t b, float up, bool lo) {
+// The two D tiles 2 q, 2 q + 1 as a piece: its halves times `up`.
+__device__ __forceinline__ void store_piece(_Float16* at, f32x4_t a, f32x4_t b, float up) {
   const float x[8] = {a[0] * up, a[1] * up, a[2] * up, a[3] * up, b[0] * up, b[1] * up, b[2] * up, b[3] * up};
   const half8_t hi = halves(x);
   *reinterpret_cast<half8_t*>(at) = hi;
-  if (lo) *reinterpret_cast<half8_t*>(at + kGdrFragHalves) = rest(x, hi);
+  *reinterpret_cast<half8_t*>(at + kGdrFragHalves) = rest(x, hi);
 }
 
 // BWD: also the pieces of T^T and, in place of Pm's, those of Pm^T.
 template <int NP, bool BF16, bool VEC, bool BWD>
 __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs p, const GdrWork ws, int chunks,
-                                                            int out_lo, int blocks_a_group) {
+                                                            int blocks_a_group) {
   constexpr int RAW = BF16 ? 1 : 2;
   constexpr int kMat = RAW * kGdrC * NP;              // halves of K (or Q)
   constexpr int kKQ = 2 * kMat * 2;                   // bytes
@@ -232,8 +232,7 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         if (BWD ? (q == 0 && w >= 2) : (q == 1 && w < 2)) continue;
-        store_piece(out + (BWD ? gdr_frag_up(w, q) : gdr_frag(w, q)) * 2 * kGdrFragHalves, x[2 * q], x[2 * q + 1], s.up,
-                    BWD || out_lo);
+        store_piece(out + (BWD ? gdr_frag_up(w, q) : gdr_frag(w, q)) * 2 * kGdrFragHalves, x[2 * q], x[2 * q + 1], s.up);
       }
     }
     if (w == 1) {
@@ -310,39 +309,39 @@ __global__ __launch_bounds__(kThreads) void gdr_prep_kernel(const GatedDeltaArgs
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (q == 1 && w < 2) continue;
-      store_piece(out + gdr_frag(w, q) * 2 * kGdrFragHalves, R[2 * q], R[2 * q + 1], st.up, true);
+      store_piece(out + gdr_frag(w, q) * 2 * kGdrFragHalves, R[2 * q], R[2 * q + 1], st.up);
     }
     if constexpr (BWD) {
       out = ws.Tt + item * kGdrPieceHalves + lane * 8;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         if (q == 0 && w >= 2) continue;
-        store_piece(out + gdr_frag_up(w, q) * 2 * kGdrFragHalves, C[2 * q], C[2 * q + 1], st.up, true);
+        store_piece(out + gdr_frag_up(w, q) * 2 * kGdrFragHalves, C[2 * q], C[2 * q + 1], st.up);
       }
     }
   }
 }
 
 template <int NP, bool BF16, bool VEC>
-void launch_np(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, unsigned blocks, int out_lo, int a_group,
+void launch_np(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, unsigned blocks, int a_group,
                bool backward, hipStream_t st) {
   if (backward) {
-    gdr_prep_kernel<NP, BF16, VEC, true><<<blocks, kThreads, 0, st>>>(a, ws, chunks, out_lo, a_group);
+    gdr_prep_kernel<NP, BF16, VEC, true><<<blocks, kThreads, 0, st>>>(a, ws, chunks, a_group);
   } else {
-    gdr_prep_kernel<NP, BF16, VEC, false><<<blocks, kThreads, 0, st>>>(a, ws, chunks, out_lo, a_group);
+    gdr_prep_kernel<NP, BF16, VEC, false><<<blocks, kThreads, 0, st>>>(a, ws, chunks, a_group);
   }
 }
 
 template <int NP, bool BF16>
-void launch_vec(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, unsigned blocks, int out_lo, int a_group,
+void launch_vec(const GatedDeltaArgs& a, const GdrWork& ws, int chunks, unsigned blocks, int a_group,
                 bool backward, bool vec, hipStream_t st) {
-  vec ? launch_np<NP, BF16, true>(a, ws, chunks, blocks, out_lo, a_group, backward, st)
-      : launch_np<NP, BF16, false>(a, ws, chunks, blocks, out_lo, a_group, backward, st);
+  vec ? launch_np<NP, BF16, true>(a, ws, chunks, blocks, a_group, backward, st)
+      : launch_np<NP, BF16, false>(a, ws, chunks, blocks, a_group, backward, st);
 }
 
 }  // namespace
 
-int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, int out_lo, bool backward, bool vec,
+int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, bool vec,
                     void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   // Measured (a whole forward, a block a group against a block a head): 2 groups
@@ -354,11 +353,11 @@ int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, 
   const unsigned blocks = static_cast<unsigned>(groups * a_group);
   const int n = static_cast<int>(chunks);
   if (a.dstate <= 64) {
-    a.in_bf16 ? launch_vec<64, true>(a, ws, n, blocks, out_lo, a_group, backward, vec, st)
-              : launch_vec<64, false>(a, ws, n, blocks, out_lo, a_group, backward, vec, st);
+    a.in_bf16 ? launch_vec<64, true>(a, ws, n, blocks, a_group, backward, vec, st)
+              : launch_vec<64, false>(a, ws, n, blocks, a_group, backward, vec, st);
   } else {
-    a.in_bf16 ? launch_vec<128, true>(a, ws, n, blocks, out_lo, a_group, backward, vec, st)
-              : launch_vec<128, false>(a, ws, n, blocks, out_lo, a_group, backward, vec, st);
+    a.in_bf16 ? launch_vec<128, true>(a, ws, n, blocks, a_group, backward, vec, st)
+              : launch_vec<128, false>(a, ws, n, blocks, a_group, backward, vec, st);
   }
   return static_cast<int>(hipGetLastError());
 }

@@ -356,7 +356,7 @@ inline bool gdr_both_at_once(const GatedDeltaArgs& a) {
 
 // Launchers (0 or a HIP error code). vec: every row of q and k starts on a
 // 16-byte boundary and N is a multiple of 8.
-int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, int out_lo, bool backward, bool vec,
+int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, bool backward, bool vec,
                     void* stream);
 int launch_gdr_chunk_b(const GatedDeltaArgs& a, const GdrWork& ws, const GdrPlan& pl, bool backward, void* stream);
 int launch_gdr_chunk_f(const GatedDeltaArgs& a, const GdrWork& ws, const GdrPlan& pl, bool backward, void* stream);
