@@ -509,7 +509,8 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
       float ddt = dg * A;
       if (p.dt_softplus) ddt *= sigmoid_f(x);
       float db = dbeta;
-      if (p.beta_sigmoid) db *= beta * (1.0f - beta);
+      // (1 - beta of the rounded beta would be 0 from a raw strength of 17 on)
+      if (p.beta_sigmoid) db *= sigmoid_f(beta_raw) * sigmoid_f(-beta_raw);
       if (t < out_rows) {
         const int64_t at = (row0 + t) * H + h;
         a.ddt[at] = t < rows ? ddt : 0.0f;
