@@ -211,7 +211,7 @@ GdrWork gdr_work(void* workspace, const GdrPlan& pl, const GatedDeltaArgs& a) {
   ws.X = reinterpret_cast<float*>(base + pl.off_x);
   ws.E = reinterpret_cast<float*>(base + pl.off_e);
   ws.top = reinterpret_cast<float*>(base + pl.off_top);
-  ws.part = reinterpret_cast<float*>(base + pl.off_part);
+  ws.part = reinterpret_cast<double*>(base + pl.off_part);
   ws.map = reinterpret_cast<float*>(base + pl.off_map);
   ws.seg = reinterpret_cast<float*>(base + pl.off_seg);
   ws.seg_stride = a.batch * a.nheads * a.headdim * a.dstate;

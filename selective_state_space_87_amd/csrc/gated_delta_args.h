@@ -131,7 +131,7 @@ inline GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t nkheads, 
     p.off_x = take(state);
     p.off_e = take(static_cast<size_t>(64 * headdim) * 4);
     p.off_top = take(5 * 32 * 4);
-    p.off_part = take(2 * 4);
+    p.off_part = take(2 * 8);
   }
   p.bytes = at;
   return p;

@@ -88,7 +88,8 @@ __device__ __forceinline__ float uniform(float v) {
   return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
 }
 
-__device__ __forceinline__ float wave_sum64(float v) {
+template <typename T>
+__device__ __forceinline__ T wave_sum64(T v) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
   return v;
@@ -125,8 +126,9 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
   __shared__ __align__(16) char pool[kStage > kG ? kStage : kG];
   __shared__ double sC[kGdrC];
   __shared__ float sBeta[kGdrC], sKn[kGdrC], sQn[kGdrC], sKup[kGdrC], sQup[kGdrC];
-  __shared__ float sRow[4][2][kGdrC];                     // q.N1, k.N2, k.N3 (half the columns each), sum_s beta_s Z
-  __shared__ float sCol[8][kGdrC];                        // a wave's sums of Z down the columns
+  __shared__ float sRow[3][2][kGdrC];                     // q.N1, k.N2, k.N3 (half the columns each)
+  __shared__ double sRowZ[2][kGdrC];                      // sum_s beta_s Z (of either term of Z)
+  __shared__ double sCol[8][kGdrC];                       // a wave's sums of Z down the columns
   __shared__ float sDot[8], sTop[8];
   const GatedDeltaArgs& p = a.f;
   _Float16* sS = reinterpret_cast<_Float16*>(pool);       // [2][32][RS]
@@ -199,7 +201,7 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
           a.ddt[(row0 + lane) * H + h] = 0.0f;
           a.dbeta[(row0 + lane) * H + h] = 0.0f;
         }
-        if (lane == 0) ws.part[item] = ws.part[items + item] = 0.0f;
+        if (lane == 0) ws.part[item] = ws.part[items + item] = 0.0;
       }
       continue;
     }
@@ -310,13 +312,14 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     __syncthreads();  // the staged pieces are done with; Gq and Gk take their place
 
     const double cend = sC[kGdrC - 1];
-    float into[4], wt[4], row_z[4];
+    float into[4], wt[4];
+    double row_z[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = 16 * w + 4 * g + i;
       into[i] = exp2_hw(static_cast<float>(sC[t]));
       wt[i] = sBeta[t] * exp2_hw(static_cast<float>(cend - sC[t]));
-      row_z[i] = 0.0f;
+      row_z[i] = 0.0;
     }
     // Gq and the first term of Z (half 0), Gk and the second (half 1).
     {
@@ -329,7 +332,7 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
       for (int i = 0; i < 4; ++i) lnt[i] = ln[16 * w + 4 * g + i] * lup;
 #pragma unroll
       for (int si = 0; si < 4; ++si) {
-        float col_z = 0.0f;
+        double col_z = 0.0;
         const int s = 16 * si + m;
         if (si <= w) {
           f32x4_t xk = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};  // q_t . k_s or k_t . k_s
@@ -353,7 +356,7 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
             const float dec = exp2_hw(static_cast<float>(sC[t] - cs)) * (lnt[i] * kns);
             const float u = in ? tri[si][i] * unit * dec : 0.0f;
             const float z = in ? u * (xk[i] * whole) : 0.0f;  // (no product of a masked infinity)
-            row_z[i] = fmaf(bs, z, row_z[i]);
+            row_z[i] = fma(static_cast<double>(bs), static_cast<double>(z), row_z[i]);
             col_z += z;
             tri[si][i] = u * bs;
             mx = fmaxf(mx, fabsf(tri[si][i]));
@@ -361,11 +364,16 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
         } else {
           tri[si] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        const auto x32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(col_z), __float_as_uint(col_z), false, false);
-        col_z = __uint_as_float(x32[0]) + __uint_as_float(x32[1]);
-        const auto x16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(col_z), __float_as_uint(col_z), false, false);
-        col_z = __uint_as_float(x16[0]) + __uint_as_float(x16[1]);
+        col_z += __shfl_xor(col_z, 32);
+        col_z += __shfl_xor(col_z, 16);
         if (g == 0) sCol[w8][s] = col_z;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        double z = row_z[i];
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) z += __shfl_xor(z, d);
+        if (m == 0) sRowZ[hf][16 * w + 4 * g + i] = z;
       }
       mx = lanes16_max(col_max(mx));
       if (place == 0) sTop[w8] = mx;
@@ -397,12 +405,10 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
       for (int i = 0; i < 4; ++i) {
         const int t = 16 * w + 4 * g + i;
         const float q1 = lanes16_sum(r1[i]), q2 = lanes16_sum(r2[i]), q3 = lanes16_sum(r3[i]);
-        const float qz = lanes16_sum(row_z[i]);
         if (m == 0) {
           sRow[0][hf][t] = q1 * sQn[t];
           sRow[1][hf][t] = q2 * sKn[t];
           sRow[2][hf][t] = q3 * sKn[t];
-          sRow[3][hf][t] = qz;
         }
       }
     }
@@ -482,21 +488,26 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
 
     // The gates: lane t of wave 0.
     if (w8 == 0) {
+      // Summed in double, Z's sums over rows and columns above as well: what a pair
+      // of steps on the same side of t adds to one of them it takes from the other,
+      // to the bit, and does not leave 64 roundings in d(dt A)_t, which then all
+      // point one way in dA. (In float32: ddt off by 6.4e-7, now 2.7e-7; 9 us less.)
       const int t = anew(lane);  // (its addresses are not kept from one head to the next)
       const double cl = sC[t];
       const float in = exp2_hw(static_cast<float>(cl));
       const float last = exp2_hw(static_cast<float>(cend - cl));
       const float beta = sBeta[t];
-      float colz = 0.0f, dots = 0.0f;
+      double colz = 0.0, dots = 0.0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) colz += sCol[k][t], dots += sDot[k];
       const auto row = [&](int k) { return sRow[k][0][t] + sRow[k][1][t]; };
       const float r3 = row(2);
-      const float w3 = beta * last * r3;
-      const float dc = p.scale * in * row(0) - in * row(1) - w3 + row(3) - beta * colz;
-      const float dbeta = fmaf(last, r3, colz);
+      const double w3 = static_cast<double>(beta * last) * r3;
+      const double dc = static_cast<double>(p.scale * in) * row(0) - static_cast<double>(in) * row(1) - w3 +
+                        (sRowZ[0][t] + sRowZ[1][t]) - static_cast<double>(beta) * colz;
+      const float dbeta = fmaf(last, r3, static_cast<float>(colz));
       // sum over the steps from t on, the end's own part with the last one
-      const float at_end = wave_sum64(w3) + exp2_hw(static_cast<float>(cend)) * dots;
+      const double at_end = wave_sum64(w3) + static_cast<double>(exp2_hw(static_cast<float>(cend))) * dots;
       double suffix = dc;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
@@ -504,7 +515,7 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
         if (t + d < 64) suffix += o;
       }
       const float dt = p.dt_softplus ? softplus_f(x) : x;
-      float dg = static_cast<float>(suffix + static_cast<double>(at_end));
+      float dg = static_cast<float>(suffix + at_end);
       if (t >= rows || dt * A < kGdrMinLogDecay) dg = 0.0f;  // behind the end; where the decay was cut off
       float ddt = dg * A;
       if (p.dt_softplus) ddt *= sigmoid_f(x);
@@ -516,8 +527,9 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
         a.ddt[at] = t < rows ? ddt : 0.0f;
         a.dbeta[at] = t < rows ? db : 0.0f;
       }
-      const float da = wave_sum64(t < rows && dg != 0.0f ? dg * dt : 0.0f);
-      const float dbias = wave_sum64(t < rows ? ddt : 0.0f);
+      // (In double to the last sum: terms of thousands of steps cancel.)
+      const double da = wave_sum64(t < rows && dg != 0.0f ? static_cast<double>(dg) * dt : 0.0);
+      const double dbias = wave_sum64(t < rows ? static_cast<double>(ddt) : 0.0);
       if (t == 0) {
         ws.part[item] = da;
         ws.part[items + item] = dbias;
@@ -587,14 +599,14 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
 }
 
 // dA[h] and ddt_bias[h]: the items' parts, added in a fixed order (each thread
-// every 256th of a head's batch rows and chunks, then a tree).
-__global__ __launch_bounds__(kThreads) void gdr_gate_sums_kernel(const float* __restrict__ part, int64_t batch, int H,
+// every 512th of a head's batch rows and chunks, then a tree) and rounded once.
+__global__ __launch_bounds__(kThreads) void gdr_gate_sums_kernel(const double* __restrict__ part, int64_t batch, int H,
                                                                  int64_t chunks, float* __restrict__ dA,
                                                                  float* __restrict__ dbias) {
-  __shared__ float sums[2][kThreads];
+  __shared__ double sums[2][kThreads];
   const int h = blockIdx.x, tid = threadIdx.x;
   const int64_t n = batch * chunks, items = n * H;
-  float u = 0.0f, v = 0.0f;
+  double u = 0.0, v = 0.0;
   for (int64_t i = tid; i < n; i += kThreads) {
     const int64_t at = ((i / chunks) * H + h) * chunks + i % chunks;
     u += part[at];
@@ -611,8 +623,8 @@ __global__ __launch_bounds__(kThreads) void gdr_gate_sums_kernel(const float* __
     __syncthreads();
   }
   if (tid == 0) {
-    dA[h] = sums[0][0];
-    if (dbias != nullptr) dbias[h] = sums[1][0];
+    dA[h] = static_cast<float>(sums[0][0]);
+    if (dbias != nullptr) dbias[h] = static_cast<float>(sums[1][0]);
   }
 }
 

@@ -216,7 +216,7 @@ struct GdrWork {  // device pointers into the workspace
   float* X;       // [items][P][N] gradient of the state leaving it
   float* E;       // [items][64][P]
   float* top;     // [items][kGdrMaxima][kGdrMaxSlots]
-  float* part;    // [2][items]: an item's part of dA and of ddt_bias
+  double* part;   // [2][items]: an item's part of dA and of ddt_bias
   float* map;     // [heads][segments][P + N][N]: a segment's map (forward in segments)
   float* seg;     // [segments][heads][P][N]: state entering a segment
   int64_t seg_stride;  // elements from one segment's states to the next's

@@ -1,4 +1,6 @@
-"""Gradients of the gates: strengths whose sigmoid is saturated."""
+"""Gradients of the gates: strengths whose sigmoid is saturated, and the sums over
+all steps behind dA and ddt_bias.
+"""
 
 import numpy as np
 import pytest
@@ -33,4 +35,43 @@ def test_saturated_strengths(sign, dtype):
     unit = np.exp(-x) / (1.0 + np.exp(-x)) ** 2
     worst = float(np.abs((got - ref) / unit).max() / (TOL * np.abs(ref / unit).max()))
     print(f"dbeta at {sign:+.0f} x 8 .. 20, {dtype}: {worst:.3f} of the tolerance", flush=True)
+    assert worst <= 1.0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(2, 150, 1, 2, 32, 16), (3, 1000, 2, 2, 64, 48), (2, 2500, 1, 4, 16, 16)])
+def test_sums_over_the_steps(size, dtype):
+    """With A = -1 and no softplus, ddt = -d(dt A) to the bit, so that ddt_bias is
+    the sum of ddt and dA that of -ddt (dt + dt_bias) over all steps: rounded once,
+    2^-24 of the sum, beside what a sum in 64 bits is off by (2^-52 of the absolute
+    values, a term at a time) and the float32 rounding of dt + dt_bias, taken here
+    as the kernel takes it."""
+    p = problem(*size, dtype, 73, raw=False)
+    H = size[3]
+    p["A"] = torch.full((H,), -1.0, device="cuda")
+    p["dt_bias"] = torch.full((H,), 0.0625, device="cuda")
+    dy, dh = seeds(p, 74)
+    got = run(p, dy, dh, raw=False)
+    ddt = got["ddt"].double().cpu().numpy()
+    dt = (p["dt"].float() + p["dt_bias"]).double().cpu().numpy()
+    for name, terms in (("ddt_bias", ddt), ("dA", -ddt * dt)):
+        want, mag = terms.sum((0, 1)), np.abs(terms).sum((0, 1))
+        room = 2.0**-24 * np.abs(want) + 2.0**-52 * terms[..., 0].size * mag
+        worst = float((np.abs(got[name].double().cpu().numpy() - want) / room).max())
+        print(f"{name} {size} {dtype}: {worst:.3f} of the tolerance", flush=True)
+        assert worst <= 1.0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(2, 64, 1, 2, 64, 48), (1, 300, 2, 2, 128, 32), (2, 50, 1, 3, 33, 16)])
+def test_a_decay_of_nothing_has_no_gradient(size, dtype):
+    """Without an initial state the first step's decay changes nothing, and every
+    term of d(dt A) behind it comes twice, with either sign: sums of 64 x 64 terms
+    in 64 bits leave 2^-53 a term of at most 64 x 64 times the largest, 2^-29 of it."""
+    p = problem(*size, dtype, 75)
+    p["h0"] = None
+    dy, dh = seeds(p, 76)
+    ddt = run(p, dy, dh)["ddt"].double().cpu().numpy()
+    worst = float((np.abs(ddt[:, 0]).max((0,)) / (2.0**-29 * np.abs(ddt).max((0, 1)))).max())
+    print(f"ddt of the first step, {size} {dtype}: {worst:.3g} of the tolerance", flush=True)
     assert worst <= 1.0
