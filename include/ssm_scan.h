@@ -425,7 +425,7 @@ int ssm_ssd_fwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, 
  *
  *   batch, seqlen              : B >= 0, 0 <= L < 2^30.
  *   nkheads, nheads            : G and H; H a multiple of G (else
- *                                SSM_E_SHAPE), H = 0 only with G = 0.
+ *                                SSM_E_SHAPE); both 0 or neither.
  *   headdim, dstate            : 1 <= P <= 256, 1 <= N <= 128 (else
  *                                SSM_E_UNSUPPORTED). B H times the 16-column
  *                                slices of P, and times the 64-step blocks of

@@ -606,7 +606,7 @@ struct GdrSizes {
 int gdr_sizes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, int64_t headdim, int64_t dstate,
               int in_dtype, GdrSizes* z) {
   if (batch < 0 || seqlen < 0 || nkheads < 0 || nheads < 0 || headdim < 1 || dstate < 1) return SSM_E_SHAPE;
-  if (nkheads == 0 ? nheads != 0 : nheads % nkheads != 0) return SSM_E_SHAPE;
+  if ((nkheads == 0) != (nheads == 0) || (nkheads > 0 && nheads % nkheads != 0)) return SSM_E_SHAPE;
   if (headdim > ssm::kGdrMaxHeadDim || dstate > ssm::kGdrMaxState) return SSM_E_UNSUPPORTED;
   if (in_dtype != 0 && in_dtype != 1) return SSM_E_DTYPE;
   *z = GdrSizes{batch, seqlen, nkheads, nheads, headdim, dstate, 0, 0, 0, 0, 0, 0};

@@ -212,3 +212,13 @@ def test_steps_of_column_ranges():
         binding._step_of("q", q[:, :, ::2], 2, 8)
     with pytest.raises(ValueError):
         binding._step_of("q", q[..., ::2], 2, 8)
+
+
+@pytest.mark.parametrize("call", [fwd, bwd, upd])
+def test_key_heads_without_value_heads(lib, call):
+    """H = 0 with G > 0 has gradients of q and k that no kernel would write."""
+    assert call(lib, H=0, vs=0) == E_SHAPE
+    assert call(lib, B=0, H=0, vs=0) == E_SHAPE
+    assert call(lib, G=0, H=0, qs=0, ks=0, vs=0) == OK
+    assert lib.ssm_gated_delta_workspace_bytes(2, 64, 2, 0, 8, 8, 0) == 0
+    assert lib.ssm_gated_delta_bwd_workspace_bytes(2, 64, 2, 0, 8, 8, 0) == 0
