@@ -546,8 +546,10 @@ int ssm_gated_delta_bwd(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t 
  *   s = x + residual  (s = x when residual is NULL), rounded to res_dtype
  *   n = s / sqrt(mean(s^2) + eps) * weight            (weight NULL: 1)
  *   y = n, or with out_dtype 2: scales[r] = max|n| / 448 over the row (1 when
- *       that is 0, and at least 2^-126) and y = n / scales[r] in the 8-bit format e4m3 (OCP: 448 is
- *       its largest value), rounded to nearest even
+ *       that is 0, and at least 2^-126) and y = n / scales[r] in the 8-bit
+ *       format e4m3 (OCP: 448 is its largest value), rounded to nearest even; the
+ *       quotient is taken in float32, so that an element within some 2^-23 of
+ *       itself of a border between two 8-bit values (3 in 10^7) may take the other
  *
  *   rows, dim                  : R >= 0, 1 <= d <= 16384 (else
  *                                SSM_E_UNSUPPORTED), R < 2^31.
