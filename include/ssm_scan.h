@@ -462,14 +462,20 @@ int ssm_ssd_fwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, 
  *                                      on a 16-byte boundary (NULL when 0)
  *
  * q, k, v, dt, beta and y need the alignment of their element type only; rows
- * that start on 16-byte boundaries with N and P multiples of 8 are read
- * fastest. Products are taken in 22 bits or more of every float32 operand and
- * added in float32; a bfloat16 y is the float32 y rounded once. Results are
- * bitwise deterministic. Errors grow as the products of the steps' maps
- * exp(dt A) (1 - beta k k^T) do: not at all where 0 <= beta |k|^2 <= 2, as with
- * both the sigmoid and the norm. A value of a step that is not finite may make
- * every y and state element of its head NaN from the start of its block of 64
- * steps on.
+ * that start on 16-byte boundaries with N and P multiples of 8 are read fastest.
+ * Sequences of up to 8 steps are taken step by step in float32, longer ones in
+ * blocks of 64 steps. There products are added in float32, and a float32 operand
+ * has 22 bits, but no more than down to 2^-38 of the largest element that shares
+ * its power of two: of the row of a key or query, of half a column of the state,
+ * of 32 steps of a column of v - k^T S, of a block's triangle of k . k. An
+ * element less than 2^-16 of that one has fewer bits: a small v beside a v of
+ * the same channel and 32 steps that is 10^6 times as large is right to 2^-18 of
+ * itself. A bfloat16 y is the float32 y rounded once. Results are bitwise
+ * deterministic. Errors grow as the products of the steps' maps exp(dt A) (1 -
+ * beta k k^T) do: not at all where 0 <= beta |k|^2 <= 2, as with both the
+ * sigmoid and the norm. A value of a step that is not finite may make every y
+ * and state element of its head NaN, from that step on where a sequence has up
+ * to 8 steps, else from the start of its block of 64 steps on.
  */
 size_t ssm_gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
                                        int64_t headdim, int64_t dstate, int in_dtype);
@@ -523,9 +529,12 @@ int ssm_gated_delta_update(int64_t batch, int64_t nkheads, int64_t nheads, int64
  *                                      ssm_gated_delta_bwd_workspace_bytes(),
  *                                      on a 16-byte boundary
  * No output may overlap an input, another output or the workspace. Bitwise
- * deterministic (sums over steps, batch rows and shared heads in a fixed
- * order). A value that is not finite may make every gradient of its head and of
- * the q and k that it shares NaN.
+ * deterministic (sums over steps, batch rows and shared heads in a fixed order).
+ * Operands have 22 bits, down to 2^-38 of the largest element that shares their
+ * power of two, here for the sums over channels that of a whole block of 64
+ * steps (of its dy, v - k^T S, state and their gradients). A value that is not
+ * finite may make every gradient of its head and of the q and k that it shares
+ * NaN.
  */
 size_t ssm_gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads,
                                            int64_t headdim, int64_t dstate, int in_dtype);
