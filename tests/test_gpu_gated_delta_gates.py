@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests.test_gpu_gated_delta import problem
-from tests.test_gpu_gated_delta_bwd import TOL, reference, run, seeds
+from tests.test_gpu_gated_delta_bwd import TOL, compare, reference, run, seeds
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +75,18 @@ def test_a_decay_of_nothing_has_no_gradient(size, dtype):
     worst = float((np.abs(ddt[:, 0]).max((0,)) / (2.0**-29 * np.abs(ddt).max((0, 1)))).max())
     print(f"ddt of the first step, {size} {dtype}: {worst:.3g} of the tolerance", flush=True)
     assert worst <= 1.0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_decays_that_forget_nearly_everything(dtype):
+    """Log decays of -10 to -14 at every step: d(dt A) is e^-10 to e^-14 of the
+    terms that its sum over the later steps cancels, and is held to the tolerance of
+    a gradient on its own scale. (In float32 the cancelled terms, times e^14, would
+    leave a tenth of it; in 64 bits they leave 64 x 64 x 2^-53 x e^14 = 2^-21.)"""
+    p = problem(2, 150, 1, 2, 64, 48, dtype, 77)
+    step = 10.0 + 4.0 * torch.rand(p["dt"].shape, generator=torch.Generator().manual_seed(9))
+    p["dt"], p["dt_bias"] = step.to(p["dt"].dtype).cuda(), torch.zeros(2, device="cuda")
+    p["A"] = torch.full((2,), -1.0, device="cuda")
+    dy, dh = seeds(p, 78)
+    ref, got = reference(p, dy, dh), run(p, dy, dh)
+    compare(f"strong decays {dtype}", {x: got[x] for x in ("ddt", "dA", "ddt_bias")}, ref)
