@@ -514,7 +514,7 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
         const double o = __shfl_down(suffix, d);
         if (t + d < 64) suffix += o;
       }
-      const float dt = p.dt_softplus ? softplus_f(x) : x;
+      const float dt = p.dt_softplus ? gdr_softplus(x) : x;
       float dg = static_cast<float>(suffix + at_end);
       if (t >= rows || dt * A < kGdrMinLogDecay) dg = 0.0f;  // behind the end; where the decay was cut off
       float ddt = dg * A;

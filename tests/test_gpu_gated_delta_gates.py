@@ -1,11 +1,13 @@
-"""Gradients of the gates: strengths whose sigmoid is saturated, and the sums over
-all steps behind dA and ddt_bias.
+"""The gates and their gradients: step sizes and strengths far down the softplus
+and the sigmoid, strengths whose sigmoid is saturated, and the sums over all steps
+behind dA and ddt_bias.
 """
 
 import numpy as np
 import pytest
 import torch
 
+from selective_state_space_87_amd import binding
 from tests.test_gpu_gated_delta import problem
 from tests.test_gpu_gated_delta_bwd import TOL, compare, reference, run, seeds
 
@@ -90,3 +92,28 @@ def test_decays_that_forget_nearly_everything(dtype):
     dy, dh = seeds(p, 78)
     ref, got = reference(p, dy, dh), run(p, dy, dh)
     compare(f"strong decays {dtype}", {x: got[x] for x in ("ddt", "dA", "ddt_bias")}, ref)
+
+
+@pytest.mark.parametrize("lo,hi", [(-20.0, -12.0), (-12.0, -6.0), (-6.0, -2.0)])
+def test_small_step_sizes_and_strengths(lo, hi):
+    """exp(dt A) and beta out of one step of 2048 heads: with k = 0 the state is
+    exp(dt A) times itself, with k = v = 1 and no state it is beta. Their roundings
+    are within 2^-22 of dt A or of beta, and point no one way: 2048 of them leave
+    2^-22 / 2048^(1/2) < 2^-27 of it, where log2(e) rounded to float32 left |x| 2^-26
+    in every dt and beta. The hardware's base-2 exponential, logarithm and inverse
+    may each be off by 2^-26 the same way (a quarter of their last place), A and
+    the state by no more: 2^-24 is allowed."""
+    H = 2048
+    g = torch.Generator().manual_seed(79)
+    x = (lo + (hi - lo) * torch.rand(1, H, generator=g)).cuda()
+    A = (-4.0 / torch.nn.functional.softplus(x[0].double())).float()
+    one, none = torch.ones(1, H, 1, device="cuda"), torch.zeros(1, H, 1, device="cuda")
+    state = torch.ones(1, H, 1, 1, device="cuda")
+    binding.ssm_gated_delta_update(state, none, none, none, x, A, x, dt_softplus=True, scale=1.0)
+    want = torch.log1p(torch.exp(x[0].double())) * A.double()
+    off = float((state.double().flatten().log() / want - 1).mean())
+    state = torch.zeros(1, H, 1, 1, device="cuda")
+    binding.ssm_gated_delta_update(state, one, one, one, 0 * x, A, x, beta_sigmoid=True, scale=1.0)
+    beta = float((state.double().flatten() * (1 + torch.exp(-x[0].double())) - 1).mean())
+    print(f"mean error at {lo} .. {hi}: dt {off:.1e}, beta {beta:.1e}", flush=True)
+    assert abs(off) <= 2.0**-24 and abs(beta) <= 2.0**-24
