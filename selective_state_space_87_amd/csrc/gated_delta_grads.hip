@@ -13,6 +13,9 @@
 //   dc_t = scale e^c_t q_t . N1_t - e^c_t k_t . N2_t - w_t k_t . N3_t + sum_s beta_s Z[t,s] - beta_t sum_u Z[u,t]
 //          (+ sum_s w_s k_s . N3_s + e^c_end <X, S> at the chunk's end)
 //   d(dt A)_t = sum_{u >= t} dc_u
+// Signs (see gdr_mma.h): every other 16 columns n of S and X, and every other row
+// of E, are taken negative, so that the products' errors cancel in the sums over n
+// and over steps; X comes with every other 16 of its rows p negative already.
 // Gq and Gk are kept with the row factors of both their sides (those of k on
 // the columns, of q or k on the rows) and taken out of the products' rows again:
 // one set of halves, read by rows and, transposed by the LDS, by columns, serves
@@ -257,20 +260,22 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
     float dot = 0.0f;  // this thread's part of <X, S>
 
     for (int p0 = 0; p0 < P; p0 += 32) {
+      const int at_tid = anew(tid);  // (for the signs, that they are not kept in registers)
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kSXT; ++i) {
         const int e = (i * kThreads + tid) * 8 % (32 * NP), pr = e / NP, n = e % NP;
+        const int from = (i * kThreads + at_tid) * 8 % (32 * NP), sp = from / NP >> 4, sn = from % NP >> 4;
         if (32 * NP / 8 >= kThreads || tid < 32 * NP / 8) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dot = fmaf(fs[i][k], fx[i][k], dot);
+          for (int k = 0; k < 8; ++k) dot = fmaf(flip(fs[i][k], sp), fx[i][k], dot);
         }
         // (with 64 states two threads have, and write, the same piece)
-        store_split(sS + pr * RS + n, kSX, fs[i], top[kMaxS].up);
-        store_split(sX + pr * RS + n, kSX, fx[i], top[kMaxX].up);
+        store_split(sS + pr * RS + n, kSX, fs[i], flip(top[kMaxS].up, sn));
+        store_split(sX + pr * RS + n, kSX, fx[i], flip(top[kMaxX].up, sn ^ sp));
       }
       store_split((hf == 0 ? sY : sD) + trow * kPS + tcol, kTP, fy, top[hf == 0 ? kMaxDY : kMaxDE].up);
-      if (hf == 0) store_split(sE + trow * kPS + tcol, kTP, fe, top[kMaxE].up);
+      if (hf == 0) store_split(sE + trow * kPS + tcol, kTP, fe, flip(top[kMaxE].up, at_tid >> 2));
       __syncthreads();
       fetch(p0 + 32);  // (past the last columns: zeros)
       const int at = (16 * w + m) * kPS + 8 * g;
@@ -326,7 +331,7 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
       const _Float16* left = hf == 0 ? sQ : sK;
       const float* ln = hf == 0 ? sQn : sKn;
       const float lup = hf == 0 ? qunit.up : kunit.up, whole = (hf == 0 ? qunit.down : kunit.down) * kunit.down;
-      const float unit = hf == 0 ? top[kMaxDY].down * top[kMaxE].down * p.scale : -(top[kMaxDE].down * top[kMaxE].down);
+      const float unit = flip(hf == 0 ? top[kMaxDY].down * top[kMaxE].down * p.scale : -(top[kMaxDE].down * top[kMaxE].down), m);
       float mx = 0.0f, lnt[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) lnt[i] = ln[16 * w + 4 * g + i] * lup;
@@ -393,7 +398,8 @@ __global__ __launch_bounds__(kThreads) void gdr_grads_kernel(const GatedDeltaBwd
             kv += static_cast<float>(sK[kLo + at]);
             qv += static_cast<float>(sQ[kLo + at]);
           }
-          const float v1 = n1[j][i] * f1, v2 = n2[j][i] * f2, v3 = n3[j][i] * f3;
+          const float v1 = n1[j][i] * (j & 1 ? -f1 : f1), v2 = n2[j][i] * (j & 1 ? -f2 : f2);
+          const float v3 = n3[j][i] * ((i ^ j) & 1 ? -f3 : f3);
           r1[i] = fmaf(qv, v1, r1[i]);
           r2[i] = fmaf(kv, v2, r2[i]);
           r3[i] = fmaf(kv, v3, r3[i]);

@@ -11,7 +11,8 @@
 // pair, a chunk ahead: Pm^T dY and Q^T (qf dY), which the state's waves add from
 // LDS, and all loads (202 us for (2, 4096, 16 heads of 128 x 128), 253 with a pair's
 // own waves doing it). X is left in the workspace for every chunk (the gradient
-// of its leaving state), dE in dv.
+// of its leaving state), dE in dv. Every other slice is walked with the other sign
+// (see gdr_mma.h), and its X is left so.
 #include <hip/hip_runtime.h>
 
 #include "gated_delta_chunk.h"
@@ -77,6 +78,7 @@ __device__ __forceinline__ void gdr_walk_back(const GatedDeltaBwdArgs& a, const 
   const int b = bh / H, h = bh % H, kh = h / (H / G);
   const int col = (place % pblocks) * 16 * NPAIR + 16 * pr + m;
   const bool col_ok = col < P;
+  const int odd = (col >> 4) & 1;  // the slice's X, dY and U are taken negative, and X is left so
   const int64_t L = p.seqlen;
   const int64_t len = gdr_row_steps(p.seqlens, b, L);
   const int n_chunks = static_cast<int>((len + kGdrC - 1) / kGdrC);
@@ -110,7 +112,7 @@ __device__ __forceinline__ void gdr_walk_back(const GatedDeltaBwdArgs& a, const 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int n = n0 + 32 * (j / 2) + 8 * g + 4 * (j & 1) + i;
-        X[j][i] = (a.dh_final != nullptr && col_ok && n < N) ? a.dh_final[sb + n] : 0.0f;
+        X[j][i] = (a.dh_final != nullptr && col_ok && n < N) ? flip(a.dh_final[sb + n], odd) : 0.0f;
       }
     }
     half8_t Xh[NK], Xl[NK];
@@ -202,7 +204,7 @@ __device__ __forceinline__ void gdr_walk_back(const GatedDeltaBwdArgs& a, const 
       // dE = T^T U
       f32x4_t E[2];
       {
-        const float tri = sF[4 * kGdrC + 1], down = su.down * tri;
+        const float tri = flip(sF[4 * kGdrC + 1], odd), down = su.down * tri;
         const auto T = [&](int f, int half) __attribute__((always_inline)) {
           return *reinterpret_cast<const half8_t*>(sT + (2 * f + half) * kGdrFragHalves + lane * 8);
         };
@@ -244,7 +246,7 @@ __device__ __forceinline__ void gdr_walk_back(const GatedDeltaBwdArgs& a, const 
           for (int i = 0; i < 4; ++i) B[u][i] = E[u][i] * -fk[i];
         }
         sd = pow2_to_top(tiles_absmax<2>(B));
-        tiles_to_operand<true>(B[0], B[1], sd.up, Bh, Bl);
+        tiles_to_operand<true>(B[0], B[1], flip(sd.up, odd), Bh, Bl);
         *piece(W::kXB, r, 0) = Bh;
         *piece(W::kXB, r, 1) = Bl;
         xb_f[64 * r + lane] = sd.down;
@@ -300,7 +302,7 @@ __device__ __forceinline__ void gdr_walk_back(const GatedDeltaBwdArgs& a, const 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int n = n0 + 32 * (j / 2) + 8 * g + 4 * (j & 1) + i;
-          if (n < N) a.dh0[sb + n] = X[j][i];
+          if (n < N) a.dh0[sb + n] = flip(X[j][i], odd);
         }
       }
     }
@@ -387,7 +389,7 @@ __device__ __forceinline__ void gdr_walk_back(const GatedDeltaBwdArgs& a, const 
     const Pow2 sy = pow2_to_top(ytop);
     half8_t Yh[2], Yl[2];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) tiles_to_operand<true>(Y[2 * q], Y[2 * q + 1], sy.up, Yh[q], Yl[q]);
+    for (int q = 0; q < 2; ++q) tiles_to_operand<true>(Y[2 * q], Y[2 * q + 1], flip(sy.up, odd), Yh[q], Yl[q]);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -414,7 +416,7 @@ __device__ __forceinline__ void gdr_walk_back(const GatedDeltaBwdArgs& a, const 
     const Pow2 sa = pow2_to_top(tiles_absmax<4>(Y));
     a_down = sa.down;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) tiles_to_operand<true>(Y[2 * q], Y[2 * q + 1], sa.up, Ah[q], Al[q]);
+    for (int q = 0; q < 2; ++q) tiles_to_operand<true>(Y[2 * q], Y[2 * q + 1], flip(sa.up, odd), Ah[q], Al[q]);
     const float my = lanes16_max(ytop);
     buffer_store_f32<false>(my, raw_buffer(ws.top + (item0 + c) * kGdrMaxima * kGdrMaxSlots, kGdrMaxima * kGdrMaxSlots * 4),
                             lane == 0 && col < P ? static_cast<uint32_t>(kMaxDY * kGdrMaxSlots + col / 16 * 2 + r) * 4 : kOutOfRange);

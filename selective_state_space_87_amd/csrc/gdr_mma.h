@@ -24,6 +24,14 @@
 // two and leave again in the float32 factor that the result is multiplied with
 // anyway. (Two bfloat16 halves would hold 16 bits: 2^-17 of an element.)
 //
+// The sums inside a matrix instruction are not rounded alike for x and -x: random
+// operands come out 1e-9 of the result's size too low on the average, measured,
+// which is nothing beside the 5e-8 that they are off by, but all one way. Where q,
+// k and v have a mean of their own, sums over thousands of steps gather it: dA and
+// ddt_bias were off by 8e-7 and 6e-7. So the backward takes every other of the
+// slices, tiles or rows that such a sum goes over with the other sign, in the power
+// of two that it is scaled with anyway: 4e-7 and 3e-7.
+//
 // Layouts of v_mfma_f32_16x16x32_f16, lane l = 16 g + m: A[m][8 g + j],
 // B[8 g + j][m] (j = 0..7), D[4 g + i][m] (i = 0..3). The order of the 32
 // contraction indices is free as long as A and B agree, so the D of two tiles
@@ -57,6 +65,11 @@ __device__ __forceinline__ constexpr int gdr_frag(int tt, int p) { return tt < 2
 
 __device__ __forceinline__ f32x4_t mfma16(half8_t a, half8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// x, or -x where n is odd.
+__device__ __forceinline__ float flip(float x, int n) {
+  return __uint_as_float(__float_as_uint(x) ^ (static_cast<uint32_t>(n) << 31));
 }
 
 // x, as a value that the compiler cannot trace back: what is computed from it

@@ -117,3 +117,25 @@ def test_small_step_sizes_and_strengths(lo, hi):
     beta = float((state.double().flatten() * (1 + torch.exp(-x[0].double())) - 1).mean())
     print(f"mean error at {lo} .. {hi}: dt {off:.1e}, beta {beta:.1e}", flush=True)
     assert abs(off) <= 2.0**-24 and abs(beta) <= 2.0**-24
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_roundings_point_no_one_way(dtype):
+    """Gradients are odd in (dy, dh): what those of (dy, dh) and (-dy, -dh) add up to
+    is what a rounding does not do alike for both signs. q, k and v have a mean of
+    their own here, as the convolution's SiLU leaves them. Where a chunk's part (of a
+    head) has either sign as likely, all parts add up to less than 4 (sum a^2)^(1/2), a
+    part being at most a, the sum of its absolute values: 4 n^(-1/2) of all absolute
+    values for n parts of a like size. All one way it was up to a half of them."""
+    B, L, G, H, N, P = 2, 4096, 8, 8, 128, 128
+    p = problem(B, L, G, H, N, P, dtype, 80)
+    for x in "qkv":
+        p[x] = torch.nn.functional.silu(p[x].float()).to(p[x].dtype)
+    dy, dh = seeds(p, 81)
+    plus, minus = run(p, dy, dh), run(p, -dy, -dh)
+    n = B * H * L // 64
+    for x in ("ddt", "dbeta", "dv"):
+        s = plus[x].double() + minus[x].double()
+        worst = float(s.sum().abs() / s.abs().sum())
+        print(f"{x} {dtype}: {worst:.3f} of {4 * n ** -0.5:.3f}", flush=True)
+        assert worst <= 4 * n ** -0.5, x
