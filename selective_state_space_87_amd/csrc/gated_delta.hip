@@ -16,7 +16,7 @@
 // sums.
 //
 // The update is bound by HBM: the state is read and written once. 128 batch rows
-// of 32 heads of 128 x 128 (537 MB): 109 us, 4.9 TB/s, as fast as a large copy.
+// of 32 heads of 128 x 128 (537 MB): 109 us, 4.9 TB/s, 117 us the call, as fast as a large copy.
 #include <hip/hip_runtime.h>
 
 #include "device_math.h"

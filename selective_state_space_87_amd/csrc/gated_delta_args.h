@@ -70,17 +70,18 @@ struct GdrPlan {
 };
 // Up to this length the recurrence is taken: its time grows with the steps, a
 // chunk's does not. Measured (bf16, N = P = 128, chunks against recurrence) at 4, 8
-// and 16 steps: 2 heads 19 us against 18, 20, 32; 256 heads 51 against 20, 27, 45;
-// 2048 heads 242 against 109, 175, 315.
+// and 16 steps: 2 heads 19 us against 19, 20, 33; 256 heads 39 against 25, 34, 42;
+// 2048 heads 208 to 218 against 95, 169, 319.
 constexpr int64_t kGdrRecurrentSteps = 8;
 // Segments: with at most kGdrFewSlices slices of 16 columns (batch, heads and
 // head size together) the walks of whole sequences leave most of the device
 // idle, and finding the segments' states first (a pass over P + N columns in
 // place of P) costs less than it gives. As many segments as make
 // kGdrManySlices slices, 4 to 32, of at least kGdrSegChunks chunks. Measured
-// (bf16, N = P = 128, whole -> in segments): 1 head of 65536 steps 1760 -> 216
-// us, 8 heads 2118 -> 786, 16 heads (128 slices) 2237 -> 1329; 4 heads of 4096
-// steps 130 -> 78, 2 of 2048 74 -> 60 (in two segments 80).
+// (bf16, N = P = 128, whole -> in segments): 1 head of 65536 steps 1785 -> 218
+// us, 8 heads 2136 -> 684, 16 heads (128 slices) 2337 -> 1308, 32 heads 2639 -> 2785
+// (not taken); 16 heads of 16384 steps 594 -> 365, 4 of 4096 133 -> 79, 2 of 2048
+// 76 -> 58 (in two segments 80).
 constexpr int64_t kGdrFewSlices = 128, kGdrManySlices = 1024, kGdrSegChunks = 8, kGdrMinSegs = 4, kGdrMaxSegs = 32;
 inline GdrPlan plan_gated_delta(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t nheads, int64_t headdim,
                                 int64_t dstate, int in_bf16, bool backward) {

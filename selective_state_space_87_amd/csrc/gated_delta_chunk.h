@@ -15,11 +15,13 @@
 // one phase behind, and move K, Q, T, Pm and the factors of the next chunk from
 // memory through their registers into LDS. Every product is of two halves, for a
 // bfloat16 y too: with one in those of y, y is off by 2^-11 of its terms, which
-// cancel, and the layer below took 568 us in place of 654. A chain as long as this is bound by
-// what a single wave can issue, not by the units. Measured at (4, 8192, 16 key and
-// 32 value heads of 128 x 128), bfloat16: 500 us (one wave for all of a slice's
-// work 790, a pair without waves for y and the loads 590), 3.9 us a chunk with four
-// pairs a CU; vector instructions 54 % of a SIMD's cycles, LDS 53 %, matrix cores 24 %.
+// cancel, and the whole forward below took 568 us in place of 654.
+// A chain as long as this is bound by what a single wave can issue, not by the
+// units. Measured at (4, 8192, 16 key and 32 value heads of 128 x 128), bfloat16:
+// 458 us, 3.6 us a chunk with four pairs a CU; vector instructions 52 % of a SIMD's
+// cycles, LDS 55 %, matrix cores 29 %. (When it was built, against the walk of that
+// time: one wave for all of a slice's work 790 us, a pair without waves for y and
+// the loads 590, with them 520.)
 #pragma once
 
 #include "gdr_mma.h"

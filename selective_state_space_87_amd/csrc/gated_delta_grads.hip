@@ -24,8 +24,8 @@
 // row tile w % 4 and half w / 4 of the N columns (and of dP and M: the one or
 // the other). The heads that share q and k are taken one after another, their
 // dq and dk added in registers: no partial sums in memory, no atomics.
-// Measured at (2, 4096, 16 heads of 128 x 128), bfloat16 inputs, 0.55 GB in and
-// 0.13 GB out: 235 us, one block a CU. (Four waves a block: 600 us, for the 192
+// Measured at (2, 4096, 16 heads of 128 x 128), bfloat16 inputs, 0.54 GB in and
+// 0.14 GB out: 226 us, one block a CU. (Four waves a block: 600 us, for the 192
 // registers of a wave's accumulators left none for operands. Gq and Gk in
 // float32, made into halves once for each of the four products: 30 us more. Gates
 // and scales read where they are used: 17 us more. Addresses kept over the heads,

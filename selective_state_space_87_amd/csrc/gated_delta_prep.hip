@@ -19,8 +19,8 @@
 // Sums of log decays are in double, and kept as two floats whose differences
 // are taken apart: behind a step that forgets nearly everything the sums are
 // large and the differences small.
-// Measured at (4, 8192, 16 key and 32 value heads of 128 x 128), bfloat16: 194 us
-// for 0.28 GB in and 0.59 GB out, 4.5 TB/s. (T through LDS and stored from there: 216.)
+// Measured at (4, 8192, 16 key and 32 value heads of 128 x 128), bfloat16: 191 us
+// for 0.28 GB in and 0.69 GB out, 5.1 TB/s. (T through LDS and stored from there 22 us more.)
 #include <hip/hip_runtime.h>
 
 #include "gdr_mma.h"
@@ -345,8 +345,8 @@ int launch_gdr_prep(const GatedDeltaArgs& a, const GdrWork& ws, int64_t chunks, 
                     void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   // Measured (a whole forward, a block a group against a block a head): 2 groups
-  // of 2 heads 21.6 us, 18.2; 4 of 4 heads 29.0, 18.3; 78 of 2 46.8, 43.9; 256 of 4
-  // 130, 123; 512 of 2 57.5, 58.4; 1024 of 4 267, 279.
+  // of 2 heads 21.8 us, 17.9; 4 of 4 heads 30.5, 19.0; 78 of 2 47.1, 43.3; 256 of 4
+  // 134, 128; 512 of 2 61.5, 61.8; 1024 of 4 277, 290.
   constexpr int64_t kGroupsEnough = 512;
   const int64_t groups = a.batch * a.nkheads * chunks;
   const int a_group = groups < kGroupsEnough ? static_cast<int>(a.nheads / a.nkheads) : 1;

