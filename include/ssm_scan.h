@@ -575,7 +575,8 @@ int ssm_gated_delta_bwd(int64_t batch, int64_t seqlen, int64_t nkheads, int64_t 
  *                                may equal residual
  *   scales    [R]     float32: required with out_dtype 2, NULL otherwise
  * Alignment: that of the element types; 16-byte aligned arrays with d a
- * multiple of 8 are read fastest. Sums are in float32; deterministic.
+ * multiple of 8 are read fastest. Sums are in float32 (a row whose sum of
+ * squares passes its range, elements near 2^64, comes out as 0); deterministic.
  */
 int ssm_rms_norm_fwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, int out_dtype, float eps,
                      const void* x, const void* residual, const float* weight,
