@@ -63,8 +63,9 @@ extern "C" {
 /* 2: the workspace must be 16-byte aligned; the forward with checkpoints and
  * the backward from them were added.
  * 3: the gated delta rule (forward, backward, single-token update) and the RMS
- * norm (forward, backward) were added. */
-#define SSM_ABI_VERSION 3
+ * norm (forward, backward) were added.
+ * 4: the layer norm and the dropout (forward, backward) were added. */
+#define SSM_ABI_VERSION 4
 
 /* Status codes. */
 #define SSM_OK 0
@@ -606,6 +607,108 @@ size_t ssm_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
 int ssm_rms_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps,
                      const void* s, const float* weight, const float* dy, const float* dresidual,
                      float* ds, float* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Dropout of a block's branch, with the residual stream's addition where the
+ * branch joins it:
+ *
+ *   y = drop(x) + residual           (y = drop(x) when residual is NULL)
+ *   drop(x)[e] = x[e] * 65536 / (65536 - T) where bits(e) >= T, else 0,
+ *   T = round(p * 65536)
+ *
+ * Nothing of the mask is stored: element e's 16 bits are a half word of
+ * Philox4x32-10 (Salmon, Moraes, Dror, Shaw, SC 2011) at the 128-bit counter
+ * (low and high word of e / 8, step, call) under the key `seed`; word (e mod 8)
+ * / 2, its low half for even e. The share that is dropped is thus T / 65536, and the
+ * factor is its exact counterpart. `seed` (64 bits) and `step` (its low 32 bits
+ * count) are read from DEVICE memory when the kernel runs: a captured call
+ * draws anew in every replay before which the caller has changed them. The gradient
+ * needs the values that the forward had. `call` tells the calls apart that
+ * share a seed and a step.
+ *
+ *   n                          : elements, 0 <= n <= 2^52
+ *   in_dtype                   : of x, 0 float32, 1 bfloat16
+ *   res_dtype                  : of residual and y (with residual NULL, y has
+ *                                in_dtype), 0 or 1
+ *   p                          : 0 <= p <= 1 (else SSM_E_UNSUPPORTED)
+ *   rng       [2]     int64     {seed, step}, 8-byte aligned
+ *   x         [n]     in_dtype
+ *   residual  [n]     res_dtype (optional)
+ *   y         [n]               may equal residual, or x of the same type
+ * Element alignment suffices. An element that is dropped is 0 whatever it held
+ * (infinities and NaN too). The product is rounded to float32 before the sum.
+ */
+int ssm_dropout_fwd(int64_t n, int in_dtype, int res_dtype, double p, uint32_t call,
+                    const int64_t* rng, const void* x, const void* residual, void* y, void* stream);
+
+/*
+ * Gradient of the dropout: dx = drop(dy), with the forward's p, call and rng
+ * (the residual's gradient is dy itself). dy, dx [n] float32; dx may equal dy.
+ */
+int ssm_dropout_bwd(int64_t n, double p, uint32_t call, const int64_t* rng, const float* dy, float* dx,
+                    void* stream);
+
+/*
+ * Layer norm of rows, with the (dropped-out) branch's addition to the residual
+ * stream in front: the counterpart of ssm_rms_norm_fwd that takes the mean off.
+ *
+ *   s = drop(x) + residual  (s = x when residual is NULL), rounded to res_dtype;
+ *       drop as in ssm_dropout_fwd over x's R d elements (p = 0: drop(x) = x)
+ *   y = (s - mean(s)) / sqrt(var(s) + eps) * weight + bias
+ *       var(s) = mean((s - mean(s))^2); weight NULL: 1; bias NULL: 0
+ *
+ *   rows, dim                  : 0 <= R < 2^31, 1 <= d <= 16384 (else
+ *                                SSM_E_UNSUPPORTED).
+ *   in_dtype, out_dtype        : of x and y, 0 float32, 1 bfloat16
+ *   res_dtype                  : of residual and residual_out, 0 or 1
+ *   eps                        : >= 0 (else SSM_E_UNSUPPORTED)
+ *   p, call, rng               : as for ssm_dropout_fwd; p > 0 needs residual
+ *                                (else SSM_E_UNSUPPORTED); rng may be NULL
+ *                                when p = 0
+ *   x         [R, d]  in_dtype
+ *   residual  [R, d]  res_dtype (optional)
+ *   weight, bias [d]  float32   (optional)
+ *   y         [R, d]  out_dtype; must not overlap any input
+ *   residual_out [R, d] res_dtype: s; required with residual, NULL without;
+ *                                may equal residual
+ * Element alignment suffices. Sums are in float32, of differences from the
+ * row's mean: a row far from zero keeps its variance. (A row whose squares pass
+ * float32's range, differences near 2^64, comes out as bias.) Deterministic.
+ */
+int ssm_layer_norm_fwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, int out_dtype, float eps,
+                       double p, uint32_t call, const int64_t* rng,
+                       const void* x, const void* residual, const float* weight, const float* bias,
+                       void* y, void* residual_out, void* stream);
+
+/*
+ * Gradients of the layer norm. s is what the forward normalised (residual_out,
+ * or x when there was no residual), dy the gradient w.r.t. y, dresidual the
+ * gradient that reaches residual_out from elsewhere.
+ *
+ *   r = 1 / sqrt(var(s) + eps),  n = (s - mean(s)) r,  u = dy * weight
+ *   ds = r (u - mean(u) - n mean(u n)) + dresidual   (the gradient w.r.t.
+ *                                                     residual)
+ *   dx = drop(ds)                                    (w.r.t. x)
+ *   dweight, dbias = sums over rows of dy n, dy
+ *
+ *   s         [R, d]  s_dtype (0 float32, 1 bfloat16)
+ *   weight    [d]     float32   (optional, 1)
+ *   dy        [R, d]  float32
+ *   dresidual [R, d]  float32   (optional, 0)
+ *   ds        [R, d]  float32   output; may equal dresidual or dy
+ *   dx        [R, d]  float32   output; required when p > 0, else optional
+ *                               (then equal to ds); may equal dresidual or dy
+ *   dweight, dbias [d] float32  outputs (optional)
+ *   p, call, rng                the forward's
+ *   workspace, workspace_bytes  at least ssm_layer_norm_bwd_workspace_bytes(),
+ *                               on a 16-byte boundary (NULL when neither
+ *                               dweight nor dbias is given)
+ */
+size_t ssm_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+int ssm_layer_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps, double p, uint32_t call,
+                       const int64_t* rng, const void* s, const float* weight, const float* dy,
+                       const float* dresidual, float* ds, float* dx, float* dweight, float* dbias,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

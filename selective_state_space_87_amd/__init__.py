@@ -10,11 +10,16 @@ from .binding import (  # noqa: F401
     ssm_abi_version,
     ssm_causal_conv1d_fwd,
     ssm_causal_conv1d_update,
+    ssm_dropout_bwd,
+    ssm_dropout_fwd,
     ssm_gated_delta_bwd,
     ssm_gated_delta_bwd_workspace_bytes,
     ssm_gated_delta_fwd,
     ssm_gated_delta_update,
     ssm_gated_delta_workspace_bytes,
+    ssm_layer_norm_bwd,
+    ssm_layer_norm_bwd_workspace_bytes,
+    ssm_layer_norm_fwd,
     ssm_rms_norm_bwd,
     ssm_rms_norm_bwd_workspace_bytes,
     ssm_rms_norm_fwd,

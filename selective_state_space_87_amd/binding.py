@@ -104,6 +104,17 @@ def _load():
         lib.ssm_rms_norm_bwd_workspace_bytes.argtypes = [i64] * 2
         lib.ssm_rms_norm_bwd.restype = i32
         lib.ssm_rms_norm_bwd.argtypes = [i64] * 2 + [i32, f32] + [vp] * 7 + [sz, vp]
+        f64, u32 = ctypes.c_double, ctypes.c_uint32
+        lib.ssm_dropout_fwd.restype = i32
+        lib.ssm_dropout_fwd.argtypes = [i64, i32, i32, f64, u32] + [vp] * 5
+        lib.ssm_dropout_bwd.restype = i32
+        lib.ssm_dropout_bwd.argtypes = [i64, f64, u32] + [vp] * 4
+        lib.ssm_layer_norm_fwd.restype = i32
+        lib.ssm_layer_norm_fwd.argtypes = [i64] * 2 + [i32] * 3 + [f32, f64, u32] + [vp] * 8
+        lib.ssm_layer_norm_bwd_workspace_bytes.restype = sz
+        lib.ssm_layer_norm_bwd_workspace_bytes.argtypes = [i64] * 2
+        lib.ssm_layer_norm_bwd.restype = i32
+        lib.ssm_layer_norm_bwd.argtypes = [i64] * 2 + [i32, f32, f64, u32] + [vp] * 10 + [sz, vp]
         _lib = lib
         return lib
 
@@ -838,3 +849,156 @@ def ssm_rms_norm_bwd(s, weight, dy, dresidual=None, eps=1e-5, ds=None, workspace
                                   _stream_handle(stream, dev))
     _check("ssm_rms_norm_bwd", st)
     return ds, dweight
+
+
+def _drop_args(p, rng, call, dev, needed=True):
+    """Checked (p, call, rng) of a dropout; rng is needed unless p is 0 and not ``needed``."""
+    p, call = float(p), int(call)
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be within [0, 1] (got {p})")
+    if not 0 <= call < 1 << 32:
+        raise ValueError(f"call must be a 32-bit number (got {call})")
+    if rng is None and (needed or p > 0):
+        raise ValueError("rng, an int64 device tensor {seed, step}, is required")
+    _dev_tensor("rng", rng, (2,), (torch.int64,), dev)
+    return p, call
+
+
+def ssm_dropout_fwd(x, p, rng, call=0, residual=None, y=None, stream=None):
+    """Dropout, with the residual's addition; see ssm_dropout_fwd in include/ssm_scan.h.
+
+    x: float32 or bfloat16, contiguous; residual: the same shape, float32 or
+    bfloat16; rng: int64 [2] on the device, {seed, step}, read when the kernel
+    runs (a captured call draws anew once they have changed); ``call`` tells
+    apart the calls that share them. Returns y, of the residual's type (x's
+    without one); it may be the residual, or x of y's type, itself.
+    """
+    lib = _load()
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPE_CODE:
+        raise ValueError("x must be a float32 or bfloat16 tensor")
+    dev = x.device
+    _dev_tensor("x", x, x.shape, (x.dtype,), dev)
+    _dev_tensor("residual", residual, x.shape, (torch.float32, torch.bfloat16), dev)
+    p, call = _drop_args(p, rng, call, dev)
+    out = x.dtype if residual is None else residual.dtype
+    with _launch_context(dev, stream):
+        if y is None:
+            y = torch.empty(x.shape, dtype=out, device=dev)
+        _dev_tensor("y", y, x.shape, (out,), dev)
+        st = lib.ssm_dropout_fwd(x.numel(), _DTYPE_CODE[x.dtype], _DTYPE_CODE[out], p, call, _ptr(rng), _ptr(x),
+                                 _ptr(residual), _ptr(y), _stream_handle(stream, dev))
+    _check("ssm_dropout_fwd", st)
+    return y
+
+
+def ssm_dropout_bwd(dy, p, rng, call=0, dx=None, stream=None):
+    """Gradient of the dropout, float32; see ssm_dropout_bwd in include/ssm_scan.h.
+
+    p, rng (with the values the forward had) and call as for ssm_dropout_fwd.
+    Returns dx, which may be dy itself.
+    """
+    lib = _load()
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError("dy must be a torch.Tensor")
+    dev, f32 = dy.device, (torch.float32,)
+    _dev_tensor("dy", dy, dy.shape, f32, dev)
+    p, call = _drop_args(p, rng, call, dev)
+    with _launch_context(dev, stream):
+        if dx is None:
+            dx = torch.empty(dy.shape, dtype=torch.float32, device=dev)
+        _dev_tensor("dx", dx, dy.shape, f32, dev)
+        st = lib.ssm_dropout_bwd(dy.numel(), p, call, _ptr(rng), _ptr(dy), _ptr(dx), _stream_handle(stream, dev))
+    _check("ssm_dropout_bwd", st)
+    return dx
+
+
+def _rows_of(name, t):
+    if not isinstance(t, torch.Tensor) or t.dim() < 1 or t.dtype not in _DTYPE_CODE:
+        raise ValueError(f"{name} must be a float32 or bfloat16 tensor [..., d]")
+    rows = 1
+    for n in t.shape[:-1]:
+        rows *= n
+    return t.device, rows, t.shape[-1]
+
+
+def ssm_layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, p=0.0, rng=None, call=0,
+                       out_dtype=None, y=None, residual_out=None, stream=None):
+    """Layer norm of rows with the (dropped-out) branch's addition to the
+    residual stream; see ssm_layer_norm_fwd in include/ssm_scan.h.
+
+    x: [..., d] float32 or bfloat16, contiguous; residual: the same shape,
+    float32 or bfloat16; weight, bias: [d] float32. p, rng, call: as for
+    ssm_dropout_fwd, of x (with a residual only). Returns a dict: y, and
+    residual_out (with a residual; may be the residual itself).
+    """
+    lib = _load()
+    dev, rows, d = _rows_of("x", x)
+    _dev_tensor("x", x, x.shape, (x.dtype,), dev)
+    _dev_tensor("weight", weight, (d,), (torch.float32,), dev)
+    _dev_tensor("bias", bias, (d,), (torch.float32,), dev)
+    _dev_tensor("residual", residual, x.shape, (torch.float32, torch.bfloat16), dev)
+    p, call = _drop_args(p, rng, call, dev, needed=False)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    if out_dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported output dtype {out_dtype}")
+    if residual is None and (residual_out is not None or p > 0):
+        raise ValueError("residual_out and p > 0 need a residual")
+    with _launch_context(dev, stream):
+        if y is None:
+            y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        _dev_tensor("y", y, x.shape, (out_dtype,), dev)
+        if residual is not None:
+            if residual_out is None:
+                residual_out = torch.empty_like(residual)
+            _dev_tensor("residual_out", residual_out, x.shape, (residual.dtype,), dev)
+        st = lib.ssm_layer_norm_fwd(rows, d, _DTYPE_CODE[x.dtype],
+                                    0 if residual is None else _DTYPE_CODE[residual.dtype], _DTYPE_CODE[out_dtype],
+                                    float(eps), p, call, _ptr(rng), _ptr(x), _ptr(residual), _ptr(weight),
+                                    _ptr(bias), _ptr(y), _ptr(residual_out), _stream_handle(stream, dev))
+    _check("ssm_layer_norm_fwd", st)
+    return {"y": y} if residual is None else {"y": y, "residual_out": residual_out}
+
+
+def ssm_layer_norm_bwd_workspace_bytes(rows, dim) -> int:
+    return int(_load().ssm_layer_norm_bwd_workspace_bytes(rows, dim))
+
+
+def ssm_layer_norm_bwd(s, weight, dy, dresidual=None, eps=1e-5, p=0.0, rng=None, call=0, ds=None, dx=None,
+                       workspace=None, stream=None):
+    """Gradients of the layer norm; see ssm_layer_norm_bwd in include/ssm_scan.h.
+
+    s: what the forward normalised (residual_out, or x without a residual)
+    [..., d]; weight: [d] float32 or None; dy, dresidual: [..., d] float32; p,
+    rng, call: the forward's. Returns a dict of float32 tensors: ds (the
+    gradient of the residual, and of x without dropout), dweight, dbias, and dx
+    (of x) when p > 0 or dx is given.
+    """
+    lib = _load()
+    dev, rows, d = _rows_of("s", s)
+    f32 = (torch.float32,)
+    _dev_tensor("s", s, s.shape, (s.dtype,), dev)
+    _dev_tensor("weight", weight, (d,), f32, dev)
+    if dy is None:
+        raise ValueError("dy is required")
+    _dev_tensor("dy", dy, s.shape, f32, dev)
+    _dev_tensor("dresidual", dresidual, s.shape, f32, dev)
+    p, call = _drop_args(p, rng, call, dev, needed=False)
+    with _launch_context(dev, stream):
+        if ds is None:
+            ds = torch.empty(s.shape, dtype=torch.float32, device=dev)
+        _dev_tensor("ds", ds, s.shape, f32, dev)
+        if dx is None and p > 0:
+            dx = torch.empty(s.shape, dtype=torch.float32, device=dev)
+        _dev_tensor("dx", dx, s.shape, f32, dev)
+        sums = torch.empty((2, d), dtype=torch.float32, device=dev)
+        dweight, dbias = sums[0], sums[1]
+        ws_bytes = int(lib.ssm_layer_norm_bwd_workspace_bytes(rows, d))
+        if workspace is None and ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        ws_size = _check_workspace(workspace, dev)
+        st = lib.ssm_layer_norm_bwd(rows, d, _DTYPE_CODE[s.dtype], float(eps), p, call, _ptr(rng), _ptr(s),
+                                    _ptr(weight), _ptr(dy), _ptr(dresidual), _ptr(ds), _ptr(dx), _ptr(dweight),
+                                    _ptr(dbias), _ptr(workspace), ws_size, _stream_handle(stream, dev))
+    _check("ssm_layer_norm_bwd", st)
+    out = {"ds": ds, "dweight": dweight, "dbias": dbias}
+    return out if dx is None else dict(out, dx=dx)

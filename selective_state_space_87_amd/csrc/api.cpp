@@ -6,6 +6,7 @@
 
 #include "gated_delta_args.h"
 #include "kernels.h"
+#include "layer_norm.h"
 #include "rms_norm.h"
 #include "ssm_scan.h"
 
@@ -964,6 +965,154 @@ int ssm_rms_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps,
   a.s_bf16 = s_dtype;
   a.eps = eps;
   return ssm::launch_rms_norm_bwd ? map_hip(ssm::launch_rms_norm_bwd(a, stream)) : SSM_E_HIP;
+}
+
+int ssm_dropout_fwd(int64_t n, int in_dtype, int res_dtype, double p, uint32_t call,
+                    const int64_t* rng, const void* x, const void* residual, void* y, void* stream) {
+  if (n < 0 || n > kMaxElems) return SSM_E_SHAPE;
+  if (!(p >= 0.0 && p <= 1.0)) return SSM_E_UNSUPPORTED;
+  if ((in_dtype != 0 && in_dtype != 1) || (residual && res_dtype != 0 && res_dtype != 1)) return SSM_E_DTYPE;
+  if (n == 0) return SSM_OK;
+  if (rng == nullptr || x == nullptr || y == nullptr) return SSM_E_NULLPTR;
+  const int out_dtype = residual ? res_dtype : in_dtype;
+  const int64_t isz = in_dtype == 1 ? 2 : 4, osz = out_dtype == 1 ? 2 : 4;
+  if (!aligned(rng, 8) || !aligned(x, static_cast<uintptr_t>(isz)) || !aligned(residual, static_cast<uintptr_t>(osz)) ||
+      !aligned(y, static_cast<uintptr_t>(osz))) {
+    return SSM_E_ALIGN;
+  }
+  const Range rx = span(x, n, isz), rr = span(residual, n, osz), ry = span(y, n, osz);
+  if (overlaps(ry, span(rng, 2, 8))) return SSM_E_ALIAS;
+  // in place: a thread has read its elements before it writes them
+  if (overlaps(ry, rx) && (ry.lo != rx.lo || isz != osz)) return SSM_E_ALIAS;
+  if (overlaps(ry, rr) && ry.lo != rr.lo) return SSM_E_ALIAS;
+
+  ssm::DropoutArgs a;
+  a.x = x;
+  a.residual = residual;
+  a.y = y;
+  a.n = n;
+  a.in_bf16 = in_dtype;
+  a.out_bf16 = out_dtype;
+  a.drop = ssm::drop_args(rng, call, p);
+  return ssm::launch_dropout ? map_hip(ssm::launch_dropout(a, stream)) : SSM_E_HIP;
+}
+
+int ssm_dropout_bwd(int64_t n, double p, uint32_t call, const int64_t* rng, const float* dy, float* dx,
+                    void* stream) {
+  return ssm_dropout_fwd(n, 0, 0, p, call, rng, dy, nullptr, dx, stream);
+}
+
+int ssm_layer_norm_fwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, int out_dtype, float eps,
+                       double p, uint32_t call, const int64_t* rng,
+                       const void* x, const void* residual, const float* weight, const float* bias,
+                       void* y, void* residual_out, void* stream) {
+  int64_t n;
+  if (rows < 0 || dim < 1 || !safe_mul(rows, dim, &n)) return SSM_E_SHAPE;
+  if (dim > ssm::kLayerNormMaxDim || rows > 0x7fffffff || !(eps >= 0.0f)) return SSM_E_UNSUPPORTED;
+  if (!(p >= 0.0 && p <= 1.0) || (p > 0.0 && residual == nullptr && rows > 0)) return SSM_E_UNSUPPORTED;
+  if ((in_dtype != 0 && in_dtype != 1) || (residual && res_dtype != 0 && res_dtype != 1) ||
+      (out_dtype != 0 && out_dtype != 1)) {
+    return SSM_E_DTYPE;
+  }
+  if (rows == 0) return SSM_OK;
+  if (x == nullptr || y == nullptr || (residual == nullptr) != (residual_out == nullptr) ||
+      (p > 0.0 && rng == nullptr)) {
+    return SSM_E_NULLPTR;
+  }
+  const int64_t isz = in_dtype == 1 ? 2 : 4, rsz = res_dtype == 1 ? 2 : 4, osz = out_dtype == 1 ? 2 : 4;
+  if (!aligned(x, static_cast<uintptr_t>(isz)) || !aligned(residual, static_cast<uintptr_t>(rsz)) ||
+      !aligned(residual_out, static_cast<uintptr_t>(rsz)) || !aligned(weight, 4) || !aligned(bias, 4) ||
+      !aligned(y, static_cast<uintptr_t>(osz)) || !aligned(rng, 8)) {
+    return SSM_E_ALIGN;
+  }
+  const Range rr = span(residual, n, rsz), ry = span(y, n, osz), ro = span(residual_out, n, rsz);
+  const Range in[] = {span(x, n, isz), span(weight, dim, 4), span(bias, dim, 4), span(rng, 2, 8)};
+  for (const Range& r : in) {
+    if (overlaps(ry, r) || overlaps(ro, r)) return SSM_E_ALIAS;
+  }
+  if (overlaps(ry, rr) || overlaps(ry, ro) || (overlaps(ro, rr) && ro.lo != rr.lo)) return SSM_E_ALIAS;
+
+  ssm::LayerNormArgs a;
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.bias = bias;
+  a.y = y;
+  a.residual_out = residual_out;
+  a.rows = rows;
+  a.dim = dim;
+  a.in_bf16 = in_dtype;
+  a.res_bf16 = residual ? res_dtype : 0;
+  a.out_bf16 = out_dtype;
+  a.eps = eps;
+  a.drop = ssm::drop_args(rng, call, p);
+  return ssm::launch_layer_norm ? map_hip(ssm::launch_layer_norm(a, stream)) : SSM_E_HIP;
+}
+
+size_t ssm_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim) {
+  int64_t n;
+  if (rows < 1 || dim < 1 || dim > ssm::kLayerNormMaxDim || rows > 0x7fffffff || !safe_mul(rows, dim, &n)) return 0;
+  return static_cast<size_t>(ssm::layer_norm_bwd_blocks(rows, dim)) * static_cast<size_t>(dim) * 8;
+}
+
+int ssm_layer_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps, double p, uint32_t call,
+                       const int64_t* rng, const void* s, const float* weight, const float* dy,
+                       const float* dresidual, float* ds, float* dx, float* dweight, float* dbias,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  int64_t n;
+  if (rows < 0 || dim < 1 || !safe_mul(rows, dim, &n)) return SSM_E_SHAPE;
+  if (dim > ssm::kLayerNormMaxDim || rows > 0x7fffffff || !(eps >= 0.0f) || !(p >= 0.0 && p <= 1.0)) {
+    return SSM_E_UNSUPPORTED;
+  }
+  if (s_dtype != 0 && s_dtype != 1) return SSM_E_DTYPE;
+  if (rows == 0 && dweight == nullptr && dbias == nullptr) return SSM_OK;
+  if (rows > 0 && (s == nullptr || dy == nullptr || ds == nullptr)) return SSM_E_NULLPTR;
+  if (rows > 0 && p > 0.0 && (rng == nullptr || dx == nullptr)) return SSM_E_NULLPTR;
+  const int64_t ssz = s_dtype == 1 ? 2 : 4;
+  const void* f32_ptrs[] = {weight, dy, dresidual, ds, dx, dweight, dbias};
+  for (const void* q : f32_ptrs) {
+    if (!aligned(q, 4)) return SSM_E_ALIGN;
+  }
+  if (!aligned(s, static_cast<uintptr_t>(ssz)) || !aligned(rng, 8)) return SSM_E_ALIGN;
+  const size_t need = dweight || dbias ? ssm_layer_norm_bwd_workspace_bytes(rows, dim) : 0;
+  if (need > 0 && workspace != nullptr && !aligned(workspace, 16)) return SSM_E_ALIGN;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_E_WORKSPACE;
+  const Range rs = span(s, n, ssz), rw = span(weight, dim, 4), ry = span(dy, n, 4), rr = span(dresidual, n, 4);
+  const Range rg = span(rng, 2, 8);
+  const Range rds = span(ds, n, 4), rdx = span(dx, n, 4), rdw = span(dweight, dim, 4), rdb = span(dbias, dim, 4);
+  const Range rws = span(need > 0 ? workspace : nullptr, static_cast<int64_t>(need), 1);
+  // ds and dx are written where dy and dresidual have been read; nothing else is shared
+  const Range fixed[] = {rs, rw, rg, rdw, rdb, rws};
+  for (const Range& r : fixed) {
+    if (overlaps(rds, r) || overlaps(rdx, r)) return SSM_E_ALIAS;
+  }
+  const Range rows_in[] = {ry, rr};
+  for (const Range& r : rows_in) {
+    if ((overlaps(rds, r) && rds.lo != r.lo) || (overlaps(rdx, r) && rdx.lo != r.lo)) return SSM_E_ALIAS;
+  }
+  if (overlaps(rds, rdx)) return SSM_E_ALIAS;
+  const Range in[] = {rs, rw, ry, rr, rg};
+  for (const Range& r : in) {
+    if (overlaps(rdw, r) || overlaps(rdb, r) || overlaps(rws, r)) return SSM_E_ALIAS;
+  }
+  if (overlaps(rdw, rws) || overlaps(rdb, rws) || overlaps(rdw, rdb)) return SSM_E_ALIAS;
+
+  ssm::LayerNormBwdArgs a;
+  a.s = s;
+  a.weight = weight;
+  a.dy = dy;
+  a.dresidual = dresidual;
+  a.ds = ds;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.workspace = workspace;
+  a.rows = rows;
+  a.dim = dim;
+  a.s_bf16 = s_dtype;
+  a.eps = eps;
+  a.drop = ssm::drop_args(rng, call, p);
+  return ssm::launch_layer_norm_bwd ? map_hip(ssm::launch_layer_norm_bwd(a, stream)) : SSM_E_HIP;
 }
 
 }  // extern "C"

@@ -1,0 +1,347 @@
+// Layer norm of rows with the dropped-out residual addition, and its gradients.
+//
+//   s = drop(x) + residual;  d = s - mean(s);  y = d r weight + bias,
+//   r = 1 / sqrt(mean(d^2) + eps)
+//   u = dy weight, n = d r:  ds = r (u - mean(u) - n mean(u n)) + dresidual,
+//   dx = drop(ds);  dweight = sum_rows dy n;  dbias = sum_rows dy
+//
+// Bounded by HBM: a row crosses it once and lives in the registers of its
+// threads between the sums and the output: one wave a row up to 1024 elements,
+// four rows a block; above, a block of 4, 8 or 16 waves a row. The mean is
+// taken first, then the sums of the differences from it, their squares and
+// (backward) their products: a row far from zero loses nothing, and what the
+// first sum was rounded by is taken off as the mean of the differences.
+#include <hip/hip_runtime.h>
+
+#include "device_math.h"
+#include "layer_norm.h"
+#include "philox.h"
+#include "rows.h"
+
+namespace ssm {
+
+namespace {
+
+constexpr int block_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+// RES: 0 none, 1 float32, 2 bfloat16.
+template <int TPR, int NPK, bool BF16_IN, int RES, bool BF16_OUT>
+__global__ __launch_bounds__(block_threads(TPR)) void layer_norm_kernel(const LayerNormArgs p) {
+  constexpr int kRows = block_threads(TPR) / TPR, kWaves = TPR / 64;
+  __shared__ float sum_slots[kWaves][1], square_slots[kWaves][2];
+  const int dim = static_cast<int>(p.dim);
+  const int t = threadIdx.x % TPR;
+  const float inv = 1.0f / static_cast<float>(dim);
+  float w[NPK][8], bias[NPK][8];
+#pragma unroll
+  for (int i = 0; i < NPK; ++i) {
+    const int e = (i * TPR + t) * 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[i][k] = 1.0f, bias[i][k] = 0.0f;
+    if (p.weight != nullptr) load_piece<false>(p.weight, e, dim - e, w[i]);
+    if (p.bias != nullptr) load_piece<false>(p.bias, e, dim - e, bias[i]);
+  }
+  DropKey key{};
+  if (p.drop.threshold != 0) key = drop_key(p.drop.rng, p.drop.call, p.drop.threshold, p.drop.scale);
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR; row < p.rows;
+       row += static_cast<int64_t>(gridDim.x) * kRows) {
+    const int64_t at = row * dim;
+    float s[NPK][8], sum[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NPK; ++i) {
+      const int e = (i * TPR + t) * 8;
+      load_piece<BF16_IN>(p.x, at + e, dim - e, s[i]);
+    }
+    if constexpr (RES != 0) {
+      float r[NPK][8];
+#pragma unroll
+      for (int i = 0; i < NPK; ++i) {
+        const int e = (i * TPR + t) * 8;
+        load_piece<RES == 2>(p.residual, at + e, dim - e, r[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < NPK; ++i) {
+        const int e = (i * TPR + t) * 8;
+        if (p.drop.threshold != 0 && e < dim) drop8(key, static_cast<uint64_t>(at + e), s[i]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          s[i][k] += r[i][k];
+          // the norm is taken of what the stream holds
+          if constexpr (RES == 2) s[i][k] = bf16_bits_to_f32(f32_to_bf16_bits(s[i][k]));
+        }
+        store_piece<RES == 2>(p.residual_out, at + e, dim - e, s[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NPK; ++i) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[0] += s[i][k];
+    }
+    row_sums<TPR>(sum, sum_slots);
+    const float mean = sum[0] * inv;
+    float sums[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NPK; ++i) {
+      const int left = dim - (i * TPR + t) * 8;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s[i][k] = k < left ? s[i][k] - mean : 0.0f;
+        sums[0] += s[i][k];
+        sums[1] = fmaf(s[i][k], s[i][k], sums[1]);
+      }
+    }
+    row_sums<TPR>(sums, square_slots);
+    const float rest = sums[0] * inv;
+    const float var = fmaf(-rest, rest, sums[1] * inv);
+    const float r = rsqrtf((var < 0.0f ? 0.0f : var) + p.eps);  // (NaN stays)
+#pragma unroll
+    for (int i = 0; i < NPK; ++i) {
+      const int e = (i * TPR + t) * 8;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[i][k] = fmaf((s[i][k] - rest) * r, w[i][k], bias[i][k]);
+      store_piece<BF16_OUT>(p.y, at + e, dim - e, s[i]);
+    }
+  }
+}
+
+// Gradients. A block takes every gridDim.x-th row (or four rows, one a wave)
+// and keeps its parts of dweight and dbias in registers; the parts are added by
+// layer_norm_sums_kernel in block order.
+template <int TPR, int NPK, bool BF16>
+__global__ __launch_bounds__(block_threads(TPR)) void layer_norm_bwd_kernel(const LayerNormBwdArgs p) {
+  constexpr int kRows = block_threads(TPR) / TPR, kWaves = TPR / 64;
+  __shared__ float sum_slots[kWaves][1], product_slots[kWaves][4];
+  const int dim = static_cast<int>(p.dim);
+  const int t = threadIdx.x % TPR, part = threadIdx.x / TPR;
+  const float inv = 1.0f / static_cast<float>(dim);
+  float dw[NPK][8], db[NPK][8], w[NPK][8];
+#pragma unroll
+  for (int i = 0; i < NPK; ++i) {
+    const int e = (i * TPR + t) * 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dw[i][k] = db[i][k] = 0.0f, w[i][k] = 1.0f;
+    if (p.weight != nullptr) load_piece<false>(p.weight, e, dim - e, w[i]);
+  }
+  DropKey key{};
+  if (p.dx != nullptr && p.drop.threshold != 0) {
+    key = drop_key(p.drop.rng, p.drop.call, p.drop.threshold, p.drop.scale);
+  }
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + part; row < p.rows;
+       row += static_cast<int64_t>(gridDim.x) * kRows) {
+    const int64_t at = row * dim;
+    float s[NPK][8], g[NPK][8], o[NPK][8], sum[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NPK; ++i) {
+      const int e = (i * TPR + t) * 8;
+      load_piece<BF16>(p.s, at + e, dim - e, s[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NPK; ++i) {
+      const int e = (i * TPR + t) * 8;
+      load_piece<false>(p.dy, at + e, dim - e, g[i]);
+    }
+    if (p.dresidual != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NPK; ++i) {
+        const int e = (i * TPR + t) * 8;
+        load_piece<false>(p.dresidual, at + e, dim - e, o[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NPK; ++i) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[i][k] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NPK; ++i) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[0] += s[i][k];
+    }
+    row_sums<TPR>(sum, sum_slots);
+    const float mean = sum[0] * inv;
+    float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // of d, d^2, u, u d
+#pragma unroll
+    for (int i = 0; i < NPK; ++i) {
+      const int left = dim - (i * TPR + t) * 8;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s[i][k] = k < left ? s[i][k] - mean : 0.0f;
+        const float u = g[i][k] * w[i][k];
+        sums[0] += s[i][k];
+        sums[1] = fmaf(s[i][k], s[i][k], sums[1]);
+        sums[2] += u;
+        sums[3] = fmaf(u, s[i][k], sums[3]);
+      }
+    }
+    row_sums<TPR>(sums, product_slots);
+    const float rest = sums[0] * inv, mu = sums[2] * inv;
+    const float var = fmaf(-rest, rest, sums[1] * inv);
+    const float r = rsqrtf((var < 0.0f ? 0.0f : var) + p.eps);
+    const float c = fmaf(-rest, mu, sums[3] * inv) * r;  // mean(u n)
+#pragma unroll
+    for (int i = 0; i < NPK; ++i) {
+      const int e = (i * TPR + t) * 8;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float n = (s[i][k] - rest) * r;
+        dw[i][k] = fmaf(g[i][k], n, dw[i][k]);
+        db[i][k] += g[i][k];
+        o[i][k] = fmaf(r, fmaf(g[i][k], w[i][k], -mu) - n * c, o[i][k]);
+      }
+      store_piece<false>(p.ds, at + e, dim - e, o[i]);
+      if (p.dx != nullptr && e < dim) {
+        if (p.drop.threshold != 0) drop8(key, static_cast<uint64_t>(at + e), o[i]);
+        store_piece<false>(p.dx, at + e, dim - e, o[i]);
+      }
+    }
+  }
+  if (p.dweight == nullptr && p.dbias == nullptr) return;
+  // parts [block][dweight, dbias][dim]
+  float* out = static_cast<float*>(p.workspace) + static_cast<int64_t>(blockIdx.x) * 2 * dim;
+  if constexpr (kRows == 1) {
+#pragma unroll
+    for (int i = 0; i < NPK; ++i) {
+      const int e = (i * TPR + t) * 8;
+      store_piece<false>(out, e, dim - e, dw[i]);
+      store_piece<false>(out, dim + e, dim - e, db[i]);
+    }
+  } else {
+    __shared__ float adds[kRows][NPK * 8 * TPR];
+    const auto add = [&](float (&v)[NPK][8], int64_t to) {
+#pragma unroll
+      for (int i = 0; i < NPK; ++i) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) adds[part][(i * 8 + k) * TPR + t] = v[i][k];
+      }
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int i = 0; i < NPK; ++i) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int from = (i * 8 + k) * TPR + t;
+            v[i][k] = (adds[0][from] + adds[1][from]) + (adds[2][from] + adds[3][from]);
+          }
+          const int e = (i * TPR + t) * 8;
+          store_piece<false>(out, to + e, dim - e, v[i]);
+        }
+      }
+      __syncthreads();
+    };
+    add(dw, 0);
+    add(db, dim);
+  }
+}
+
+// dweight[c], dbias[c] = sums over the blocks' parts: 64 of the 2 dim columns a
+// block, sixteen waves each adding every sixteenth part, eight loads at a time,
+// then the sixteen sums in order.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void layer_norm_sums_kernel(const float* __restrict__ parts, int nparts,
+                                                                         int dim, float* __restrict__ dweight,
+                                                                         float* __restrict__ dbias) {
+  __shared__ float sums[kSumWaves][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int c = static_cast<int>(blockIdx.x) * 64 + lane;
+  const int64_t step = 2 * static_cast<int64_t>(dim);
+  float acc = 0.0f;
+  if (c < 2 * dim) {
+    int i = w;
+    for (; i + 7 * kSumWaves < nparts; i += 8 * kSumWaves) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = parts[(i + k * kSumWaves) * step + c];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc += v[k];
+    }
+    for (; i < nparts; i += kSumWaves) acc += parts[i * step + c];
+  }
+  sums[w][lane] = acc;
+  __syncthreads();
+  if (w == 0 && c < 2 * dim) {
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kSumWaves; ++k) v += sums[k][lane];
+    if (c < dim) {
+      if (dweight != nullptr) dweight[c] = v;
+    } else if (dbias != nullptr) {
+      dbias[c - dim] = v;
+    }
+  }
+}
+
+// f(threads per row, pieces a thread) for a row of `dim` elements.
+template <typename F>
+void by_width(int64_t dim, F&& f) {
+  using std::integral_constant;
+  if (dim <= 512) {
+    f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  } else if (dim <= 1024) {
+    f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  } else if (dim <= 2048) {
+    f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  } else if (dim <= 4096) {
+    f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  } else if (dim <= 8192) {
+    f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+  } else {
+    f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  }
+}
+
+// Blocks that take rows in turn, each with its weights in registers.
+constexpr int64_t kForwardBlocks = 4096;
+
+template <bool BI, int RES>
+void launch_norm(const LayerNormArgs& a, hipStream_t st) {
+  by_width(a.dim, [&](auto tpr, auto npk) {
+    constexpr int TPR = decltype(tpr)::value, NPK = decltype(npk)::value, kBlock = block_threads(TPR);
+    const int64_t groups = (a.rows + kBlock / TPR - 1) / (kBlock / TPR);
+    const unsigned blocks = static_cast<unsigned>(groups < kForwardBlocks ? groups : kForwardBlocks);
+    a.out_bf16 ? layer_norm_kernel<TPR, NPK, BI, RES, true><<<blocks, kBlock, 0, st>>>(a)
+               : layer_norm_kernel<TPR, NPK, BI, RES, false><<<blocks, kBlock, 0, st>>>(a);
+  });
+}
+
+template <bool BI>
+void launch_norm_res(const LayerNormArgs& a, hipStream_t st) {
+  if (a.residual == nullptr) {
+    launch_norm<BI, 0>(a, st);
+  } else if (a.res_bf16) {
+    launch_norm<BI, 2>(a, st);
+  } else {
+    launch_norm<BI, 1>(a, st);
+  }
+}
+
+}  // namespace
+
+int launch_layer_norm(const LayerNormArgs& a, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  a.in_bf16 ? launch_norm_res<true>(a, st) : launch_norm_res<false>(a, st);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_layer_norm_bwd(const LayerNormBwdArgs& a, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  int nparts = 0;
+  if (a.rows > 0) {
+    nparts = static_cast<int>(layer_norm_bwd_blocks(a.rows, a.dim));
+    by_width(a.dim, [&](auto tpr, auto npk) {
+      constexpr int TPR = decltype(tpr)::value, NPK = decltype(npk)::value, kBlock = block_threads(TPR);
+      const unsigned blocks = static_cast<unsigned>(nparts);
+      a.s_bf16 ? layer_norm_bwd_kernel<TPR, NPK, true><<<blocks, kBlock, 0, st>>>(a)
+               : layer_norm_bwd_kernel<TPR, NPK, false><<<blocks, kBlock, 0, st>>>(a);
+    });
+    if (const hipError_t e = hipGetLastError()) return static_cast<int>(e);
+  }
+  if (a.dweight != nullptr || a.dbias != nullptr) {
+    const unsigned blocks = static_cast<unsigned>((2 * a.dim + 63) / 64);
+    layer_norm_sums_kernel<<<blocks, 64 * kSumWaves, 0, st>>>(static_cast<const float*>(a.workspace), nparts,
+                                                              static_cast<int>(a.dim), a.dweight, a.dbias);
+  }
+  return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace ssm
