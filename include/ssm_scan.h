@@ -64,7 +64,8 @@ extern "C" {
  * the backward from them were added.
  * 3: the gated delta rule (forward, backward, single-token update) and the RMS
  * norm (forward, backward) were added.
- * 4: the layer norm and the dropout (forward, backward) were added. */
+ * 4: the layer norm and the dropout (forward, backward) and the gradients of the
+ * causal convolution were added. */
 #define SSM_ABI_VERSION 4
 
 /* Status codes. */
@@ -709,6 +710,39 @@ int ssm_layer_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps, double
                        const int64_t* rng, const void* s, const float* weight, const float* dy,
                        const float* dresidual, float* ds, float* dx, float* dweight, float* dbias,
                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of a loss through ssm_causal_conv1d_fwd with the same inputs, given
+ * dy = dL/dy and optionally dstate_out:
+ *
+ *   g[b,l,d]  = dy[b,l,d] * silu'(out[b,l,d])   (dy itself without the activation)
+ *   dx[b,l,d] = sum_{k<K} weight[d,k] * g[b, l+(K-1)-k, d]   (+ dstate_out of
+ *               the input's slot), for the inputs of the carried state (l < 0) too:
+ *               dstate_in
+ *   dweight[d,k] = sum_{b,l} g[b,l,d] * x[b, l-(K-1)+k, d];  dbias[d] = sum_{b,l} g
+ *
+ *   sizes, in_dtype (of x), silu_activation and inputs as for the forward.
+ *   dy        [B, L, d]   float32   gradient w.r.t. y
+ *   dstate_out [B, d, K-1] float32  gradient w.r.t. state_out (optional, 0)
+ *   dx        [B, L, d]   float32   output
+ *   dweight   [d, K]      float32   output (optional)
+ *   dbias     [d]         float32   output (optional, with or without a bias)
+ *   dstate_in [B, d, K-1] float32   output (optional, with or without a state)
+ *   workspace, workspace_bytes      at least
+ *                                   ssm_causal_conv1d_bwd_workspace_bytes(), on a
+ *                                   16-byte boundary (NULL when neither dweight
+ *                                   nor dbias is given)
+ * x, dy and dx must be 16-byte aligned, float32 arrays 4-byte aligned. No
+ * output may overlap an input, another output or the workspace. Deterministic:
+ * the sums are taken in segments of the steps, joined in a fixed order.
+ */
+size_t ssm_causal_conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t width);
+int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width,
+                          int in_dtype, int silu_activation,
+                          const void* x, const float* weight, const float* bias, const float* state_in,
+                          const float* dy, const float* dstate_out,
+                          float* dx, float* dweight, float* dbias, float* dstate_in,
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

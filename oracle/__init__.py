@@ -18,7 +18,7 @@ Sources, cited by tag throughout:
 - [Notes]       lyirs.cc, "Mamba" (study notes on Gu & Dao 2023).
 """
 
-from .conv_oracle import causal_conv1d, causal_conv1d_update  # noqa: F401
+from .conv_oracle import causal_conv1d, causal_conv1d_bwd, causal_conv1d_update  # noqa: F401
 from .scan_bwd_oracle import selective_scan_bwd  # noqa: F401
 from .ssd_oracle import ssd_quadratic, ssd_recurrent  # noqa: F401
 from .ssm_oracle import (  # noqa: F401

@@ -31,7 +31,7 @@ import numpy as np
 
 from .ssm_oracle import silu
 
-__all__ = ["causal_conv1d", "causal_conv1d_update"]
+__all__ = ["causal_conv1d", "causal_conv1d_update", "causal_conv1d_bwd"]
 
 
 def _f64(x):
@@ -67,3 +67,28 @@ def causal_conv1d_update(state, x, weight, bias=None, silu_activation=True):
     x = _f64(x)
     y, state_out = causal_conv1d(x[:, None, :], weight, bias, silu_activation, state)
     return y[:, 0, :], state_out
+
+
+def causal_conv1d_bwd(x, weight, dy, bias=None, silu_activation=True, state=None, dstate_out=None):
+    """Gradients of sum(dy y) + sum(dstate_out state_out): a dict of dx, dweight,
+    dbias, dstate_in, and `g`, the gradient of the value before the activation.
+    Term by term from the forward's sum: out[l] takes weight[:, k] xe[l + k]."""
+    x, w, dy = _f64(x), _f64(weight), _f64(dy)
+    Bt, L, d = x.shape
+    K = w.shape[1]
+    prefix = np.zeros((Bt, K - 1, d)) if state is None else np.transpose(_f64(state), (0, 2, 1))
+    xe = np.concatenate([prefix, x], axis=1)
+    g = dy
+    if silu_activation:
+        z = causal_conv1d(x, w, bias, False, state)[0]
+        s = 0.5 * (1.0 + np.tanh(0.5 * z))  # the sigmoid, without overflow
+        g = dy * s * (1.0 + z * (1.0 - s))
+    dxe = np.zeros_like(xe)
+    dw = np.zeros_like(w)
+    for k in range(K):
+        dxe[:, k:k + L] += g * w[:, k]
+        dw[:, k] = (g * xe[:, k:k + L]).sum((0, 1))
+    if dstate_out is not None:
+        dxe[:, L:] += np.transpose(_f64(dstate_out), (0, 2, 1))
+    return dict(dx=dxe[:, K - 1:], dweight=dw, dbias=g.sum((0, 1)), g=g,
+                dstate_in=np.transpose(dxe[:, :K - 1], (0, 2, 1)).copy())

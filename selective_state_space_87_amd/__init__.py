@@ -8,6 +8,8 @@ unloadable library raises at once.
 
 from .binding import (  # noqa: F401
     ssm_abi_version,
+    ssm_causal_conv1d_bwd,
+    ssm_causal_conv1d_bwd_workspace_bytes,
     ssm_causal_conv1d_fwd,
     ssm_causal_conv1d_update,
     ssm_dropout_bwd,

@@ -115,6 +115,10 @@ def _load():
         lib.ssm_layer_norm_bwd_workspace_bytes.argtypes = [i64] * 2
         lib.ssm_layer_norm_bwd.restype = i32
         lib.ssm_layer_norm_bwd.argtypes = [i64] * 2 + [i32, f32, f64, u32] + [vp] * 10 + [sz, vp]
+        lib.ssm_causal_conv1d_bwd_workspace_bytes.restype = sz
+        lib.ssm_causal_conv1d_bwd_workspace_bytes.argtypes = [i64] * 4
+        lib.ssm_causal_conv1d_bwd.restype = i32
+        lib.ssm_causal_conv1d_bwd.argtypes = [i64] * 4 + [i32] * 2 + [vp] * 11 + [sz, vp]
         _lib = lib
         return lib
 
@@ -1002,3 +1006,51 @@ def ssm_layer_norm_bwd(s, weight, dy, dresidual=None, eps=1e-5, p=0.0, rng=None,
     _check("ssm_layer_norm_bwd", st)
     out = {"ds": ds, "dweight": dweight, "dbias": dbias}
     return out if dx is None else dict(out, dx=dx)
+
+
+def ssm_causal_conv1d_bwd_workspace_bytes(batch, seqlen, dim, width) -> int:
+    return int(_load().ssm_causal_conv1d_bwd_workspace_bytes(batch, seqlen, dim, width))
+
+
+def ssm_causal_conv1d_bwd(x, weight, dy, bias=None, state_in=None, dstate_out=None, silu_activation=True,
+                          dx=None, workspace=None, stream=None):
+    """Gradients of the causal convolution; see ssm_causal_conv1d_bwd in include/ssm_scan.h.
+
+    x, weight, bias, state_in: the forward's; dy: [B, L, d], dstate_out:
+    [B, d, K-1] float32. Returns a dict of float32 tensors: dx, dweight,
+    dstate_in, and dbias when bias is given.
+    """
+    lib = _load()
+    if not isinstance(x, torch.Tensor) or x.dim() != 3 or x.dtype not in _DTYPE_CODE:
+        raise ValueError("x must be a 3-d float32 or bfloat16 tensor [B, L, d]")
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a 2-d tensor [d, K]")
+    dev, f32 = x.device, (torch.float32,)
+    Bt, L, d = x.shape
+    K = weight.shape[1]
+    _dev_tensor("x", x, (Bt, L, d), (x.dtype,), dev)
+    _dev_tensor("weight", weight, (d, K), f32, dev)
+    _dev_tensor("bias", bias, (d,), f32, dev)
+    _dev_tensor("state_in", state_in, (Bt, d, K - 1), f32, dev)
+    if dy is None:
+        raise ValueError("dy is required")
+    _dev_tensor("dy", dy, (Bt, L, d), f32, dev)
+    _dev_tensor("dstate_out", dstate_out, (Bt, d, K - 1), f32, dev)
+    new = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)  # noqa: E731
+    with _launch_context(dev, stream):
+        if dx is None:
+            dx = new(Bt, L, d)
+        _dev_tensor("dx", dx, (Bt, L, d), f32, dev)
+        out = dict(dx=dx, dweight=new(d, K), dstate_in=new(Bt, d, K - 1))
+        if bias is not None:
+            out["dbias"] = new(d)
+        ws_bytes = int(lib.ssm_causal_conv1d_bwd_workspace_bytes(Bt, L, d, K))
+        if workspace is None and ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        ws_size = _check_workspace(workspace, dev)
+        st = lib.ssm_causal_conv1d_bwd(Bt, L, d, K, _DTYPE_CODE[x.dtype], 1 if silu_activation else 0, _ptr(x),
+                                       _ptr(weight), _ptr(bias), _ptr(state_in), _ptr(dy), _ptr(dstate_out),
+                                       _ptr(dx), _ptr(out["dweight"]), _ptr(out.get("dbias")),
+                                       _ptr(out["dstate_in"]), _ptr(workspace), ws_size, _stream_handle(stream, dev))
+    _check("ssm_causal_conv1d_bwd", st)
+    return out

@@ -4,6 +4,7 @@
 // side effects (and without a HIP device being present at all).
 #include <cstdint>
 
+#include "conv1d_bwd.h"
 #include "gated_delta_args.h"
 #include "kernels.h"
 #include "layer_norm.h"
@@ -1113,6 +1114,83 @@ int ssm_layer_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps, double
   a.eps = eps;
   a.drop = ssm::drop_args(rng, call, p);
   return ssm::launch_layer_norm_bwd ? map_hip(ssm::launch_layer_norm_bwd(a, stream)) : SSM_E_HIP;
+}
+
+size_t ssm_causal_conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t width) {
+  int64_t t, k;
+  if (batch < 1 || batch > 65535 || seqlen < 0 || seqlen > kMaxConvSeq || dim < 1 || width < 1 ||
+      width > kMaxConvWidth) {
+    return 0;
+  }
+  if (!safe_mul(batch, seqlen, &t) || !safe_mul(t, dim, &t) || !safe_mul(batch, dim, &k) ||
+      !safe_mul(k, width + 1, &k)) {
+    return 0;
+  }
+  return ssm::plan_conv1d_bwd(batch, seqlen, dim, width).bytes;
+}
+
+int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width,
+                          int in_dtype, int silu_activation,
+                          const void* x, const float* weight, const float* bias, const float* state_in,
+                          const float* dy, const float* dstate_out,
+                          float* dx, float* dweight, float* dbias, float* dstate_in,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  if (batch < 0 || seqlen < 0 || dim < 0 || width < 1) return SSM_E_SHAPE;
+  if (width > kMaxConvWidth || batch > 65535 || seqlen > kMaxConvSeq) return SSM_E_UNSUPPORTED;
+  if (in_dtype != 0 && in_dtype != 1) return SSM_E_DTYPE;
+  int64_t bl, bld, bd, bds, dk, most;
+  if (!safe_mul(batch, seqlen, &bl) || !safe_mul(bl, dim, &bld) || !safe_mul(batch, dim, &bd) ||
+      !safe_mul(bd, width - 1, &bds) || !safe_mul(dim, width, &dk) || !safe_mul(bd, width + 1, &most) ||
+      !safe_mul(dim, width + 1, &most)) {
+    return SSM_E_SHAPE;
+  }
+  if (dim == 0 || (batch == 0 && dweight == nullptr && dbias == nullptr)) return SSM_OK;
+  if (batch > 0 && weight == nullptr) return SSM_E_NULLPTR;
+  if (bl > 0 && (x == nullptr || dy == nullptr || dx == nullptr)) return SSM_E_NULLPTR;
+  const void* vec_ptrs[] = {x, dy, dx};
+  for (const void* q : vec_ptrs) {
+    if (!aligned(q, 16)) return SSM_E_ALIGN;
+  }
+  const void* f32_ptrs[] = {weight, bias, state_in, dstate_out, dweight, dbias, dstate_in};
+  for (const void* q : f32_ptrs) {
+    if (!aligned(q, 4)) return SSM_E_ALIGN;
+  }
+  const size_t need = dweight || dbias ? ssm_causal_conv1d_bwd_workspace_bytes(batch, seqlen, dim, width) : 0;
+  if (need > 0 && workspace != nullptr && !aligned(workspace, 16)) return SSM_E_ALIGN;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_E_WORKSPACE;
+  const int64_t isz = in_dtype == 1 ? 2 : 4;
+  const Range in[] = {span(x, bld, isz), span(weight, dk, 4), span(bias, dim, 4), span(state_in, bds, 4),
+                      span(dy, bld, 4), span(dstate_out, bds, 4)};
+  const Range out[] = {span(dx, bld, 4), span(dweight, dk, 4), span(dbias, dim, 4), span(dstate_in, bds, 4),
+                       span(need > 0 ? workspace : nullptr, static_cast<int64_t>(need), 1)};
+  for (int i = 0; i < 5; ++i) {
+    for (const Range& r : in) {
+      if (overlaps(out[i], r)) return SSM_E_ALIAS;
+    }
+    for (int j = 0; j < i; ++j) {
+      if (overlaps(out[i], out[j])) return SSM_E_ALIAS;
+    }
+  }
+
+  ssm::ConvBwdArgs a;
+  a.x = x;
+  a.weight = weight;
+  a.bias = bias;
+  a.state_in = state_in;
+  a.dy = dy;
+  a.dstate_out = dstate_out;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.dstate_in = dstate_in;
+  a.workspace = workspace;
+  a.batch = batch;
+  a.seqlen = seqlen;
+  a.dim = dim;
+  a.width = width;
+  a.in_bf16 = in_dtype;
+  a.silu = silu_activation ? 1 : 0;
+  return ssm::launch_conv1d_bwd ? map_hip(ssm::launch_conv1d_bwd(a, stream)) : SSM_E_HIP;
 }
 
 }  // extern "C"

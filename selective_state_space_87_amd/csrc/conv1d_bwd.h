@@ -1,0 +1,54 @@
+// Interface between the C-ABI front end (api.cpp) and the launcher of the causal
+// convolution's gradients, and the plan of a call. Host-only types; nothing here
+// crosses the public ABI.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+namespace ssm {
+
+struct ConvBwdArgs {
+  const void* x;
+  const float* weight;
+  const float* bias;         // or null
+  const float* state_in;     // or null
+  const float* dy;
+  const float* dstate_out;   // or null
+  float* dx;
+  float* dweight;            // or null
+  float* dbias;              // or null
+  float* dstate_in;          // or null
+  void* workspace;
+  int64_t batch, seqlen, dim, width;
+  int in_bf16, silu;
+};
+
+// Weak: the validation front end also links without these kernels (a host-only
+// build); a call that passes validation there reports a launch failure.
+__attribute__((weak)) int launch_conv1d_bwd(const ConvBwdArgs& a, void* stream);
+
+// A batch row's steps are walked in `segs` segments of `seg` steps at the same
+// time; each leaves its part of the filters' gradients, [parts][width + 1][dim].
+struct ConvBwdPlan {
+  int64_t seg, segs;
+  size_t bytes;
+};
+
+constexpr int64_t kConvBwdMinSeg = 32, kConvBwdMaxSeg = 512, kConvBwdBlocks = 2048;
+
+inline ConvBwdPlan plan_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width) {
+  ConvBwdPlan p{};
+  const auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  const int64_t groups = batch * ceil_div(dim, dim % 4 == 0 ? 1024 : 256);
+  const int64_t wanted = ceil_div(kConvBwdBlocks, groups > 0 ? groups : 1);
+  int64_t seg = ceil_div(ceil_div(seqlen, wanted), 16) * 16;
+  seg = seg < kConvBwdMinSeg ? kConvBwdMinSeg : (seg > kConvBwdMaxSeg ? kConvBwdMaxSeg : seg);
+  while (ceil_div(seqlen, seg) > 65535) seg *= 2;
+  p.seg = seg;
+  p.segs = seqlen > 0 ? ceil_div(seqlen, seg) : 1;
+  p.bytes = static_cast<size_t>(batch * p.segs) * static_cast<size_t>((width + 1) * dim) * 4;
+  return p;
+}
+
+}  // namespace ssm

@@ -1,0 +1,279 @@
+// Gradients of the causal depthwise conv1d + SiLU (conv1d.hip), for gfx950.
+//
+// Per batch row b, channel d, step l, filter width K, with the inputs before
+// step 0 from the carried state (or zero):
+//   out[l] = bias + sum_k w[k] x[l - (K-1) + k];  y = silu(out)
+//   g[l]   = dy[l] silu'(out[l])                   (out is computed again)
+//   dx[l]  = sum_k w[k] g[l + K-1 - k]             (l < 0: the carried state's)
+//   dw[k]  = sum_{b,l} g[l] x[l - (K-1) + k];  dbias = sum_{b,l} g[l]
+//
+// Bounded by HBM: x and dy are read once, dx written once. As forward, a thread
+// has VC = 4 adjacent channels and walks a segment of steps with the last K
+// inputs and the last K values of g in registers (circular: after unrolling by
+// K nothing moves). dx[l] is complete K - 1 steps after l, so a segment walks
+// K - 1 steps past its end; those steps' g is the next segment's too, but only
+// the step's own segment counts it in dw. The width is a compile-time one: taps
+// of zero in front of a narrower filter would make 0 * infinity of what they meet.
+#include <hip/hip_runtime.h>
+
+#include "conv1d_bwd.h"
+#include "device_math.h"
+
+namespace ssm {
+
+namespace {
+
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kBlock = 256;
+
+template <int VC, bool BF16>
+__device__ __forceinline__ void load_in(const void* base, int64_t i, float (&v)[VC]) {
+  if constexpr (VC == 4 && BF16) {
+    const u32x2 r = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(base) + i);
+    v[0] = __uint_as_float(r.x << 16);
+    v[1] = __uint_as_float(r.x & 0xffff0000u);
+    v[2] = __uint_as_float(r.y << 16);
+    v[3] = __uint_as_float(r.y & 0xffff0000u);
+  } else if constexpr (VC == 4) {
+    const f32x4 r = *reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + i);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = r[c];
+  } else {
+    v[0] = load_elem<BF16>(base, i);
+  }
+}
+
+template <int VC>
+__device__ __forceinline__ void store_out(float* p, const float (&v)[VC]) {
+  if constexpr (VC == 4) {
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
+  } else {
+    p[0] = v[0];
+  }
+}
+
+// silu'(z) = s (1 + z (1 - s)), s = 1 / (1 + e^-z); 1 - s = e^-z s. (e^-z is
+// infinite below z = -88: s and the derivative are 0 there, as s z is.)
+__device__ __forceinline__ float silu_slope(float z) {
+  const float e = exp2_hw(-z * kLog2e), s = rcp_hw(1.0f + e);
+  return z < -80.0f ? 0.0f : s * fmaf(z, e * s, 1.0f);
+}
+
+template <int K, int VC, bool BF16, bool SILU>
+__global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(const ConvBwdArgs a, int seg) {
+  constexpr int kGroup = K * (K < 8 ? 8 / K : 1);  // steps whose loads are issued together
+  const int64_t L = a.seqlen, Dm = a.dim;
+  const int64_t c0 = (static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x) * VC;
+  if (c0 >= Dm) return;
+  const int64_t b = blockIdx.z;
+  const int64_t row0 = b * L;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * seg;
+  const int64_t t1 = t0 + seg < L ? t0 + seg : L;
+
+  float w[K][VC], bv[VC], dw[K][VC], db[VC];
+#pragma unroll
+  for (int c = 0; c < VC; ++c) {
+    bv[c] = a.bias ? a.bias[c0 + c] : 0.0f;
+    db[c] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k][c] = a.weight[(c0 + c) * K + k], dw[k][c] = 0.0f;
+  }
+
+  // Slot s of the windows holds the step that is s modulo K past t0.
+  float x[K][VC], g[K][VC];
+#pragma unroll
+  for (int j = 1; j < K; ++j) {
+    const int64_t t = t0 - K + j;
+    if (t >= 0) {
+      load_in<VC, BF16>(a.x, (row0 + t) * Dm + c0, x[j]);
+    } else {  // t0 = 0: the carried state's slot K - 1 + t
+#pragma unroll
+      for (int c = 0; c < VC; ++c) {
+        x[j][c] = a.state_in && K - 1 + t >= 0 ? a.state_in[(b * Dm + c0 + c) * (K - 1) + (K - 1 + t)] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < VC; ++c) g[j][c] = 0.0f;
+  }
+  // One step: x[u] holds its input, d its dy; l = t - (K - 1) is complete.
+  const auto step = [&](int64_t t, int u, const float (&d)[VC], bool live, bool own, bool emit)
+                        __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < VC; ++c) {
+      float out = bv[c];
+#pragma unroll
+      for (int k = 0; k < K; ++k) out = fmaf(w[k][c], x[(u + 1 + k) % K][c], out);
+      g[u][c] = live ? (SILU ? d[c] * silu_slope(out) : d[c]) : 0.0f;
+    }
+    if (own) {
+#pragma unroll
+      for (int c = 0; c < VC; ++c) {
+        db[c] += g[u][c];
+#pragma unroll
+        for (int k = 0; k < K; ++k) dw[k][c] = fmaf(g[u][c], x[(u + 1 + k) % K][c], dw[k][c]);
+      }
+    }
+    if (emit) {
+      const int64_t l = t - (K - 1);
+      float o[VC];
+#pragma unroll
+      for (int c = 0; c < VC; ++c) {
+        o[c] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) o[c] = fmaf(w[k][c], g[(u + K - k) % K][c], o[c]);  // g[t - k]
+      }
+      const int64_t j = l - (L - (K - 1));  // the carried-out state's slot of input l
+      if (j >= 0 && a.dstate_out) {
+#pragma unroll
+        for (int c = 0; c < VC; ++c) o[c] += a.dstate_out[(b * Dm + c0 + c) * (K - 1) + j];
+      }
+      if (l >= 0) {
+        store_out<VC>(a.dx + (row0 + l) * Dm + c0, o);
+      } else if (a.dstate_in) {
+#pragma unroll
+        for (int c = 0; c < VC; ++c) a.dstate_in[(b * Dm + c0 + c) * (K - 1) + (K - 1) + l] = o[c];
+      }
+    }
+  };
+  // A step that may lie past the end, where there is no output: g is 0.
+  const auto edge = [&](int64_t t, int u, bool own, bool emit) __attribute__((always_inline)) {
+    float d[VC];
+#pragma unroll
+    for (int c = 0; c < VC; ++c) x[u][c] = d[c] = 0.0f;
+    if (t < L) {
+      load_in<VC, BF16>(a.x, (row0 + t) * Dm + c0, x[u]);
+      load_in<VC, false>(a.dy, (row0 + t) * Dm + c0, d);
+    }
+    step(t, u, d, t < L, own, emit);
+  };
+
+  // The first K - 1 steps complete nothing of the segment's own: at the
+  // sequence's start the carried state's inputs.
+#pragma unroll
+  for (int u = 0; u < K - 1; ++u) edge(t0 + u, u, t0 + u < t1, t0 == 0);
+  if (t0 < t1) {
+    edge(t0 + K - 1, K - 1, t0 + K - 1 < t1, true);
+    int64_t t = t0 + K;
+    for (; t + kGroup <= t1; t += kGroup) {
+      float in[kGroup][VC], d[kGroup][VC];
+#pragma unroll
+      for (int u = 0; u < kGroup; ++u) load_in<VC, BF16>(a.x, (row0 + t + u) * Dm + c0, in[u]);
+#pragma unroll
+      for (int u = 0; u < kGroup; ++u) load_in<VC, false>(a.dy, (row0 + t + u) * Dm + c0, d[u]);
+#pragma unroll
+      for (int u = 0; u < kGroup; ++u) {
+#pragma unroll
+        for (int c = 0; c < VC; ++c) x[u % K][c] = in[u][c];
+        step(t + u, u % K, d[u], true, true, true);
+      }
+    }
+    // What is left of the segment, and the K - 1 steps behind it that complete its last dx.
+    for (; t < t1 + K - 1; t += K) {
+#pragma unroll
+      for (int u = 0; u < K; ++u) {
+        if (t + u < t1 + K - 1) edge(t + u, u, t + u < t1, true);
+      }
+    }
+  }
+
+  if (a.dweight == nullptr && a.dbias == nullptr) return;
+  // parts [batch row, segment][k, then bias][channel]
+  float* part = static_cast<float*>(a.workspace) + (b * gridDim.y + blockIdx.y) * (K + 1) * Dm + c0;
+#pragma unroll
+  for (int c = 0; c < VC; ++c) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) part[k * Dm + c] = dw[k][c];
+    part[K * Dm + c] = db[c];
+  }
+}
+
+// dweight[d, k], dbias[d] = sums over the parts: 64 of the (K + 1) d columns a
+// block, sixteen waves each adding every sixteenth part, eight loads at a time,
+// then the sixteen sums in order.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void conv1d_bwd_sums_kernel(const float* __restrict__ parts,
+                                                                         int64_t nparts, int64_t dim, int width,
+                                                                         float* __restrict__ dweight,
+                                                                         float* __restrict__ dbias) {
+  __shared__ float sums[kSumWaves][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane, cols = (width + 1) * dim;
+  float acc = 0.0f;
+  if (c < cols) {
+    int64_t i = w;
+    for (; i + 7 * kSumWaves < nparts; i += 8 * kSumWaves) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = parts[(i + k * kSumWaves) * cols + c];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc += v[k];
+    }
+    for (; i < nparts; i += kSumWaves) acc += parts[i * cols + c];
+  }
+  sums[w][lane] = acc;
+  __syncthreads();
+  if (w == 0 && c < cols) {
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kSumWaves; ++k) v += sums[k][lane];
+    const int64_t k = c / dim, d = c - k * dim;
+    if (k < width) {
+      if (dweight != nullptr) dweight[d * width + k] = v;
+    } else if (dbias != nullptr) {
+      dbias[d] = v;
+    }
+  }
+}
+
+template <int K, bool BF16>
+void launch_width(const ConvBwdArgs& a, const ConvBwdPlan& p, hipStream_t st) {
+  // Four channels per thread when rows stay aligned for 8/16-byte accesses.
+  const int vc = a.dim % 4 == 0 ? 4 : 1;
+  const int64_t groups = (a.dim + vc - 1) / vc;
+  const dim3 grid(static_cast<unsigned>((groups + kBlock - 1) / kBlock), static_cast<unsigned>(p.segs),
+                  static_cast<unsigned>(a.batch));
+  const int seg = static_cast<int>(p.seg);
+  if (vc == 4) {
+    a.silu ? conv1d_bwd_kernel<K, 4, BF16, true><<<grid, kBlock, 0, st>>>(a, seg)
+           : conv1d_bwd_kernel<K, 4, BF16, false><<<grid, kBlock, 0, st>>>(a, seg);
+  } else {
+    a.silu ? conv1d_bwd_kernel<K, 1, BF16, true><<<grid, kBlock, 0, st>>>(a, seg)
+           : conv1d_bwd_kernel<K, 1, BF16, false><<<grid, kBlock, 0, st>>>(a, seg);
+  }
+}
+
+template <bool BF16>
+void launch_type(const ConvBwdArgs& a, const ConvBwdPlan& p, hipStream_t st) {
+  switch (a.width) {
+    case 1: return launch_width<1, BF16>(a, p, st);
+    case 2: return launch_width<2, BF16>(a, p, st);
+    case 3: return launch_width<3, BF16>(a, p, st);
+    case 4: return launch_width<4, BF16>(a, p, st);
+    case 5: return launch_width<5, BF16>(a, p, st);
+    case 6: return launch_width<6, BF16>(a, p, st);
+    case 7: return launch_width<7, BF16>(a, p, st);
+    default: return launch_width<8, BF16>(a, p, st);
+  }
+}
+
+}  // namespace
+
+int launch_conv1d_bwd(const ConvBwdArgs& a, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const ConvBwdPlan p = plan_conv1d_bwd(a.batch, a.seqlen, a.dim, a.width);
+  if (a.batch > 0) {
+    a.in_bf16 ? launch_type<true>(a, p, st) : launch_type<false>(a, p, st);
+    if (const hipError_t e = hipGetLastError()) return static_cast<int>(e);
+  }
+  if (a.dweight != nullptr || a.dbias != nullptr) {
+    const int64_t cols = (a.width + 1) * a.dim;
+    conv1d_bwd_sums_kernel<<<static_cast<unsigned>((cols + 63) / 64), 64 * kSumWaves, 0, st>>>(
+        static_cast<const float*>(a.workspace), a.batch * p.segs, a.dim, static_cast<int>(a.width), a.dweight,
+        a.dbias);
+  }
+  return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace ssm

@@ -1,4 +1,5 @@
-"""Argument validation of the layer norm's and the dropout's entry points.
+"""Argument validation of the entry points of the layer norm, the dropout and the
+causal convolution's gradients.
 
 CPU only. Every call here fails validation (or has nothing to do) before the
 library touches the device; the fake pointers are never dereferenced.
@@ -42,6 +43,12 @@ def norm_bwd(lib, rows=4, dim=32, sd=0, eps=1e-5, p=0.1, call=0, rng=P, s=2 * P,
              ds=6 * P, dx=7 * P, dw=8 * P, db=9 * P, ws=10 * P, wsb=1 << 20):
     return lib.ssm_layer_norm_bwd(rows, dim, sd, eps, p, call, vp(rng), vp(s), vp(w), vp(dy), vp(dr), vp(ds), vp(dx),
                                   vp(dw), vp(db), vp(ws), wsb, None)
+
+
+def conv_bwd(lib, B=2, L=8, d=8, K=4, ind=0, silu=1, x=P, w=2 * P, b=3 * P, st=4 * P, dy=5 * P, dst=6 * P, dx=7 * P,
+             dw=8 * P, db=9 * P, dsi=10 * P, ws=11 * P, wsb=1 << 20):
+    return lib.ssm_causal_conv1d_bwd(B, L, d, K, ind, silu, vp(x), vp(w), vp(b), vp(st), vp(dy), vp(dst), vp(dx),
+                                     vp(dw), vp(db), vp(dsi), vp(ws), wsb, None)
 
 
 def test_dropout(lib):
@@ -111,3 +118,28 @@ def test_layer_norm_bwd(lib):
     assert norm_bwd(lib, dw=9 * P) == E_ALIAS and norm_bwd(lib, dw=10 * P) == E_ALIAS
     assert norm_bwd(lib, rows=0, dw=None, db=None) == OK
     assert lib.ssm_layer_norm_bwd_workspace_bytes(0, 32) == lib.ssm_layer_norm_bwd_workspace_bytes(4, 16385) == 0
+
+
+def test_conv_bwd(lib):
+    assert conv_bwd(lib, B=-1) == conv_bwd(lib, L=-1) == conv_bwd(lib, d=-1) == conv_bwd(lib, K=0) == E_SHAPE
+    assert conv_bwd(lib, B=60000, L=1 << 20, d=1 << 30) == E_SHAPE
+    assert conv_bwd(lib, K=9) == conv_bwd(lib, B=65536) == conv_bwd(lib, L=4194241) == E_UNSUPPORTED
+    assert conv_bwd(lib, ind=2) == E_DTYPE
+    for name in ("x", "w", "dy", "dx"):
+        assert conv_bwd(lib, **{name: None}) == E_NULLPTR, name
+    for name, at in dict(x=1, dy=5, dx=7).items():
+        assert conv_bwd(lib, **{name: at * P + 8}) == E_ALIGN, name
+    for name, at in dict(w=2, b=3, st=4, dst=6, dw=8, db=9, dsi=10).items():
+        assert conv_bwd(lib, **{name: at * P + 2}) == E_ALIGN, name
+    need = lib.ssm_causal_conv1d_bwd_workspace_bytes(2, 8, 8, 4)
+    assert need >= 2 * 5 * 8 * 4
+    assert conv_bwd(lib, ws=None) == E_WORKSPACE and conv_bwd(lib, wsb=need - 1) == E_WORKSPACE
+    assert conv_bwd(lib, ws=11 * P + 8) == E_ALIGN
+    outs = dict(dx=7, dw=8, db=9, dsi=10, ws=11)
+    for name, own in outs.items():
+        for at in range(1, 12):
+            if at != own:
+                assert conv_bwd(lib, **{name: at * P}) == E_ALIAS, (name, at)
+    assert conv_bwd(lib, d=0, x=None) == OK and conv_bwd(lib, B=0, dw=None, db=None, x=None) == OK
+    for bad in ((0, 8, 8, 4), (2, -1, 8, 4), (2, 8, 0, 4), (2, 8, 8, 9), (65536, 8, 8, 4), (2, 8, 1 << 55, 4)):
+        assert lib.ssm_causal_conv1d_bwd_workspace_bytes(*bad) == 0
