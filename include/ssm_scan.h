@@ -64,8 +64,9 @@ extern "C" {
  * the backward from them were added.
  * 3: the gated delta rule (forward, backward, single-token update) and the RMS
  * norm (forward, backward) were added.
- * 4: the layer norm and the dropout (forward, backward) and the gradients of the
- * causal convolution were added. */
+ * 4: the gated linear recurrence (forward, backward, single-token update), the
+ * layer norm and the dropout (forward, backward) and the gradients of the causal
+ * convolution were added. */
 #define SSM_ABI_VERSION 4
 
 /* Status codes. */
@@ -85,6 +86,10 @@ extern "C" {
 #define SSM_FLAG_ZOH 2          /* input coefficient k = (exp(dt A) - 1) / A, else k = dt   */
 #define SSM_FLAG_BETA_SIGMOID 4 /* write strength sigmoid(beta), else beta (gated delta rule) */
 #define SSM_FLAG_QK_L2NORM 8    /* q and k divided by sqrt(|.|^2 + 1e-6) (gated delta rule) */
+/* (gated linear recurrence; at most one of SSM_FLAG_SOFTPLUS and the first, one of the others) */
+#define SSM_FLAG_GATE_SIGMOID 16     /* the gate is sigmoid(gate + gate_bias)     */
+#define SSM_FLAG_INPUT_NORM 32       /* the input is weighted by sqrt(1 - a^2)    */
+#define SSM_FLAG_INPUT_COMPLEMENT 64 /* the input is weighted by 1 - a            */
 
 /* Version of this ABI (SSM_ABI_VERSION of the header the library was built from). */
 int ssm_abi_version(void);
@@ -743,6 +748,120 @@ int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
                           const float* dy, const float* dstate_out,
                           float* dx, float* dweight, float* dbias, float* dstate_in,
                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gated linear recurrence: a layer with one state a channel, whose decay and
+ * input are gated element by element. It stands next to the selective scan (the
+ * same recurrence h = a h + b, where the scan has N states a channel and inputs B
+ * shared by the channels; "从 Transformer 到 Mamba", ybb.press, section 2). Per
+ * batch row b, channel d, step t:
+ *
+ *   u = gate[b,t,d] + gate_bias[d]
+ *   g = u, softplus(u) (SSM_FLAG_SOFTPLUS) or sigmoid(u) (SSM_FLAG_GATE_SIGMOID)
+ *   a = exp(A[d] * g)
+ *   w = 1, sqrt(1 - a^2) (SSM_FLAG_INPUT_NORM) or 1 - a (SSM_FLAG_INPUT_COMPLEMENT)
+ *   v = x[b,t,d] * sigmoid(input_gate[b,t,d] + input_bias[d])   (x without one)
+ *   h = a h + w v;  y[b,t,d] = h
+ *
+ * With the softplus, A = -1 and the complement, the decay is sigmoid(-u) and the
+ * weight sigmoid(u).
+ *
+ *   batch, seqlen, dim         : B >= 0, 0 <= L < 2^30, 0 <= D < 2^23, B D <
+ *                                2^30, B ceil(D / 64) ceil(L / 64) <= 2^30
+ *                                (else SSM_E_UNSUPPORTED).
+ *   in_dtype, out_dtype        : of x and the gates; of y. 0 float32, 1 bfloat16.
+ *   flags                      : at most one of the gate's and one of the
+ *                                weight's (else SSM_E_UNSUPPORTED).
+ *   x_step, gate_step, input_gate_step : elements between consecutive steps of
+ *                                each (at least D, else SSM_E_SHAPE; below 2^23,
+ *                                else SSM_E_UNSUPPORTED); batch rows are L times
+ *                                as far apart. The three may thus be column
+ *                                ranges of one projection's output.
+ *   x, gate   [B, L, D]  in_dtype
+ *   input_gate [B, L, D] in_dtype  (optional)
+ *   A         [D]        float32   expected A g <= 0 (a decay above 1 grows, and
+ *                                  sqrt(1 - a^2) is NaN then)
+ *   gate_bias, input_bias [D] float32 (optional, 0; the latter is used with an
+ *                                  input gate only)
+ *   h0        [B, D]     float32   initial state (optional, 0)
+ *   seqlens   [B]        int32     steps that each batch row has (optional, L for
+ *                                  all; taken as 0 below 0 and as L above L).
+ *                                  Steps behind a row's last are not read; their
+ *                                  y is 0.
+ *   y         [B, L, D]  out_dtype must not overlap any input
+ *   h_final   [B, D]     float32   state behind each row's last step (optional);
+ *                                  may equal h0
+ *   states                         ssm_gated_linear_states_bytes() bytes on a
+ *                                  16-byte boundary (optional): what the
+ *                                  backward would else compute again. Their
+ *                                  layout is the library's own.
+ *   workspace, workspace_bytes     at least ssm_gated_linear_workspace_bytes(),
+ *                                  on a 16-byte boundary (NULL when 0)
+ *
+ * Element alignment suffices; rows on 16-byte boundaries are read fastest. All is
+ * float32 between the inputs and y, which is rounded once. The decay's
+ * rounding, 2^-24 of it, is one of the recurrence's: where a channel's a stays near
+ * 1, h can be off by some 2^-24 / (1 - a) of itself at worst. Results are
+ * bitwise deterministic. A value that is not finite stays in its channel of its
+ * batch row, and does not reach an earlier step.
+ */
+size_t ssm_gated_linear_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
+size_t ssm_gated_linear_states_bytes(int64_t batch, int64_t seqlen, int64_t dim);
+int ssm_gated_linear_fwd(int64_t batch, int64_t seqlen, int64_t dim, int in_dtype, int out_dtype, int flags,
+                         int64_t x_step, int64_t gate_step, int64_t input_gate_step,
+                         const void* x, const void* gate, const float* A, const void* input_gate,
+                         const float* gate_bias, const float* input_bias, const float* h0, const int32_t* seqlens,
+                         void* y, float* h_final, float* states, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
+ * Gated linear recurrence, one token: the step above with L = 1 and h0 = h_final
+ * = state, in place. x, gate, input_gate, y [B, D]; the steps are the elements
+ * between batch rows.
+ *   state     [B, D]     float32   read, then overwritten
+ *   y         [B, D]     out_dtype must not overlap state or inputs
+ */
+int ssm_gated_linear_update(int64_t batch, int64_t dim, int in_dtype, int out_dtype, int flags,
+                            int64_t x_step, int64_t gate_step, int64_t input_gate_step,
+                            float* state, const void* x, const void* gate, const float* A, const void* input_gate,
+                            const float* gate_bias, const float* input_bias, void* y, void* stream);
+
+/*
+ * Gradients of a loss through ssm_gated_linear_fwd with the same inputs, given dy
+ * = dL/dy and optionally dh_final. In reverse over the steps, with the gradient
+ * D of h:
+ *
+ *   D = D + dy;  dv = w D;  dx = sigmoid(..) dv;  dinput_gate = x dv sigmoid'(..)
+ *   d(A g) = a h_{t-1} D + (dw / d(A g)) v D,  dw / d(A g) = 0, -a^2 / w, -a
+ *   dA = sum d(A g) g;  dgate = d(A g) A g'(u);  D = a D
+ *
+ * Where a is 1 (A g = 0), sqrt(1 - a^2) has no derivative: its term is taken as 0.
+ * Steps behind a row's length have gradient 0.
+ *
+ *   inputs, sizes, flags, steps as for the forward.
+ *   states                         the forward's (optional: computed again when
+ *                                  NULL)
+ *   dy        [B, L, D]  float32
+ *   dh_final  [B, D]     float32   (optional, 0)
+ *   dx, dgate [B, L, D]  float32   outputs, dense
+ *   dinput_gate [B, L, D] float32  output, with an input gate; else NULL
+ *   dA        [D]        float32   output
+ *   dgate_bias, dinput_bias [D] float32 outputs (optional)
+ *   dh0       [B, D]     float32   output (optional)
+ *   workspace, workspace_bytes     at least ssm_gated_linear_bwd_workspace_bytes()
+ *                                  (with_states: 1 when states is given), on a
+ *                                  16-byte boundary
+ * No output may overlap an input, another output or the workspace. Bitwise
+ * deterministic.
+ */
+size_t ssm_gated_linear_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int with_states);
+int ssm_gated_linear_bwd(int64_t batch, int64_t seqlen, int64_t dim, int in_dtype, int flags,
+                         int64_t x_step, int64_t gate_step, int64_t input_gate_step,
+                         const void* x, const void* gate, const float* A, const void* input_gate,
+                         const float* gate_bias, const float* input_bias, const float* h0, const int32_t* seqlens,
+                         const float* states, const float* dy, const float* dh_final,
+                         float* dx, float* dgate, float* dinput_gate, float* dA, float* dgate_bias,
+                         float* dinput_bias, float* dh0, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -34,3 +34,4 @@ from .gated_delta_oracle import gated_delta, gated_delta_bwd  # noqa: F401
 from .rms_norm_oracle import e4m3_nearest, rms_norm, rms_norm_bwd  # noqa: F401
 from .dropout_oracle import dropout, dropout_bits, dropout_threshold, philox4x32  # noqa: F401
 from .layer_norm_oracle import layer_norm, layer_norm_bwd  # noqa: F401
+from .gated_linear_oracle import gated_linear, gated_linear_bwd  # noqa: F401

@@ -19,6 +19,12 @@ from .binding import (  # noqa: F401
     ssm_gated_delta_fwd,
     ssm_gated_delta_update,
     ssm_gated_delta_workspace_bytes,
+    ssm_gated_linear_bwd,
+    ssm_gated_linear_bwd_workspace_bytes,
+    ssm_gated_linear_fwd,
+    ssm_gated_linear_states_bytes,
+    ssm_gated_linear_update,
+    ssm_gated_linear_workspace_bytes,
     ssm_layer_norm_bwd,
     ssm_layer_norm_bwd_workspace_bytes,
     ssm_layer_norm_fwd,

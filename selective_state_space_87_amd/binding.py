@@ -119,6 +119,18 @@ def _load():
         lib.ssm_causal_conv1d_bwd_workspace_bytes.argtypes = [i64] * 4
         lib.ssm_causal_conv1d_bwd.restype = i32
         lib.ssm_causal_conv1d_bwd.argtypes = [i64] * 4 + [i32] * 2 + [vp] * 11 + [sz, vp]
+        lib.ssm_gated_linear_workspace_bytes.restype = sz
+        lib.ssm_gated_linear_workspace_bytes.argtypes = [i64] * 3
+        lib.ssm_gated_linear_states_bytes.restype = sz
+        lib.ssm_gated_linear_states_bytes.argtypes = [i64] * 3
+        lib.ssm_gated_linear_fwd.restype = i32
+        lib.ssm_gated_linear_fwd.argtypes = [i64] * 3 + [i32] * 3 + [i64] * 3 + [vp] * 12 + [sz, vp]
+        lib.ssm_gated_linear_update.restype = i32
+        lib.ssm_gated_linear_update.argtypes = [i64] * 2 + [i32] * 3 + [i64] * 3 + [vp] * 9
+        lib.ssm_gated_linear_bwd_workspace_bytes.restype = sz
+        lib.ssm_gated_linear_bwd_workspace_bytes.argtypes = [i64] * 3 + [i32]
+        lib.ssm_gated_linear_bwd.restype = i32
+        lib.ssm_gated_linear_bwd.argtypes = [i64] * 3 + [i32] * 2 + [i64] * 3 + [vp] * 19 + [sz, vp]
         _lib = lib
         return lib
 
@@ -1054,3 +1066,178 @@ def ssm_causal_conv1d_bwd(x, weight, dy, bias=None, state_in=None, dstate_out=No
                                        _ptr(out["dstate_in"]), _ptr(workspace), ws_size, _stream_handle(stream, dev))
     _check("ssm_causal_conv1d_bwd", st)
     return out
+
+
+FLAG_GATE_SIGMOID = 16      # SSM_FLAG_GATE_SIGMOID
+FLAG_INPUT_NORM = 32        # SSM_FLAG_INPUT_NORM
+FLAG_INPUT_COMPLEMENT = 64  # SSM_FLAG_INPUT_COMPLEMENT
+
+
+def _glr_inputs(x, gate, A, input_gate, gate_bias, input_bias, lead):
+    """Checked lead sizes, dim, device and steps of the gated linear recurrence's inputs."""
+    if not isinstance(x, torch.Tensor) or x.dim() != lead + 1 or x.dtype not in _DTYPE_CODE:
+        raise ValueError(f"x must be a {lead + 1}-d float32 or bfloat16 tensor")
+    dev, shape, D = x.device, x.shape, x.shape[lead]
+    for name, t in (("x", x), ("gate", gate), ("input_gate", input_gate)):
+        if t is not None or name != "input_gate":
+            _strided_tensor(name, t, shape, x.dtype, dev)
+    if A is None:
+        raise ValueError("A is required")
+    f32 = (torch.float32,)
+    _dev_tensor("A", A, (D,), f32, dev)
+    _dev_tensor("gate_bias", gate_bias, (D,), f32, dev)
+    _dev_tensor("input_bias", input_bias, (D,), f32, dev)
+    if input_bias is not None and input_gate is None:
+        raise ValueError("input_bias needs an input_gate")
+    steps = [D if t is None or t.is_contiguous() else _step_of(name, t.unsqueeze(-2), lead, D)
+             for name, t in (("x", x), ("gate", gate), ("input_gate", input_gate))]
+    return tuple(shape[:lead]), D, dev, steps
+
+
+def _glr_flags(gate_sigmoid, gate_softplus, input_norm, input_complement):
+    if (gate_sigmoid and gate_softplus) or (input_norm and input_complement):
+        raise ValueError("at most one of gate_sigmoid and gate_softplus, and of input_norm and input_complement")
+    return ((FLAG_GATE_SIGMOID if gate_sigmoid else 0) | (FLAG_SOFTPLUS if gate_softplus else 0)
+            | (FLAG_INPUT_NORM if input_norm else 0) | (FLAG_INPUT_COMPLEMENT if input_complement else 0))
+
+
+def ssm_gated_linear_workspace_bytes(batch, seqlen, dim) -> int:
+    return int(_load().ssm_gated_linear_workspace_bytes(batch, seqlen, dim))
+
+
+def ssm_gated_linear_states_bytes(batch, seqlen, dim) -> int:
+    return int(_load().ssm_gated_linear_states_bytes(batch, seqlen, dim))
+
+
+def _glr_states(states, need, dev):
+    if not isinstance(states, torch.Tensor) or states.device != dev or states.dtype != torch.float32:
+        raise ValueError("states must be a float32 tensor on the inputs' device, or True in the forward")
+    if not states.is_contiguous() or states.numel() * 4 < need:
+        raise ValueError(f"states must be contiguous and hold {need} bytes")
+
+
+def ssm_gated_linear_fwd(x, gate, A, input_gate=None, gate_bias=None, input_bias=None, gate_sigmoid=False,
+                         gate_softplus=False, input_norm=False, input_complement=False, h0=None, seqlens=None,
+                         out_dtype=None, return_final_state=False, y=None, h_final=None, states=None,
+                         workspace=None, stream=None):
+    """Gated linear recurrence forward; see ssm_gated_linear_fwd in include/ssm_scan.h.
+
+    x, gate, input_gate: [B, L, D] (all float32 or all bfloat16; each may be a
+    column range of a wider dense array); A, gate_bias, input_bias: [D], h0:
+    [B, D] float32; seqlens: [B] int32. ``states``: a float32 tensor of
+    ssm_gated_linear_states_bytes() bytes, or True to allocate one, for
+    ssm_gated_linear_bwd. Returns y [B, L, D] or (y, h_final); with states, (y,
+    h_final, states).
+    """
+    lib = _load()
+    (Bt, L), D, dev, steps = _glr_inputs(x, gate, A, input_gate, gate_bias, input_bias, 2)
+    flags = _glr_flags(gate_sigmoid, gate_softplus, input_norm, input_complement)
+    _dev_tensor("h0", h0, (Bt, D), (torch.float32,), dev)
+    _dev_tensor("seqlens", seqlens, (Bt,), (torch.int32,), dev)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    if out_dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported output dtype {out_dtype}")
+    with _launch_context(dev, stream):
+        if y is None:
+            y = torch.empty((Bt, L, D), dtype=out_dtype, device=dev)
+        _dev_tensor("y", y, (Bt, L, D), (out_dtype,), dev)
+        if return_final_state and h_final is None:
+            h_final = torch.empty((Bt, D), dtype=torch.float32, device=dev)
+        _dev_tensor("h_final", h_final, (Bt, D), (torch.float32,), dev)
+        if states is not None:
+            need = int(lib.ssm_gated_linear_states_bytes(Bt, L, D))
+            if states is True:
+                states = torch.empty(max(need // 4, 1), dtype=torch.float32, device=dev)
+            _glr_states(states, need, dev)
+        ws_bytes = int(lib.ssm_gated_linear_workspace_bytes(Bt, L, D))
+        if workspace is None and ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        ws_size = _check_workspace(workspace, dev)
+        st = lib.ssm_gated_linear_fwd(Bt, L, D, _DTYPE_CODE[x.dtype], _DTYPE_CODE[out_dtype], flags, *steps, _ptr(x),
+                                      _ptr(gate), _ptr(A), _ptr(input_gate), _ptr(gate_bias), _ptr(input_bias),
+                                      _ptr(h0), _ptr(seqlens), _ptr(y), _ptr(h_final), _ptr(states),
+                                      _ptr(workspace), ws_size, _stream_handle(stream, dev))
+    _check("ssm_gated_linear_fwd", st)
+    if states is not None:
+        return y, h_final, states
+    if return_final_state or h_final is not None:
+        return y, h_final
+    return y
+
+
+def ssm_gated_linear_update(state, x, gate, A, input_gate=None, gate_bias=None, input_bias=None, gate_sigmoid=False,
+                            gate_softplus=False, input_norm=False, input_complement=False, out_dtype=None, y=None,
+                            stream=None):
+    """One token of the gated linear recurrence, in place on ``state``; see
+    ssm_gated_linear_update in include/ssm_scan.h.
+
+    state: [B, D] float32 (updated in place); x, gate, input_gate: [B, D].
+    Returns y [B, D].
+    """
+    lib = _load()
+    (Bt,), D, dev, steps = _glr_inputs(x, gate, A, input_gate, gate_bias, input_bias, 1)
+    flags = _glr_flags(gate_sigmoid, gate_softplus, input_norm, input_complement)
+    if state is None:
+        raise ValueError("state is required")
+    _dev_tensor("state", state, (Bt, D), (torch.float32,), dev)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    if out_dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported output dtype {out_dtype}")
+    with _launch_context(dev, stream):
+        if y is None:
+            y = torch.empty((Bt, D), dtype=out_dtype, device=dev)
+        _dev_tensor("y", y, (Bt, D), (out_dtype,), dev)
+        st = lib.ssm_gated_linear_update(Bt, D, _DTYPE_CODE[x.dtype], _DTYPE_CODE[out_dtype], flags, *steps,
+                                         _ptr(state), _ptr(x), _ptr(gate), _ptr(A), _ptr(input_gate),
+                                         _ptr(gate_bias), _ptr(input_bias), _ptr(y), _stream_handle(stream, dev))
+    _check("ssm_gated_linear_update", st)
+    return y
+
+
+def ssm_gated_linear_bwd_workspace_bytes(batch, seqlen, dim, with_states=False) -> int:
+    return int(_load().ssm_gated_linear_bwd_workspace_bytes(batch, seqlen, dim, 1 if with_states else 0))
+
+
+def ssm_gated_linear_bwd(x, gate, A, dy, input_gate=None, gate_bias=None, input_bias=None, gate_sigmoid=False,
+                         gate_softplus=False, input_norm=False, input_complement=False, h0=None, dh_final=None,
+                         seqlens=None, states=None, workspace=None, stream=None):
+    """Gradients of the gated linear recurrence; see ssm_gated_linear_bwd in include/ssm_scan.h.
+
+    Inputs as ssm_gated_linear_fwd, plus dy [B, L, D] and dh_final [B, D]
+    (float32), and ``states`` as that call left them (computed again without).
+    Returns a dict of float32 tensors: dx, dgate, dA, dh0, dinput_gate with an
+    input gate, dgate_bias and dinput_bias when the biases are given.
+    """
+    lib = _load()
+    (Bt, L), D, dev, steps = _glr_inputs(x, gate, A, input_gate, gate_bias, input_bias, 2)
+    flags = _glr_flags(gate_sigmoid, gate_softplus, input_norm, input_complement)
+    f32 = (torch.float32,)
+    _dev_tensor("h0", h0, (Bt, D), f32, dev)
+    _dev_tensor("seqlens", seqlens, (Bt,), (torch.int32,), dev)
+    if dy is None:
+        raise ValueError("dy is required")
+    _dev_tensor("dy", dy, (Bt, L, D), f32, dev)
+    _dev_tensor("dh_final", dh_final, (Bt, D), f32, dev)
+    if states is not None:
+        _glr_states(states, int(lib.ssm_gated_linear_states_bytes(Bt, L, D)), dev)
+    new = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)  # noqa: E731
+    with _launch_context(dev, stream):
+        g = dict(dx=new(Bt, L, D), dgate=new(Bt, L, D), dA=new(D), dh0=new(Bt, D))
+        if input_gate is not None:
+            g["dinput_gate"] = new(Bt, L, D)
+        if gate_bias is not None:
+            g["dgate_bias"] = new(D)
+        if input_bias is not None:
+            g["dinput_bias"] = new(D)
+        ws_bytes = int(lib.ssm_gated_linear_bwd_workspace_bytes(Bt, L, D, 0 if states is None else 1))
+        if workspace is None and ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        ws_size = _check_workspace(workspace, dev)
+        st = lib.ssm_gated_linear_bwd(Bt, L, D, _DTYPE_CODE[x.dtype], flags, *steps, _ptr(x), _ptr(gate), _ptr(A),
+                                      _ptr(input_gate), _ptr(gate_bias), _ptr(input_bias), _ptr(h0), _ptr(seqlens),
+                                      _ptr(states), _ptr(dy), _ptr(dh_final), _ptr(g["dx"]), _ptr(g["dgate"]),
+                                      _ptr(g.get("dinput_gate")), _ptr(g["dA"]), _ptr(g.get("dgate_bias")),
+                                      _ptr(g.get("dinput_bias")), _ptr(g["dh0"]), _ptr(workspace), ws_size,
+                                      _stream_handle(stream, dev))
+    _check("ssm_gated_linear_bwd", st)
+    return g

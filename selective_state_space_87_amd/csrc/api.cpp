@@ -6,6 +6,7 @@
 
 #include "conv1d_bwd.h"
 #include "gated_delta_args.h"
+#include "gated_linear_args.h"
 #include "kernels.h"
 #include "layer_norm.h"
 #include "rms_norm.h"
@@ -1191,6 +1192,272 @@ int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
   a.in_bf16 = in_dtype;
   a.silu = silu_activation ? 1 : 0;
   return ssm::launch_conv1d_bwd ? map_hip(ssm::launch_conv1d_bwd(a, stream)) : SSM_E_HIP;
+}
+
+}  // extern "C"
+
+namespace {
+
+struct GlrSizes {
+  int64_t batch, seqlen, dim;
+  int64_t bl, bld, bd;
+};
+
+constexpr int kGlrFlags =
+    SSM_FLAG_SOFTPLUS | SSM_FLAG_GATE_SIGMOID | SSM_FLAG_INPUT_NORM | SSM_FLAG_INPUT_COMPLEMENT;
+
+int glr_sizes(int64_t batch, int64_t seqlen, int64_t dim, GlrSizes* z) {
+  if (batch < 0 || seqlen < 0 || dim < 0) return SSM_E_SHAPE;
+  *z = GlrSizes{batch, seqlen, dim, 0, 0, 0};
+  if (!safe_mul(batch, seqlen, &z->bl) || !safe_mul(z->bl, dim, &z->bld) || !safe_mul(batch, dim, &z->bd)) {
+    return SSM_E_SHAPE;
+  }
+  if (seqlen >= (int64_t(1) << 30) || dim >= (int64_t(1) << 23) || z->bd >= (int64_t(1) << 30) ||
+      !ssm::gated_linear_fits(batch, seqlen, dim)) {
+    return SSM_E_UNSUPPORTED;
+  }
+  return SSM_OK;
+}
+
+// Types, options and steps; `rows` rows of x and the gates.
+int glr_options(const GlrSizes& z, int64_t rows, int in_dtype, int flags, int64_t x_step, int64_t gate_step,
+                int64_t igate_step, bool gated) {
+  if (in_dtype != 0 && in_dtype != 1) return SSM_E_DTYPE;
+  const int act = flags & (SSM_FLAG_SOFTPLUS | SSM_FLAG_GATE_SIGMOID);
+  const int scale = flags & (SSM_FLAG_INPUT_NORM | SSM_FLAG_INPUT_COMPLEMENT);
+  if ((flags & ~kGlrFlags) != 0 || act == (SSM_FLAG_SOFTPLUS | SSM_FLAG_GATE_SIGMOID) ||
+      scale == (SSM_FLAG_INPUT_NORM | SSM_FLAG_INPUT_COMPLEMENT)) {
+    return SSM_E_UNSUPPORTED;
+  }
+  if (!gated) igate_step = z.dim;
+  if (x_step < z.dim || gate_step < z.dim || igate_step < z.dim) return SSM_E_SHAPE;
+  // the rows of a tile of steps are addressed with 32-bit offsets
+  constexpr int64_t most = int64_t(1) << 23;
+  if (x_step >= most || gate_step >= most || igate_step >= most) return SSM_E_UNSUPPORTED;
+  int64_t t;
+  if (!safe_mul(rows, x_step, &t) || !safe_mul(rows, gate_step, &t) || !safe_mul(rows, igate_step, &t)) {
+    return SSM_E_SHAPE;
+  }
+  return SSM_OK;
+}
+
+// in[0..7]: x, gate, input gate, A, the biases, h0, seqlens.
+void glr_inputs(const GlrSizes& z, int64_t rows, const ssm::GatedLinearArgs& a, Range* in) {
+  const int64_t isz = a.in_bf16 ? 2 : 4;
+  in[0] = span(a.x, strided(rows, a.x_step, z.dim), isz);
+  in[1] = span(a.gate, strided(rows, a.gate_step, z.dim), isz);
+  in[2] = span(a.igate, strided(rows, a.igate_step, z.dim), isz);
+  in[3] = span(a.A, z.dim, 4);
+  in[4] = span(a.gbias, z.dim, 4);
+  in[5] = span(a.ibias, z.dim, 4);
+  in[6] = span(a.h0, z.bd, 4);
+  in[7] = span(a.seqlens, z.batch, 4);
+}
+
+ssm::GatedLinearArgs glr_args(const GlrSizes& z, int in_dtype, int flags, int64_t x_step, int64_t gate_step,
+                              int64_t igate_step, const void* x, const void* gate, const float* A,
+                              const void* input_gate, const float* gate_bias, const float* input_bias,
+                              const float* h0, const int32_t* seqlens) {
+  ssm::GatedLinearArgs a{};
+  a.x = x;
+  a.gate = gate;
+  a.igate = input_gate;
+  a.A = A;
+  a.gbias = gate_bias;
+  a.ibias = input_bias;
+  a.h0 = h0;
+  a.seqlens = seqlens;
+  a.batch = z.batch;
+  a.seqlen = z.seqlen;
+  a.dim = z.dim;
+  a.x_step = x_step;
+  a.gate_step = gate_step;
+  a.igate_step = input_gate ? igate_step : 0;
+  a.in_bf16 = in_dtype;
+  a.act = flags & SSM_FLAG_SOFTPLUS ? ssm::kGateSoftplus
+                                    : (flags & SSM_FLAG_GATE_SIGMOID ? ssm::kGateSigmoid : ssm::kGateRaw);
+  a.scale = flags & SSM_FLAG_INPUT_NORM
+                ? ssm::kInputNorm
+                : (flags & SSM_FLAG_INPUT_COMPLEMENT ? ssm::kInputComplement : ssm::kInputPlain);
+  return a;
+}
+
+// Pointers every entry needs: NULL and alignment.
+int glr_pointers(const ssm::GatedLinearArgs& a, bool any_step) {
+  if (a.A == nullptr || (any_step && (a.x == nullptr || a.gate == nullptr))) return SSM_E_NULLPTR;
+  const uintptr_t isz = a.in_bf16 ? 2 : 4;
+  const void* in_ptrs[] = {a.x, a.gate, a.igate};
+  for (const void* q : in_ptrs) {
+    if (!aligned(q, isz)) return SSM_E_ALIGN;
+  }
+  const void* f32_ptrs[] = {a.A, a.gbias, a.ibias, a.h0, a.seqlens, a.h_final};
+  for (const void* q : f32_ptrs) {
+    if (!aligned(q, 4)) return SSM_E_ALIGN;
+  }
+  return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssm_gated_linear_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
+  GlrSizes z;
+  return glr_sizes(batch, seqlen, dim, &z) == SSM_OK ? ssm::gated_linear_workspace_bytes(batch, seqlen, dim) : 0;
+}
+
+size_t ssm_gated_linear_states_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
+  GlrSizes z;
+  return glr_sizes(batch, seqlen, dim, &z) == SSM_OK ? ssm::gated_linear_states_bytes(batch, seqlen, dim) : 0;
+}
+
+int ssm_gated_linear_fwd(int64_t batch, int64_t seqlen, int64_t dim, int in_dtype, int out_dtype, int flags,
+                         int64_t x_step, int64_t gate_step, int64_t input_gate_step,
+                         const void* x, const void* gate, const float* A, const void* input_gate,
+                         const float* gate_bias, const float* input_bias, const float* h0, const int32_t* seqlens,
+                         void* y, float* h_final, float* states, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  GlrSizes z;
+  int st = glr_sizes(batch, seqlen, dim, &z);
+  if (st != SSM_OK) return st;
+  if (out_dtype != 0 && out_dtype != 1) return SSM_E_DTYPE;
+  st = glr_options(z, z.bl, in_dtype, flags, x_step, gate_step, input_gate_step, input_gate != nullptr);
+  if (st != SSM_OK) return st;
+  if (z.bd == 0) return SSM_OK;
+  ssm::GatedLinearArgs a = glr_args(z, in_dtype, flags, x_step, gate_step, input_gate_step, x, gate, A, input_gate,
+                                    gate_bias, input_bias, h0, seqlens);
+  a.h_final = h_final;
+  st = glr_pointers(a, seqlen > 0);
+  if (st != SSM_OK) return st;
+  if (seqlen > 0 && y == nullptr) return SSM_E_NULLPTR;
+  const int64_t osz = out_dtype == 1 ? 2 : 4;
+  if (!aligned(y, static_cast<uintptr_t>(osz)) || !aligned(states, 16)) return SSM_E_ALIGN;
+  const size_t need = ssm::gated_linear_workspace_bytes(batch, seqlen, dim);
+  if (need > 0 && workspace != nullptr && !aligned(workspace, 16)) return SSM_E_ALIGN;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_E_WORKSPACE;
+  Range in[8];
+  glr_inputs(z, z.bl, a, in);
+  const Range rhf = span(h_final, z.bd, 4);
+  const Range out[] = {span(y, z.bld, osz), rhf,
+                       span(states, static_cast<int64_t>(ssm::gated_linear_states_bytes(batch, seqlen, dim)), 1),
+                       span(need > 0 ? workspace : nullptr, static_cast<int64_t>(need), 1)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 8; ++j) {
+      if (i == 1 && j == 6 && rhf.lo == in[6].lo) continue;  // h_final may be h0
+      if (overlaps(out[i], in[j])) return SSM_E_ALIAS;
+    }
+    for (int j = 0; j < i; ++j) {
+      if (overlaps(out[i], out[j])) return SSM_E_ALIAS;
+    }
+  }
+  a.y = y;
+  a.states = states;
+  a.workspace = workspace;
+  a.out_bf16 = out_dtype;
+  return ssm::launch_gated_linear ? map_hip(ssm::launch_gated_linear(a, stream)) : SSM_E_HIP;
+}
+
+int ssm_gated_linear_update(int64_t batch, int64_t dim, int in_dtype, int out_dtype, int flags,
+                            int64_t x_step, int64_t gate_step, int64_t input_gate_step,
+                            float* state, const void* x, const void* gate, const float* A, const void* input_gate,
+                            const float* gate_bias, const float* input_bias, void* y, void* stream) {
+  GlrSizes z;
+  int st = glr_sizes(batch, 1, dim, &z);
+  if (st != SSM_OK) return st;
+  if (out_dtype != 0 && out_dtype != 1) return SSM_E_DTYPE;
+  st = glr_options(z, batch, in_dtype, flags, x_step, gate_step, input_gate_step, input_gate != nullptr);
+  if (st != SSM_OK) return st;
+  if (z.bd == 0) return SSM_OK;
+  ssm::GatedLinearArgs a = glr_args(z, in_dtype, flags, x_step, gate_step, input_gate_step, x, gate, A, input_gate,
+                                    gate_bias, input_bias, nullptr, nullptr);
+  a.h_final = state;
+  st = glr_pointers(a, true);
+  if (st != SSM_OK) return st;
+  if (state == nullptr || y == nullptr) return SSM_E_NULLPTR;
+  const int64_t osz = out_dtype == 1 ? 2 : 4;
+  if (!aligned(y, static_cast<uintptr_t>(osz))) return SSM_E_ALIGN;
+  Range in[8];
+  glr_inputs(z, batch, a, in);
+  const Range ry = span(y, z.bd, osz), rs = span(state, z.bd, 4);
+  for (const Range& r : in) {
+    if (overlaps(ry, r) || overlaps(rs, r)) return SSM_E_ALIAS;
+  }
+  if (overlaps(ry, rs)) return SSM_E_ALIAS;
+  a.y = y;
+  a.out_bf16 = out_dtype;
+  return ssm::launch_gated_linear_update ? map_hip(ssm::launch_gated_linear_update(a, stream)) : SSM_E_HIP;
+}
+
+size_t ssm_gated_linear_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int with_states) {
+  GlrSizes z;
+  if (glr_sizes(batch, seqlen, dim, &z) != SSM_OK) return 0;
+  return ssm::gated_linear_bwd_workspace_bytes(batch, seqlen, dim, with_states != 0);
+}
+
+int ssm_gated_linear_bwd(int64_t batch, int64_t seqlen, int64_t dim, int in_dtype, int flags,
+                         int64_t x_step, int64_t gate_step, int64_t input_gate_step,
+                         const void* x, const void* gate, const float* A, const void* input_gate,
+                         const float* gate_bias, const float* input_bias, const float* h0, const int32_t* seqlens,
+                         const float* states, const float* dy, const float* dh_final,
+                         float* dx, float* dgate, float* dinput_gate, float* dA, float* dgate_bias,
+                         float* dinput_bias, float* dh0, void* workspace, size_t workspace_bytes, void* stream) {
+  GlrSizes z;
+  int st = glr_sizes(batch, seqlen, dim, &z);
+  if (st != SSM_OK) return st;
+  st = glr_options(z, z.bl, in_dtype, flags, x_step, gate_step, input_gate_step, input_gate != nullptr);
+  if (st != SSM_OK) return st;
+  if (dim == 0) return SSM_OK;
+  ssm::GatedLinearArgs a = glr_args(z, in_dtype, flags, x_step, gate_step, input_gate_step, x, gate, A, input_gate,
+                                    gate_bias, input_bias, h0, seqlens);
+  st = glr_pointers(a, z.bl > 0);
+  if (st != SSM_OK) return st;
+  if (dA == nullptr || (z.bl > 0 && (dy == nullptr || dx == nullptr || dgate == nullptr)) ||
+      (z.bl > 0 && (dinput_gate == nullptr) != (input_gate == nullptr))) {
+    return SSM_E_NULLPTR;
+  }
+  const void* f32_ptrs[] = {dy, dh_final, dx, dgate, dinput_gate, dA, dgate_bias, dinput_bias, dh0};
+  for (const void* q : f32_ptrs) {
+    if (!aligned(q, 4)) return SSM_E_ALIGN;
+  }
+  if (!aligned(states, 16)) return SSM_E_ALIGN;
+  const size_t need = ssm::gated_linear_bwd_workspace_bytes(batch, seqlen, dim, states != nullptr);
+  if (need > 0 && workspace != nullptr && !aligned(workspace, 16)) return SSM_E_ALIGN;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_E_WORKSPACE;
+  Range in[11];
+  glr_inputs(z, z.bl, a, in);
+  in[8] = span(states, static_cast<int64_t>(ssm::gated_linear_states_bytes(batch, seqlen, dim)), 1);
+  in[9] = span(dy, z.bld, 4);
+  in[10] = span(dh_final, z.bd, 4);
+  const Range out[] = {span(dx, z.bld, 4),
+                       span(dgate, z.bld, 4),
+                       span(dinput_gate, z.bld, 4),
+                       span(dA, dim, 4),
+                       span(dgate_bias, dim, 4),
+                       span(dinput_bias, dim, 4),
+                       span(dh0, z.bd, 4),
+                       span(need > 0 ? workspace : nullptr, static_cast<int64_t>(need), 1)};
+  for (int i = 0; i < 8; ++i) {
+    for (const Range& r : in) {
+      if (overlaps(out[i], r)) return SSM_E_ALIAS;
+    }
+    for (int j = 0; j < i; ++j) {
+      if (overlaps(out[i], out[j])) return SSM_E_ALIAS;
+    }
+  }
+  ssm::GatedLinearBwdArgs q{};
+  a.states = const_cast<float*>(states);
+  a.workspace = workspace;
+  q.f = a;
+  q.dy = dy;
+  q.dh_final = dh_final;
+  q.dx = dx;
+  q.dgate = dgate;
+  q.digate = dinput_gate;
+  q.dA = dA;
+  q.dgbias = dgate_bias;
+  q.dibias = dinput_bias;
+  q.dh0 = dh0;
+  return ssm::launch_gated_linear_bwd ? map_hip(ssm::launch_gated_linear_bwd(q, stream)) : SSM_E_HIP;
 }
 
 }  // extern "C"

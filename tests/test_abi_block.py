@@ -1,5 +1,5 @@
-"""Argument validation of the entry points of the layer norm, the dropout and the
-causal convolution's gradients.
+"""Argument validation of the entry points of the gated linear recurrence, the
+layer norm, the dropout and the causal convolution's gradients.
 
 CPU only. Every call here fails validation (or has nothing to do) before the
 library touches the device; the fake pointers are never dereferenced.
@@ -49,6 +49,26 @@ def conv_bwd(lib, B=2, L=8, d=8, K=4, ind=0, silu=1, x=P, w=2 * P, b=3 * P, st=4
              dw=8 * P, db=9 * P, dsi=10 * P, ws=11 * P, wsb=1 << 20):
     return lib.ssm_causal_conv1d_bwd(B, L, d, K, ind, silu, vp(x), vp(w), vp(b), vp(st), vp(dy), vp(dst), vp(dx),
                                      vp(dw), vp(db), vp(dsi), vp(ws), wsb, None)
+
+
+def rec(lib, B=2, L=8, D=8, ind=0, outd=0, flags=16 | 32, xs=8, gs=8, igs=8, x=P, g=2 * P, A=3 * P, ig=4 * P, gb=5 * P,
+        ib=6 * P, h0=7 * P, lens=8 * P, y=9 * P, hf=10 * P, st=11 * P, ws=12 * P, wsb=1 << 24):
+    return lib.ssm_gated_linear_fwd(B, L, D, ind, outd, flags, xs, gs, igs, vp(x), vp(g), vp(A), vp(ig), vp(gb), vp(ib),
+                                    vp(h0), vp(lens), vp(y), vp(hf), vp(st), vp(ws), wsb, None)
+
+
+def rec_upd(lib, B=2, D=8, ind=0, outd=0, flags=16 | 32, xs=8, gs=8, igs=8, state=P, x=2 * P, g=3 * P, A=4 * P, ig=5 * P,
+            gb=6 * P, ib=7 * P, y=8 * P):
+    return lib.ssm_gated_linear_update(B, D, ind, outd, flags, xs, gs, igs, vp(state), vp(x), vp(g), vp(A), vp(ig),
+                                       vp(gb), vp(ib), vp(y), None)
+
+
+def rec_bwd(lib, B=2, L=8, D=8, ind=0, flags=16 | 32, xs=8, gs=8, igs=8, x=P, g=2 * P, A=3 * P, ig=4 * P, gb=5 * P,
+            ib=6 * P, h0=7 * P, lens=8 * P, st=9 * P, dy=10 * P, dh=11 * P, dx=12 * P, dg=13 * P, dig=14 * P, dA=15 * P,
+            dgb=16 * P, dib=17 * P, dh0=18 * P, ws=19 * P, wsb=1 << 24):
+    return lib.ssm_gated_linear_bwd(B, L, D, ind, flags, xs, gs, igs, vp(x), vp(g), vp(A), vp(ig), vp(gb), vp(ib),
+                                    vp(h0), vp(lens), vp(st), vp(dy), vp(dh), vp(dx), vp(dg), vp(dig), vp(dA), vp(dgb),
+                                    vp(dib), vp(dh0), vp(ws), wsb, None)
 
 
 def test_dropout(lib):
@@ -143,3 +163,82 @@ def test_conv_bwd(lib):
     assert conv_bwd(lib, d=0, x=None) == OK and conv_bwd(lib, B=0, dw=None, db=None, x=None) == OK
     for bad in ((0, 8, 8, 4), (2, -1, 8, 4), (2, 8, 0, 4), (2, 8, 8, 9), (65536, 8, 8, 4), (2, 8, 1 << 55, 4)):
         assert lib.ssm_causal_conv1d_bwd_workspace_bytes(*bad) == 0
+
+
+@pytest.mark.parametrize("call", [rec, rec_upd, rec_bwd])
+def test_recurrence_sizes_types_and_options(lib, call):
+    assert call(lib, B=-1) == call(lib, D=-1) == E_SHAPE
+    assert call(lib, B=1 << 45, D=1 << 22, xs=1 << 22, gs=1 << 22, igs=1 << 22) == E_SHAPE
+    assert call(lib, D=1 << 23, xs=1 << 23, gs=1 << 23, igs=1 << 23) == E_UNSUPPORTED
+    assert call(lib, B=1 << 28) == E_UNSUPPORTED
+    assert call(lib, ind=2) == E_DTYPE
+    for flags in (1 | 16, 32 | 64, 2, 4, 8, 128, -1):
+        assert call(lib, flags=flags) == E_UNSUPPORTED, flags
+    for name in ("xs", "gs", "igs"):
+        assert call(lib, **{name: 7}) == E_SHAPE, name
+        assert call(lib, **{name: 1 << 23}) == E_UNSUPPORTED, name
+    for name in ("x", "g", "A"):
+        assert call(lib, **{name: None}) == E_NULLPTR, name
+    for name in ("x", "g", "ig"):
+        assert call(lib, ind=1, **{name: P + 1}) == E_ALIGN, name
+        assert call(lib, **{name: P + 2}) == E_ALIGN, name
+    for name in ("A", "gb", "ib"):
+        assert call(lib, **{name: P + 2}) == E_ALIGN, name
+
+
+def test_recurrence_forward(lib):
+    assert rec(lib, L=-1) == E_SHAPE and rec(lib, L=1 << 30) == E_UNSUPPORTED
+    assert rec(lib, outd=2) == E_DTYPE
+    assert rec(lib, ig=None, igs=0, y=None) == E_NULLPTR     # (the step of an absent gate does not count)
+    for name, at in dict(h0=7, lens=8, y=9, hf=10).items():
+        assert rec(lib, **{name: at * P + 2}) == E_ALIGN, name
+    assert rec(lib, st=11 * P + 8) == E_ALIGN
+    ins = dict(x=1, g=2, A=3, ig=4, gb=5, ib=6, h0=7, lens=8)
+    for name, at in ins.items():
+        assert rec(lib, y=at * P) == E_ALIAS and rec(lib, st=at * P) == E_ALIAS, name
+        if name != "h0":
+            assert rec(lib, hf=at * P) == E_ALIAS, name
+    assert rec(lib, hf=7 * P + 4) == rec(lib, hf=9 * P) == rec(lib, st=9 * P) == rec(lib, st=10 * P) == E_ALIAS
+    assert rec(lib, xs=1 << 20, y=P + 4 * 15 * (1 << 20)) == E_ALIAS   # the last row of a column range
+    assert rec(lib, B=0, x=None, A=None, y=None) == rec(lib, D=0, xs=0, gs=0, igs=0, x=None, y=None) == OK
+    big = dict(L=1 << 14, D=256, xs=256, gs=256, igs=256, **{k: (i + 1) << 40 for i, k in enumerate(
+        ("x", "g", "A", "ig", "gb", "ib", "h0", "lens", "y", "hf", "st", "ws"))})
+    need = lib.ssm_gated_linear_workspace_bytes(2, 1 << 14, 256)
+    if need:
+        assert rec(lib, **{**big, "ws": None}) == rec(lib, **big, wsb=need - 1) == E_WORKSPACE
+        assert rec(lib, **{**big, "ws": (12 << 40) + 8}, wsb=need) == E_ALIGN
+        for at in range(1, 12):
+            assert rec(lib, **{**big, "ws": at << 40}, wsb=need) == E_ALIAS, at
+    for bad in ((-1, 8, 8), (2, 1 << 30, 8), (2, 8, 1 << 23)):
+        assert lib.ssm_gated_linear_workspace_bytes(*bad) == lib.ssm_gated_linear_states_bytes(*bad) == 0
+
+
+def test_recurrence_update(lib):
+    assert rec_upd(lib, outd=2) == E_DTYPE
+    assert rec_upd(lib, state=None) == rec_upd(lib, y=None) == E_NULLPTR
+    assert rec_upd(lib, state=P + 2) == rec_upd(lib, y=8 * P + 2) == E_ALIGN
+    for at in range(1, 8):
+        assert rec_upd(lib, y=at * P) == E_ALIAS, at
+    for at in range(2, 9):
+        assert rec_upd(lib, state=at * P) == E_ALIAS, at
+    assert rec_upd(lib, B=0, state=None) == OK
+
+
+def test_recurrence_backward(lib):
+    for name in ("dy", "dx", "dg", "dig", "dA"):
+        assert rec_bwd(lib, **{name: None}) == E_NULLPTR, name
+    assert rec_bwd(lib, ig=None) == E_NULLPTR                # dinput_gate without an input gate
+    for name, at in dict(dy=10, dh=11, dx=12, dg=13, dig=14, dA=15, dgb=16, dib=17, dh0=18).items():
+        assert rec_bwd(lib, **{name: at * P + 2}) == E_ALIGN, name
+    assert rec_bwd(lib, st=9 * P + 8) == rec_bwd(lib, ws=19 * P + 8) == E_ALIGN
+    outs = dict(dx=12, dg=13, dig=14, dA=15, dgb=16, dib=17, dh0=18, ws=19)
+    for name, own in outs.items():
+        for at in range(1, 20):
+            if at != own:
+                assert rec_bwd(lib, **{name: at * P}) == E_ALIAS, (name, at)
+    for st in (9 * P, None):
+        need = lib.ssm_gated_linear_bwd_workspace_bytes(2, 8, 8, 1 if st else 0)
+        assert need > 0
+        assert rec_bwd(lib, st=st, ws=None) == rec_bwd(lib, st=st, wsb=need - 1) == E_WORKSPACE
+    assert lib.ssm_gated_linear_bwd_workspace_bytes(2, 1 << 30, 8, 1) == 0
+    assert rec_bwd(lib, D=0, xs=0, gs=0, igs=0, dA=None) == OK
