@@ -767,7 +767,7 @@ int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
  * weight sigmoid(u).
  *
  *   batch, seqlen, dim         : B >= 0, 0 <= L < 2^30, 0 <= D < 2^23, B D <
- *                                2^30, B ceil(D / 64) ceil(L / 64) <= 2^30
+ *                                2^30, B ceil(D / 64) ceil(L / 64) < 2^24
  *                                (else SSM_E_UNSUPPORTED).
  *   in_dtype, out_dtype        : of x and the gates; of y. 0 float32, 1 bfloat16.
  *   flags                      : at most one of the gate's and one of the

@@ -37,7 +37,8 @@ DEVICE_SOURCES = ["scan_fwd.hip", "scan_fwd_bb.hip", "scan_fwd_bf.hip", "scan_fw
                   "scan_noalloc.hip", "gated_delta.hip", "gated_delta_prep.hip",
                   "gated_delta_chunk_b.hip", "gated_delta_chunk_f.hip", "gdr_segments.hip", "gated_delta_reverse.hip", "gated_delta_grads.hip",
                   "rms_norm.hip", "layer_norm.hip", "dropout.hip", "conv1d_bwd.hip",
-                  "gated_linear.hip"]
+                  "gated_linear.hip", "gated_linear_fwd_b.hip", "gated_linear_fwd_f.hip", "gated_linear_bwd_b.hip",
+                  "gated_linear_bwd_f.hip"]
 HOST_SOURCES = ["api.cpp", "plan.cpp"]
 PROBE_SOURCES = ["probe.hip"]
 

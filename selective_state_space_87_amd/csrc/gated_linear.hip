@@ -1,182 +1,151 @@
-// Gated linear recurrence, forward, single token and backward: the plain form,
-// one thread a batch row and channel, step by step.
+// Gated linear recurrence: the step-by-step kernel (single tokens and short
+// sequences), the sums of the parameters' gradients, and the launchers; the tiles
+// of long sequences are in gated_linear_{fwd,bwd}.h.
 #include <hip/hip_runtime.h>
 
-#include "gated_linear.h"
+#include "gated_linear_tile.h"
 
 namespace ssm {
 
 namespace {
 
-constexpr int kThreads = 64;
-
-template <bool BF16, int ACT, int SCALE>
-struct Element {
-  float u, g, slope, la, a, w, x, s, s_slope, v;
-  __device__ __forceinline__ Element(const GatedLinearArgs& p, int64_t row, int64_t d) {
-    u = load_elem<BF16>(p.gate, row * p.gate_step + d) + (p.gbias ? p.gbias[d] : 0.0f);
-    g = gate_value_slope<ACT>(u, &slope);
-    la = p.A[d] * g;
-    a = decay(la);
-    w = input_weight<SCALE>(la, a);
-    x = load_elem<BF16>(p.x, row * p.x_step + d);
-    s = 1.0f, s_slope = 0.0f;
-    if (p.igate) {
-      s = sigmoid_slope(load_elem<BF16>(p.igate, row * p.igate_step + d) + (p.ibias ? p.ibias[d] : 0.0f), &s_slope);
-    }
-    v = x * s;
-  }
-};
-
-__device__ __forceinline__ int64_t row_steps(const GatedLinearArgs& p, int64_t b) {
-  return gdr_row_steps(p.seqlens, static_cast<int>(b), p.seqlen);
-}
-
-template <bool BF16, int ACT, int SCALE>
-__global__ __launch_bounds__(kThreads) void gated_linear_kernel(const GatedLinearArgs p) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= p.batch * p.dim) return;
-  const int64_t b = i / p.dim, d = i - b * p.dim, steps = row_steps(p, b);
-  float h = p.h0 ? p.h0[i] : 0.0f;
+// A thread walks VC channels of a batch row.
+template <bool BF16, int ACT, int SCALE, bool GATED>
+__global__ __launch_bounds__(kGlrThreads) void glr_walk_kernel(const GatedLinearArgs p) {
+  constexpr int VC = GlrLane<BF16>::VC;
+  const int64_t per_row = (p.dim + VC - 1) / VC;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kGlrThreads + threadIdx.x;
+  if (i >= p.batch * per_row) return;
+  const int64_t b = i / per_row;
+  const int c = static_cast<int>(i - b * per_row) * VC, left = static_cast<int>(p.dim) - c;
+  const int64_t steps = gdr_row_steps(p.seqlens, static_cast<int>(b), p.seqlen);
+  GlrParams<VC, GATED> par;
+  GlrRaw<BF16, GATED, 1> raw;
+  if (steps > 0) raw.load(p, b * p.seqlen, c, left, 0, 1, left >= VC);
+  par.load(p, c, left);
+  float h[VC] = {};
+  if (p.h0 != nullptr) glr_load_f32<VC>(p.h0, b * p.dim + c, left, h);
+  if (p.states != nullptr && p.seqlen > 0) glr_store_f32<VC>(p.states, b * p.dim + c, left, h);
   for (int64_t t = 0; t < p.seqlen; ++t) {
-    const int64_t at = (b * p.seqlen + t) * p.dim + d;
-    if (p.states) p.states[at] = h;
+    float y[VC] = {};
     if (t < steps) {
-      const Element<BF16, ACT, SCALE> e(p, b * p.seqlen + t, d);
-      h = fmaf(e.a, h, e.w * e.v);
+      const GlrRaw<BF16, GATED, 1> now = raw;
+      if (t + 1 < steps) raw.load(p, b * p.seqlen + t + 1, c, left, 0, 1, left >= VC);
+#pragma unroll
+      for (int v = 0; v < VC; ++v) {
+        const float la = par.A[v] * gate_value<ACT>(glr_elem<BF16>(now.gate[0], v) + par.gbias[v]);
+        const float a = decay(la);
+        float in = glr_elem<BF16>(now.x[0], v);
+        if constexpr (GATED) in *= sigmoid_f(glr_elem<BF16>(now.igate[0], v) + par.ibias[v]);
+        h[v] = fmaf(a, h[v], input_weight<SCALE>(la, a) * in);
+        y[v] = h[v];
+      }
     }
-    if (p.y) {
-      const float y = t < steps ? h : 0.0f;
-      p.out_bf16 ? store_elem<true>(p.y, at, y) : store_elem<false>(p.y, at, y);
+    if (p.y != nullptr) {
+      const int64_t to = (b * p.seqlen + t) * p.dim + c;
+      if (p.out_bf16) {
+        glr_store_bf16<VC>(p.y, to, left, y);
+      } else {
+        glr_store_f32<VC>(static_cast<float*>(p.y), to, left, y);
+      }
     }
   }
-  if (p.h_final) p.h_final[i] = h;
+  if (p.h_final != nullptr) glr_store_f32<VC>(p.h_final, b * p.dim + c, left, h);
 }
 
-template <bool BF16, int ACT, int SCALE>
-__global__ __launch_bounds__(kThreads) void gated_linear_bwd_kernel(const GatedLinearBwdArgs q) {
-  const GatedLinearArgs& p = q.f;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, n = p.batch * p.dim;
-  if (i >= n) return;
-  const int64_t b = i / p.dim, d = i - b * p.dim, steps = row_steps(p, b);
-  float dh = q.dh_final ? q.dh_final[i] : 0.0f;
-  double dA = 0.0, dgb = 0.0, dib = 0.0;
-  for (int64_t t = p.seqlen - 1; t >= 0; --t) {
-    const int64_t at = (b * p.seqlen + t) * p.dim + d;
-    float dx = 0.0f, dg = 0.0f, di = 0.0f;
-    if (t < steps) {
-      const Element<BF16, ACT, SCALE> e(p, b * p.seqlen + t, d);
-      dh += q.dy[at];
-      const float dv = e.w * dh;
-      dx = dv * e.s;
-      di = dv * e.x * e.s_slope;
-      const float dla = dh * fmaf(e.a, p.states[at], input_weight_slope<SCALE>(e.a, e.w) * e.v);
-      dg = dla * p.A[d] * e.slope;
-      dA += dla * e.g;
-      dgb += dg;
-      dib += di;
-      dh *= e.a;
-    }
-    q.dx[at] = dx;
-    q.dgate[at] = dg;
-    if (q.digate) q.digate[at] = di;
-  }
-  if (q.dh0) q.dh0[i] = dh;
-  double* parts = static_cast<double*>(p.workspace);
-  parts[i] = dA, parts[n + i] = dgb, parts[2 * n + i] = dib;
+template <bool BF16>
+void launch_walk(const GatedLinearArgs& a, hipStream_t st) {
+  const int64_t threads = a.batch * ((a.dim + GlrLane<BF16>::VC - 1) / GlrLane<BF16>::VC);
+  const unsigned blocks = static_cast<unsigned>((threads + kGlrThreads - 1) / kGlrThreads);
+  glr_by_form(a, [&](auto act, auto scale, auto gated) {
+    glr_walk_kernel<BF16, decltype(act)::value, decltype(scale)::value, decltype(gated)::value>
+        <<<blocks, kGlrThreads, 0, st>>>(a);
+  });
 }
 
-__global__ __launch_bounds__(kThreads) void gated_linear_sums_kernel(const GatedLinearBwdArgs q) {
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, n = q.f.batch * q.f.dim;
-  if (d >= q.f.dim) return;
-  const double* parts = static_cast<const double*>(q.f.workspace);
-  float* out[3] = {q.dA, q.dgbias, q.dibias};
-  for (int k = 0; k < 3; ++k) {
-    double sum = 0.0;
-    for (int64_t i = d; i < n; i += q.f.dim) sum += parts[k * n + i];
-    if (out[k]) out[k][d] = static_cast<float>(sum);
+__global__ __launch_bounds__(kGlrThreads) void glr_clear_kernel(u32x4* words, int64_t n) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGlrThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kGlrThreads + threadIdx.x; i < n; i += step) {
+    const uint32_t v = i < 16 ? 0u : kGlrMissing;  // the count's 256 bytes, then the words
+    words[i] = u32x4{v, v, v, v};
   }
 }
 
-// One token: the step above, in place on the state.
-template <bool BF16, int ACT, int SCALE>
-__global__ __launch_bounds__(kThreads) void gated_linear_update_kernel(const GatedLinearArgs p) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= p.batch * p.dim) return;
-  const int64_t b = i / p.dim, d = i - b * p.dim;
-  const Element<BF16, ACT, SCALE> e(p, b, d);
-  const float h = fmaf(e.a, p.h_final[i], e.w * e.v);
-  p.h_final[i] = h;
-  p.out_bf16 ? store_elem<true>(p.y, i, h) : store_elem<false>(p.y, i, h);
-}
-
-// f(in_bf16, act, scale) as compile-time constants.
-template <typename F>
-void by_form(const GatedLinearArgs& p, F&& f) {
-  using std::integral_constant;
-  const auto scale = [&](auto bf16, auto act) {
-    if (p.scale == kInputNorm) {
-      f(bf16, act, integral_constant<int, kInputNorm>{});
-    } else if (p.scale == kInputComplement) {
-      f(bf16, act, integral_constant<int, kInputComplement>{});
-    } else {
-      f(bf16, act, integral_constant<int, kInputPlain>{});
+// dA, dgate_bias, dinput_bias: 64 of the 3 D columns a block, sixteen waves each
+// adding every sixteenth tile's part in double, then the sixteen sums in order.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void glr_sums_kernel(const float* __restrict__ parts, int64_t nparts,
+                                                                  int64_t dim, float* dA, float* dgbias,
+                                                                  float* dibias) {
+  __shared__ double sums[kSumWaves][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane, cols = 3 * dim;
+  double acc = 0.0;
+  if (c < cols) {
+    int64_t i = w;
+    for (; i + 7 * kSumWaves < nparts; i += 8 * kSumWaves) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = parts[(i + k * kSumWaves) * cols + c];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc += v[k];
     }
-  };
-  const auto act = [&](auto bf16) {
-    if (p.act == kGateSigmoid) {
-      scale(bf16, integral_constant<int, kGateSigmoid>{});
-    } else if (p.act == kGateSoftplus) {
-      scale(bf16, integral_constant<int, kGateSoftplus>{});
-    } else {
-      scale(bf16, integral_constant<int, kGateRaw>{});
-    }
-  };
-  p.in_bf16 ? act(std::true_type{}) : act(std::false_type{});
+    for (; i < nparts; i += kSumWaves) acc += parts[i * cols + c];
+  }
+  sums[w][lane] = acc;
+  __syncthreads();
+  if (w == 0 && c < cols) {
+    double v = 0.0;
+#pragma unroll
+    for (int k = 0; k < kSumWaves; ++k) v += sums[k][lane];
+    const int64_t which = c / dim;
+    float* out = which == 0 ? dA : (which == 1 ? dgbias : dibias);
+    if (out != nullptr) out[c - which * dim] = static_cast<float>(v);
+  }
 }
-
-unsigned blocks_of(int64_t n) { return static_cast<unsigned>((n + kThreads - 1) / kThreads); }
 
 }  // namespace
 
+void launch_glr_clear(const GlrChainPlan& p, void* workspace, hipStream_t st) {
+  const int64_t n = static_cast<int64_t>(p.bytes / 16);
+  const int64_t blocks = (n + kGlrThreads - 1) / kGlrThreads;
+  glr_clear_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), kGlrThreads, 0, st>>>(
+      static_cast<u32x4*>(workspace), n);
+}
+
 int launch_gated_linear(const GatedLinearArgs& a, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  by_form(a, [&](auto bf16, auto act, auto scale) {
-    gated_linear_kernel<decltype(bf16)::value, decltype(act)::value, decltype(scale)::value>
-        <<<blocks_of(a.batch * a.dim), kThreads, 0, st>>>(a);
-  });
+  if (a.seqlen <= kGlrWalkSteps) {
+    a.in_bf16 ? launch_walk<true>(a, st) : launch_walk<false>(a, st);
+  } else {
+    const GlrChainPlan plan = plan_glr_chain(a.batch, a.seqlen, a.dim, kGlrFwdSteps);
+    a.in_bf16 ? launch_glr_fwd<true>(a, plan, st) : launch_glr_fwd<false>(a, plan, st);
+  }
   return static_cast<int>(hipGetLastError());
 }
 
-int launch_gated_linear_update(const GatedLinearArgs& a, void* stream) {
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  by_form(a, [&](auto bf16, auto act, auto scale) {
-    gated_linear_update_kernel<decltype(bf16)::value, decltype(act)::value, decltype(scale)::value>
-        <<<blocks_of(a.batch * a.dim), kThreads, 0, st>>>(a);
-  });
-  return static_cast<int>(hipGetLastError());
+int launch_gated_linear_update(const GatedLinearArgs& given, void* stream) {
+  GatedLinearArgs a = given;
+  a.h0 = a.h_final;
+  return launch_gated_linear(a, stream);
 }
 
 int launch_gated_linear_bwd(const GatedLinearBwdArgs& given, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   GatedLinearBwdArgs a = given;
+  const GlrBwdPlan plan = plan_gated_linear_bwd(a.f.batch, a.f.seqlen, a.f.dim, a.f.states != nullptr);
   if (a.f.batch > 0) {
     if (a.f.states == nullptr) {
-      GatedLinearArgs f = a.f;
-      f.y = nullptr;
-      f.h_final = nullptr;
-      f.states = reinterpret_cast<float*>(static_cast<char*>(a.f.workspace) +
-                                          gated_linear_parts_bytes(a.f.batch, a.f.dim));
-      if (const int e = launch_gated_linear(f, stream)) return e;
-      a.f.states = f.states;
+      a.f.states = reinterpret_cast<float*>(static_cast<char*>(a.f.workspace) + plan.off_states);
+      if (const int e = launch_gated_linear(a.f, stream)) return e;
     }
-    by_form(a.f, [&](auto bf16, auto act, auto scale) {
-      gated_linear_bwd_kernel<decltype(bf16)::value, decltype(act)::value, decltype(scale)::value>
-          <<<blocks_of(a.f.batch * a.f.dim), kThreads, 0, st>>>(a);
-    });
+    a.f.in_bf16 ? launch_glr_bwd<true>(a, plan, st) : launch_glr_bwd<false>(a, plan, st);
     if (const hipError_t e = hipGetLastError()) return static_cast<int>(e);
   }
-  gated_linear_sums_kernel<<<blocks_of(a.f.dim), kThreads, 0, st>>>(a);
+  const int64_t cols = 3 * a.f.dim;
+  glr_sums_kernel<<<static_cast<unsigned>((cols + 63) / 64), 64 * kSumWaves, 0, st>>>(
+      reinterpret_cast<const float*>(static_cast<const char*>(a.f.workspace) + plan.off_parts),
+      a.f.batch * plan.chain.tiles, a.f.dim, a.dA, a.dgbias, a.dibias);
   return static_cast<int>(hipGetLastError());
 }
 

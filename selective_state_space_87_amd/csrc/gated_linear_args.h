@@ -49,22 +49,72 @@ __attribute__((weak)) int launch_gated_linear(const GatedLinearArgs& a, void* st
 __attribute__((weak)) int launch_gated_linear_update(const GatedLinearArgs& a, void* stream);  // h_final: the state
 __attribute__((weak)) int launch_gated_linear_bwd(const GatedLinearBwdArgs& a, void* stream);
 
-// Tiles of 64 channels and 64 steps, at most.
+// A long sequence runs in tiles of 64 channels, kGlrFwdSteps steps forward and
+// kGlrBwdSteps backward, a block each. A tile's part of the recurrence is a pair
+// (product of the decays, state from a zero start) a channel; a chain in the
+// workspace joins the pairs (gated_linear_tile.h): a word a tile and channel, and
+// one for every kGlrWindow tiles.
+constexpr int kGlrChannels = 64, kGlrFwdSteps = 128, kGlrBwdSteps = 64, kGlrWindow = 8;
+
+// Up to this length a sequence is walked step by step, with no tiles.
+constexpr int64_t kGlrWalkSteps = 16;
+
+// At most as many blocks of 256 threads as keep a launch below 2^32 threads.
 inline bool gated_linear_fits(int64_t batch, int64_t seqlen, int64_t dim) {
-  return batch * ((dim + 63) / 64) * ((seqlen + 63) / 64) <= (int64_t(1) << 30);
+  const int64_t tiles = (seqlen + kGlrBwdSteps - 1) / kGlrBwdSteps;
+  return batch * ((dim + kGlrChannels - 1) / kGlrChannels) * (tiles > 0 ? tiles : 1) < (int64_t(1) << 24);
 }
 
+struct GlrChainPlan {
+  int64_t groups, tiles;  // blocks of channels, over the batch rows; tiles of steps
+  size_t off_words, off_states, bytes;
+};
+
+inline GlrChainPlan plan_glr_chain(int64_t batch, int64_t seqlen, int64_t dim, int steps) {
+  GlrChainPlan p{};
+  p.groups = batch * ((dim + kGlrChannels - 1) / kGlrChannels);
+  p.tiles = (seqlen + steps - 1) / steps;
+  if (p.tiles <= 1) return p;
+  const size_t word = static_cast<size_t>(p.groups) * kGlrChannels * 8;
+  p.off_words = 256;  // behind the tickets' counter
+  p.off_states = p.off_words + static_cast<size_t>(p.tiles) * word;
+  p.bytes = p.off_states + static_cast<size_t>(p.tiles / kGlrWindow) * word;
+  return p;
+}
+
+// States entering every tile of kGlrBwdSteps steps, [B, tiles, D] float32.
 inline size_t gated_linear_states_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
-  return static_cast<size_t>(batch * seqlen * dim) * 4;
+  return static_cast<size_t>(batch * ((seqlen + kGlrBwdSteps - 1) / kGlrBwdSteps) * dim) * 4;
 }
-inline size_t gated_linear_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
-// Parts of dA, dgate_bias and dinput_bias, one a batch row, and the states when they are not given.
-inline size_t gated_linear_parts_bytes(int64_t batch, int64_t dim) {
-  return (static_cast<size_t>(batch * dim) * 3 * 8 + 255) & ~size_t(255);
+inline size_t gated_linear_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
+  return plan_glr_chain(batch, seqlen, dim, kGlrFwdSteps).bytes;
 }
+
+// Backward: the chain (the forward's too, when the states are not given), the
+// states, and a tile's parts of dA, dgate_bias and dinput_bias.
+struct GlrBwdPlan {
+  GlrChainPlan chain;
+  size_t off_parts, off_states, bytes;
+};
+
+inline GlrBwdPlan plan_gated_linear_bwd(int64_t batch, int64_t seqlen, int64_t dim, bool have_states) {
+  GlrBwdPlan p{};
+  const auto align = [](size_t n) { return (n + 255) & ~size_t(255); };
+  p.chain = plan_glr_chain(batch, seqlen, dim, kGlrBwdSteps);
+  size_t chain = p.chain.bytes;
+  if (!have_states) {
+    const size_t fwd = gated_linear_workspace_bytes(batch, seqlen, dim);
+    if (fwd > chain) chain = fwd;
+  }
+  p.off_parts = align(chain);
+  p.off_states = p.off_parts + align(static_cast<size_t>(p.chain.tiles * batch * dim) * 3 * 4);
+  p.bytes = p.off_states + (have_states ? 0 : align(gated_linear_states_bytes(batch, seqlen, dim)));
+  return p;
+}
+
 inline size_t gated_linear_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, bool have_states) {
-  return gated_linear_parts_bytes(batch, dim) + (have_states ? 0 : gated_linear_states_bytes(batch, seqlen, dim));
+  return plan_gated_linear_bwd(batch, seqlen, dim, have_states).bytes;
 }
 
 }  // namespace ssm

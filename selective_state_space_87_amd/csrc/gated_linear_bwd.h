@@ -1,0 +1,241 @@
+// Backward tiles of the gated linear recurrence; instantiated for bfloat16 and
+// float32 inputs in gated_linear_bwd_{b,f}.hip. See gated_linear_tile.h.
+//
+// With E the gradient that reaches a step's state from behind, D = E + dy, and a D
+// reaches the state before: the maps E -> P E + R of slices and tiles join from
+// the last to the first, over the same products P of decays as forward. A tile
+// (64 steps) has the state that enters it from the forward, takes both
+// recurrences through its slices at once, and computes its gates a second time
+// where the gradients are formed: the inputs stay in registers, what was made of
+// them would not fit. Its sums over steps are one part a tile, joined in double
+// in a fixed order (glr_sums_kernel).
+#pragma once
+
+#include "gated_linear_tile.h"
+
+namespace ssm {
+
+template <bool BF16, int ACT, int SCALE, bool GATED, bool CHAIN>
+__global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearBwdArgs q, const GlrChain chain,
+                                                              const uint32_t tiles, float* parts) {
+  using Lane = GlrLane<BF16>;
+  constexpr int VC = Lane::VC, SL = Lane::kSlices, TS = kGlrBwdSteps / SL, kRun = SL / 4;
+  __shared__ __attribute__((aligned(16))) float lp[SL][kGlrChannels], ls[SL][kGlrChannels], lr[SL][kGlrChannels];
+  __shared__ float rp[4][kGlrChannels], rs[4][kGlrChannels], rr[4][kGlrChannels];
+  __shared__ float enter_h[kGlrChannels], enter_e[kGlrChannels];
+  __shared__ uint32_t slot;
+  const GatedLinearArgs& p = q.f;
+  uint32_t tile = blockIdx.x;
+  if constexpr (CHAIN) tile = glr_ticket(chain, &slot);
+  const uint32_t place = CHAIN ? tile / chain.groups : 0;   // the last tiles first
+  const uint32_t k = CHAIN ? tiles - 1 - place : 0;
+  const GlrTile at = glr_tile(p, CHAIN ? tile - place * chain.groups : tile);
+  const int64_t t0 = static_cast<int64_t>(k) * kGlrBwdSteps;
+  const int slice = threadIdx.x / Lane::kLanes;
+  const int ch = static_cast<int>(threadIdx.x % Lane::kLanes) * VC, c = at.c0 + ch;
+  const int left = static_cast<int>(p.dim) - c;
+  const int there = p.seqlen - t0 < kGlrBwdSteps ? static_cast<int>(p.seqlen - t0) : kGlrBwdSteps;
+  const int n = at.steps - t0 < there ? static_cast<int>(at.steps - t0) : there;
+  const int lane = threadIdx.x & 63, run = threadIdx.x >> 6, ce = at.c0 + lane;
+  float* part = parts + (static_cast<int64_t>(at.b) * tiles + k) * 3 * p.dim;
+  if (n <= 0) {  // behind the row's end: gradients of 0, and nobody waits for it
+    const float zero[VC] = {};
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+      const int64_t to = (at.row0 + t0 + slice * TS + i) * p.dim + c;
+      if (slice * TS + i < there) {
+        glr_store_f32<VC>(q.dx, to, left, zero);
+        glr_store_f32<VC>(q.dgate, to, left, zero);
+        if constexpr (GATED) glr_store_f32<VC>(q.digate, to, left, zero);
+      }
+    }
+    if (run == 0 && ce < p.dim) {
+      if (there > 0) part[ce] = part[p.dim + ce] = part[2 * p.dim + ce] = 0.0f;
+      const int64_t i = static_cast<int64_t>(at.b) * p.dim + ce;
+      if (k == 0 && q.dh0 != nullptr) q.dh0[i] = q.dh_final != nullptr ? q.dh_final[i] : 0.0f;
+    }
+    return;
+  }
+
+  GlrRaw<BF16, GATED, TS> raw;
+  GlrParams<VC, GATED> par;
+  float dy[TS][VC], a[TS][VC], b[TS][VC];
+  const bool whole = n == kGlrBwdSteps && at.c0 + kGlrChannels <= p.dim;
+  raw.load(p, at.row0 + t0, c, left, slice * TS, n, whole);
+#pragma unroll
+  for (int i = 0; i < TS; ++i) {
+    const int64_t from = (at.row0 + t0 + slice * TS + i) * p.dim + c;
+    if (whole) {
+#pragma unroll
+      for (int w = 0; w < VC / 4; ++w) {
+        const u32x4 d = glr_load_whole<false>(q.dy, from + 4 * w);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) dy[i][4 * w + v] = __uint_as_float(d[v]);
+      }
+    } else {
+      glr_load_f32<VC>(q.dy, from, slice * TS + i < n ? left : 0, dy[i]);
+    }
+  }
+  par.load(p, c, left);
+  {
+    float P[VC], S[VC], R[VC];
+#pragma unroll
+    for (int v = 0; v < VC; ++v) P[v] = 1.0f, S[v] = R[v] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+      const bool on = slice * TS + i < n;
+#pragma unroll
+      for (int v = 0; v < VC; ++v) {
+        const float la = par.A[v] * gate_value<ACT>(glr_elem<BF16>(raw.gate[i], v) + par.gbias[v]);
+        const float d = decay(la);
+        float in = glr_elem<BF16>(raw.x[i], v);
+        if constexpr (GATED) in *= sigmoid_f(glr_elem<BF16>(raw.igate[i], v) + par.ibias[v]);
+        a[i][v] = on ? d : 1.0f;
+        b[i][v] = on ? input_weight<SCALE>(la, d) * in : 0.0f;
+        P[v] *= a[i][v];
+        S[v] = fmaf(a[i][v], S[v], b[i][v]);
+      }
+    }
+#pragma unroll
+    for (int i = TS - 1; i >= 0; --i) {
+#pragma unroll
+      for (int v = 0; v < VC; ++v) R[v] = a[i][v] * (dy[i][v] + R[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < VC; ++v) lp[slice][ch + v] = P[v], ls[slice][ch + v] = S[v], lr[slice][ch + v] = R[v];
+  }
+  __syncthreads();
+  float sp[kRun], ss[kRun], sr[kRun];
+  float rP = 1.0f, rS = 0.0f, rR = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    sp[i] = lp[run * kRun + i][lane], ss[i] = ls[run * kRun + i][lane], sr[i] = lr[run * kRun + i][lane];
+    rP *= sp[i];
+    rS = fmaf(sp[i], rS, ss[i]);
+  }
+#pragma unroll
+  for (int i = kRun - 1; i >= 0; --i) rR = fmaf(sp[i], rR, sr[i]);
+  rp[run][lane] = rP, rs[run][lane] = rS, rr[run][lane] = rR;
+  __syncthreads();
+  if (run == 0) {
+    const int64_t i = static_cast<int64_t>(at.b) * p.dim + ce;
+    float e = q.dh_final != nullptr && ce < p.dim ? q.dh_final[i] : 0.0f;
+    enter_h[lane] = ce < p.dim ? p.states[(static_cast<int64_t>(at.b) * tiles + k) * p.dim + ce] : 0.0f;
+    float P = rp[3][lane], R = rr[3][lane];
+#pragma unroll
+    for (int r = 2; r >= 0; --r) {
+      P *= rp[r][lane];
+      R = fmaf(rp[r][lane], R, rr[r][lane]);
+    }
+    if constexpr (CHAIN) {
+      const uint32_t last = static_cast<uint32_t>((at.steps - 1) / kGlrBwdSteps);
+      e = glr_enter(chain, static_cast<uint32_t>(at.group), last - k, P, R, e);
+    }
+    enter_e[lane] = e;
+    if (k == 0 && q.dh0 != nullptr && ce < p.dim) q.dh0[i] = fmaf(P, e, R);
+  }
+  __syncthreads();
+  {
+    float h = enter_h[lane], e = enter_e[lane];
+#pragma unroll
+    for (int r = 0; r < 3; ++r) {
+      if (r < run) h = fmaf(rp[r][lane], h, rs[r][lane]);
+    }
+#pragma unroll
+    for (int r = 3; r > 0; --r) {
+      if (r > run) e = fmaf(rp[r][lane], e, rr[r][lane]);
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      ls[run * kRun + i][lane] = h;
+      h = fmaf(sp[i], h, ss[i]);
+    }
+#pragma unroll
+    for (int i = kRun - 1; i >= 0; --i) {
+      lr[run * kRun + i][lane] = e;
+      e = fmaf(sp[i], e, sr[i]);
+    }
+  }
+  __syncthreads();
+
+  float before[TS][VC], E[VC], sumA[VC], sumg[VC], sumi[VC];
+#pragma unroll
+  for (int v = 0; v < VC; ++v) {
+    float h = ls[slice][ch + v];
+    E[v] = lr[slice][ch + v];
+    sumA[v] = sumg[v] = sumi[v] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+      before[i][v] = h;
+      h = fmaf(a[i][v], h, b[i][v]);
+    }
+  }
+#pragma unroll
+  for (int i = TS - 1; i >= 0; --i) {
+    const int s = slice * TS + i;
+    const bool on = s < n;
+    float dx[VC], dg[VC], di[VC];
+#pragma unroll
+    for (int v = 0; v < VC; ++v) {
+      const float D = dy[i][v] + E[v];
+      float slope, islope = 0.0f, in = glr_elem<BF16>(raw.x[i], v), sig = 1.0f;
+      const float g = gate_value_slope<ACT>(glr_elem<BF16>(raw.gate[i], v) + par.gbias[v], &slope);
+      const float w = input_weight<SCALE>(par.A[v] * g, a[i][v]);
+      const float dv = on ? w * D : 0.0f;
+      if constexpr (GATED) sig = sigmoid_slope(glr_elem<BF16>(raw.igate[i], v) + par.ibias[v], &islope);
+      dx[v] = dv * sig;
+      di[v] = dv * in * islope;
+      const float dla = on ? D * fmaf(a[i][v], before[i][v], input_weight_slope<SCALE>(a[i][v], w) * (in * sig)) : 0.0f;
+      dg[v] = dla * par.A[v] * slope;
+      sumA[v] = fmaf(dla, g, sumA[v]);
+      sumg[v] += dg[v];
+      sumi[v] += di[v];
+      E[v] = a[i][v] * D;
+    }
+    if (s < there) {
+      const int64_t to = (at.row0 + t0 + s) * p.dim + c;
+      glr_store_f32<VC>(q.dx, to, left, dx);
+      glr_store_f32<VC>(q.dgate, to, left, dg);
+      if constexpr (GATED) glr_store_f32<VC>(q.digate, to, left, di);
+    }
+  }
+  __syncthreads();  // ls and lr have been read
+#pragma unroll
+  for (int v = 0; v < VC; ++v) lp[slice][ch + v] = sumA[v], ls[slice][ch + v] = sumg[v], lr[slice][ch + v] = sumi[v];
+  __syncthreads();
+  float total[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    total[0] += lp[run * kRun + i][lane];
+    total[1] += ls[run * kRun + i][lane];
+    total[2] += lr[run * kRun + i][lane];
+  }
+  rp[run][lane] = total[0], rs[run][lane] = total[1], rr[run][lane] = total[2];
+  __syncthreads();
+  if (run == 0 && ce < p.dim) {
+    part[ce] = (rp[0][lane] + rp[1][lane]) + (rp[2][lane] + rp[3][lane]);
+    part[p.dim + ce] = (rs[0][lane] + rs[1][lane]) + (rs[2][lane] + rs[3][lane]);
+    part[2 * p.dim + ce] = (rr[0][lane] + rr[1][lane]) + (rr[2][lane] + rr[3][lane]);
+  }
+}
+
+template <bool BF16>
+void launch_glr_bwd(const GatedLinearBwdArgs& a, const GlrBwdPlan& plan, hipStream_t st) {
+  const GlrChainPlan& cp = plan.chain;
+  float* parts = reinterpret_cast<float*>(static_cast<char*>(a.f.workspace) + plan.off_parts);
+  const uint32_t tiles = static_cast<uint32_t>(cp.tiles);
+  glr_by_form(a.f, [&](auto act, auto scale, auto gated) {
+    constexpr int ACT = decltype(act)::value, SCALE = decltype(scale)::value;
+    constexpr bool GATED = decltype(gated)::value;
+    if (cp.tiles > 1) {
+      launch_glr_clear(cp, a.f.workspace, st);
+      glr_bwd_kernel<BF16, ACT, SCALE, GATED, true><<<static_cast<unsigned>(cp.groups * cp.tiles), kGlrThreads, 0, st>>>(
+          a, glr_chain(cp, a.f.workspace), tiles, parts);
+    } else {
+      glr_bwd_kernel<BF16, ACT, SCALE, GATED, false>
+          <<<static_cast<unsigned>(cp.groups), kGlrThreads, 0, st>>>(a, GlrChain{}, tiles, parts);
+    }
+  });
+}
+
+}  // namespace ssm

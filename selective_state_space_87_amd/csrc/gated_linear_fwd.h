@@ -1,0 +1,150 @@
+// Forward tiles of the gated linear recurrence; instantiated for bfloat16 and
+// float32 inputs in gated_linear_fwd_{b,f}.hip. See gated_linear_tile.h.
+#pragma once
+
+#include "gated_linear_tile.h"
+
+namespace ssm {
+
+template <bool BF16, int ACT, int SCALE, bool GATED, bool CHAIN>
+__global__ __launch_bounds__(kGlrThreads) void glr_fwd_kernel(const GatedLinearArgs p, const GlrChain chain) {
+  using Lane = GlrLane<BF16>;
+  constexpr int VC = Lane::VC, SL = Lane::kSlices, TS = kGlrFwdSteps / SL, kRun = SL / 4;
+  __shared__ __attribute__((aligned(16))) float lp[SL][kGlrChannels], ls[SL][kGlrChannels];
+  __shared__ float rp[4][kGlrChannels], rs[4][kGlrChannels], enter[kGlrChannels];
+  __shared__ uint32_t slot;
+  uint32_t tile = blockIdx.x;
+  if constexpr (CHAIN) tile = glr_ticket(chain, &slot);
+  const uint32_t k = CHAIN ? tile / chain.groups : 0;
+  const GlrTile at = glr_tile(p, CHAIN ? tile - k * chain.groups : tile);
+  const int64_t t0 = static_cast<int64_t>(k) * kGlrFwdSteps;
+  const int slice = threadIdx.x / Lane::kLanes;
+  const int c = at.c0 + static_cast<int>(threadIdx.x % Lane::kLanes) * VC;
+  const int left = static_cast<int>(p.dim) - c;
+  const int there = p.seqlen - t0 < kGlrFwdSteps ? static_cast<int>(p.seqlen - t0) : kGlrFwdSteps;  // steps of the array
+  const int n = at.steps - t0 < there ? static_cast<int>(at.steps - t0) : there;                    // of the batch row
+  const auto put = [&](int s, const float (&v)[VC]) {
+    const int64_t to = (at.row0 + t0 + s) * p.dim + c;
+    if (p.out_bf16) {
+      glr_store_bf16<VC>(p.y, to, left, v);
+    } else {
+      glr_store_f32<VC>(static_cast<float*>(p.y), to, left, v);
+    }
+  };
+  if (n <= 0 && k > 0) {  // behind the row's end: nothing here, and nobody waits for it
+    if (p.y != nullptr) {
+      const float zero[VC] = {};
+#pragma unroll
+      for (int i = 0; i < TS; ++i) {
+        if (slice * TS + i < there) put(slice * TS + i, zero);
+      }
+    }
+    return;
+  }
+
+  float a[TS][VC], b[TS][VC], P[VC], S[VC];
+  {
+    GlrRaw<BF16, GATED, TS> raw;
+    GlrParams<VC, GATED> par;
+    raw.load(p, at.row0 + t0, c, left, slice * TS, n, n == kGlrFwdSteps && at.c0 + kGlrChannels <= p.dim);
+    par.load(p, c, left);
+#pragma unroll
+    for (int v = 0; v < VC; ++v) P[v] = 1.0f, S[v] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+      const bool on = slice * TS + i < n;
+#pragma unroll
+      for (int v = 0; v < VC; ++v) {
+        const float la = par.A[v] * gate_value<ACT>(glr_elem<BF16>(raw.gate[i], v) + par.gbias[v]);
+        const float d = decay(la);
+        float in = glr_elem<BF16>(raw.x[i], v);
+        if constexpr (GATED) in *= sigmoid_f(glr_elem<BF16>(raw.igate[i], v) + par.ibias[v]);
+        a[i][v] = on ? d : 1.0f;
+        b[i][v] = on ? input_weight<SCALE>(la, d) * in : 0.0f;
+        P[v] *= a[i][v];
+        S[v] = fmaf(a[i][v], S[v], b[i][v]);
+      }
+    }
+  }
+
+  const int ch = c - at.c0;
+#pragma unroll
+  for (int v = 0; v < VC; ++v) lp[slice][ch + v] = P[v], ls[slice][ch + v] = S[v];
+  __syncthreads();
+  // 64 channels, four runs of slices
+  const int lane = threadIdx.x & 63, run = threadIdx.x >> 6;
+  float sp[kRun], ss[kRun];
+  float rP = 1.0f, rS = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    sp[i] = lp[run * kRun + i][lane], ss[i] = ls[run * kRun + i][lane];
+    rP *= sp[i];
+    rS = fmaf(sp[i], rS, ss[i]);
+  }
+  rp[run][lane] = rP, rs[run][lane] = rS;
+  __syncthreads();
+  if (run == 0) {
+    const int ce = at.c0 + lane;
+    float h = p.h0 != nullptr && ce < p.dim ? p.h0[static_cast<int64_t>(at.b) * p.dim + ce] : 0.0f;
+    if constexpr (CHAIN) {
+#pragma unroll
+      for (int r = 1; r < 4; ++r) {
+        rP *= rp[r][lane];
+        rS = fmaf(rp[r][lane], rS, rs[r][lane]);
+      }
+      h = glr_enter(chain, static_cast<uint32_t>(at.group), k, rP, rS, h);
+    }
+    enter[lane] = h;
+  }
+  __syncthreads();
+  float h = enter[lane];
+#pragma unroll
+  for (int r = 0; r < 3; ++r) {
+    if (r < run) h = fmaf(rp[r][lane], h, rs[r][lane]);
+  }
+  if (p.states != nullptr && run % 2 == 0 && run * kRun * TS < there && at.c0 + lane < p.dim) {
+    const int64_t tiles = (p.seqlen + kGlrBwdSteps - 1) / kGlrBwdSteps;
+    p.states[(at.b * tiles + t0 / kGlrBwdSteps + run / 2) * p.dim + at.c0 + lane] = h;
+  }
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    ls[run * kRun + i][lane] = h;
+    h = fmaf(sp[i], h, ss[i]);
+  }
+  if (run == 3 && p.h_final != nullptr && t0 + n == at.steps && at.c0 + lane < p.dim) {
+    p.h_final[static_cast<int64_t>(at.b) * p.dim + at.c0 + lane] = h;
+  }
+  __syncthreads();
+  if (p.y == nullptr) return;
+#pragma unroll
+  for (int v = 0; v < VC; ++v) S[v] = ls[slice][ch + v];
+#pragma unroll
+  for (int i = 0; i < TS; ++i) {
+    const int s = slice * TS + i;
+    float out[VC];
+#pragma unroll
+    for (int v = 0; v < VC; ++v) {
+      S[v] = fmaf(a[i][v], S[v], b[i][v]);
+      out[v] = s < n ? S[v] : 0.0f;
+    }
+    if (s < there) put(s, out);
+  }
+}
+
+template <bool BF16>
+void launch_glr_fwd(const GatedLinearArgs& a, const GlrChainPlan& plan, hipStream_t st) {
+  glr_by_form(a, [&](auto act, auto scale, auto gated) {
+    constexpr int ACT = decltype(act)::value, SCALE = decltype(scale)::value;
+    constexpr bool GATED = decltype(gated)::value;
+    if (plan.tiles > 1) {
+      launch_glr_clear(plan, a.workspace, st);
+      glr_fwd_kernel<BF16, ACT, SCALE, GATED, true>
+          <<<static_cast<unsigned>(plan.groups * plan.tiles), kGlrThreads, 0, st>>>(a, glr_chain(plan, a.workspace));
+    } else {
+      glr_fwd_kernel<BF16, ACT, SCALE, GATED, false>
+          <<<static_cast<unsigned>(plan.groups), kGlrThreads, 0, st>>>(a, GlrChain{});
+    }
+  });
+}
+
+}  // namespace ssm

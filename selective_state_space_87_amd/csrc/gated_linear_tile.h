@@ -1,0 +1,323 @@
+// Tiles of the gated linear recurrence (gfx950): 64 channels and a number of
+// steps, a block of 256 threads each, and the chain that joins the tiles of a
+// channel.
+//
+// A thread has VC adjacent channels, one 16-byte load of x or a gate (8 of
+// bfloat16, 4 of float32; at whatever boundary the row starts on), and TS
+// consecutive steps, a slice: consecutive lanes have consecutive channels, so a
+// load of a wave reads 8 (4) whole rows of the tile. All a tile's loads are
+// issued before the first is used.
+//
+// A recurrence h <- a h + b over some steps is the map h -> P h + S (P the product
+// of the a, S the result from 0), and maps join as (P2 P1, P2 S1 + S2). In the
+// tile slices are joined through LDS: 256 threads as 64 channels of 4 runs of
+// slices. Over the tiles there is the chain: every tile publishes its map, and
+// one in kGlrWindow the state behind it; a tile reads the last such state
+// before it and the maps from there on, all at once, and joins them in order.
+// So the input is read once, the joins are the same in every run (results are
+// deterministic), and the serial part is one exchange through memory every
+// kGlrWindow tiles.
+//
+// Waiting always ends. A block takes its tile by a ticket (an atomic count), and
+// tickets go along the chain: what a tile waits for is held by a block that
+// started earlier, which publishes its map before it waits, and its state after
+// waiting for earlier ones only; the first waits for nothing. A wait also
+// ends by itself, with NaN, after kGlrMostPolls tries (some seconds), should
+// two calls at once have been given the same workspace.
+//
+// Data travel in the words themselves (64 bits: the map or the state and a mark),
+// so no fence is needed: a word is either not there (all ones, as cleared
+// before the launch) or whole.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "gated_linear.h"
+
+namespace ssm {
+
+constexpr int kGlrThreads = 256;
+constexpr uint32_t kGlrMissing = 0xffffffffu;
+constexpr int kGlrMostPolls = 1 << 22;
+
+// ---- a thread's inputs of one step
+
+template <bool BF16>
+struct GlrLane {
+  static constexpr int VC = BF16 ? 8 : 4;                 // channels of a thread
+  static constexpr int kLanes = kGlrChannels / VC;        // threads over the channels
+  static constexpr int kSlices = kGlrThreads / kLanes;    // slices of a tile
+};
+
+typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes of channels from element `at` on, of which `left` are there (zeros for the others).
+template <bool BF16>
+__device__ __forceinline__ u32x4 glr_load(const void* base, int64_t at, int left) {
+  constexpr int VC = GlrLane<BF16>::VC;
+  u32x4 w = {0u, 0u, 0u, 0u};
+  if (left >= VC) {
+    if constexpr (BF16) {
+      w = *reinterpret_cast<const u32x4_2*>(static_cast<const uint16_t*>(base) + at);
+    } else {
+      w = *reinterpret_cast<const u32x4_4*>(static_cast<const uint32_t*>(base) + at);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < VC; ++c) {
+      if (c < left) {
+        const uint32_t e = load_bits<BF16>(base, at + c);
+        if constexpr (BF16) {
+          w[c / 2] |= e << (16 * (c & 1));
+        } else {
+          w[c] = e;
+        }
+      }
+    }
+  }
+  return w;
+}
+
+// The same where all of them are there.
+template <bool BF16>
+__device__ __forceinline__ u32x4 glr_load_whole(const void* base, int64_t at) {
+  if constexpr (BF16) {
+    return *reinterpret_cast<const u32x4_2*>(static_cast<const uint16_t*>(base) + at);
+  } else {
+    return *reinterpret_cast<const u32x4_4*>(static_cast<const uint32_t*>(base) + at);
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float glr_elem(const u32x4& w, int c) {
+  if constexpr (BF16) {
+    return __uint_as_float(c & 1 ? w[c / 2] & 0xffff0000u : w[c / 2] << 16);
+  } else {
+    return __uint_as_float(w[c]);
+  }
+}
+
+template <int VC>
+__device__ __forceinline__ void glr_load_f32(const float* base, int64_t at, int left, float (&v)[VC]) {
+#pragma unroll
+  for (int q = 0; q < VC / 4; ++q) {
+    const u32x4 w = glr_load<false>(base, at + 4 * q, left - 4 * q);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[4 * q + c] = __uint_as_float(w[c]);
+  }
+}
+
+template <int VC>
+__device__ __forceinline__ void glr_store_f32(float* base, int64_t at, int left, const float (&v)[VC]) {
+  if (left >= VC) {
+#pragma unroll
+    for (int q = 0; q < VC / 4; ++q) {
+      u32x4 w;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) w[c] = __float_as_uint(v[4 * q + c]);
+      *reinterpret_cast<u32x4_4*>(base + at + 4 * q) = w;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < VC; ++c) {
+      if (c < left) base[at + c] = v[c];
+    }
+  }
+}
+
+template <int VC>
+__device__ __forceinline__ void glr_store_bf16(void* base, int64_t at, int left, const float (&v)[VC]) {
+  uint16_t* p = static_cast<uint16_t*>(base) + at;
+  if (left >= VC) {
+#pragma unroll
+    for (int q = 0; q < VC / 4; ++q) {
+      typedef uint32_t u32x2_2 __attribute__((ext_vector_type(2), aligned(2)));
+      u32x2_2 w;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        w[c] = static_cast<uint32_t>(f32_to_bf16_bits(v[4 * q + 2 * c])) |
+               (static_cast<uint32_t>(f32_to_bf16_bits(v[4 * q + 2 * c + 1])) << 16);
+      }
+      *reinterpret_cast<u32x2_2*>(p + 4 * q) = w;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < VC; ++c) {
+      if (c < left) p[c] = f32_to_bf16_bits(v[c]);
+    }
+  }
+}
+
+// Inputs of a thread's slice, TS steps from tile step `s0` on, n steps of the
+// tile being there. A tile that is there whole is loaded without a branch, so
+// that all loads are on their way before the first is waited for.
+template <bool BF16, bool GATED, int TS>
+struct GlrRaw {
+  u32x4 x[TS], gate[TS], igate[GATED ? TS : 1];
+
+  __device__ __forceinline__ void load(const GatedLinearArgs& p, int64_t row, int c, int left, int s0, int n, bool whole) {
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < TS; ++i) {
+        gate[i] = glr_load_whole<BF16>(p.gate, (row + s0 + i) * p.gate_step + c);
+        x[i] = glr_load_whole<BF16>(p.x, (row + s0 + i) * p.x_step + c);
+        if constexpr (GATED) igate[i] = glr_load_whole<BF16>(p.igate, (row + s0 + i) * p.igate_step + c);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < TS; ++i) {
+        const int have = s0 + i < n ? left : 0;
+        gate[i] = glr_load<BF16>(p.gate, (row + s0 + i) * p.gate_step + c, have);
+        x[i] = glr_load<BF16>(p.x, (row + s0 + i) * p.x_step + c, have);
+        if constexpr (GATED) igate[i] = glr_load<BF16>(p.igate, (row + s0 + i) * p.igate_step + c, have);
+      }
+    }
+  }
+};
+
+// A thread's channels' parameters.
+template <int VC, bool GATED>
+struct GlrParams {
+  float A[VC], gbias[VC], ibias[VC];
+
+  __device__ __forceinline__ void load(const GatedLinearArgs& p, int c, int left) {
+    glr_load_f32<VC>(p.A, c, left, A);
+#pragma unroll
+    for (int v = 0; v < VC; ++v) gbias[v] = ibias[v] = 0.0f;
+    if (p.gbias != nullptr) glr_load_f32<VC>(p.gbias, c, left, gbias);
+    if (GATED && p.ibias != nullptr) glr_load_f32<VC>(p.ibias, c, left, ibias);
+  }
+};
+
+// ---- a tile's place
+
+struct GlrTile {
+  int64_t row0;   // first row of its batch row in [B L, ..]
+  int64_t steps;  // steps that the batch row has
+  int b, c0;      // batch row, first channel
+  int group;      // (batch row, 64 channels)
+};
+
+__device__ __forceinline__ GlrTile glr_tile(const GatedLinearArgs& p, uint32_t group) {
+  GlrTile t;
+  const uint32_t per_row = static_cast<uint32_t>((p.dim + kGlrChannels - 1) / kGlrChannels);
+  t.group = static_cast<int>(group);
+  t.b = static_cast<int>(group / per_row);
+  t.c0 = static_cast<int>(group % per_row) * kGlrChannels;
+  t.row0 = static_cast<int64_t>(t.b) * p.seqlen;
+  t.steps = gdr_row_steps(p.seqlens, t.b, p.seqlen);
+  return t;
+}
+
+// ---- the chain
+
+struct GlrChain {
+  uint32_t* tickets;
+  uint64_t* maps;     // [tile][group][64]: S, and P (never all ones) above
+  uint64_t* states;   // [window][group][64]: the state, and 0 above
+  uint32_t groups;
+};
+
+inline GlrChain glr_chain(const GlrChainPlan& p, void* workspace) {
+  char* w = static_cast<char*>(workspace);
+  return GlrChain{reinterpret_cast<uint32_t*>(w), reinterpret_cast<uint64_t*>(w + p.off_words),
+                  reinterpret_cast<uint64_t*>(w + p.off_states), static_cast<uint32_t>(p.groups)};
+}
+
+__device__ __forceinline__ uint64_t glr_word(float low, uint32_t high) {
+  return static_cast<uint64_t>(__float_as_uint(low)) | (static_cast<uint64_t>(high) << 32);
+}
+__device__ __forceinline__ void glr_put(uint64_t* at, uint64_t w) {
+  __hip_atomic_store(at, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t glr_get(const uint64_t* at) {
+  return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// One wave: the state that enters place `q` of the chain, given the map (P, S) of
+// the tile there and the state `start` that enters place 0. Lane l has channel l.
+__device__ __forceinline__ float glr_enter(const GlrChain& c, uint32_t group, uint32_t q, float P, float S, float start) {
+  const int lane = threadIdx.x & 63;
+  const auto at = [&](uint32_t place) {
+    return (static_cast<int64_t>(place) * c.groups + group) * kGlrChannels + lane;
+  };
+  uint32_t high = __float_as_uint(P);
+  if (high == kGlrMissing) high = 0x7fc00000u;  // one NaN for another
+  glr_put(c.maps + at(q), glr_word(S, high));
+  const uint32_t window = q / kGlrWindow, j = q % kGlrWindow;
+  uint64_t map[kGlrWindow - 1], state = 0;
+#pragma unroll
+  for (int i = 0; i < kGlrWindow - 1; ++i) map[i] = 0;
+  for (int tries = 0;; ++tries) {
+    bool missing = false;
+    if (window > 0) {
+      state = glr_get(c.states + at(window - 1));
+      missing |= static_cast<uint32_t>(state >> 32) == kGlrMissing;
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kGlrWindow - 1; ++i) {
+      if (i < j) {
+        map[i] = glr_get(c.maps + at(q - j + i));
+        missing |= static_cast<uint32_t>(map[i] >> 32) == kGlrMissing;
+      }
+    }
+    if (!__any(missing)) break;
+    if (tries == kGlrMostPolls) {
+      start = __uint_as_float(0x7fc00000u);
+      state = glr_word(start, 0);
+      break;
+    }
+    __builtin_amdgcn_s_sleep(1);
+  }
+  float h = window > 0 ? __uint_as_float(static_cast<uint32_t>(state)) : start;
+#pragma unroll
+  for (uint32_t i = 0; i < kGlrWindow - 1; ++i) {
+    if (i < j) h = fmaf(__uint_as_float(static_cast<uint32_t>(map[i] >> 32)), h, __uint_as_float(static_cast<uint32_t>(map[i])));
+  }
+  if (j == kGlrWindow - 1) glr_put(c.states + at(window), glr_word(fmaf(P, h, S), 0));
+  return h;
+}
+
+// The block's ticket.
+__device__ __forceinline__ uint32_t glr_ticket(const GlrChain& c, uint32_t* slot) {
+  if (threadIdx.x == 0) *slot = atomicAdd(c.tickets, 1u);
+  __syncthreads();
+  return *slot;
+}
+
+// Clears a chain's words to "not there" and its count to 0 (a kernel, not a memset: graphs take it).
+void launch_glr_clear(const GlrChainPlan& p, void* workspace, hipStream_t st);
+
+// f(act, scale, with an input gate) as compile-time constants.
+template <typename F>
+void glr_by_form(const GatedLinearArgs& p, F&& f) {
+  using std::integral_constant;
+  const auto gated = [&](auto act, auto scale) {
+    p.igate != nullptr ? f(act, scale, std::true_type{}) : f(act, scale, std::false_type{});
+  };
+  const auto scale = [&](auto act) {
+    if (p.scale == kInputNorm) {
+      gated(act, integral_constant<int, kInputNorm>{});
+    } else if (p.scale == kInputComplement) {
+      gated(act, integral_constant<int, kInputComplement>{});
+    } else {
+      gated(act, integral_constant<int, kInputPlain>{});
+    }
+  };
+  if (p.act == kGateSigmoid) {
+    scale(integral_constant<int, kGateSigmoid>{});
+  } else if (p.act == kGateSoftplus) {
+    scale(integral_constant<int, kGateSoftplus>{});
+  } else {
+    scale(integral_constant<int, kGateRaw>{});
+  }
+}
+
+template <bool BF16>
+void launch_glr_fwd(const GatedLinearArgs& a, const GlrChainPlan& plan, hipStream_t st);
+template <bool BF16>
+void launch_glr_bwd(const GatedLinearBwdArgs& a, const GlrBwdPlan& plan, hipStream_t st);
+
+}  // namespace ssm
