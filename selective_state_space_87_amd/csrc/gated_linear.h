@@ -14,67 +14,84 @@
 
 namespace ssm {
 
-// 1 - e^la, given a = e^la. Near 0 the difference would cancel: the Taylor series
-// of (e^x - 1) / x to x^5 is taken up to |x| = 1/4 (the first dropped term,
-// x^6 / 5040, is below 2^-24 there); beyond, 1 - a is off by 2^-24 / 0.22 at most.
-__device__ __forceinline__ float one_minus_decay(float la, float a) {
-  const float s = fmaf(fmaf(fmaf(fmaf(fmaf(la, 1.0f / 720.0f, 1.0f / 120.0f), la, 1.0f / 24.0f), la, 1.0f / 6.0f), la,
-                            0.5f), la, 1.0f);
-  return fabsf(la) < 0.25f ? -la * s : 1.0f - a;
+// The exponents are taken in base 2 and the parameters come scaled: A2 = A log2(e),
+// and for a sigmoid the bias as -bias log2(e), so that its exponent is one fused
+// product and sum. That exponent's rounding, and the bias's, are 2^-24 (|u| + |bias|) of
+// e^-u, and so of a gate far down the sigmoid: the two instructions a gate that
+// a compensated exponent takes more (of 30 an element) would cost 15% of the
+// forward's time for it.
+
+// 1 - 2^t for t <= 0, given a = 2^t. Near 0 the difference would cancel: the Taylor
+// series of (e^x - 1) / x to x^5, x = t ln 2, is taken up to |x| = 1/4 (the first
+// dropped term, x^6 / 5040, is below 2^-24 there); beyond, `far` is off by some
+// 2^-24 / 0.22.
+__device__ __forceinline__ float one_minus_exp2(float t, float far) {
+  constexpr float l = kLn2, l2 = l * l, l3 = l2 * l, l4 = l3 * l, l5 = l4 * l, l6 = l5 * l;
+  const float s = fmaf(fmaf(fmaf(fmaf(fmaf(t, -l6 / 720.0f, -l5 / 120.0f), t, -l4 / 24.0f), t, -l3 / 6.0f), t,
+                            -l2 / 2.0f), t, -l);
+  return fabsf(t) < 0.25f * kLog2e ? t * s : far;
 }
 
-// sigmoid(u) and its derivative sigmoid(u) sigmoid(-u), from one exponential.
-// (s (1 - s) would lose what is left of the derivative where s is near 1.)
-__device__ __forceinline__ float sigmoid_slope(float u, float* slope) {
-  const float v = exp_minus_abs(u), r = rcp_hw(1.0f + v);
-  *slope = v * r * r;
-  return u < 0.0f ? v * r : r;
+// sigmoid(x + bias), given -bias log2(e). (e is infinite below -88: 0.)
+__device__ __forceinline__ float glr_sigmoid(float x, float nb) { return rcp_hw(1.0f + exp2_hw(fmaf(x, -kLog2e, nb))); }
+
+// The same with its derivative s (1 - s) = e s^2, which keeps what is left of it
+// where s is near 1. (The exponent ends at 126: 0 times infinity would be NaN.)
+__device__ __forceinline__ float glr_sigmoid_slope(float x, float nb, float* slope) {
+  float t = fmaf(x, -kLog2e, nb);
+  t = t > 126.0f ? 126.0f : t;
+  const float e = exp2_hw(t), r = rcp_hw(1.0f + e);
+  *slope = e * r * r;
+  return r;
 }
 
+// max(u, 0) + log1p(v), v = e^-|u|, as in softplus_f; the slope is sigmoid(u).
+__device__ __forceinline__ float glr_softplus(float u, float* slope) {
+  const float v = exp2_hw(-fabsf(u) * kLog2e), w = 1.0f + v;
+  if (slope != nullptr) *slope = (u < 0.0f ? v : 1.0f) * rcp_hw(w);
+  return fmaxf(u, 0.0f) + fmaf(log2_hw(w), kLn2, v - (w - 1.0f));
+}
+
+// Value of the gate (and its derivative) given its raw value and the scaled bias.
 template <int ACT>
-__device__ __forceinline__ float gate_value(float u) {
+__device__ __forceinline__ float gate_value(float x, float bias) {
   if constexpr (ACT == kGateSoftplus) {
-    return gdr_softplus(u);
+    return glr_softplus(x + bias, nullptr);
   } else if constexpr (ACT == kGateSigmoid) {
-    return sigmoid_f(u);
+    return glr_sigmoid(x, bias);
   } else {
-    return u;
+    return x + bias;
   }
 }
-
-// The same with the gate's derivative.
 template <int ACT>
-__device__ __forceinline__ float gate_value_slope(float u, float* slope) {
+__device__ __forceinline__ float gate_value_slope(float x, float bias, float* slope) {
   if constexpr (ACT == kGateSoftplus) {
-    const float v = exp_minus_abs(u), w = 1.0f + v, r = rcp_hw(w);
-    *slope = u < 0.0f ? v * r : r;
-    return fmaxf(u, 0.0f) + fmaf(log2_hw(w), kLn2, v - (w - 1.0f));
+    return glr_softplus(x + bias, slope);
   } else if constexpr (ACT == kGateSigmoid) {
-    return sigmoid_slope(u, slope);
+    return glr_sigmoid_slope(x, bias, slope);
   } else {
     *slope = 1.0f;
-    return u;
+    return x + bias;
   }
 }
 
-__device__ __forceinline__ float decay(float la) { return exp2_hw(la * kLog2e); }
-
+// Weight of the input, given t = log2(a) and a. sqrt(1 - a^2): 1 - 2^(2t).
 template <int SCALE>
-__device__ __forceinline__ float input_weight(float la, float a) {
+__device__ __forceinline__ float input_weight(float t, float a) {
   if constexpr (SCALE == kInputNorm) {
-    return __builtin_amdgcn_sqrtf(one_minus_decay(la, a) * (1.0f + a));  // 1 - a^2
+    return __builtin_amdgcn_sqrtf(one_minus_exp2(2.0f * t, fmaf(-a, a, 1.0f)));
   } else if constexpr (SCALE == kInputComplement) {
-    return one_minus_decay(la, a);
+    return one_minus_exp2(t, 1.0f - a);
   } else {
     return 1.0f;
   }
 }
 
-// dw / d la. Where a is 1 the square root has no derivative: 0 is taken.
+// dw / d(ln a). Where a is 1 the square root has no derivative: 0 is taken.
 template <int SCALE>
 __device__ __forceinline__ float input_weight_slope(float a, float w) {
   if constexpr (SCALE == kInputNorm) {
-    return w != 0.0f ? -a * a / w : 0.0f;
+    return w != 0.0f ? -a * a * rcp_hw(w) : 0.0f;
   } else if constexpr (SCALE == kInputComplement) {
     return -a;
   } else {

@@ -19,7 +19,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_walk_kernel(const GatedLinear
   const int64_t b = i / per_row;
   const int c = static_cast<int>(i - b * per_row) * VC, left = static_cast<int>(p.dim) - c;
   const int64_t steps = gdr_row_steps(p.seqlens, static_cast<int>(b), p.seqlen);
-  GlrParams<VC, GATED> par;
+  GlrParams<VC, ACT, GATED> par;
   GlrRaw<BF16, GATED, 1> raw;
   if (steps > 0) raw.load(p, b * p.seqlen, c, left, 0, 1, left >= VC);
   par.load(p, c, left);
@@ -31,15 +31,10 @@ __global__ __launch_bounds__(kGlrThreads) void glr_walk_kernel(const GatedLinear
     if (t < steps) {
       const GlrRaw<BF16, GATED, 1> now = raw;
       if (t + 1 < steps) raw.load(p, b * p.seqlen + t + 1, c, left, 0, 1, left >= VC);
+      float a[1][VC], in[1][VC];
+      glr_elements<BF16, ACT, SCALE, GATED, 1, VC>(now, par, a, in);
 #pragma unroll
-      for (int v = 0; v < VC; ++v) {
-        const float la = par.A[v] * gate_value<ACT>(glr_elem<BF16>(now.gate[0], v) + par.gbias[v]);
-        const float a = decay(la);
-        float in = glr_elem<BF16>(now.x[0], v);
-        if constexpr (GATED) in *= sigmoid_f(glr_elem<BF16>(now.igate[0], v) + par.ibias[v]);
-        h[v] = fmaf(a, h[v], input_weight<SCALE>(la, a) * in);
-        y[v] = h[v];
-      }
+      for (int v = 0; v < VC; ++v) y[v] = h[v] = fmaf(a[0][v], h[v], in[0][v]);
     }
     if (p.y != nullptr) {
       const int64_t to = (b * p.seqlen + t) * p.dim + c;

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
   }
 
   GlrRaw<BF16, GATED, TS> raw;
-  GlrParams<VC, GATED> par;
+  GlrParams<VC, ACT, GATED> par;
   float dy[TS][VC], a[TS][VC], b[TS][VC];
   const bool whole = n == kGlrBwdSteps && at.c0 + kGlrChannels <= p.dim;
   raw.load(p, at.row0 + t0, c, left, slice * TS, n, whole);
@@ -78,23 +78,14 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
   }
   par.load(p, c, left);
   {
+    glr_elements<BF16, ACT, SCALE, GATED, TS, VC>(raw, par, a, b);
+    if (!whole) glr_mask<TS, VC>(slice * TS, n, a, b);
     float P[VC], S[VC], R[VC];
 #pragma unroll
-    for (int v = 0; v < VC; ++v) P[v] = 1.0f, S[v] = R[v] = 0.0f;
+    for (int v = 0; v < VC; ++v) {
+      P[v] = 1.0f, S[v] = R[v] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < TS; ++i) {
-      const bool on = slice * TS + i < n;
-#pragma unroll
-      for (int v = 0; v < VC; ++v) {
-        const float la = par.A[v] * gate_value<ACT>(glr_elem<BF16>(raw.gate[i], v) + par.gbias[v]);
-        const float d = decay(la);
-        float in = glr_elem<BF16>(raw.x[i], v);
-        if constexpr (GATED) in *= sigmoid_f(glr_elem<BF16>(raw.igate[i], v) + par.ibias[v]);
-        a[i][v] = on ? d : 1.0f;
-        b[i][v] = on ? input_weight<SCALE>(la, d) * in : 0.0f;
-        P[v] *= a[i][v];
-        S[v] = fmaf(a[i][v], S[v], b[i][v]);
-      }
+      for (int i = 0; i < TS; ++i) P[v] *= a[i][v], S[v] = fmaf(a[i][v], S[v], b[i][v]);
     }
 #pragma unroll
     for (int i = TS - 1; i >= 0; --i) {
@@ -179,14 +170,14 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
     for (int v = 0; v < VC; ++v) {
       const float D = dy[i][v] + E[v];
       float slope, islope = 0.0f, in = glr_elem<BF16>(raw.x[i], v), sig = 1.0f;
-      const float g = gate_value_slope<ACT>(glr_elem<BF16>(raw.gate[i], v) + par.gbias[v], &slope);
-      const float w = input_weight<SCALE>(par.A[v] * g, a[i][v]);
+      const float g = gate_value_slope<ACT>(glr_elem<BF16>(raw.gate[i], v), par.gbias[v], &slope);
+      const float w = input_weight<SCALE>(par.A2[v] * g, a[i][v]);
       const float dv = on ? w * D : 0.0f;
-      if constexpr (GATED) sig = sigmoid_slope(glr_elem<BF16>(raw.igate[i], v) + par.ibias[v], &islope);
+      if constexpr (GATED) sig = glr_sigmoid_slope(glr_elem<BF16>(raw.igate[i], v), par.ibias[v], &islope);
       dx[v] = dv * sig;
       di[v] = dv * in * islope;
       const float dla = on ? D * fmaf(a[i][v], before[i][v], input_weight_slope<SCALE>(a[i][v], w) * (in * sig)) : 0.0f;
-      dg[v] = dla * par.A[v] * slope;
+      dg[v] = dla * (par.A2[v] * kLn2) * slope;
       sumA[v] = fmaf(dla, g, sumA[v]);
       sumg[v] += dg[v];
       sumi[v] += di[v];

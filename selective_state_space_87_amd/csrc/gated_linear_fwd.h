@@ -23,12 +23,12 @@ __global__ __launch_bounds__(kGlrThreads) void glr_fwd_kernel(const GatedLinearA
   const int left = static_cast<int>(p.dim) - c;
   const int there = p.seqlen - t0 < kGlrFwdSteps ? static_cast<int>(p.seqlen - t0) : kGlrFwdSteps;  // steps of the array
   const int n = at.steps - t0 < there ? static_cast<int>(at.steps - t0) : there;                    // of the batch row
-  const auto put = [&](int s, const float (&v)[VC]) {
+  const auto put = [&](int s, int wide, const float (&v)[VC]) __attribute__((always_inline)) {
     const int64_t to = (at.row0 + t0 + s) * p.dim + c;
     if (p.out_bf16) {
-      glr_store_bf16<VC>(p.y, to, left, v);
+      glr_store_bf16<VC>(p.y, to, wide, v);
     } else {
-      glr_store_f32<VC>(static_cast<float*>(p.y), to, left, v);
+      glr_store_f32<VC>(static_cast<float*>(p.y), to, wide, v);
     }
   };
   if (n <= 0 && k > 0) {  // behind the row's end: nothing here, and nobody waits for it
@@ -36,35 +36,27 @@ __global__ __launch_bounds__(kGlrThreads) void glr_fwd_kernel(const GatedLinearA
       const float zero[VC] = {};
 #pragma unroll
       for (int i = 0; i < TS; ++i) {
-        if (slice * TS + i < there) put(slice * TS + i, zero);
+        if (slice * TS + i < there) put(slice * TS + i, left, zero);
       }
     }
     return;
   }
 
   float a[TS][VC], b[TS][VC], P[VC], S[VC];
+  const bool whole = n == kGlrFwdSteps && at.c0 + kGlrChannels <= p.dim;
   {
     GlrRaw<BF16, GATED, TS> raw;
-    GlrParams<VC, GATED> par;
-    raw.load(p, at.row0 + t0, c, left, slice * TS, n, n == kGlrFwdSteps && at.c0 + kGlrChannels <= p.dim);
+    GlrParams<VC, ACT, GATED> par;
+    raw.load(p, at.row0 + t0, c, left, slice * TS, n, whole);
     par.load(p, c, left);
+    glr_elements<BF16, ACT, SCALE, GATED, TS, VC>(raw, par, a, b);
+  }
+  if (!whole) glr_mask<TS, VC>(slice * TS, n, a, b);
 #pragma unroll
-    for (int v = 0; v < VC; ++v) P[v] = 1.0f, S[v] = 0.0f;
+  for (int v = 0; v < VC; ++v) {
+    P[v] = 1.0f, S[v] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < TS; ++i) {
-      const bool on = slice * TS + i < n;
-#pragma unroll
-      for (int v = 0; v < VC; ++v) {
-        const float la = par.A[v] * gate_value<ACT>(glr_elem<BF16>(raw.gate[i], v) + par.gbias[v]);
-        const float d = decay(la);
-        float in = glr_elem<BF16>(raw.x[i], v);
-        if constexpr (GATED) in *= sigmoid_f(glr_elem<BF16>(raw.igate[i], v) + par.ibias[v]);
-        a[i][v] = on ? d : 1.0f;
-        b[i][v] = on ? input_weight<SCALE>(la, d) * in : 0.0f;
-        P[v] *= a[i][v];
-        S[v] = fmaf(a[i][v], S[v], b[i][v]);
-      }
-    }
+    for (int i = 0; i < TS; ++i) P[v] *= a[i][v], S[v] = fmaf(a[i][v], S[v], b[i][v]);
   }
 
   const int ch = c - at.c0;
@@ -118,16 +110,25 @@ __global__ __launch_bounds__(kGlrThreads) void glr_fwd_kernel(const GatedLinearA
   if (p.y == nullptr) return;
 #pragma unroll
   for (int v = 0; v < VC; ++v) S[v] = ls[slice][ch + v];
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < TS; ++i) {
-    const int s = slice * TS + i;
-    float out[VC];
+    for (int i = 0; i < TS; ++i) {
 #pragma unroll
-    for (int v = 0; v < VC; ++v) {
-      S[v] = fmaf(a[i][v], S[v], b[i][v]);
-      out[v] = s < n ? S[v] : 0.0f;
+      for (int v = 0; v < VC; ++v) S[v] = fmaf(a[i][v], S[v], b[i][v]);
+      put(slice * TS + i, VC, S);
     }
-    if (s < there) put(s, out);
+  } else {
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+      const int s = slice * TS + i;
+      float out[VC];
+#pragma unroll
+      for (int v = 0; v < VC; ++v) {
+        S[v] = fmaf(a[i][v], S[v], b[i][v]);
+        out[v] = s < n ? S[v] : 0.0f;
+      }
+      if (s < there) put(s, left, out);
+    }
   }
 }
 

@@ -177,19 +177,56 @@ struct GlrRaw {
   }
 };
 
-// A thread's channels' parameters.
-template <int VC, bool GATED>
+// A thread's channels' parameters, scaled as gated_linear.h takes them.
+template <int VC, int ACT, bool GATED>
 struct GlrParams {
-  float A[VC], gbias[VC], ibias[VC];
+  float A2[VC], gbias[VC], ibias[VC];
 
   __device__ __forceinline__ void load(const GatedLinearArgs& p, int c, int left) {
-    glr_load_f32<VC>(p.A, c, left, A);
+    glr_load_f32<VC>(p.A, c, left, A2);
 #pragma unroll
-    for (int v = 0; v < VC; ++v) gbias[v] = ibias[v] = 0.0f;
-    if (p.gbias != nullptr) glr_load_f32<VC>(p.gbias, c, left, gbias);
-    if (GATED && p.ibias != nullptr) glr_load_f32<VC>(p.ibias, c, left, ibias);
+    for (int v = 0; v < VC; ++v) A2[v] *= kLog2e, gbias[v] = ibias[v] = 0.0f;
+    if (p.gbias != nullptr) {
+      glr_load_f32<VC>(p.gbias, c, left, gbias);
+      if constexpr (ACT == kGateSigmoid) {
+#pragma unroll
+        for (int v = 0; v < VC; ++v) gbias[v] *= -kLog2e;
+      }
+    }
+    if (GATED && p.ibias != nullptr) {
+      glr_load_f32<VC>(p.ibias, c, left, ibias);
+#pragma unroll
+      for (int v = 0; v < VC; ++v) ibias[v] *= -kLog2e;
+    }
   }
 };
+
+// Decays a and inputs b of a slice. (Steps that are not there: see glr_mask.)
+template <bool BF16, int ACT, int SCALE, bool GATED, int TS, int VC>
+__device__ __forceinline__ void glr_elements(const GlrRaw<BF16, GATED, TS>& raw, const GlrParams<VC, ACT, GATED>& par,
+                                             float (&a)[TS][VC], float (&b)[TS][VC]) {
+#pragma unroll
+  for (int i = 0; i < TS; ++i) {
+#pragma unroll
+    for (int v = 0; v < VC; ++v) {
+      const float t = par.A2[v] * gate_value<ACT>(glr_elem<BF16>(raw.gate[i], v), par.gbias[v]);
+      a[i][v] = exp2_hw(t);
+      b[i][v] = glr_elem<BF16>(raw.x[i], v) * input_weight<SCALE>(t, a[i][v]);
+      if constexpr (GATED) b[i][v] *= glr_sigmoid(glr_elem<BF16>(raw.igate[i], v), par.ibias[v]);
+    }
+  }
+}
+
+// Steps from the n-th of the tile on leave the state: decay 1, input 0.
+template <int TS, int VC>
+__device__ __forceinline__ void glr_mask(int s0, int n, float (&a)[TS][VC], float (&b)[TS][VC]) {
+#pragma unroll
+  for (int i = 0; i < TS; ++i) {
+    const bool on = s0 + i < n;
+#pragma unroll
+    for (int v = 0; v < VC; ++v) a[i][v] = on ? a[i][v] : 1.0f, b[i][v] = on ? b[i][v] : 0.0f;
+  }
+}
 
 // ---- a tile's place
 
