@@ -9,10 +9,12 @@ namespace ssm {
 
 namespace {
 
+constexpr int walk_channels(bool bf16) { return bf16 ? 8 : 4; }
+
 // A thread walks VC channels of a batch row.
 template <bool BF16, int ACT, int SCALE, bool GATED>
 __global__ __launch_bounds__(kGlrThreads) void glr_walk_kernel(const GatedLinearArgs p) {
-  constexpr int VC = GlrLane<BF16>::VC;
+  constexpr int VC = walk_channels(BF16);
   const int64_t per_row = (p.dim + VC - 1) / VC;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kGlrThreads + threadIdx.x;
   if (i >= p.batch * per_row) return;
@@ -20,16 +22,16 @@ __global__ __launch_bounds__(kGlrThreads) void glr_walk_kernel(const GatedLinear
   const int c = static_cast<int>(i - b * per_row) * VC, left = static_cast<int>(p.dim) - c;
   const int64_t steps = gdr_row_steps(p.seqlens, static_cast<int>(b), p.seqlen);
   GlrParams<VC, ACT, GATED> par;
-  GlrRaw<BF16, GATED, 1> raw;
+  GlrRaw<BF16, GATED, VC, 1> raw;
   if (steps > 0) raw.load(p, b * p.seqlen, c, left, 0, 1, left >= VC);
   par.load(p, c, left);
   float h[VC] = {};
   if (p.h0 != nullptr) glr_load_f32<VC>(p.h0, b * p.dim + c, left, h);
-  if (p.states != nullptr && p.seqlen > 0) glr_store_f32<VC>(p.states, b * p.dim + c, left, h);
+  if (p.states != nullptr && p.seqlen > 0) glr_store<false, VC>(p.states, b * p.dim + c, left, h);
   for (int64_t t = 0; t < p.seqlen; ++t) {
     float y[VC] = {};
     if (t < steps) {
-      const GlrRaw<BF16, GATED, 1> now = raw;
+      const GlrRaw<BF16, GATED, VC, 1> now = raw;
       if (t + 1 < steps) raw.load(p, b * p.seqlen + t + 1, c, left, 0, 1, left >= VC);
       float a[1][VC], in[1][VC];
       glr_elements<BF16, ACT, SCALE, GATED, 1, VC>(now, par, a, in);
@@ -39,18 +41,18 @@ __global__ __launch_bounds__(kGlrThreads) void glr_walk_kernel(const GatedLinear
     if (p.y != nullptr) {
       const int64_t to = (b * p.seqlen + t) * p.dim + c;
       if (p.out_bf16) {
-        glr_store_bf16<VC>(p.y, to, left, y);
+        glr_store<true, VC>(p.y, to, left, y);
       } else {
-        glr_store_f32<VC>(static_cast<float*>(p.y), to, left, y);
+        glr_store<false, VC>(p.y, to, left, y);
       }
     }
   }
-  if (p.h_final != nullptr) glr_store_f32<VC>(p.h_final, b * p.dim + c, left, h);
+  if (p.h_final != nullptr) glr_store<false, VC>(p.h_final, b * p.dim + c, left, h);
 }
 
 template <bool BF16>
 void launch_walk(const GatedLinearArgs& a, hipStream_t st) {
-  const int64_t threads = a.batch * ((a.dim + GlrLane<BF16>::VC - 1) / GlrLane<BF16>::VC);
+  const int64_t threads = a.batch * ((a.dim + walk_channels(BF16) - 1) / walk_channels(BF16));
   const unsigned blocks = static_cast<unsigned>((threads + kGlrThreads - 1) / kGlrThreads);
   glr_by_form(a, [&](auto act, auto scale, auto gated) {
     glr_walk_kernel<BF16, decltype(act)::value, decltype(scale)::value, decltype(gated)::value>
@@ -58,11 +60,11 @@ void launch_walk(const GatedLinearArgs& a, hipStream_t st) {
   });
 }
 
-__global__ __launch_bounds__(kGlrThreads) void glr_clear_kernel(u32x4* words, int64_t n) {
+__global__ __launch_bounds__(kGlrThreads) void glr_clear_kernel(uint4* words, int64_t n) {
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGlrThreads;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kGlrThreads + threadIdx.x; i < n; i += step) {
     const uint32_t v = i < 16 ? 0u : kGlrMissing;  // the count's 256 bytes, then the words
-    words[i] = u32x4{v, v, v, v};
+    words[i] = make_uint4(v, v, v, v);
   }
 }
 
@@ -105,7 +107,7 @@ void launch_glr_clear(const GlrChainPlan& p, void* workspace, hipStream_t st) {
   const int64_t n = static_cast<int64_t>(p.bytes / 16);
   const int64_t blocks = (n + kGlrThreads - 1) / kGlrThreads;
   glr_clear_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), kGlrThreads, 0, st>>>(
-      static_cast<u32x4*>(workspace), n);
+      static_cast<uint4*>(workspace), n);
 }
 
 int launch_gated_linear(const GatedLinearArgs& a, void* stream) {

@@ -18,10 +18,11 @@ namespace ssm {
 template <bool BF16, int ACT, int SCALE, bool GATED, bool CHAIN>
 __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearBwdArgs q, const GlrChain chain,
                                                               const uint32_t tiles, float* parts) {
-  using Lane = GlrLane<BF16>;
-  constexpr int VC = Lane::VC, SL = Lane::kSlices, TS = kGlrBwdSteps / SL, kRun = SL / 4;
+  constexpr int VC = 4;
+  using Shape = GlrShape<VC, kGlrBwdSteps>;
+  constexpr int SL = Shape::kSlices, TS = Shape::kSteps, kRun = Shape::kRun;
   __shared__ __attribute__((aligned(16))) float lp[SL][kGlrChannels], ls[SL][kGlrChannels], lr[SL][kGlrChannels];
-  __shared__ float rp[4][kGlrChannels], rs[4][kGlrChannels], rr[4][kGlrChannels];
+  __shared__ float rp[kGlrRuns][kGlrChannels], rs[kGlrRuns][kGlrChannels], rr[kGlrRuns][kGlrChannels];
   __shared__ float enter_h[kGlrChannels], enter_e[kGlrChannels];
   __shared__ uint32_t slot;
   const GatedLinearArgs& p = q.f;
@@ -31,12 +32,12 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
   const uint32_t k = CHAIN ? tiles - 1 - place : 0;
   const GlrTile at = glr_tile(p, CHAIN ? tile - place * chain.groups : tile);
   const int64_t t0 = static_cast<int64_t>(k) * kGlrBwdSteps;
-  const int slice = threadIdx.x / Lane::kLanes;
-  const int ch = static_cast<int>(threadIdx.x % Lane::kLanes) * VC, c = at.c0 + ch;
+  const int slice = threadIdx.x / Shape::kLanes;
+  const int ch = static_cast<int>(threadIdx.x % Shape::kLanes) * VC, c = at.c0 + ch;
   const int left = static_cast<int>(p.dim) - c;
   const int there = p.seqlen - t0 < kGlrBwdSteps ? static_cast<int>(p.seqlen - t0) : kGlrBwdSteps;
   const int n = at.steps - t0 < there ? static_cast<int>(at.steps - t0) : there;
-  const int lane = threadIdx.x & 63, run = threadIdx.x >> 6, ce = at.c0 + lane;
+  const int lane = threadIdx.x % kGlrChannels, run = threadIdx.x / kGlrChannels, ce = at.c0 + lane;
   float* part = parts + (static_cast<int64_t>(at.b) * tiles + k) * 3 * p.dim;
   if (n <= 0) {  // behind the row's end: gradients of 0, and nobody waits for it
     const float zero[VC] = {};
@@ -44,9 +45,9 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
     for (int i = 0; i < TS; ++i) {
       const int64_t to = (at.row0 + t0 + slice * TS + i) * p.dim + c;
       if (slice * TS + i < there) {
-        glr_store_f32<VC>(q.dx, to, left, zero);
-        glr_store_f32<VC>(q.dgate, to, left, zero);
-        if constexpr (GATED) glr_store_f32<VC>(q.digate, to, left, zero);
+        glr_store<false, VC>(q.dx, to, left, zero);
+        glr_store<false, VC>(q.dgate, to, left, zero);
+        if constexpr (GATED) glr_store<false, VC>(q.digate, to, left, zero);
       }
     }
     if (run == 0 && ce < p.dim) {
@@ -57,23 +58,25 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
     return;
   }
 
-  GlrRaw<BF16, GATED, TS> raw;
+  GlrRaw<BF16, GATED, VC, TS> raw;
   GlrParams<VC, ACT, GATED> par;
   float dy[TS][VC], a[TS][VC], b[TS][VC];
   const bool whole = n == kGlrBwdSteps && at.c0 + kGlrChannels <= p.dim;
   raw.load(p, at.row0 + t0, c, left, slice * TS, n, whole);
-#pragma unroll
-  for (int i = 0; i < TS; ++i) {
-    const int64_t from = (at.row0 + t0 + slice * TS + i) * p.dim + c;
+  {
+    const int64_t from = (at.row0 + t0 + slice * TS) * p.dim + c;
+    typename GlrPack<false, VC>::Words d[TS];
     if (whole) {
 #pragma unroll
-      for (int w = 0; w < VC / 4; ++w) {
-        const u32x4 d = glr_load_whole<false>(q.dy, from + 4 * w);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) dy[i][4 * w + v] = __uint_as_float(d[v]);
-      }
+      for (int i = 0; i < TS; ++i) d[i] = glr_load<false, VC>(q.dy, from + i * p.dim, VC);
     } else {
-      glr_load_f32<VC>(q.dy, from, slice * TS + i < n ? left : 0, dy[i]);
+#pragma unroll
+      for (int i = 0; i < TS; ++i) d[i] = glr_load<false, VC>(q.dy, from + i * p.dim, slice * TS + i < n ? left : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+#pragma unroll
+      for (int v = 0; v < VC; ++v) dy[i][v] = __uint_as_float(d[i][v]);
     }
   }
   par.load(p, c, left);
@@ -185,9 +188,9 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
     }
     if (s < there) {
       const int64_t to = (at.row0 + t0 + s) * p.dim + c;
-      glr_store_f32<VC>(q.dx, to, left, dx);
-      glr_store_f32<VC>(q.dgate, to, left, dg);
-      if constexpr (GATED) glr_store_f32<VC>(q.digate, to, left, di);
+      glr_store<false, VC>(q.dx, to, left, dx);
+      glr_store<false, VC>(q.dgate, to, left, dg);
+      if constexpr (GATED) glr_store<false, VC>(q.digate, to, left, di);
     }
   }
   __syncthreads();  // ls and lr have been read

@@ -7,28 +7,29 @@
 namespace ssm {
 
 template <bool BF16, int ACT, int SCALE, bool GATED, bool CHAIN>
-__global__ __launch_bounds__(kGlrThreads) void glr_fwd_kernel(const GatedLinearArgs p, const GlrChain chain) {
-  using Lane = GlrLane<BF16>;
-  constexpr int VC = Lane::VC, SL = Lane::kSlices, TS = kGlrFwdSteps / SL, kRun = SL / 4;
+__global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(const GatedLinearArgs p, const GlrChain chain) {
+  constexpr int VC = BF16 ? 8 : 4;
+  using Shape = GlrShape<VC, kGlrFwdSteps>;
+  constexpr int SL = Shape::kSlices, TS = Shape::kSteps, kRun = Shape::kRun;
   __shared__ __attribute__((aligned(16))) float lp[SL][kGlrChannels], ls[SL][kGlrChannels];
-  __shared__ float rp[4][kGlrChannels], rs[4][kGlrChannels], enter[kGlrChannels];
+  __shared__ float rp[kGlrRuns][kGlrChannels], rs[kGlrRuns][kGlrChannels], enter[kGlrChannels];
   __shared__ uint32_t slot;
   uint32_t tile = blockIdx.x;
   if constexpr (CHAIN) tile = glr_ticket(chain, &slot);
   const uint32_t k = CHAIN ? tile / chain.groups : 0;
   const GlrTile at = glr_tile(p, CHAIN ? tile - k * chain.groups : tile);
   const int64_t t0 = static_cast<int64_t>(k) * kGlrFwdSteps;
-  const int slice = threadIdx.x / Lane::kLanes;
-  const int c = at.c0 + static_cast<int>(threadIdx.x % Lane::kLanes) * VC;
+  const int slice = threadIdx.x / Shape::kLanes;
+  const int c = at.c0 + static_cast<int>(threadIdx.x % Shape::kLanes) * VC;
   const int left = static_cast<int>(p.dim) - c;
   const int there = p.seqlen - t0 < kGlrFwdSteps ? static_cast<int>(p.seqlen - t0) : kGlrFwdSteps;  // steps of the array
   const int n = at.steps - t0 < there ? static_cast<int>(at.steps - t0) : there;                    // of the batch row
   const auto put = [&](int s, int wide, const float (&v)[VC]) __attribute__((always_inline)) {
     const int64_t to = (at.row0 + t0 + s) * p.dim + c;
     if (p.out_bf16) {
-      glr_store_bf16<VC>(p.y, to, wide, v);
+      glr_store<true, VC>(p.y, to, wide, v);
     } else {
-      glr_store_f32<VC>(static_cast<float*>(p.y), to, wide, v);
+      glr_store<false, VC>(p.y, to, wide, v);
     }
   };
   if (n <= 0 && k > 0) {  // behind the row's end: nothing here, and nobody waits for it
@@ -45,7 +46,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_fwd_kernel(const GatedLinearA
   float a[TS][VC], b[TS][VC], P[VC], S[VC];
   const bool whole = n == kGlrFwdSteps && at.c0 + kGlrChannels <= p.dim;
   {
-    GlrRaw<BF16, GATED, TS> raw;
+    GlrRaw<BF16, GATED, VC, TS> raw;
     GlrParams<VC, ACT, GATED> par;
     raw.load(p, at.row0 + t0, c, left, slice * TS, n, whole);
     par.load(p, c, left);
@@ -64,7 +65,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_fwd_kernel(const GatedLinearA
   for (int v = 0; v < VC; ++v) lp[slice][ch + v] = P[v], ls[slice][ch + v] = S[v];
   __syncthreads();
   // 64 channels, four runs of slices
-  const int lane = threadIdx.x & 63, run = threadIdx.x >> 6;
+  const int lane = threadIdx.x % kGlrChannels, run = threadIdx.x / kGlrChannels;
   float sp[kRun], ss[kRun];
   float rP = 1.0f, rS = 0.0f;
 #pragma unroll

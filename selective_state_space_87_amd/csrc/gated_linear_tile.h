@@ -2,11 +2,11 @@
 // steps, a block of 256 threads each, and the chain that joins the tiles of a
 // channel.
 //
-// A thread has VC adjacent channels, one 16-byte load of x or a gate (8 of
-// bfloat16, 4 of float32; at whatever boundary the row starts on), and TS
-// consecutive steps, a slice: consecutive lanes have consecutive channels, so a
-// load of a wave reads 8 (4) whole rows of the tile. All a tile's loads are
-// issued before the first is used.
+// A thread has VC adjacent channels (forward one 16-byte load of x or a gate, 8 of
+// bfloat16 or 4 of float32; backward 4, whose float32 gradients are 16 bytes; at
+// whatever boundary the row starts on), and some consecutive steps, a slice:
+// consecutive lanes have consecutive channels, so a load of a wave reads whole rows
+// of the tile. All a tile's loads are issued before the first is used.
 //
 // A recurrence h <- a h + b over some steps is the map h -> P h + S (P the product
 // of the a, S the result from 0), and maps join as (P2 P1, P2 S1 + S2). In the
@@ -37,32 +37,41 @@
 namespace ssm {
 
 constexpr int kGlrThreads = 256;
+constexpr int kGlrRuns = 4;  // runs of slices: kGlrThreads / kGlrChannels
 constexpr uint32_t kGlrMissing = 0xffffffffu;
 constexpr int kGlrMostPolls = 1 << 22;
 
 // ---- a thread's inputs of one step
 
-template <bool BF16>
-struct GlrLane {
-  static constexpr int VC = BF16 ? 8 : 4;                 // channels of a thread
+// How 256 threads lie on a tile of STEPS steps, with VC channels a thread.
+template <int VC, int STEPS>
+struct GlrShape {
   static constexpr int kLanes = kGlrChannels / VC;        // threads over the channels
   static constexpr int kSlices = kGlrThreads / kLanes;    // slices of a tile
+  static constexpr int kSteps = STEPS / kSlices;          // steps of a slice
+  static constexpr int kRun = kSlices / kGlrRuns;         // slices of a run
 };
 
-typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// VC elements in as many words as they take; any element boundary (the memory
+// unit takes all), read once: past the caches.
+template <bool BF16, int VC>
+struct GlrPack {
+  static constexpr int N = BF16 ? VC / 2 : VC;
+  typedef uint32_t Words __attribute__((ext_vector_type(N)));
+  typedef uint32_t Any __attribute__((ext_vector_type(N), aligned(BF16 ? 2 : 4)));
+};
 
-// 16 bytes of channels from element `at` on, of which `left` are there (zeros for the others).
-template <bool BF16>
-__device__ __forceinline__ u32x4 glr_load(const void* base, int64_t at, int left) {
-  constexpr int VC = GlrLane<BF16>::VC;
-  u32x4 w = {0u, 0u, 0u, 0u};
+// Elements at .. at + VC - 1, of which `left` are there (zeros for the others).
+template <bool BF16, int VC, bool ONCE = true>
+__device__ __forceinline__ typename GlrPack<BF16, VC>::Words glr_load(const void* base, int64_t at, int left) {
+  using Pack = GlrPack<BF16, VC>;
+  typename Pack::Words w = {};
   if (left >= VC) {
-    if constexpr (BF16) {
-      w = *reinterpret_cast<const u32x4_2*>(static_cast<const uint16_t*>(base) + at);
+    const auto* from = reinterpret_cast<const typename Pack::Any*>(static_cast<const char*>(base) + at * (BF16 ? 2 : 4));
+    if constexpr (ONCE) {
+      w = __builtin_nontemporal_load(from);
     } else {
-      w = *reinterpret_cast<const u32x4_4*>(static_cast<const uint32_t*>(base) + at);
+      w = *from;
     }
   } else {
 #pragma unroll
@@ -80,18 +89,8 @@ __device__ __forceinline__ u32x4 glr_load(const void* base, int64_t at, int left
   return w;
 }
 
-// The same where all of them are there.
-template <bool BF16>
-__device__ __forceinline__ u32x4 glr_load_whole(const void* base, int64_t at) {
-  if constexpr (BF16) {
-    return *reinterpret_cast<const u32x4_2*>(static_cast<const uint16_t*>(base) + at);
-  } else {
-    return *reinterpret_cast<const u32x4_4*>(static_cast<const uint32_t*>(base) + at);
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ float glr_elem(const u32x4& w, int c) {
+template <bool BF16, typename W>
+__device__ __forceinline__ float glr_elem(const W& w, int c) {
   if constexpr (BF16) {
     return __uint_as_float(c & 1 ? w[c / 2] & 0xffff0000u : w[c / 2] << 16);
   } else {
@@ -99,53 +98,36 @@ __device__ __forceinline__ float glr_elem(const u32x4& w, int c) {
   }
 }
 
+// float32 parameters and states: several blocks read the same.
 template <int VC>
 __device__ __forceinline__ void glr_load_f32(const float* base, int64_t at, int left, float (&v)[VC]) {
 #pragma unroll
   for (int q = 0; q < VC / 4; ++q) {
-    const u32x4 w = glr_load<false>(base, at + 4 * q, left - 4 * q);
+    const auto w = glr_load<false, 4, false>(base, at + 4 * q, left - 4 * q);
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[4 * q + c] = __uint_as_float(w[c]);
   }
 }
 
-template <int VC>
-__device__ __forceinline__ void glr_store_f32(float* base, int64_t at, int left, const float (&v)[VC]) {
+template <bool BF16, int VC>
+__device__ __forceinline__ void glr_store(void* base, int64_t at, int left, const float (&v)[VC]) {
+  using Pack = GlrPack<BF16, VC>;
   if (left >= VC) {
+    typename Pack::Any w;
 #pragma unroll
-    for (int q = 0; q < VC / 4; ++q) {
-      u32x4 w;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) w[c] = __float_as_uint(v[4 * q + c]);
-      *reinterpret_cast<u32x4_4*>(base + at + 4 * q) = w;
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < VC; ++c) {
-      if (c < left) base[at + c] = v[c];
-    }
-  }
-}
-
-template <int VC>
-__device__ __forceinline__ void glr_store_bf16(void* base, int64_t at, int left, const float (&v)[VC]) {
-  uint16_t* p = static_cast<uint16_t*>(base) + at;
-  if (left >= VC) {
-#pragma unroll
-    for (int q = 0; q < VC / 4; ++q) {
-      typedef uint32_t u32x2_2 __attribute__((ext_vector_type(2), aligned(2)));
-      u32x2_2 w;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        w[c] = static_cast<uint32_t>(f32_to_bf16_bits(v[4 * q + 2 * c])) |
-               (static_cast<uint32_t>(f32_to_bf16_bits(v[4 * q + 2 * c + 1])) << 16);
+    for (int i = 0; i < Pack::N; ++i) {
+      if constexpr (BF16) {
+        w[i] = static_cast<uint32_t>(f32_to_bf16_bits(v[2 * i])) |
+               (static_cast<uint32_t>(f32_to_bf16_bits(v[2 * i + 1])) << 16);
+      } else {
+        w[i] = __float_as_uint(v[i]);
       }
-      *reinterpret_cast<u32x2_2*>(p + 4 * q) = w;
     }
+    __builtin_nontemporal_store(w, reinterpret_cast<typename Pack::Any*>(static_cast<char*>(base) + at * (BF16 ? 2 : 4)));
   } else {
 #pragma unroll
     for (int c = 0; c < VC; ++c) {
-      if (c < left) p[c] = f32_to_bf16_bits(v[c]);
+      if (c < left) store_elem<BF16>(base, at + c, v[c]);
     }
   }
 }
@@ -153,25 +135,27 @@ __device__ __forceinline__ void glr_store_bf16(void* base, int64_t at, int left,
 // Inputs of a thread's slice, TS steps from tile step `s0` on, n steps of the
 // tile being there. A tile that is there whole is loaded without a branch, so
 // that all loads are on their way before the first is waited for.
-template <bool BF16, bool GATED, int TS>
+template <bool BF16, bool GATED, int VC, int TS>
 struct GlrRaw {
-  u32x4 x[TS], gate[TS], igate[GATED ? TS : 1];
+  typename GlrPack<BF16, VC>::Words x[TS], gate[TS], igate[GATED ? TS : 1];
 
   __device__ __forceinline__ void load(const GatedLinearArgs& p, int64_t row, int c, int left, int s0, int n, bool whole) {
+    const int64_t ax = (row + s0) * p.x_step + c, ag = (row + s0) * p.gate_step + c;
+    const int64_t ai = GATED ? (row + s0) * p.igate_step + c : 0;
     if (whole) {
 #pragma unroll
       for (int i = 0; i < TS; ++i) {
-        gate[i] = glr_load_whole<BF16>(p.gate, (row + s0 + i) * p.gate_step + c);
-        x[i] = glr_load_whole<BF16>(p.x, (row + s0 + i) * p.x_step + c);
-        if constexpr (GATED) igate[i] = glr_load_whole<BF16>(p.igate, (row + s0 + i) * p.igate_step + c);
+        gate[i] = glr_load<BF16, VC>(p.gate, ag + i * p.gate_step, VC);
+        x[i] = glr_load<BF16, VC>(p.x, ax + i * p.x_step, VC);
+        if constexpr (GATED) igate[i] = glr_load<BF16, VC>(p.igate, ai + i * p.igate_step, VC);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < TS; ++i) {
         const int have = s0 + i < n ? left : 0;
-        gate[i] = glr_load<BF16>(p.gate, (row + s0 + i) * p.gate_step + c, have);
-        x[i] = glr_load<BF16>(p.x, (row + s0 + i) * p.x_step + c, have);
-        if constexpr (GATED) igate[i] = glr_load<BF16>(p.igate, (row + s0 + i) * p.igate_step + c, have);
+        gate[i] = glr_load<BF16, VC>(p.gate, ag + i * p.gate_step, have);
+        x[i] = glr_load<BF16, VC>(p.x, ax + i * p.x_step, have);
+        if constexpr (GATED) igate[i] = glr_load<BF16, VC>(p.igate, ai + i * p.igate_step, have);
       }
     }
   }
@@ -203,7 +187,7 @@ struct GlrParams {
 
 // Decays a and inputs b of a slice. (Steps that are not there: see glr_mask.)
 template <bool BF16, int ACT, int SCALE, bool GATED, int TS, int VC>
-__device__ __forceinline__ void glr_elements(const GlrRaw<BF16, GATED, TS>& raw, const GlrParams<VC, ACT, GATED>& par,
+__device__ __forceinline__ void glr_elements(const GlrRaw<BF16, GATED, VC, TS>& raw, const GlrParams<VC, ACT, GATED>& par,
                                              float (&a)[TS][VC], float (&b)[TS][VC]) {
 #pragma unroll
   for (int i = 0; i < TS; ++i) {
@@ -276,7 +260,7 @@ __device__ __forceinline__ uint64_t glr_get(const uint64_t* at) {
 // One wave: the state that enters place `q` of the chain, given the map (P, S) of
 // the tile there and the state `start` that enters place 0. Lane l has channel l.
 __device__ __forceinline__ float glr_enter(const GlrChain& c, uint32_t group, uint32_t q, float P, float S, float start) {
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x % kGlrChannels;
   const auto at = [&](uint32_t place) {
     return (static_cast<int64_t>(place) * c.groups + group) * kGlrChannels + lane;
   };
