@@ -60,10 +60,10 @@ void launch_walk(const GatedLinearArgs& a, hipStream_t st) {
   });
 }
 
-__global__ __launch_bounds__(kGlrThreads) void glr_clear_kernel(uint4* words, int64_t n) {
+__global__ __launch_bounds__(kGlrThreads) void glr_clear_kernel(uint4* words, int64_t counts, int64_t n) {
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGlrThreads;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kGlrThreads + threadIdx.x; i < n; i += step) {
-    const uint32_t v = i < 16 ? 0u : kGlrMissing;  // the count's 256 bytes, then the words
+    const uint32_t v = i < counts ? 0u : kGlrMissing;
     words[i] = make_uint4(v, v, v, v);
   }
 }
@@ -107,7 +107,7 @@ void launch_glr_clear(const GlrChainPlan& p, void* workspace, hipStream_t st) {
   const int64_t n = static_cast<int64_t>(p.bytes / 16);
   const int64_t blocks = (n + kGlrThreads - 1) / kGlrThreads;
   glr_clear_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), kGlrThreads, 0, st>>>(
-      static_cast<uint4*>(workspace), n);
+      static_cast<uint4*>(workspace), static_cast<int64_t>(p.off_words / 16), n);
 }
 
 int launch_gated_linear(const GatedLinearArgs& a, void* stream) {

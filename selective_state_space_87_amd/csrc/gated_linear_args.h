@@ -55,6 +55,7 @@ __attribute__((weak)) int launch_gated_linear_bwd(const GatedLinearBwdArgs& a, v
 // workspace joins the pairs (gated_linear_tile.h): a word a tile and channel, and
 // one for every kGlrWindow tiles.
 constexpr int kGlrChannels = 64, kGlrFwdSteps = 128, kGlrBwdSteps = 64, kGlrWindow = 8;
+constexpr int kGlrTicketBytes = 64;  // a count of its own line for every group
 
 // Up to this length a sequence is walked step by step, with no tiles.
 constexpr int64_t kGlrWalkSteps = 16;
@@ -67,6 +68,7 @@ inline bool gated_linear_fits(int64_t batch, int64_t seqlen, int64_t dim) {
 
 struct GlrChainPlan {
   int64_t groups, tiles;  // blocks of channels, over the batch rows; tiles of steps
+  int64_t columns;        // groups, rounded up to one for each of the 8 XCDs
   size_t off_words, off_states, bytes;
 };
 
@@ -74,9 +76,10 @@ inline GlrChainPlan plan_glr_chain(int64_t batch, int64_t seqlen, int64_t dim, i
   GlrChainPlan p{};
   p.groups = batch * ((dim + kGlrChannels - 1) / kGlrChannels);
   p.tiles = (seqlen + steps - 1) / steps;
+  p.columns = (p.groups + 7) / 8 * 8;
   if (p.tiles <= 1) return p;
   const size_t word = static_cast<size_t>(p.groups) * kGlrChannels * 8;
-  p.off_words = 256;  // behind the tickets' counter
+  p.off_words = static_cast<size_t>(p.groups) * kGlrTicketBytes;
   p.off_states = p.off_words + static_cast<size_t>(p.tiles) * word;
   p.bytes = p.off_states + static_cast<size_t>(p.tiles / kGlrWindow) * word;
   return p;

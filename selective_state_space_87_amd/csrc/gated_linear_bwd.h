@@ -26,11 +26,13 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
   __shared__ float enter_h[kGlrChannels], enter_e[kGlrChannels];
   __shared__ uint32_t slot;
   const GatedLinearArgs& p = q.f;
-  uint32_t tile = blockIdx.x;
-  if constexpr (CHAIN) tile = glr_ticket(chain, &slot);
-  const uint32_t place = CHAIN ? tile / chain.groups : 0;   // the last tiles first
-  const uint32_t k = CHAIN ? tiles - 1 - place : 0;
-  const GlrTile at = glr_tile(p, CHAIN ? tile - place * chain.groups : tile);
+  uint32_t k = 0, group = blockIdx.x;
+  if constexpr (CHAIN) {
+    k = glr_ticket(chain, &slot, &group);
+    if (k == kGlrMissing) return;
+    k = tiles - 1 - k;  // the last tiles first
+  }
+  const GlrGroup at = glr_group(p, group);
   const int64_t t0 = static_cast<int64_t>(k) * kGlrBwdSteps;
   const int slice = threadIdx.x / Shape::kLanes;
   const int ch = static_cast<int>(threadIdx.x % Shape::kLanes) * VC, c = at.c0 + ch;
@@ -115,15 +117,15 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
     const int64_t i = static_cast<int64_t>(at.b) * p.dim + ce;
     float e = q.dh_final != nullptr && ce < p.dim ? q.dh_final[i] : 0.0f;
     enter_h[lane] = ce < p.dim ? p.states[(static_cast<int64_t>(at.b) * tiles + k) * p.dim + ce] : 0.0f;
-    float P = rp[3][lane], R = rr[3][lane];
+    float P = 1.0f, R = 0.0f;
 #pragma unroll
-    for (int r = 2; r >= 0; --r) {
+    for (int r = kGlrRuns - 1; r >= 0; --r) {
       P *= rp[r][lane];
       R = fmaf(rp[r][lane], R, rr[r][lane]);
     }
     if constexpr (CHAIN) {
       const uint32_t last = static_cast<uint32_t>((at.steps - 1) / kGlrBwdSteps);
-      e = glr_enter(chain, static_cast<uint32_t>(at.group), last - k, P, R, e);
+      e = glr_enter(chain, group, last - k, P, R, e);
     }
     enter_e[lane] = e;
     if (k == 0 && q.dh0 != nullptr && ce < p.dim) q.dh0[i] = fmaf(P, e, R);
@@ -132,11 +134,11 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
   {
     float h = enter_h[lane], e = enter_e[lane];
 #pragma unroll
-    for (int r = 0; r < 3; ++r) {
+    for (int r = 0; r < kGlrRuns - 1; ++r) {
       if (r < run) h = fmaf(rp[r][lane], h, rs[r][lane]);
     }
 #pragma unroll
-    for (int r = 3; r > 0; --r) {
+    for (int r = kGlrRuns - 1; r > 0; --r) {
       if (r > run) e = fmaf(rp[r][lane], e, rr[r][lane]);
     }
 #pragma unroll
@@ -207,9 +209,11 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
   rp[run][lane] = total[0], rs[run][lane] = total[1], rr[run][lane] = total[2];
   __syncthreads();
   if (run == 0 && ce < p.dim) {
-    part[ce] = (rp[0][lane] + rp[1][lane]) + (rp[2][lane] + rp[3][lane]);
-    part[p.dim + ce] = (rs[0][lane] + rs[1][lane]) + (rs[2][lane] + rs[3][lane]);
-    part[2 * p.dim + ce] = (rr[0][lane] + rr[1][lane]) + (rr[2][lane] + rr[3][lane]);
+    float sum[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int r = 0; r < kGlrRuns; ++r) sum[0] += rp[r][lane], sum[1] += rs[r][lane], sum[2] += rr[r][lane];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) part[i * p.dim + ce] = sum[i];
   }
 }
 
@@ -223,7 +227,7 @@ void launch_glr_bwd(const GatedLinearBwdArgs& a, const GlrBwdPlan& plan, hipStre
     constexpr bool GATED = decltype(gated)::value;
     if (cp.tiles > 1) {
       launch_glr_clear(cp, a.f.workspace, st);
-      glr_bwd_kernel<BF16, ACT, SCALE, GATED, true><<<static_cast<unsigned>(cp.groups * cp.tiles), kGlrThreads, 0, st>>>(
+      glr_bwd_kernel<BF16, ACT, SCALE, GATED, true><<<static_cast<unsigned>(cp.columns * cp.tiles), kGlrThreads, 0, st>>>(
           a, glr_chain(cp, a.f.workspace), tiles, parts);
     } else {
       glr_bwd_kernel<BF16, ACT, SCALE, GATED, false>

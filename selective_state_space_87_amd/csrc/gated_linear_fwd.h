@@ -14,10 +14,12 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(const GatedLine
   __shared__ __attribute__((aligned(16))) float lp[SL][kGlrChannels], ls[SL][kGlrChannels];
   __shared__ float rp[kGlrRuns][kGlrChannels], rs[kGlrRuns][kGlrChannels], enter[kGlrChannels];
   __shared__ uint32_t slot;
-  uint32_t tile = blockIdx.x;
-  if constexpr (CHAIN) tile = glr_ticket(chain, &slot);
-  const uint32_t k = CHAIN ? tile / chain.groups : 0;
-  const GlrTile at = glr_tile(p, CHAIN ? tile - k * chain.groups : tile);
+  uint32_t k = 0, group = blockIdx.x;
+  if constexpr (CHAIN) {
+    k = glr_ticket(chain, &slot, &group);
+    if (k == kGlrMissing) return;
+  }
+  const GlrGroup at = glr_group(p, group);
   const int64_t t0 = static_cast<int64_t>(k) * kGlrFwdSteps;
   const int slice = threadIdx.x / Shape::kLanes;
   const int c = at.c0 + static_cast<int>(threadIdx.x % Shape::kLanes) * VC;
@@ -81,30 +83,31 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(const GatedLine
     float h = p.h0 != nullptr && ce < p.dim ? p.h0[static_cast<int64_t>(at.b) * p.dim + ce] : 0.0f;
     if constexpr (CHAIN) {
 #pragma unroll
-      for (int r = 1; r < 4; ++r) {
+      for (int r = 1; r < kGlrRuns; ++r) {
         rP *= rp[r][lane];
         rS = fmaf(rp[r][lane], rS, rs[r][lane]);
       }
-      h = glr_enter(chain, static_cast<uint32_t>(at.group), k, rP, rS, h);
+      h = glr_enter(chain, group, k, rP, rS, h);
     }
     enter[lane] = h;
   }
   __syncthreads();
   float h = enter[lane];
 #pragma unroll
-  for (int r = 0; r < 3; ++r) {
+  for (int r = 0; r < kGlrRuns - 1; ++r) {
     if (r < run) h = fmaf(rp[r][lane], h, rs[r][lane]);
   }
-  if (p.states != nullptr && run % 2 == 0 && run * kRun * TS < there && at.c0 + lane < p.dim) {
+  const int first = run * kRun * TS;  // step of the tile that the run starts with
+  if (p.states != nullptr && first % kGlrBwdSteps == 0 && first < there && at.c0 + lane < p.dim) {
     const int64_t tiles = (p.seqlen + kGlrBwdSteps - 1) / kGlrBwdSteps;
-    p.states[(at.b * tiles + t0 / kGlrBwdSteps + run / 2) * p.dim + at.c0 + lane] = h;
+    p.states[(at.b * tiles + (t0 + first) / kGlrBwdSteps) * p.dim + at.c0 + lane] = h;
   }
 #pragma unroll
   for (int i = 0; i < kRun; ++i) {
     ls[run * kRun + i][lane] = h;
     h = fmaf(sp[i], h, ss[i]);
   }
-  if (run == 3 && p.h_final != nullptr && t0 + n == at.steps && at.c0 + lane < p.dim) {
+  if (run == kGlrRuns - 1 && p.h_final != nullptr && t0 + n == at.steps && at.c0 + lane < p.dim) {
     p.h_final[static_cast<int64_t>(at.b) * p.dim + at.c0 + lane] = h;
   }
   __syncthreads();
@@ -141,7 +144,7 @@ void launch_glr_fwd(const GatedLinearArgs& a, const GlrChainPlan& plan, hipStrea
     if (plan.tiles > 1) {
       launch_glr_clear(plan, a.workspace, st);
       glr_fwd_kernel<BF16, ACT, SCALE, GATED, true>
-          <<<static_cast<unsigned>(plan.groups * plan.tiles), kGlrThreads, 0, st>>>(a, glr_chain(plan, a.workspace));
+          <<<static_cast<unsigned>(plan.columns * plan.tiles), kGlrThreads, 0, st>>>(a, glr_chain(plan, a.workspace));
     } else {
       glr_fwd_kernel<BF16, ACT, SCALE, GATED, false>
           <<<static_cast<unsigned>(plan.groups), kGlrThreads, 0, st>>>(a, GlrChain{});

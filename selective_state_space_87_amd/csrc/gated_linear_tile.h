@@ -18,8 +18,8 @@
 // deterministic), and the serial part is one exchange through memory every
 // kGlrWindow tiles.
 //
-// Waiting always ends. A block takes its tile by a ticket (an atomic count), and
-// tickets go along the chain: what a tile waits for is held by a block that
+// Waiting always ends. A block takes its tile by a ticket (an atomic count of its
+// group's), and tickets go along the chain: what a tile waits for is held by a block that
 // started earlier, which publishes its map before it waits, and its state after
 // waiting for earlier ones only; the first waits for nothing. A wait also
 // ends by itself, with NaN, after kGlrMostPolls tries (some seconds), should
@@ -37,7 +37,7 @@
 namespace ssm {
 
 constexpr int kGlrThreads = 256;
-constexpr int kGlrRuns = 4;  // runs of slices: kGlrThreads / kGlrChannels
+constexpr int kGlrRuns = kGlrThreads / kGlrChannels;  // runs of slices
 constexpr uint32_t kGlrMissing = 0xffffffffu;
 constexpr int kGlrMostPolls = 1 << 22;
 
@@ -212,19 +212,17 @@ __device__ __forceinline__ void glr_mask(int s0, int n, float (&a)[TS][VC], floa
   }
 }
 
-// ---- a tile's place
+// ---- the place of a group, 64 channels of a batch row
 
-struct GlrTile {
+struct GlrGroup {
   int64_t row0;   // first row of its batch row in [B L, ..]
   int64_t steps;  // steps that the batch row has
   int b, c0;      // batch row, first channel
-  int group;      // (batch row, 64 channels)
 };
 
-__device__ __forceinline__ GlrTile glr_tile(const GatedLinearArgs& p, uint32_t group) {
-  GlrTile t;
+__device__ __forceinline__ GlrGroup glr_group(const GatedLinearArgs& p, uint32_t group) {
+  GlrGroup t;
   const uint32_t per_row = static_cast<uint32_t>((p.dim + kGlrChannels - 1) / kGlrChannels);
-  t.group = static_cast<int>(group);
   t.b = static_cast<int>(group / per_row);
   t.c0 = static_cast<int>(group % per_row) * kGlrChannels;
   t.row0 = static_cast<int64_t>(t.b) * p.seqlen;
@@ -235,16 +233,17 @@ __device__ __forceinline__ GlrTile glr_tile(const GatedLinearArgs& p, uint32_t g
 // ---- the chain
 
 struct GlrChain {
-  uint32_t* tickets;
+  uint32_t* tickets;  // a count a group, kGlrTicketBytes apart
   uint64_t* maps;     // [tile][group][64]: S, and P (never all ones) above
   uint64_t* states;   // [window][group][64]: the state, and 0 above
-  uint32_t groups;
+  uint32_t groups, columns;
 };
 
 inline GlrChain glr_chain(const GlrChainPlan& p, void* workspace) {
   char* w = static_cast<char*>(workspace);
   return GlrChain{reinterpret_cast<uint32_t*>(w), reinterpret_cast<uint64_t*>(w + p.off_words),
-                  reinterpret_cast<uint64_t*>(w + p.off_states), static_cast<uint32_t>(p.groups)};
+                  reinterpret_cast<uint64_t*>(w + p.off_states), static_cast<uint32_t>(p.groups),
+                  static_cast<uint32_t>(p.columns)};
 }
 
 __device__ __forceinline__ uint64_t glr_word(float low, uint32_t high) {
@@ -301,9 +300,14 @@ __device__ __forceinline__ float glr_enter(const GlrChain& c, uint32_t group, ui
   return h;
 }
 
-// The block's ticket.
-__device__ __forceinline__ uint32_t glr_ticket(const GlrChain& c, uint32_t* slot) {
-  if (threadIdx.x == 0) *slot = atomicAdd(c.tickets, 1u);
+// The block's place in its group's chain, or kGlrMissing for a block of no group.
+// Blocks of one group are `columns` apart, a multiple of 8, so that they run on one
+// XCD and the chain's words stay in its L2. A count a group: one for all
+// would be the bound, 12 ns a tile (33000 tiles 420 us).
+__device__ __forceinline__ uint32_t glr_ticket(const GlrChain& c, uint32_t* slot, uint32_t* group) {
+  *group = blockIdx.x % 8 * (c.columns / 8) + blockIdx.x / 8 % (c.columns / 8);
+  if (*group >= c.groups) return kGlrMissing;
+  if (threadIdx.x == 0) *slot = atomicAdd(c.tickets + *group * (kGlrTicketBytes / 4), 1u);
   __syncthreads();
   return *slot;
 }
