@@ -35,13 +35,17 @@ struct ConvBwdPlan {
   size_t bytes;
 };
 
-constexpr int64_t kConvBwdMinSeg = 32, kConvBwdMaxSeg = 512, kConvBwdBlocks = 2048;
+// As many segments as make kConvBwdWaves waves, 8 a CU: all at once (three times as
+// many fit with few registers, but not with four channels' filters, and a second
+// round of fewer waves costs more than it gives). Measured at (4, 8192, 4096, width
+// 4) bfloat16, where 512, 768, 1024, 2048 blocks of four waves: 263, 284, 302, 279 us.
+constexpr int64_t kConvBwdMinSeg = 16, kConvBwdMaxSeg = 512, kConvBwdWaves = 2048;
 
 inline ConvBwdPlan plan_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width) {
   ConvBwdPlan p{};
   const auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  const int64_t groups = batch * ceil_div(dim, dim % 4 == 0 ? 1024 : 256);
-  const int64_t wanted = ceil_div(kConvBwdBlocks, groups > 0 ? groups : 1);
+  const int64_t groups = batch * ceil_div(dim, 256);  // waves, of four channels a thread
+  const int64_t wanted = ceil_div(kConvBwdWaves, groups > 0 ? groups : 1);
   int64_t seg = ceil_div(ceil_div(seqlen, wanted), 16) * 16;
   seg = seg < kConvBwdMinSeg ? kConvBwdMinSeg : (seg > kConvBwdMaxSeg ? kConvBwdMaxSeg : seg);
   while (ceil_div(seqlen, seg) > 65535) seg *= 2;

@@ -23,21 +23,25 @@ namespace ssm {
 
 namespace {
 
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+// Any element boundary: rows of odd widths start anywhere, and the memory unit
+// takes all. x and dy stream through once, dx too: past the caches.
+typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
-constexpr int kBlock = 256;
+constexpr int kBlock = 64;
 
 template <int VC, bool BF16>
 __device__ __forceinline__ void load_in(const void* base, int64_t i, float (&v)[VC]) {
   if constexpr (VC == 4 && BF16) {
-    const u32x2 r = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(base) + i);
+    const u32x2_any r =
+        __builtin_nontemporal_load(reinterpret_cast<const u32x2_any*>(static_cast<const uint16_t*>(base) + i));
     v[0] = __uint_as_float(r.x << 16);
     v[1] = __uint_as_float(r.x & 0xffff0000u);
     v[2] = __uint_as_float(r.y << 16);
     v[3] = __uint_as_float(r.y & 0xffff0000u);
   } else if constexpr (VC == 4) {
-    const f32x4 r = *reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + i);
+    const f32x4_any r =
+        __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(static_cast<const float*>(base) + i));
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = r[c];
   } else {
@@ -48,7 +52,7 @@ __device__ __forceinline__ void load_in(const void* base, int64_t i, float (&v)[
 template <int VC>
 __device__ __forceinline__ void store_out(float* p, const float (&v)[VC]) {
   if constexpr (VC == 4) {
-    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
+    __builtin_nontemporal_store(f32x4_any{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_any*>(p));
   } else {
     p[0] = v[0];
   }
@@ -65,8 +69,11 @@ template <int K, int VC, bool BF16, bool SILU>
 __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(const ConvBwdArgs a, int seg) {
   constexpr int kGroup = K * (K < 8 ? 8 / K : 1);  // steps whose loads are issued together
   const int64_t L = a.seqlen, Dm = a.dim;
-  const int64_t c0 = (static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x) * VC;
+  int64_t c0 = (static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x) * VC;
   if (c0 >= Dm) return;
+  // The last thread of an odd width takes the last VC channels, some of them its
+  // neighbour's too: both find, and write, the same values.
+  if (c0 > Dm - VC) c0 = Dm - VC;
   const int64_t b = blockIdx.z;
   const int64_t row0 = b * L;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * seg;
@@ -229,8 +236,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void conv1d_bwd_sums_kernel(const f
 
 template <int K, bool BF16>
 void launch_width(const ConvBwdArgs& a, const ConvBwdPlan& p, hipStream_t st) {
-  // Four channels per thread when rows stay aligned for 8/16-byte accesses.
-  const int vc = a.dim % 4 == 0 ? 4 : 1;
+  const int vc = a.dim >= 4 ? 4 : 1;
   const int64_t groups = (a.dim + vc - 1) / vc;
   const dim3 grid(static_cast<unsigned>((groups + kBlock - 1) / kBlock), static_cast<unsigned>(p.segs),
                   static_cast<unsigned>(a.batch));

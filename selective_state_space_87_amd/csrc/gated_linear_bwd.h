@@ -64,6 +64,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
   GlrParams<VC, ACT, GATED> par;
   float dy[TS][VC], a[TS][VC], b[TS][VC];
   const bool whole = n == kGlrBwdSteps && at.c0 + kGlrChannels <= p.dim;
+  par.load(p, c, left);  // first, since loads come in order: what needs it need not wait for all of the tile
   raw.load(p, at.row0 + t0, c, left, slice * TS, n, whole);
   {
     const int64_t from = (at.row0 + t0 + slice * TS) * p.dim + c;
@@ -81,7 +82,6 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
       for (int v = 0; v < VC; ++v) dy[i][v] = __uint_as_float(d[i][v]);
     }
   }
-  par.load(p, c, left);
   {
     glr_elements<BF16, ACT, SCALE, GATED, TS, VC>(raw, par, a, b);
     if (!whole) glr_mask<TS, VC>(slice * TS, n, a, b);

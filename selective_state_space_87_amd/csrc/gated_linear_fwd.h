@@ -50,8 +50,8 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(const GatedLine
   {
     GlrRaw<BF16, GATED, VC, TS> raw;
     GlrParams<VC, ACT, GATED> par;
+    par.load(p, c, left);  // first, since loads come in order: the first step's gates need not wait for the last's
     raw.load(p, at.row0 + t0, c, left, slice * TS, n, whole);
-    par.load(p, c, left);
     glr_elements<BF16, ACT, SCALE, GATED, TS, VC>(raw, par, a, b);
   }
   if (!whole) glr_mask<TS, VC>(slice * TS, n, a, b);
