@@ -899,8 +899,9 @@ def ssm_dropout_fwd(x, p, rng, call=0, residual=None, y=None, stream=None):
     out = x.dtype if residual is None else residual.dtype
     with _launch_context(dev, stream):
         if y is None:
-            y = torch.empty(x.shape, dtype=out, device=dev)
-        _dev_tensor("y", y, x.shape, (out,), dev)
+            y = torch.empty_like(x if residual is None else residual)
+        else:
+            _dev_tensor("y", y, x.shape, (out,), dev)
         st = lib.ssm_dropout_fwd(x.numel(), _DTYPE_CODE[x.dtype], _DTYPE_CODE[out], p, call, _ptr(rng), _ptr(x),
                                  _ptr(residual), _ptr(y), _stream_handle(stream, dev))
     _check("ssm_dropout_fwd", st)
@@ -921,8 +922,9 @@ def ssm_dropout_bwd(dy, p, rng, call=0, dx=None, stream=None):
     p, call = _drop_args(p, rng, call, dev)
     with _launch_context(dev, stream):
         if dx is None:
-            dx = torch.empty(dy.shape, dtype=torch.float32, device=dev)
-        _dev_tensor("dx", dx, dy.shape, f32, dev)
+            dx = torch.empty_like(dy)
+        else:
+            _dev_tensor("dx", dx, dy.shape, f32, dev)
         st = lib.ssm_dropout_bwd(dy.numel(), p, call, _ptr(rng), _ptr(dy), _ptr(dx), _stream_handle(stream, dev))
     _check("ssm_dropout_bwd", st)
     return dx
@@ -961,12 +963,13 @@ def ssm_layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, p=0.0
         raise ValueError("residual_out and p > 0 need a residual")
     with _launch_context(dev, stream):
         if y is None:
-            y = torch.empty(x.shape, dtype=out_dtype, device=dev)
-        _dev_tensor("y", y, x.shape, (out_dtype,), dev)
-        if residual is not None:
-            if residual_out is None:
-                residual_out = torch.empty_like(residual)
+            y = _out_like(x, out_dtype)
+        else:
+            _dev_tensor("y", y, x.shape, (out_dtype,), dev)
+        if residual_out is not None:
             _dev_tensor("residual_out", residual_out, x.shape, (residual.dtype,), dev)
+        elif residual is not None:
+            residual_out = torch.empty_like(residual)
         st = lib.ssm_layer_norm_fwd(rows, d, _DTYPE_CODE[x.dtype],
                                     0 if residual is None else _DTYPE_CODE[residual.dtype], _DTYPE_CODE[out_dtype],
                                     float(eps), p, call, _ptr(rng), _ptr(x), _ptr(residual), _ptr(weight),
@@ -1001,13 +1004,15 @@ def ssm_layer_norm_bwd(s, weight, dy, dresidual=None, eps=1e-5, p=0.0, rng=None,
     p, call = _drop_args(p, rng, call, dev, needed=False)
     with _launch_context(dev, stream):
         if ds is None:
-            ds = torch.empty(s.shape, dtype=torch.float32, device=dev)
-        _dev_tensor("ds", ds, s.shape, f32, dev)
-        if dx is None and p > 0:
-            dx = torch.empty(s.shape, dtype=torch.float32, device=dev)
-        _dev_tensor("dx", dx, s.shape, f32, dev)
-        sums = torch.empty((2, d), dtype=torch.float32, device=dev)
-        dweight, dbias = sums[0], sums[1]
+            ds = torch.empty_like(dy)
+        else:
+            _dev_tensor("ds", ds, s.shape, f32, dev)
+        if dx is not None:
+            _dev_tensor("dx", dx, s.shape, f32, dev)
+        elif p > 0:
+            dx = torch.empty_like(dy)
+        dweight = torch.empty((d,), dtype=torch.float32, device=dev) if weight is None else torch.empty_like(weight)
+        dbias = torch.empty_like(dweight)
         ws_bytes = int(lib.ssm_layer_norm_bwd_workspace_bytes(rows, d))
         if workspace is None and ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
@@ -1048,14 +1053,15 @@ def ssm_causal_conv1d_bwd(x, weight, dy, bias=None, state_in=None, dstate_out=No
         raise ValueError("dy is required")
     _dev_tensor("dy", dy, (Bt, L, d), f32, dev)
     _dev_tensor("dstate_out", dstate_out, (Bt, d, K - 1), f32, dev)
-    new = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)  # noqa: E731
     with _launch_context(dev, stream):
         if dx is None:
-            dx = new(Bt, L, d)
-        _dev_tensor("dx", dx, (Bt, L, d), f32, dev)
-        out = dict(dx=dx, dweight=new(d, K), dstate_in=new(Bt, d, K - 1))
+            dx = torch.empty_like(dy)
+        else:
+            _dev_tensor("dx", dx, (Bt, L, d), f32, dev)
+        out = dict(dx=dx, dweight=torch.empty_like(weight),
+                   dstate_in=torch.empty((Bt, d, K - 1), dtype=torch.float32, device=dev))
         if bias is not None:
-            out["dbias"] = new(d)
+            out["dbias"] = torch.empty_like(bias)
         ws_bytes = int(lib.ssm_causal_conv1d_bwd_workspace_bytes(Bt, L, d, K))
         if workspace is None and ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
@@ -1073,25 +1079,56 @@ FLAG_INPUT_NORM = 32        # SSM_FLAG_INPUT_NORM
 FLAG_INPUT_COMPLEMENT = 64  # SSM_FLAG_INPUT_COMPLEMENT
 
 
+def _row_step(name, t, D):
+    """Elements between consecutive steps of t ([B, L, D] or [B, D]), a dense
+    array or a column range of one."""
+    if t.is_contiguous():
+        return D
+    strides, shape = t.stride(), t.shape
+    if strides[-1] == 1 and len(strides) == 3 and shape[1] > 1 and (shape[0] <= 1 or strides[0] == shape[1] * strides[1]):
+        return strides[1]
+    return _step_of(name, t.unsqueeze(-2), len(strides) - 1, D)
+
+
 def _glr_inputs(x, gate, A, input_gate, gate_bias, input_bias, lead):
     """Checked lead sizes, dim, device and steps of the gated linear recurrence's inputs."""
     if not isinstance(x, torch.Tensor) or x.dim() != lead + 1 or x.dtype not in _DTYPE_CODE:
         raise ValueError(f"x must be a {lead + 1}-d float32 or bfloat16 tensor")
-    dev, shape, D = x.device, x.shape, x.shape[lead]
-    for name, t in (("x", x), ("gate", gate), ("input_gate", input_gate)):
-        if t is not None or name != "input_gate":
-            _strided_tensor(name, t, shape, x.dtype, dev)
-    if A is None:
-        raise ValueError("A is required")
-    f32 = (torch.float32,)
-    _dev_tensor("A", A, (D,), f32, dev)
-    _dev_tensor("gate_bias", gate_bias, (D,), f32, dev)
-    _dev_tensor("input_bias", input_bias, (D,), f32, dev)
-    if input_bias is not None and input_gate is None:
-        raise ValueError("input_bias needs an input_gate")
-    steps = [D if t is None or t.is_contiguous() else _step_of(name, t.unsqueeze(-2), lead, D)
-             for name, t in (("x", x), ("gate", gate), ("input_gate", input_gate))]
-    return tuple(shape[:lead]), D, dev, steps
+    dev, shape, ind, f32 = x.device, x.shape, x.dtype, torch.float32
+    D = shape[lead]
+    # all is as it should be: one expression, as in _dev_tensor
+    try:
+        fits = (x.is_cuda and gate.shape == shape and gate.dtype is ind and gate.device == dev and A.shape == (D,)
+                and A.dtype is f32 and A.device == dev and A.is_contiguous()
+                and (input_gate is None or (input_gate.shape == shape and input_gate.dtype is ind
+                                            and input_gate.device == dev))
+                and (gate_bias is None or (gate_bias.shape == (D,) and gate_bias.dtype is f32
+                                           and gate_bias.device == dev and gate_bias.is_contiguous()))
+                and (input_bias is None or (input_gate is not None and input_bias.shape == (D,)
+                                            and input_bias.dtype is f32 and input_bias.device == dev
+                                            and input_bias.is_contiguous())))
+    except AttributeError:  # not a tensor
+        fits = False
+    if not fits:
+        for name, t in (("x", x), ("gate", gate), ("input_gate", input_gate)):
+            if t is not None or name != "input_gate":
+                _strided_tensor(name, t, shape, ind, dev)
+        if A is None:
+            raise ValueError("A is required")
+        _dev_tensor("A", A, (D,), (f32,), dev)
+        _dev_tensor("gate_bias", gate_bias, (D,), (f32,), dev)
+        _dev_tensor("input_bias", input_bias, (D,), (f32,), dev)
+        if input_bias is not None and input_gate is None:
+            raise ValueError("input_bias needs an input_gate")
+    return shape[:lead], D, dev, (_row_step("x", x, D), _row_step("gate", gate, D),
+                                  D if input_gate is None else _row_step("input_gate", input_gate, D))
+
+
+def _out_like(t, dtype):
+    """An output of t's shape: torch.empty_like is the quickest where t is such a tensor itself."""
+    if t.dtype is dtype and t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty(t.shape, dtype=dtype, device=t.device)
 
 
 def _glr_flags(gate_sigmoid, gate_softplus, input_norm, input_complement):
@@ -1139,11 +1176,13 @@ def ssm_gated_linear_fwd(x, gate, A, input_gate=None, gate_bias=None, input_bias
         raise ValueError(f"unsupported output dtype {out_dtype}")
     with _launch_context(dev, stream):
         if y is None:
-            y = torch.empty((Bt, L, D), dtype=out_dtype, device=dev)
-        _dev_tensor("y", y, (Bt, L, D), (out_dtype,), dev)
-        if return_final_state and h_final is None:
-            h_final = torch.empty((Bt, D), dtype=torch.float32, device=dev)
-        _dev_tensor("h_final", h_final, (Bt, D), (torch.float32,), dev)
+            y = _out_like(x, out_dtype)
+        else:
+            _dev_tensor("y", y, (Bt, L, D), (out_dtype,), dev)
+        if h_final is not None:
+            _dev_tensor("h_final", h_final, (Bt, D), (torch.float32,), dev)
+        elif return_final_state:
+            h_final = torch.empty((Bt, D), dtype=torch.float32, device=dev) if h0 is None else torch.empty_like(h0)
         if states is not None:
             need = int(lib.ssm_gated_linear_states_bytes(Bt, L, D))
             if states is True:
@@ -1185,8 +1224,9 @@ def ssm_gated_linear_update(state, x, gate, A, input_gate=None, gate_bias=None, 
         raise ValueError(f"unsupported output dtype {out_dtype}")
     with _launch_context(dev, stream):
         if y is None:
-            y = torch.empty((Bt, D), dtype=out_dtype, device=dev)
-        _dev_tensor("y", y, (Bt, D), (out_dtype,), dev)
+            y = _out_like(x, out_dtype)
+        else:
+            _dev_tensor("y", y, (Bt, D), (out_dtype,), dev)
         st = lib.ssm_gated_linear_update(Bt, D, _DTYPE_CODE[x.dtype], _DTYPE_CODE[out_dtype], flags, *steps,
                                          _ptr(state), _ptr(x), _ptr(gate), _ptr(A), _ptr(input_gate),
                                          _ptr(gate_bias), _ptr(input_bias), _ptr(y), _stream_handle(stream, dev))
@@ -1220,15 +1260,15 @@ def ssm_gated_linear_bwd(x, gate, A, dy, input_gate=None, gate_bias=None, input_
     _dev_tensor("dh_final", dh_final, (Bt, D), f32, dev)
     if states is not None:
         _glr_states(states, int(lib.ssm_gated_linear_states_bytes(Bt, L, D)), dev)
-    new = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)  # noqa: E731
+    like = torch.empty_like
     with _launch_context(dev, stream):
-        g = dict(dx=new(Bt, L, D), dgate=new(Bt, L, D), dA=new(D), dh0=new(Bt, D))
+        g = dict(dx=like(dy), dgate=like(dy), dA=like(A), dh0=torch.empty((Bt, D), dtype=torch.float32, device=dev))
         if input_gate is not None:
-            g["dinput_gate"] = new(Bt, L, D)
+            g["dinput_gate"] = like(dy)
         if gate_bias is not None:
-            g["dgate_bias"] = new(D)
+            g["dgate_bias"] = like(A)
         if input_bias is not None:
-            g["dinput_bias"] = new(D)
+            g["dinput_bias"] = like(A)
         ws_bytes = int(lib.ssm_gated_linear_bwd_workspace_bytes(Bt, L, D, 0 if states is None else 1))
         if workspace is None and ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)

@@ -271,8 +271,10 @@ __global__ __launch_bounds__(64 * kSumWaves) void layer_norm_sums_kernel(const f
   }
 }
 
-// f(threads per row, pieces a thread) for a row of `dim` elements.
-template <typename F>
+// f(threads per row, pieces a thread) for a row of `dim` elements. WIDE: of a row
+// above 8192 elements (backward 4 pieces on 512 threads: the 128 registers that 1024
+// threads leave each would not hold a row's three arrays and the two sums).
+template <int WIDE, typename F>
 void by_width(int64_t dim, F&& f) {
   using std::integral_constant;
   if (dim <= 512) {
@@ -286,7 +288,7 @@ void by_width(int64_t dim, F&& f) {
   } else if (dim <= 8192) {
     f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
   } else {
-    f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    f(integral_constant<int, WIDE>{}, integral_constant<int, 2048 / WIDE>{});
   }
 }
 
@@ -295,7 +297,7 @@ constexpr int64_t kForwardBlocks = 4096;
 
 template <bool BI, int RES>
 void launch_norm(const LayerNormArgs& a, hipStream_t st) {
-  by_width(a.dim, [&](auto tpr, auto npk) {
+  by_width<1024>(a.dim, [&](auto tpr, auto npk) {
     constexpr int TPR = decltype(tpr)::value, NPK = decltype(npk)::value, kBlock = block_threads(TPR);
     const int64_t groups = (a.rows + kBlock / TPR - 1) / (kBlock / TPR);
     const unsigned blocks = static_cast<unsigned>(groups < kForwardBlocks ? groups : kForwardBlocks);
@@ -328,7 +330,7 @@ int launch_layer_norm_bwd(const LayerNormBwdArgs& a, void* stream) {
   int nparts = 0;
   if (a.rows > 0) {
     nparts = static_cast<int>(layer_norm_bwd_blocks(a.rows, a.dim));
-    by_width(a.dim, [&](auto tpr, auto npk) {
+    by_width<512>(a.dim, [&](auto tpr, auto npk) {
       constexpr int TPR = decltype(tpr)::value, NPK = decltype(npk)::value, kBlock = block_threads(TPR);
       const unsigned blocks = static_cast<unsigned>(nparts);
       a.s_bf16 ? layer_norm_bwd_kernel<TPR, NPK, true><<<blocks, kBlock, 0, st>>>(a)
