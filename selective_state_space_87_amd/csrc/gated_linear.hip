@@ -9,12 +9,11 @@ namespace ssm {
 
 namespace {
 
-constexpr int walk_channels(bool bf16) { return bf16 ? 8 : 4; }
-
-// A thread walks VC channels of a batch row.
+// A thread walks four channels of a batch row, the next step's inputs on their way
+// while one is taken.
 template <bool BF16, int ACT, int SCALE, bool GATED>
 __global__ __launch_bounds__(kGlrThreads) void glr_walk_kernel(const GatedLinearArgs p) {
-  constexpr int VC = walk_channels(BF16);
+  constexpr int VC = 4;
   const int64_t per_row = (p.dim + VC - 1) / VC;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kGlrThreads + threadIdx.x;
   if (i >= p.batch * per_row) return;
@@ -52,7 +51,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_walk_kernel(const GatedLinear
 
 template <bool BF16>
 void launch_walk(const GatedLinearArgs& a, hipStream_t st) {
-  const int64_t threads = a.batch * ((a.dim + walk_channels(BF16) - 1) / walk_channels(BF16));
+  const int64_t threads = a.batch * ((a.dim + 3) / 4);
   const unsigned blocks = static_cast<unsigned>((threads + kGlrThreads - 1) / kGlrThreads);
   glr_by_form(a, [&](auto act, auto scale, auto gated) {
     glr_walk_kernel<BF16, decltype(act)::value, decltype(scale)::value, decltype(gated)::value>
@@ -112,7 +111,7 @@ void launch_glr_clear(const GlrChainPlan& p, void* workspace, hipStream_t st) {
 
 int launch_gated_linear(const GatedLinearArgs& a, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (a.seqlen <= kGlrWalkSteps) {
+  if (gated_linear_walks(a.batch, a.seqlen, a.dim)) {
     a.in_bf16 ? launch_walk<true>(a, st) : launch_walk<false>(a, st);
   } else {
     const GlrChainPlan plan = plan_glr_chain(a.batch, a.seqlen, a.dim, kGlrFwdSteps);

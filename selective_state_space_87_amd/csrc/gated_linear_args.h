@@ -57,8 +57,16 @@ __attribute__((weak)) int launch_gated_linear_bwd(const GatedLinearBwdArgs& a, v
 constexpr int kGlrChannels = 64, kGlrFwdSteps = 128, kGlrBwdSteps = 64, kGlrWindow = 8;
 constexpr int kGlrTicketBytes = 64;  // a count of its own line for every group
 
-// Up to this length a sequence is walked step by step, with no tiles.
-constexpr int64_t kGlrWalkSteps = 16;
+// Whether a sequence is walked step by step instead, a thread four channels: a step
+// takes 0.45 us however few the channels are, a tile as long for 1 step as for 64,
+// but blocks of many tiles are mostly idle. Measured, walked against tiles (us,
+// bfloat16): 1 x 2560 channels, 8, 12, 16, 64 steps 6.1, 7.8, 9.5, 31 against 8.6
+// throughout; 16 x 2560 6.3, 8.4, 11.8, 44 against 12.8; 128 x 4096 9.8, 13.7, 17.7, 60
+// against 87 (float32, 64 steps: 95 against 113).
+inline bool gated_linear_walks(int64_t batch, int64_t seqlen, int64_t dim) {
+  const int64_t groups = batch * ((dim + kGlrChannels - 1) / kGlrChannels);
+  return seqlen <= 12 || (seqlen <= kGlrBwdSteps && seqlen <= groups / 64);
+}
 
 // At most as many blocks of 256 threads as keep a launch below 2^32 threads.
 inline bool gated_linear_fits(int64_t batch, int64_t seqlen, int64_t dim) {
