@@ -272,13 +272,13 @@ __device__ __forceinline__ float glr_enter(const GlrChain& c, uint32_t group, ui
   for (int i = 0; i < kGlrWindow - 1; ++i) map[i] = 0;
   for (int tries = 0;; ++tries) {
     bool missing = false;
-    if (window > 0) {
+    if (window > 0 && (tries == 0 || __any(static_cast<uint32_t>(state >> 32) == kGlrMissing))) {
       state = glr_get(c.states + at(window - 1));
       missing |= static_cast<uint32_t>(state >> 32) == kGlrMissing;
     }
 #pragma unroll
     for (uint32_t i = 0; i < kGlrWindow - 1; ++i) {
-      if (i < j) {
+      if (i < j && (tries == 0 || __any(static_cast<uint32_t>(map[i] >> 32) == kGlrMissing))) {
         map[i] = glr_get(c.maps + at(q - j + i));
         missing |= static_cast<uint32_t>(map[i] >> 32) == kGlrMissing;
       }
