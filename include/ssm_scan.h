@@ -726,7 +726,8 @@ int ssm_layer_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps, double
  *               dstate_in
  *   dweight[d,k] = sum_{b,l} g[b,l,d] * x[b, l-(K-1)+k, d];  dbias[d] = sum_{b,l} g
  *
- *   sizes, in_dtype (of x), silu_activation and inputs as for the forward.
+ *   sizes, in_dtype (of x), silu_activation and inputs as for the forward, and
+ *   (K + 1) d < 2^28 (else SSM_E_UNSUPPORTED).
  *   dy        [B, L, d]   float32   gradient w.r.t. y
  *   dstate_out [B, d, K-1] float32  gradient w.r.t. state_out (optional, 0)
  *   dx        [B, L, d]   float32   output
@@ -767,7 +768,8 @@ int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
  * weight sigmoid(u).
  *
  *   batch, seqlen, dim         : B >= 0, 0 <= L < 2^30, 0 <= D < 2^23, B D <
- *                                2^30, B ceil(D / 64) ceil(L / 64) < 2^24
+ *                                2^30, and B ceil(D / 64), rounded up to a
+ *                                multiple of 8, times ceil(L / 64) < 2^24
  *                                (else SSM_E_UNSUPPORTED).
  *   in_dtype, out_dtype        : of x and the gates; of y. 0 float32, 1 bfloat16.
  *   flags                      : at most one of the gate's and one of the
@@ -796,7 +798,10 @@ int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
  *                                  backward would else compute again. Their
  *                                  layout is the library's own.
  *   workspace, workspace_bytes     at least ssm_gated_linear_workspace_bytes(),
- *                                  on a 16-byte boundary (NULL when 0)
+ *                                  on a 16-byte boundary (NULL when 0). Its tiles
+ *                                  wait for one another through it: calls that
+ *                                  may run at the same time need one each (their
+ *                                  results would be wrong, after some time).
  *
  * Element alignment suffices; rows on 16-byte boundaries are read fastest. All is
  * float32 between the inputs and y, which is rounded once. The decay's
@@ -850,7 +855,8 @@ int ssm_gated_linear_update(int64_t batch, int64_t dim, int in_dtype, int out_dt
  *   dh0       [B, D]     float32   output (optional)
  *   workspace, workspace_bytes     at least ssm_gated_linear_bwd_workspace_bytes()
  *                                  (with_states: 1 when states is given), on a
- *                                  16-byte boundary
+ *                                  16-byte boundary; one for each of calls that
+ *                                  may run at the same time
  * No output may overlap an input, another output or the workspace. Bitwise
  * deterministic.
  */

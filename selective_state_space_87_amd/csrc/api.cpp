@@ -1145,6 +1145,7 @@ int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
       !safe_mul(dim, width + 1, &most)) {
     return SSM_E_SHAPE;
   }
+  if (most >= (int64_t(1) << 28)) return SSM_E_UNSUPPORTED;  // the sums' launch: sixteen threads a column
   if (dim == 0 || (batch == 0 && dweight == nullptr && dbias == nullptr)) return SSM_OK;
   if (batch > 0 && weight == nullptr) return SSM_E_NULLPTR;
   if (bl > 0 && (x == nullptr || dy == nullptr || dx == nullptr)) return SSM_E_NULLPTR;

@@ -144,24 +144,31 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(const ConvBwdArgs a,
       }
     }
   };
-  // A step that may lie past the end, where there is no output: g is 0.
-  const auto edge = [&](int64_t t, int u, bool own, bool emit) __attribute__((always_inline)) {
-    float d[VC];
+  // N steps from t on, of which the last may lie past the end, where there is no
+  // output: g is 0. All loads come before the first step, those past the end from
+  // the last row: no branch stands between them.
+  const auto edges = [&](int64_t t, auto head) __attribute__((always_inline)) {
+    constexpr bool kHead = decltype(head)::value;  // the segment's first steps, else those behind the groups
+    float in[K][VC], d[K][VC];
 #pragma unroll
-    for (int c = 0; c < VC; ++c) x[u][c] = d[c] = 0.0f;
-    if (t < L) {
-      load_in<VC, BF16>(a.x, (row0 + t) * Dm + c0, x[u]);
-      load_in<VC, false>(a.dy, (row0 + t) * Dm + c0, d);
+    for (int u = 0; u < K; ++u) {
+      const int64_t row = row0 + (t + u < L ? t + u : L - 1);
+      load_in<VC, BF16>(a.x, row * Dm + c0, in[u]);
+      load_in<VC, false>(a.dy, row * Dm + c0, d[u]);
     }
-    step(t, u, d, t < L, own, emit);
+#pragma unroll
+    for (int u = 0; u < K; ++u) {
+      const bool live = t + u < L;
+#pragma unroll
+      for (int c = 0; c < VC; ++c) x[u][c] = live ? in[u][c] : 0.0f;
+      // the first K - 1 steps complete nothing of the segment's own: at the sequence's
+      // start the carried state's inputs
+      if (kHead || t + u < t1 + K - 1) step(t + u, u, d[u], live, t + u < t1, !kHead || u == K - 1 || t0 == 0);
+    }
   };
 
-  // The first K - 1 steps complete nothing of the segment's own: at the
-  // sequence's start the carried state's inputs.
-#pragma unroll
-  for (int u = 0; u < K - 1; ++u) edge(t0 + u, u, t0 + u < t1, t0 == 0);
-  if (t0 < t1) {
-    edge(t0 + K - 1, K - 1, t0 + K - 1 < t1, true);
+  if (L > 0) {  // (then t0 < t1)
+    edges(t0, std::true_type{});
     int64_t t = t0 + K;
     for (; t + kGroup <= t1; t += kGroup) {
       float in[kGroup][VC], d[kGroup][VC];
@@ -177,10 +184,14 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(const ConvBwdArgs a,
       }
     }
     // What is left of the segment, and the K - 1 steps behind it that complete its last dx.
-    for (; t < t1 + K - 1; t += K) {
+    for (; t < t1 + K - 1; t += K) edges(t, std::false_type{});
+  } else if (a.dstate_in) {  // no step: the state has passed through
 #pragma unroll
-      for (int u = 0; u < K; ++u) {
-        if (t + u < t1 + K - 1) edge(t + u, u, t + u < t1, true);
+    for (int c = 0; c < VC; ++c) {
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) {
+        const int64_t at = (b * Dm + c0 + c) * (K - 1) + j;
+        a.dstate_in[at] = a.dstate_out ? a.dstate_out[at] : 0.0f;
       }
     }
   }

@@ -22,8 +22,7 @@ template <bool BF16_IN, bool RES, bool BF16_OUT>
 __global__ __launch_bounds__(kThreads) void dropout_kernel(const DropoutArgs p) {
   const DropKey key = drop_key(p.drop.rng, p.drop.call, p.drop.threshold, p.drop.scale);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads * 8;
-  for (int64_t e = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 8; e < p.n; e += step) {
-    const int left = p.n - e < 8 ? static_cast<int>(p.n - e) : 8;
+  const auto piece = [&](int64_t e, int left) __attribute__((always_inline)) {
     float v[8], r[8];
     load_piece<BF16_IN>(p.x, e, left, v);
     if constexpr (RES) load_piece<BF16_OUT>(p.residual, e, left, r);
@@ -33,6 +32,13 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const DropoutArgs p) 
       for (int k = 0; k < 8; ++k) v[k] += r[k];
     }
     store_piece<BF16_OUT>(p.y, e, left, v);
+  };
+  for (int64_t e = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 8; e < p.n; e += step) {
+    if (p.n - e >= 8) {
+      piece(e, 8);  // no branch on the way: the loads are under way while the bits are drawn
+    } else {
+      piece(e, static_cast<int>(p.n - e));
+    }
   }
 }
 

@@ -54,7 +54,7 @@ __attribute__((weak)) int launch_gated_linear_bwd(const GatedLinearBwdArgs& a, v
 // (product of the decays, state from a zero start) a channel; a chain in the
 // workspace joins the pairs (gated_linear_tile.h): a word a tile and channel, and
 // one for every kGlrWindow tiles.
-constexpr int kGlrChannels = 64, kGlrFwdSteps = 128, kGlrBwdSteps = 64, kGlrWindow = 8;
+constexpr int kGlrChannels = 64, kGlrFwdSteps = 128, kGlrBwdSteps = 64, kGlrWindow = 4;
 constexpr int kGlrTicketBytes = 64;  // a count of its own line for every group
 
 // Whether a sequence is walked step by step instead, a thread four channels: a step
@@ -68,10 +68,12 @@ inline bool gated_linear_walks(int64_t batch, int64_t seqlen, int64_t dim) {
   return seqlen <= 12 || (seqlen <= kGlrBwdSteps && seqlen <= groups / 64);
 }
 
-// At most as many blocks of 256 threads as keep a launch below 2^32 threads.
+// At most as many blocks of 256 threads as keep a launch below 2^32 threads (the
+// groups of channels are rounded up to a multiple of 8, see GlrChainPlan).
 inline bool gated_linear_fits(int64_t batch, int64_t seqlen, int64_t dim) {
   const int64_t tiles = (seqlen + kGlrBwdSteps - 1) / kGlrBwdSteps;
-  return batch * ((dim + kGlrChannels - 1) / kGlrChannels) * (tiles > 0 ? tiles : 1) < (int64_t(1) << 24);
+  const int64_t groups = (batch * ((dim + kGlrChannels - 1) / kGlrChannels) + 7) / 8 * 8;
+  return groups * (tiles > 0 ? tiles : 1) < (int64_t(1) << 24);
 }
 
 struct GlrChainPlan {

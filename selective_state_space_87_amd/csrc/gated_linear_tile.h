@@ -22,8 +22,9 @@
 // group's), and tickets go along the chain: what a tile waits for is held by a block that
 // started earlier, which publishes its map before it waits, and its state after
 // waiting for earlier ones only; the first waits for nothing. A wait also
-// ends by itself, with NaN, after kGlrMostPolls tries (some seconds), should
-// two calls at once have been given the same workspace.
+// ends by itself, with NaN, after kGlrMostPolls tries (some 0.1 s, where 10 us are
+// usual), should two calls at once have been given the same workspace; a place
+// past the last tile, which a ticket could then be, has no steps.
 //
 // Data travel in the words themselves (64 bits: the map or the state and a mark),
 // so no fence is needed: a word is either not there (all ones, as cleared
@@ -39,7 +40,7 @@ namespace ssm {
 constexpr int kGlrThreads = 256;
 constexpr int kGlrRuns = kGlrThreads / kGlrChannels;  // runs of slices
 constexpr uint32_t kGlrMissing = 0xffffffffu;
-constexpr int kGlrMostPolls = 1 << 22;
+constexpr int kGlrMostPolls = 1 << 16;
 
 // ---- a thread's inputs of one step
 
@@ -265,36 +266,37 @@ __device__ __forceinline__ float glr_enter(const GlrChain& c, uint32_t group, ui
   };
   uint32_t high = __float_as_uint(P);
   if (high == kGlrMissing) high = 0x7fc00000u;  // one NaN for another
+  // h_final may be h0: the start has been read before the last tile, which waits for this map, can write it.
+  asm volatile("" : : "v"(start) : "memory");
   glr_put(c.maps + at(q), glr_word(S, high));
   const uint32_t window = q / kGlrWindow, j = q % kGlrWindow;
-  uint64_t map[kGlrWindow - 1], state = 0;
+  // All words are read at once, with no branch between (each read takes 1 us or more
+  // through the memory that the XCDs share): those that are not needed are this
+  // place's own.
+  const uint64_t* from[kGlrWindow];
 #pragma unroll
-  for (int i = 0; i < kGlrWindow - 1; ++i) map[i] = 0;
+  for (uint32_t i = 0; i < kGlrWindow - 1; ++i) from[i] = c.maps + at(i < j ? q - j + i : q);
+  from[kGlrWindow - 1] = window > 0 ? c.states + at(window - 1) : c.maps + at(q);
+  uint64_t word[kGlrWindow];
   for (int tries = 0;; ++tries) {
-    bool missing = false;
-    if (window > 0 && (tries == 0 || __any(static_cast<uint32_t>(state >> 32) == kGlrMissing))) {
-      state = glr_get(c.states + at(window - 1));
-      missing |= static_cast<uint32_t>(state >> 32) == kGlrMissing;
-    }
 #pragma unroll
-    for (uint32_t i = 0; i < kGlrWindow - 1; ++i) {
-      if (i < j && (tries == 0 || __any(static_cast<uint32_t>(map[i] >> 32) == kGlrMissing))) {
-        map[i] = glr_get(c.maps + at(q - j + i));
-        missing |= static_cast<uint32_t>(map[i] >> 32) == kGlrMissing;
-      }
-    }
+    for (uint32_t i = 0; i < kGlrWindow; ++i) word[i] = glr_get(from[i]);
+    bool missing = false;
+#pragma unroll
+    for (uint32_t i = 0; i < kGlrWindow; ++i) missing |= static_cast<uint32_t>(word[i] >> 32) == kGlrMissing;
     if (!__any(missing)) break;
     if (tries == kGlrMostPolls) {
       start = __uint_as_float(0x7fc00000u);
-      state = glr_word(start, 0);
+      word[kGlrWindow - 1] = glr_word(start, 0);
       break;
     }
     __builtin_amdgcn_s_sleep(1);
   }
-  float h = window > 0 ? __uint_as_float(static_cast<uint32_t>(state)) : start;
+  float h = window > 0 ? __uint_as_float(static_cast<uint32_t>(word[kGlrWindow - 1])) : start;
 #pragma unroll
   for (uint32_t i = 0; i < kGlrWindow - 1; ++i) {
-    if (i < j) h = fmaf(__uint_as_float(static_cast<uint32_t>(map[i] >> 32)), h, __uint_as_float(static_cast<uint32_t>(map[i])));
+    const float P0 = __uint_as_float(static_cast<uint32_t>(word[i] >> 32)), S0 = __uint_as_float(static_cast<uint32_t>(word[i]));
+    h = i < j ? fmaf(P0, h, S0) : h;
   }
   if (j == kGlrWindow - 1) glr_put(c.states + at(window), glr_word(fmaf(P, h, S), 0));
   return h;

@@ -143,6 +143,7 @@ def test_layer_norm_bwd(lib):
 def test_conv_bwd(lib):
     assert conv_bwd(lib, B=-1) == conv_bwd(lib, L=-1) == conv_bwd(lib, d=-1) == conv_bwd(lib, K=0) == E_SHAPE
     assert conv_bwd(lib, B=60000, L=1 << 20, d=1 << 30) == E_SHAPE
+    assert conv_bwd(lib, d=1 << 26, L=0, K=3) == E_UNSUPPORTED
     assert conv_bwd(lib, K=9) == conv_bwd(lib, B=65536) == conv_bwd(lib, L=4194241) == E_UNSUPPORTED
     assert conv_bwd(lib, ind=2) == E_DTYPE
     for name in ("x", "w", "dy", "dx"):
@@ -188,6 +189,8 @@ def test_recurrence_sizes_types_and_options(lib, call):
 
 def test_recurrence_forward(lib):
     assert rec(lib, L=-1) == E_SHAPE and rec(lib, L=1 << 30) == E_UNSUPPORTED
+    # eight groups of channels at least, times blocks of 64 steps: 2^24 are too many
+    assert rec(lib, B=1, L=1 << 27) == E_UNSUPPORTED and rec(lib, B=1, L=(1 << 27) - 64, y=None) == E_NULLPTR
     assert rec(lib, outd=2) == E_DTYPE
     assert rec(lib, ig=None, igs=0, y=None) == E_NULLPTR     # (the step of an absent gate does not count)
     for name, at in dict(h0=7, lens=8, y=9, hf=10).items():
