@@ -35,10 +35,9 @@ struct ConvBwdPlan {
   size_t bytes;
 };
 
-// As many segments as make kConvBwdWaves waves, 8 a CU: all at once (three times as
-// many fit with few registers, but not with four channels' filters, and a second
-// round of fewer waves costs more than it gives). Measured at (4, 8192, 4096, width
-// 4) bfloat16, where 512, 768, 1024, 2048 blocks of four waves: 263, 284, 302, 279 us.
+// As many segments as make kConvBwdWaves waves, 8 a CU: they are all there at once
+// (12 would fit at width 4, and 8 at width 8), and their parts are few. Measured at (4,
+// 8192, 4096, width 4) bfloat16: 2048, 3072, 4096, 8192 waves 263, 284, 302, 279 us.
 constexpr int64_t kConvBwdMinSeg = 16, kConvBwdMaxSeg = 512, kConvBwdWaves = 2048;
 
 inline ConvBwdPlan plan_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width) {

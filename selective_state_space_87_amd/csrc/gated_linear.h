@@ -17,9 +17,9 @@ namespace ssm {
 // The exponents are taken in base 2 and the parameters come scaled: A2 = A log2(e),
 // and for a sigmoid the bias as -bias log2(e), so that its exponent is one fused
 // product and sum. That exponent's rounding, and the bias's, are 2^-24 (|u| + |bias|) of
-// e^-u, and so of a gate far down the sigmoid: the two instructions a gate that
-// a compensated exponent takes more (of 30 an element) would cost 15% of the
-// forward's time for it.
+// e^-u, and so of a gate far down the sigmoid. A compensated exponent takes four
+// instructions more a gate, eight on the 37 an element that the forward has, which
+// fill 0.6 of its time: they are left out.
 
 // 1 - 2^t for t <= 0, given a = 2^t. Near 0 the difference would cancel: the Taylor
 // series of (e^x - 1) / x to x^5, x = t ln 2, is taken up to |x| = 1/4 (the first

@@ -53,7 +53,10 @@ __attribute__((weak)) int launch_gated_linear_bwd(const GatedLinearBwdArgs& a, v
 // kGlrBwdSteps backward, a block each. A tile's part of the recurrence is a pair
 // (product of the decays, state from a zero start) a channel; a chain in the
 // workspace joins the pairs (gated_linear_tile.h): a word a tile and channel, and
-// one for every kGlrWindow tiles.
+// one for every kGlrWindow tiles. Measured at (4, 8192, 4096) and (1, 65536, 2560)
+// bfloat16: tiles of 64 steps 238 and 372 us, of 128 steps 219 and 305 (backward 64
+// steps are what 163 registers hold); windows of 2, 3, 4, 5, 8, 16 tiles 213, 215, 214, 214,
+// 219, 236 us and 309, 296, 294 to 301, 292, 305, 323.
 constexpr int kGlrChannels = 64, kGlrFwdSteps = 128, kGlrBwdSteps = 64, kGlrWindow = 4;
 constexpr int kGlrTicketBytes = 64;  // a count of its own line for every group
 

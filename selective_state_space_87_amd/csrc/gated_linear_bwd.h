@@ -9,6 +9,10 @@
 // where the gradients are formed: the inputs stay in registers, what was made of
 // them would not fit. Its sums over steps are one part a tile, joined in double
 // in a fixed order (glr_sums_kernel).
+//
+// Bounded by HBM: (8, 2048, 1536) bfloat16 with both gates 112 us, 5.0 TB/s of the
+// inputs, dy and the three gradients; four channels a thread (eight, whose float32
+// gradients go in two stores each: 179 us with an earlier chain, four 134).
 #pragma once
 
 #include "gated_linear_tile.h"

@@ -16,7 +16,8 @@
 // before it and the maps from there on, all at once, and joins them in order.
 // So the input is read once, the joins are the same in every run (results are
 // deterministic), and the serial part is one exchange through memory every
-// kGlrWindow tiles.
+// kGlrWindow tiles. (Reading it twice, for the maps and for the states, would
+// take 14 bytes an element for 8.)
 //
 // Waiting always ends. A block takes its tile by a ticket (an atomic count of its
 // group's), and tickets go along the chain: what a tile waits for is held by a block that
@@ -304,8 +305,9 @@ __device__ __forceinline__ float glr_enter(const GlrChain& c, uint32_t group, ui
 
 // The block's place in its group's chain, or kGlrMissing for a block of no group.
 // Blocks of one group are `columns` apart, a multiple of 8, so that they run on one
-// XCD and the chain's words stay in its L2. A count a group: one for all
-// would be the bound, 12 ns a tile (33000 tiles 420 us).
+// XCD and neighbouring channels on the same: rows are read in pieces of some KB
+// (with neighbours on different XCDs (4, 8192, 4096) took 257 us in place of 239). A count
+// a group: one for all would be the bound, 12 ns a tile (33000 tiles 420 us).
 __device__ __forceinline__ uint32_t glr_ticket(const GlrChain& c, uint32_t* slot, uint32_t* group) {
   *group = blockIdx.x % 8 * (c.columns / 8) + blockIdx.x / 8 % (c.columns / 8);
   if (*group >= c.groups) return kGlrMissing;

@@ -10,7 +10,12 @@
 // four rows a block; above, a block of 4, 8 or 16 waves a row. The mean is
 // taken first, then the sums of the differences from it, their squares and
 // (backward) their products: a row far from zero loses nothing, and what the
-// first sum was rounded by is taken off as the mean of the differences.
+// first sum was rounded by is taken off as the mean of the differences. Blocks
+// take rows in turn, the weights staying in their registers. Measured: (32768,
+// 4096) bfloat16 with dropout and a float32 residual 295 us, 5.5 TB/s (a large copy
+// reaches 5.1); gradients of (32768, 4096) with a float32 residual 385 to 405 us, 5.3
+// to 5.6 TB/s; (1000, 1537) float32 10 us and 4 us for the sums. Streams past the caches
+// (nontemporal) took 332 us forward, a next row on its way backward 415 us.
 #include <hip/hip_runtime.h>
 
 #include "device_math.h"

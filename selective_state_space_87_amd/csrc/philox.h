@@ -2,9 +2,10 @@
 // "Parallel random numbers: as easy as 1, 2, 3", SC 2011). A block of eight
 // consecutive elements takes the four words at counter (block's low and high
 // word, step, call) under the 64-bit key `seed`: element e the (e mod 8)-th
-// half word, low half first. Sixteen bits an element: with 32, the ten rounds
-// would serve four elements and cost as much as the bytes of a bfloat16 array
-// take to cross HBM (some 35 issue slots an element against 30).
+// half word, low half first. Sixteen bits an element: the ten rounds (some 110
+// instructions, 20 of them products at a quarter of the rate) take 21 issue slots an
+// element so, where a bfloat16 array's 4 bytes take 30 slots' time to cross HBM; with
+// 32 bits they would serve four elements and take 42.
 #pragma once
 
 #include <hip/hip_runtime.h>
