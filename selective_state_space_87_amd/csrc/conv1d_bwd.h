@@ -37,7 +37,7 @@ struct ConvBwdPlan {
 
 // As many segments as make kConvBwdWaves waves, 8 a CU: they are all there at once
 // (12 would fit at width 4, and 8 at width 8), and their parts are few. Measured at (4,
-// 8192, 4096, width 4) bfloat16: 2048, 3072, 4096, 8192 waves 263, 284, 302, 279 us.
+// 8192, 4096, width 4) bfloat16: 8, 12, 16, 32 waves a CU 263, 284, 302, 279 us.
 constexpr int64_t kConvBwdMinSeg = 16, kConvBwdMaxSeg = 512, kConvBwdWaves = 2048;
 
 inline ConvBwdPlan plan_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width) {
