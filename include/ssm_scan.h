@@ -626,7 +626,7 @@ int ssm_rms_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps,
  * Philox4x32-10 (Salmon, Moraes, Dror, Shaw, SC 2011) at the 128-bit counter
  * (low and high word of e / 8, step, call) under the key `seed`; word (e mod 8)
  * / 2, its low half for even e. The share that is dropped is thus T / 65536, and the
- * factor is its exact counterpart. `seed` (64 bits) and `step` (its low 32 bits
+ * factor, a float32, its counterpart. `seed` (64 bits) and `step` (its low 32 bits
  * count) are read from DEVICE memory when the kernel runs: a captured call
  * draws anew in every replay before which the caller has changed them. The gradient
  * needs the values that the forward had. `call` tells the calls apart that

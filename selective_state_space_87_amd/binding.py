@@ -1163,7 +1163,8 @@ def ssm_gated_linear_fwd(x, gate, A, input_gate=None, gate_bias=None, input_bias
     column range of a wider dense array); A, gate_bias, input_bias: [D], h0:
     [B, D] float32; seqlens: [B] int32. ``states``: a float32 tensor of
     ssm_gated_linear_states_bytes() bytes, or True to allocate one, for
-    ssm_gated_linear_bwd. Returns y [B, L, D] or (y, h_final); with states, (y,
+    ssm_gated_linear_bwd. A given ``workspace`` serves one call at a time (none:
+    each call has its own). Returns y [B, L, D] or (y, h_final); with states, (y,
     h_final, states).
     """
     lib = _load()

@@ -23,7 +23,7 @@
 // group's), and tickets go along the chain: what a tile waits for is held by a block that
 // started earlier, which publishes its map before it waits, and its state after
 // waiting for earlier ones only; the first waits for nothing. A wait also
-// ends by itself, with NaN, after kGlrMostPolls tries (some 0.1 s, where 10 us are
+// ends by itself, with NaN, after kGlrMostPolls tries (some 0.4 s, where 10 us are
 // usual), should two calls at once have been given the same workspace; a place
 // past the last tile, which a ticket could then be, has no steps.
 //
@@ -41,7 +41,7 @@ namespace ssm {
 constexpr int kGlrThreads = 256;
 constexpr int kGlrRuns = kGlrThreads / kGlrChannels;  // runs of slices
 constexpr uint32_t kGlrMissing = 0xffffffffu;
-constexpr int kGlrMostPolls = 1 << 16;
+constexpr int kGlrMostPolls = 1 << 18;
 
 // ---- a thread's inputs of one step
 
