@@ -60,6 +60,22 @@ __attribute__((weak)) int launch_gated_linear_bwd(const GatedLinearBwdArgs& a, v
 constexpr int kGlrChannels = 64, kGlrFwdSteps = 128, kGlrBwdSteps = 64, kGlrWindow = 4;
 constexpr int kGlrTicketBytes = 64;  // a count of its own line for every group
 
+// The tile that a ticket is for: the first tiles first, backward the last first.
+// kGlrNoTile for a ticket past the last tile, whatever it is: two calls at once that
+// have been given the same workspace draw from one count, or find another call's words there.
+constexpr uint32_t kGlrNoTile = 0xffffffffu;
+constexpr uint32_t glr_tile_of(uint32_t ticket, uint32_t tiles, bool back) {
+  return ticket >= tiles ? kGlrNoTile : (back ? tiles - 1 - ticket : ticket);
+}
+
+// How many of `steps` steps lie in the tile of `size` steps from t0 on: at most size, 0
+// or less where they end before it. (A tile that glr_tile_of gives starts below 2^30, as
+// sequences are shorter: the difference fits. Taking it as 0 where it is less costs
+// the forward's kernel 2%, 217 us for 213 at (4, 8192, 4096) bfloat16.)
+constexpr int glr_steps_in(int64_t steps, int64_t t0, int size) {
+  return steps - t0 < size ? static_cast<int>(steps - t0) : size;
+}
+
 // Whether a sequence is walked step by step instead, a thread four channels: a step
 // takes 0.45 us however few the channels are, a tile as long for 1 step as for 64,
 // but blocks of many tiles are mostly idle. Measured, walked against tiles (us,

@@ -32,17 +32,16 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
   const GatedLinearArgs& p = q.f;
   uint32_t k = 0, group = blockIdx.x;
   if constexpr (CHAIN) {
-    k = glr_ticket(chain, &slot, &group);
-    if (k == kGlrMissing) return;
-    k = tiles - 1 - k;  // the last tiles first
+    k = glr_ticket<true>(chain, &slot, &group);
+    if (k == kGlrNoTile) return;
   }
   const GlrGroup at = glr_group(p, group);
   const int64_t t0 = static_cast<int64_t>(k) * kGlrBwdSteps;
   const int slice = threadIdx.x / Shape::kLanes;
   const int ch = static_cast<int>(threadIdx.x % Shape::kLanes) * VC, c = at.c0 + ch;
   const int left = static_cast<int>(p.dim) - c;
-  const int there = p.seqlen - t0 < kGlrBwdSteps ? static_cast<int>(p.seqlen - t0) : kGlrBwdSteps;
-  const int n = at.steps - t0 < there ? static_cast<int>(at.steps - t0) : there;
+  const int there = glr_steps_in(p.seqlen, t0, kGlrBwdSteps);
+  const int n = glr_steps_in(at.steps, t0, there);
   const int lane = threadIdx.x % kGlrChannels, run = threadIdx.x / kGlrChannels, ce = at.c0 + lane;
   float* part = parts + (static_cast<int64_t>(at.b) * tiles + k) * 3 * p.dim;
   if (n <= 0) {  // behind the row's end: gradients of 0, and nobody waits for it

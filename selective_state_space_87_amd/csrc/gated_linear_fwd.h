@@ -25,16 +25,16 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(const GatedLine
   __shared__ uint32_t slot;
   uint32_t k = 0, group = blockIdx.x;
   if constexpr (CHAIN) {
-    k = glr_ticket(chain, &slot, &group);
-    if (k == kGlrMissing) return;
+    k = glr_ticket<false>(chain, &slot, &group);
+    if (k == kGlrNoTile) return;
   }
   const GlrGroup at = glr_group(p, group);
   const int64_t t0 = static_cast<int64_t>(k) * kGlrFwdSteps;
   const int slice = threadIdx.x / Shape::kLanes;
   const int c = at.c0 + static_cast<int>(threadIdx.x % Shape::kLanes) * VC;
   const int left = static_cast<int>(p.dim) - c;
-  const int there = p.seqlen - t0 < kGlrFwdSteps ? static_cast<int>(p.seqlen - t0) : kGlrFwdSteps;  // steps of the array
-  const int n = at.steps - t0 < there ? static_cast<int>(at.steps - t0) : there;                    // of the batch row
+  const int there = glr_steps_in(p.seqlen, t0, kGlrFwdSteps);  // steps of the array
+  const int n = glr_steps_in(at.steps, t0, there);             // of the batch row
   const auto put = [&](int s, int wide, const float (&v)[VC]) __attribute__((always_inline)) {
     const int64_t to = (at.row0 + t0 + s) * p.dim + c;
     if (p.out_bf16) {

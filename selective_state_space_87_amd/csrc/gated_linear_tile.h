@@ -24,8 +24,8 @@
 // started earlier, which publishes its map before it waits, and its state after
 // waiting for earlier ones only; the first waits for nothing. A wait also
 // ends by itself, with NaN, after kGlrMostPolls tries (some 0.4 s, where 10 us are
-// usual), should two calls at once have been given the same workspace; a place
-// past the last tile, which a ticket could then be, has no steps.
+// usual), should two calls at once have been given the same workspace; a block
+// whose ticket, then, is past the last tile does nothing.
 //
 // Data travel in the words themselves (64 bits: the map or the state and a mark),
 // so no fence is needed: a word is either not there (all ones, as cleared
@@ -238,14 +238,14 @@ struct GlrChain {
   uint32_t* tickets;  // a count a group, kGlrTicketBytes apart
   uint64_t* maps;     // [tile][group][64]: S, and P (never all ones) above
   uint64_t* states;   // [window][group][64]: the state, and 0 above
-  uint32_t groups, columns;
+  uint32_t groups, columns, tiles;
 };
 
 inline GlrChain glr_chain(const GlrChainPlan& p, void* workspace) {
   char* w = static_cast<char*>(workspace);
   return GlrChain{reinterpret_cast<uint32_t*>(w), reinterpret_cast<uint64_t*>(w + p.off_words),
                   reinterpret_cast<uint64_t*>(w + p.off_states), static_cast<uint32_t>(p.groups),
-                  static_cast<uint32_t>(p.columns)};
+                  static_cast<uint32_t>(p.columns), static_cast<uint32_t>(p.tiles)};
 }
 
 __device__ __forceinline__ uint64_t glr_word(float low, uint32_t high) {
@@ -303,17 +303,18 @@ __device__ __forceinline__ float glr_enter(const GlrChain& c, uint32_t group, ui
   return h;
 }
 
-// The block's place in its group's chain, or kGlrMissing for a block of no group.
+// The block's tile of its group's chain, or kGlrNoTile for a block of no group.
 // Blocks of one group are `columns` apart, a multiple of 8, so that they run on one
 // XCD and neighbouring channels on the same: rows are read in pieces of some KB
 // (with neighbours on different XCDs (4, 8192, 4096) took 257 us in place of 239). A count
 // a group: one for all would be the bound, 12 ns a tile (33000 tiles 420 us).
+template <bool BACK>
 __device__ __forceinline__ uint32_t glr_ticket(const GlrChain& c, uint32_t* slot, uint32_t* group) {
   *group = blockIdx.x % 8 * (c.columns / 8) + blockIdx.x / 8 % (c.columns / 8);
-  if (*group >= c.groups) return kGlrMissing;
+  if (*group >= c.groups) return kGlrNoTile;
   if (threadIdx.x == 0) *slot = atomicAdd(c.tickets + *group * (kGlrTicketBytes / 4), 1u);
   __syncthreads();
-  return *slot;
+  return glr_tile_of(*slot, c.tiles, BACK);
 }
 
 // Clears a chain's words to "not there" and its count to 0 (a kernel, not a memset: graphs take it).
