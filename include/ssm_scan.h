@@ -804,9 +804,10 @@ int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
  *                                  results would be wrong, after some time).
  *
  * Element alignment suffices; rows on 16-byte boundaries are read fastest. All is
- * float32 between the inputs and y, which is rounded once. The decay's
- * rounding, 2^-24 of it, is one of the recurrence's: where a channel's a stays near
- * 1, h can be off by some 2^-24 / (1 - a) of itself at worst. Results are
+ * float32 between the inputs and y, which is rounded once. A gate is within 2^-24
+ * (16 + |u|) of itself: u is a float32 sum, and its rounding alone is |u| of that. The
+ * decay's rounding, 2^-24 of it, is one of the recurrence's: where a channel's a stays
+ * near 1, h can be off by some 2^-24 / (1 - a) of itself at worst. Results are
  * bitwise deterministic. A value that is not finite stays in its channel of its
  * batch row, and does not reach an earlier step.
  */

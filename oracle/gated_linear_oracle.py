@@ -8,12 +8,11 @@ the state, its y is 0.
 
 With the results come their rooms: how far a float32 evaluation may be off, by
 counting roundings (E = 2^-24 relative each) through the same recurrences on
-magnitudes. A gate is off by (16 + 1.25 (|u| + |bias|)) E of itself: the rounding
-of u log2(e), or of the bias times log2(e) and their sum, is |u| E + |bias| E of e^-u, the
-constant's own 0.22 E as many times; an exponential, a logarithm, a reciprocal
-and sums are 16 E. la = A g is off by one E more, a by |la| times that and 3 E more, w
-by the gate's and 24 E (what 1 - a cancels is at most 5-fold), v by 12 E and its gate's
-1.25 (|u| + |bias|) E. A state takes these, and one rounding a step; joins of tiles, a second
+magnitudes. A gate is off by (16 + |u|) E of itself: the sum u is off by E |u|, which
+is as much of e^-u; an exponential, a logarithm, a reciprocal and sums are 16 E. la = A g
+is off by one E more, a by |la| times that and 3 E more, w by the gate's and 24 E (what 1
+- a cancels is at most 5-fold), v by 12 E and its gate's |u| E. A state takes these, and
+one rounding a step; joins of tiles, a second
 evaluation and another order of the sums are covered by twice that and 16 E of
 the magnitude. bfloat16 outputs are the caller's to add.
 """
@@ -67,11 +66,10 @@ class _Parts:
             A, g, slope, la, a, w, dw, x, s, t)
         self.v = x * s
         # relative errors
-        bias = lambda b: 0.0 if b is None else np.abs(_f64(b))  # noqa: E731
-        self.rg = ((16 + 1.25 * (np.abs(u) + bias(gate_bias))) * curve + 1) * E
+        self.rg = ((16 + np.abs(u)) * curve + 1) * E
         self.ra = np.abs(la) * (self.rg + 4 * E) + 3 * E
         self.rw = self.rg + 24 * E if scale is not None else 0 * a
-        self.rv = (12 + 1.25 * (np.abs(ui) + bias(input_bias))) * E
+        self.rv = (12 + np.abs(ui)) * E
         self.rdw = 2 * self.ra + self.rw + 8 * E
 
 

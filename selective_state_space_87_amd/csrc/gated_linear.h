@@ -14,64 +14,81 @@
 
 namespace ssm {
 
-// The exponents are taken in base 2 and the parameters come scaled: A2 = A log2(e),
-// and for a sigmoid the bias as -bias log2(e), so that its exponent is one fused
-// product and sum. That exponent's rounding, and the bias's, are 2^-24 (|u| + |bias|) of
-// e^-u, and so of a gate far down the sigmoid. A compensated exponent takes four
-// instructions more a gate, eight on the 37 an element that the forward has, which
-// fill 0.6 of its time: they are left out.
+// The decay's exponent is taken in base 2 and its parameter comes scaled: A2 = A log2(e).
+//
+// A gate's exponential e^y, y = -u or -|u|, is compensated: with t = y log2(e), rounded,
+// e^y = 2^t e^(y - t ln 2), and what is left, y - t ln 2, is one fused product and sum
+// (ln 2's own rounding is 0.05 2^-24 |y| of it) and at most 1.3 2^-24 |y|, so that e^y is
+// 2^t q with q = 1 + y - t ln 2. Without q a gate far down the sigmoid would be off by that
+// much beside what the sum u was rounded by. It takes five instructions more a gate, 47
+// for 37 an element with both, which the loads hide ((4, 8192, 4096) bfloat16 212 us; one
+// tile of 64 rows, 64 us for 62); e^-|u| as gated_delta.h takes it costs ten (238 us).
+struct GlrExp {
+  float e, q;  // 2^t and q: the product is left to what takes it
+};
+__device__ __forceinline__ GlrExp glr_exp(float y, float t) { return GlrExp{exp2_hw(t), 1.0f + fmaf(t, -kLn2, y)}; }
 
-// 1 - 2^t for t <= 0, given a = 2^t. Near 0 the difference would cancel: the Taylor
-// series of (e^x - 1) / x to x^5, x = t ln 2, is taken up to |x| = 1/4 (the first
-// dropped term, x^6 / 5040, is below 2^-24 there); beyond, `far` is off by some
+// 1 - 2^(TIMES t) for t <= 0. Near 0 the difference would cancel: the Taylor series of
+// (e^x - 1) / x to x^5, x = TIMES t ln 2, is taken up to |x| = 1/4 (the first dropped term,
+// x^6 / 5040, is below 2^-24 there); beyond, `far`, the difference itself, is off by some
 // 2^-24 / 0.22.
+template <int TIMES>
 __device__ __forceinline__ float one_minus_exp2(float t, float far) {
-  constexpr float l = kLn2, l2 = l * l, l3 = l2 * l, l4 = l3 * l, l5 = l4 * l, l6 = l5 * l;
+  constexpr float l = TIMES * kLn2, l2 = l * l, l3 = l2 * l, l4 = l3 * l, l5 = l4 * l, l6 = l5 * l;
   const float s = fmaf(fmaf(fmaf(fmaf(fmaf(t, -l6 / 720.0f, -l5 / 120.0f), t, -l4 / 24.0f), t, -l3 / 6.0f), t,
                             -l2 / 2.0f), t, -l);
-  return fabsf(t) < 0.25f * kLog2e ? t * s : far;
+  return fabsf(t) < 0.25f / TIMES * kLog2e ? t * s : far;
 }
 
-// sigmoid(x + bias), given -bias log2(e). (e is infinite below -88: 0.)
-__device__ __forceinline__ float glr_sigmoid(float x, float nb) { return rcp_hw(1.0f + exp2_hw(fmaf(x, -kLog2e, nb))); }
-
-// The same with its derivative s (1 - s) = e s^2, which keeps what is left of it
-// where s is near 1. (The exponent ends at 126: 0 times infinity would be NaN.)
-__device__ __forceinline__ float glr_sigmoid_slope(float x, float nb, float* slope) {
-  float t = fmaf(x, -kLog2e, nb);
-  t = t > 126.0f ? 126.0f : t;
-  const float e = exp2_hw(t), r = rcp_hw(1.0f + e);
-  *slope = e * r * r;
-  return r;
+// e^-u, of which the sigmoid is made: u ends at 88, where the sigmoid is 1 (infinity would
+// leave NaN behind it), and t at 126, where it is 0: q then takes the value beyond
+// float32 for u = -infinity. NaN stays, by the first minimum or in q.
+__device__ __forceinline__ GlrExp glr_sigmoid_exp(float u) {
+  u = __builtin_elementwise_minimum(u, 88.0f);
+  return glr_exp(-u, fminf(u * -kLog2e, 126.0f));
+}
+__device__ __forceinline__ float glr_sigmoid(float u) {
+  const GlrExp v = glr_sigmoid_exp(u);
+  return rcp_hw(fmaf(v.e, v.q, 1.0f));
+}
+// The same with its derivative s (1 - s) = s (e^-u s), which keeps what is left of it
+// where s is near 1. (Where s is 0, infinity times it: the minimum makes 1 of that.)
+__device__ __forceinline__ float glr_sigmoid_slope(float u, float* slope) {
+  const GlrExp v = glr_sigmoid_exp(u);
+  const float s = rcp_hw(fmaf(v.e, v.q, 1.0f));
+  *slope = s * fminf(v.e * v.q * s, 1.0f);
+  return s;
 }
 
 // max(u, 0) + log1p(v), v = e^-|u|, as in softplus_f; the slope is sigmoid(u).
 __device__ __forceinline__ float glr_softplus(float u, float* slope) {
-  const float v = exp2_hw(-fabsf(u) * kLog2e), w = 1.0f + v;
+  const float y = __builtin_elementwise_maximum(-fabsf(u), -126.0f);
+  const GlrExp x = glr_exp(y, y * kLog2e);
+  const float v = x.e * x.q, w = 1.0f + v;
   if (slope != nullptr) *slope = (u < 0.0f ? v : 1.0f) * rcp_hw(w);
   return fmaxf(u, 0.0f) + fmaf(log2_hw(w), kLn2, v - (w - 1.0f));
 }
 
-// Value of the gate (and its derivative) given its raw value and the scaled bias.
+// Value of the gate (and its derivative).
 template <int ACT>
-__device__ __forceinline__ float gate_value(float x, float bias) {
+__device__ __forceinline__ float gate_value(float u) {
   if constexpr (ACT == kGateSoftplus) {
-    return glr_softplus(x + bias, nullptr);
+    return glr_softplus(u, nullptr);
   } else if constexpr (ACT == kGateSigmoid) {
-    return glr_sigmoid(x, bias);
+    return glr_sigmoid(u);
   } else {
-    return x + bias;
+    return u;
   }
 }
 template <int ACT>
-__device__ __forceinline__ float gate_value_slope(float x, float bias, float* slope) {
+__device__ __forceinline__ float gate_value_slope(float u, float* slope) {
   if constexpr (ACT == kGateSoftplus) {
-    return glr_softplus(x + bias, slope);
+    return glr_softplus(u, slope);
   } else if constexpr (ACT == kGateSigmoid) {
-    return glr_sigmoid_slope(x, bias, slope);
+    return glr_sigmoid_slope(u, slope);
   } else {
     *slope = 1.0f;
-    return x + bias;
+    return u;
   }
 }
 
@@ -79,15 +96,17 @@ __device__ __forceinline__ float gate_value_slope(float x, float bias, float* sl
 template <int SCALE>
 __device__ __forceinline__ float input_weight(float t, float a) {
   if constexpr (SCALE == kInputNorm) {
-    return __builtin_amdgcn_sqrtf(one_minus_exp2(2.0f * t, fmaf(-a, a, 1.0f)));
+    return __builtin_amdgcn_sqrtf(one_minus_exp2<2>(t, fmaf(-a, a, 1.0f)));
   } else if constexpr (SCALE == kInputComplement) {
-    return one_minus_exp2(t, 1.0f - a);
+    return one_minus_exp2<1>(t, 1.0f - a);
   } else {
     return 1.0f;
   }
 }
 
-// dw / d(ln a). Where a is 1 the square root has no derivative: 0 is taken.
+// dw / d(ln a). Where a is 1 the square root has no derivative: 0 is taken. (The hardware's
+// reciprocal is off by one unit in the last place, half a unit more than a division of
+// ten instructions; w itself is off by several where 1 - a^2 cancels.)
 template <int SCALE>
 __device__ __forceinline__ float input_weight_slope(float a, float w) {
   if constexpr (SCALE == kInputNorm) {

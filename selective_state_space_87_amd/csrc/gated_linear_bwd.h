@@ -68,26 +68,29 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
   float dy[TS][VC], a[TS][VC], b[TS][VC];
   const bool whole = n == kGlrBwdSteps && at.c0 + kGlrChannels <= p.dim;
   par.load(p, c, left);  // first, since loads come in order: what needs it need not wait for all of the tile
-  raw.load(p, at.row0 + t0, c, left, slice * TS, n, whole);
-  {
+  // Each path computes for itself: where they have met all loads are waited for (training
+  // step (8, 2048, 1536) 173.5 us for 170).
+  const auto take = [&](auto all) __attribute__((always_inline)) {
+    constexpr bool kAll = decltype(all)::value;
+    raw.load(p, at.row0 + t0, c, left, slice * TS, n, kAll);
     const int64_t from = (at.row0 + t0 + slice * TS) * p.dim + c;
     typename GlrPack<false, VC>::Words d[TS];
-    if (whole) {
 #pragma unroll
-      for (int i = 0; i < TS; ++i) d[i] = glr_load<false, VC>(q.dy, from + i * p.dim, VC);
-    } else {
-#pragma unroll
-      for (int i = 0; i < TS; ++i) d[i] = glr_load<false, VC>(q.dy, from + i * p.dim, slice * TS + i < n ? left : 0);
-    }
+    for (int i = 0; i < TS; ++i) d[i] = glr_load<false, VC>(q.dy, from + i * p.dim, kAll ? VC : (slice * TS + i < n ? left : 0));
+    glr_elements<BF16, ACT, SCALE, GATED, TS, VC>(raw, par, a, b);
+    if constexpr (!kAll) glr_mask<TS, VC>(slice * TS, n, a, b);
 #pragma unroll
     for (int i = 0; i < TS; ++i) {
 #pragma unroll
       for (int v = 0; v < VC; ++v) dy[i][v] = __uint_as_float(d[i][v]);
     }
+  };
+  if (whole) {
+    take(std::true_type{});
+  } else {
+    take(std::false_type{});
   }
   {
-    glr_elements<BF16, ACT, SCALE, GATED, TS, VC>(raw, par, a, b);
-    if (!whole) glr_mask<TS, VC>(slice * TS, n, a, b);
     float P[VC], S[VC], R[VC];
 #pragma unroll
     for (int v = 0; v < VC; ++v) {
@@ -157,6 +160,7 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
   }
   __syncthreads();
 
+  raw.template forget<ACT>();
   float before[TS][VC], E[VC], sumA[VC], sumg[VC], sumi[VC];
 #pragma unroll
   for (int v = 0; v < VC; ++v) {
@@ -178,10 +182,10 @@ __global__ __launch_bounds__(kGlrThreads) void glr_bwd_kernel(const GatedLinearB
     for (int v = 0; v < VC; ++v) {
       const float D = dy[i][v] + E[v];
       float slope, islope = 0.0f, in = glr_elem<BF16>(raw.x[i], v), sig = 1.0f;
-      const float g = gate_value_slope<ACT>(glr_elem<BF16>(raw.gate[i], v), par.gbias[v], &slope);
+      const float g = gate_value_slope<ACT>(glr_elem<BF16>(raw.gate[i], v) + par.gbias[v], &slope);
       const float w = input_weight<SCALE>(par.A2[v] * g, a[i][v]);
       const float dv = on ? w * D : 0.0f;
-      if constexpr (GATED) sig = glr_sigmoid_slope(glr_elem<BF16>(raw.igate[i], v), par.ibias[v], &islope);
+      if constexpr (GATED) sig = glr_sigmoid_slope(glr_elem<BF16>(raw.igate[i], v) + par.ibias[v], &islope);
       dx[v] = dv * sig;
       di[v] = dv * in * islope;
       const float dla = on ? D * fmaf(a[i][v], before[i][v], input_weight_slope<SCALE>(a[i][v], w) * (in * sig)) : 0.0f;

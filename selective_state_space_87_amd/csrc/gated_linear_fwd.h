@@ -35,8 +35,9 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(const GatedLine
   const int left = static_cast<int>(p.dim) - c;
   const int there = glr_steps_in(p.seqlen, t0, kGlrFwdSteps);  // steps of the array
   const int n = glr_steps_in(at.steps, t0, there);             // of the batch row
+  int cy = c;
   const auto put = [&](int s, int wide, const float (&v)[VC]) __attribute__((always_inline)) {
-    const int64_t to = (at.row0 + t0 + s) * p.dim + c;
+    const int64_t to = (at.row0 + t0 + s) * p.dim + cy;
     if (p.out_bf16) {
       glr_store<true, VC>(p.y, to, wide, v);
     } else {
@@ -60,10 +61,18 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(const GatedLine
     GlrRaw<BF16, GATED, VC, TS> raw;
     GlrParams<VC, ACT, GATED> par;
     par.load(p, c, left);  // first, since loads come in order: the first step's gates need not wait for the last's
-    raw.load(p, at.row0 + t0, c, left, slice * TS, n, whole);
-    glr_elements<BF16, ACT, SCALE, GATED, TS, VC>(raw, par, a, b);
+    // In the chain a tile that is whole computes on its own path: where two paths have
+    // met all loads are waited for ((4, 8192, 4096) bfloat16 212 us for 220). Of a sequence
+    // in one tile that costs more registers than it gains (60 rows of 100 steps 62 us for 57).
+    if (CHAIN && whole) {
+      raw.load(p, at.row0 + t0, c, left, slice * TS, n, true);
+      glr_elements<BF16, ACT, SCALE, GATED, TS, VC>(raw, par, a, b);
+    } else {
+      raw.load(p, at.row0 + t0, c, left, slice * TS, n, !CHAIN && whole);
+      glr_elements<BF16, ACT, SCALE, GATED, TS, VC>(raw, par, a, b);
+      if (CHAIN || !whole) glr_mask<TS, VC>(slice * TS, n, a, b);
+    }
   }
-  if (!whole) glr_mask<TS, VC>(slice * TS, n, a, b);
 #pragma unroll
   for (int v = 0; v < VC; ++v) {
     P[v] = 1.0f, S[v] = 0.0f;
@@ -121,6 +130,7 @@ __global__ __launch_bounds__(kGlrThreads, 4) void glr_fwd_kernel(const GatedLine
   }
   __syncthreads();
   if (p.y == nullptr) return;
+  asm volatile("" : "+v"(cy));  // y's addresses are made here, not kept from the loads on (some forms would spill)
 #pragma unroll
   for (int v = 0; v < VC; ++v) S[v] = ls[slice][ch + v];
   if (whole) {
