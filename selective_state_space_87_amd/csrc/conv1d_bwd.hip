@@ -211,17 +211,17 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(const ConvBwdArgs a,
 }
 
 // dweight[d, k], dbias[d] = sums over the parts: 64 of the (K + 1) d columns a
-// block, sixteen waves each adding every sixteenth part, eight loads at a time,
-// then the sixteen sums in order.
+// block, sixteen waves each adding every sixteenth part in double, eight loads at a
+// time, then the sixteen sums in order.
 constexpr int kSumWaves = 16;
 __global__ __launch_bounds__(64 * kSumWaves) void conv1d_bwd_sums_kernel(const float* __restrict__ parts,
                                                                          int64_t nparts, int64_t dim, int width,
                                                                          float* __restrict__ dweight,
                                                                          float* __restrict__ dbias) {
-  __shared__ float sums[kSumWaves][64];
+  __shared__ double sums[kSumWaves][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane, cols = (width + 1) * dim;
-  float acc = 0.0f;
+  double acc = 0.0;
   if (c < cols) {
     int64_t i = w;
     for (; i + 7 * kSumWaves < nparts; i += 8 * kSumWaves) {
@@ -236,14 +236,14 @@ __global__ __launch_bounds__(64 * kSumWaves) void conv1d_bwd_sums_kernel(const f
   sums[w][lane] = acc;
   __syncthreads();
   if (w == 0 && c < cols) {
-    float v = 0.0f;
+    double v = 0.0;
 #pragma unroll
     for (int k = 0; k < kSumWaves; ++k) v += sums[k][lane];
     const int64_t k = c / dim, d = c - k * dim;
     if (k < width) {
-      if (dweight != nullptr) dweight[d * width + k] = v;
+      if (dweight != nullptr) dweight[d * width + k] = static_cast<float>(v);
     } else if (dbias != nullptr) {
-      dbias[d] = v;
+      dbias[d] = static_cast<float>(v);
     }
   }
 }
