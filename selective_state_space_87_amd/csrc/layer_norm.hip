@@ -240,17 +240,17 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_bwd_kernel(cons
 }
 
 // dweight[c], dbias[c] = sums over the blocks' parts: 64 of the 2 dim columns a
-// block, sixteen waves each adding every sixteenth part, eight loads at a time,
-// then the sixteen sums in order.
+// block, sixteen waves each adding every sixteenth part in double, eight loads at a
+// time, then the sixteen sums in order.
 constexpr int kSumWaves = 16;
 __global__ __launch_bounds__(64 * kSumWaves) void layer_norm_sums_kernel(const float* __restrict__ parts, int nparts,
                                                                          int dim, float* __restrict__ dweight,
                                                                          float* __restrict__ dbias) {
-  __shared__ float sums[kSumWaves][64];
+  __shared__ double sums[kSumWaves][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int c = static_cast<int>(blockIdx.x) * 64 + lane;
   const int64_t step = 2 * static_cast<int64_t>(dim);
-  float acc = 0.0f;
+  double acc = 0.0;
   if (c < 2 * dim) {
     int i = w;
     for (; i + 7 * kSumWaves < nparts; i += 8 * kSumWaves) {
@@ -265,13 +265,13 @@ __global__ __launch_bounds__(64 * kSumWaves) void layer_norm_sums_kernel(const f
   sums[w][lane] = acc;
   __syncthreads();
   if (w == 0 && c < 2 * dim) {
-    float v = 0.0f;
+    double v = 0.0;
 #pragma unroll
     for (int k = 0; k < kSumWaves; ++k) v += sums[k][lane];
     if (c < dim) {
-      if (dweight != nullptr) dweight[c] = v;
+      if (dweight != nullptr) dweight[c] = static_cast<float>(v);
     } else if (dbias != nullptr) {
-      dbias[c - dim] = v;
+      dbias[c - dim] = static_cast<float>(v);
     }
   }
 }

@@ -1,0 +1,81 @@
+"""How the layer norm's gradients of its parameters are added up over the rows: at row
+counts where a block takes many rows, in both layouts (four rows of up to 1024 elements
+at a time, one of more).
+
+A sum takes 64 roundings on the way to its block's part (a row each, or a row of each of
+four waves and their join), one for every 64 rows more of the block's, is joined in
+double and rounded once: with T turns of a block, at most (64 + T / 64 + 4) 2^-24 of the
+terms' magnitudes.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from selective_state_space_87_amd import binding
+
+pytestmark = pytest.mark.gpu
+E = 2.0 ** -24
+BLOCKS = 512
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no HIP device")
+
+
+def turns(rows, dim):
+    groups = -(-rows // (4 if dim <= 1024 else 1))
+    return -(-groups // min(groups, BLOCKS))
+
+
+def roundings(rows, dim):
+    return 64 + turns(rows, dim) / 64 + 4
+
+
+@pytest.mark.parametrize("rows,dim,least", [(20000, 64, 9), (9001, 1000, 5), (33000, 1100, 65), (300001, 17, 147),
+                                            (131075, 8, 64), (40001, 1025, 79), (2050, 16384, 5), (70003, 1537, 137)])
+@pytest.mark.parametrize("st", [torch.float32, torch.bfloat16])
+def test_parameters_over_many_rows(rows, dim, least, st):
+    assert turns(rows, dim) >= least
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    s, dy, w = (0.5 + rn(rows, dim)).to(st), 1.0 + rn(rows, dim), 1 + 0.1 * rn(dim)
+    got = binding.ssm_layer_norm_bwd(s, w, dy)
+    # the definition in float64, some rows at a time
+    dw, db, mw, mb = (torch.zeros(dim, dtype=torch.float64, device="cuda") for _ in range(4))
+    ma = torch.zeros_like(mw)
+    for a in range(0, rows, 8192):
+        d = s[a:a + 8192].double()
+        d -= d.mean(-1, keepdim=True)
+        n = d / torch.sqrt((d * d).mean(-1, keepdim=True) + 1e-5)
+        y = dy[a:a + 8192].double()
+        dw += (y * n).sum(0)
+        db += y.sum(0)
+        mw += (y * n).abs().sum(0)
+        mb += y.abs().sum(0)
+    # a value n is off by 3e-6 of itself and 1.5e-6 (derived for the forward's y)
+    room = roundings(rows, dim) * E * mw + 3e-6 * mw + 1.5e-6 * mb
+    assert ((got["dweight"].double() - dw).abs() <= room).all()
+    assert ((got["dbias"].double() - db).abs() <= roundings(rows, dim) * E * mb).all()
+    # and the oracle itself, of the last rows alone
+    last = slice(rows - 40, rows)
+    ref = oracle.layer_norm_bwd(s[last].double().cpu().numpy(), w.double().cpu().numpy(), dy[last].double().cpu().numpy())
+    one = binding.ssm_layer_norm_bwd(s[last].clone(), w, dy[last].clone())
+    assert torch.equal(got["ds"][last], one["ds"])
+    assert np.abs(one["dbias"].double().cpu().numpy() - ref[2]).max() <= 70 * E * float(dy[last].abs().sum(0).max())
+
+
+@pytest.mark.parametrize("rows,dim", [(20000, 64), (9001, 1000), (32767, 1100), (131071, 8), (30000, 4096)])
+def test_whole_numbers_are_rounded_once(rows, dim):
+    # up to 64 turns a block: its sums stay below 2^24, and are exact
+    assert turns(rows, dim) <= 64
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    dy = torch.randint(0, 16384, (rows, dim), generator=g, device="cuda")
+    s = torch.randn(rows, dim, generator=g, device="cuda")
+    got = binding.ssm_layer_norm_bwd(s, None, dy.float())
+    want = dy.sum(0)
+    assert (want > 2 ** 24).all()
+    assert np.array_equal(got["dbias"].cpu().numpy(), want.cpu().numpy().astype(np.float32))
