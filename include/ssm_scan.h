@@ -709,6 +709,9 @@ int ssm_layer_norm_fwd(int64_t rows, int64_t dim, int in_dtype, int res_dtype, i
  *   workspace, workspace_bytes  at least ssm_layer_norm_bwd_workspace_bytes(),
  *                               on a 16-byte boundary (NULL when neither
  *                               dweight nor dbias is given)
+ * The sums over rows are taken in float32, 64 turns of a block at a time (a row each;
+ * four up to 1024 elements; 512 blocks at most), and joined in double: with T turns a
+ * block, within (68 + T / 64) 2^-24 of the terms' magnitudes. Deterministic.
  */
 size_t ssm_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
 int ssm_layer_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps, double p, uint32_t call,

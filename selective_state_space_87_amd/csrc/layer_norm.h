@@ -73,4 +73,7 @@ inline int64_t layer_norm_bwd_blocks(int64_t rows, int64_t dim) {
   return groups < 512 ? groups : 512;
 }
 
+// Turns of a block (a row each, or four) after which its sums go to second ones.
+constexpr int64_t kLayerNormFold = 64;
+
 }  // namespace ssm

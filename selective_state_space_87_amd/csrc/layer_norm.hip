@@ -110,8 +110,12 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_kernel(const La
 }
 
 // Gradients. A block takes every gridDim.x-th row (or four rows, one a wave)
-// and keeps its parts of dweight and dbias in registers; the parts are added by
-// layer_norm_sums_kernel in block order.
+// and keeps its sums of dweight and dbias in registers. Every kLayerNormFold turns they
+// are added to second sums, so that a sum takes that many roundings and one for every
+// kLayerNormFold turns, not one a row. The second sums are registers too where four rows
+// go to a block, where 64 turns may take no more than 100 us (10^6 rows of 64) and adding
+// through the workspace 2; of longer rows, whose registers are full, they are the block's
+// part in the workspace. The parts are added by layer_norm_sums_kernel in block order.
 template <int TPR, int NPK, bool BF16>
 __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_bwd_kernel(const LayerNormBwdArgs p) {
   constexpr int kRows = block_threads(TPR) / TPR, kWaves = TPR / 64;
@@ -127,93 +131,115 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_bwd_kernel(cons
     for (int k = 0; k < 8; ++k) dw[i][k] = db[i][k] = 0.0f, w[i][k] = 1.0f;
     if (p.weight != nullptr) load_piece<false>(p.weight, e, dim - e, w[i]);
   }
+  float dw2[NPK][8] = {}, db2[NPK][8] = {};  // (kRows > 1)
   DropKey key{};
   if (p.dx != nullptr && p.drop.threshold != 0) {
     key = drop_key(p.drop.rng, p.drop.call, p.drop.threshold, p.drop.scale);
   }
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + part; row < p.rows;
-       row += static_cast<int64_t>(gridDim.x) * kRows) {
-    const int64_t at = row * dim;
-    float s[NPK][8], g[NPK][8], o[NPK][8], sum[1] = {0.0f};
+  // parts [block][dweight, dbias][dim]
+  float* out = static_cast<float*>(p.workspace) + static_cast<int64_t>(blockIdx.x) * 2 * dim;
+  // A piece of the part: written the first time, added to afterwards, by the same thread.
+  const auto keep = [&](int at, int left, float (&v)[8], bool first) __attribute__((always_inline)) {
+    if (!first) {
+      float before[8];
+      load_piece<false>(out, at, left, before);
 #pragma unroll
-    for (int i = 0; i < NPK; ++i) {
-      const int e = (i * TPR + t) * 8;
-      load_piece<BF16>(p.s, at + e, dim - e, s[i]);
+      for (int k = 0; k < 8; ++k) v[k] += before[k];
     }
-#pragma unroll
-    for (int i = 0; i < NPK; ++i) {
-      const int e = (i * TPR + t) * 8;
-      load_piece<false>(p.dy, at + e, dim - e, g[i]);
-    }
-    if (p.dresidual != nullptr) {
+    store_piece<false>(out, at, left, v);
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  bool first = true;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + part; row < p.rows; first = false) {
+    const int64_t fold = p.rows - row < kLayerNormFold * step ? p.rows : row + kLayerNormFold * step;
+    for (; row < fold; row += step) {
+      const int64_t at = row * dim;
+      float s[NPK][8], g[NPK][8], o[NPK][8], sum[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < NPK; ++i) {
         const int e = (i * TPR + t) * 8;
-        load_piece<false>(p.dresidual, at + e, dim - e, o[i]);
+        load_piece<BF16>(p.s, at + e, dim - e, s[i]);
       }
-    } else {
+#pragma unroll
+      for (int i = 0; i < NPK; ++i) {
+        const int e = (i * TPR + t) * 8;
+        load_piece<false>(p.dy, at + e, dim - e, g[i]);
+      }
+      if (p.dresidual != nullptr) {
+#pragma unroll
+        for (int i = 0; i < NPK; ++i) {
+          const int e = (i * TPR + t) * 8;
+          load_piece<false>(p.dresidual, at + e, dim - e, o[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NPK; ++i) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[i][k] = 0.0f;
+        }
+      }
 #pragma unroll
       for (int i = 0; i < NPK; ++i) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[i][k] = 0.0f;
+        for (int k = 0; k < 8; ++k) sum[0] += s[i][k];
+      }
+      row_sums<TPR>(sum, sum_slots);
+      const float mean = sum[0] * inv;
+      float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // of d, d^2, u, u d
+#pragma unroll
+      for (int i = 0; i < NPK; ++i) {
+        const int left = dim - (i * TPR + t) * 8;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          s[i][k] = k < left ? s[i][k] - mean : 0.0f;
+          const float u = g[i][k] * w[i][k];
+          sums[0] += s[i][k];
+          sums[1] = fmaf(s[i][k], s[i][k], sums[1]);
+          sums[2] += u;
+          sums[3] = fmaf(u, s[i][k], sums[3]);
+        }
+      }
+      row_sums<TPR>(sums, product_slots);
+      const float rest = sums[0] * inv, mu = sums[2] * inv;
+      const float var = fmaf(-rest, rest, sums[1] * inv);
+      const float r = rsqrtf((var < 0.0f ? 0.0f : var) + p.eps);
+      const float c = fmaf(-rest, mu, sums[3] * inv) * r;  // mean(u n)
+#pragma unroll
+      for (int i = 0; i < NPK; ++i) {
+        const int e = (i * TPR + t) * 8;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float n = (s[i][k] - rest) * r;
+          dw[i][k] = fmaf(g[i][k], n, dw[i][k]);
+          db[i][k] += g[i][k];
+          o[i][k] = fmaf(r, fmaf(g[i][k], w[i][k], -mu) - n * c, o[i][k]);
+        }
+        store_piece<false>(p.ds, at + e, dim - e, o[i]);
+        if (p.dx != nullptr && e < dim) {
+          if (p.drop.threshold != 0) drop8(key, static_cast<uint64_t>(at + e), o[i]);
+          store_piece<false>(p.dx, at + e, dim - e, o[i]);
+        }
       }
     }
+    if (p.dweight == nullptr && p.dbias == nullptr) continue;
 #pragma unroll
     for (int i = 0; i < NPK; ++i) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum[0] += s[i][k];
-    }
-    row_sums<TPR>(sum, sum_slots);
-    const float mean = sum[0] * inv;
-    float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // of d, d^2, u, u d
-#pragma unroll
-    for (int i = 0; i < NPK; ++i) {
-      const int left = dim - (i * TPR + t) * 8;
+      if constexpr (kRows == 1) {
+        const int e = (i * TPR + t) * 8;
+        keep(e, dim - e, dw[i], first);
+        keep(dim + e, dim - e, db[i], first);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        s[i][k] = k < left ? s[i][k] - mean : 0.0f;
-        const float u = g[i][k] * w[i][k];
-        sums[0] += s[i][k];
-        sums[1] = fmaf(s[i][k], s[i][k], sums[1]);
-        sums[2] += u;
-        sums[3] = fmaf(u, s[i][k], sums[3]);
-      }
-    }
-    row_sums<TPR>(sums, product_slots);
-    const float rest = sums[0] * inv, mu = sums[2] * inv;
-    const float var = fmaf(-rest, rest, sums[1] * inv);
-    const float r = rsqrtf((var < 0.0f ? 0.0f : var) + p.eps);
-    const float c = fmaf(-rest, mu, sums[3] * inv) * r;  // mean(u n)
-#pragma unroll
-    for (int i = 0; i < NPK; ++i) {
-      const int e = (i * TPR + t) * 8;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float n = (s[i][k] - rest) * r;
-        dw[i][k] = fmaf(g[i][k], n, dw[i][k]);
-        db[i][k] += g[i][k];
-        o[i][k] = fmaf(r, fmaf(g[i][k], w[i][k], -mu) - n * c, o[i][k]);
-      }
-      store_piece<false>(p.ds, at + e, dim - e, o[i]);
-      if (p.dx != nullptr && e < dim) {
-        if (p.drop.threshold != 0) drop8(key, static_cast<uint64_t>(at + e), o[i]);
-        store_piece<false>(p.dx, at + e, dim - e, o[i]);
+        if constexpr (kRows > 1) dw2[i][k] += dw[i][k], db2[i][k] += db[i][k];
+        dw[i][k] = db[i][k] = 0.0f;
       }
     }
   }
-  if (p.dweight == nullptr && p.dbias == nullptr) return;
-  // parts [block][dweight, dbias][dim]
-  float* out = static_cast<float*>(p.workspace) + static_cast<int64_t>(blockIdx.x) * 2 * dim;
-  if constexpr (kRows == 1) {
-#pragma unroll
-    for (int i = 0; i < NPK; ++i) {
-      const int e = (i * TPR + t) * 8;
-      store_piece<false>(out, e, dim - e, dw[i]);
-      store_piece<false>(out, dim + e, dim - e, db[i]);
-    }
-  } else {
+  if constexpr (kRows > 1) {
+    if (p.dweight == nullptr && p.dbias == nullptr) return;
     __shared__ float adds[kRows][NPK * 8 * TPR];
-    const auto add = [&](float (&v)[NPK][8], int64_t to) {
+    const auto add = [&](float (&v)[NPK][8], int to) {
 #pragma unroll
       for (int i = 0; i < NPK; ++i) {
 #pragma unroll
@@ -234,8 +260,8 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_bwd_kernel(cons
       }
       __syncthreads();
     };
-    add(dw, 0);
-    add(db, dim);
+    add(dw2, 0);
+    add(db2, dim);
   }
 }
 

@@ -79,3 +79,19 @@ def test_whole_numbers_are_rounded_once(rows, dim):
     want = dy.sum(0)
     assert (want > 2 ** 24).all()
     assert np.array_equal(got["dbias"].cpu().numpy(), want.cpu().numpy().astype(np.float32))
+
+
+@pytest.mark.parametrize("rows,dim", [(1 << 22, 8), (1 << 20, 1026)])
+def test_sums_of_one_sign_do_not_drift(rows, dim):
+    """2048 turns a block: one value added 2048 times in float32 is off by 270 roundings of the sum."""
+    assert turns(rows, dim) == 2048
+    value = np.float32(0.1)
+    s = torch.zeros(rows, dim, dtype=torch.bfloat16, device="cuda")
+    s[:, ::2] = 1.0
+    dy = torch.full((rows, dim), float(value), device="cuda")
+    got = binding.ssm_layer_norm_bwd(s, None, dy)
+    want = float(value) * rows
+    assert float((got["dbias"].double() - want).abs().max()) <= roundings(rows, dim) * E * want
+    n = 0.5 / np.sqrt(0.25 + 1e-5)
+    sign = torch.where(torch.arange(dim, device="cuda") % 2 == 0, 1.0, -1.0).double()
+    assert float((got["dweight"].double() - sign * n * want).abs().max()) <= (roundings(rows, dim) * E + 4.5e-6) * want
