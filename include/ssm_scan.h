@@ -730,7 +730,7 @@ int ssm_layer_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps, double
  *   dweight[d,k] = sum_{b,l} g[b,l,d] * x[b, l-(K-1)+k, d];  dbias[d] = sum_{b,l} g
  *
  *   sizes, in_dtype (of x), silu_activation and inputs as for the forward, and
- *   (K + 1) d < 2^28 (else SSM_E_UNSUPPORTED).
+ *   (K + 1) d <= 2^28 - 64 (else SSM_E_UNSUPPORTED).
  *   dy        [B, L, d]   float32   gradient w.r.t. y
  *   dstate_out [B, d, K-1] float32  gradient w.r.t. state_out (optional, 0)
  *   dx        [B, L, d]   float32   output

@@ -1145,7 +1145,8 @@ int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
       !safe_mul(dim, width + 1, &most)) {
     return SSM_E_SHAPE;
   }
-  if (most >= (int64_t(1) << 28)) return SSM_E_UNSUPPORTED;  // the sums' launch: sixteen threads a column
+  // the sums' launch has 1024 threads for every 64 columns begun, and a launch fewer than 2^32
+  if ((most + 63) / 64 >= (int64_t(1) << 22)) return SSM_E_UNSUPPORTED;
   if (dim == 0 || (batch == 0 && dweight == nullptr && dbias == nullptr)) return SSM_OK;
   if (batch > 0 && weight == nullptr) return SSM_E_NULLPTR;
   if (bl > 0 && (x == nullptr || dy == nullptr || dx == nullptr)) return SSM_E_NULLPTR;
