@@ -20,6 +20,8 @@ constexpr int64_t kMaxCkptState = 16;  // forward checkpoints: the backward's ti
 constexpr int64_t kMaxElems = int64_t(1) << 52;
 constexpr int64_t kMaxConvWidth = 8;
 constexpr int64_t kMaxConvSeq = int64_t(65535) * 64;  // 65535 segments of 64 steps
+// (the gradients' segments are another dimension of a launch's blocks)
+static_assert(kMaxConvSeq / ssm::kConvBwdMaxSeg < 65535 && ssm::kConvBwdWaves <= 65535);
 
 struct Range {
   uintptr_t lo = 0, hi = 0;  // [lo, hi); empty when lo == hi

@@ -36,8 +36,9 @@ struct ConvBwdPlan {
 };
 
 // As many segments as make kConvBwdWaves waves, 8 a CU: they are all there at once
-// (12 would fit at width 4, and 8 at width 8), and their parts are few. Measured at (4,
-// 8192, 4096, width 4) bfloat16: 8, 12, 16, 32 waves a CU 263, 284, 302, 279 us.
+// (12 would fit at width 4, and 8 at width 8), and their parts are few. Measured (the call)
+// at (4, 8192, 4096, width 4): 8, 12, 16, 32 waves a CU 250, 280, 265, 266 us in bfloat16,
+// 298, 331, 345, 341 in float32; (1, 4096, 2560) bfloat16 33, 37, 37, 36.
 constexpr int64_t kConvBwdMinSeg = 16, kConvBwdMaxSeg = 512, kConvBwdWaves = 2048;
 
 inline ConvBwdPlan plan_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width) {
@@ -47,7 +48,6 @@ inline ConvBwdPlan plan_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, i
   const int64_t wanted = ceil_div(kConvBwdWaves, groups > 0 ? groups : 1);
   int64_t seg = ceil_div(ceil_div(seqlen, wanted), 16) * 16;
   seg = seg < kConvBwdMinSeg ? kConvBwdMinSeg : (seg > kConvBwdMaxSeg ? kConvBwdMaxSeg : seg);
-  while (ceil_div(seqlen, seg) > 65535) seg *= 2;
   p.seg = seg;
   p.segs = seqlen > 0 ? ceil_div(seqlen, seg) : 1;
   p.bytes = static_cast<size_t>(batch * p.segs) * static_cast<size_t>((width + 1) * dim) * 4;
