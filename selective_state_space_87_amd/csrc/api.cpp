@@ -1235,7 +1235,8 @@ int glr_options(const GlrSizes& z, int64_t rows, int in_dtype, int flags, int64_
   }
   if (!gated) igate_step = z.dim;
   if (x_step < z.dim || gate_step < z.dim || igate_step < z.dim) return SSM_E_SHAPE;
-  // the rows of a tile of steps are addressed with 32-bit offsets
+  // The limit on D holds for the steps too. (The kernels address with 64 bits; it keeps the
+  // rows of a tile, 128 of float32, within 2^32 bytes of the first.)
   constexpr int64_t most = int64_t(1) << 23;
   if (x_step >= most || gate_step >= most || igate_step >= most) return SSM_E_UNSUPPORTED;
   int64_t t;

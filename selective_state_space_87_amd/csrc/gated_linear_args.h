@@ -54,9 +54,9 @@ __attribute__((weak)) int launch_gated_linear_bwd(const GatedLinearBwdArgs& a, v
 // (product of the decays, state from a zero start) a channel; a chain in the
 // workspace joins the pairs (gated_linear_tile.h): a word a tile and channel, and
 // one for every kGlrWindow tiles. Measured at (4, 8192, 4096) and (1, 65536, 2560)
-// bfloat16: tiles of 64 steps 238 and 372 us, of 128 steps 219 and 305 (backward 64
-// steps are what 163 registers hold); windows of 2, 3, 4, 5, 8, 16 tiles 213, 215, 214, 214,
-// 219, 236 us and 309, 296, 294 to 301, 292, 305, 323.
+// bfloat16: tiles of 64 steps 229 and 363 us, of 128 steps 214 and 295 (backward 64
+// steps are what 142 to 157 registers hold); windows of 2, 3, 4, 5, 8, 16 tiles 215, 215, 214,
+// 216, 217, 230 us and 310, 300, 295, 294, 292, 312.
 constexpr int kGlrChannels = 64, kGlrFwdSteps = 128, kGlrBwdSteps = 64, kGlrWindow = 4;
 constexpr int kGlrTicketBytes = 64;  // a count of its own line for every group
 
@@ -77,11 +77,11 @@ constexpr int glr_steps_in(int64_t steps, int64_t t0, int size) {
 }
 
 // Whether a sequence is walked step by step instead, a thread four channels: a step
-// takes 0.45 us however few the channels are, a tile as long for 1 step as for 64,
-// but blocks of many tiles are mostly idle. Measured, walked against tiles (us,
-// bfloat16): 1 x 2560 channels, 8, 12, 16, 64 steps 6.1, 7.8, 9.5, 31 against 8.6
-// throughout; 16 x 2560 6.3, 8.4, 11.8, 44 against 12.8; 128 x 4096 9.8, 13.7, 17.7, 60
-// against 87 (float32, 64 steps: 95 against 113).
+// takes 0.5 us however few the channels are, a tile as long for 1 step as for 64,
+// but blocks of many tiles are mostly idle. Measured, walked against tiles (us in the
+// kernel, bfloat16): 1 x 2560 channels, 8, 12, 16, 64 steps 5.8, 7.6, 9.6, 32 against 9
+// throughout; 16 x 2560 6.5, 8.4, 10, 39 against 15; 128 x 4096 10, 14, 17, 65 against 100
+// (float32, 64 steps: 93 against 110).
 inline bool gated_linear_walks(int64_t batch, int64_t seqlen, int64_t dim) {
   const int64_t groups = batch * ((dim + kGlrChannels - 1) / kGlrChannels);
   return seqlen <= 12 || (seqlen <= kGlrBwdSteps && seqlen <= groups / 64);
