@@ -19,6 +19,7 @@
 // of zero in front of a narrower filter would make 0 * infinity of what they meet.
 #include <hip/hip_runtime.h>
 
+#include "column_sums.h"
 #include "conv1d_bwd.h"
 #include "device_math.h"
 
@@ -210,43 +211,21 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(const ConvBwdArgs a,
   }
 }
 
-// dweight[d, k], dbias[d] = sums over the parts: 64 of the (K + 1) d columns a
-// block, sixteen waves each adding every sixteenth part in double, eight loads at a
-// time, then the sixteen sums in order.
-constexpr int kSumWaves = 16;
-__global__ __launch_bounds__(64 * kSumWaves) void conv1d_bwd_sums_kernel(const float* __restrict__ parts,
-                                                                         int64_t nparts, int64_t dim, int width,
-                                                                         float* __restrict__ dweight,
-                                                                         float* __restrict__ dbias) {
-  __shared__ double sums[kSumWaves][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane, cols = (width + 1) * dim;
-  double acc = 0.0;
-  if (c < cols) {
-    int64_t i = w;
-    for (; i + 7 * kSumWaves < nparts; i += 8 * kSumWaves) {
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = parts[(i + k * kSumWaves) * cols + c];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc += v[k];
-    }
-    for (; i < nparts; i += kSumWaves) acc += parts[i * cols + c];
-  }
-  sums[w][lane] = acc;
-  __syncthreads();
-  if (w == 0 && c < cols) {
-    double v = 0.0;
-#pragma unroll
-    for (int k = 0; k < kSumWaves; ++k) v += sums[k][lane];
+// Columns [k, then bias][channel] of the parts: dweight is [channel][k].
+struct StoreFilters {
+  float* dweight;
+  float* dbias;
+  int64_t dim, width;
+
+  __device__ __forceinline__ void operator()(int64_t c, float v) const {
     const int64_t k = c / dim, d = c - k * dim;
     if (k < width) {
-      if (dweight != nullptr) dweight[d * width + k] = static_cast<float>(v);
+      if (dweight != nullptr) dweight[d * width + k] = v;
     } else if (dbias != nullptr) {
-      dbias[d] = static_cast<float>(v);
+      dbias[d] = v;
     }
   }
-}
+};
 
 template <int K, bool BF16>
 void launch_width(const ConvBwdArgs& a, const ConvBwdPlan& p, hipStream_t st) {
@@ -288,10 +267,8 @@ int launch_conv1d_bwd(const ConvBwdArgs& a, void* stream) {
     if (const hipError_t e = hipGetLastError()) return static_cast<int>(e);
   }
   if (a.dweight != nullptr || a.dbias != nullptr) {
-    const int64_t cols = (a.width + 1) * a.dim;
-    conv1d_bwd_sums_kernel<<<static_cast<unsigned>((cols + 63) / 64), 64 * kSumWaves, 0, st>>>(
-        static_cast<const float*>(a.workspace), a.batch * p.segs, a.dim, static_cast<int>(a.width), a.dweight,
-        a.dbias);
+    launch_column_sums(a.workspace, a.batch * p.segs, (a.width + 1) * a.dim,
+                       StoreFilters{a.dweight, a.dbias, a.dim, a.width}, st);
   }
   return static_cast<int>(hipGetLastError());
 }

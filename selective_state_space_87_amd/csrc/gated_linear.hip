@@ -1,8 +1,9 @@
 // Gated linear recurrence: the step-by-step kernel (single tokens and short
-// sequences), the sums of the parameters' gradients, and the launchers; the tiles
-// of long sequences are in gated_linear_{fwd,bwd}.h.
+// sequences), and the launchers; the tiles of long sequences are in
+// gated_linear_{fwd,bwd}.h.
 #include <hip/hip_runtime.h>
 
+#include "column_sums.h"
 #include "gated_linear_tile.h"
 
 namespace ssm {
@@ -67,39 +68,6 @@ __global__ __launch_bounds__(kGlrThreads) void glr_clear_kernel(uint4* words, in
   }
 }
 
-// dA, dgate_bias, dinput_bias: 64 of the 3 D columns a block, sixteen waves each
-// adding every sixteenth tile's part in double, then the sixteen sums in order.
-constexpr int kSumWaves = 16;
-__global__ __launch_bounds__(64 * kSumWaves) void glr_sums_kernel(const float* __restrict__ parts, int64_t nparts,
-                                                                  int64_t dim, float* dA, float* dgbias,
-                                                                  float* dibias) {
-  __shared__ double sums[kSumWaves][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane, cols = 3 * dim;
-  double acc = 0.0;
-  if (c < cols) {
-    int64_t i = w;
-    for (; i + 7 * kSumWaves < nparts; i += 8 * kSumWaves) {
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = parts[(i + k * kSumWaves) * cols + c];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc += v[k];
-    }
-    for (; i < nparts; i += kSumWaves) acc += parts[i * cols + c];
-  }
-  sums[w][lane] = acc;
-  __syncthreads();
-  if (w == 0 && c < cols) {
-    double v = 0.0;
-#pragma unroll
-    for (int k = 0; k < kSumWaves; ++k) v += sums[k][lane];
-    const int64_t which = c / dim;
-    float* out = which == 0 ? dA : (which == 1 ? dgbias : dibias);
-    if (out != nullptr) out[c - which * dim] = static_cast<float>(v);
-  }
-}
-
 }  // namespace
 
 void launch_glr_clear(const GlrChainPlan& p, void* workspace, hipStream_t st) {
@@ -138,10 +106,8 @@ int launch_gated_linear_bwd(const GatedLinearBwdArgs& given, void* stream) {
     a.f.in_bf16 ? launch_glr_bwd<true>(a, plan, st) : launch_glr_bwd<false>(a, plan, st);
     if (const hipError_t e = hipGetLastError()) return static_cast<int>(e);
   }
-  const int64_t cols = 3 * a.f.dim;
-  glr_sums_kernel<<<static_cast<unsigned>((cols + 63) / 64), 64 * kSumWaves, 0, st>>>(
-      reinterpret_cast<const float*>(static_cast<const char*>(a.f.workspace) + plan.off_parts),
-      a.f.batch * plan.chain.tiles, a.f.dim, a.dA, a.dgbias, a.dibias);
+  launch_column_sums(static_cast<const char*>(a.f.workspace) + plan.off_parts, a.f.batch * plan.chain.tiles, 3 * a.f.dim,
+                     StoreRows<3>{{a.dA, a.dgbias, a.dibias}, a.f.dim}, st);
   return static_cast<int>(hipGetLastError());
 }
 

@@ -70,8 +70,7 @@ constexpr uint32_t glr_tile_of(uint32_t ticket, uint32_t tiles, bool back) {
 
 // How many of `steps` steps lie in the tile of `size` steps from t0 on: at most size, 0
 // or less where they end before it. (A tile that glr_tile_of gives starts below 2^30, as
-// sequences are shorter: the difference fits. Taking it as 0 where it is less costs
-// the forward's kernel 2%, 217 us for 213 at (4, 8192, 4096) bfloat16.)
+// sequences are shorter: the difference fits 32 bits.)
 constexpr int glr_steps_in(int64_t steps, int64_t t0, int size) {
   return steps - t0 < size ? static_cast<int>(steps - t0) : size;
 }

@@ -8,7 +8,7 @@
 // recurrences through its slices at once, and computes its gates a second time
 // where the gradients are formed: the inputs stay in registers, what was made of
 // them would not fit. Its sums over steps are one part a tile, joined in double
-// in a fixed order (glr_sums_kernel).
+// in a fixed order (column_sums.h).
 //
 // Bounded by HBM: (8, 2048, 1536) bfloat16 with both gates 112 us, 5.0 TB/s of the
 // inputs, dy and the three gradients; four channels a thread (eight, whose float32

@@ -18,6 +18,7 @@
 // (nontemporal) took 332 us forward, a next row on its way backward 415 us.
 #include <hip/hip_runtime.h>
 
+#include "column_sums.h"
 #include "device_math.h"
 #include "layer_norm.h"
 #include "philox.h"
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_kernel(const La
 // kLayerNormFold turns, not one a row. The second sums are registers too where four rows
 // go to a block, where 64 turns may take no more than 100 us (10^6 rows of 64) and adding
 // through the workspace 2; of longer rows, whose registers are full, they are the block's
-// part in the workspace. The parts are added by layer_norm_sums_kernel in block order.
+// part in the workspace. The parts are added in block order (column_sums.h).
 template <int TPR, int NPK, bool BF16>
 __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_bwd_kernel(const LayerNormBwdArgs p) {
   constexpr int kRows = block_threads(TPR) / TPR, kWaves = TPR / 64;
@@ -265,43 +266,6 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_bwd_kernel(cons
   }
 }
 
-// dweight[c], dbias[c] = sums over the blocks' parts: 64 of the 2 dim columns a
-// block, sixteen waves each adding every sixteenth part in double, eight loads at a
-// time, then the sixteen sums in order.
-constexpr int kSumWaves = 16;
-__global__ __launch_bounds__(64 * kSumWaves) void layer_norm_sums_kernel(const float* __restrict__ parts, int nparts,
-                                                                         int dim, float* __restrict__ dweight,
-                                                                         float* __restrict__ dbias) {
-  __shared__ double sums[kSumWaves][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int c = static_cast<int>(blockIdx.x) * 64 + lane;
-  const int64_t step = 2 * static_cast<int64_t>(dim);
-  double acc = 0.0;
-  if (c < 2 * dim) {
-    int i = w;
-    for (; i + 7 * kSumWaves < nparts; i += 8 * kSumWaves) {
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = parts[(i + k * kSumWaves) * step + c];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc += v[k];
-    }
-    for (; i < nparts; i += kSumWaves) acc += parts[i * step + c];
-  }
-  sums[w][lane] = acc;
-  __syncthreads();
-  if (w == 0 && c < 2 * dim) {
-    double v = 0.0;
-#pragma unroll
-    for (int k = 0; k < kSumWaves; ++k) v += sums[k][lane];
-    if (c < dim) {
-      if (dweight != nullptr) dweight[c] = static_cast<float>(v);
-    } else if (dbias != nullptr) {
-      dbias[c - dim] = static_cast<float>(v);
-    }
-  }
-}
-
 // f(threads per row, pieces a thread) for a row of `dim` elements. WIDE: of a row
 // above 8192 elements (backward 4 pieces on 512 threads: the 128 registers that 1024
 // threads leave each would not hold a row's three arrays and the two sums).
@@ -358,9 +322,9 @@ int launch_layer_norm(const LayerNormArgs& a, void* stream) {
 
 int launch_layer_norm_bwd(const LayerNormBwdArgs& a, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  int nparts = 0;
+  int64_t nparts = 0;
   if (a.rows > 0) {
-    nparts = static_cast<int>(layer_norm_bwd_blocks(a.rows, a.dim));
+    nparts = layer_norm_bwd_blocks(a.rows, a.dim);
     by_width<512>(a.dim, [&](auto tpr, auto npk) {
       constexpr int TPR = decltype(tpr)::value, NPK = decltype(npk)::value, kBlock = block_threads(TPR);
       const unsigned blocks = static_cast<unsigned>(nparts);
@@ -370,9 +334,7 @@ int launch_layer_norm_bwd(const LayerNormBwdArgs& a, void* stream) {
     if (const hipError_t e = hipGetLastError()) return static_cast<int>(e);
   }
   if (a.dweight != nullptr || a.dbias != nullptr) {
-    const unsigned blocks = static_cast<unsigned>((2 * a.dim + 63) / 64);
-    layer_norm_sums_kernel<<<blocks, 64 * kSumWaves, 0, st>>>(static_cast<const float*>(a.workspace), nparts,
-                                                              static_cast<int>(a.dim), a.dweight, a.dbias);
+    launch_column_sums(a.workspace, nparts, 2 * a.dim, StoreRows<2>{{a.dweight, a.dbias}, a.dim}, st);
   }
   return static_cast<int>(hipGetLastError());
 }
