@@ -786,7 +786,9 @@ int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
  *   x, gate   [B, L, D]  in_dtype
  *   input_gate [B, L, D] in_dtype  (optional)
  *   A         [D]        float32   expected A g <= 0 (a decay above 1 grows, and
- *                                  sqrt(1 - a^2) is NaN then)
+ *                                  sqrt(1 - a^2) is NaN then; where the product of
+ *                                  such decays over 128 steps passes float32's
+ *                                  range, a state of 0 becomes NaN too)
  *   gate_bias, input_bias [D] float32 (optional, 0; the latter is used with an
  *                                  input gate only)
  *   h0        [B, D]     float32   initial state (optional, 0)
@@ -804,8 +806,10 @@ int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
  *   workspace, workspace_bytes     at least ssm_gated_linear_workspace_bytes(),
  *                                  on a 16-byte boundary (NULL when 0). Its tiles
  *                                  wait for one another through it: calls that
- *                                  may run at the same time need one each (their
- *                                  results would be wrong, after some time).
+ *                                  may run at the same time need one each. (Two
+ *                                  that share one end, after some time, with wrong
+ *                                  results, NaN among them, and no status says so;
+ *                                  nothing outside their arrays is touched.)
  *
  * Element alignment suffices; rows on 16-byte boundaries are read fastest. All is
  * float32 between the inputs and y, which is rounded once. A gate is within 2^-24
@@ -813,7 +817,10 @@ int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
  * decay's rounding, 2^-24 of it, is one of the recurrence's: where a channel's a stays
  * near 1, h can be off by some 2^-24 / (1 - a) of itself at worst. Results are
  * bitwise deterministic. A value that is not finite stays in its channel of its
- * batch row, and does not reach an earlier step.
+ * batch row, and does not reach an earlier step. An infinite state does not become
+ * finite again; it becomes NaN at a decay of 0 and, where a sequence is not taken step by
+ * step, wherever the product of the decays over some steps is 0 in float32: which of the
+ * two it is can differ with the sequence's length.
  */
 size_t ssm_gated_linear_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
 size_t ssm_gated_linear_states_bytes(int64_t batch, int64_t seqlen, int64_t dim);

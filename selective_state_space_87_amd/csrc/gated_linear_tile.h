@@ -17,7 +17,9 @@
 // So the input is read once, the joins are the same in every run (results are
 // deterministic), and the serial part is one exchange through memory every
 // kGlrWindow tiles. (Reading it twice, for the maps and for the states, would
-// take 14 bytes an element for 8.)
+// take 14 bytes an element for 8.) Where P underflows to 0, a finite state loses less than
+// 2^-149 of itself; an infinite one becomes NaN, where step by step it stays infinite.
+// (Telling such a P from a decay of 0 would take instructions an element.)
 //
 // Waiting always ends. A block takes its tile by a ticket (an atomic count of its
 // group's), and tickets go along the chain: what a tile waits for is held by a block that
