@@ -95,3 +95,22 @@ def test_sums_of_one_sign_do_not_drift(rows, dim):
     n = 0.5 / np.sqrt(0.25 + 1e-5)
     sign = torch.where(torch.arange(dim, device="cuda") % 2 == 0, 1.0, -1.0).double()
     assert float((got["dweight"].double() - sign * n * want).abs().max()) <= (roundings(rows, dim) * E + 4.5e-6) * want
+
+
+def test_sums_of_more_elements_than_32_bits_count():
+    """Few rows with a gradient among 530000 without one: 1036 turns a block, 2^31 elements and more."""
+    rows, dim = 530000, 4100
+    g = torch.Generator(device="cuda").manual_seed(3)
+    at = torch.tensor([0, 511, 512, 40 * 512 + 7, 523775, 523776, rows - 1], device="cuda")
+    s = torch.full((rows, dim), 0.5, device="cuda", dtype=torch.bfloat16)
+    dy = torch.zeros(rows, dim, device="cuda")
+    s[at] = torch.randn(len(at), dim, generator=g, device="cuda").bfloat16()
+    dy[at] = torch.randn(len(at), dim, generator=g, device="cuda")
+    got = binding.ssm_layer_norm_bwd(s, None, dy)
+    d = s[at].double()
+    d -= d.mean(-1, keepdim=True)
+    n, y = d / torch.sqrt((d * d).mean(-1, keepdim=True) + 1e-5), dy[at].double()
+    # (a row of one value has no n: what rounding leaves of it meets a gradient of 0)
+    room = (3e-6 + 8 * E) * (y * n).abs().sum(0) + 1.5e-6 * y.abs().sum(0)
+    assert ((got["dweight"].double() - (y * n).sum(0)).abs() <= room).all()
+    assert ((got["dbias"].double() - y.sum(0)).abs() <= 8 * E * y.abs().sum(0)).all()
