@@ -743,8 +743,8 @@ int ssm_layer_norm_bwd(int64_t rows, int64_t dim, int s_dtype, float eps, double
  *                                   nor dbias is given)
  * x, dy and dx must be 16-byte aligned, float32 arrays 4-byte aligned. No
  * output may overlap an input, another output or the workspace. Deterministic:
- * the sums are taken in segments of at most 512 steps in float32, joined in double in
- * a fixed order.
+ * the sums are taken in segments of at most 512 steps in float32, five to eight steps
+ * at a time, and joined in double in a fixed order.
  */
 size_t ssm_causal_conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t width);
 int ssm_causal_conv1d_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width,

@@ -84,6 +84,7 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(const ConvBwdArgs a,
   const int64_t t1 = t0 + seg < L ? t0 + seg : L;
 
   float w[K][VC], bv[VC], dw[K][VC], db[VC];
+  float dw2[K][VC] = {}, db2[VC] = {};  // the segment's sums, to which dw and db go every group of steps
 #pragma unroll
   for (int c = 0; c < VC; ++c) {
     bv[c] = a.bias ? a.bias[c0 + c] : 0.0f;
@@ -171,8 +172,20 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(const ConvBwdArgs a,
     }
   };
 
+  // A sum takes a rounding for every group and one for every step of a group, not one for
+  // every step of a segment.
+  const auto fold = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < VC; ++c) {
+      db2[c] += db[c], db[c] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) dw2[k][c] += dw[k][c], dw[k][c] = 0.0f;
+    }
+  };
+
   if (L > 0) {  // (then t0 < t1)
     edges(t0, std::true_type{});
+    fold();
     int64_t t = t0 + K;
     for (; t + kGroup <= t1; t += kGroup) {
       float in[kGroup][VC], d[kGroup][VC];
@@ -186,9 +199,11 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(const ConvBwdArgs a,
         for (int c = 0; c < VC; ++c) x[u % K][c] = in[u][c];
         step(t + u, u % K, d[u], true, true, true);
       }
+      fold();
     }
     // What is left of the segment, and the K - 1 steps behind it that complete its last dx.
     for (; t < t1 + K - 1; t += K) edges(t, std::false_type{});
+    fold();
   } else if (a.dstate_in) {  // no step: the state has passed through
 #pragma unroll
     for (int c = 0; c < VC; ++c) {
@@ -206,8 +221,8 @@ __global__ __launch_bounds__(kBlock) void conv1d_bwd_kernel(const ConvBwdArgs a,
 #pragma unroll
   for (int c = 0; c < VC; ++c) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) part[k * Dm + c] = dw[k][c];
-    part[K * Dm + c] = db[c];
+    for (int k = 0; k < K; ++k) part[k * Dm + c] = dw2[k][c];
+    part[K * Dm + c] = db2[c];
   }
 }
 
