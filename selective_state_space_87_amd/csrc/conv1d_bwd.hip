@@ -14,7 +14,7 @@
 // K - 1 steps past its end; those steps' g is the next segment's too, but only
 // the step's own segment counts it in dw. Measured: (4, 8192, 4096, width 4)
 // bfloat16 245 us and 4.6 us for the sums, 5.4 TB/s of x, dy and dx (a large copy
-// reaches 5.1); (2, 777, 333, width 3) float32 10.6 and 3.9 us, some five loads' chains.
+// reaches 5.1); (2, 777, 333, width 3) float32 11 and 3.9 us, some five loads' chains.
 // The width is a compile-time one: taps
 // of zero in front of a narrower filter would make 0 * infinity of what they meet.
 #include <hip/hip_runtime.h>

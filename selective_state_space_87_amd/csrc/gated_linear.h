@@ -20,9 +20,10 @@ namespace ssm {
 // e^y = 2^t e^(y - t ln 2), and what is left, y - t ln 2, is one fused product and sum
 // (ln 2's own rounding is 0.05 2^-24 |y| of it) and at most 1.3 2^-24 |y|, so that e^y is
 // 2^t q with q = 1 + y - t ln 2. Without q a gate far down the sigmoid would be off by that
-// much beside what the sum u was rounded by. It takes five instructions more a gate, 47
-// for 37 an element with both, which the loads hide ((4, 8192, 4096) bfloat16 212 us; one
-// tile of 64 rows, 64 us for 62); e^-|u| as gated_delta.h takes it costs ten (238 us).
+// much beside what the sum u was rounded by. It takes five instructions more a gate, 45
+// for 37 an element with both, which the loads hide (the call at (4, 8192, 4096) bfloat16
+// 214 us for 214; 64 rows of 128 steps, one tile each, 64 for 62); e^-|u| as gated_delta.h
+// takes it costs ten (238).
 struct GlrExp {
   float e, q;  // 2^t and q: the product is left to what takes it
 };

@@ -10,8 +10,8 @@
 // them would not fit. Its sums over steps are one part a tile, joined in double
 // in a fixed order (column_sums.h).
 //
-// Bounded by HBM: (8, 2048, 1536) bfloat16 with both gates 112 us, 5.0 TB/s of the
-// inputs, dy and the three gradients; four channels a thread (eight, whose float32
+// Bounded by HBM: (8, 2048, 1536) bfloat16 with both gates 115 us, 4.8 TB/s of the
+// inputs, dy and the three gradients, 115 instructions an element; four channels a thread (eight, whose float32
 // gradients go in two stores each: 179 us with an earlier chain, four 134).
 #pragma once
 

@@ -1,14 +1,14 @@
 // Forward tiles of the gated linear recurrence; instantiated for bfloat16 and
 // float32 inputs in gated_linear_fwd_{b,f}.hip. See gated_linear_tile.h.
 //
-// Bounded by HBM: (4, 8192, 4096) bfloat16 with both gates 209 us, 5.1 TB/s, as a large
-// copy; (1, 65536, 2560) 287 us, where 40 groups of channels are chains of 512 tiles,
-// 4.7 TB/s. Vector work is 37 instructions an element, 0.6 of the time. The decays
+// Bounded by HBM: (4, 8192, 4096) bfloat16 with both gates 210 us, 5.1 TB/s, as a large
+// copy; (1, 65536, 2560) 286 us, where 40 groups of channels are chains of 512 tiles,
+// 4.7 TB/s. Vector work is 45 instructions an element, 0.74 of the time. The decays
 // and inputs of a thread's 32 elements stay in registers while the tile waits
 // for the state that enters it; what hides that wait, and the loads, are the other
-// blocks of the CU: four of 128 registers (with three, at 136, 252 us in place of 239;
-// with five, spilling, 252; blocks that stay and load the next tile while one waits,
-// three of 168 registers, 295).
+// blocks of the CU: four of 128 registers (with earlier gates, at 239 us: three of 136 252,
+// five, spilling, 252; blocks that stay and load the next tile while one waits, three of
+// 168 registers, 295).
 #pragma once
 
 #include "gated_linear_tile.h"
